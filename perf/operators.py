@@ -76,7 +76,13 @@ def _heads(rng):
     k = rng.choice([1, 2, 4, 8, 8, 12, 16])
     q = min(48, k * rng.choice([1, 2, 3, 4, 7, 8]))
     d = rng.choice([64, 64, 72, 80, 96, 112, 128, 128, 128, 192, 256, 40])
-    rot = d if rng.random() < 0.6 else 2 * rng.randint(4, d // 2)
+    part = rng.random()
+    if part < 0.6:
+        rot = d
+    elif part < 0.9:
+        rot = 2 * int(d * rng.choice([0.25, 0.4, 0.5, 0.75]) / 2)
+    else:
+        rot = 2 * rng.randint(4, d // 2)
     return q, k, d, rot
 
 
