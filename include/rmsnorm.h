@@ -64,6 +64,9 @@ typedef struct CUstream_st *rmsnorm_stream_t;
 /* I/O types (the `dtype` argument). */
 enum { RMSNORM_F32 = 0, RMSNORM_BF16 = 1 };
 
+/* Storage type of a cache (rmsnorm_paged_kv_t.cache_dtype) beside the I/O types. */
+enum { RMSNORM_E4M3 = 2 };
+
 /* Status codes. */
 enum {
     RMSNORM_OK = 0,
@@ -313,6 +316,128 @@ int rmsnorm_qk_plan_for(const void *x, const void *y, int64_t tokens, int64_t x_
                         int64_t y_token_stride, int32_t q_heads, int32_t k_heads,
                         int64_t head_dim, const void *q_w, const void *k_w, int dtype,
                         rmsnorm_plan_t *plan);
+
+/*
+ * Rotary positions, with one or several axes (a text position; time, height
+ * and width of an image or video patch).  The first rot_dim elements of a
+ * head are rot_dim / 2 pairs, (i, i + rot_dim / 2), or (2 i, 2 i + 1) with
+ * interleaved = 1; the pairs are shared out to the axes in order, section[a]
+ * pairs to axis a.  Pair i of a token turns by
+ *   theta = positions[axis of i][token] * inv_freq[i]
+ * (an integer times an fp32 value, as real numbers: positions of any size
+ * lose no precision: |position| * (1 + inv_freq) * 2^-64 turns at most), to
+ *   y_a = a cos theta - b sin theta,   y_b = a sin theta + b cos theta.
+ * Elements past rot_dim are not turned.
+ */
+typedef struct {
+    const void *positions;      /* device, int32 or int64 [axes, position_stride]        */
+    const float *inv_freq;      /* device [rot_dim / 2], finite                          */
+    int64_t position_stride;    /* elements between the axes' rows; >= tokens with
+                                   axes > 1, not looked at with one axis                 */
+    int32_t position_bytes;     /* 4 or 8                                                */
+    int32_t axes;               /* 1..4                                                  */
+    int32_t rot_dim;            /* even, 2..head_dim                                     */
+    int32_t interleaved;        /* 0: pairs (i, i + rot_dim / 2); 1: pairs (2 i, 2 i + 1) */
+    int32_t section[4];         /* pairs of each axis (>= 0), rot_dim / 2 in all         */
+} rmsnorm_rope_t;
+
+/*
+ * Fused query + key head norm and rotation in one launch: the heads, layout,
+ * weights, weight_bias and eps of rmsnorm_qk_fwd, the normalised heads then
+ * turned as above and rounded once.  norm = 0 turns the heads as they are (no
+ * weights, no bias).  head_dim is even, at most 512 (RMSNORM_EUNSUPPORTED
+ * above).  y == x (same stride) works in place; other overlaps are undefined.
+ * Accuracy: fp32 arithmetic; the sine and cosine of the exact angle to 2e-7.
+ * Pointers and strides that are multiples of 16 bytes, with rot_dim / 2 and
+ * (head_dim - rot_dim) / 2 multiples of 16 bytes of elements, move 128 bits
+ * at a time; anything else narrower, with the same results up to rounding.
+ * Returns RMSNORM_OK or a negative status (RMSNORM_EINVAL also for a
+ * malformed rope: see rmsnorm_rope_t).  tokens == 0 does nothing.
+ */
+int rmsnorm_qk_rope_fwd(const void *x, void *y, int64_t tokens, int64_t x_token_stride,
+                        int64_t y_token_stride, int32_t q_heads, int32_t k_heads, int64_t head_dim,
+                        const void *q_w, const void *k_w, float weight_bias, float eps, int norm,
+                        const rmsnorm_rope_t *rope, int dtype, rmsnorm_stream_t stream);
+
+/*
+ * Gradient of rmsnorm_qk_rope_fwd.  With g = dy turned back by theta,
+ * dn = g (w + weight_bias) and r = rsqrt(mean(x^2) + eps), for every head
+ *   dx    = r (dn - x r^2 mean(dn x))      (g itself with norm = 0)
+ *   dq_w  = sum over tokens and query heads of g x r,  dk_w the key heads'
+ *   dy, x, dx   packed token rows as in the forward, a stride each (x may be
+ *               NULL with norm = 0); dx may be dy or x (same stride).
+ *               Elements past the query and key heads are neither read nor
+ *               written.
+ *   dq_w, dk_w  [head_dim], both or neither (NULL: not computed)
+ *   workspace   DEVICE memory, 16-byte aligned, of at least
+ *               rmsnorm_qk_rope_bwd_workspace_bytes(head_dim) bytes, used by
+ *               no one else until the call's work is done; may be NULL
+ *               without dq_w and dk_w
+ * The weights' gradients are summed in fp32 in an order that follows from the
+ * sizes and the device alone (no atomics), and rounded once.  tokens == 0
+ * writes zeros to them.
+ */
+int rmsnorm_qk_rope_bwd(const void *dy, const void *x, void *dx, int64_t tokens, int64_t dy_token_stride,
+                        int64_t x_token_stride, int64_t dx_token_stride, int32_t q_heads, int32_t k_heads,
+                        int64_t head_dim, const void *q_w, const void *k_w, void *dq_w, void *dk_w,
+                        float weight_bias, float eps, int norm, const rmsnorm_rope_t *rope, int dtype,
+                        void *workspace, uint64_t workspace_bytes, rmsnorm_stream_t stream);
+
+/* Bytes of workspace rmsnorm_qk_rope_bwd needs for its weights' gradients (no
+   CUDA call), or RMSNORM_EINVAL / RMSNORM_EUNSUPPORTED for the head_dim. */
+int64_t rmsnorm_qk_rope_bwd_workspace_bytes(int64_t head_dim);
+
+/*
+ * A paged key / value cache and the batch of sequences that is appended to
+ * it.  Cache row `index` of sequence s is row index % page_size of page
+ * page_table[s * page_table_stride + index / page_size]; head h of it starts
+ * at page * page_stride + row * row_stride + h * head_stride (elements, the
+ * same in k_cache and v_cache; rows of all heads, or heads of all rows, are
+ * both such strides).
+ */
+typedef struct {
+    void *k_cache, *v_cache;    /* device                                                */
+    const int32_t *page_table;  /* device [seqs, page_table_stride]                      */
+    const int32_t *cu_tokens;   /* device [seqs + 1]: sequence s brings tokens
+                                   cu_tokens[s] .. cu_tokens[s + 1] - 1 (cu_tokens[0] = 0,
+                                   none of them falling)                                 */
+    const int32_t *cache_lens;  /* device [seqs]: rows already in the cache              */
+    int32_t *dropped;           /* device, optional: see below                           */
+    int64_t page_table_stride;  /* >= max_pages                                          */
+    int64_t page_stride, row_stride, head_stride;
+    int32_t seqs;
+    int32_t max_pages;          /* entries of a sequence's page table                    */
+    int32_t num_pages;          /* pages of the cache                                    */
+    int32_t page_size;          /* rows of a page, >= 1                                  */
+    int32_t cache_dtype;        /* the I/O type, or RMSNORM_E4M3                         */
+    float k_scale, v_scale;     /* E4M3: a code stands for code * scale (> 0, finite)    */
+} rmsnorm_paged_kv_t;
+
+/*
+ * Appends a ragged batch's keys and values to a paged cache, the heads
+ * normalised and turned on the way, in one launch.  Token rows are packed
+ * [q_heads | kv_heads keys | kv_heads values] heads of head_dim; query and
+ * key heads go through rmsnorm_qk_rope_fwd's operation, queries to q_out
+ * ([tokens, q_heads * head_dim], a stride of its own; q_out == x with x's
+ * stride works in place), keys and values to the cache.  Token t of sequence
+ * s is row cache_lens[s] + t - cu_tokens[s] of it, which is also its position
+ * when rope->positions is NULL (one axis then).  E4M3 caches hold
+ * E4M3(value / scale) of the unrounded value, nearest-even, saturated at 448
+ * (infinities too; NaN stays NaN).
+ *   tokens       rows of x and q_out; rows from cu_tokens[seqs] on are padding:
+ *                not read, and q_out left as it was there
+ *   cache_lens   is not changed: the caller adds the new tokens to it
+ * A row whose index lies past max_pages pages or in a page outside
+ * 0 .. num_pages - 1 (-1 marks an absent page) is not written; its queries
+ * are still computed, and 1 is added to *dropped where that is given.  A
+ * cache row that two tokens of one call name (a page listed twice) holds an
+ * unspecified mix of them.  seqs == 0 or tokens == 0 does nothing.
+ */
+int rmsnorm_qkv_append(const void *x, void *q_out, int64_t tokens, int64_t x_token_stride,
+                       int64_t q_token_stride, int32_t q_heads, int32_t kv_heads, int64_t head_dim,
+                       const void *q_w, const void *k_w, float weight_bias, float eps, int norm,
+                       const rmsnorm_rope_t *rope, const rmsnorm_paged_kv_t *kv, int dtype,
+                       rmsnorm_stream_t stream);
 
 /*
  * RMSNorm with a block-scaled MXFP8 output (OCP Microscaling Formats v1.0:

@@ -18,6 +18,7 @@ LIB_PATH = os.path.join(PKG, "librmsnorm_gb300.so")
 
 RMSNORM_F32 = 0
 RMSNORM_BF16 = 1
+RMSNORM_E4M3 = 2          # storage type of a cache
 
 RMSNORM_OK = 0
 RMSNORM_EINVAL = -1
@@ -65,7 +66,9 @@ def tma_rings(row_bytes, pc, res, w):
 # Every symbol the header declares (checked by the CPU tests).
 EXPORTED = ["rmsnorm_fwd", "rmsnorm_regime", "rmsnorm_plan", "rmsnorm_plan_ex", "rmsnorm_plan_for",
             "rmsnorm_fwd_plan", "rmsnorm_fwd_ex", "rmsnorm_fwd_cast",
-            "rmsnorm_qk_fwd", "rmsnorm_qk_plan_for", "rmsnorm_fwd_mxfp8", "rmsnorm_mxfp8_plan_for",
+            "rmsnorm_qk_fwd", "rmsnorm_qk_plan_for",
+            "rmsnorm_qk_rope_fwd", "rmsnorm_qk_rope_bwd", "rmsnorm_qk_rope_bwd_workspace_bytes", "rmsnorm_qkv_append",
+            "rmsnorm_fwd_mxfp8", "rmsnorm_mxfp8_plan_for",
             "rmsnorm_fwd_nvfp4", "rmsnorm_nvfp4_plan_for",
             "layernorm_fwd", "layernorm_plan_for",
             "rmsnorm_fwd_host", "rmsnorm_host_workspace_bytes", "rmsnorm_fwd_host_static",
@@ -111,6 +114,43 @@ class Plan(ctypes.Structure):
         return f"Plan({self.as_dict()})"
 
 
+class Rope(ctypes.Structure):
+    """Mirror of ``rmsnorm_rope_t``."""
+    _fields_ = [
+        ("positions", ctypes.c_void_p),
+        ("inv_freq", ctypes.c_void_p),
+        ("position_stride", ctypes.c_int64),
+        ("position_bytes", ctypes.c_int32),
+        ("axes", ctypes.c_int32),
+        ("rot_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("section", ctypes.c_int32 * 4),
+    ]
+
+
+class PagedKV(ctypes.Structure):
+    """Mirror of ``rmsnorm_paged_kv_t``."""
+    _fields_ = [
+        ("k_cache", ctypes.c_void_p),
+        ("v_cache", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p),
+        ("cu_tokens", ctypes.c_void_p),
+        ("cache_lens", ctypes.c_void_p),
+        ("dropped", ctypes.c_void_p),
+        ("page_table_stride", ctypes.c_int64),
+        ("page_stride", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+        ("seqs", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("cache_dtype", ctypes.c_int32),
+        ("k_scale", ctypes.c_float),
+        ("v_scale", ctypes.c_float),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -147,6 +187,19 @@ def load():
         lib.rmsnorm_qk_plan_for.argtypes = [vp, vp, i64, i64, i64, ctypes.c_int32, ctypes.c_int32, i64, vp, vp,
                                             i32, ctypes.POINTER(Plan)]
         lib.rmsnorm_qk_plan_for.restype = i32
+        f32 = ctypes.c_float
+        lib.rmsnorm_qk_rope_fwd.argtypes = [vp, vp, i64, i64, i64, ctypes.c_int32, ctypes.c_int32, i64, vp, vp, f32,
+                                            f32, i32, ctypes.POINTER(Rope), i32, vp]
+        lib.rmsnorm_qk_rope_fwd.restype = i32
+        lib.rmsnorm_qk_rope_bwd.argtypes = [vp, vp, vp, i64, i64, i64, i64, ctypes.c_int32, ctypes.c_int32, i64, vp,
+                                            vp, vp, vp, f32, f32, i32, ctypes.POINTER(Rope), i32, vp,
+                                            ctypes.c_uint64, vp]
+        lib.rmsnorm_qk_rope_bwd.restype = i32
+        lib.rmsnorm_qk_rope_bwd_workspace_bytes.argtypes = [i64]
+        lib.rmsnorm_qk_rope_bwd_workspace_bytes.restype = i64
+        lib.rmsnorm_qkv_append.argtypes = [vp, vp, i64, i64, i64, ctypes.c_int32, ctypes.c_int32, i64, vp, vp, f32,
+                                           f32, i32, ctypes.POINTER(Rope), ctypes.POINTER(PagedKV), i32, vp]
+        lib.rmsnorm_qkv_append.restype = i32
         lib.rmsnorm_fwd_mxfp8.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, ctypes.c_float, ctypes.c_float, i32,
                                           ctypes.POINTER(Plan), vp]
         lib.rmsnorm_fwd_mxfp8.restype = i32
@@ -261,6 +314,56 @@ def rmsnorm_qk_plan_for(x, y, tokens, x_token_stride, y_token_stride, q_heads, k
     _check(load().rmsnorm_qk_plan_for(x, y, tokens, x_token_stride, y_token_stride, q_heads, k_heads,
                                       head_dim, q_w, k_w, dtype, ctypes.byref(p)), "rmsnorm_qk_plan_for")
     return p
+
+
+def rmsnorm_qk_rope_fwd(x, y, tokens, x_token_stride, y_token_stride, q_heads, k_heads, head_dim, q_w, k_w,
+                        weight_bias, eps, norm, rope, dtype, stream=0):
+    _check(rmsnorm_qk_rope_fwd_status(x, y, tokens, x_token_stride, y_token_stride, q_heads, k_heads, head_dim, q_w,
+                                      k_w, weight_bias, eps, norm, rope, dtype, stream), "rmsnorm_qk_rope_fwd")
+
+
+def rmsnorm_qk_rope_fwd_status(x, y, tokens, x_token_stride, y_token_stride, q_heads, k_heads, head_dim, q_w, k_w,
+                               weight_bias, eps, norm, rope, dtype, stream=0) -> int:
+    return load().rmsnorm_qk_rope_fwd(x, y, tokens, x_token_stride, y_token_stride, q_heads, k_heads, head_dim, q_w,
+                                      k_w, weight_bias, eps, norm, _plan_ref(rope), dtype, stream)
+
+
+def rmsnorm_qk_rope_bwd(dy, x, dx, tokens, dy_token_stride, x_token_stride, dx_token_stride, q_heads, k_heads,
+                        head_dim, q_w, k_w, dq_w, dk_w, weight_bias, eps, norm, rope, dtype, workspace,
+                        workspace_bytes, stream=0):
+    _check(rmsnorm_qk_rope_bwd_status(dy, x, dx, tokens, dy_token_stride, x_token_stride, dx_token_stride, q_heads,
+                                      k_heads, head_dim, q_w, k_w, dq_w, dk_w, weight_bias, eps, norm, rope, dtype,
+                                      workspace, workspace_bytes, stream), "rmsnorm_qk_rope_bwd")
+
+
+def rmsnorm_qk_rope_bwd_status(dy, x, dx, tokens, dy_token_stride, x_token_stride, dx_token_stride, q_heads, k_heads,
+                               head_dim, q_w, k_w, dq_w, dk_w, weight_bias, eps, norm, rope, dtype, workspace,
+                               workspace_bytes, stream=0) -> int:
+    return load().rmsnorm_qk_rope_bwd(dy, x, dx, tokens, dy_token_stride, x_token_stride, dx_token_stride, q_heads,
+                                      k_heads, head_dim, q_w, k_w, dq_w, dk_w, weight_bias, eps, norm,
+                                      _plan_ref(rope), dtype, workspace, workspace_bytes, stream)
+
+
+def _bytes_or_raise(n, where) -> int:
+    if n < 0:
+        raise RmsNormError(int(n), where)
+    return int(n)
+
+
+def rmsnorm_qk_rope_bwd_workspace_bytes(head_dim) -> int:
+    return _bytes_or_raise(load().rmsnorm_qk_rope_bwd_workspace_bytes(head_dim), "rmsnorm_qk_rope_bwd_workspace_bytes")
+
+
+def rmsnorm_qkv_append(x, q_out, tokens, x_token_stride, q_token_stride, q_heads, kv_heads, head_dim, q_w, k_w,
+                       weight_bias, eps, norm, rope, kv, dtype, stream=0):
+    _check(rmsnorm_qkv_append_status(x, q_out, tokens, x_token_stride, q_token_stride, q_heads, kv_heads, head_dim,
+                                     q_w, k_w, weight_bias, eps, norm, rope, kv, dtype, stream), "rmsnorm_qkv_append")
+
+
+def rmsnorm_qkv_append_status(x, q_out, tokens, x_token_stride, q_token_stride, q_heads, kv_heads, head_dim, q_w, k_w,
+                              weight_bias, eps, norm, rope, kv, dtype, stream=0) -> int:
+    return load().rmsnorm_qkv_append(x, q_out, tokens, x_token_stride, q_token_stride, q_heads, kv_heads, head_dim,
+                                     q_w, k_w, weight_bias, eps, norm, _plan_ref(rope), _plan_ref(kv), dtype, stream)
 
 
 def rmsnorm_fwd_mxfp8(x, residual, w, codes, scales, residual_out, rows, hidden, eps, weight_bias, dtype,

@@ -174,6 +174,229 @@ def qk_norm(qkv: torch.Tensor, q_heads: int, k_heads: int, head_dim: int, q_w: O
     return out
 
 
+def _empty(shape, dtype, device, stream):
+    """An output or workspace allocated for work on ``stream`` (None: the
+    current one), so that its memory is not handed out again before that work
+    is done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _launch(device, stream, call, *args):
+    """call(*args, stream handle) with the tensors' device current."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    s = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        call(*args, s)
+    else:
+        with torch.cuda.device(device):
+            call(*args, s)
+
+
+def _head_rows(t: torch.Tensor, name: str, width: int, like=None) -> int:
+    """Token stride of a [tokens, >= width] tensor of packed heads (the last
+    dimension contiguous), on the device and of the type of ``like``."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
+    if t.dim() != 2 or t.shape[1] < width:
+        raise ValueError(f"{name} must be a 2-D tensor of at least {width} columns, got {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if like is not None:
+        if t.device != like.device or t.dtype != like.dtype:
+            raise ValueError(f"{name} must match the device {like.device} and dtype {like.dtype}")
+        if t.shape[0] != like.shape[0]:
+            raise ValueError(f"{name} has {t.shape[0]} rows, expected {like.shape[0]}")
+    return max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+
+
+def _vector(t, name, size, like, dtype=None):
+    """Checks a contiguous [size] tensor on the device of ``like``."""
+    if t is None:
+        return
+    dtype = like.dtype if dtype is None else dtype
+    if t.device != like.device or t.dtype != dtype or t.dim() != 1 or t.shape[0] != size or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [{size}] tensor of {dtype} on {like.device}")
+
+
+def _rope_arg(positions, inv_freq, sections, interleaved, tokens, head_dim, like) -> N.Rope:
+    pairs = inv_freq.shape[0] if inv_freq.dim() == 1 else -1
+    _vector(inv_freq, "inv_freq", pairs, like, torch.float32)
+    if not 1 <= pairs <= head_dim // 2:
+        raise ValueError(f"inv_freq must hold 1..{head_dim // 2} frequencies, one for each rotated pair")
+    sections = (pairs,) if sections is None else sections
+    axes = len(sections)
+    if not 1 <= axes <= 4 or min(sections) < 0 or sum(sections) != pairs:
+        raise ValueError(f"sections must be 1..4 counts that add up to {pairs}")
+    r = N.Rope()
+    if positions is not None:
+        if positions.device != like.device or positions.dtype not in (torch.int32, torch.int64):
+            raise ValueError(f"positions must be an int32 or int64 tensor on {like.device}")
+        p = positions[None] if positions.dim() == 1 else positions
+        if tuple(p.shape) != (axes, tokens) or (tokens > 1 and p.stride(1) != 1):
+            raise ValueError(f"positions must be [{axes}, {tokens}] with a contiguous last dimension, "
+                             f"got {tuple(positions.shape)}")
+        r.positions = p.data_ptr()
+        r.position_stride = p.stride(0) if tokens > 1 else max(p.stride(0), tokens)
+        r.position_bytes = p.element_size()
+    else:
+        r.position_bytes = 4
+    r.inv_freq = inv_freq.data_ptr()
+    r.axes = axes
+    r.rot_dim = 2 * pairs
+    r.interleaved = 1 if interleaved else 0
+    r.section[:axes] = sections
+    return r
+
+
+def qk_norm_rope(qkv: torch.Tensor, q_heads: int, k_heads: int, head_dim: int, positions: torch.Tensor,
+                 inv_freq: torch.Tensor, q_w: Optional[torch.Tensor] = None, k_w: Optional[torch.Tensor] = None,
+                 eps: float = 1e-6, weight_bias: float = 0.0, norm: bool = True, sections=None,
+                 interleaved: bool = False, out: Optional[torch.Tensor] = None,
+                 stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """``qk_norm`` with the rotary positions applied to the normalised heads, in one launch.
+
+    ``positions`` is [tokens] or [axes, tokens] (int32 or int64), ``inv_freq``
+    (fp32) holds one frequency for each rotated pair: the first
+    2 * len(inv_freq) elements of a head turn.  ``sections`` shares the pairs
+    out to the axes in order (default: all to one axis); pairs are
+    (i, i + len(inv_freq)), or neighbours with ``interleaved``.  ``norm=False``
+    turns the heads as they are.  The result goes to ``out``, whose first
+    q_heads + k_heads heads are written (``out=qkv`` works in place), or to a
+    new [tokens, (q_heads + k_heads) * head_dim] tensor.
+    """
+    code = dtype_code(qkv.dtype)
+    width = (q_heads + k_heads) * head_dim
+    xs = _head_rows(qkv, "qkv", width)
+    tokens = qkv.shape[0]
+    _vector(q_w, "q_w", head_dim, qkv)
+    _vector(k_w, "k_w", head_dim, qkv)
+    rope = _rope_arg(positions, inv_freq, sections, interleaved, tokens, head_dim, qkv)
+    if out is None:
+        out = _empty((tokens, width), qkv.dtype, qkv.device, stream)
+    ys = _head_rows(out, "out", width, qkv)
+    _launch(qkv.device, stream, N.rmsnorm_qk_rope_fwd, _ptr(qkv), _ptr(out), tokens, xs, ys, q_heads, k_heads, head_dim,
+            _ptr(q_w), _ptr(k_w), weight_bias, eps, int(norm), rope, code)
+    return out
+
+
+def qk_norm_rope_backward(dout: torch.Tensor, qkv: Optional[torch.Tensor], q_heads: int, k_heads: int, head_dim: int,
+                          positions: torch.Tensor, inv_freq: torch.Tensor, q_w: Optional[torch.Tensor] = None,
+                          k_w: Optional[torch.Tensor] = None, eps: float = 1e-6, weight_bias: float = 0.0,
+                          norm: bool = True, sections=None, interleaved: bool = False,
+                          out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                          stream: Optional[torch.cuda.Stream] = None):
+    """Gradient of ``qk_norm_rope``: returns (dqkv, dq_w, dk_w).
+
+    ``dout`` holds the gradient of the rotated heads, ``qkv`` the forward's
+    input (None with ``norm=False``).  dqkv goes to ``out`` (its first
+    q_heads + k_heads heads; ``out=dout`` works in place) or to a new tensor;
+    dq_w and dk_w are None without weights.  ``workspace`` is a CUDA uint8
+    tensor of ``rmsnorm_qk_rope_bwd_workspace_bytes(head_dim)`` bytes
+    (allocated when not given).
+    """
+    code = dtype_code(dout.dtype)
+    width = (q_heads + k_heads) * head_dim
+    gs = _head_rows(dout, "dout", width)
+    tokens = dout.shape[0]
+    if qkv is None and norm:
+        raise ValueError("the norm's gradient needs qkv")
+    xs = _head_rows(qkv, "qkv", width, dout) if qkv is not None else max(width, 1)
+    _vector(q_w, "q_w", head_dim, dout)
+    _vector(k_w, "k_w", head_dim, dout)
+    rope = _rope_arg(positions, inv_freq, sections, interleaved, tokens, head_dim, dout)
+    if out is None:
+        out = _empty((tokens, width), dout.dtype, dout.device, stream)
+    ds = _head_rows(out, "out", width, dout)
+    dq_w = dk_w = None
+    need = 0
+    if q_w is not None and k_w is not None:
+        both = _empty((2, head_dim), dout.dtype, dout.device, stream)
+        dq_w, dk_w = both[0], both[1]
+        need = N.rmsnorm_qk_rope_bwd_workspace_bytes(head_dim)
+        workspace = _workspace(workspace, need, dout.device, stream)
+    _launch(dout.device, stream, N.rmsnorm_qk_rope_bwd, _ptr(dout), _ptr(qkv), _ptr(out), tokens, gs, xs, ds, q_heads,
+            k_heads, head_dim, _ptr(q_w), _ptr(k_w), _ptr(dq_w), _ptr(dk_w), weight_bias, eps, int(norm), rope, code,
+            _ptr(workspace) if need else None, need)
+    return out, dq_w, dk_w
+
+
+def _workspace(workspace, need, device, stream):
+    if workspace is None:
+        return _empty((need,), torch.uint8, device, stream)
+    if workspace.device != device or not workspace.is_contiguous() or \
+            workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace must be a contiguous tensor of at least {need} bytes on {device}")
+    return workspace
+
+
+_CACHE_CODES = {torch.bfloat16: N.RMSNORM_BF16, torch.float32: N.RMSNORM_F32, torch.float8_e4m3fn: N.RMSNORM_E4M3}
+
+
+def qkv_append(qkv: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+               cu_tokens: torch.Tensor, cache_lens: torch.Tensor, q_heads: int, kv_heads: int, head_dim: int,
+               inv_freq: torch.Tensor, positions: Optional[torch.Tensor] = None, q_w: Optional[torch.Tensor] = None,
+               k_w: Optional[torch.Tensor] = None, eps: float = 1e-6, weight_bias: float = 0.0, norm: bool = True,
+               sections=None, interleaved: bool = False, k_scale: float = 1.0, v_scale: float = 1.0,
+               q_out: Optional[torch.Tensor] = None, dropped: Optional[torch.Tensor] = None,
+               stream: Optional[torch.cuda.Stream] = None) -> Optional[torch.Tensor]:
+    """Appends a ragged batch to a paged cache: Q+K norm and rotation as in
+    ``qk_norm_rope``, queries to ``q_out`` (returned), keys and values to the
+    cache, in one launch.
+
+    ``qkv`` is [tokens, (q_heads + 2 * kv_heads) * head_dim].  The caches are
+    [num_pages, page_size, kv_heads, head_dim] tensors of any strides with a
+    contiguous last dimension (so a permuted view of a cache kept head by head
+    too), in qkv's type or float8_e4m3fn, where a code stands for
+    code * ``k_scale`` (``v_scale``).  Sequence s brings the tokens
+    cu_tokens[s] .. cu_tokens[s + 1] - 1 (int32, [seqs + 1]) and has
+    cache_lens[s] rows (int32) in the pages page_table[s] (int32, [seqs,
+    max_pages], -1: no page); cache_lens is left as it is.  ``positions``
+    defaults to the row's index in its sequence.  Rows behind the last
+    sequence are left alone; rows without a page are not written and counted
+    in ``dropped`` (int32, [1], added to) where given.
+    """
+    code = dtype_code(qkv.dtype)
+    xs = _head_rows(qkv, "qkv", (q_heads + 2 * kv_heads) * head_dim)
+    tokens = qkv.shape[0]
+    _vector(q_w, "q_w", head_dim, qkv)
+    _vector(k_w, "k_w", head_dim, qkv)
+    rope = _rope_arg(positions, inv_freq, sections, interleaved, tokens, head_dim, qkv)
+    shape, strides = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or shape[2] != kv_heads or shape[3] != head_dim or strides[3] != 1:
+        raise ValueError(f"k_cache must be [num_pages, page_size, {kv_heads}, {head_dim}] with a contiguous last "
+                         f"dimension, got {tuple(shape)}")
+    if v_cache.shape != shape or v_cache.stride() != strides or v_cache.dtype != k_cache.dtype:
+        raise ValueError("v_cache must have the shape, strides and dtype of k_cache")
+    if k_cache.device != qkv.device or v_cache.device != qkv.device:
+        raise ValueError(f"the caches must be on {qkv.device}")
+    if k_cache.dtype not in (qkv.dtype, torch.float8_e4m3fn):
+        raise TypeError(f"caches of {k_cache.dtype}: {qkv.dtype} or float8_e4m3fn only")
+    if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.device != qkv.device or \
+            (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError(f"page_table must be a 2-D int32 tensor on {qkv.device} with a contiguous last dimension")
+    seqs, max_pages = page_table.shape
+    _vector(cu_tokens, "cu_tokens", seqs + 1, qkv, torch.int32)
+    _vector(cache_lens, "cache_lens", seqs, qkv, torch.int32)
+    _vector(dropped, "dropped", 1, qkv, torch.int32)
+    qs = 0
+    if q_heads > 0:
+        if q_out is None:
+            q_out = _empty((tokens, q_heads * head_dim), qkv.dtype, qkv.device, stream)
+        qs = _head_rows(q_out, "q_out", q_heads * head_dim, qkv)
+    kv = N.PagedKV(
+        k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), cu_tokens.data_ptr(), cache_lens.data_ptr(),
+        _ptr(dropped), max(page_table.stride(0), max_pages) if seqs <= 1 else page_table.stride(0),
+        strides[0] if shape[0] > 1 else 0, strides[1] if shape[1] > 1 else 0, strides[2] if shape[2] > 1 else 0,
+        seqs, max_pages, shape[0], shape[1], _CACHE_CODES[k_cache.dtype], k_scale, v_scale)
+    _launch(qkv.device, stream, N.rmsnorm_qkv_append, _ptr(qkv), _ptr(q_out) if q_heads > 0 else None, tokens, xs, qs,
+            q_heads, kv_heads, head_dim, _ptr(q_w), _ptr(k_w), weight_bias, eps, int(norm), rope, kv, code)
+    return q_out
+
+
 def qk_plan_for(qkv: torch.Tensor, q_heads: int, k_heads: int, head_dim: int, q_w=None, k_w=None,
                 out=None) -> N.Plan:
     """The plan ``qk_norm`` would launch for these tensors."""

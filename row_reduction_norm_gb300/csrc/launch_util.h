@@ -1,0 +1,53 @@
+// launch_util.h -- what the entry points of the operators beside the norm
+// share (internal): the per-device caches of rmsnorm_api.cu and small host
+// helpers.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "rmsnorm.h"
+
+namespace rrn {
+
+// The current device and its SM count.  A status (RMSNORM_OK or RMSNORM_ECUDA).
+int current_device_sms(int *dev, int *sms);
+// Resident blocks a SM of a kernel (cached per device, kernel and shared memory).
+int resident_blocks(int dev, const void *fn, int block, size_t smem, int *blocks);
+
+inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+inline int size_of(int dtype) { return dtype == RMSNORM_BF16 ? 2 : 4; }
+
+inline bool on_boundary(const void *p, int64_t bytes) {
+    return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0;
+}
+
+// Launch with programmatic stream serialisation (every kernel of the library
+// waits for the work before it through griddepcontrol before it touches memory).
+inline int launch_kernel(const void *fn, dim3 grid, int block, size_t smem, rmsnorm_stream_t stream, void **argv) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelExC(&cfg, fn, argv) != cudaSuccess) {
+        (void)cudaGetLastError();   // clear the non-sticky launch error
+        return RMSNORM_ECUDA;
+    }
+    return RMSNORM_OK;
+}
+
+// Sums of the columns of partial[rows][cols] into the I/O type: columns
+// 0 .. split - 1 to out0, the rest to out1 (colsum.cu).
+int launch_colsum(const float *partial, int rows, int64_t cols, int64_t split, void *out0, void *out1, int dtype,
+                  rmsnorm_stream_t stream);
+
+}  // namespace rrn

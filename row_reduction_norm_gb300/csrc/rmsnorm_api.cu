@@ -17,6 +17,7 @@
 #include <mutex>
 
 #include "kernel_table.h"
+#include "launch_util.h"
 #include "layernorm_kernels.cuh"
 #include "rmsnorm.h"
 #include "rmsnorm_kernels.cuh"
@@ -793,6 +794,19 @@ int make_ln(const void *x, const void *residual, const void *w, const void *b, v
 }
 
 }  // namespace
+
+namespace rrn {
+
+int current_device_sms(int *dev, int *sms) {
+    if (cudaGetDevice(dev) != cudaSuccess) return RMSNORM_ECUDA;
+    return sm_count_of(*dev, sms);
+}
+
+int resident_blocks(int dev, const void *fn, int block, size_t smem, int *blocks) {
+    return blocks_per_sm_of(dev, fn, block, smem, blocks);
+}
+
+}  // namespace rrn
 
 extern "C" {
 

@@ -1,0 +1,35 @@
+// f32 instantiations of the rotary forward and of the paged append.
+#include "rope_kernels.cuh"
+#include "rope_pick.h"
+
+namespace rrn {
+namespace {
+
+template <typename T, int VE, int K, int UN, bool IL>
+const void *one(int mode) {
+    switch (mode) {
+        case kRopePlain: return reinterpret_cast<const void *>(&rope_kernel<T, VE, K, IL, kRopePlain, UN>);
+        case kRopeAppend: return reinterpret_cast<const void *>(&rope_kernel<T, VE, K, IL, kRopeAppend, UN>);
+        case kRopeAppendE4m3: return reinterpret_cast<const void *>(&rope_kernel<T, VE, K, IL, kRopeAppendE4m3, UN>);
+        default: return nullptr;
+    }
+}
+
+template <typename T, int VE, int K, int UN>
+const void *mode_of(bool il, int mode) {
+    return il ? one<T, VE, K, UN, true>(mode) : one<T, VE, K, UN, false>(mode);
+}
+
+}  // namespace
+
+const void *rope_fwd_f32(int shape, bool il, int mode) {
+    switch (shape) {
+        case 0: return mode_of<F32, 4, 1, 4>(il, mode);
+        case 1: return mode_of<F32, 4, 2, 2>(il, mode);
+        case 2: return mode_of<F32, 2, 2, 4>(il, mode);
+        case 3: return mode_of<F32, 1, 8, 2>(il, mode);
+        default: return nullptr;
+    }
+}
+
+}  // namespace rrn
