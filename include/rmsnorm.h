@@ -440,6 +440,68 @@ int rmsnorm_qkv_append(const void *x, void *q_out, int64_t tokens, int64_t x_tok
                        rmsnorm_stream_t stream);
 
 /*
+ * Residual dropout fused with RMSNorm:
+ *   residual_out = RN_T( residual + keep_i * x_i / q ),   y = the op of
+ *   rmsnorm_fwd_ex on it (weight w, weight_bias)
+ * keep_i is 1 with probability q = 1 - round(65536 p_drop) / 65536 and is a
+ * function of the seed and offset in `rng` and of the element's place alone
+ * (Philox4x32-10 of Salmon et al., SC 2011): the counter's low 64 bits are
+ * row * ceil(hidden / 8) + column / 8, its high 64 bits the offset, the key is
+ * the seed; the four words are eight 16-bit numbers, low half first, and
+ * element column % 8 is kept when its number is at least 65536 (1 - q).  No
+ * mask is stored: rmsnorm_dropout_bwd makes it again.  A dropped element adds
+ * 0 whatever x holds there (NaN and infinity too).
+ *   x, residual, y, residual_out   [rows, hidden], all required (y and
+ *               residual_out distinct; either may be x or residual)
+ *   w           [hidden], optional
+ *   p_drop      0 <= p_drop < 1 - 2^-17 (0: nothing is dropped, rng may be NULL)
+ *   rng         DEVICE pointer to two uint64 (seed, offset), 8-byte aligned:
+ *               read when the kernel runs, so a captured call takes the values
+ *               of its replay
+ * Other arguments, layout, alignment and status codes as rmsnorm_fwd_ex.
+ */
+int rmsnorm_dropout_fwd(const void *x, const void *residual, const void *w, void *y,
+                        void *residual_out, int64_t rows, int64_t hidden, float eps,
+                        float weight_bias, float p_drop, const uint64_t *rng, int dtype,
+                        rmsnorm_stream_t stream);
+
+/*
+ * Gradient of rmsnorm_fwd / rmsnorm_fwd_ex in its input h (x, or residual_out
+ * with a residual, which is then the gradient of x and of the residual both):
+ *   g = dy (w + weight_bias),   r = rsqrt(mean(h^2) + eps)
+ *   dx = RN_T( r (g - h r^2 mean(g h)) + dresidual_out )
+ *   dw = sum over rows of dy h r
+ *   dresidual_out  optional: the gradient that reaches h on another way
+ *   w, dw          [hidden]; dw optional, only with w
+ *   workspace      DEVICE memory, 16-byte aligned, of at least
+ *                  rmsnorm_bwd_workspace_bytes(rows, hidden, dtype) bytes, used
+ *                  by no one else until the call's work is done; may be NULL
+ *                  without dw
+ * dx may be any of the inputs of its shape.  dw is summed in fp32 in an order
+ * that follows from the sizes, the alignment and the device alone (no
+ * atomics), and rounded once; rows == 0 writes zeros to it.  Other arguments,
+ * layout, alignment and status codes as rmsnorm_fwd_ex.
+ */
+int rmsnorm_bwd(const void *dy, const void *h, const void *w, const void *dresidual_out, void *dx,
+                void *dw, int64_t rows, int64_t hidden, float eps, float weight_bias, int dtype,
+                void *workspace, uint64_t workspace_bytes, rmsnorm_stream_t stream);
+
+/* Bytes of workspace that rmsnorm_bwd and rmsnorm_dropout_bwd need on the
+   current device (its SM count is queried once), or a negative status. */
+int64_t rmsnorm_bwd_workspace_bytes(int64_t rows, int64_t hidden, int dtype);
+
+/*
+ * Gradient of rmsnorm_dropout_fwd, h being its residual_out: dresidual as
+ * rmsnorm_bwd's dx, and dx_i = RN_T( keep_i / q * the unrounded dresidual_i ),
+ * with the mask of the same rng and p_drop.  dresidual and dx are both
+ * required and distinct.
+ */
+int rmsnorm_dropout_bwd(const void *dy, const void *h, const void *w, const void *dresidual_out,
+                        void *dresidual, void *dx, void *dw, int64_t rows, int64_t hidden, float eps,
+                        float weight_bias, float p_drop, const uint64_t *rng, int dtype,
+                        void *workspace, uint64_t workspace_bytes, rmsnorm_stream_t stream);
+
+/*
  * RMSNorm with a block-scaled MXFP8 output (OCP Microscaling Formats v1.0:
  * E4M3 elements, one E8M0 scale per 32 elements; block-scaled low-precision
  * formats are named in "CuTeDSL at Perplexity", section "Blackwell

@@ -68,6 +68,7 @@ EXPORTED = ["rmsnorm_fwd", "rmsnorm_regime", "rmsnorm_plan", "rmsnorm_plan_ex", 
             "rmsnorm_fwd_plan", "rmsnorm_fwd_ex", "rmsnorm_fwd_cast",
             "rmsnorm_qk_fwd", "rmsnorm_qk_plan_for",
             "rmsnorm_qk_rope_fwd", "rmsnorm_qk_rope_bwd", "rmsnorm_qk_rope_bwd_workspace_bytes", "rmsnorm_qkv_append",
+            "rmsnorm_dropout_fwd", "rmsnorm_bwd", "rmsnorm_bwd_workspace_bytes", "rmsnorm_dropout_bwd",
             "rmsnorm_fwd_mxfp8", "rmsnorm_mxfp8_plan_for",
             "rmsnorm_fwd_nvfp4", "rmsnorm_nvfp4_plan_for",
             "layernorm_fwd", "layernorm_plan_for",
@@ -200,6 +201,15 @@ def load():
         lib.rmsnorm_qkv_append.argtypes = [vp, vp, i64, i64, i64, ctypes.c_int32, ctypes.c_int32, i64, vp, vp, f32,
                                            f32, i32, ctypes.POINTER(Rope), ctypes.POINTER(PagedKV), i32, vp]
         lib.rmsnorm_qkv_append.restype = i32
+        u64 = ctypes.c_uint64
+        lib.rmsnorm_dropout_fwd.argtypes = [vp, vp, vp, vp, vp, i64, i64, f32, f32, f32, vp, i32, vp]
+        lib.rmsnorm_dropout_fwd.restype = i32
+        lib.rmsnorm_bwd.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, f32, f32, i32, vp, u64, vp]
+        lib.rmsnorm_bwd.restype = i32
+        lib.rmsnorm_bwd_workspace_bytes.argtypes = [i64, i64, i32]
+        lib.rmsnorm_bwd_workspace_bytes.restype = i64
+        lib.rmsnorm_dropout_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, f32, f32, f32, vp, i32, vp, u64, vp]
+        lib.rmsnorm_dropout_bwd.restype = i32
         lib.rmsnorm_fwd_mxfp8.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, ctypes.c_float, ctypes.c_float, i32,
                                           ctypes.POINTER(Plan), vp]
         lib.rmsnorm_fwd_mxfp8.restype = i32
@@ -364,6 +374,45 @@ def rmsnorm_qkv_append_status(x, q_out, tokens, x_token_stride, q_token_stride, 
                               weight_bias, eps, norm, rope, kv, dtype, stream=0) -> int:
     return load().rmsnorm_qkv_append(x, q_out, tokens, x_token_stride, q_token_stride, q_heads, kv_heads, head_dim,
                                      q_w, k_w, weight_bias, eps, norm, _plan_ref(rope), _plan_ref(kv), dtype, stream)
+
+
+def rmsnorm_dropout_fwd(x, residual, w, y, residual_out, rows, hidden, eps, weight_bias, p_drop, rng, dtype, stream=0):
+    _check(rmsnorm_dropout_fwd_status(x, residual, w, y, residual_out, rows, hidden, eps, weight_bias, p_drop, rng,
+                                      dtype, stream), "rmsnorm_dropout_fwd")
+
+
+def rmsnorm_dropout_fwd_status(x, residual, w, y, residual_out, rows, hidden, eps, weight_bias, p_drop, rng, dtype,
+                               stream=0) -> int:
+    return load().rmsnorm_dropout_fwd(x, residual, w, y, residual_out, rows, hidden, eps, weight_bias, p_drop, rng,
+                                      dtype, stream)
+
+
+def rmsnorm_bwd(dy, h, w, dresidual_out, dx, dw, rows, hidden, eps, weight_bias, dtype, workspace, workspace_bytes,
+                stream=0):
+    _check(rmsnorm_bwd_status(dy, h, w, dresidual_out, dx, dw, rows, hidden, eps, weight_bias, dtype, workspace,
+                              workspace_bytes, stream), "rmsnorm_bwd")
+
+
+def rmsnorm_bwd_status(dy, h, w, dresidual_out, dx, dw, rows, hidden, eps, weight_bias, dtype, workspace,
+                       workspace_bytes, stream=0) -> int:
+    return load().rmsnorm_bwd(dy, h, w, dresidual_out, dx, dw, rows, hidden, eps, weight_bias, dtype, workspace,
+                              workspace_bytes, stream)
+
+
+def rmsnorm_bwd_workspace_bytes(rows, hidden, dtype) -> int:
+    return _bytes_or_raise(load().rmsnorm_bwd_workspace_bytes(rows, hidden, dtype), "rmsnorm_bwd_workspace_bytes")
+
+
+def rmsnorm_dropout_bwd(dy, h, w, dresidual_out, dresidual, dx, dw, rows, hidden, eps, weight_bias, p_drop, rng, dtype,
+                        workspace, workspace_bytes, stream=0):
+    _check(rmsnorm_dropout_bwd_status(dy, h, w, dresidual_out, dresidual, dx, dw, rows, hidden, eps, weight_bias,
+                                      p_drop, rng, dtype, workspace, workspace_bytes, stream), "rmsnorm_dropout_bwd")
+
+
+def rmsnorm_dropout_bwd_status(dy, h, w, dresidual_out, dresidual, dx, dw, rows, hidden, eps, weight_bias, p_drop, rng,
+                               dtype, workspace, workspace_bytes, stream=0) -> int:
+    return load().rmsnorm_dropout_bwd(dy, h, w, dresidual_out, dresidual, dx, dw, rows, hidden, eps, weight_bias,
+                                      p_drop, rng, dtype, workspace, workspace_bytes, stream)
 
 
 def rmsnorm_fwd_mxfp8(x, residual, w, codes, scales, residual_out, rows, hidden, eps, weight_bias, dtype,

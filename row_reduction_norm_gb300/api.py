@@ -397,6 +397,125 @@ def qkv_append(qkv: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     return q_out
 
 
+def _rows_of(t: torch.Tensor, name: str):
+    """(rows, hidden) of a contiguous CUDA tensor."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
+    if t.dim() < 1 or t.shape[-1] < 1:
+        raise ValueError(f"{name} must have a last dimension of at least one element")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.numel() // t.shape[-1], t.shape[-1]
+
+
+def _like(t, name, x):
+    if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {tuple(x.shape)} tensor of {x.dtype} on {x.device}")
+
+
+def _rng_arg(rng, p, like):
+    if rng is None:
+        if p:
+            raise ValueError("dropout needs rng, an int64 tensor of seed and offset")
+        return None
+    if rng.device != like.device or rng.dtype not in (torch.int64, torch.uint64) or rng.numel() != 2 or \
+            not rng.is_contiguous():
+        raise ValueError(f"rng must be a contiguous int64 tensor of seed and offset on {like.device}")
+    return rng.data_ptr()
+
+
+def rms_norm_dropout(x: torch.Tensor, residual: torch.Tensor, p: float, rng: Optional[torch.Tensor],
+                     w: Optional[torch.Tensor] = None, eps: float = 1e-6, weight_bias: float = 0.0,
+                     out: Optional[torch.Tensor] = None, residual_out: Optional[torch.Tensor] = None,
+                     stream: Optional[torch.cuda.Stream] = None):
+    """Residual dropout and RMSNorm in one launch: returns (y, residual_out),
+    residual_out = residual + dropout(x), y = its norm.
+
+    ``rng`` is a CUDA int64 tensor (seed, offset), read when the kernel runs;
+    the same values give the same mask, which is never stored, so a step that
+    wants another mask changes the offset.  ``p`` is rounded to a multiple of
+    2^-16, and kept elements are scaled by the inverse of the probability that
+    makes.
+    """
+    code = dtype_code(x.dtype)
+    rows, hidden = _rows_of(x, "x")
+    _like(residual, "residual", x)
+    _vector(w, "w", hidden, x)
+    r = _rng_arg(rng, p, x)
+    if out is None:
+        out = _empty(x.shape, x.dtype, x.device, stream)
+    else:
+        _like(out, "out", x)
+    if residual_out is None:
+        residual_out = _empty(x.shape, x.dtype, x.device, stream)
+    else:
+        _like(residual_out, "residual_out", x)
+    _launch(x.device, stream, N.rmsnorm_dropout_fwd, _ptr(x), _ptr(residual), _ptr(w), _ptr(out), _ptr(residual_out),
+            rows, hidden, eps, weight_bias, p, r, code)
+    return out, residual_out
+
+
+def _backward_args(dy, h, w, dresidual_out, workspace, stream):
+    rows, hidden = _rows_of(dy, "dy")
+    _like(h, "h", dy)
+    if dresidual_out is not None:
+        _like(dresidual_out, "dresidual_out", dy)
+    _vector(w, "w", hidden, dy)
+    if w is None:
+        return rows, hidden, None, None, 0
+    dw = _empty((hidden,), dy.dtype, dy.device, stream)
+    with torch.cuda.device(dy.device):
+        need = N.rmsnorm_bwd_workspace_bytes(rows, hidden, dtype_code(dy.dtype))
+    return rows, hidden, dw, _workspace(workspace, need, dy.device, stream), need
+
+
+def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, w: Optional[torch.Tensor] = None,
+                      dresidual_out: Optional[torch.Tensor] = None, eps: float = 1e-6, weight_bias: float = 0.0,
+                      out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                      stream: Optional[torch.cuda.Stream] = None):
+    """Gradient of ``rms_norm``: returns (dx, dw), dw None without a weight.
+
+    ``h`` is what was normalised: x, or residual_out with a residual, whose
+    gradient dx then is too.  ``dresidual_out``, the gradient that reaches h
+    past the norm, is added.  ``workspace``: a CUDA uint8 tensor of
+    ``rmsnorm_bwd_workspace_bytes(rows, hidden, dtype)`` bytes (allocated when
+    not given).
+    """
+    code = dtype_code(dy.dtype)
+    rows, hidden, dw, workspace, need = _backward_args(dy, h, w, dresidual_out, workspace, stream)
+    if out is None:
+        out = _empty(dy.shape, dy.dtype, dy.device, stream)
+    else:
+        _like(out, "out", dy)
+    _launch(dy.device, stream, N.rmsnorm_bwd, _ptr(dy), _ptr(h), _ptr(w), _ptr(dresidual_out), _ptr(out), _ptr(dw),
+            rows, hidden, eps, weight_bias, code, _ptr(workspace), need)
+    return out, dw
+
+
+def rms_norm_dropout_backward(dy: torch.Tensor, h: torch.Tensor, p: float, rng: Optional[torch.Tensor],
+                              w: Optional[torch.Tensor] = None, dresidual_out: Optional[torch.Tensor] = None,
+                              eps: float = 1e-6, weight_bias: float = 0.0, dresidual: Optional[torch.Tensor] = None,
+                              dx: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                              stream: Optional[torch.cuda.Stream] = None):
+    """Gradient of ``rms_norm_dropout`` (``h``: its residual_out, with the same
+    ``p`` and ``rng``): returns (dresidual, dx, dw), dw None without a weight.
+    Other arguments as ``rms_norm_backward``."""
+    code = dtype_code(dy.dtype)
+    rows, hidden, dw, workspace, need = _backward_args(dy, h, w, dresidual_out, workspace, stream)
+    r = _rng_arg(rng, p, dy)
+    if dresidual is None:
+        dresidual = _empty(dy.shape, dy.dtype, dy.device, stream)
+    else:
+        _like(dresidual, "dresidual", dy)
+    if dx is None:
+        dx = _empty(dy.shape, dy.dtype, dy.device, stream)
+    else:
+        _like(dx, "dx", dy)
+    _launch(dy.device, stream, N.rmsnorm_dropout_bwd, _ptr(dy), _ptr(h), _ptr(w), _ptr(dresidual_out), _ptr(dresidual),
+            _ptr(dx), _ptr(dw), rows, hidden, eps, weight_bias, p, r, code, _ptr(workspace), need)
+    return dresidual, dx, dw
+
+
 def qk_plan_for(qkv: torch.Tensor, q_heads: int, k_heads: int, head_dim: int, q_w=None, k_w=None,
                 out=None) -> N.Plan:
     """The plan ``qk_norm`` would launch for these tensors."""

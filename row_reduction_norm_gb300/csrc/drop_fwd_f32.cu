@@ -1,0 +1,35 @@
+// f32 register-kernel instantiations of the residual dropout's forward.
+#include "dropout_kernels.cuh"
+#include "dropout_pick.h"
+
+namespace rrn {
+namespace {
+
+template <typename T, int GT>
+const void *of_ch(int ch) {
+    switch (ch) {
+        case 1: return reinterpret_cast<const void *>(&drop_fwd_kernel<T, GT, 1>);
+        case 2: return reinterpret_cast<const void *>(&drop_fwd_kernel<T, GT, 2>);
+        case 3: return reinterpret_cast<const void *>(&drop_fwd_kernel<T, GT, 3>);
+        case 4: return reinterpret_cast<const void *>(&drop_fwd_kernel<T, GT, 4>);
+        default: return nullptr;
+    }
+}
+
+}  // namespace
+
+const void *drop_fwd_f32(int gt, int ch) {
+    if (gt == 512 && ch == 6) return reinterpret_cast<const void *>(&drop_fwd_kernel<F32, 512, 6>);
+    if (gt == 512 && ch == 8) return reinterpret_cast<const void *>(&drop_fwd_kernel<F32, 512, 8>);
+    switch (gt) {
+        case 8: return of_ch<F32, 8>(ch);
+        case 32: return of_ch<F32, 32>(ch);
+        case 64: return of_ch<F32, 64>(ch);
+        case 128: return of_ch<F32, 128>(ch);
+        case 256: return of_ch<F32, 256>(ch);
+        case 512: return of_ch<F32, 512>(ch);
+        default: return nullptr;
+    }
+}
+
+}  // namespace rrn

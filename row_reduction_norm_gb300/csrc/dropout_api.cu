@@ -1,0 +1,249 @@
+// dropout_api.cu -- entry points of the residual dropout fused with RMSNorm
+// and of RMSNorm's gradient (declared in include/rmsnorm.h): argument checks,
+// the choice of a kernel and its grid, the launch.
+#include <climits>
+#include <cmath>
+#include <cstring>
+#include <mutex>
+
+#include "dropout_kernels.cuh"
+#include "dropout_pick.h"
+#include "launch_util.h"
+
+namespace {
+
+using rrn::div_up;
+
+constexpr int64_t kMaxHidden = 65536;
+// Rows the two-pass gradient keeps its sums of dw for in shared memory: 192
+// KB of sums and 6 KB of mask bits within the 227 KB of a block.
+constexpr int64_t kSmemSums = 49152;
+constexpr int kMaxSmem = 226 * 1024;
+
+// Blocks a SM of the gradient at most: each keeps a row of fp32 sums, which
+// are written and read once more.
+int64_t blocks_a_sm(int64_t hidden) { return hidden <= 2048 ? 4 : hidden <= 16384 ? 2 : 1; }
+
+int check_rows(const void *const *ptrs, int n, int64_t rows, int64_t hidden, float eps, float w_bias, const void *w,
+               int dtype) {
+    if (dtype != RMSNORM_F32 && dtype != RMSNORM_BF16) return RMSNORM_EINVAL;
+    if (rows < 0 || hidden <= 0) return RMSNORM_EINVAL;
+    if (!std::isfinite(eps) || eps < 0.f || !std::isfinite(w_bias)) return RMSNORM_EINVAL;
+    if (hidden > kMaxHidden) return RMSNORM_EUNSUPPORTED;
+    if (w_bias != 0.f && w == nullptr) return RMSNORM_EINVAL;
+    const int64_t s = rrn::size_of(dtype);
+    if (rows > INT64_MAX / 8 / (hidden * s)) return RMSNORM_EINVAL;
+    for (int i = 0; i < n; ++i)
+        if (!rrn::on_boundary(ptrs[i], s)) return RMSNORM_EINVAL;
+    return RMSNORM_OK;
+}
+
+bool vec_ok(const void *const *ptrs, int n, int64_t hidden, int dtype) {
+    if (hidden * rrn::size_of(dtype) % 16 != 0) return false;
+    for (int i = 0; i < n; ++i)
+        if (!rrn::on_boundary(ptrs[i], 16)) return false;
+    return true;
+}
+
+// Dropout probability as the 16-bit threshold it is rounded to.
+int threshold_of(float p, uint32_t *thr) {
+    if (!(p >= 0.f) || !(p < 1.f)) return RMSNORM_EINVAL;
+    const double t = std::floor((double)p * 65536.0 + 0.5);
+    if (t > 65535.0) return RMSNORM_EINVAL;
+    *thr = (uint32_t)t;
+    return RMSNORM_OK;
+}
+
+// Threads a row (of those compiled) and chunks a thread that hold `nch`
+// chunks, about four a thread; false when they are too many.
+bool reg_shape(int64_t nch, int max_ch, int *gt, int *ch) {
+    for (int g : rrn::kDropGT) {
+        const int64_t need = div_up(nch, g);
+        if (need <= 4) {
+            *gt = g;
+            *ch = (int)need;
+            return true;
+        }
+        if (g == 512 && need <= max_ch) {
+            *gt = g;
+            *ch = need <= 6 ? 6 : 8;
+            return true;
+        }
+    }
+    return false;
+}
+
+int loop_block(bool vec, int64_t hidden) { return vec || hidden > 4096 ? 1024 : 256; }
+
+// Opt a kernel in to large dynamic shared memory, once per device and kernel.
+int allow_smem(int dev, const void *fn) {
+    struct Entry {
+        int dev;
+        const void *fn;
+    };
+    static std::mutex mu;
+    static Entry done[256];
+    static int used = 0;
+    std::lock_guard<std::mutex> lk(mu);
+    for (int i = 0; i < used; ++i)
+        if (done[i].dev == dev && done[i].fn == fn) return RMSNORM_OK;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return RMSNORM_ECUDA;
+    }
+    if (used < 256) done[used++] = Entry{dev, fn};
+    return RMSNORM_OK;
+}
+
+void fill(rrn::DropParams *p, const void *w, int64_t rows, int64_t hidden, float eps, float w_bias, uint32_t thr,
+          const uint64_t *rng, int dtype) {
+    std::memset(p, 0, sizeof(*p));
+    p->w = w;
+    p->rng = rng;
+    p->rows = rows;
+    p->row_elems = hidden;
+    p->row_bytes = hidden * rrn::size_of(dtype);
+    p->blocks_per_row = div_up(hidden, 8);
+    p->thr = thr;
+    p->scale = (float)(65536.0 / (65536.0 - (double)thr));
+    p->hidden_f = (float)hidden;
+    p->eps = eps;
+    p->w_bias = w_bias;
+}
+
+int backward(const void *dy, const void *h, const void *w, const void *dh, void *dres, void *dx, void *dw, int64_t rows,
+             int64_t hidden, float eps, float w_bias, uint32_t thr, const uint64_t *rng, int dtype, void *workspace,
+             uint64_t workspace_bytes, rmsnorm_stream_t stream) {
+    const void *ptrs[] = {dy, h, w, dh, dres, dx, dw};
+    int st = check_rows(ptrs, 7, rows, hidden, eps, w_bias, w, dtype);
+    if (st != RMSNORM_OK) return st;
+    if (dw != nullptr && w == nullptr) return RMSNORM_EINVAL;
+    if (rows > 0 && (dy == nullptr || h == nullptr || dres == nullptr || dx == dres)) return RMSNORM_EINVAL;
+    if (rows == 0 && dw == nullptr) return RMSNORM_OK;
+    int dev = 0, sms = 0;
+    if ((st = rrn::current_device_sms(&dev, &sms)) != RMSNORM_OK) return st;
+    const int64_t most = blocks_a_sm(hidden) * sms;
+    if (dw != nullptr && (workspace == nullptr || !rrn::on_boundary(workspace, 16) ||
+                          workspace_bytes < (uint64_t)rmsnorm_bwd_workspace_bytes(rows, hidden, dtype)))
+        return RMSNORM_EINVAL;
+    int64_t blocks = 0;
+    if (rows > 0) {
+        rrn::DropParams p;
+        fill(&p, w, rows, hidden, eps, w_bias, thr, rng, dtype);
+        p.dy = dy;
+        p.h = h;
+        p.dh = dh;
+        p.dres = dres;
+        p.dx = dx;
+        p.partial = static_cast<float *>(workspace);
+        const bool vec = vec_ok(ptrs, 6, hidden, dtype);
+        const int V = 16 / rrn::size_of(dtype);
+        p.units = (int32_t)(vec ? hidden / V : hidden);
+        const void *fn;
+        int threads, gt = 0, ch = 0;
+        int64_t groups = rows;
+        size_t smem = 0;
+        if (vec && reg_shape(hidden / V, 4, &gt, &ch)) {
+            fn = dtype == RMSNORM_BF16 ? rrn::drop_bwd_bf16(gt, ch, dw != nullptr)
+                                       : rrn::drop_bwd_f32(gt, ch, dw != nullptr);
+            threads = rrn::drop_block_threads(gt);
+            groups = div_up(rows, threads / gt);
+            if (dw != nullptr && threads > gt) smem = (size_t)hidden * sizeof(float);
+        } else {
+            threads = loop_block(vec, hidden);
+            fn = rrn::drop_bwd_loop(dtype, vec, threads, dw != nullptr);
+            p.acc_in_smem = dw != nullptr && hidden <= kSmemSums;
+            smem = (p.acc_in_smem ? (size_t)hidden * sizeof(float) : 0) + (size_t)(thr ? p.blocks_per_row : 0);
+            if (smem > 48 * 1024 && (st = allow_smem(dev, fn)) != RMSNORM_OK) return st;
+        }
+        if (fn == nullptr) return RMSNORM_EINVAL;
+        int resident = 0;
+        if ((st = rrn::resident_blocks(dev, fn, threads, smem, &resident)) != RMSNORM_OK) return st;
+        blocks = (int64_t)sms * resident;
+        if (dw != nullptr && blocks > most) blocks = most;
+        if (blocks > groups) blocks = groups;
+        void *argv[] = {&p};
+        st = rrn::launch_kernel(fn, dim3((unsigned)blocks), threads, smem, stream, argv);
+        if (st != RMSNORM_OK) return st;
+    }
+    if (dw == nullptr) return RMSNORM_OK;
+    return rrn::launch_colsum(static_cast<const float *>(workspace), (int)blocks, hidden, hidden, dw, nullptr, dtype,
+                              stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+int rmsnorm_dropout_fwd(const void *x, const void *residual, const void *w, void *y, void *residual_out, int64_t rows,
+                        int64_t hidden, float eps, float weight_bias, float p_drop, const uint64_t *rng, int dtype,
+                        rmsnorm_stream_t stream) {
+    const void *ptrs[] = {x, residual, w, y, residual_out};
+    int st = check_rows(ptrs, 5, rows, hidden, eps, weight_bias, w, dtype);
+    if (st != RMSNORM_OK) return st;
+    uint32_t thr = 0;
+    if ((st = threshold_of(p_drop, &thr)) != RMSNORM_OK) return st;
+    if (rows == 0) return RMSNORM_OK;
+    if (x == nullptr || residual == nullptr || y == nullptr || residual_out == nullptr || y == residual_out)
+        return RMSNORM_EINVAL;
+    if (thr != 0 && (rng == nullptr || !rrn::on_boundary(rng, 8))) return RMSNORM_EINVAL;
+    rrn::DropParams p;
+    fill(&p, w, rows, hidden, eps, weight_bias, thr, rng, dtype);
+    p.x = x;
+    p.res = residual;
+    p.y = y;
+    p.h_out = residual_out;
+    const bool vec = vec_ok(ptrs, 5, hidden, dtype);
+    const int V = 16 / rrn::size_of(dtype);
+    p.units = (int32_t)(vec ? hidden / V : hidden);
+    const void *fn;
+    int threads, gt = 0, ch = 0;
+    int64_t blocks = rows;
+    size_t smem = 0;
+    if (vec && reg_shape(hidden / V, 8, &gt, &ch)) {
+        fn = dtype == RMSNORM_BF16 ? rrn::drop_fwd_bf16(gt, ch) : rrn::drop_fwd_f32(gt, ch);
+        threads = rrn::drop_block_threads(gt);
+        blocks = div_up(rows, threads / gt);
+    } else {
+        threads = loop_block(vec, hidden);
+        fn = rrn::drop_fwd_loop(dtype, vec, threads);
+        smem = (size_t)(thr ? p.blocks_per_row : 0);
+    }
+    if (fn == nullptr) return RMSNORM_EINVAL;
+    if (blocks > INT_MAX) blocks = INT_MAX;
+    void *argv[] = {&p};
+    return rrn::launch_kernel(fn, dim3((unsigned)blocks), threads, smem, stream, argv);
+}
+
+int64_t rmsnorm_bwd_workspace_bytes(int64_t rows, int64_t hidden, int dtype) {
+    if ((dtype != RMSNORM_F32 && dtype != RMSNORM_BF16) || rows < 0 || hidden <= 0) return RMSNORM_EINVAL;
+    if (hidden > kMaxHidden) return RMSNORM_EUNSUPPORTED;
+    int dev = 0, sms = 0;
+    const int st = rrn::current_device_sms(&dev, &sms);
+    if (st != RMSNORM_OK) return st;
+    int64_t blocks = blocks_a_sm(hidden) * sms;
+    if (blocks > rows) blocks = rows > 0 ? rows : 1;
+    return blocks * hidden * (int64_t)sizeof(float);
+}
+
+int rmsnorm_bwd(const void *dy, const void *h, const void *w, const void *dresidual_out, void *dx, void *dw,
+                int64_t rows, int64_t hidden, float eps, float weight_bias, int dtype, void *workspace,
+                uint64_t workspace_bytes, rmsnorm_stream_t stream) {
+    return backward(dy, h, w, dresidual_out, dx, nullptr, dw, rows, hidden, eps, weight_bias, 0, nullptr, dtype,
+                    workspace, workspace_bytes, stream);
+}
+
+int rmsnorm_dropout_bwd(const void *dy, const void *h, const void *w, const void *dresidual_out, void *dresidual,
+                        void *dx, void *dw, int64_t rows, int64_t hidden, float eps, float weight_bias, float p_drop,
+                        const uint64_t *rng, int dtype, void *workspace, uint64_t workspace_bytes,
+                        rmsnorm_stream_t stream) {
+    uint32_t thr = 0;
+    const int st = threshold_of(p_drop, &thr);
+    if (st != RMSNORM_OK) return st;
+    if (rows > 0 && (dx == nullptr || (thr != 0 && (rng == nullptr || !rrn::on_boundary(rng, 8)))))
+        return RMSNORM_EINVAL;
+    return backward(dy, h, w, dresidual_out, dresidual, dx, dw, rows, hidden, eps, weight_bias, thr, rng, dtype,
+                    workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,514 @@
+// dropout_kernels.cuh -- residual dropout fused with RMSNorm, and the
+// gradient of RMSNorm with and without it.
+//
+// Forward, per row:   h = RN_T(residual + keep * s * x),  y = RN_T(h r (w + b)),
+//                     r = rsqrt(mean(h^2) + eps)
+// Gradient, per row:  g = dy (w + b),  d = r (g - h r^2 mean(g h)) + dh
+//                     dresidual = RN_T(d),  dx = RN_T(keep * s * d)
+//                     dw = sum over rows of dy h r
+//
+// The mask is never stored: keep is a function of the seed, the offset and
+// the element's place, so the gradient makes the same one again.  Elements
+// 8 k .. 8 k + 7 of a row share one call of the Philox4x32-10 generator
+// (Salmon, Moraes, Dror, Shaw: "Parallel random numbers: as easy as 1, 2, 3",
+// SC 2011) at counter (row * ceil(hidden / 8) + k, offset) under key seed: its
+// 128 bits are eight 16-bit numbers, element e takes number e % 8, low half
+// of a word first, and is kept when that is at least thr = round(65536 p).
+// Sixteen bits an element halve the generator's work against 32 (about 8
+// integer instructions an element, hidden behind the row's loads); the kept
+// elements are scaled by s = 65536 / (65536 - thr), the inverse of the
+// probability with which they are really kept, so the mean is exact.
+#pragma once
+
+#include "rmsnorm_kernels.cuh"
+
+namespace rrn {
+
+struct DropParams {
+    const void *x, *res, *w;     // forward: x, residual;  w nullable
+    const void *dy, *h, *dh;     // gradient: dh (of residual_out) nullable
+    void *y, *h_out;             // forward
+    void *dres, *dx;             // gradient: dx only with dropout
+    float *partial;              // gradient: [blocks][row_elems] sums of dw, or NULL
+    const uint64_t *rng;         // seed, offset
+    int64_t rows;
+    int64_t row_elems, row_bytes;
+    int64_t blocks_per_row;      // ceil(row_elems / 8): generator calls a row
+    int32_t units;               // loads a row
+    uint32_t thr;                // 0: no dropout
+    float scale;
+    float hidden_f, eps, w_bias;
+    int32_t acc_in_smem;         // two-pass gradient: dw sums in shared memory, else in partial
+};
+
+// --------------------------------------------------------------- generator
+
+__device__ __forceinline__ uint4 philox(uint64_t seed, uint64_t offset, uint64_t index) {
+    uint32_t c0 = (uint32_t)index, c1 = (uint32_t)(index >> 32);
+    uint32_t c2 = (uint32_t)offset, c3 = (uint32_t)(offset >> 32);
+    uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
+#pragma unroll
+    for (int r = 0; r < 10; ++r) {
+        const uint64_t p = (uint64_t)c0 * 0xD2511F53u, q = (uint64_t)c2 * 0xCD9E8D57u;
+        c0 = (uint32_t)(q >> 32) ^ c1 ^ k0;
+        c1 = (uint32_t)q;
+        c2 = (uint32_t)(p >> 32) ^ c3 ^ k1;
+        c3 = (uint32_t)p;
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return make_uint4(c0, c1, c2, c3);
+}
+
+__device__ __forceinline__ uint32_t keep2(uint32_t word, uint32_t thr) {
+    return (uint32_t)((word & 0xffffu) >= thr) | ((uint32_t)((word >> 16) >= thr) << 1);
+}
+
+// Bit e of the result: whether element e of the 8-element block is kept.
+__device__ __forceinline__ uint32_t keep_block(uint64_t seed, uint64_t offset, uint64_t index, uint32_t thr) {
+    const uint4 u = philox(seed, offset, index);
+    return keep2(u.x, thr) | (keep2(u.y, thr) << 2) | (keep2(u.z, thr) << 4) | (keep2(u.w, thr) << 6);
+}
+
+// The V bits of 16-byte chunk u of a row (a block, or half a one).
+template <int V>
+__device__ __forceinline__ uint32_t keep_chunk(uint64_t seed, uint64_t offset, int64_t row_block, int u, uint32_t thr) {
+    if constexpr (V == 8) {
+        return keep_block(seed, offset, (uint64_t)(row_block + u), thr);
+    } else {
+        return keep_block(seed, offset, (uint64_t)(row_block + u / 2), thr) >> (4 * (u & 1));
+    }
+}
+
+__host__ __device__ constexpr int drop_block_threads(int gt) { return gt >= 256 ? gt : 256; }
+
+// Sums of two values over a row's GT threads (every thread of the block calls).
+template <int GT>
+__device__ __forceinline__ float2 row_sums(float a, float b, float2 (*red)[GT > 32 ? GT / 32 : 1], int slot, int t) {
+    constexpr int LANES = GT < 32 ? GT : 32, WPR = GT > 32 ? GT / 32 : 1;
+#pragma unroll
+    for (int off = LANES / 2; off > 0; off >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, off);
+        b += __shfl_xor_sync(0xffffffffu, b, off);
+    }
+    if constexpr (WPR > 1) {
+        if ((t & 31) == 0) red[slot][t / 32] = make_float2(a, b);
+        __syncthreads();
+        float va[WPR], vb[WPR];
+#pragma unroll
+        for (int i = 0; i < WPR; ++i) {
+            const float2 v = red[slot][i];
+            va[i] = v.x;
+            vb[i] = v.y;
+        }
+        a = tree_sum(va);
+        b = tree_sum(vb);
+    }
+    return make_float2(a, b);
+}
+
+// ----------------------------------------------------------------- forward
+// The register kernel's layout: GT threads a row, CH chunks a thread.
+template <typename T, int GT, int CH>
+__global__ void __launch_bounds__(drop_block_threads(GT)) drop_fwd_kernel(const DropParams p) {
+    constexpr int V = T::kVec, BLOCK = drop_block_threads(GT), RPB = BLOCK / GT;
+    __shared__ float2 red[2][RPB][GT > 32 ? GT / 32 : 1];
+    const int tid = threadIdx.x, slot = tid / GT, t = tid % GT;
+    pdl_wait_for_inputs();
+    pdl_allow_dependents();
+    uint64_t seed = 0, offset = 0;
+    if (p.thr) {
+        seed = p.rng[0];
+        offset = p.rng[1];
+    }
+    int parity = 0;
+    for (int64_t first = (int64_t)blockIdx.x * RPB; first < p.rows; first += (int64_t)gridDim.x * RPB) {
+        const int64_t row = first + slot;
+        const bool ok = row < p.rows;
+        const int64_t off = row * p.row_bytes;
+        Chunk xc[CH], hc[CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int u = c * GT + t;
+            const bool in = ok && u < p.units;
+            xc[c] = in ? ld_stream16(static_cast<const char *>(p.x) + off + (int64_t)u * 16) : Chunk{{0u, 0u, 0u, 0u}};
+            hc[c] = in ? ld_stream16(static_cast<const char *>(p.res) + off + (int64_t)u * 16) : Chunk{{0u, 0u, 0u, 0u}};
+        }
+        float acc[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = 0.f;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int u = c * GT + t;
+            const uint32_t keep = p.thr ? keep_chunk<V>(seed, offset, row * p.blocks_per_row, u, p.thr) : 0xffu;
+            float a[V], b[V];
+            unpack(xc[c], a, T{});
+            unpack(hc[c], b, T{});
+#pragma unroll
+            for (int e = 0; e < V; ++e) a[e] = add_round(b[e], (keep >> e) & 1u ? a[e] * p.scale : 0.f, T{});
+            hc[c] = pack(a, T{});
+            if (ok && u < p.units) st16(static_cast<char *>(p.h_out) + off + (int64_t)u * 16, hc[c]);
+            sq_accumulate(a, acc);
+        }
+        const float sum = row_sums<GT>(tree_sum(acc), 0.f, red[parity], slot, t).x;
+        parity ^= 1;
+        const float r = rsqrtf(sum / p.hidden_f + p.eps);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int u = c * GT + t;
+            if (ok && u < p.units) {
+                float a[V], wv[V];
+                unpack(hc[c], a, T{});
+                if (p.w != nullptr) {
+                    unpack(ld_readonly16(static_cast<const char *>(p.w) + (int64_t)u * 16), wv, T{});
+                    scale_out_pairs<kWeightBias>(a, r, wv, p.w_bias);
+                } else {
+                    scale_out_pairs<kNoWeight>(a, r, wv, 0.f);
+                }
+                st16(static_cast<char *>(p.y) + off + (int64_t)u * 16, pack(a, T{}));
+            }
+        }
+    }
+}
+
+// Masks of a row as bits in shared memory (one byte a generator call), by the
+// whole block; the caller syncs around it.
+__device__ __forceinline__ void stage_mask(const DropParams &p, uint8_t *mask, uint64_t seed, uint64_t offset, int64_t row) {
+    for (int k = threadIdx.x; k < (int)p.blocks_per_row; k += blockDim.x)
+        mask[k] = (uint8_t)keep_block(seed, offset, (uint64_t)(row * p.blocks_per_row + k), p.thr);
+}
+
+// V bits of unit u (VE elements) out of the staged mask.
+template <int VE>
+__device__ __forceinline__ uint32_t staged_keep(const uint8_t *mask, int64_t u) {
+    if constexpr (VE == 8) return mask[u];
+    else if constexpr (VE == 4) return mask[u >> 1] >> (4 * (int)(u & 1));
+    else return mask[u >> 3] >> (int)(u & 7);
+}
+
+// Two passes over a row by a whole block, for rows without 16-byte alignment
+// (VE = 1) or too long for registers: the second pass reads h back from L2.
+template <typename T, int VE, int BLOCK>
+__global__ void __launch_bounds__(BLOCK) drop_fwd_loop_kernel(const DropParams p) {
+    using IO = UnitIO<T, VE>;
+    using Raw = typename IO::Raw;
+    constexpr int U = VE == 1 ? 8 : 2;
+    __shared__ float2 red[2][1][BLOCK / 32];
+    extern __shared__ uint8_t mask[];   // [blocks_per_row], with dropout
+    const int tid = threadIdx.x;
+    const int64_t n = p.units;
+    pdl_wait_for_inputs();
+    pdl_allow_dependents();
+    uint64_t seed = 0, offset = 0;
+    if (p.thr) {
+        seed = p.rng[0];
+        offset = p.rng[1];
+    }
+    int parity = 0;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        const int64_t off = row * p.row_bytes;
+        const void *xr = static_cast<const char *>(p.x) + off, *rr = static_cast<const char *>(p.res) + off;
+        void *hr = static_cast<char *>(p.h_out) + off, *yr = static_cast<char *>(p.y) + off;
+        if (p.thr) {
+            stage_mask(p, mask, seed, offset, row);   // the last row's readers are behind its sum's barrier
+            __syncthreads();
+        }
+        float acc[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+        for (int64_t base = tid; base < n; base += (int64_t)BLOCK * U) {
+            Raw xa[U], ra[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int64_t u = base + (int64_t)j * BLOCK;
+                xa[j] = u < n ? IO::load_last(xr, u) : IO::zero();
+                ra[j] = u < n ? IO::load_last(rr, u) : IO::zero();
+            }
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int64_t u = base + (int64_t)j * BLOCK;
+                if (u >= n) break;
+                const uint32_t keep = p.thr ? staged_keep<VE>(mask, u) : 0xffu;
+                float a[VE], b[VE];
+                IO::widen(xa[j], a);
+                IO::widen(ra[j], b);
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    a[e] = add_round(b[e], (keep >> e) & 1u ? a[e] * p.scale : 0.f, T{});
+                    const int k = (j * VE + e) & 7;
+                    acc[k] = fmaf(a[e], a[e], acc[k]);
+                }
+                IO::store(hr, u, a);
+            }
+        }
+        const float sum = row_sums<BLOCK>(tree_sum(acc), 0.f, red[parity], 0, tid).x;
+        parity ^= 1;
+        const float r = rsqrtf(sum / p.hidden_f + p.eps);
+        for (int64_t base = tid; base < n; base += (int64_t)BLOCK * U) {
+            Raw ha[U], wa[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int64_t u = base + (int64_t)j * BLOCK;
+                ha[j] = u < n ? IO::load_last(hr, u) : IO::zero();
+                wa[j] = u < n && p.w != nullptr ? IO::load_w(p.w, u) : IO::zero();
+            }
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int64_t u = base + (int64_t)j * BLOCK;
+                if (u >= n) break;
+                float a[VE], wv[VE];
+                IO::widen(ha[j], a);
+                IO::widen(wa[j], wv);
+#pragma unroll
+                for (int e = 0; e < VE; ++e)
+                    a[e] = p.w != nullptr ? (a[e] * r) * (wv[e] + p.w_bias) : a[e] * r;
+                IO::store(yr, u, a);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- gradient
+// Persistent blocks of RPB row slots; a thread keeps its columns' share of dw
+// in registers over all its rows, the slots are added up in order at the end
+// and the block's sums go to partial[block].
+template <typename T, int GT, int CH, bool DW>
+__global__ void __launch_bounds__(drop_block_threads(GT)) drop_bwd_kernel(const DropParams p) {
+    constexpr int V = T::kVec, BLOCK = drop_block_threads(GT), RPB = BLOCK / GT;
+    __shared__ float2 red[2][RPB][GT > 32 ? GT / 32 : 1];
+    extern __shared__ float slots[];   // [row_elems], with DW and RPB > 1
+    const int tid = threadIdx.x, slot = tid / GT, t = tid % GT;
+    pdl_wait_for_inputs();
+    pdl_allow_dependents();
+    uint64_t seed = 0, offset = 0;
+    if (p.thr) {
+        seed = p.rng[0];
+        offset = p.rng[1];
+    }
+    float dw[DW ? CH : 1][V];
+#pragma unroll
+    for (int c = 0; c < (DW ? CH : 1); ++c)
+#pragma unroll
+        for (int e = 0; e < V; ++e) dw[c][e] = 0.f;
+    Chunk wc[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int u = c * GT + t;
+        wc[c] = p.w != nullptr && u < p.units ? ld_readonly16(static_cast<const char *>(p.w) + (int64_t)u * 16)
+                                              : Chunk{{0u, 0u, 0u, 0u}};
+    }
+    int parity = 0;
+    for (int64_t first = (int64_t)blockIdx.x * RPB; first < p.rows; first += (int64_t)gridDim.x * RPB) {
+        const int64_t row = first + slot;
+        const bool ok = row < p.rows;
+        const int64_t off = row * p.row_bytes;
+        Chunk gc[CH], hc[CH], dc[CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int u = c * GT + t;
+            const bool in = ok && u < p.units;
+            gc[c] = in ? ld_stream16(static_cast<const char *>(p.dy) + off + (int64_t)u * 16) : Chunk{{0u, 0u, 0u, 0u}};
+            hc[c] = in ? ld_stream16(static_cast<const char *>(p.h) + off + (int64_t)u * 16) : Chunk{{0u, 0u, 0u, 0u}};
+        }
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int u = c * GT + t;
+            dc[c] = ok && u < p.units && p.dh != nullptr
+                        ? ld_stream16(static_cast<const char *>(p.dh) + off + (int64_t)u * 16)
+                        : Chunk{{0u, 0u, 0u, 0u}};
+        }
+        float sq[V], dot[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) sq[e] = dot[e] = 0.f;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            float h[V], g[V], w[V];
+            unpack(hc[c], h, T{});
+            unpack(gc[c], g, T{});
+            unpack(wc[c], w, T{});
+            sq_accumulate(h, sq);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                if (p.w != nullptr) g[e] *= w[e] + p.w_bias;
+                dot[e] = fmaf(g[e], h[e], dot[e]);
+            }
+        }
+        const float2 s = row_sums<GT>(tree_sum(sq), tree_sum(dot), red[parity], slot, t);
+        parity ^= 1;
+        // an idle slot's zeros must add nothing, whatever eps is
+        const float r = ok ? rsqrtf(s.x / p.hidden_f + p.eps) : 0.f;
+        const float m = (r * r) * (s.y / p.hidden_f);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int u = c * GT + t;
+            float h[V], g[V], w[V], d[V];
+            unpack(hc[c], h, T{});
+            unpack(gc[c], g, T{});
+            unpack(wc[c], w, T{});
+            unpack(dc[c], d, T{});
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                if constexpr (DW) dw[c][e] = fmaf(g[e], h[e] * r, dw[c][e]);
+                if (p.w != nullptr) g[e] *= w[e] + p.w_bias;
+                const float v = r * (g[e] - h[e] * m);
+                d[e] = p.dh != nullptr ? v + d[e] : v;
+            }
+            if (ok && u < p.units) {
+                st16(static_cast<char *>(p.dres) + off + (int64_t)u * 16, pack(d, T{}));
+                if (p.dx != nullptr) {
+                    const uint32_t keep = p.thr ? keep_chunk<V>(seed, offset, row * p.blocks_per_row, u, p.thr) : 0xffu;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) d[e] = (keep >> e) & 1u ? d[e] * p.scale : 0.f;
+                    st16(static_cast<char *>(p.dx) + off + (int64_t)u * 16, pack(d, T{}));
+                }
+            }
+        }
+    }
+    if constexpr (DW) {
+        float *out = p.partial + (int64_t)blockIdx.x * p.row_elems;
+        if constexpr (RPB > 1) {
+            for (int s = 0; s < RPB; ++s) {
+                if (slot == s) {
+#pragma unroll
+                    for (int c = 0; c < CH; ++c) {
+                        const int u = c * GT + t;
+                        if (u < p.units)
+#pragma unroll
+                            for (int e = 0; e < V; ++e)
+                                slots[u * V + e] = s == 0 ? dw[c][e] : slots[u * V + e] + dw[c][e];
+                    }
+                }
+                __syncthreads();
+            }
+            for (int i = tid; i < (int)p.row_elems; i += BLOCK) out[i] = slots[i];
+        } else {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const int u = c * GT + t;
+                if (u < p.units)
+#pragma unroll
+                    for (int e = 0; e < V; e += 4)
+                        *reinterpret_cast<float4 *>(out + (int64_t)u * V + e) =
+                            make_float4(dw[c][e], dw[c][e + 1], dw[c][e + 2], dw[c][e + 3]);
+            }
+        }
+    }
+}
+
+// Two passes over a row by a whole block (rows without 16-byte alignment, or
+// too long for registers).  A thread owns the same columns of every row, so
+// its sums of dw need no barrier; they sit in shared memory, or, for rows too
+// long for it, in the block's own row of `partial` (in L2).
+template <typename T, int VE, int BLOCK, bool DW>
+__global__ void __launch_bounds__(BLOCK) drop_bwd_loop_kernel(const DropParams p) {
+    using IO = UnitIO<T, VE>;
+    using Raw = typename IO::Raw;
+    constexpr int U = VE == 1 ? 4 : 2;
+    __shared__ float2 red[2][1][BLOCK / 32];
+    extern __shared__ float sums[];   // [row_elems] with acc_in_smem, then the mask's bytes
+    const int tid = threadIdx.x;
+    const int64_t n = p.units;
+    float *out = DW ? p.partial + (int64_t)blockIdx.x * p.row_elems : nullptr;
+    float *acc = DW && p.acc_in_smem ? sums : out;
+    uint8_t *mask = reinterpret_cast<uint8_t *>(sums + (DW && p.acc_in_smem ? p.row_elems : 0));
+    pdl_wait_for_inputs();
+    pdl_allow_dependents();
+    uint64_t seed = 0, offset = 0;
+    if (p.thr) {
+        seed = p.rng[0];
+        offset = p.rng[1];
+    }
+    if constexpr (DW) {
+        for (int64_t u = tid; u < n; u += BLOCK)
+#pragma unroll
+            for (int e = 0; e < VE; ++e) acc[u * VE + e] = 0.f;
+    }
+    int parity = 0;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        const int64_t off = row * p.row_bytes;
+        const void *gr = static_cast<const char *>(p.dy) + off, *hr = static_cast<const char *>(p.h) + off;
+        const void *dr = p.dh != nullptr ? static_cast<const char *>(p.dh) + off : nullptr;
+        void *outr = static_cast<char *>(p.dres) + off;
+        void *xr = p.dx != nullptr ? static_cast<char *>(p.dx) + off : nullptr;
+        float sq[8], dot[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sq[i] = dot[i] = 0.f;
+        for (int64_t base = tid; base < n; base += (int64_t)BLOCK * U) {
+            Raw ga[U], ha[U], wa[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int64_t u = base + (int64_t)j * BLOCK;
+                ga[j] = u < n ? IO::load_first(gr, u) : IO::zero();
+                ha[j] = u < n ? IO::load_first(hr, u) : IO::zero();
+                wa[j] = u < n && p.w != nullptr ? IO::load_w(p.w, u) : IO::zero();
+            }
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                float g[VE], h[VE], w[VE];
+                IO::widen(ga[j], g);
+                IO::widen(ha[j], h);
+                IO::widen(wa[j], w);
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    if (p.w != nullptr) g[e] *= w[e] + p.w_bias;
+                    const int k = (j * VE + e) & 7;
+                    sq[k] = fmaf(h[e], h[e], sq[k]);
+                    dot[k] = fmaf(g[e], h[e], dot[k]);
+                }
+            }
+        }
+        if (p.thr) {
+            if (BLOCK == 32) __syncwarp();
+            stage_mask(p, mask, seed, offset, row);   // read after the sums' barrier
+        }
+        const float2 s = row_sums<BLOCK>(tree_sum(sq), tree_sum(dot), red[parity], 0, tid);
+        parity ^= 1;
+        const float r = rsqrtf(s.x / p.hidden_f + p.eps);
+        const float m = (r * r) * (s.y / p.hidden_f);
+        for (int64_t base = tid; base < n; base += (int64_t)BLOCK * U) {
+            Raw ga[U], ha[U], wa[U], da[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int64_t u = base + (int64_t)j * BLOCK;
+                ga[j] = u < n ? IO::load_last(gr, u) : IO::zero();
+                ha[j] = u < n ? IO::load_last(hr, u) : IO::zero();
+                wa[j] = u < n && p.w != nullptr ? IO::load_w(p.w, u) : IO::zero();
+                da[j] = u < n && dr != nullptr ? IO::load_last(dr, u) : IO::zero();
+            }
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int64_t u = base + (int64_t)j * BLOCK;
+                if (u >= n) break;
+                float g[VE], h[VE], w[VE], d[VE];
+                IO::widen(ga[j], g);
+                IO::widen(ha[j], h);
+                IO::widen(wa[j], w);
+                IO::widen(da[j], d);
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    if constexpr (DW) acc[u * VE + e] = fmaf(g[e], h[e] * r, acc[u * VE + e]);
+                    if (p.w != nullptr) g[e] *= w[e] + p.w_bias;
+                    const float v = r * (g[e] - h[e] * m);
+                    d[e] = dr != nullptr ? v + d[e] : v;
+                }
+                IO::store(outr, u, d);
+                if (xr != nullptr) {
+                    const uint32_t keep = p.thr ? staged_keep<VE>(mask, u) : 0xffu;
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) d[e] = (keep >> e) & 1u ? d[e] * p.scale : 0.f;
+                    IO::store(xr, u, d);
+                }
+            }
+        }
+        if (p.thr) __syncthreads();   // the mask is read before the next row's is staged
+    }
+    if constexpr (DW) {
+        if (p.acc_in_smem) {
+            for (int64_t u = tid; u < n; u += BLOCK)
+#pragma unroll
+                for (int e = 0; e < VE; ++e) out[u * VE + e] = sums[u * VE + e];
+        }
+    }
+}
+
+}  // namespace rrn
