@@ -13,9 +13,6 @@ namespace {
 
 using rrn::div_up;
 
-// Warps a launch spreads over before a warp is given more than one head
-// iteration of a token: the resident warps of 16 a SM.
-constexpr int kSpreadWarps = 16;
 // Blocks of the gradient kernel at most (its workspace is sized for them).
 constexpr int kBwdMaxBlocks = 1024;
 
@@ -70,7 +67,7 @@ int make_rope(int64_t tokens, int64_t x_stride, int32_t q_heads, int32_t k_heads
     p->v_heads = v_heads;
     p->head_dim = (int32_t)head_dim;
     p->norm = norm;
-    p->head_dim_f = (float)head_dim;
+    p->inv_dim = 1.f / (float)head_dim;
     p->eps = eps;
     p->w_bias = w_bias;
     p->pos = rope->positions;
@@ -92,9 +89,8 @@ bool stride_ok(int64_t stride, int64_t width, int64_t tokens, int64_t s) {
 }
 
 // The widest shape that the head's halves, and every address and stride of
-// the call (all multiples of `unit` elements), allow.  A head is held by the
-// fewest lanes, a power of two, so that more heads run side by side; but by
-// the most where pieces are narrower than 16 bytes, so that neighbouring
+// the call (all multiples of `unit` elements), allow; a head is held by as
+// many lanes as it has units, up to a power of two, so that neighbouring
 // lanes read neighbouring pieces.
 int pick_shape(int dtype, int64_t unit, rrn::RopeParams *p) {
     const rrn::RopeShape *table = dtype == RMSNORM_BF16 ? rrn::kRopeShapesBf16 : rrn::kRopeShapesF32;
@@ -120,31 +116,16 @@ struct Unit {
     int64_t get() const { return (int64_t)(bits & (~bits + 1)); }
 };
 
-struct Grid {
-    dim3 blocks;
-    int threads;
-    size_t smem;
-};
+// Warps a block: eight, fewer while that leaves a SM without a block.
+int block_warps(int64_t work, int sms) {
+    int warps = rrn::kRopeMaxWarps;
+    while (warps > 1 && work < (int64_t)warps * sms) warps /= 2;
+    return warps;
+}
 
-// Slices of a token's heads and warps a block: tokens times slices fill the
-// device where they can, one warp a block while there are fewer than SMs.
-Grid forward_grid(int sms, rrn::RopeParams *p) {
-    const int hpw = 32 / p->lanes;
-    const int64_t iters = div_up((int64_t)p->q_heads + p->k_heads + p->v_heads, hpw);
-    const int64_t want = (int64_t)sms * kSpreadWarps;
-    int64_t slices = div_up(want, p->tokens);
-    if (slices > iters) slices = iters;
-    if (slices > 65535) slices = 65535;
-    p->iters = (int32_t)div_up(iters, slices);
-    slices = div_up(iters, p->iters);
-    int warps = 1;
-    while (warps < rrn::kRopeMaxWarps && 2 * warps <= p->tokens && p->tokens * slices / (2 * warps) >= sms) warps *= 2;
-    Grid g;
-    const int64_t x = div_up(p->tokens, warps);
-    g.blocks = dim3((unsigned)(x < INT_MAX ? x : INT_MAX), (unsigned)slices);
-    g.threads = 32 * warps;
-    g.smem = (size_t)warps * 2 * p->R * sizeof(float);
-    return g;
+// Shared memory of a block: turn fractions, each warp's angles.
+size_t angle_bytes(const rrn::RopeParams *p, int warps) {
+    return (size_t)((p->R + 1) & ~1) * sizeof(uint64_t) + (size_t)warps * 2 * p->R * sizeof(float);
 }
 
 const void *forward_kernel(int dtype, int shape, bool il, int mode) {
@@ -158,9 +139,20 @@ int launch_forward(rrn::RopeParams *p, int dtype, int64_t unit, bool il, int mod
     const int shape = pick_shape(dtype, unit, p);
     const void *fn = forward_kernel(dtype, shape, il, mode);
     if (fn == nullptr) return RMSNORM_EINVAL;
-    const Grid g = forward_grid(sms, p);
+    // a run of head iterations for every warp of a resident grid, or one
+    // iteration a warp while there are fewer
+    p->per = (int32_t)div_up((int64_t)p->q_heads + p->k_heads + p->v_heads, 32 / p->lanes);
+    const int64_t work = p->tokens * p->per;
+    const int warps = block_warps(work, sms);
+    const size_t smem = angle_bytes(p, warps);
+    int resident = 0;
+    if ((st = rrn::resident_blocks(dev, fn, 32 * warps, smem, &resident)) != RMSNORM_OK) return st;
+    int64_t blocks = (int64_t)sms * resident;
+    if (blocks > div_up(work, warps)) blocks = div_up(work, warps);
+    p->each = work / (blocks * warps);
+    p->extra = work % (blocks * warps);
     void *argv[] = {p};
-    return rrn::launch_kernel(fn, g.blocks, g.threads, g.smem, stream, argv);
+    return rrn::launch_kernel(fn, dim3((unsigned)blocks), 32 * warps, smem, stream, argv);
 }
 
 }  // namespace
@@ -241,15 +233,21 @@ int rmsnorm_qk_rope_bwd(const void *dy, const void *x, void *dx, int64_t tokens,
                                                : rrn::rope_bwd_f32(shape, il, norm == 1);
         if (fn == nullptr) return RMSNORM_EINVAL;
         const int hpw = 32 / p.lanes;
-        const int64_t work = tokens * (div_up(q_heads, hpw) + div_up(k_heads, hpw));
-        int warps = rrn::kRopeMaxWarps;
-        while (warps > 1 && work < (int64_t)warps * sms) warps /= 2;
-        const size_t smem = (size_t)warps * (2 * p.R + p.head_dim) * sizeof(float);
+        p.per = (int32_t)div_up(q_heads, hpw);
+        p.per_k = (int32_t)div_up(k_heads, hpw);
+        const int64_t work = tokens * (p.per + p.per_k);
+        const int warps = block_warps(work, sms);
+        const size_t smem = angle_bytes(&p, warps) + (size_t)rrn::rope_weight_floats(dtype, shape) * sizeof(float) +
+                            (size_t)(dq_w != nullptr ? warps * head_dim : 0) * sizeof(float);
         int resident = 0;
         if ((st = rrn::resident_blocks(dev, fn, 32 * warps, smem, &resident)) != RMSNORM_OK) return st;
         blocks = (int64_t)sms * resident;
         if (blocks > kBwdMaxBlocks) blocks = kBwdMaxBlocks;
         if (blocks > div_up(work, warps)) blocks = div_up(work, warps);
+        p.each = tokens * p.per / (blocks * warps);
+        p.extra = tokens * p.per % (blocks * warps);
+        p.each_k = tokens * p.per_k / (blocks * warps);
+        p.extra_k = tokens * p.per_k % (blocks * warps);
         void *argv[] = {&p};
         st = rrn::launch_kernel(fn, dim3((unsigned)blocks), 32 * warps, smem, stream, argv);
         if (st != RMSNORM_OK) return st;

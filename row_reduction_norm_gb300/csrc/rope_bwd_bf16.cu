@@ -15,10 +15,10 @@ const void *one(bool norm) {
 
 const void *rope_bwd_bf16(int shape, bool il, bool norm) {
     switch (shape) {
-        case 0: return il ? one<BF16, 8, 1, 2, true>(norm) : one<BF16, 8, 1, 2, false>(norm);
-        case 1: return il ? one<BF16, 4, 1, 2, true>(norm) : one<BF16, 4, 1, 2, false>(norm);
+        case 0: return il ? one<BF16, 8, 1, 1, true>(norm) : one<BF16, 8, 1, 1, false>(norm);
+        case 1: return il ? one<BF16, 4, 1, 1, true>(norm) : one<BF16, 4, 1, 1, false>(norm);
         case 2: return il ? one<BF16, 4, 2, 1, true>(norm) : one<BF16, 4, 2, 1, false>(norm);
-        case 3: return il ? one<BF16, 2, 2, 2, true>(norm) : one<BF16, 2, 2, 2, false>(norm);
+        case 3: return il ? one<BF16, 2, 2, 1, true>(norm) : one<BF16, 2, 2, 1, false>(norm);
         case 4: return il ? one<BF16, 1, 8, 1, true>(norm) : one<BF16, 1, 8, 1, false>(norm);
         default: return nullptr;
     }

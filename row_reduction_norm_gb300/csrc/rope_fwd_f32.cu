@@ -24,10 +24,10 @@ const void *mode_of(bool il, int mode) {
 
 const void *rope_fwd_f32(int shape, bool il, int mode) {
     switch (shape) {
-        case 0: return mode_of<F32, 4, 1, 4>(il, mode);
+        case 0: return mode_of<F32, 4, 1, 2>(il, mode);
         case 1: return mode_of<F32, 4, 2, 2>(il, mode);
-        case 2: return mode_of<F32, 2, 2, 4>(il, mode);
-        case 3: return mode_of<F32, 1, 8, 2>(il, mode);
+        case 2: return mode_of<F32, 2, 2, 2>(il, mode);
+        case 3: return mode_of<F32, 1, 8, 1>(il, mode);
         default: return nullptr;
     }
 }

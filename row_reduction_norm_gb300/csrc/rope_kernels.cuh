@@ -13,9 +13,11 @@
 // Work layout.  A lane owns K "units" of a head: unit u is VE pairs, held as
 // two pieces of VE elements, so both halves of every pair sit in one lane and
 // the rotation needs no exchange.  G lanes share a head, 32 / G heads run
-// side by side in a warp, and a warp walks the heads of one token: the
-// token's sines and cosines are computed once per warp (each pair by one
-// lane) and shared through shared memory behind warp syncs only.
+// side by side in a warp (a head iteration), and the batch's iterations are
+// cut into equal runs, one a warp, whose next loads are under way while the
+// present heads are worked on.  A token's sines and cosines are computed once
+// by each warp that is at the token (each pair by one lane) and shared through
+// shared memory behind warp syncs only.
 //
 // Angles.  Positions are integers, so only the fraction of a turn per step
 // matters: inv_freq / 2 pi is held as a 64-bit fixed-point fraction of a turn
@@ -32,6 +34,8 @@ namespace rrn {
 constexpr int kRopeMaxDim = 512;      // head_dim
 constexpr int kRopeMaxAxes = 4;
 constexpr int kRopeMaxWarps = 8;      // warps a block
+// Blocks a SM that a shape's registers are budgeted for.
+__host__ __device__ constexpr int rope_resident(int ve, int k) { return ve * k <= 8 && ve > 1 && !(ve == 4 && k == 2) ? 2 : 1; }
 
 struct RopeParams {
     const void *x;            // packed token rows (query, key, [value] heads)
@@ -44,7 +48,7 @@ struct RopeParams {
     int32_t q_heads, k_heads, v_heads;       // v_heads: append only
     int32_t head_dim;
     int32_t norm;
-    float head_dim_f, eps, w_bias;
+    float inv_dim, eps, w_bias;
     // rotation
     const void *pos;          // [axes][pos_stride], 32 or 64 bit; append: NULL = index in the cache
     int64_t pos_stride;
@@ -54,7 +58,8 @@ struct RopeParams {
     int32_t R;
     int32_t units, rot_units; // pair units of a head, and the rotated ones among them
     int32_t lanes;            // G: lanes a head, a power of two
-    int32_t iters;            // head iterations a slice of a token's heads takes
+    int32_t per, per_k;       // head iterations a token (gradient: of its query, its key heads)
+    int64_t each, extra, each_k, extra_k;   // a warp's run of them: each, one more for the first `extra`
     // paged cache (append)
     const int32_t *cu_tokens, *cache_lens, *page_table;
     int64_t table_stride;
@@ -85,7 +90,27 @@ struct Piece {
         for (int i = 0; i < kWords; ++i) r.u[i] = 0u;
         return r;
     }
-    // Streamed (read once) loads; weights take the read-only path.
+    // Weights: read by every warp, kept in L1.
+    __device__ static __forceinline__ Raw load_w(const char *p) {
+        Raw r;
+        if constexpr (kBytes == 2) {
+            r.u[0] = *reinterpret_cast<const uint16_t *>(p);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) r.u[i] = 0u;
+            if constexpr (kBytes == 16) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(p);
+                r.u[0] = v.x, r.u[1] = v.y, r.u[2] = v.z, r.u[3] = v.w;
+            } else if constexpr (kBytes == 8) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(p);
+                r.u[0] = v.x, r.u[1] = v.y;
+            } else {
+                r.u[0] = *reinterpret_cast<const uint32_t *>(p);
+            }
+        }
+        return r;
+    }
+    // Streamed (read once) loads.
     __device__ static __forceinline__ Raw load(const char *p) {
         Raw r;
         if constexpr (kBytes == 16) {
@@ -177,25 +202,81 @@ __device__ __forceinline__ void unit_offsets(const RopeParams &p, int u, int &a,
     }
 }
 
-// Pair j of a unit held as va, vb: interleaved pairs are neighbours.
+// The 2 x 2 turn of each pair, with whatever weights the caller folded in:
+//   y_a = ca x_a + cb x_b,   y_b = cc x_a + cd x_b
+// two fp32 operations an instruction.  Half split: the unit's pieces are the
+// pairs' first and second elements; interleaved: neighbours are a pair.
+template <int VE>
+struct Turn {
+    float ca[VE], cb[VE], cc[VE], cd[VE];
+};
+
 template <int VE, bool IL>
-__device__ __forceinline__ void turn_unit(float (&va)[VE], float (&vb)[VE], const float (&c)[VE], const float (&s)[VE]) {
-    if constexpr (IL && VE > 1) {
+__device__ __forceinline__ void turn_unit(float (&xa)[VE], float (&xb)[VE], const Turn<VE> &m) {
+    if constexpr (VE == 1) {
+        const float a = xa[0], b = xb[0];
+        xa[0] = fmaf(m.ca[0], a, m.cb[0] * b);
+        xb[0] = fmaf(m.cc[0], a, m.cd[0] * b);
+    } else if constexpr (IL) {
 #pragma unroll
-        for (int j = 0; j < VE / 2; ++j) {
-            const float a0 = va[2 * j], b0 = va[2 * j + 1], a1 = vb[2 * j], b1 = vb[2 * j + 1];
-            va[2 * j] = a0 * c[j] - b0 * s[j];
-            va[2 * j + 1] = a0 * s[j] + b0 * c[j];
-            vb[2 * j] = a1 * c[VE / 2 + j] - b1 * s[VE / 2 + j];
-            vb[2 * j + 1] = a1 * s[VE / 2 + j] + b1 * c[VE / 2 + j];
+        for (int j = 0; j < VE; ++j) {
+            float (&x)[VE] = j < VE / 2 ? xa : xb;
+            const int e = 2 * (j % (VE / 2));
+            const float2 y = __ffma2_rn(make_float2(x[e], x[e]), make_float2(m.ca[j], m.cc[j]),
+                                        __fmul2_rn(make_float2(x[e + 1], x[e + 1]), make_float2(m.cb[j], m.cd[j])));
+            x[e] = y.x;
+            x[e + 1] = y.y;
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < VE; ++j) {
-            const float a = va[j], b = vb[j];
-            va[j] = a * c[j] - b * s[j];
-            vb[j] = a * s[j] + b * c[j];
+        for (int j = 0; j < VE; j += 2) {
+            const float2 a = make_float2(xa[j], xa[j + 1]), b = make_float2(xb[j], xb[j + 1]);
+            const float2 u = __ffma2_rn(make_float2(m.ca[j], m.ca[j + 1]), a,
+                                        __fmul2_rn(make_float2(m.cb[j], m.cb[j + 1]), b));
+            const float2 v = __ffma2_rn(make_float2(m.cc[j], m.cc[j + 1]), a,
+                                        __fmul2_rn(make_float2(m.cd[j], m.cd[j + 1]), b));
+            xa[j] = u.x, xa[j + 1] = u.y;
+            xb[j] = v.x, xb[j + 1] = v.y;
         }
+    }
+}
+
+// x *= r, and x *= w elementwise; sums of products.
+template <int VE>
+__device__ __forceinline__ void scale_by(float (&x)[VE], float r) {
+    if constexpr (VE == 1) {
+        x[0] *= r;
+    } else {
+#pragma unroll
+        for (int j = 0; j < VE; j += 2) {
+            const float2 v = __fmul2_rn(make_float2(x[j], x[j + 1]), make_float2(r, r));
+            x[j] = v.x, x[j + 1] = v.y;
+        }
+    }
+}
+
+template <int VE>
+__device__ __forceinline__ void times(float (&x)[VE], const float (&w)[VE]) {
+    if constexpr (VE == 1) {
+        x[0] *= w[0];
+    } else {
+#pragma unroll
+        for (int j = 0; j < VE; j += 2) {
+            const float2 v = __fmul2_rn(make_float2(x[j], x[j + 1]), make_float2(w[j], w[j + 1]));
+            x[j] = v.x, x[j + 1] = v.y;
+        }
+    }
+}
+
+// acc += x * y, elements of either parity in a sum of their own.
+template <int VE>
+__device__ __forceinline__ void dot_into(float2 &acc, const float (&x)[VE], const float (&y)[VE]) {
+    if constexpr (VE == 1) {
+        acc.x = fmaf(x[0], y[0], acc.x);
+    } else {
+#pragma unroll
+        for (int j = 0; j < VE; j += 2)
+            acc = __ffma2_rn(make_float2(x[j], x[j + 1]), make_float2(y[j], y[j + 1]), acc);
     }
 }
 
@@ -221,16 +302,25 @@ __device__ __forceinline__ uint64_t turn_fraction(float f) {
 
 // Sine and cosine of position * fraction turns: the nearest quarter turn is
 // taken off in integers, so what is rounded to fp32 is at most an eighth of a
-// turn.
+// turn, t in [-pi/4, pi/4], where the Taylor series up to t^9 and t^10 are off
+// by t^11 / 11! < 2e-9 and t^12 / 12! < 2e-10.
 __device__ __forceinline__ void sincos_turns(uint64_t phase, float &s, float &c) {
-    const uint32_t t = (uint32_t)((phase + 0x80000000ull) >> 32);   // 2^-32 turns
-    const uint32_t q = (t + 0x20000000u) >> 30;
-    const int32_t rem = (int32_t)(t - (q << 30));                   // [-2^29, 2^29)
-    float sr, cr;
-    sincospif((float)rem * 4.656612873077392578125e-10f, &sr, &cr); // 2^-31: half turns
+    const uint32_t t32 = (uint32_t)((phase + 0x80000000ull) >> 32);   // 2^-32 turns
+    const uint32_t q = (t32 + 0x20000000u) >> 30;
+    const float t = (float)(int32_t)(t32 - (q << 30)) * 1.46291807926715968e-9f;   // 2 pi / 2^32
+    const float z = t * t;
+    float sr = fmaf(z, 2.75573192e-6f, -1.98412698e-4f);   // 1/9!, -1/7!, 1/5!, -1/3!
+    sr = fmaf(z, sr, 8.33333333e-3f);
+    sr = fmaf(z, sr, -1.66666667e-1f);
+    sr = fmaf(t * z, sr, t);
+    float cr = fmaf(z, -2.75573192e-7f, 2.48015873e-5f);   // -1/10!, 1/8!, -1/6!, 1/4!, -1/2!
+    cr = fmaf(z, cr, -1.38888889e-3f);
+    cr = fmaf(z, cr, 4.16666667e-2f);
+    cr = fmaf(z, cr, -0.5f);
+    cr = fmaf(z, cr, 1.f);
     const float ss = (q & 1u) ? cr : sr, cc = (q & 1u) ? sr : cr;
-    s = (q & 2u) ? -ss : ss;
-    c = ((q + 1u) & 2u) ? -cc : cc;
+    s = __uint_as_float(__float_as_uint(ss) ^ ((q & 2u) << 30));
+    c = __uint_as_float(__float_as_uint(cc) ^ (((q + 1u) & 2u) << 30));
 }
 
 __device__ __forceinline__ int axis_of(const RopeParams &p, int i) {
@@ -242,82 +332,131 @@ __device__ __forceinline__ int64_t position_of(const RopeParams &p, int axis, in
     return p.pos64 ? static_cast<const int64_t *>(p.pos)[at] : (int64_t)static_cast<const int32_t *>(p.pos)[at];
 }
 
-// The token's cosines and sines into the warp's shared memory (cs[0 .. R) and
-// cs[R .. 2R)), pair i by lane i % 32.  given: positions come from p.pos,
-// else every pair takes `index`.
-__device__ __forceinline__ void stage_angles(const RopeParams &p, float *cs, int lane, int64_t token, bool given,
-                                             int64_t index) {
+// Shared memory of a block: the pairs' turn fractions [R] (once a block),
+// then for each warp the cosines and sines [2][R] of the token it is at.
+__device__ __forceinline__ void stage_fractions(const RopeParams &p, uint64_t *frac) {
+    for (int i = threadIdx.x; i < p.R; i += blockDim.x) frac[i] = turn_fraction(p.inv_freq[i]);
+    __syncthreads();
+}
+
+// The token's cosines and sines, pair i by lane i % 32.  given: positions
+// come from p.pos, else every pair takes `index`.
+__device__ __forceinline__ void stage_angles(const RopeParams &p, const uint64_t *frac, float *cs, int lane,
+                                             int64_t token, bool given, int64_t index) {
     __syncwarp();   // the warp's reads of the previous token's angles are done
     for (int i = lane; i < p.R; i += 32) {
         const int64_t at = given ? position_of(p, axis_of(p, i), token) : index;
         float s, c;
-        sincos_turns((uint64_t)at * turn_fraction(p.inv_freq[i]), s, c);
+        sincos_turns((uint64_t)at * frac[i], s, c);
         cs[i] = c;
         cs[p.R + i] = s;
     }
     __syncwarp();
 }
 
-// A lane's angles out of the staged ones.
-template <int VE, int K>
-struct Angles {
-    float c[K][VE], s[K][VE];
-    __device__ __forceinline__ void read(const RopeParams &p, const float *cs, int t) {
+// VE consecutive fp32 values out of shared memory (16-byte aligned where VE
+// is a multiple of 4: R is then one too).
+template <int VE>
+__device__ __forceinline__ void read_floats(const float *p, float (&v)[VE]) {
+    if constexpr (VE % 4 == 0) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int u = t + k * p.lanes;
-            if (u < p.rot_units) {
-                const float *pc = cs + u * VE, *ps = pc + p.R;
-                if constexpr (VE % 4 == 0) {   // R is a multiple of VE: 16-byte aligned
-#pragma unroll
-                    for (int j = 0; j < VE; j += 4) {
-                        const float4 a = *reinterpret_cast<const float4 *>(pc + j);
-                        const float4 b = *reinterpret_cast<const float4 *>(ps + j);
-                        c[k][j] = a.x, c[k][j + 1] = a.y, c[k][j + 2] = a.z, c[k][j + 3] = a.w;
-                        s[k][j] = b.x, s[k][j + 1] = b.y, s[k][j + 2] = b.z, s[k][j + 3] = b.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < VE; ++j) {
-                        c[k][j] = pc[j];
-                        s[k][j] = ps[j];
-                    }
-                }
-            }
+        for (int j = 0; j < VE; j += 4) {
+            const float4 a = *reinterpret_cast<const float4 *>(p + j);
+            v[j] = a.x, v[j + 1] = a.y, v[j + 2] = a.z, v[j + 3] = a.w;
         }
+    } else {
+#pragma unroll
+        for (int j = 0; j < VE; ++j) v[j] = p[j];
     }
-};
+}
 
 // Sum over the G lanes of a head (G a power of two, run-time).
 __device__ __forceinline__ float lanes_sum(float v, int g) {
-    for (int off = g >> 1; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    if (g > 1) v += __shfl_xor_sync(0xffffffffu, v, 1);
+    if (g > 2) v += __shfl_xor_sync(0xffffffffu, v, 2);
+    if (g > 4) v += __shfl_xor_sync(0xffffffffu, v, 4);
+    if (g > 8) v += __shfl_xor_sync(0xffffffffu, v, 8);
+    if (g > 16) v += __shfl_xor_sync(0xffffffffu, v, 16);
     return v;
 }
 
-// The head weights (w + bias) of a lane's units; 1 without a weight.
-template <typename T, int VE, int K, bool IL>
-__device__ __forceinline__ void read_weight(const RopeParams &p, const void *w, int t, float (&wa)[K][VE],
-                                            float (&wb)[K][VE]) {
+// The head weights (w + bias) of unit u; 1 without a weight.
+template <typename T, int VE, bool IL>
+__device__ __forceinline__ void read_weight(const RopeParams &p, const void *w, int u, float (&wa)[VE], float (&wb)[VE]) {
     using P = Piece<T, VE>;
     constexpr int S = (int)sizeof(typename T::storage);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
+    for (int j = 0; j < VE; ++j) wa[j] = wb[j] = 1.f;
+    if (w != nullptr && u < p.units) {
+        int a, b;
+        unit_offsets<VE, IL>(p, u, a, b);
+        P::widen(P::load_w(static_cast<const char *>(w) + a * S), wa);
+        P::widen(P::load_w(static_cast<const char *>(w) + b * S), wb);
 #pragma unroll
-        for (int j = 0; j < VE; ++j) wa[k][j] = wb[k][j] = 1.f;
-        const int u = t + k * p.lanes;
-        if (w != nullptr && u < p.units) {
-            int a, b;
-            unit_offsets<VE, IL>(p, u, a, b);
-            P::widen(P::load(static_cast<const char *>(w) + (int64_t)a * S), wa[k]);
-            P::widen(P::load(static_cast<const char *>(w) + (int64_t)b * S), wb[k]);
-#pragma unroll
-            for (int j = 0; j < VE; ++j) {
-                wa[k][j] += p.w_bias;
-                wb[k][j] += p.w_bias;
-            }
+        for (int j = 0; j < VE; ++j) {
+            wa[j] += p.w_bias;
+            wb[j] += p.w_bias;
         }
     }
 }
+
+// The turn of unit u with the weight of its elements folded in (y = turn of
+// w x); units past the rotated part hold w in ca and cd alone, which the
+// caller applies without the cross terms.
+template <typename T, int VE, bool IL>
+__device__ __forceinline__ void weighted_turn(const RopeParams &p, const float *cs, const void *w, int u, Turn<VE> &m) {
+    float wa[VE], wb[VE];
+    read_weight<T, VE, IL>(p, w, u, wa, wb);
+    if (u < p.rot_units) {
+        float c[VE], s[VE];
+        read_floats<VE>(cs + u * VE, c);
+        read_floats<VE>(cs + p.R + u * VE, s);
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+            // the weights of pair j's two elements
+            const float w0 = !IL || VE == 1 ? wa[j] : (2 * j < VE ? wa[(2 * j) % VE] : wb[(2 * j) % VE]);
+            const float w1 = !IL || VE == 1 ? wb[j] : (2 * j < VE ? wa[(2 * j + 1) % VE] : wb[(2 * j + 1) % VE]);
+            m.ca[j] = w0 * c[j];
+            m.cb[j] = -w1 * s[j];
+            m.cc[j] = w0 * s[j];
+            m.cd[j] = w1 * c[j];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+            m.ca[j] = wa[j];
+            m.cd[j] = wb[j];
+            m.cb[j] = m.cc[j] = 0.f;
+        }
+    }
+}
+
+// The flat list of head iterations (32 / G heads of one token each, `per` a
+// token) cut into equal runs, one a warp.
+struct Run {
+    int64_t token, at, end;
+    int it;
+    __device__ __forceinline__ void start(int64_t warp, int64_t each, int64_t extra, int per) {
+        at = warp * each + (warp < extra ? warp : extra);
+        end = at + each + (warp < extra ? 1 : 0);
+        token = ((at | per) >> 32) == 0 ? (int64_t)((uint32_t)at / (uint32_t)per) : at / per;
+        it = (int)(at - token * per);
+    }
+    // Iterations of the run from here on that are of this token, at most n.
+    __device__ __forceinline__ int count(int per, int n) const {
+        const int64_t left = end - at;
+        const int c = per - it < n ? per - it : n;
+        return left < c ? (int)left : c;
+    }
+    __device__ __forceinline__ void advance(int n, int per) {
+        at += n;
+        it += n;
+        if (it == per) {
+            it = 0;
+            ++token;
+        }
+    }
+};
 
 // ------------------------------------------------------------ paged cache
 
@@ -354,279 +493,357 @@ __device__ __forceinline__ int64_t cache_row(const RopeParams &p, int seq, int64
 enum RopeMode { kRopePlain = 0, kRopeAppend = 1, kRopeAppendE4m3 = 2 };
 
 // ----------------------------------------------------------------- forward
-// grid.x: groups of blockDim / 32 tokens, one a warp; grid.y: slices of a
-// token's heads.  UN head iterations are loaded before the first is used.
+// UN head iterations are loaded while the UN before them are worked on.  A
+// value's weight is folded into its token's turn, so a head costs its sum of
+// squares, one 2 x 2 turn a pair and one product with r.
 template <typename T, int VE, int K, bool IL, int MODE, int UN>
-__global__ void __launch_bounds__(32 * kRopeMaxWarps) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(VE, K)) rope_kernel(const RopeParams p) {
     using P = Piece<T, VE>;
     using Raw = typename P::Raw;
     constexpr int S = (int)sizeof(typename T::storage);
     constexpr bool APPEND = MODE != kRopePlain;
-    extern __shared__ __align__(16) float cs_all[];
+    extern __shared__ __align__(16) unsigned char smem[];
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int G = p.lanes, t = lane & (G - 1), group = lane / G, hpw = 32 / G;
-    float *cs = cs_all + warp * 2 * p.R;
-    const int heads = p.q_heads + p.k_heads + p.v_heads;
-    const int turned = p.q_heads + p.k_heads;
-    const int first = blockIdx.y * p.iters * hpw;
-    const int last = first + p.iters * hpw < heads ? first + p.iters * hpw : heads;
+    uint64_t *frac = reinterpret_cast<uint64_t *>(smem);
+    float *cs = reinterpret_cast<float *>(frac + ((p.R + 1) & ~1)) + warp * 2 * p.R;
+    const int heads = p.q_heads + p.k_heads + p.v_heads, turned = p.q_heads + p.k_heads;
+    const int per = p.per;
 
-    int oa[K], ob[K];   // byte offsets of the lane's pieces in a head
+    int oa[K], ob[K];   // byte offsets of the lane's pieces in a head; -1: no unit
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        int a = 0, b = 0;
-        if (t + k * G < p.units) unit_offsets<VE, IL>(p, t + k * G, a, b);
-        oa[k] = a;
-        ob[k] = b;
+        oa[k] = ob[k] = -1;
+        if (t + k * G < p.units) {
+            unit_offsets<VE, IL>(p, t + k * G, oa[k], ob[k]);
+            oa[k] *= S;
+            ob[k] *= S;
+        }
     }
+    const int head_bytes = p.head_dim * S;
 
+    Run run;
+    run.start((int64_t)blockIdx.x * warps + warp, p.each, p.extra, per);
     pdl_wait_for_inputs();
     pdl_allow_dependents();
+    if constexpr (APPEND) {   // rows behind the last sequence are left as they are
+        const int64_t valid = p.cu_tokens[p.seqs];
+        const int64_t most = (valid < 0 ? 0 : valid) * per;
+        if (run.end > most) run.end = most;
+    }
 
-    for (int64_t token = (int64_t)blockIdx.x * warps + warp; token < p.tokens; token += (int64_t)gridDim.x * warps) {
-        int64_t index = 0, row = -1;
-        if constexpr (APPEND) {
-            if (token >= p.cu_tokens[p.seqs]) break;   // behind the last sequence: left as it is
-            const int seq = sequence_of(p, token, lane);
-            index = (int64_t)p.cache_lens[seq] + (token - p.cu_tokens[seq]);
-            row = cache_row(p, seq, index);
-            // the slice that holds the first key head counts the token
-            if (row < 0 && p.dropped != nullptr && lane == 0 && p.q_heads >= first && p.q_heads < last)
-                atomicAdd(p.dropped, 1);
-        }
-        const char *xr = static_cast<const char *>(p.x) + token * p.x_stride;
-        char *yr = static_cast<char *>(p.y) + token * p.y_stride;
-        if (first < turned) stage_angles(p, cs, lane, token, p.pos != nullptr, index);
-        Angles<VE, K> ang;
-        ang.read(p, cs, t);
-        float wa[K][VE], wb[K][VE];
-        int held = -1;   // whose weights the lane holds: 0 query, 1 key
-
-        for (int h0 = first; h0 < last; h0 += UN * hpw) {
-            Raw ra[UN][K], rb[UN][K];
+    auto load = [&](const Run &r, int n, Raw (&ra)[UN][K], Raw (&rb)[UN][K]) {
+        const char *src = static_cast<const char *>(p.x) + r.token * p.x_stride;
 #pragma unroll
-            for (int n = 0; n < UN; ++n) {
-                const int h = h0 + n * hpw + group;
+        for (int i = 0; i < UN; ++i) {
+            const int h = (r.it + i) * hpw + group;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                ra[i][k] = rb[i][k] = P::zero();
+                if (i < n && h < heads && oa[k] >= 0) {
+                    ra[i][k] = P::load(src + (h * head_bytes + oa[k]));
+                    rb[i][k] = P::load(src + (h * head_bytes + ob[k]));
+                }
+            }
+        }
+    };
+
+    int64_t row = -1;
+    int held = -1;              // whose weights are in m: 0 query, 1 key
+    Turn<VE> m[K];
+    // One batch: `now` holds it, the next one's loads go into `next`.
+    auto step = [&](Raw (&na)[UN][K], Raw (&nb)[UN][K], Raw (&xa)[UN][K], Raw (&xb)[UN][K], bool first) {
+        const int n = run.count(per, UN);
+        Run ahead = run;
+        ahead.advance(n, per);
+        const int more = ahead.count(per, UN);
+        if (more > 0) load(ahead, more, xa, xb);
+        if (first || run.it == 0) {   // a token the warp has not been at
+            int64_t index = 0;
+            if constexpr (APPEND) {
+                const int seq = sequence_of(p, run.token, lane);
+                index = (int64_t)p.cache_lens[seq] + (run.token - p.cu_tokens[seq]);
+                row = cache_row(p, seq, index);
+            }
+            if (run.it * hpw < turned) stage_angles(p, frac, cs, lane, run.token, p.pos != nullptr, index);
+            held = -1;
+        }
+        char *yr = static_cast<char *>(p.y) + run.token * p.y_stride;
+#pragma unroll
+        for (int i = 0; i < UN; ++i) {
+            if (i >= n) break;   // the same for every lane
+            const int h = (run.it + i) * hpw + group;
+            const bool value = APPEND && h >= turned;
+            float va[K][VE], vb[K][VE];
+            float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                P::widen(na[i][k], va[k]);
+                P::widen(nb[i][k], vb[k]);
+                dot_into<VE>(acc, va[k], va[k]);
+                dot_into<VE>(acc, vb[k], vb[k]);
+            }
+            float r = 1.f;
+            if (p.norm) r = rsqrtf(fmaf(lanes_sum(acc.x + acc.y, G), p.inv_dim, p.eps));
+            if (!value) {
+                const int kind = h >= p.q_heads;
+                if (kind != held) {
+                    held = kind;
+#pragma unroll
+                    for (int k = 0; k < K; ++k)
+                        weighted_turn<T, VE, IL>(p, cs, kind ? p.k_w : p.q_w, t + k * G, m[k]);
+                }
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
-                    ra[n][k] = rb[n][k] = P::zero();
-                    if (h < last && t + k * G < p.units) {
-                        const char *src = xr + (int64_t)h * p.head_dim * S;
-                        ra[n][k] = P::load(src + oa[k] * S);
-                        rb[n][k] = P::load(src + ob[k] * S);
+                    if (t + k * G < p.rot_units) {
+                        turn_unit<VE, IL>(va[k], vb[k], m[k]);
+                    } else {
+                        times<VE>(va[k], m[k].ca);
+                        times<VE>(vb[k], m[k].cd);
+                    }
+                    if (p.norm) {
+                        scale_by<VE>(va[k], r);
+                        scale_by<VE>(vb[k], r);
                     }
                 }
             }
+            if (!APPEND || h < p.q_heads) {
+                char *dst = yr + (int64_t)h * head_bytes;
 #pragma unroll
-            for (int n = 0; n < UN; ++n) {
-                if (h0 + n * hpw >= last) break;   // the same for every lane
-                const int h = h0 + n * hpw + group;
-                const bool value = APPEND && h >= turned;
-                float va[K][VE], vb[K][VE];
-#pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    P::widen(ra[n][k], va[k]);
-                    P::widen(rb[n][k], vb[k]);
-                }
-                if (p.norm) {
-                    float acc = 0.f;
-#pragma unroll
-                    for (int k = 0; k < K; ++k) {
-                        float sq[VE];
-#pragma unroll
-                        for (int j = 0; j < VE; ++j) sq[j] = fmaf(vb[k][j], vb[k][j], va[k][j] * va[k][j]);
-                        acc += tree_sum(sq);
+                for (int k = 0; k < K; ++k)
+                    if (h < heads && oa[k] >= 0) {
+                        P::store(dst + oa[k], va[k]);
+                        P::store(dst + ob[k], vb[k]);
                     }
-                    const float r = rsqrtf(lanes_sum(acc, G) / p.head_dim_f + p.eps);
-                    if (!value) {
-                        const int kind = h >= p.q_heads;
-                        if (kind != held) {
-                            read_weight<T, VE, K, IL>(p, kind ? p.k_w : p.q_w, t, wa, wb);
-                            held = kind;
-                        }
-#pragma unroll
-                        for (int k = 0; k < K; ++k)
-#pragma unroll
-                            for (int j = 0; j < VE; ++j) {
-                                va[k][j] = (va[k][j] * r) * wa[k][j];
-                                vb[k][j] = (vb[k][j] * r) * wb[k][j];
-                            }
-                    }
-                }
-                if (!value) {
-#pragma unroll
-                    for (int k = 0; k < K; ++k)
-                        if (t + k * G < p.rot_units) turn_unit<VE, IL>(va[k], vb[k], ang.c[k], ang.s[k]);
-                }
-                if (h >= last) continue;
-                if (!APPEND || h < p.q_heads) {
-                    char *dst = yr + (int64_t)h * p.head_dim * S;
-#pragma unroll
-                    for (int k = 0; k < K; ++k)
-                        if (t + k * G < p.units) {
-                            P::store(dst + oa[k] * S, va[k]);
-                            P::store(dst + ob[k] * S, vb[k]);
-                        }
-                } else if (row >= 0) {
+            } else {
+                if (row < 0) {
+                    if (h == p.q_heads && t == 0 && p.dropped != nullptr) atomicAdd(p.dropped, 1);
+                } else if (h < heads) {
                     const int j = value ? h - turned : h - p.q_heads;
                     char *dst = static_cast<char *>(value ? p.v_cache : p.k_cache) + row + (int64_t)j * p.head_stride;
 #pragma unroll
                     for (int k = 0; k < K; ++k)
-                        if (t + k * G < p.units) {
+                        if (oa[k] >= 0) {
                             if constexpr (MODE == kRopeAppendE4m3) {
                                 const float inv = value ? p.v_inv : p.k_inv;
-                                P::store_e4m3(dst + oa[k], va[k], inv);
-                                P::store_e4m3(dst + ob[k], vb[k], inv);
+                                P::store_e4m3(dst + oa[k] / S, va[k], inv);
+                                P::store_e4m3(dst + ob[k] / S, vb[k], inv);
                             } else {
-                                P::store(dst + oa[k] * S, va[k]);
-                                P::store(dst + ob[k] * S, vb[k]);
+                                P::store(dst + oa[k], va[k]);
+                                P::store(dst + ob[k], vb[k]);
                             }
                         }
                 }
             }
         }
+        run = ahead;
+    };
+
+    // the first loads are on their way while the block prepares its table
+    Raw ra[UN][K], rb[UN][K], sa[UN][K], sb[UN][K];
+    if (run.at < run.end) load(run, run.count(per, UN), ra, rb);
+    stage_fractions(p, frac);
+    bool first = true;
+    while (run.at < run.end) {
+        step(ra, rb, sa, sb, first);
+        first = false;
+        if (run.at >= run.end) break;
+        step(sa, sb, ra, rb, false);
     }
 }
 
 // ---------------------------------------------------------------- gradient
 // Persistent blocks.  The query heads of all tokens, then the key heads, are
-// a flat list of head iterations (32 / G heads of one token each); every warp
-// takes an equal run of it, keeps its share of the weight's gradient in
-// registers, and the block's sum goes to partial[block][kind][D].  The order
-// of every sum follows from the sizes and the grid: no atomics.
+// a flat list of head iterations each; every warp takes an equal run of it,
+// keeps its share of the weight's gradient in registers, and the block's sum
+// goes to partial[block][kind][D].  The order of every sum follows from the
+// sizes and the grid: no atomics.
 // x is read only with the norm; without it dx = dy turned back.
 template <typename T, int VE, int K, bool IL, bool NORM, int UN>
-__global__ void __launch_bounds__(32 * kRopeMaxWarps) rope_bwd_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(VE, K)) rope_bwd_kernel(const RopeParams p) {
     using P = Piece<T, VE>;
     using Raw = typename P::Raw;
     constexpr int S = (int)sizeof(typename T::storage);
-    extern __shared__ __align__(16) float cs_all[];
+    constexpr int KN = NORM ? K : 1, UX = NORM ? UN : 1;
+    extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int G = p.lanes, t = lane & (G - 1), group = lane / G, hpw = 32 / G;
+    uint64_t *frac = reinterpret_cast<uint64_t *>(smem);
+    float *cs_all = reinterpret_cast<float *>(frac + ((p.R + 1) & ~1));
     float *cs = cs_all + warp * 2 * p.R;
-    float *sums = cs_all + warps * 2 * p.R;   // [warps][D], with a weight
+    float *wsm = cs_all + warps * 2 * p.R;    // the kind's weight in lane order, with the norm
+    float *sums = wsm + (NORM ? K * VE * 64 : 0);   // [warps][D], with a weight's gradient
 
     int oa[K], ob[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        int a = 0, b = 0;
-        if (t + k * G < p.units) unit_offsets<VE, IL>(p, t + k * G, a, b);
-        oa[k] = a;
-        ob[k] = b;
+        oa[k] = ob[k] = -1;
+        if (t + k * G < p.units) {
+            unit_offsets<VE, IL>(p, t + k * G, oa[k], ob[k]);
+            oa[k] *= S;
+            ob[k] *= S;
+        }
     }
+    const int head_bytes = p.head_dim * S;
     pdl_wait_for_inputs();
     pdl_allow_dependents();
+    stage_fractions(p, frac);
 
-    const int64_t all = (int64_t)gridDim.x * warps, me = (int64_t)blockIdx.x * warps + warp;
+    const int64_t me = (int64_t)blockIdx.x * warps + warp;
     for (int kind = 0; kind < 2; ++kind) {
-        const int heads = kind ? p.k_heads : p.q_heads, base = kind ? p.q_heads : 0;
-        float ga[NORM ? K : 1][VE], gb[NORM ? K : 1][VE];   // the weight's gradient
-        if constexpr (NORM) {
+        const int heads = kind ? p.k_heads : p.q_heads;
+        const int per = kind ? p.per_k : p.per;   // iterations a token
+        float ga[KN][VE], gb[KN][VE];             // the weight's gradient
 #pragma unroll
-            for (int k = 0; k < K; ++k)
+        for (int k = 0; k < KN; ++k)
 #pragma unroll
-                for (int j = 0; j < VE; ++j) ga[k][j] = gb[k][j] = 0.f;
-        }
+            for (int j = 0; j < VE; ++j) ga[k][j] = gb[k][j] = 0.f;
         if (heads > 0) {
-            const int per = (heads + hpw - 1) / hpw;   // iterations a token
-            const int64_t total = p.tokens * per, each = total / all, extra = total - each * all;
-            int64_t at = me * each + (me < extra ? me : extra);
-            const int64_t end = at + each + (me < extra ? 1 : 0);
-            float wa[K][VE], wb[K][VE];
-            if constexpr (NORM) read_weight<T, VE, K, IL>(p, kind ? p.k_w : p.q_w, t, wa, wb);
-            while (at < end) {
-                const int64_t token = at / per;
-                const int i0 = (int)(at - token * per);
-                const int i1 = end - at < per - i0 ? i0 + (int)(end - at) : per;
-                at += i1 - i0;
-                stage_angles(p, cs, lane, token, true, 0);
-                Angles<VE, K> ang;
-                ang.read(p, cs, t);
+            Run run;
+            run.start(me, kind ? p.each_k : p.each, kind ? p.extra_k : p.extra, per);
+            if constexpr (NORM) {   // the kind's weights, unit by unit: 2 VE floats each
+                __syncthreads();
+                for (int u = threadIdx.x; u < p.units; u += blockDim.x) {
+                    float wa[VE], wb[VE];
+                    read_weight<T, VE, IL>(p, kind ? p.k_w : p.q_w, u, wa, wb);
 #pragma unroll
-                for (int k = 0; k < K; ++k)
-#pragma unroll
-                    for (int j = 0; j < VE; ++j) ang.s[k][j] = -ang.s[k][j];
-                const int64_t head0 = (int64_t)base * p.head_dim * S;
-                const char *xr = static_cast<const char *>(p.x) + token * p.x_stride + head0;
-                const char *gr = static_cast<const char *>(p.dy) + token * p.dy_stride + head0;
-                char *yr = static_cast<char *>(p.y) + token * p.y_stride + head0;
-                for (int i = i0; i < i1; i += UN) {
-                    Raw da[UN][K], db[UN][K], xa[NORM ? UN : 1][K], xb[NORM ? UN : 1][K];
-#pragma unroll
-                    for (int n = 0; n < UN; ++n) {
-                        const int h = (i + n) * hpw + group;
-                        const bool in = i + n < i1 && h < heads;
-                        const int64_t off = (int64_t)h * p.head_dim * S;
-#pragma unroll
-                        for (int k = 0; k < K; ++k) {
-                            da[n][k] = db[n][k] = P::zero();
-                            if constexpr (NORM) xa[n][k] = xb[n][k] = P::zero();
-                            if (in && t + k * G < p.units) {
-                                da[n][k] = P::load(gr + off + oa[k] * S);
-                                db[n][k] = P::load(gr + off + ob[k] * S);
-                                if constexpr (NORM) {
-                                    xa[n][k] = P::load(xr + off + oa[k] * S);
-                                    xb[n][k] = P::load(xr + off + ob[k] * S);
-                                }
-                            }
-                        }
+                    for (int j = 0; j < VE; ++j) {
+                        wsm[2 * VE * u + j] = wa[j];
+                        wsm[2 * VE * u + VE + j] = wb[j];
                     }
+                }
+                __syncthreads();
+            }
+            const int64_t head0 = (int64_t)(kind ? p.q_heads : 0) * head_bytes;
+            const char *x0 = static_cast<const char *>(p.x) + head0, *g0 = static_cast<const char *>(p.dy) + head0;
+            char *y0 = static_cast<char *>(p.y) + head0;
+
+            auto load = [&](const Run &r, int n, Raw (&da)[UN][K], Raw (&db)[UN][K], Raw (&xa)[UX][K],
+                            Raw (&xb)[UX][K]) {
+                const char *gr = g0 + r.token * p.dy_stride;
+                const char *xr = x0 + r.token * p.x_stride;
 #pragma unroll
-                    for (int n = 0; n < UN; ++n) {
-                        if (i + n >= i1) break;   // the same for every lane
-                        const int h = (i + n) * hpw + group;
-                        float va[K][VE], vb[K][VE];
+                for (int i = 0; i < UN; ++i) {
+                    const int h = (r.it + i) * hpw + group;
 #pragma unroll
-                        for (int k = 0; k < K; ++k) {
-                            P::widen(da[n][k], va[k]);
-                            P::widen(db[n][k], vb[k]);
-                            if (t + k * G < p.rot_units) turn_unit<VE, IL>(va[k], vb[k], ang.c[k], ang.s[k]);
-                        }
-                        if constexpr (NORM) {
-                            float fa[K][VE], fb[K][VE];
-                            float sq = 0.f, dot = 0.f;
-#pragma unroll
-                            for (int k = 0; k < K; ++k) {
-                                P::widen(xa[n][k], fa[k]);
-                                P::widen(xb[n][k], fb[k]);
-                                float u[VE], v[VE];
-#pragma unroll
-                                for (int j = 0; j < VE; ++j) {
-                                    u[j] = fmaf(fb[k][j], fb[k][j], fa[k][j] * fa[k][j]);
-                                    v[j] = fmaf(vb[k][j] * wb[k][j], fb[k][j], (va[k][j] * wa[k][j]) * fa[k][j]);
-                                }
-                                sq += tree_sum(u);
-                                dot += tree_sum(v);
+                    for (int k = 0; k < K; ++k) {
+                        da[i][k] = db[i][k] = P::zero();
+                        if constexpr (NORM) xa[i][k] = xb[i][k] = P::zero();
+                        if (i < n && h < heads && oa[k] >= 0) {
+                            da[i][k] = P::load(gr + (h * head_bytes + oa[k]));
+                            db[i][k] = P::load(gr + (h * head_bytes + ob[k]));
+                            if constexpr (NORM) {
+                                xa[i][k] = P::load(xr + (h * head_bytes + oa[k]));
+                                xb[i][k] = P::load(xr + (h * head_bytes + ob[k]));
                             }
-                            for (int off = G >> 1; off > 0; off >>= 1) {
-                                sq += __shfl_xor_sync(0xffffffffu, sq, off);
-                                dot += __shfl_xor_sync(0xffffffffu, dot, off);
-                            }
-                            // an idle head's zeros must add nothing, whatever eps is
-                            const float r = h < heads ? rsqrtf(sq / p.head_dim_f + p.eps) : 0.f;
-                            const float m = (r * r) * (dot / p.head_dim_f);
-#pragma unroll
-                            for (int k = 0; k < K; ++k)
-#pragma unroll
-                                for (int j = 0; j < VE; ++j) {
-                                    ga[k][j] = fmaf(va[k][j], fa[k][j] * r, ga[k][j]);
-                                    gb[k][j] = fmaf(vb[k][j], fb[k][j] * r, gb[k][j]);
-                                    va[k][j] = r * (va[k][j] * wa[k][j] - fa[k][j] * m);
-                                    vb[k][j] = r * (vb[k][j] * wb[k][j] - fb[k][j] * m);
-                                }
-                        }
-                        if (h < heads) {
-                            char *dst = yr + (int64_t)h * p.head_dim * S;
-#pragma unroll
-                            for (int k = 0; k < K; ++k)
-                                if (t + k * G < p.units) {
-                                    P::store(dst + oa[k] * S, va[k]);
-                                    P::store(dst + ob[k] * S, vb[k]);
-                                }
                         }
                     }
                 }
+            };
+
+            auto step = [&](Raw (&da)[UN][K], Raw (&db)[UN][K], Raw (&xa)[UX][K], Raw (&xb)[UX][K], Raw (&ea)[UN][K],
+                            Raw (&eb)[UN][K], Raw (&za)[UX][K], Raw (&zb)[UX][K], bool first) {
+                const int n = run.count(per, UN);
+                Run ahead = run;
+                ahead.advance(n, per);
+                const int more = ahead.count(per, UN);
+                if (more > 0) load(ahead, more, ea, eb, za, zb);
+                if (first || run.it == 0) {
+                    stage_angles(p, frac, cs, lane, run.token, true, 0);
+                }
+                char *yr = y0 + run.token * p.y_stride;
+#pragma unroll
+                for (int i = 0; i < UN; ++i) {
+                    if (i >= n) break;   // the same for every lane
+                    const int h = (run.it + i) * hpw + group;
+                    // cosines, sines and weights come from shared memory at each
+                    // use: held in registers they spilled (128 a thread)
+                    float va[K][VE], vb[K][VE], fa[KN][VE], fb[KN][VE];
+                    float2 sq = make_float2(0.f, 0.f), dot = sq;
+#pragma unroll
+                    for (int k = 0; k < K; ++k) {
+                        P::widen(da[i][k], va[k]);
+                        P::widen(db[i][k], vb[k]);
+                        const int u = t + k * G;
+                        if (u < p.rot_units) {
+                            Turn<VE> m;
+                            read_floats<VE>(cs + u * VE, m.ca);
+                            read_floats<VE>(cs + p.R + u * VE, m.cb);
+#pragma unroll
+                            for (int j = 0; j < VE; ++j) {
+                                m.cc[j] = -m.cb[j];
+                                m.cd[j] = m.ca[j];
+                            }
+                            turn_unit<VE, IL>(va[k], vb[k], m);
+                        }
+                        if constexpr (NORM) {
+                            float wa[VE], wb[VE];
+                            const float *pw = wsm + 2 * VE * (u < p.units ? u : 0);
+                            read_floats<VE>(pw, wa);
+                            read_floats<VE>(pw + VE, wb);
+                            P::widen(xa[i][k], fa[k]);
+                            P::widen(xb[i][k], fb[k]);
+                            dot_into<VE>(sq, fa[k], fa[k]);
+                            dot_into<VE>(sq, fb[k], fb[k]);
+                            float ta[VE], tb[VE];
+#pragma unroll
+                            for (int j = 0; j < VE; ++j) ta[j] = fa[k][j], tb[j] = fb[k][j];
+                            times<VE>(ta, va[k]);   // x g, summed with the weight
+                            times<VE>(tb, vb[k]);
+                            dot_into<VE>(dot, ta, wa);
+                            dot_into<VE>(dot, tb, wb);
+                        }
+                    }
+                    if constexpr (NORM) {
+                        const float s1 = lanes_sum(sq.x + sq.y, G), s2 = lanes_sum(dot.x + dot.y, G);
+                        // an idle head's zeros must add nothing, whatever eps is
+                        const float r = h < heads ? rsqrtf(fmaf(s1, p.inv_dim, p.eps)) : 0.f;
+                        const float mean = (s2 * p.inv_dim) * r;   // dx = r (w g - (x r) mean)
+#pragma unroll
+                        for (int k = 0; k < K; ++k) {
+                            scale_by<VE>(fa[k], r);
+                            scale_by<VE>(fb[k], r);
+#pragma unroll
+                            for (int j = 0; j < VE; ++j) {
+                                ga[k][j] = fmaf(va[k][j], fa[k][j], ga[k][j]);
+                                gb[k][j] = fmaf(vb[k][j], fb[k][j], gb[k][j]);
+                            }
+                            const int u = t + k * G;
+                            float wa[VE], wb[VE];
+                            const float *pw = wsm + 2 * VE * (u < p.units ? u : 0);
+                            read_floats<VE>(pw, wa);
+                            read_floats<VE>(pw + VE, wb);
+                            times<VE>(va[k], wa);
+                            times<VE>(vb[k], wb);
+#pragma unroll
+                            for (int j = 0; j < VE; ++j) {
+                                va[k][j] = fmaf(fa[k][j], -mean, va[k][j]);
+                                vb[k][j] = fmaf(fb[k][j], -mean, vb[k][j]);
+                            }
+                            scale_by<VE>(va[k], r);
+                            scale_by<VE>(vb[k], r);
+                        }
+                    }
+                    char *dst = yr + (int64_t)h * head_bytes;
+#pragma unroll
+                    for (int k = 0; k < K; ++k)
+                        if (h < heads && oa[k] >= 0) {
+                            P::store(dst + oa[k], va[k]);
+                            P::store(dst + ob[k], vb[k]);
+                        }
+                }
+                run = ahead;
+            };
+
+            Raw da[UN][K], db[UN][K], xa[UX][K], xb[UX][K], ea[UN][K], eb[UN][K], za[UX][K], zb[UX][K];
+            bool first = true;
+            if (run.at < run.end) load(run, run.count(per, UN), da, db, xa, xb);
+            while (run.at < run.end) {
+                step(da, db, xa, xb, ea, eb, za, zb, first);
+                first = false;
+                if (run.at >= run.end) break;
+                step(ea, eb, za, zb, da, db, xa, xb, false);
             }
         }
         if constexpr (NORM) {
@@ -644,11 +861,11 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps) rope_bwd_kernel(const Rope
                 if (group == 0) {
 #pragma unroll
                     for (int k = 0; k < K; ++k)
-                        if (t + k * G < p.units)
+                        if (oa[k] >= 0)
 #pragma unroll
                             for (int j = 0; j < VE; ++j) {
-                                sums[warp * p.head_dim + oa[k] + j] = ga[k][j];
-                                sums[warp * p.head_dim + ob[k] + j] = gb[k][j];
+                                sums[warp * p.head_dim + oa[k] / S + j] = ga[k][j];
+                                sums[warp * p.head_dim + ob[k] / S + j] = gb[k][j];
                             }
                 }
                 __syncthreads();
