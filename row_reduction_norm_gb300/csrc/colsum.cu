@@ -14,10 +14,13 @@ constexpr int kColsumWarps = 32;
 
 template <typename T>
 __global__ void __launch_bounds__(32 * kColsumWarps)
-colsum_kernel(const float *partial, int rows, int64_t cols, int64_t split, void *out0, void *out1) {
+colsum_kernel(const float *partial, int rows0, int rows1, int64_t cols, void *out0, void *out1) {
     __shared__ float part[kColsumWarps][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t col = (int64_t)blockIdx.x * 32 + lane;
+    const int rows = blockIdx.y ? rows1 : rows0;
+    if (blockIdx.y) partial += (int64_t)rows0 * cols;
+    void *out = blockIdx.y ? out1 : out0;
     pdl_wait_for_inputs();
     pdl_allow_dependents();
     float v[4] = {0.f, 0.f, 0.f, 0.f};
@@ -33,20 +36,17 @@ colsum_kernel(const float *partial, int rows, int64_t cols, int64_t split, void 
     // warp w adds up column w of the block
     const int64_t mine = (int64_t)blockIdx.x * 32 + warp;
     const float s = butterfly_sum<32>(part[lane][warp]);
-    if (lane == 0 && mine < cols) {
-        if (mine < split) st_scalar(out0, mine, s, T{});
-        else st_scalar(out1, mine - split, s, T{});
-    }
+    if (lane == 0 && mine < cols) st_scalar(out, mine, s, T{});
 }
 
 }  // namespace
 
-int launch_colsum(const float *partial, int rows, int64_t cols, int64_t split, void *out0, void *out1, int dtype,
+int launch_colsum(const float *partial, int rows0, int rows1, int64_t cols, void *out0, void *out1, int dtype,
                   rmsnorm_stream_t stream) {
-    void *argv[] = {&partial, &rows, &cols, &split, &out0, &out1};
+    void *argv[] = {&partial, &rows0, &rows1, &cols, &out0, &out1};
     const void *fn = dtype == RMSNORM_BF16 ? reinterpret_cast<const void *>(&colsum_kernel<BF16>)
                                            : reinterpret_cast<const void *>(&colsum_kernel<F32>);
-    return launch_kernel(fn, dim3((unsigned)div_up(cols, 32)), 32 * kColsumWarps, 0, stream, argv);
+    return launch_kernel(fn, dim3((unsigned)div_up(cols, 32), out1 != nullptr ? 2 : 1), 32 * kColsumWarps, 0, stream, argv);
 }
 
 }  // namespace rrn

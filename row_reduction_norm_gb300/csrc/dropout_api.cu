@@ -4,7 +4,6 @@
 #include <climits>
 #include <cmath>
 #include <cstring>
-#include <mutex>
 
 #include "dropout_kernels.cuh"
 #include "dropout_pick.h"
@@ -18,7 +17,6 @@ constexpr int64_t kMaxHidden = 65536;
 // Rows the two-pass gradient keeps its sums of dw for in shared memory: 192
 // KB of sums and 6 KB of mask bits within the 227 KB of a block.
 constexpr int64_t kSmemSums = 49152;
-constexpr int kMaxSmem = 226 * 1024;
 
 // Blocks a SM of the gradient at most: each keeps a row of fp32 sums, which
 // are written and read once more.
@@ -74,26 +72,6 @@ bool reg_shape(int64_t nch, int max_ch, int *gt, int *ch) {
 }
 
 int loop_block(bool vec, int64_t hidden) { return vec || hidden > 4096 ? 1024 : 256; }
-
-// Opt a kernel in to large dynamic shared memory, once per device and kernel.
-int allow_smem(int dev, const void *fn) {
-    struct Entry {
-        int dev;
-        const void *fn;
-    };
-    static std::mutex mu;
-    static Entry done[256];
-    static int used = 0;
-    std::lock_guard<std::mutex> lk(mu);
-    for (int i = 0; i < used; ++i)
-        if (done[i].dev == dev && done[i].fn == fn) return RMSNORM_OK;
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return RMSNORM_ECUDA;
-    }
-    if (used < 256) done[used++] = Entry{dev, fn};
-    return RMSNORM_OK;
-}
 
 void fill(rrn::DropParams *p, const void *w, int64_t rows, int64_t hidden, float eps, float w_bias, uint32_t thr,
           const uint64_t *rng, int dtype) {
@@ -154,7 +132,7 @@ int backward(const void *dy, const void *h, const void *w, const void *dh, void 
             fn = rrn::drop_bwd_loop(dtype, vec, threads, dw != nullptr);
             p.acc_in_smem = dw != nullptr && hidden <= kSmemSums;
             smem = (p.acc_in_smem ? (size_t)hidden * sizeof(float) : 0) + (size_t)(thr ? p.blocks_per_row : 0);
-            if (smem > 48 * 1024 && (st = allow_smem(dev, fn)) != RMSNORM_OK) return st;
+            if (smem > 48 * 1024 && (st = rrn::allow_smem(dev, fn)) != RMSNORM_OK) return st;
         }
         if (fn == nullptr) return RMSNORM_EINVAL;
         int resident = 0;
@@ -167,8 +145,7 @@ int backward(const void *dy, const void *h, const void *w, const void *dh, void 
         if (st != RMSNORM_OK) return st;
     }
     if (dw == nullptr) return RMSNORM_OK;
-    return rrn::launch_colsum(static_cast<const float *>(workspace), (int)blocks, hidden, hidden, dw, nullptr, dtype,
-                              stream);
+    return rrn::launch_colsum(static_cast<const float *>(workspace), (int)blocks, 0, hidden, dw, nullptr, dtype, stream);
 }
 
 }  // namespace

@@ -45,9 +45,12 @@ inline int launch_kernel(const void *fn, dim3 grid, int block, size_t smem, rmsn
     return RMSNORM_OK;
 }
 
-// Sums of the columns of partial[rows][cols] into the I/O type: columns
-// 0 .. split - 1 to out0, the rest to out1 (colsum.cu).
-int launch_colsum(const float *partial, int rows, int64_t cols, int64_t split, void *out0, void *out1, int dtype,
+// Opt a kernel in to 226 KB of dynamic shared memory (cached per device and kernel).
+int allow_smem(int dev, const void *fn);
+
+// Sums of the columns of partial[rows0 + rows1][cols] into the I/O type: of
+// the first rows0 rows to out0, of the rest to out1 (nullable; colsum.cu).
+int launch_colsum(const float *partial, int rows0, int rows1, int64_t cols, void *out0, void *out1, int dtype,
                   rmsnorm_stream_t stream);
 
 }  // namespace rrn

@@ -806,6 +806,18 @@ int resident_blocks(int dev, const void *fn, int block, size_t smem, int *blocks
     return blocks_per_sm_of(dev, fn, block, smem, blocks);
 }
 
+int allow_smem(int dev, const void *fn) {
+    std::lock_guard<std::mutex> lk(g_mu);
+    for (int i = 0; i < g_attr_used; ++i)
+        if (g_attr[i].dev == dev && g_attr[i].fn == fn) return RMSNORM_OK;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTmaSmemBudget) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return RMSNORM_ECUDA;
+    }
+    if (g_attr_used < kOccSlots) g_attr[g_attr_used++] = AttrEntry{dev, fn};
+    return RMSNORM_OK;
+}
+
 }  // namespace rrn
 
 extern "C" {

@@ -73,6 +73,7 @@ int make_rope(int64_t tokens, int64_t x_stride, int32_t q_heads, int32_t k_heads
     p->pos = rope->positions;
     p->pos_stride = rope->axes > 1 ? rope->position_stride : 0;
     p->pos64 = rope->position_bytes == 8;
+    p->axes = rope->axes;
     p->inv_freq = rope->inv_freq;
     p->R = rope->rot_dim / 2;
     int32_t at = 0;
@@ -116,18 +117,6 @@ struct Unit {
     int64_t get() const { return (int64_t)(bits & (~bits + 1)); }
 };
 
-// Warps a block: eight, fewer while that leaves a SM without a block.
-int block_warps(int64_t work, int sms) {
-    int warps = rrn::kRopeMaxWarps;
-    while (warps > 1 && work < (int64_t)warps * sms) warps /= 2;
-    return warps;
-}
-
-// Shared memory of a block: turn fractions, each warp's angles.
-size_t angle_bytes(const rrn::RopeParams *p, int warps) {
-    return (size_t)((p->R + 1) & ~1) * sizeof(uint64_t) + (size_t)warps * 2 * p->R * sizeof(float);
-}
-
 const void *forward_kernel(int dtype, int shape, bool il, int mode) {
     return dtype == RMSNORM_BF16 ? rrn::rope_fwd_bf16(shape, il, mode) : rrn::rope_fwd_f32(shape, il, mode);
 }
@@ -139,20 +128,28 @@ int launch_forward(rrn::RopeParams *p, int dtype, int64_t unit, bool il, int mod
     const int shape = pick_shape(dtype, unit, p);
     const void *fn = forward_kernel(dtype, shape, il, mode);
     if (fn == nullptr) return RMSNORM_EINVAL;
-    // a run of head iterations for every warp of a resident grid, or one
-    // iteration a warp while there are fewer
-    p->per = (int32_t)div_up((int64_t)p->q_heads + p->k_heads + p->v_heads, 32 / p->lanes);
-    const int64_t work = p->tokens * p->per;
-    const int warps = block_warps(work, sms);
-    const size_t smem = angle_bytes(p, warps);
+    // A run of jobs for every resident block.  A job is a token's heads; with
+    // fewer tokens than blocks it is a slice of them, one head iteration a
+    // warp where that many blocks fit.
+    const int64_t iters = div_up((int64_t)p->q_heads + p->k_heads + p->v_heads, 32 / p->lanes);
+    const size_t smem = (size_t)rrn::rope_smem_floats(p->head_dim, p->R) * sizeof(float);
     int resident = 0;
-    if ((st = rrn::resident_blocks(dev, fn, 32 * warps, smem, &resident)) != RMSNORM_OK) return st;
-    int64_t blocks = (int64_t)sms * resident;
-    if (blocks > div_up(work, warps)) blocks = div_up(work, warps);
-    p->each = work / (blocks * warps);
-    p->extra = work % (blocks * warps);
+    if (smem > 48 * 1024 && (st = rrn::allow_smem(dev, fn)) != RMSNORM_OK) return st;
+    if ((st = rrn::resident_blocks(dev, fn, 32 * rrn::kRopeMaxWarps, smem, &resident)) != RMSNORM_OK) return st;
+    const int64_t most = (int64_t)sms * resident;
+    int64_t slices = 1;
+    if (p->tokens < most) {
+        slices = most / p->tokens;
+        if (slices > div_up(iters, rrn::kRopeMaxWarps)) slices = div_up(iters, rrn::kRopeMaxWarps);
+    }
+    p->iters = (int32_t)div_up(iters, slices);
+    p->slices = (int32_t)div_up(iters, p->iters);
+    const int64_t jobs = p->tokens * p->slices;
+    const int64_t blocks = jobs < most ? jobs : most;
+    p->each = jobs / blocks;
+    p->extra = jobs % blocks;
     void *argv[] = {p};
-    return rrn::launch_kernel(fn, dim3((unsigned)blocks), 32 * warps, smem, stream, argv);
+    return rrn::launch_kernel(fn, dim3((unsigned)blocks), 32 * rrn::kRopeMaxWarps, smem, stream, argv);
 }
 
 }  // namespace
@@ -184,7 +181,7 @@ int rmsnorm_qk_rope_fwd(const void *x, void *y, int64_t tokens, int64_t x_token_
 int64_t rmsnorm_qk_rope_bwd_workspace_bytes(int64_t head_dim) {
     if (head_dim <= 0 || head_dim % 2 != 0) return RMSNORM_EINVAL;
     if (head_dim > rrn::kRopeMaxDim) return RMSNORM_EUNSUPPORTED;
-    return (int64_t)kBwdMaxBlocks * 2 * head_dim * (int64_t)sizeof(float);
+    return (int64_t)kBwdMaxBlocks * head_dim * (int64_t)sizeof(float);
 }
 
 int rmsnorm_qk_rope_bwd(const void *dy, const void *x, void *dx, int64_t tokens, int64_t dy_token_stride,
@@ -219,8 +216,9 @@ int rmsnorm_qk_rope_bwd(const void *dy, const void *x, void *dx, int64_t tokens,
     p.dy_stride = dy_token_stride * s;
     p.y_stride = dx_token_stride * s;
     p.partial = static_cast<float *>(dq_w != nullptr ? workspace : nullptr);
-    int64_t blocks = 0;
+    int64_t blocks_q = 0, blocks_k = 0;
     if (tokens > 0) {
+        const size_t sum_bytes = (size_t)rrn::kRopeMaxWarps * head_dim * sizeof(float);
         Unit u;
         u.at(dy, s), u.at(dx, s), u.at(q_w, s), u.at(k_w, s);
         u.step(dy_token_stride), u.step(dx_token_stride);
@@ -233,27 +231,38 @@ int rmsnorm_qk_rope_bwd(const void *dy, const void *x, void *dx, int64_t tokens,
                                                : rrn::rope_bwd_f32(shape, il, norm == 1);
         if (fn == nullptr) return RMSNORM_EINVAL;
         const int hpw = 32 / p.lanes;
-        p.per = (int32_t)div_up(q_heads, hpw);
-        p.per_k = (int32_t)div_up(k_heads, hpw);
-        const int64_t work = tokens * (p.per + p.per_k);
-        const int warps = block_warps(work, sms);
-        const size_t smem = angle_bytes(&p, warps) + (size_t)rrn::rope_weight_floats(dtype, shape) * sizeof(float) +
-                            (size_t)(dq_w != nullptr ? warps * head_dim : 0) * sizeof(float);
+        p.iters = (int32_t)div_up(q_heads, hpw);
+        p.iters_k = (int32_t)div_up(k_heads, hpw);
+        const size_t smem = (size_t)rrn::rope_smem_floats((int)head_dim, p.R) * sizeof(float) > sum_bytes
+                                ? (size_t)rrn::rope_smem_floats((int)head_dim, p.R) * sizeof(float)
+                                : sum_bytes;
         int resident = 0;
-        if ((st = rrn::resident_blocks(dev, fn, 32 * warps, smem, &resident)) != RMSNORM_OK) return st;
-        blocks = (int64_t)sms * resident;
-        if (blocks > kBwdMaxBlocks) blocks = kBwdMaxBlocks;
-        if (blocks > div_up(work, warps)) blocks = div_up(work, warps);
-        p.each = tokens * p.per / (blocks * warps);
-        p.extra = tokens * p.per % (blocks * warps);
-        p.each_k = tokens * p.per_k / (blocks * warps);
-        p.extra_k = tokens * p.per_k % (blocks * warps);
+        if (smem > 48 * 1024 && (st = rrn::allow_smem(dev, fn)) != RMSNORM_OK) return st;
+        if ((st = rrn::resident_blocks(dev, fn, 32 * rrn::kRopeMaxWarps, smem, &resident)) != RMSNORM_OK) return st;
+        int64_t most = (int64_t)sms * resident;
+        if (most > kBwdMaxBlocks) most = kBwdMaxBlocks;
+        // blocks shared out by the head iterations of the two kinds, at most
+        // one a token for each
+        const int64_t all = (int64_t)p.iters + p.iters_k;
+        int64_t bq = q_heads == 0 ? 0 : k_heads == 0 ? most : most * p.iters / all;
+        if (q_heads > 0 && bq < 1) bq = 1;
+        int64_t bk = k_heads == 0 ? 0 : most - bq;
+        if (k_heads > 0 && bk < 1) bk = 1;
+        if (bq > tokens) bq = tokens;
+        if (bk > tokens) bk = tokens;
+        p.q_blocks = (int32_t)bq;
+        p.each = bq > 0 ? tokens / bq : 0;
+        p.extra = bq > 0 ? tokens % bq : 0;
+        p.each_k = bk > 0 ? tokens / bk : 0;
+        p.extra_k = bk > 0 ? tokens % bk : 0;
+        blocks_q = bq;
+        blocks_k = bk;
         void *argv[] = {&p};
-        st = rrn::launch_kernel(fn, dim3((unsigned)blocks), 32 * warps, smem, stream, argv);
+        st = rrn::launch_kernel(fn, dim3((unsigned)(bq + bk)), 32 * rrn::kRopeMaxWarps, smem, stream, argv);
         if (st != RMSNORM_OK) return st;
     }
     if (dq_w == nullptr) return RMSNORM_OK;
-    return rrn::launch_colsum(static_cast<const float *>(workspace), (int)blocks, 2 * head_dim, head_dim, dq_w, dk_w,
+    return rrn::launch_colsum(static_cast<const float *>(workspace), (int)blocks_q, (int)blocks_k, head_dim, dq_w, dk_w,
                               dtype, stream);
 }
 

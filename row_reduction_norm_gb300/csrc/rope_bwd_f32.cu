@@ -5,20 +5,20 @@
 namespace rrn {
 namespace {
 
-template <typename T, int VE, int K, int UN, bool IL>
+template <typename T, int VE, int K, bool IL>
 const void *one(bool norm) {
-    return norm ? reinterpret_cast<const void *>(&rope_bwd_kernel<T, VE, K, IL, true, UN>)
-                : reinterpret_cast<const void *>(&rope_bwd_kernel<T, VE, K, IL, false, UN>);
+    return norm ? reinterpret_cast<const void *>(&rope_bwd_kernel<T, VE, K, IL, true>)
+                : reinterpret_cast<const void *>(&rope_bwd_kernel<T, VE, K, IL, false>);
 }
 
 }  // namespace
 
 const void *rope_bwd_f32(int shape, bool il, bool norm) {
     switch (shape) {
-        case 0: return il ? one<F32, 4, 1, 1, true>(norm) : one<F32, 4, 1, 1, false>(norm);
-        case 1: return il ? one<F32, 4, 2, 1, true>(norm) : one<F32, 4, 2, 1, false>(norm);
-        case 2: return il ? one<F32, 2, 2, 1, true>(norm) : one<F32, 2, 2, 1, false>(norm);
-        case 3: return il ? one<F32, 1, 8, 1, true>(norm) : one<F32, 1, 8, 1, false>(norm);
+        case 0: return il ? one<F32, 4, 1, true>(norm) : one<F32, 4, 1, false>(norm);
+        case 1: return il ? one<F32, 4, 2, true>(norm) : one<F32, 4, 2, false>(norm);
+        case 2: return il ? one<F32, 2, 2, true>(norm) : one<F32, 2, 2, false>(norm);
+        case 3: return il ? one<F32, 1, 8, true>(norm) : one<F32, 1, 8, false>(norm);
         default: return nullptr;
     }
 }

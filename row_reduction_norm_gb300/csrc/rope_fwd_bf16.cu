@@ -5,30 +5,30 @@
 namespace rrn {
 namespace {
 
-template <typename T, int VE, int K, int UN, bool IL>
+template <typename T, int VE, int K, bool IL>
 const void *one(int mode) {
     switch (mode) {
-        case kRopePlain: return reinterpret_cast<const void *>(&rope_kernel<T, VE, K, IL, kRopePlain, UN>);
-        case kRopeAppend: return reinterpret_cast<const void *>(&rope_kernel<T, VE, K, IL, kRopeAppend, UN>);
-        case kRopeAppendE4m3: return reinterpret_cast<const void *>(&rope_kernel<T, VE, K, IL, kRopeAppendE4m3, UN>);
+        case kRopePlain: return reinterpret_cast<const void *>(&rope_kernel<T, VE, K, IL, kRopePlain>);
+        case kRopeAppend: return reinterpret_cast<const void *>(&rope_kernel<T, VE, K, IL, kRopeAppend>);
+        case kRopeAppendE4m3: return reinterpret_cast<const void *>(&rope_kernel<T, VE, K, IL, kRopeAppendE4m3>);
         default: return nullptr;
     }
 }
 
-template <typename T, int VE, int K, int UN>
+template <typename T, int VE, int K>
 const void *mode_of(bool il, int mode) {
-    return il ? one<T, VE, K, UN, true>(mode) : one<T, VE, K, UN, false>(mode);
+    return il ? one<T, VE, K, true>(mode) : one<T, VE, K, false>(mode);
 }
 
 }  // namespace
 
 const void *rope_fwd_bf16(int shape, bool il, int mode) {
     switch (shape) {
-        case 0: return mode_of<BF16, 8, 1, 2>(il, mode);
-        case 1: return mode_of<BF16, 4, 1, 2>(il, mode);
-        case 2: return mode_of<BF16, 4, 2, 2>(il, mode);
-        case 3: return mode_of<BF16, 2, 2, 2>(il, mode);
-        case 4: return mode_of<BF16, 1, 8, 1>(il, mode);
+        case 0: return mode_of<BF16, 8, 1>(il, mode);
+        case 1: return mode_of<BF16, 4, 1>(il, mode);
+        case 2: return mode_of<BF16, 4, 2>(il, mode);
+        case 3: return mode_of<BF16, 2, 2>(il, mode);
+        case 4: return mode_of<BF16, 1, 8>(il, mode);
         default: return nullptr;
     }
 }

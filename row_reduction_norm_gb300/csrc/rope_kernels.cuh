@@ -13,11 +13,13 @@
 // Work layout.  A lane owns K "units" of a head: unit u is VE pairs, held as
 // two pieces of VE elements, so both halves of every pair sit in one lane and
 // the rotation needs no exchange.  G lanes share a head, 32 / G heads run
-// side by side in a warp (a head iteration), and the batch's iterations are
-// cut into equal runs, one a warp, whose next loads are under way while the
-// present heads are worked on.  A token's sines and cosines are computed once
-// by each warp that is at the token (each pair by one lane) and shared through
-// shared memory behind warp syncs only.
+// side by side in a warp (a head iteration).  A block takes an equal run of
+// tokens in tiles of one token a warp: each warp makes its token's table of
+// cosines and sines in shared memory, then the tile's head iterations go
+// round the warps.  Every factor of a head (cosine, sine, weights) is read
+// from shared memory where it is used, so a thread needs few registers and
+// many warps hide the loads' latency: with the factors in registers 16 warps
+// a SM were resident and bf16 8192 tokens x 40 heads of 128 took 36 us.
 //
 // Angles.  Positions are integers, so only the fraction of a turn per step
 // matters: inv_freq / 2 pi is held as a 64-bit fixed-point fraction of a turn
@@ -29,20 +31,27 @@
 
 #include "rmsnorm_kernels.cuh"
 
+#ifndef ROPE_FR
+#define ROPE_FR 4
+#endif
+#ifndef ROPE_BR
+#define ROPE_BR 2
+#endif
 namespace rrn {
 
 constexpr int kRopeMaxDim = 512;      // head_dim
 constexpr int kRopeMaxAxes = 4;
 constexpr int kRopeMaxWarps = 8;      // warps a block
 // Blocks a SM that a shape's registers are budgeted for.
-__host__ __device__ constexpr int rope_resident(int ve, int k) { return ve * k <= 8 && ve > 1 && !(ve == 4 && k == 2) ? 2 : 1; }
+__host__ __device__ constexpr int rope_resident(int ve, int k) { return ve * k <= 8 ? ROPE_FR : 2; }
+__host__ __device__ constexpr int rope_bwd_resident(int ve, int k) { return ve * k <= 8 ? ROPE_BR : 1; }
 
 struct RopeParams {
     const void *x;            // packed token rows (query, key, [value] heads)
     const void *dy;           // gradient: of the rotated rows
     void *y;                  // rotated rows (append: of the query heads); gradient: dx
     const void *q_w, *k_w;    // nullable
-    float *partial;           // gradient: [blocks][2][D] sums of the weights' gradients, or NULL
+    float *partial;           // gradient: [blocks][D] sums of the weights' gradients, or NULL
     int64_t tokens;
     int64_t x_stride, y_stride, dy_stride;   // bytes between token rows
     int32_t q_heads, k_heads, v_heads;       // v_heads: append only
@@ -52,14 +61,16 @@ struct RopeParams {
     // rotation
     const void *pos;          // [axes][pos_stride], 32 or 64 bit; append: NULL = index in the cache
     int64_t pos_stride;
-    int32_t pos64;
+    int32_t pos64, axes;
     int32_t cut[3];           // first pair of axes 1, 2, 3 (R where there is none)
     const float *inv_freq;    // [R]
     int32_t R;
     int32_t units, rot_units; // pair units of a head, and the rotated ones among them
     int32_t lanes;            // G: lanes a head, a power of two
-    int32_t per, per_k;       // head iterations a token (gradient: of its query, its key heads)
-    int64_t each, extra, each_k, extra_k;   // a warp's run of them: each, one more for the first `extra`
+    int32_t iters, iters_k;   // head iterations a job (gradient: a token's query heads, its key heads)
+    int32_t slices;           // forward: jobs a token
+    int32_t q_blocks;         // gradient: blocks of the query heads
+    int64_t each, extra, each_k, extra_k;   // a block's run of jobs: each, one more for the first `extra`
     // paged cache (append)
     const int32_t *cu_tokens, *cache_lens, *page_table;
     int64_t table_stride;
@@ -88,26 +99,6 @@ struct Piece {
         Raw r;
 #pragma unroll
         for (int i = 0; i < kWords; ++i) r.u[i] = 0u;
-        return r;
-    }
-    // Weights: read by every warp, kept in L1.
-    __device__ static __forceinline__ Raw load_w(const char *p) {
-        Raw r;
-        if constexpr (kBytes == 2) {
-            r.u[0] = *reinterpret_cast<const uint16_t *>(p);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kWords; ++i) r.u[i] = 0u;
-            if constexpr (kBytes == 16) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(p);
-                r.u[0] = v.x, r.u[1] = v.y, r.u[2] = v.z, r.u[3] = v.w;
-            } else if constexpr (kBytes == 8) {
-                const uint2 v = *reinterpret_cast<const uint2 *>(p);
-                r.u[0] = v.x, r.u[1] = v.y;
-            } else {
-                r.u[0] = *reinterpret_cast<const uint32_t *>(p);
-            }
-        }
         return r;
     }
     // Streamed (read once) loads.
@@ -202,81 +193,97 @@ __device__ __forceinline__ void unit_offsets(const RopeParams &p, int u, int &a,
     }
 }
 
-// The 2 x 2 turn of each pair, with whatever weights the caller folded in:
-//   y_a = ca x_a + cb x_b,   y_b = cc x_a + cd x_b
-// two fp32 operations an instruction.  Half split: the unit's pieces are the
-// pairs' first and second elements; interleaved: neighbours are a pair.
-template <int VE>
-struct Turn {
-    float ca[VE], cb[VE], cc[VE], cd[VE];
-};
-
+// Places of a unit's pair j in the unit's 2 VE elements (a's, then b's).
 template <int VE, bool IL>
-__device__ __forceinline__ void turn_unit(float (&xa)[VE], float (&xb)[VE], const Turn<VE> &m) {
-    if constexpr (VE == 1) {
-        const float a = xa[0], b = xb[0];
-        xa[0] = fmaf(m.ca[0], a, m.cb[0] * b);
-        xb[0] = fmaf(m.cc[0], a, m.cd[0] * b);
+__device__ __forceinline__ constexpr int first_of(int j) { return IL ? 2 * j : j; }
+template <int VE, bool IL>
+__device__ __forceinline__ constexpr int second_of(int j) { return IL ? 2 * j + 1 : VE + j; }
+
+// Pairs read from a table of factors at a time.
+__host__ __device__ constexpr int pairs_at_once(int ve) { return ve < 4 ? ve : 4; }
+
+// Where pair j of unit u stands in a table of `units` units: the lanes of a
+// head read consecutive 16 (8, 4) bytes.
+template <int VE>
+__device__ __forceinline__ int table_at(int units, int u, int j) {
+    constexpr int N = pairs_at_once(VE);
+    return ((j / N) * units + u) * N + j % N;
+}
+
+template <int N>
+__device__ __forceinline__ void read_table(const float *p, float (&v)[N]) {
+    if constexpr (N == 4) {
+        const float4 a = *reinterpret_cast<const float4 *>(p);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    } else if constexpr (N == 2) {
+        const float2 a = *reinterpret_cast<const float2 *>(p);
+        v[0] = a.x, v[1] = a.y;
+    } else {
+        v[0] = p[0];
+    }
+}
+
+// Pairs j0 .. j0 + N - 1 of a unit turned by (c, s), two fp32 operations an
+// instruction.
+template <int VE, bool IL, int N>
+__device__ __forceinline__ void turn_pairs(float (&e)[2 * VE], int j0, const float (&c)[N], const float (&s)[N]) {
+    if constexpr (N == 1) {
+        float &a = e[first_of<VE, IL>(j0)], &b = e[second_of<VE, IL>(j0)];
+        const float x = a, y = b;
+        a = fmaf(x, c[0], -(y * s[0]));
+        b = fmaf(x, s[0], y * c[0]);
     } else if constexpr (IL) {
 #pragma unroll
-        for (int j = 0; j < VE; ++j) {
-            float (&x)[VE] = j < VE / 2 ? xa : xb;
-            const int e = 2 * (j % (VE / 2));
-            const float2 y = __ffma2_rn(make_float2(x[e], x[e]), make_float2(m.ca[j], m.cc[j]),
-                                        __fmul2_rn(make_float2(x[e + 1], x[e + 1]), make_float2(m.cb[j], m.cd[j])));
-            x[e] = y.x;
-            x[e + 1] = y.y;
+        for (int j = 0; j < N; ++j) {
+            float &a = e[2 * (j0 + j)], &b = e[2 * (j0 + j) + 1];
+            const float2 v = __ffma2_rn(make_float2(a, a), make_float2(c[j], s[j]),
+                                        __fmul2_rn(make_float2(b, b), make_float2(-s[j], c[j])));
+            a = v.x, b = v.y;
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < VE; j += 2) {
-            const float2 a = make_float2(xa[j], xa[j + 1]), b = make_float2(xb[j], xb[j + 1]);
-            const float2 u = __ffma2_rn(make_float2(m.ca[j], m.ca[j + 1]), a,
-                                        __fmul2_rn(make_float2(m.cb[j], m.cb[j + 1]), b));
-            const float2 v = __ffma2_rn(make_float2(m.cc[j], m.cc[j + 1]), a,
-                                        __fmul2_rn(make_float2(m.cd[j], m.cd[j + 1]), b));
-            xa[j] = u.x, xa[j + 1] = u.y;
-            xb[j] = v.x, xb[j + 1] = v.y;
+        for (int j = 0; j < N; j += 2) {
+            const float2 a = make_float2(e[j0 + j], e[j0 + j + 1]);
+            const float2 b = make_float2(e[VE + j0 + j], e[VE + j0 + j + 1]);
+            const float2 cc = make_float2(c[j], c[j + 1]), ss = make_float2(s[j], s[j + 1]);
+            const float2 u = __ffma2_rn(a, cc, __fmul2_rn(b, make_float2(-s[j], -s[j + 1])));
+            const float2 v = __ffma2_rn(a, ss, __fmul2_rn(b, cc));
+            e[j0 + j] = u.x, e[j0 + j + 1] = u.y;
+            e[VE + j0 + j] = v.x, e[VE + j0 + j + 1] = v.y;
         }
     }
 }
 
-// x *= r, and x *= w elementwise; sums of products.
-template <int VE>
-__device__ __forceinline__ void scale_by(float (&x)[VE], float r) {
-    if constexpr (VE == 1) {
-        x[0] *= r;
+// The N pairs from j0 on, first and second elements, times (w0, w1) and r.
+template <int VE, bool IL, int N>
+__device__ __forceinline__ void weigh_pairs(float (&e)[2 * VE], int j0, const float (&w0)[N], const float (&w1)[N],
+                                            float r) {
+    const float2 r2 = make_float2(r, r);
+    if constexpr (N == 1 || IL) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            float &a = e[first_of<VE, IL>(j0 + j)], &b = e[second_of<VE, IL>(j0 + j)];
+            const float2 v = __fmul2_rn(__fmul2_rn(make_float2(a, b), r2), make_float2(w0[j], w1[j]));
+            a = v.x, b = v.y;
+        }
     } else {
 #pragma unroll
-        for (int j = 0; j < VE; j += 2) {
-            const float2 v = __fmul2_rn(make_float2(x[j], x[j + 1]), make_float2(r, r));
-            x[j] = v.x, x[j + 1] = v.y;
+        for (int j = 0; j < N; j += 2) {
+            float &a0 = e[j0 + j], &a1 = e[j0 + j + 1], &b0 = e[VE + j0 + j], &b1 = e[VE + j0 + j + 1];
+            const float2 u = __fmul2_rn(__fmul2_rn(make_float2(a0, a1), r2), make_float2(w0[j], w0[j + 1]));
+            const float2 v = __fmul2_rn(__fmul2_rn(make_float2(b0, b1), r2), make_float2(w1[j], w1[j + 1]));
+            a0 = u.x, a1 = u.y, b0 = v.x, b1 = v.y;
         }
     }
 }
 
-template <int VE>
-__device__ __forceinline__ void times(float (&x)[VE], const float (&w)[VE]) {
-    if constexpr (VE == 1) {
-        x[0] *= w[0];
-    } else {
+// acc += sum of squares of a unit's elements.
+template <int N>
+__device__ __forceinline__ void squares_into(float2 &acc, const float (&e)[N]) {
 #pragma unroll
-        for (int j = 0; j < VE; j += 2) {
-            const float2 v = __fmul2_rn(make_float2(x[j], x[j + 1]), make_float2(w[j], w[j + 1]));
-            x[j] = v.x, x[j + 1] = v.y;
-        }
-    }
-}
-
-// acc += x * y, elements of either parity in a sum of their own.
-template <int VE>
-__device__ __forceinline__ void dot_into(float2 &acc, const float (&x)[VE], const float (&y)[VE]) {
-    if constexpr (VE == 1) {
-        acc.x = fmaf(x[0], y[0], acc.x);
-    } else {
-#pragma unroll
-        for (int j = 0; j < VE; j += 2)
-            acc = __ffma2_rn(make_float2(x[j], x[j + 1]), make_float2(y[j], y[j + 1]), acc);
+    for (int j = 0; j < N; j += 2) {
+        const float2 v = make_float2(e[j], e[j + 1]);
+        acc = __ffma2_rn(v, v, acc);
     }
 }
 
@@ -327,136 +334,65 @@ __device__ __forceinline__ int axis_of(const RopeParams &p, int i) {
     return (i >= p.cut[0]) + (i >= p.cut[1]) + (i >= p.cut[2]);
 }
 
-__device__ __forceinline__ int64_t position_of(const RopeParams &p, int axis, int64_t token) {
-    const int64_t at = (int64_t)axis * p.pos_stride + token;
+// Shared memory of a block, in floats: the weights of the pairs' first and
+// second elements [2 kinds][2][D / 2], then two tiles of cosines and sines
+// [2][kRopeMaxWarps][2][R], all in table order.
+__host__ __device__ constexpr int rope_smem_floats(int head_dim, int R) {
+    return 2 * head_dim + 2 * kRopeMaxWarps * 2 * R;
+}
+
+// A token's position on axis `lane` (lanes past the axes: the last one).
+__device__ __forceinline__ int64_t lane_position(const RopeParams &p, int lane, int64_t token) {
+    const int64_t at = (int64_t)(lane < p.axes ? lane : p.axes - 1) * p.pos_stride + token;
     return p.pos64 ? static_cast<const int64_t *>(p.pos)[at] : (int64_t)static_cast<const int32_t *>(p.pos)[at];
 }
 
-// Shared memory of a block: the pairs' turn fractions [R] (once a block),
-// then for each warp the cosines and sines [2][R] of the token it is at.
-__device__ __forceinline__ void stage_fractions(const RopeParams &p, uint64_t *frac) {
-    for (int i = threadIdx.x; i < p.R; i += blockDim.x) frac[i] = turn_fraction(p.inv_freq[i]);
-    __syncthreads();
-}
-
-// The token's cosines and sines, pair i by lane i % 32.  given: positions
-// come from p.pos, else every pair takes `index`.
-__device__ __forceinline__ void stage_angles(const RopeParams &p, const uint64_t *frac, float *cs, int lane,
-                                             int64_t token, bool given, int64_t index) {
-    __syncwarp();   // the warp's reads of the previous token's angles are done
-    for (int i = lane; i < p.R; i += 32) {
-        const int64_t at = given ? position_of(p, axis_of(p, i), token) : index;
-        float s, c;
-        sincos_turns((uint64_t)at * frac[i], s, c);
-        cs[i] = c;
-        cs[p.R + i] = s;
-    }
-    __syncwarp();
-}
-
-// VE consecutive fp32 values out of shared memory (16-byte aligned where VE
-// is a multiple of 4: R is then one too).
+// A token's cosines and sines (cs[0 .. R), cs[R .. 2R)) by one warp, pair i
+// by lane i % 32, from the position that lane a holds for axis a.
 template <int VE>
-__device__ __forceinline__ void read_floats(const float *p, float (&v)[VE]) {
-    if constexpr (VE % 4 == 0) {
-#pragma unroll
-        for (int j = 0; j < VE; j += 4) {
-            const float4 a = *reinterpret_cast<const float4 *>(p + j);
-            v[j] = a.x, v[j + 1] = a.y, v[j + 2] = a.z, v[j + 3] = a.w;
+__device__ __forceinline__ void make_angles(const RopeParams &p, float *cs, int lane, int64_t pos) {
+    constexpr int N = pairs_at_once(VE);
+    for (int i = lane; i - lane < p.R; i += 32) {
+        int64_t at = pos;
+        if (p.axes > 1) at = __shfl_sync(0xffffffffu, pos, axis_of(p, i));
+        if (i < p.R) {
+            float s, c;
+            sincos_turns((uint64_t)at * turn_fraction(p.inv_freq[i]), s, c);
+            // unit i / VE, pair i % VE of it
+            const int k = table_at<VE>(p.rot_units, i / VE, i % VE);
+            cs[k] = c;
+            cs[p.R + k] = s;
         }
-    } else {
-#pragma unroll
-        for (int j = 0; j < VE; ++j) v[j] = p[j];
     }
+    (void)N;
 }
 
-// Sum over the G lanes of a head (G a power of two, run-time).
-__device__ __forceinline__ float lanes_sum(float v, int g) {
-    if (g > 1) v += __shfl_xor_sync(0xffffffffu, v, 1);
-    if (g > 2) v += __shfl_xor_sync(0xffffffffu, v, 2);
-    if (g > 4) v += __shfl_xor_sync(0xffffffffu, v, 4);
-    if (g > 8) v += __shfl_xor_sync(0xffffffffu, v, 8);
-    if (g > 16) v += __shfl_xor_sync(0xffffffffu, v, 16);
-    return v;
-}
-
-// The head weights (w + bias) of unit u; 1 without a weight.
+// Both kinds' head weights (w + bias; 1 without a weight) into the tables, by
+// the whole block.
 template <typename T, int VE, bool IL>
-__device__ __forceinline__ void read_weight(const RopeParams &p, const void *w, int u, float (&wa)[VE], float (&wb)[VE]) {
-    using P = Piece<T, VE>;
-    constexpr int S = (int)sizeof(typename T::storage);
-#pragma unroll
-    for (int j = 0; j < VE; ++j) wa[j] = wb[j] = 1.f;
-    if (w != nullptr && u < p.units) {
-        int a, b;
-        unit_offsets<VE, IL>(p, u, a, b);
-        P::widen(P::load_w(static_cast<const char *>(w) + a * S), wa);
-        P::widen(P::load_w(static_cast<const char *>(w) + b * S), wb);
-#pragma unroll
-        for (int j = 0; j < VE; ++j) {
-            wa[j] += p.w_bias;
-            wb[j] += p.w_bias;
+__device__ __forceinline__ void make_weights(const RopeParams &p, float *wsm) {
+    const int D = p.head_dim;
+    for (int i = threadIdx.x; i < 2 * D; i += blockDim.x) {
+        const int kind = i >= D, e = i - kind * D;
+        const void *w = kind ? p.k_w : p.q_w;
+        // element e: which pair, and whether it is its second element
+        int pair, second;
+        if (IL) {
+            pair = e >> 1;
+            second = e & 1;
+        } else if (e < 2 * p.R) {
+            second = e >= p.R;
+            pair = e - second * p.R;
+        } else {
+            const int half = D / 2 - p.R;
+            second = e - 2 * p.R >= half;
+            pair = p.R + (e - 2 * p.R - second * half);
         }
+        float v = 1.f;
+        if (w != nullptr) v = widen_bits(ld_bits(w, e, T{}, 2), T{}) + p.w_bias;
+        wsm[(kind * 2 + second) * (D / 2) + table_at<VE>(p.units, pair / VE, pair % VE)] = v;
     }
 }
-
-// The turn of unit u with the weight of its elements folded in (y = turn of
-// w x); units past the rotated part hold w in ca and cd alone, which the
-// caller applies without the cross terms.
-template <typename T, int VE, bool IL>
-__device__ __forceinline__ void weighted_turn(const RopeParams &p, const float *cs, const void *w, int u, Turn<VE> &m) {
-    float wa[VE], wb[VE];
-    read_weight<T, VE, IL>(p, w, u, wa, wb);
-    if (u < p.rot_units) {
-        float c[VE], s[VE];
-        read_floats<VE>(cs + u * VE, c);
-        read_floats<VE>(cs + p.R + u * VE, s);
-#pragma unroll
-        for (int j = 0; j < VE; ++j) {
-            // the weights of pair j's two elements
-            const float w0 = !IL || VE == 1 ? wa[j] : (2 * j < VE ? wa[(2 * j) % VE] : wb[(2 * j) % VE]);
-            const float w1 = !IL || VE == 1 ? wb[j] : (2 * j < VE ? wa[(2 * j + 1) % VE] : wb[(2 * j + 1) % VE]);
-            m.ca[j] = w0 * c[j];
-            m.cb[j] = -w1 * s[j];
-            m.cc[j] = w0 * s[j];
-            m.cd[j] = w1 * c[j];
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < VE; ++j) {
-            m.ca[j] = wa[j];
-            m.cd[j] = wb[j];
-            m.cb[j] = m.cc[j] = 0.f;
-        }
-    }
-}
-
-// The flat list of head iterations (32 / G heads of one token each, `per` a
-// token) cut into equal runs, one a warp.
-struct Run {
-    int64_t token, at, end;
-    int it;
-    __device__ __forceinline__ void start(int64_t warp, int64_t each, int64_t extra, int per) {
-        at = warp * each + (warp < extra ? warp : extra);
-        end = at + each + (warp < extra ? 1 : 0);
-        token = ((at | per) >> 32) == 0 ? (int64_t)((uint32_t)at / (uint32_t)per) : at / per;
-        it = (int)(at - token * per);
-    }
-    // Iterations of the run from here on that are of this token, at most n.
-    __device__ __forceinline__ int count(int per, int n) const {
-        const int64_t left = end - at;
-        const int c = per - it < n ? per - it : n;
-        return left < c ? (int)left : c;
-    }
-    __device__ __forceinline__ void advance(int n, int per) {
-        at += n;
-        it += n;
-        if (it == per) {
-            it = 0;
-            ++token;
-        }
-    }
-};
 
 // ------------------------------------------------------------ paged cache
 
@@ -492,389 +428,418 @@ __device__ __forceinline__ int64_t cache_row(const RopeParams &p, int seq, int64
 
 enum RopeMode { kRopePlain = 0, kRopeAppend = 1, kRopeAppendE4m3 = 2 };
 
+// A lane's units of a head: where their pieces start (bytes), and which exist.
+// Lanes without a unit take unit 0's place (they load it like a neighbour: no
+// branch, no zeroing) and have no part in sums and stores.
+template <int VE, int K, bool IL, int S>
+struct Lane {
+    int oa[K], ob[K], unit[K];
+    bool act[K];
+    __device__ __forceinline__ void set(const RopeParams &p, int t) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            act[k] = t + k * p.lanes < p.units;
+            unit[k] = act[k] ? t + k * p.lanes : 0;
+            unit_offsets<VE, IL>(p, unit[k], oa[k], ob[k]);
+            oa[k] *= S;
+            ob[k] *= S;
+        }
+    }
+};
+
+// A block's run of jobs (a token's slice of head iterations; equal runs, one
+// more for the first `extra` blocks).
+struct Jobs {
+    int64_t first, last;
+    __device__ __forceinline__ void set(int64_t block, int64_t each, int64_t extra) {
+        first = block * each + (block < extra ? block : extra);
+        last = first + each + (block < extra ? 1 : 0);
+    }
+};
+
+template <typename T, int VE>
+__device__ __forceinline__ void widen_unit(const typename Piece<T, VE>::Raw &a, const typename Piece<T, VE>::Raw &b,
+                                           float (&e)[2 * VE]) {
+    float x[VE], y[VE];
+    Piece<T, VE>::widen(a, x);
+    Piece<T, VE>::widen(b, y);
+#pragma unroll
+    for (int j = 0; j < VE; ++j) {
+        e[j] = x[j];
+        e[VE + j] = y[j];
+    }
+}
+
+// Keeps the compiler from holding the widened values of a raw piece across
+// this point: they are widened again where they are needed.
+template <typename Raw>
+__device__ __forceinline__ void forget(Raw &r) {
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(r.u) / 4); ++i) asm volatile("" : "+r"(r.u[i]));
+}
+
+// Sum over the G lanes of a head (G a power of two, run-time), of one or two values.
+__device__ __forceinline__ float lanes_sum(float v, int g) {
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1)
+        if (g > off) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
 // ----------------------------------------------------------------- forward
-// UN head iterations are loaded while the UN before them are worked on.  A
-// value's weight is folded into its token's turn, so a head costs its sum of
-// squares, one 2 x 2 turn a pair and one product with r.
-template <typename T, int VE, int K, bool IL, int MODE, int UN>
+template <typename T, int VE, int K, bool IL, int MODE>
 __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(VE, K)) rope_kernel(const RopeParams p) {
     using P = Piece<T, VE>;
     using Raw = typename P::Raw;
     constexpr int S = (int)sizeof(typename T::storage);
+    constexpr int N = pairs_at_once(VE);
     constexpr bool APPEND = MODE != kRopePlain;
-    extern __shared__ __align__(16) unsigned char smem[];
+    extern __shared__ __align__(16) float wsm[];
+    __shared__ int64_t rows[2][kRopeMaxWarps];   // append: where the tile's tokens go, -1: nowhere
 
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G = p.lanes, t = lane & (G - 1), group = lane / G, hpw = 32 / G;
-    uint64_t *frac = reinterpret_cast<uint64_t *>(smem);
-    float *cs = reinterpret_cast<float *>(frac + ((p.R + 1) & ~1)) + warp * 2 * p.R;
+    float *tiles = wsm + 2 * p.head_dim;
     const int heads = p.q_heads + p.k_heads + p.v_heads, turned = p.q_heads + p.k_heads;
-    const int per = p.per;
-
-    int oa[K], ob[K];   // byte offsets of the lane's pieces in a head; -1: no unit
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        oa[k] = ob[k] = -1;
-        if (t + k * G < p.units) {
-            unit_offsets<VE, IL>(p, t + k * G, oa[k], ob[k]);
-            oa[k] *= S;
-            ob[k] *= S;
-        }
-    }
     const int head_bytes = p.head_dim * S;
+    Lane<VE, K, IL, S> my;
+    my.set(p, t);
+    Jobs jobs;
+    jobs.set(blockIdx.x, p.each, p.extra);
 
-    Run run;
-    run.start((int64_t)blockIdx.x * warps + warp, p.each, p.extra, per);
     pdl_wait_for_inputs();
     pdl_allow_dependents();
     if constexpr (APPEND) {   // rows behind the last sequence are left as they are
         const int64_t valid = p.cu_tokens[p.seqs];
-        const int64_t most = (valid < 0 ? 0 : valid) * per;
-        if (run.end > most) run.end = most;
+        const int64_t most = (valid < 0 ? 0 : valid) * p.slices;
+        if (jobs.last > most) jobs.last = most;
     }
 
-    auto load = [&](const Run &r, int n, Raw (&ra)[UN][K], Raw (&rb)[UN][K]) {
-        const char *src = static_cast<const char *>(p.x) + r.token * p.x_stride;
+    // job j of a tile, its iteration i: token and first head iteration
+    auto load = [&](int64_t token, int it, Raw (&ra)[K], Raw (&rb)[K]) {
+        int h = it * hpw + group;
+        h = h < heads ? h : heads - 1;
+        const char *src = static_cast<const char *>(p.x) + token * p.x_stride + (int64_t)h * head_bytes;
 #pragma unroll
-        for (int i = 0; i < UN; ++i) {
-            const int h = (r.it + i) * hpw + group;
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                ra[i][k] = rb[i][k] = P::zero();
-                if (i < n && h < heads && oa[k] >= 0) {
-                    ra[i][k] = P::load(src + (h * head_bytes + oa[k]));
-                    rb[i][k] = P::load(src + (h * head_bytes + ob[k]));
-                }
-            }
+        for (int k = 0; k < K; ++k) {
+            ra[k] = P::load(src + my.oa[k]);
+            rb[k] = P::load(src + my.ob[k]);
         }
     };
 
-    int64_t row = -1;
-    int held = -1;              // whose weights are in m: 0 query, 1 key
-    Turn<VE> m[K];
-    // One batch: `now` holds it, the next one's loads go into `next`.
-    auto step = [&](Raw (&na)[UN][K], Raw (&nb)[UN][K], Raw (&xa)[UN][K], Raw (&xb)[UN][K], bool first) {
-        const int n = run.count(per, UN);
-        Run ahead = run;
-        ahead.advance(n, per);
-        const int more = ahead.count(per, UN);
-        if (more > 0) load(ahead, more, xa, xb);
-        if (first || run.it == 0) {   // a token the warp has not been at
-            int64_t index = 0;
-            if constexpr (APPEND) {
-                const int seq = sequence_of(p, run.token, lane);
-                index = (int64_t)p.cache_lens[seq] + (run.token - p.cu_tokens[seq]);
-                row = cache_row(p, seq, index);
+    bool first_tile = true;
+    int buf = 0;
+    for (int64_t base = jobs.first; base < jobs.last; base += kRopeMaxWarps, buf ^= 1) {
+        const int n = jobs.last - base < kRopeMaxWarps ? (int)(jobs.last - base) : kRopeMaxWarps;
+        // the warp's iterations of the tile: job j, iteration i of its slice
+        int j = 0, i = warp;
+        while (j < n && i >= p.iters) i -= p.iters, ++j;
+        Raw ra[K], rb[K];
+        int64_t token = base;
+        int it = i;
+        if (j < n) {
+            if (p.slices > 1) {
+                token = (base + j) / p.slices;
+                it = i + (int)(base + j - token * p.slices) * p.iters;
+            } else {
+                token = base + j;
             }
-            if (run.it * hpw < turned) stage_angles(p, frac, cs, lane, run.token, p.pos != nullptr, index);
-            held = -1;
+            load(token, it, ra, rb);
         }
-        char *yr = static_cast<char *>(p.y) + run.token * p.y_stride;
+        // the warp's own token of the tile: where it goes, its angles
+        if (warp < n) {
+            const int64_t mine = p.slices > 1 ? (base + warp) / p.slices : base + warp;
+            int64_t pos = 0;
+            if constexpr (APPEND) {
+                const int seq = sequence_of(p, mine, lane);
+                pos = (int64_t)p.cache_lens[seq] + (mine - p.cu_tokens[seq]);
+                const int64_t row = cache_row(p, seq, pos);
+                if (lane == 0) rows[buf][warp] = row;
+            }
+            if (!APPEND || p.pos != nullptr) pos = lane_position(p, lane, mine);
+            make_angles<VE>(p, tiles + (buf * kRopeMaxWarps + warp) * 2 * p.R, lane, pos);
+        }
+        if (first_tile) make_weights<T, VE, IL>(p, wsm);
+        first_tile = false;
+        __syncthreads();   // two buffers: the tile before this one may still be read
+        while (j < n) {
+            Raw ca[K], cb[K];
 #pragma unroll
-        for (int i = 0; i < UN; ++i) {
-            if (i >= n) break;   // the same for every lane
-            const int h = (run.it + i) * hpw + group;
-            const bool value = APPEND && h >= turned;
-            float va[K][VE], vb[K][VE];
-            float2 acc = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                P::widen(na[i][k], va[k]);
-                P::widen(nb[i][k], vb[k]);
-                dot_into<VE>(acc, va[k], va[k]);
-                dot_into<VE>(acc, vb[k], vb[k]);
+            for (int k = 0; k < K; ++k) ca[k] = ra[k], cb[k] = rb[k];
+            const int64_t tok = token;
+            const int h = it * hpw + group, tile_job = j;
+            i += kRopeMaxWarps;
+            while (j < n && i >= p.iters) i -= p.iters, ++j;
+            if (j < n) {   // the next one's loads
+                if (p.slices > 1) {
+                    token = (base + j) / p.slices;
+                    it = i + (int)(base + j - token * p.slices) * p.iters;
+                } else {
+                    token = base + j;
+                    it = i;
+                }
+                load(token, it, ra, rb);
             }
             float r = 1.f;
-            if (p.norm) r = rsqrtf(fmaf(lanes_sum(acc.x + acc.y, G), p.inv_dim, p.eps));
-            if (!value) {
-                const int kind = h >= p.q_heads;
-                if (kind != held) {
-                    held = kind;
-#pragma unroll
-                    for (int k = 0; k < K; ++k)
-                        weighted_turn<T, VE, IL>(p, cs, kind ? p.k_w : p.q_w, t + k * G, m[k]);
-                }
+            if (p.norm) {
+                float sum = 0.f;
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
-                    if (t + k * G < p.rot_units) {
-                        turn_unit<VE, IL>(va[k], vb[k], m[k]);
-                    } else {
-                        times<VE>(va[k], m[k].ca);
-                        times<VE>(vb[k], m[k].cd);
-                    }
-                    if (p.norm) {
-                        scale_by<VE>(va[k], r);
-                        scale_by<VE>(vb[k], r);
+                    float e[2 * VE];
+                    widen_unit<T, VE>(ca[k], cb[k], e);
+                    float2 acc = make_float2(0.f, 0.f);
+                    squares_into<2 * VE>(acc, e);
+                    sum += my.act[k] ? acc.x + acc.y : 0.f;
+                }
+                r = rsqrtf(fmaf(lanes_sum(sum, G), p.inv_dim, p.eps));
+#pragma unroll
+                for (int k = 0; k < K; ++k) forget(ca[k]), forget(cb[k]);
+            }
+            const bool value = APPEND && h >= turned;
+            const float *cs = tiles + (buf * kRopeMaxWarps + tile_job) * 2 * p.R;
+            const float *w = wsm + (h >= p.q_heads ? p.head_dim : 0);
+            int64_t row = 0;
+            if constexpr (APPEND) row = rows[buf][tile_job];
+            char *dst;
+            if (!APPEND || h < p.q_heads) {
+                dst = static_cast<char *>(p.y) + tok * p.y_stride + (int64_t)h * head_bytes;
+            } else {
+                const int o = value ? h - turned : h - p.q_heads;
+                dst = static_cast<char *>(value ? p.v_cache : p.k_cache) + row + (int64_t)o * p.head_stride;
+                if (row < 0 && h == p.q_heads && t == 0 && p.dropped != nullptr) atomicAdd(p.dropped, 1);
+            }
+            const bool store = h < heads && (!APPEND || h < p.q_heads || row >= 0);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float e[2 * VE];
+                widen_unit<T, VE>(ca[k], cb[k], e);
+                if (!value) {
+#pragma unroll
+                    for (int q = 0; q < VE; q += N) {
+                        float w0[N], w1[N];
+                        const int at = table_at<VE>(p.units, my.unit[k], q);
+                        read_table<N>(w + at, w0);
+                        read_table<N>(w + p.head_dim / 2 + at, w1);
+                        weigh_pairs<VE, IL, N>(e, q, w0, w1, r);
+                        if (my.unit[k] < p.rot_units) {
+                            float c[N], s[N];
+                            const int turn = table_at<VE>(p.rot_units, my.unit[k], q);
+                            read_table<N>(cs + turn, c);
+                            read_table<N>(cs + p.R + turn, s);
+                            turn_pairs<VE, IL, N>(e, q, c, s);
+                        }
                     }
                 }
-            }
-            if (!APPEND || h < p.q_heads) {
-                char *dst = yr + (int64_t)h * head_bytes;
+                if (store && my.act[k]) {
+                    float x[VE], y[VE];
 #pragma unroll
-                for (int k = 0; k < K; ++k)
-                    if (h < heads && oa[k] >= 0) {
-                        P::store(dst + oa[k], va[k]);
-                        P::store(dst + ob[k], vb[k]);
+                    for (int v = 0; v < VE; ++v) x[v] = e[v], y[v] = e[VE + v];
+                    if (MODE == kRopeAppendE4m3 && h >= p.q_heads) {
+                        const float inv = value ? p.v_inv : p.k_inv;
+                        P::store_e4m3(dst + my.oa[k] / S, x, inv);
+                        P::store_e4m3(dst + my.ob[k] / S, y, inv);
+                    } else {
+                        P::store(dst + my.oa[k], x);
+                        P::store(dst + my.ob[k], y);
                     }
-            } else {
-                if (row < 0) {
-                    if (h == p.q_heads && t == 0 && p.dropped != nullptr) atomicAdd(p.dropped, 1);
-                } else if (h < heads) {
-                    const int j = value ? h - turned : h - p.q_heads;
-                    char *dst = static_cast<char *>(value ? p.v_cache : p.k_cache) + row + (int64_t)j * p.head_stride;
-#pragma unroll
-                    for (int k = 0; k < K; ++k)
-                        if (oa[k] >= 0) {
-                            if constexpr (MODE == kRopeAppendE4m3) {
-                                const float inv = value ? p.v_inv : p.k_inv;
-                                P::store_e4m3(dst + oa[k] / S, va[k], inv);
-                                P::store_e4m3(dst + ob[k] / S, vb[k], inv);
-                            } else {
-                                P::store(dst + oa[k], va[k]);
-                                P::store(dst + ob[k], vb[k]);
-                            }
-                        }
                 }
             }
         }
-        run = ahead;
-    };
-
-    // the first loads are on their way while the block prepares its table
-    Raw ra[UN][K], rb[UN][K], sa[UN][K], sb[UN][K];
-    if (run.at < run.end) load(run, run.count(per, UN), ra, rb);
-    stage_fractions(p, frac);
-    bool first = true;
-    while (run.at < run.end) {
-        step(ra, rb, sa, sb, first);
-        first = false;
-        if (run.at >= run.end) break;
-        step(sa, sb, ra, rb, false);
     }
 }
 
 // ---------------------------------------------------------------- gradient
-// Persistent blocks.  The query heads of all tokens, then the key heads, are
-// a flat list of head iterations each; every warp takes an equal run of it,
-// keeps its share of the weight's gradient in registers, and the block's sum
-// goes to partial[block][kind][D].  The order of every sum follows from the
-// sizes and the grid: no atomics.
+// Blocks 0 .. q_blocks - 1 take the query heads, the rest the key heads, an
+// equal run of tokens each.  A thread keeps its units' share of the weight's
+// gradient in registers; the block's sum goes to partial[block][D], and the
+// blocks' are added up by another kernel.  The order of every sum follows
+// from the sizes and the grid: no atomics.
 // x is read only with the norm; without it dx = dy turned back.
-template <typename T, int VE, int K, bool IL, bool NORM, int UN>
-__global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(VE, K)) rope_bwd_kernel(const RopeParams p) {
+template <typename T, int VE, int K, bool IL, bool NORM>
+__global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(VE, K)) rope_bwd_kernel(const RopeParams p) {
     using P = Piece<T, VE>;
     using Raw = typename P::Raw;
     constexpr int S = (int)sizeof(typename T::storage);
-    constexpr int KN = NORM ? K : 1, UX = NORM ? UN : 1;
-    extern __shared__ __align__(16) unsigned char smem[];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    constexpr int N = pairs_at_once(VE);
+    constexpr int KN = NORM ? K : 1;
+    extern __shared__ __align__(16) float wsm[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G = p.lanes, t = lane & (G - 1), group = lane / G, hpw = 32 / G;
-    uint64_t *frac = reinterpret_cast<uint64_t *>(smem);
-    float *cs_all = reinterpret_cast<float *>(frac + ((p.R + 1) & ~1));
-    float *cs = cs_all + warp * 2 * p.R;
-    float *wsm = cs_all + warps * 2 * p.R;    // the kind's weight in lane order, with the norm
-    float *sums = wsm + (NORM ? K * VE * 64 : 0);   // [warps][D], with a weight's gradient
-
-    int oa[K], ob[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        oa[k] = ob[k] = -1;
-        if (t + k * G < p.units) {
-            unit_offsets<VE, IL>(p, t + k * G, oa[k], ob[k]);
-            oa[k] *= S;
-            ob[k] *= S;
-        }
-    }
+    float *tiles = wsm + 2 * p.head_dim;
     const int head_bytes = p.head_dim * S;
+    Lane<VE, K, IL, S> my;
+    my.set(p, t);
+    const bool key = (int)blockIdx.x >= p.q_blocks;
+    const int heads = key ? p.k_heads : p.q_heads, iters = key ? p.iters_k : p.iters;
+    Jobs jobs;
+    jobs.set(key ? blockIdx.x - p.q_blocks : blockIdx.x, key ? p.each_k : p.each, key ? p.extra_k : p.extra);
+    const int64_t head0 = key ? (int64_t)p.q_heads * head_bytes : 0;
+    const float *w = wsm + (key ? p.head_dim : 0);
+
     pdl_wait_for_inputs();
     pdl_allow_dependents();
-    stage_fractions(p, frac);
 
-    const int64_t me = (int64_t)blockIdx.x * warps + warp;
-    for (int kind = 0; kind < 2; ++kind) {
-        const int heads = kind ? p.k_heads : p.q_heads;
-        const int per = kind ? p.per_k : p.per;   // iterations a token
-        float ga[KN][VE], gb[KN][VE];             // the weight's gradient
+    auto load = [&](int64_t token, int it, Raw (&da)[K], Raw (&db)[K], Raw (&xa)[KN], Raw (&xb)[KN]) {
+        int h = it * hpw + group;
+        h = h < heads ? h : heads - 1;
+        const int64_t off = head0 + (int64_t)h * head_bytes;
+        const char *gr = static_cast<const char *>(p.dy) + token * p.dy_stride + off;
+        const char *xr = static_cast<const char *>(p.x) + token * p.x_stride + off;
 #pragma unroll
-        for (int k = 0; k < KN; ++k)
-#pragma unroll
-            for (int j = 0; j < VE; ++j) ga[k][j] = gb[k][j] = 0.f;
-        if (heads > 0) {
-            Run run;
-            run.start(me, kind ? p.each_k : p.each, kind ? p.extra_k : p.extra, per);
-            if constexpr (NORM) {   // the kind's weights, unit by unit: 2 VE floats each
-                __syncthreads();
-                for (int u = threadIdx.x; u < p.units; u += blockDim.x) {
-                    float wa[VE], wb[VE];
-                    read_weight<T, VE, IL>(p, kind ? p.k_w : p.q_w, u, wa, wb);
-#pragma unroll
-                    for (int j = 0; j < VE; ++j) {
-                        wsm[2 * VE * u + j] = wa[j];
-                        wsm[2 * VE * u + VE + j] = wb[j];
-                    }
-                }
-                __syncthreads();
-            }
-            const int64_t head0 = (int64_t)(kind ? p.q_heads : 0) * head_bytes;
-            const char *x0 = static_cast<const char *>(p.x) + head0, *g0 = static_cast<const char *>(p.dy) + head0;
-            char *y0 = static_cast<char *>(p.y) + head0;
-
-            auto load = [&](const Run &r, int n, Raw (&da)[UN][K], Raw (&db)[UN][K], Raw (&xa)[UX][K],
-                            Raw (&xb)[UX][K]) {
-                const char *gr = g0 + r.token * p.dy_stride;
-                const char *xr = x0 + r.token * p.x_stride;
-#pragma unroll
-                for (int i = 0; i < UN; ++i) {
-                    const int h = (r.it + i) * hpw + group;
-#pragma unroll
-                    for (int k = 0; k < K; ++k) {
-                        da[i][k] = db[i][k] = P::zero();
-                        if constexpr (NORM) xa[i][k] = xb[i][k] = P::zero();
-                        if (i < n && h < heads && oa[k] >= 0) {
-                            da[i][k] = P::load(gr + (h * head_bytes + oa[k]));
-                            db[i][k] = P::load(gr + (h * head_bytes + ob[k]));
-                            if constexpr (NORM) {
-                                xa[i][k] = P::load(xr + (h * head_bytes + oa[k]));
-                                xb[i][k] = P::load(xr + (h * head_bytes + ob[k]));
-                            }
-                        }
-                    }
-                }
-            };
-
-            auto step = [&](Raw (&da)[UN][K], Raw (&db)[UN][K], Raw (&xa)[UX][K], Raw (&xb)[UX][K], Raw (&ea)[UN][K],
-                            Raw (&eb)[UN][K], Raw (&za)[UX][K], Raw (&zb)[UX][K], bool first) {
-                const int n = run.count(per, UN);
-                Run ahead = run;
-                ahead.advance(n, per);
-                const int more = ahead.count(per, UN);
-                if (more > 0) load(ahead, more, ea, eb, za, zb);
-                if (first || run.it == 0) {
-                    stage_angles(p, frac, cs, lane, run.token, true, 0);
-                }
-                char *yr = y0 + run.token * p.y_stride;
-#pragma unroll
-                for (int i = 0; i < UN; ++i) {
-                    if (i >= n) break;   // the same for every lane
-                    const int h = (run.it + i) * hpw + group;
-                    // cosines, sines and weights come from shared memory at each
-                    // use: held in registers they spilled (128 a thread)
-                    float va[K][VE], vb[K][VE], fa[KN][VE], fb[KN][VE];
-                    float2 sq = make_float2(0.f, 0.f), dot = sq;
-#pragma unroll
-                    for (int k = 0; k < K; ++k) {
-                        P::widen(da[i][k], va[k]);
-                        P::widen(db[i][k], vb[k]);
-                        const int u = t + k * G;
-                        if (u < p.rot_units) {
-                            Turn<VE> m;
-                            read_floats<VE>(cs + u * VE, m.ca);
-                            read_floats<VE>(cs + p.R + u * VE, m.cb);
-#pragma unroll
-                            for (int j = 0; j < VE; ++j) {
-                                m.cc[j] = -m.cb[j];
-                                m.cd[j] = m.ca[j];
-                            }
-                            turn_unit<VE, IL>(va[k], vb[k], m);
-                        }
-                        if constexpr (NORM) {
-                            float wa[VE], wb[VE];
-                            const float *pw = wsm + 2 * VE * (u < p.units ? u : 0);
-                            read_floats<VE>(pw, wa);
-                            read_floats<VE>(pw + VE, wb);
-                            P::widen(xa[i][k], fa[k]);
-                            P::widen(xb[i][k], fb[k]);
-                            dot_into<VE>(sq, fa[k], fa[k]);
-                            dot_into<VE>(sq, fb[k], fb[k]);
-                            float ta[VE], tb[VE];
-#pragma unroll
-                            for (int j = 0; j < VE; ++j) ta[j] = fa[k][j], tb[j] = fb[k][j];
-                            times<VE>(ta, va[k]);   // x g, summed with the weight
-                            times<VE>(tb, vb[k]);
-                            dot_into<VE>(dot, ta, wa);
-                            dot_into<VE>(dot, tb, wb);
-                        }
-                    }
-                    if constexpr (NORM) {
-                        const float s1 = lanes_sum(sq.x + sq.y, G), s2 = lanes_sum(dot.x + dot.y, G);
-                        // an idle head's zeros must add nothing, whatever eps is
-                        const float r = h < heads ? rsqrtf(fmaf(s1, p.inv_dim, p.eps)) : 0.f;
-                        const float mean = (s2 * p.inv_dim) * r;   // dx = r (w g - (x r) mean)
-#pragma unroll
-                        for (int k = 0; k < K; ++k) {
-                            scale_by<VE>(fa[k], r);
-                            scale_by<VE>(fb[k], r);
-#pragma unroll
-                            for (int j = 0; j < VE; ++j) {
-                                ga[k][j] = fmaf(va[k][j], fa[k][j], ga[k][j]);
-                                gb[k][j] = fmaf(vb[k][j], fb[k][j], gb[k][j]);
-                            }
-                            const int u = t + k * G;
-                            float wa[VE], wb[VE];
-                            const float *pw = wsm + 2 * VE * (u < p.units ? u : 0);
-                            read_floats<VE>(pw, wa);
-                            read_floats<VE>(pw + VE, wb);
-                            times<VE>(va[k], wa);
-                            times<VE>(vb[k], wb);
-#pragma unroll
-                            for (int j = 0; j < VE; ++j) {
-                                va[k][j] = fmaf(fa[k][j], -mean, va[k][j]);
-                                vb[k][j] = fmaf(fb[k][j], -mean, vb[k][j]);
-                            }
-                            scale_by<VE>(va[k], r);
-                            scale_by<VE>(vb[k], r);
-                        }
-                    }
-                    char *dst = yr + (int64_t)h * head_bytes;
-#pragma unroll
-                    for (int k = 0; k < K; ++k)
-                        if (h < heads && oa[k] >= 0) {
-                            P::store(dst + oa[k], va[k]);
-                            P::store(dst + ob[k], vb[k]);
-                        }
-                }
-                run = ahead;
-            };
-
-            Raw da[UN][K], db[UN][K], xa[UX][K], xb[UX][K], ea[UN][K], eb[UN][K], za[UX][K], zb[UX][K];
-            bool first = true;
-            if (run.at < run.end) load(run, run.count(per, UN), da, db, xa, xb);
-            while (run.at < run.end) {
-                step(da, db, xa, xb, ea, eb, za, zb, first);
-                first = false;
-                if (run.at >= run.end) break;
-                step(ea, eb, za, zb, da, db, xa, xb, false);
+        for (int k = 0; k < K; ++k) {
+            da[k] = P::load(gr + my.oa[k]);
+            db[k] = P::load(gr + my.ob[k]);
+            if constexpr (NORM) {
+                xa[k] = P::load(xr + my.oa[k]);
+                xb[k] = P::load(xr + my.ob[k]);
             }
         }
-        if constexpr (NORM) {
-            if (p.partial != nullptr) {
-                // the heads side by side in the warp, then the block's warps
+    };
+
+    float gw[KN][2 * VE];   // the weight's gradient
+#pragma unroll
+    for (int k = 0; k < KN; ++k)
+#pragma unroll
+        for (int v = 0; v < 2 * VE; ++v) gw[k][v] = 0.f;
+
+    bool first_tile = true;
+    int buf = 0;
+    for (int64_t base = jobs.first; base < jobs.last; base += kRopeMaxWarps, buf ^= 1) {
+        const int n = jobs.last - base < kRopeMaxWarps ? (int)(jobs.last - base) : kRopeMaxWarps;
+        int j = 0, i = warp;
+        while (j < n && i >= iters) i -= iters, ++j;
+        Raw da[K], db[K], xa[KN], xb[KN];
+        if (j < n) load(base + j, i, da, db, xa, xb);
+        if (warp < n)
+            make_angles<VE>(p, tiles + (buf * kRopeMaxWarps + warp) * 2 * p.R, lane,
+                            lane_position(p, lane, base + warp));
+        if (first_tile && NORM) make_weights<T, VE, IL>(p, wsm);
+        first_tile = false;
+        __syncthreads();   // two buffers: the tile before this one may still be read
+        while (j < n) {
+            Raw ea[K], eb[K], ya[KN], yb[KN];
+#pragma unroll
+            for (int k = 0; k < K; ++k) ea[k] = da[k], eb[k] = db[k];
+#pragma unroll
+            for (int k = 0; k < KN; ++k) ya[k] = xa[k], yb[k] = xb[k];
+            const int64_t token = base + j;
+            const int h = i * hpw + group;
+            const float *cs = tiles + (buf * kRopeMaxWarps + j) * 2 * p.R;
+            i += kRopeMaxWarps;
+            while (j < n && i >= iters) i -= iters, ++j;
+            if (j < n) load(base + j, i, da, db, xa, xb);
+
+            float g[K][2 * VE];
+            float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                widen_unit<T, VE>(ea[k], eb[k], g[k]);
+                if (my.unit[k] < p.rot_units) {
+#pragma unroll
+                    for (int q = 0; q < VE; q += N) {
+                        float c[N], s[N];
+                        const int turn = table_at<VE>(p.rot_units, my.unit[k], q);
+                        read_table<N>(cs + turn, c);
+                        read_table<N>(cs + p.R + turn, s);
+#pragma unroll
+                        for (int v = 0; v < N; ++v) s[v] = -s[v];
+                        turn_pairs<VE, IL, N>(g[k], q, c, s);
+                    }
+                }
+                if constexpr (NORM) {
+                    float x[2 * VE];
+                    widen_unit<T, VE>(ya[k], yb[k], x);
+                    float2 sq = make_float2(0.f, 0.f), dot = sq;
+                    squares_into<2 * VE>(sq, x);
+#pragma unroll
+                    for (int q = 0; q < VE; q += N) {
+                        float w0[N], w1[N];
+                        const int at = table_at<VE>(p.units, my.unit[k], q);
+                        read_table<N>(w + at, w0);
+                        read_table<N>(w + p.head_dim / 2 + at, w1);
+#pragma unroll
+                        for (int v = 0; v < N; ++v) {
+                            const int a = first_of<VE, IL>(q + v), b = second_of<VE, IL>(q + v);
+                            dot = __ffma2_rn(__fmul2_rn(make_float2(g[k][a], g[k][b]), make_float2(w0[v], w1[v])),
+                                             make_float2(x[a], x[b]), dot);
+                        }
+                    }
+                    s1 += my.act[k] ? sq.x + sq.y : 0.f;
+                    s2 += my.act[k] ? dot.x + dot.y : 0.f;
+                }
+            }
+            float r = 1.f, mean = 0.f;
+            if constexpr (NORM) {
+                s1 = lanes_sum(s1, G);
+                s2 = lanes_sum(s2, G);
+                r = rsqrtf(fmaf(s1, p.inv_dim, p.eps));
+                mean = -(s2 * p.inv_dim) * r;   // dx = r (w g - (x r) mean)
+#pragma unroll
+                for (int k = 0; k < K; ++k) forget(ya[k]), forget(yb[k]);
+            }
+            char *dst = static_cast<char *>(p.y) + token * p.y_stride + head0 + (int64_t)h * head_bytes;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                if constexpr (NORM) {
+                    float x[2 * VE];
+                    widen_unit<T, VE>(ya[k], yb[k], x);
+#pragma unroll
+                    for (int q = 0; q < VE; q += N) {
+                        float w0[N], w1[N];
+                        const int at = table_at<VE>(p.units, my.unit[k], q);
+                        read_table<N>(w + at, w0);
+                        read_table<N>(w + p.head_dim / 2 + at, w1);
+#pragma unroll
+                        for (int v = 0; v < N; ++v) {
+                            const int a = first_of<VE, IL>(q + v), b = second_of<VE, IL>(q + v);
+                            const float2 xr = __fmul2_rn(make_float2(x[a], x[b]), make_float2(r, r));
+                            const float2 gv = make_float2(g[k][a], g[k][b]);
+                            if (h < heads) {   // an idle head's copy adds nothing
+                                const float2 acc = __ffma2_rn(gv, xr, make_float2(gw[k][a], gw[k][b]));
+                                gw[k][a] = acc.x, gw[k][b] = acc.y;
+                            }
+                            const float2 d = __fmul2_rn(
+                                __ffma2_rn(xr, make_float2(mean, mean), __fmul2_rn(gv, make_float2(w0[v], w1[v]))),
+                                make_float2(r, r));
+                            g[k][a] = d.x, g[k][b] = d.y;
+                        }
+                    }
+                }
+                if (h < heads && my.act[k]) {
+                    float u[VE], v[VE];
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) u[e] = g[k][e], v[e] = g[k][VE + e];
+                    P::store(dst + my.oa[k], u);
+                    P::store(dst + my.ob[k], v);
+                }
+            }
+        }
+    }
+    if constexpr (NORM) {
+        if (p.partial != nullptr) {
+            // the heads side by side in the warp, then the block's warps
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int v = 0; v < 2 * VE; ++v)
+                    for (int off = G; off < 32; off <<= 1) gw[k][v] += __shfl_xor_sync(0xffffffffu, gw[k][v], off);
+            __syncthreads();   // the tables are read; their place takes the warps' sums [kRopeMaxWarps][D]
+            if (group == 0) {
 #pragma unroll
                 for (int k = 0; k < K; ++k)
+                    if (my.act[k])
 #pragma unroll
-                    for (int j = 0; j < VE; ++j)
-                        for (int off = G; off < 32; off <<= 1) {
-                            ga[k][j] += __shfl_xor_sync(0xffffffffu, ga[k][j], off);
-                            gb[k][j] += __shfl_xor_sync(0xffffffffu, gb[k][j], off);
+                        for (int v = 0; v < VE; ++v) {
+                            wsm[warp * p.head_dim + my.oa[k] / S + v] = gw[k][v];
+                            wsm[warp * p.head_dim + my.ob[k] / S + v] = gw[k][VE + v];
                         }
-                __syncthreads();   // the previous kind's sums are read
-                if (group == 0) {
-#pragma unroll
-                    for (int k = 0; k < K; ++k)
-                        if (oa[k] >= 0)
-#pragma unroll
-                            for (int j = 0; j < VE; ++j) {
-                                sums[warp * p.head_dim + oa[k] / S + j] = ga[k][j];
-                                sums[warp * p.head_dim + ob[k] / S + j] = gb[k][j];
-                            }
-                }
-                __syncthreads();
-                float *out = p.partial + ((int64_t)blockIdx.x * 2 + kind) * p.head_dim;
-                for (int d = threadIdx.x; d < p.head_dim; d += blockDim.x) {
-                    float v = 0.f;
-                    for (int w = 0; w < warps; ++w) v += sums[w * p.head_dim + d];
-                    out[d] = v;
-                }
+            }
+            __syncthreads();
+            float *out = p.partial + (int64_t)blockIdx.x * p.head_dim;
+            for (int d = threadIdx.x; d < p.head_dim; d += blockDim.x) {
+                float v = 0.f;
+                for (int k = 0; k < kRopeMaxWarps; ++k) v += wsm[k * p.head_dim + d];
+                out[d] = v;
             }
         }
     }
