@@ -7,6 +7,8 @@ fallback path.
 """
 from __future__ import annotations
 
+import functools
+import struct
 from typing import Optional
 
 import torch
@@ -184,72 +186,90 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _launch(device, stream, call, *args):
-    """call(*args, stream handle) with the tensors' device current."""
-    if stream is not None and stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    s = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-    if torch.cuda.current_device() == device.index:
+# The calls below are made once a layer and token batch, and their kernels may
+# take two microseconds: the checks compare device numbers, types and shapes
+# without making device objects or contexts.
+_raw_stream = torch._C._cuda_getCurrentRawStream      # the current stream's handle, by device number
+_current_device = torch._C._cuda_getDevice
+
+
+def _launch(dev: int, stream, call, *args):
+    """call(*args, stream handle) with device number ``dev`` current."""
+    if stream is None:
+        s = _raw_stream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{dev}")
+    else:
+        s = stream.cuda_stream
+    if _current_device() == dev:
         call(*args, s)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(dev):
             call(*args, s)
 
 
-def _head_rows(t: torch.Tensor, name: str, width: int, like=None) -> int:
-    """Token stride of a [tokens, >= width] tensor of packed heads (the last
-    dimension contiguous), on the device and of the type of ``like``."""
-    if not t.is_cuda:
+def _device_of(t: torch.Tensor, name: str) -> int:
+    dev = t.get_device()
+    if dev < 0 or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
-    if t.dim() != 2 or t.shape[1] < width:
-        raise ValueError(f"{name} must be a 2-D tensor of at least {width} columns, got {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    return dev
+
+
+def _head_rows(t: torch.Tensor, name: str, width: int, tokens: int, dtype, dev: int) -> int:
+    """Token stride of a [tokens, >= width] tensor of packed heads (the last
+    dimension contiguous)."""
+    if t.get_device() != dev or t.dtype is not dtype:
+        raise ValueError(f"{name} must be a {dtype} tensor on cuda:{dev} (no CPU path)")
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != tokens or shape[1] < width:
+        raise ValueError(f"{name} must be [{tokens}, at least {width}], got {tuple(shape)}")
+    s0, s1 = t.stride()
+    if s1 != 1 and shape[1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    if like is not None:
-        if t.device != like.device or t.dtype != like.dtype:
-            raise ValueError(f"{name} must match the device {like.device} and dtype {like.dtype}")
-        if t.shape[0] != like.shape[0]:
-            raise ValueError(f"{name} has {t.shape[0]} rows, expected {like.shape[0]}")
-    return max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+    return s0 if tokens > 1 else max(s0, shape[1])
 
 
-def _vector(t, name, size, like, dtype=None):
-    """Checks a contiguous [size] tensor on the device of ``like``."""
+def _vector(t, name, size, dtype, dev: int):
+    """Address of a contiguous [size] tensor (None for None)."""
     if t is None:
-        return
-    dtype = like.dtype if dtype is None else dtype
-    if t.device != like.device or t.dtype != dtype or t.dim() != 1 or t.shape[0] != size or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous [{size}] tensor of {dtype} on {like.device}")
+        return None
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != (size,) or (size > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous [{size}] tensor of {dtype} on cuda:{dev}")
+    return t.data_ptr()
 
 
-def _rope_arg(positions, inv_freq, sections, interleaved, tokens, head_dim, like) -> N.Rope:
-    pairs = inv_freq.shape[0] if inv_freq.dim() == 1 else -1
-    _vector(inv_freq, "inv_freq", pairs, like, torch.float32)
+_pack_rope = struct.Struct("=QQqiiiiiiii").pack
+_no_sections = (0, 0, 0)
+
+
+def _rope_arg(positions, inv_freq, sections, interleaved, tokens, head_dim, dev: int) -> N.Rope:
+    pairs = inv_freq.numel()
+    freq = _vector(inv_freq, "inv_freq", pairs, torch.float32, dev)
     if not 1 <= pairs <= head_dim // 2:
         raise ValueError(f"inv_freq must hold 1..{head_dim // 2} frequencies, one for each rotated pair")
-    sections = (pairs,) if sections is None else sections
-    axes = len(sections)
-    if not 1 <= axes <= 4 or min(sections) < 0 or sum(sections) != pairs:
-        raise ValueError(f"sections must be 1..4 counts that add up to {pairs}")
-    r = N.Rope()
-    if positions is not None:
-        if positions.device != like.device or positions.dtype not in (torch.int32, torch.int64):
-            raise ValueError(f"positions must be an int32 or int64 tensor on {like.device}")
-        p = positions[None] if positions.dim() == 1 else positions
-        if tuple(p.shape) != (axes, tokens) or (tokens > 1 and p.stride(1) != 1):
-            raise ValueError(f"positions must be [{axes}, {tokens}] with a contiguous last dimension, "
-                             f"got {tuple(positions.shape)}")
-        r.positions = p.data_ptr()
-        r.position_stride = p.stride(0) if tokens > 1 else max(p.stride(0), tokens)
-        r.position_bytes = p.element_size()
+    if sections is None:
+        axes, four = 1, (pairs, 0, 0, 0)
     else:
-        r.position_bytes = 4
-    r.inv_freq = inv_freq.data_ptr()
-    r.axes = axes
-    r.rot_dim = 2 * pairs
-    r.interleaved = 1 if interleaved else 0
-    r.section[:axes] = sections
-    return r
+        axes = len(sections)
+        if not 1 <= axes <= 4 or min(sections) < 0 or sum(sections) != pairs:
+            raise ValueError(f"sections must be 1..4 counts that add up to {pairs}")
+        four = (*sections, *_no_sections)[:4]
+    at = stride = 0
+    size = 4
+    if positions is not None:
+        shape, strides = positions.shape, positions.stride()
+        kind = positions.dtype
+        if positions.get_device() != dev or (kind is not torch.int64 and kind is not torch.int32):
+            raise ValueError(f"positions must be an int32 or int64 tensor on cuda:{dev}")
+        if shape != ((axes, tokens) if len(shape) == 2 else (tokens,)) or (tokens > 1 and strides[-1] != 1) or (
+                axes > 1 and len(shape) != 2):
+            raise ValueError(f"positions must be [{axes}, {tokens}] with a contiguous last dimension, "
+                             f"got {tuple(shape)}")
+        at = positions.data_ptr()
+        size = 8 if kind is torch.int64 else 4
+        if axes > 1:
+            stride = strides[0] if tokens > 1 else max(strides[0], tokens)
+    return N.Rope.from_buffer_copy(_pack_rope(at, freq, stride, size, axes, 2 * pairs, 1 if interleaved else 0, *four))
 
 
 def qk_norm_rope(qkv: torch.Tensor, q_heads: int, k_heads: int, head_dim: int, positions: torch.Tensor,
@@ -268,18 +288,19 @@ def qk_norm_rope(qkv: torch.Tensor, q_heads: int, k_heads: int, head_dim: int, p
     q_heads + k_heads heads are written (``out=qkv`` works in place), or to a
     new [tokens, (q_heads + k_heads) * head_dim] tensor.
     """
-    code = dtype_code(qkv.dtype)
+    t = qkv.dtype
+    code = dtype_code(t)
+    dev = _device_of(qkv, "qkv")
     width = (q_heads + k_heads) * head_dim
-    xs = _head_rows(qkv, "qkv", width)
     tokens = qkv.shape[0]
-    _vector(q_w, "q_w", head_dim, qkv)
-    _vector(k_w, "k_w", head_dim, qkv)
-    rope = _rope_arg(positions, inv_freq, sections, interleaved, tokens, head_dim, qkv)
+    xs = _head_rows(qkv, "qkv", width, tokens, t, dev)
+    qw, kw = _vector(q_w, "q_w", head_dim, t, dev), _vector(k_w, "k_w", head_dim, t, dev)
+    rope = _rope_arg(positions, inv_freq, sections, interleaved, tokens, head_dim, dev)
     if out is None:
-        out = _empty((tokens, width), qkv.dtype, qkv.device, stream)
-    ys = _head_rows(out, "out", width, qkv)
-    _launch(qkv.device, stream, N.rmsnorm_qk_rope_fwd, _ptr(qkv), _ptr(out), tokens, xs, ys, q_heads, k_heads, head_dim,
-            _ptr(q_w), _ptr(k_w), weight_bias, eps, int(norm), rope, code)
+        out = _empty((tokens, width), t, qkv.device, stream)
+    ys = _head_rows(out, "out", width, tokens, t, dev)
+    _launch(dev, stream, N.rmsnorm_qk_rope_fwd, qkv.data_ptr(), out.data_ptr(), tokens, xs, ys, q_heads, k_heads,
+            head_dim, qw, kw, weight_bias, eps, 1 if norm else 0, rope, code)
     return out
 
 
@@ -298,30 +319,42 @@ def qk_norm_rope_backward(dout: torch.Tensor, qkv: Optional[torch.Tensor], q_hea
     tensor of ``rmsnorm_qk_rope_bwd_workspace_bytes(head_dim)`` bytes
     (allocated when not given).
     """
-    code = dtype_code(dout.dtype)
+    t = dout.dtype
+    code = dtype_code(t)
+    dev = _device_of(dout, "dout")
     width = (q_heads + k_heads) * head_dim
-    gs = _head_rows(dout, "dout", width)
     tokens = dout.shape[0]
+    gs = _head_rows(dout, "dout", width, tokens, t, dev)
     if qkv is None and norm:
         raise ValueError("the norm's gradient needs qkv")
-    xs = _head_rows(qkv, "qkv", width, dout) if qkv is not None else max(width, 1)
-    _vector(q_w, "q_w", head_dim, dout)
-    _vector(k_w, "k_w", head_dim, dout)
-    rope = _rope_arg(positions, inv_freq, sections, interleaved, tokens, head_dim, dout)
+    xs = _head_rows(qkv, "qkv", width, tokens, t, dev) if qkv is not None else width
+    qw, kw = _vector(q_w, "q_w", head_dim, t, dev), _vector(k_w, "k_w", head_dim, t, dev)
+    rope = _rope_arg(positions, inv_freq, sections, interleaved, tokens, head_dim, dev)
     if out is None:
-        out = _empty((tokens, width), dout.dtype, dout.device, stream)
-    ds = _head_rows(out, "out", width, dout)
-    dq_w = dk_w = None
-    need = 0
-    if q_w is not None and k_w is not None:
-        both = _empty((2, head_dim), dout.dtype, dout.device, stream)
-        dq_w, dk_w = both[0], both[1]
-        need = N.rmsnorm_qk_rope_bwd_workspace_bytes(head_dim)
+        out = _empty((tokens, width), t, dout.device, stream)
+    ds = _head_rows(out, "out", width, tokens, t, dev)
+    dq_w = dk_w = dq = dk = None
+    ws = need = 0
+    if qw is not None and kw is not None:
+        dq_w, dk_w = _empty((2, head_dim), t, dout.device, stream).unbind(0)
+        dq, dk = dq_w.data_ptr(), dk_w.data_ptr()
+        need = _rope_workspace_bytes(head_dim)
         workspace = _workspace(workspace, need, dout.device, stream)
-    _launch(dout.device, stream, N.rmsnorm_qk_rope_bwd, _ptr(dout), _ptr(qkv), _ptr(out), tokens, gs, xs, ds, q_heads,
-            k_heads, head_dim, _ptr(q_w), _ptr(k_w), _ptr(dq_w), _ptr(dk_w), weight_bias, eps, int(norm), rope, code,
-            _ptr(workspace) if need else None, need)
+        ws = workspace.data_ptr()
+    _launch(dev, stream, N.rmsnorm_qk_rope_bwd, dout.data_ptr(), _ptr(qkv), out.data_ptr(), tokens, gs, xs, ds, q_heads,
+            k_heads, head_dim, qw, kw, dq, dk, weight_bias, eps, 1 if norm else 0, rope, code, ws, need)
     return out, dq_w, dk_w
+
+
+@functools.lru_cache(maxsize=64)
+def _rope_workspace_bytes(head_dim: int) -> int:
+    return N.rmsnorm_qk_rope_bwd_workspace_bytes(head_dim)
+
+
+@functools.lru_cache(maxsize=256)
+def _bwd_workspace_bytes(rows: int, hidden: int, code: int, dev: int) -> int:
+    with torch.cuda.device(dev):
+        return N.rmsnorm_bwd_workspace_bytes(rows, hidden, code)
 
 
 def _workspace(workspace, need, device, stream):
@@ -333,6 +366,7 @@ def _workspace(workspace, need, device, stream):
     return workspace
 
 
+_pack_kv = struct.Struct("=QQQQQQqqqqiiiiiff4x").pack
 _CACHE_CODES = {torch.bfloat16: N.RMSNORM_BF16, torch.float32: N.RMSNORM_F32, torch.float8_e4m3fn: N.RMSNORM_E4M3}
 
 
@@ -359,68 +393,76 @@ def qkv_append(qkv: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     sequence are left alone; rows without a page are not written and counted
     in ``dropped`` (int32, [1], added to) where given.
     """
-    code = dtype_code(qkv.dtype)
-    xs = _head_rows(qkv, "qkv", (q_heads + 2 * kv_heads) * head_dim)
+    t = qkv.dtype
+    code = dtype_code(t)
+    dev = _device_of(qkv, "qkv")
     tokens = qkv.shape[0]
-    _vector(q_w, "q_w", head_dim, qkv)
-    _vector(k_w, "k_w", head_dim, qkv)
-    rope = _rope_arg(positions, inv_freq, sections, interleaved, tokens, head_dim, qkv)
-    shape, strides = k_cache.shape, k_cache.stride()
+    xs = _head_rows(qkv, "qkv", (q_heads + 2 * kv_heads) * head_dim, tokens, t, dev)
+    qw, kw = _vector(q_w, "q_w", head_dim, t, dev), _vector(k_w, "k_w", head_dim, t, dev)
+    rope = _rope_arg(positions, inv_freq, sections, interleaved, tokens, head_dim, dev)
+    shape, strides, kind = k_cache.shape, k_cache.stride(), k_cache.dtype
     if len(shape) != 4 or shape[2] != kv_heads or shape[3] != head_dim or strides[3] != 1:
         raise ValueError(f"k_cache must be [num_pages, page_size, {kv_heads}, {head_dim}] with a contiguous last "
                          f"dimension, got {tuple(shape)}")
-    if v_cache.shape != shape or v_cache.stride() != strides or v_cache.dtype != k_cache.dtype:
+    if v_cache.shape != shape or v_cache.stride() != strides or v_cache.dtype is not kind:
         raise ValueError("v_cache must have the shape, strides and dtype of k_cache")
-    if k_cache.device != qkv.device or v_cache.device != qkv.device:
-        raise ValueError(f"the caches must be on {qkv.device}")
-    if k_cache.dtype not in (qkv.dtype, torch.float8_e4m3fn):
-        raise TypeError(f"caches of {k_cache.dtype}: {qkv.dtype} or float8_e4m3fn only")
-    if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.device != qkv.device or \
-            (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        raise ValueError(f"page_table must be a 2-D int32 tensor on {qkv.device} with a contiguous last dimension")
+    if k_cache.get_device() != dev or v_cache.get_device() != dev:
+        raise ValueError(f"the caches must be on cuda:{dev}")
+    if kind is not t and kind is not torch.float8_e4m3fn:
+        raise TypeError(f"caches of {kind}: {t} or float8_e4m3fn only")
+    if page_table.dim() != 2 or page_table.dtype is not torch.int32 or page_table.get_device() != dev:
+        raise ValueError(f"page_table must be a 2-D int32 tensor on cuda:{dev}")
     seqs, max_pages = page_table.shape
-    _vector(cu_tokens, "cu_tokens", seqs + 1, qkv, torch.int32)
-    _vector(cache_lens, "cache_lens", seqs, qkv, torch.int32)
-    _vector(dropped, "dropped", 1, qkv, torch.int32)
+    p0, p1 = page_table.stride()
+    if p1 != 1 and max_pages > 1:
+        raise ValueError("page_table: the last dimension must be contiguous")
+    cu = _vector(cu_tokens, "cu_tokens", seqs + 1, torch.int32, dev)
+    lens = _vector(cache_lens, "cache_lens", seqs, torch.int32, dev)
+    drop = _vector(dropped, "dropped", 1, torch.int32, dev) or 0
     qs = 0
+    q_at = None
     if q_heads > 0:
         if q_out is None:
-            q_out = _empty((tokens, q_heads * head_dim), qkv.dtype, qkv.device, stream)
-        qs = _head_rows(q_out, "q_out", q_heads * head_dim, qkv)
-    kv = N.PagedKV(
-        k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), cu_tokens.data_ptr(), cache_lens.data_ptr(),
-        _ptr(dropped), max(page_table.stride(0), max_pages) if seqs <= 1 else page_table.stride(0),
-        strides[0] if shape[0] > 1 else 0, strides[1] if shape[1] > 1 else 0, strides[2] if shape[2] > 1 else 0,
-        seqs, max_pages, shape[0], shape[1], _CACHE_CODES[k_cache.dtype], k_scale, v_scale)
-    _launch(qkv.device, stream, N.rmsnorm_qkv_append, _ptr(qkv), _ptr(q_out) if q_heads > 0 else None, tokens, xs, qs,
-            q_heads, kv_heads, head_dim, _ptr(q_w), _ptr(k_w), weight_bias, eps, int(norm), rope, kv, code)
+            q_out = _empty((tokens, q_heads * head_dim), t, qkv.device, stream)
+        qs = _head_rows(q_out, "q_out", q_heads * head_dim, tokens, t, dev)
+        q_at = q_out.data_ptr()
+    # strides of dimensions of one place are never used: 0 keeps them from
+    # narrowing the accesses
+    kv = N.PagedKV.from_buffer_copy(_pack_kv(
+        k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), cu, lens, drop,
+        p0 if seqs > 1 else max(p0, max_pages), strides[0] if shape[0] > 1 else 0, strides[1] if shape[1] > 1 else 0,
+        strides[2] if shape[2] > 1 else 0, seqs, max_pages, shape[0], shape[1], _CACHE_CODES[kind], k_scale, v_scale))
+    _launch(dev, stream, N.rmsnorm_qkv_append, qkv.data_ptr(), q_at, tokens, xs, qs, q_heads, kv_heads, head_dim, qw,
+            kw, weight_bias, eps, 1 if norm else 0, rope, kv, code)
     return q_out
 
 
 def _rows_of(t: torch.Tensor, name: str):
-    """(rows, hidden) of a contiguous CUDA tensor."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
-    if t.dim() < 1 or t.shape[-1] < 1:
+    """(device number, rows, hidden) of a contiguous CUDA tensor."""
+    dev = _device_of(t, name)
+    shape = t.shape
+    if not shape or shape[-1] < 1:
         raise ValueError(f"{name} must have a last dimension of at least one element")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t.numel() // t.shape[-1], t.shape[-1]
+    return dev, t.numel() // shape[-1], shape[-1]
 
 
-def _like(t, name, x):
-    if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {tuple(x.shape)} tensor of {x.dtype} on {x.device}")
+def _like(t, name, x, dev: int) -> int:
+    """Address of a contiguous tensor of the shape and type of ``x``."""
+    if t.get_device() != dev or t.dtype is not x.dtype or t.shape != x.shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {tuple(x.shape)} tensor of {x.dtype} on cuda:{dev}")
+    return t.data_ptr()
 
 
-def _rng_arg(rng, p, like):
+def _rng_arg(rng, p, dev: int):
     if rng is None:
         if p:
             raise ValueError("dropout needs rng, an int64 tensor of seed and offset")
         return None
-    if rng.device != like.device or rng.dtype not in (torch.int64, torch.uint64) or rng.numel() != 2 or \
-            not rng.is_contiguous():
-        raise ValueError(f"rng must be a contiguous int64 tensor of seed and offset on {like.device}")
+    if rng.get_device() != dev or rng.dtype not in (torch.int64, torch.uint64) or rng.shape != (2,) or \
+            rng.stride(0) != 1:
+        raise ValueError(f"rng must be a contiguous [2] int64 tensor of seed and offset on cuda:{dev}")
     return rng.data_ptr()
 
 
@@ -438,35 +480,32 @@ def rms_norm_dropout(x: torch.Tensor, residual: torch.Tensor, p: float, rng: Opt
     makes.
     """
     code = dtype_code(x.dtype)
-    rows, hidden = _rows_of(x, "x")
-    _like(residual, "residual", x)
-    _vector(w, "w", hidden, x)
-    r = _rng_arg(rng, p, x)
+    dev, rows, hidden = _rows_of(x, "x")
+    res = _like(residual, "residual", x, dev)
+    wp = _vector(w, "w", hidden, x.dtype, dev)
+    r = _rng_arg(rng, p, dev)
     if out is None:
         out = _empty(x.shape, x.dtype, x.device, stream)
-    else:
-        _like(out, "out", x)
     if residual_out is None:
         residual_out = _empty(x.shape, x.dtype, x.device, stream)
-    else:
-        _like(residual_out, "residual_out", x)
-    _launch(x.device, stream, N.rmsnorm_dropout_fwd, _ptr(x), _ptr(residual), _ptr(w), _ptr(out), _ptr(residual_out),
-            rows, hidden, eps, weight_bias, p, r, code)
+    _launch(dev, stream, N.rmsnorm_dropout_fwd, x.data_ptr(), res, wp, _like(out, "out", x, dev),
+            _like(residual_out, "residual_out", x, dev), rows, hidden, eps, weight_bias, p, r, code)
     return out, residual_out
 
 
 def _backward_args(dy, h, w, dresidual_out, workspace, stream):
-    rows, hidden = _rows_of(dy, "dy")
-    _like(h, "h", dy)
-    if dresidual_out is not None:
-        _like(dresidual_out, "dresidual_out", dy)
-    _vector(w, "w", hidden, dy)
+    t = dy.dtype
+    code = dtype_code(t)
+    dev, rows, hidden = _rows_of(dy, "dy")
+    at = (dy.data_ptr(), _like(h, "h", dy, dev), _vector(w, "w", hidden, t, dev),
+          None if dresidual_out is None else _like(dresidual_out, "dresidual_out", dy, dev))
     if w is None:
-        return rows, hidden, None, None, 0
-    dw = _empty((hidden,), dy.dtype, dy.device, stream)
-    with torch.cuda.device(dy.device):
-        need = N.rmsnorm_bwd_workspace_bytes(rows, hidden, dtype_code(dy.dtype))
-    return rows, hidden, dw, _workspace(workspace, need, dy.device, stream), need
+        return dev, code, rows, hidden, at, None, None, 0, None
+    dw = _empty((hidden,), t, dy.device, stream)
+    need = _bwd_workspace_bytes(rows, hidden, code, dev)
+    workspace = _workspace(workspace, need, dy.device, stream)
+    # the workspace stays referenced until the call is made
+    return dev, code, rows, hidden, at, dw, workspace.data_ptr(), need, workspace
 
 
 def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, w: Optional[torch.Tensor] = None,
@@ -481,14 +520,11 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, w: Optional[torch.Tenso
     ``rmsnorm_bwd_workspace_bytes(rows, hidden, dtype)`` bytes (allocated when
     not given).
     """
-    code = dtype_code(dy.dtype)
-    rows, hidden, dw, workspace, need = _backward_args(dy, h, w, dresidual_out, workspace, stream)
+    dev, code, rows, hidden, at, dw, ws, need, keep = _backward_args(dy, h, w, dresidual_out, workspace, stream)
     if out is None:
         out = _empty(dy.shape, dy.dtype, dy.device, stream)
-    else:
-        _like(out, "out", dy)
-    _launch(dy.device, stream, N.rmsnorm_bwd, _ptr(dy), _ptr(h), _ptr(w), _ptr(dresidual_out), _ptr(out), _ptr(dw),
-            rows, hidden, eps, weight_bias, code, _ptr(workspace), need)
+    _launch(dev, stream, N.rmsnorm_bwd, *at, _like(out, "out", dy, dev), None if dw is None else dw.data_ptr(), rows,
+            hidden, eps, weight_bias, code, ws, need)
     return out, dw
 
 
@@ -500,19 +536,14 @@ def rms_norm_dropout_backward(dy: torch.Tensor, h: torch.Tensor, p: float, rng: 
     """Gradient of ``rms_norm_dropout`` (``h``: its residual_out, with the same
     ``p`` and ``rng``): returns (dresidual, dx, dw), dw None without a weight.
     Other arguments as ``rms_norm_backward``."""
-    code = dtype_code(dy.dtype)
-    rows, hidden, dw, workspace, need = _backward_args(dy, h, w, dresidual_out, workspace, stream)
-    r = _rng_arg(rng, p, dy)
+    dev, code, rows, hidden, at, dw, ws, need, keep = _backward_args(dy, h, w, dresidual_out, workspace, stream)
+    r = _rng_arg(rng, p, dev)
     if dresidual is None:
         dresidual = _empty(dy.shape, dy.dtype, dy.device, stream)
-    else:
-        _like(dresidual, "dresidual", dy)
     if dx is None:
         dx = _empty(dy.shape, dy.dtype, dy.device, stream)
-    else:
-        _like(dx, "dx", dy)
-    _launch(dy.device, stream, N.rmsnorm_dropout_bwd, _ptr(dy), _ptr(h), _ptr(w), _ptr(dresidual_out), _ptr(dresidual),
-            _ptr(dx), _ptr(dw), rows, hidden, eps, weight_bias, p, r, code, _ptr(workspace), need)
+    _launch(dev, stream, N.rmsnorm_dropout_bwd, *at, _like(dresidual, "dresidual", dy, dev), _like(dx, "dx", dy, dev),
+            None if dw is None else dw.data_ptr(), rows, hidden, eps, weight_bias, p, r, code, ws, need)
     return dresidual, dx, dw
 
 

@@ -50,7 +50,7 @@ int make_rope(int64_t tokens, int64_t x_stride, int32_t q_heads, int32_t k_heads
     if (norm == 0 && q_w != nullptr) return RMSNORM_EINVAL;
     if (q_heads < 0 || k_heads < 0 || (int64_t)q_heads + k_heads < 1) return RMSNORM_EINVAL;
     const int64_t heads = (int64_t)q_heads + k_heads + v_heads;
-    if (heads > (1 << 20)) return RMSNORM_EUNSUPPORTED;
+    if (heads * head_dim > (1 << 28)) return RMSNORM_EUNSUPPORTED;   // a token row within 31 bits
     if (head_dim > rrn::kRopeMaxDim) return RMSNORM_EUNSUPPORTED;
     const int64_t s = rrn::size_of(dtype);
     if (x_stride < heads * head_dim || (tokens > 0 && tokens > INT64_MAX / 8 / x_stride / s)) return RMSNORM_EINVAL;
@@ -91,8 +91,9 @@ bool stride_ok(int64_t stride, int64_t width, int64_t tokens, int64_t s) {
 
 // The widest shape that the head's halves, and every address and stride of
 // the call (all multiples of `unit` elements), allow; a head is held by as
-// many lanes as it has units, up to a power of two, so that neighbouring
-// lanes read neighbouring pieces.
+// many lanes as it has units (32 at most), so that neighbouring lanes read
+// neighbouring pieces and few lanes idle: fp32 heads of 80 (10 units, three
+// heads a warp) 4099 tokens x 32 heads XXX us, 19.8 with 16 lanes a head.
 int pick_shape(int dtype, int64_t unit, rrn::RopeParams *p) {
     const rrn::RopeShape *table = dtype == RMSNORM_BF16 ? rrn::kRopeShapesBf16 : rrn::kRopeShapesF32;
     const int tail = p->head_dim / 2 - p->R;
@@ -101,8 +102,8 @@ int pick_shape(int dtype, int64_t unit, rrn::RopeParams *p) {
         if (p->R % ve != 0 || tail % ve != 0 || unit % ve != 0 || units > 32 * table[i].k) continue;
         p->units = units;
         p->rot_units = p->R / ve;
-        p->lanes = 1;
-        while (p->lanes < 32 && p->lanes < units) p->lanes *= 2;
+        p->lanes = units < 32 ? units : 32;
+        p->heads_a_warp = 32 / p->lanes;
         return i;
     }
     return -1;   // unreachable: the last shape takes any head
@@ -116,6 +117,12 @@ struct Unit {
     void step(int64_t elements) { bits |= (uint64_t)elements; }
     int64_t get() const { return (int64_t)(bits & (~bits + 1)); }
 };
+
+// Whether every byte of a tile's token rows is within 31 bits of its first.
+bool tile_reaches(int64_t a, int64_t b, int64_t c) {
+    const int64_t most = INT32_MAX / rrn::kRopeMaxWarps;
+    return a <= most && b <= most && c <= most;
+}
 
 const void *forward_kernel(int dtype, int shape, bool il, int mode) {
     return dtype == RMSNORM_BF16 ? rrn::rope_fwd_bf16(shape, il, mode) : rrn::rope_fwd_f32(shape, il, mode);
@@ -131,10 +138,9 @@ int launch_forward(rrn::RopeParams *p, int dtype, int64_t unit, bool il, int mod
     // A run of jobs for every resident block.  A job is a token's heads; with
     // fewer tokens than blocks it is a slice of them, one head iteration a
     // warp where that many blocks fit.
-    const int64_t iters = div_up((int64_t)p->q_heads + p->k_heads + p->v_heads, 32 / p->lanes);
-    const size_t smem = (size_t)rrn::rope_smem_floats(p->head_dim, p->R) * sizeof(float);
+    const int64_t iters = div_up((int64_t)p->q_heads + p->k_heads + p->v_heads, p->heads_a_warp);
+    const size_t smem = rrn::kRopeSmemBytes;
     int resident = 0;
-    if (smem > 48 * 1024 && (st = rrn::allow_smem(dev, fn)) != RMSNORM_OK) return st;
     if ((st = rrn::resident_blocks(dev, fn, 32 * rrn::kRopeMaxWarps, smem, &resident)) != RMSNORM_OK) return st;
     const int64_t most = (int64_t)sms * resident;
     int64_t slices = 1;
@@ -144,6 +150,7 @@ int launch_forward(rrn::RopeParams *p, int dtype, int64_t unit, bool il, int mod
     }
     p->iters = (int32_t)div_up(iters, slices);
     p->slices = (int32_t)div_up(iters, p->iters);
+    p->tile = p->slices > 1 || !tile_reaches(p->x_stride, p->y_stride, 0) ? 1 : rrn::kRopeMaxWarps;
     const int64_t jobs = p->tokens * p->slices;
     const int64_t blocks = jobs < most ? jobs : most;
     p->each = jobs / blocks;
@@ -218,7 +225,6 @@ int rmsnorm_qk_rope_bwd(const void *dy, const void *x, void *dx, int64_t tokens,
     p.partial = static_cast<float *>(dq_w != nullptr ? workspace : nullptr);
     int64_t blocks_q = 0, blocks_k = 0;
     if (tokens > 0) {
-        const size_t sum_bytes = (size_t)rrn::kRopeMaxWarps * head_dim * sizeof(float);
         Unit u;
         u.at(dy, s), u.at(dx, s), u.at(q_w, s), u.at(k_w, s);
         u.step(dy_token_stride), u.step(dx_token_stride);
@@ -230,14 +236,11 @@ int rmsnorm_qk_rope_bwd(const void *dy, const void *x, void *dx, int64_t tokens,
         const void *fn = dtype == RMSNORM_BF16 ? rrn::rope_bwd_bf16(shape, il, norm == 1)
                                                : rrn::rope_bwd_f32(shape, il, norm == 1);
         if (fn == nullptr) return RMSNORM_EINVAL;
-        const int hpw = 32 / p.lanes;
-        p.iters = (int32_t)div_up(q_heads, hpw);
-        p.iters_k = (int32_t)div_up(k_heads, hpw);
-        const size_t smem = (size_t)rrn::rope_smem_floats((int)head_dim, p.R) * sizeof(float) > sum_bytes
-                                ? (size_t)rrn::rope_smem_floats((int)head_dim, p.R) * sizeof(float)
-                                : sum_bytes;
+        p.iters = (int32_t)div_up(q_heads, p.heads_a_warp);
+        p.iters_k = (int32_t)div_up(k_heads, p.heads_a_warp);
+        p.tile = tile_reaches(p.dy_stride, p.y_stride, norm == 1 ? p.x_stride : 0) ? rrn::kRopeMaxWarps : 1;
+        const size_t smem = rrn::kRopeSmemBytes;
         int resident = 0;
-        if (smem > 48 * 1024 && (st = rrn::allow_smem(dev, fn)) != RMSNORM_OK) return st;
         if ((st = rrn::resident_blocks(dev, fn, 32 * rrn::kRopeMaxWarps, smem, &resident)) != RMSNORM_OK) return st;
         int64_t most = (int64_t)sms * resident;
         if (most > kBwdMaxBlocks) most = kBwdMaxBlocks;

@@ -12,8 +12,8 @@
 //
 // Work layout.  A lane owns K "units" of a head: unit u is VE pairs, held as
 // two pieces of VE elements, so both halves of every pair sit in one lane and
-// the rotation needs no exchange.  G lanes share a head, 32 / G heads run
-// side by side in a warp (a head iteration).  A block takes an equal run of
+// the rotation needs no exchange.  G lanes share a head (as many as it has
+// units), 32 / G heads run side by side in a warp (a head iteration).  A block takes an equal run of
 // tokens in tiles of one token a warp: each warp makes its token's table of
 // cosines and sines in shared memory, then the tile's head iterations go
 // round the warps.  Every factor of a head (cosine, sine, weights) is read
@@ -31,20 +31,17 @@
 
 #include "rmsnorm_kernels.cuh"
 
-#ifndef ROPE_FR
-#define ROPE_FR 4
-#endif
-#ifndef ROPE_BR
-#define ROPE_BR 2
-#endif
 namespace rrn {
 
 constexpr int kRopeMaxDim = 512;      // head_dim
 constexpr int kRopeMaxAxes = 4;
 constexpr int kRopeMaxWarps = 8;      // warps a block
-// Blocks a SM that a shape's registers are budgeted for.
-__host__ __device__ constexpr int rope_resident(int ve, int k) { return ve * k <= 8 ? ROPE_FR : 2; }
-__host__ __device__ constexpr int rope_bwd_resident(int ve, int k) { return ve * k <= 8 ? ROPE_BR : 1; }
+// Blocks a SM that a shape's registers are budgeted for.  Measured on GB300,
+// bf16 8192 tokens x 40 heads of 128: the forward 31.0 us with four blocks
+// (64 registers a thread), 32.5 with three, 38.7 with five (which spill); the
+// gradient 63.5 us with two, 75.5 with three.
+__host__ __device__ constexpr int rope_resident(int ve, int k) { return ve * k <= 8 && ve > 1 ? 4 : 2; }
+__host__ __device__ constexpr int rope_bwd_resident(int ve, int k) { return ve * k <= 8 && ve > 1 ? 2 : 1; }
 
 struct RopeParams {
     const void *x;            // packed token rows (query, key, [value] heads)
@@ -66,9 +63,10 @@ struct RopeParams {
     const float *inv_freq;    // [R]
     int32_t R;
     int32_t units, rot_units; // pair units of a head, and the rotated ones among them
-    int32_t lanes;            // G: lanes a head, a power of two
+    int32_t lanes;            // G: lanes a head
+    int32_t heads_a_warp;     // 32 / G, of one head iteration
     int32_t iters, iters_k;   // head iterations a job (gradient: a token's query heads, its key heads)
-    int32_t slices;           // forward: jobs a token
+    int32_t slices, tile;     // forward: jobs a token; jobs a tile (1 or kRopeMaxWarps)
     int32_t q_blocks;         // gradient: blocks of the query heads
     int64_t each, extra, each_k, extra_k;   // a block's run of jobs: each, one more for the first `extra`
     // paged cache (append)
@@ -202,12 +200,15 @@ __device__ __forceinline__ constexpr int second_of(int j) { return IL ? 2 * j + 
 // Pairs read from a table of factors at a time.
 __host__ __device__ constexpr int pairs_at_once(int ve) { return ve < 4 ? ve : 4; }
 
-// Where pair j of unit u stands in a table of `units` units: the lanes of a
-// head read consecutive 16 (8, 4) bytes.
+// Where pair j of unit u stands in a table of factors: the lanes of a head
+// read consecutive 16 (8, 4) bytes, and every table has kRopeTable places
+// whatever the head's size (VE * K * 32 lanes at most), so that one address
+// serves all of a unit's reads.
+constexpr int kRopeTable = 256;
 template <int VE>
-__device__ __forceinline__ int table_at(int units, int u, int j) {
+__device__ __forceinline__ constexpr int table_at(int u, int j) {
     constexpr int N = pairs_at_once(VE);
-    return ((j / N) * units + u) * N + j % N;
+    return (j / N) * 32 * N + u * N + j % N;
 }
 
 template <int N>
@@ -334,12 +335,10 @@ __device__ __forceinline__ int axis_of(const RopeParams &p, int i) {
     return (i >= p.cut[0]) + (i >= p.cut[1]) + (i >= p.cut[2]);
 }
 
-// Shared memory of a block, in floats: the weights of the pairs' first and
-// second elements [2 kinds][2][D / 2], then two tiles of cosines and sines
-// [2][kRopeMaxWarps][2][R], all in table order.
-__host__ __device__ constexpr int rope_smem_floats(int head_dim, int R) {
-    return 2 * head_dim + 2 * kRopeMaxWarps * 2 * R;
-}
+// Shared memory of a block: the pairs' turn fractions (64 bits each), the
+// weights of the pairs' first and second elements (a table each for query and
+// key), then two tiles of a table of cosines and one of sines a token.
+constexpr int kRopeSmemBytes = 8 * kRopeTable + 4 * (4 * kRopeTable + 2 * kRopeMaxWarps * 2 * kRopeTable);
 
 // A token's position on axis `lane` (lanes past the axes: the last one).
 __device__ __forceinline__ int64_t lane_position(const RopeParams &p, int lane, int64_t token) {
@@ -347,28 +346,30 @@ __device__ __forceinline__ int64_t lane_position(const RopeParams &p, int lane, 
     return p.pos64 ? static_cast<const int64_t *>(p.pos)[at] : (int64_t)static_cast<const int32_t *>(p.pos)[at];
 }
 
-// A token's cosines and sines (cs[0 .. R), cs[R .. 2R)) by one warp, pair i
+// A token's tables of cosines and sines by one warp, pair i
 // by lane i % 32, from the position that lane a holds for axis a.
 template <int VE>
-__device__ __forceinline__ void make_angles(const RopeParams &p, float *cs, int lane, int64_t pos) {
-    constexpr int N = pairs_at_once(VE);
+__device__ __forceinline__ void make_angles(const RopeParams &p, const uint64_t *frac, float *cs, int lane, int64_t pos) {
     for (int i = lane; i - lane < p.R; i += 32) {
         int64_t at = pos;
         if (p.axes > 1) at = __shfl_sync(0xffffffffu, pos, axis_of(p, i));
         if (i < p.R) {
             float s, c;
-            sincos_turns((uint64_t)at * turn_fraction(p.inv_freq[i]), s, c);
-            // unit i / VE, pair i % VE of it
-            const int k = table_at<VE>(p.rot_units, i / VE, i % VE);
+            sincos_turns((uint64_t)at * frac[i], s, c);
+            const int k = table_at<VE>(i / VE, i % VE);   // pair i % VE of unit i / VE
             cs[k] = c;
-            cs[p.R + k] = s;
+            cs[kRopeTable + k] = s;
         }
     }
-    (void)N;
 }
 
-// Both kinds' head weights (w + bias; 1 without a weight) into the tables, by
-// the whole block.
+// The turn fractions, and both kinds' head weights (w + bias; 1 without a
+// weight), by the whole block.
+template <int VE>
+__device__ __forceinline__ void make_fractions(const RopeParams &p, uint64_t *frac) {
+    for (int i = threadIdx.x; i < p.R; i += blockDim.x) frac[i] = turn_fraction(p.inv_freq[i]);
+}
+
 template <typename T, int VE, bool IL>
 __device__ __forceinline__ void make_weights(const RopeParams &p, float *wsm) {
     const int D = p.head_dim;
@@ -390,7 +391,7 @@ __device__ __forceinline__ void make_weights(const RopeParams &p, float *wsm) {
         }
         float v = 1.f;
         if (w != nullptr) v = widen_bits(ld_bits(w, e, T{}, 2), T{}) + p.w_bias;
-        wsm[(kind * 2 + second) * (D / 2) + table_at<VE>(p.units, pair / VE, pair % VE)] = v;
+        wsm[(kind * 2 + second) * kRopeTable + table_at<VE>(pair / VE, pair % VE)] = v;
     }
 }
 
@@ -435,10 +436,10 @@ template <int VE, int K, bool IL, int S>
 struct Lane {
     int oa[K], ob[K], unit[K];
     bool act[K];
-    __device__ __forceinline__ void set(const RopeParams &p, int t) {
+    __device__ __forceinline__ void set(const RopeParams &p, int t, int group) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            act[k] = t + k * p.lanes < p.units;
+            act[k] = t + k * p.lanes < p.units && group < p.heads_a_warp;
             unit[k] = act[k] ? t + k * p.lanes : 0;
             unit_offsets<VE, IL>(p, unit[k], oa[k], ob[k]);
             oa[k] *= S;
@@ -470,21 +471,52 @@ __device__ __forceinline__ void widen_unit(const typename Piece<T, VE>::Raw &a, 
     }
 }
 
-// Keeps the compiler from holding the widened values of a raw piece across
-// this point: they are widened again where they are needed.
-template <typename Raw>
-__device__ __forceinline__ void forget(Raw &r) {
+// Sums over the g lanes of a head, of M values, for all of them.  t: the
+// lane's place in its head.
+template <int M>
+__device__ __forceinline__ void lanes_sum(float (&v)[M], int g, int t, int lane) {
+    auto add = [&](int off) {
 #pragma unroll
-    for (int i = 0; i < (int)(sizeof(r.u) / 4); ++i) asm volatile("" : "+r"(r.u[i]));
+        for (int i = 0; i < M; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
+    };
+    if ((g & (g - 1)) == 0) {
+        if (g >= 8) {   // the usual head sizes: one or two branches
+            add(1);
+            add(2);
+            add(4);
+            if (g > 8) {
+                add(8);
+                if (g > 16) add(16);
+            }
+        } else if (g > 1) {
+            add(1);
+            if (g > 2) add(2);
+        }
+    } else {   // heads of 40, 80, 96 ...: towards the head's first lane and back
+        for (int off = 1; off < g; off <<= 1) {
+#pragma unroll
+            for (int i = 0; i < M; ++i) {
+                const float o = __shfl_down_sync(0xffffffffu, v[i], off);
+                v[i] += t + off < g ? o : 0.f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < M; ++i) v[i] = __shfl_sync(0xffffffffu, v[i], lane - t);
+    }
 }
 
-// Sum over the G lanes of a head (G a power of two, run-time), of one or two values.
-__device__ __forceinline__ float lanes_sum(float v, int g) {
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1)
-        if (g > off) v += __shfl_xor_sync(0xffffffffu, v, off);
-    return v;
-}
+// A block's place in its run: tiles of p.tile jobs (one where a token's heads
+// are cut in slices, or where token rows lie so far apart that a tile's would
+// not be reached with 32 bits), and the warp's head iterations of a tile.
+struct Tile {
+    int j, i;   // job of the tile, head iteration of the job
+    __device__ __forceinline__ void settle(int jobs, int iters) {
+        while (i >= iters && j < jobs) {
+            i -= iters;
+            ++j;
+        }
+    }
+};
 
 // ----------------------------------------------------------------- forward
 template <typename T, int VE, int K, bool IL, int MODE>
@@ -494,16 +526,18 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(VE, K)) rope
     constexpr int S = (int)sizeof(typename T::storage);
     constexpr int N = pairs_at_once(VE);
     constexpr bool APPEND = MODE != kRopePlain;
-    extern __shared__ __align__(16) float wsm[];
+    extern __shared__ __align__(16) unsigned char smem[];
     __shared__ int64_t rows[2][kRopeMaxWarps];   // append: where the tile's tokens go, -1: nowhere
+    uint64_t *frac = reinterpret_cast<uint64_t *>(smem);
+    float *wsm = reinterpret_cast<float *>(smem + 8 * kRopeTable);
+    float *tiles = wsm + 4 * kRopeTable;
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int G = p.lanes, t = lane & (G - 1), group = lane / G, hpw = 32 / G;
-    float *tiles = wsm + 2 * p.head_dim;
+    const int G = p.lanes, group = lane / G, t = lane - group * G, hpw = p.heads_a_warp;
     const int heads = p.q_heads + p.k_heads + p.v_heads, turned = p.q_heads + p.k_heads;
-    const int head_bytes = p.head_dim * S;
+    const uint32_t head_bytes = (uint32_t)(p.head_dim * S);
     Lane<VE, K, IL, S> my;
-    my.set(p, t);
+    my.set(p, t, group);
     Jobs jobs;
     jobs.set(blockIdx.x, p.each, p.extra);
 
@@ -515,40 +549,37 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(VE, K)) rope
         if (jobs.last > most) jobs.last = most;
     }
 
-    // job j of a tile, its iteration i: token and first head iteration
-    auto load = [&](int64_t token, int it, Raw (&ra)[K], Raw (&rb)[K]) {
-        int h = it * hpw + group;
-        h = h < heads ? h : heads - 1;
-        const char *src = static_cast<const char *>(p.x) + token * p.x_stride + (int64_t)h * head_bytes;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            ra[k] = P::load(src + my.oa[k]);
-            rb[k] = P::load(src + my.ob[k]);
-        }
-    };
-
-    bool first_tile = true;
+    bool prepared = false;
     int buf = 0;
-    for (int64_t base = jobs.first; base < jobs.last; base += kRopeMaxWarps, buf ^= 1) {
-        const int n = jobs.last - base < kRopeMaxWarps ? (int)(jobs.last - base) : kRopeMaxWarps;
-        // the warp's iterations of the tile: job j, iteration i of its slice
-        int j = 0, i = warp;
-        while (j < n && i >= p.iters) i -= p.iters, ++j;
+    for (int64_t base = jobs.first; base < jobs.last; base += p.tile, buf ^= 1) {
+        const int n = jobs.last - base < p.tile ? (int)(jobs.last - base) : p.tile;
+        const int64_t token0 = p.slices > 1 ? base / p.slices : base;
+        const int h0 = p.slices > 1 ? (int)(base - token0 * p.slices) * p.iters * hpw + group : group;
+        const char *tx = static_cast<const char *>(p.x) + token0 * p.x_stride;
+        char *ty = static_cast<char *>(p.y) + token0 * p.y_stride;
+        Tile at{0, warp};
+        at.settle(n, p.iters);
         Raw ra[K], rb[K];
-        int64_t token = base;
-        int it = i;
-        if (j < n) {
-            if (p.slices > 1) {
-                token = (base + j) / p.slices;
-                it = i + (int)(base + j - token * p.slices) * p.iters;
-            } else {
-                token = base + j;
+        auto load = [&]() {
+            int h = h0 + at.i * hpw;
+            h = h < heads ? h : heads - 1;
+            const uint32_t off = (uint32_t)at.j * (uint32_t)p.x_stride + (uint32_t)h * head_bytes;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                ra[k] = P::load(tx + (off + my.oa[k]));
+                rb[k] = P::load(tx + (off + my.ob[k]));
             }
-            load(token, it, ra, rb);
+        };
+        if (at.j < n) load();
+        if (!prepared) {
+            make_fractions<VE>(p, frac);
+            make_weights<T, VE, IL>(p, wsm);
+            __syncthreads();
+            prepared = true;
         }
         // the warp's own token of the tile: where it goes, its angles
         if (warp < n) {
-            const int64_t mine = p.slices > 1 ? (base + warp) / p.slices : base + warp;
+            const int64_t mine = token0 + warp;
             int64_t pos = 0;
             if constexpr (APPEND) {
                 const int seq = sequence_of(p, mine, lane);
@@ -557,75 +588,62 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(VE, K)) rope
                 if (lane == 0) rows[buf][warp] = row;
             }
             if (!APPEND || p.pos != nullptr) pos = lane_position(p, lane, mine);
-            make_angles<VE>(p, tiles + (buf * kRopeMaxWarps + warp) * 2 * p.R, lane, pos);
+            make_angles<VE>(p, frac, tiles + (buf * kRopeMaxWarps + warp) * 2 * kRopeTable, lane, pos);
         }
-        if (first_tile) make_weights<T, VE, IL>(p, wsm);
-        first_tile = false;
         __syncthreads();   // two buffers: the tile before this one may still be read
-        while (j < n) {
+        while (at.j < n) {
             Raw ca[K], cb[K];
 #pragma unroll
             for (int k = 0; k < K; ++k) ca[k] = ra[k], cb[k] = rb[k];
-            const int64_t tok = token;
-            const int h = it * hpw + group, tile_job = j;
-            i += kRopeMaxWarps;
-            while (j < n && i >= p.iters) i -= p.iters, ++j;
-            if (j < n) {   // the next one's loads
-                if (p.slices > 1) {
-                    token = (base + j) / p.slices;
-                    it = i + (int)(base + j - token * p.slices) * p.iters;
-                } else {
-                    token = base + j;
-                    it = i;
-                }
-                load(token, it, ra, rb);
-            }
+            const int job = at.j, h = h0 + at.i * hpw;
+            at.i += kRopeMaxWarps;
+            at.settle(n, p.iters);
+            if (at.j < n) load();   // the next heads are on their way
             float r = 1.f;
             if (p.norm) {
-                float sum = 0.f;
+                float sum[1] = {0.f};
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
                     float e[2 * VE];
                     widen_unit<T, VE>(ca[k], cb[k], e);
                     float2 acc = make_float2(0.f, 0.f);
                     squares_into<2 * VE>(acc, e);
-                    sum += my.act[k] ? acc.x + acc.y : 0.f;
+                    sum[0] += my.act[k] ? acc.x + acc.y : 0.f;
                 }
-                r = rsqrtf(fmaf(lanes_sum(sum, G), p.inv_dim, p.eps));
-#pragma unroll
-                for (int k = 0; k < K; ++k) forget(ca[k]), forget(cb[k]);
+                lanes_sum<1>(sum, G, t, lane);
+                r = rsqrtf(fmaf(sum[0], p.inv_dim, p.eps));
             }
-            const bool value = APPEND && h >= turned;
-            const float *cs = tiles + (buf * kRopeMaxWarps + tile_job) * 2 * p.R;
-            const float *w = wsm + (h >= p.q_heads ? p.head_dim : 0);
-            int64_t row = 0;
-            if constexpr (APPEND) row = rows[buf][tile_job];
-            char *dst;
-            if (!APPEND || h < p.q_heads) {
-                dst = static_cast<char *>(p.y) + tok * p.y_stride + (int64_t)h * head_bytes;
-            } else {
+            const bool key = h >= p.q_heads, value = APPEND && h >= turned;
+            const float *cs = tiles + (buf * kRopeMaxWarps + job) * 2 * kRopeTable;
+            const float *w = wsm + (key ? 2 * kRopeTable : 0);
+            char *dst = ty + ((uint32_t)job * (uint32_t)p.y_stride + (uint32_t)h * head_bytes);
+            bool store = h < heads;
+            if (APPEND && key) {
+                const int64_t row = rows[buf][job];
                 const int o = value ? h - turned : h - p.q_heads;
                 dst = static_cast<char *>(value ? p.v_cache : p.k_cache) + row + (int64_t)o * p.head_stride;
-                if (row < 0 && h == p.q_heads && t == 0 && p.dropped != nullptr) atomicAdd(p.dropped, 1);
+                store = store && row >= 0;
+                if (row < 0 && h == p.q_heads && t == 0 && my.act[0] && p.dropped != nullptr) atomicAdd(p.dropped, 1);
             }
-            const bool store = h < heads && (!APPEND || h < p.q_heads || row >= 0);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 float e[2 * VE];
                 widen_unit<T, VE>(ca[k], cb[k], e);
                 if (!value) {
+                    const float *wu = w + table_at<VE>(my.unit[k], 0), *cu = cs + table_at<VE>(my.unit[k], 0);
 #pragma unroll
                     for (int q = 0; q < VE; q += N) {
                         float w0[N], w1[N];
-                        const int at = table_at<VE>(p.units, my.unit[k], q);
-                        read_table<N>(w + at, w0);
-                        read_table<N>(w + p.head_dim / 2 + at, w1);
+                        read_table<N>(wu + table_at<VE>(0, q), w0);
+                        read_table<N>(wu + kRopeTable + table_at<VE>(0, q), w1);
                         weigh_pairs<VE, IL, N>(e, q, w0, w1, r);
-                        if (my.unit[k] < p.rot_units) {
+                    }
+                    if (my.unit[k] < p.rot_units) {
+#pragma unroll
+                        for (int q = 0; q < VE; q += N) {
                             float c[N], s[N];
-                            const int turn = table_at<VE>(p.rot_units, my.unit[k], q);
-                            read_table<N>(cs + turn, c);
-                            read_table<N>(cs + p.R + turn, s);
+                            read_table<N>(cu + table_at<VE>(0, q), c);
+                            read_table<N>(cu + kRopeTable + table_at<VE>(0, q), s);
                             turn_pairs<VE, IL, N>(e, q, c, s);
                         }
                     }
@@ -634,7 +652,7 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(VE, K)) rope
                     float x[VE], y[VE];
 #pragma unroll
                     for (int v = 0; v < VE; ++v) x[v] = e[v], y[v] = e[VE + v];
-                    if (MODE == kRopeAppendE4m3 && h >= p.q_heads) {
+                    if (MODE == kRopeAppendE4m3 && key) {
                         const float inv = value ? p.v_inv : p.k_inv;
                         P::store_e4m3(dst + my.oa[k] / S, x, inv);
                         P::store_e4m3(dst + my.ob[k] / S, y, inv);
@@ -662,39 +680,24 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(VE, K)) 
     constexpr int S = (int)sizeof(typename T::storage);
     constexpr int N = pairs_at_once(VE);
     constexpr int KN = NORM ? K : 1;
-    extern __shared__ __align__(16) float wsm[];
+    extern __shared__ __align__(16) unsigned char smem[];
+    uint64_t *frac = reinterpret_cast<uint64_t *>(smem);
+    float *wsm = reinterpret_cast<float *>(smem + 8 * kRopeTable);
+    float *tiles = wsm + 4 * kRopeTable;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int G = p.lanes, t = lane & (G - 1), group = lane / G, hpw = 32 / G;
-    float *tiles = wsm + 2 * p.head_dim;
-    const int head_bytes = p.head_dim * S;
+    const int G = p.lanes, group = lane / G, t = lane - group * G, hpw = p.heads_a_warp;
+    const uint32_t head_bytes = (uint32_t)(p.head_dim * S);
     Lane<VE, K, IL, S> my;
-    my.set(p, t);
+    my.set(p, t, group);
     const bool key = (int)blockIdx.x >= p.q_blocks;
     const int heads = key ? p.k_heads : p.q_heads, iters = key ? p.iters_k : p.iters;
     Jobs jobs;
     jobs.set(key ? blockIdx.x - p.q_blocks : blockIdx.x, key ? p.each_k : p.each, key ? p.extra_k : p.extra);
-    const int64_t head0 = key ? (int64_t)p.q_heads * head_bytes : 0;
-    const float *w = wsm + (key ? p.head_dim : 0);
+    const uint32_t head0 = key ? (uint32_t)p.q_heads * head_bytes : 0u;
+    const float *w = wsm + (key ? 2 * kRopeTable : 0);
 
     pdl_wait_for_inputs();
     pdl_allow_dependents();
-
-    auto load = [&](int64_t token, int it, Raw (&da)[K], Raw (&db)[K], Raw (&xa)[KN], Raw (&xb)[KN]) {
-        int h = it * hpw + group;
-        h = h < heads ? h : heads - 1;
-        const int64_t off = head0 + (int64_t)h * head_bytes;
-        const char *gr = static_cast<const char *>(p.dy) + token * p.dy_stride + off;
-        const char *xr = static_cast<const char *>(p.x) + token * p.x_stride + off;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            da[k] = P::load(gr + my.oa[k]);
-            db[k] = P::load(gr + my.ob[k]);
-            if constexpr (NORM) {
-                xa[k] = P::load(xr + my.oa[k]);
-                xb[k] = P::load(xr + my.ob[k]);
-            }
-        }
-    };
 
     float gw[KN][2 * VE];   // the weight's gradient
 #pragma unroll
@@ -702,45 +705,66 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(VE, K)) 
 #pragma unroll
         for (int v = 0; v < 2 * VE; ++v) gw[k][v] = 0.f;
 
-    bool first_tile = true;
+    bool prepared = false;
     int buf = 0;
-    for (int64_t base = jobs.first; base < jobs.last; base += kRopeMaxWarps, buf ^= 1) {
-        const int n = jobs.last - base < kRopeMaxWarps ? (int)(jobs.last - base) : kRopeMaxWarps;
-        int j = 0, i = warp;
-        while (j < n && i >= iters) i -= iters, ++j;
+    for (int64_t base = jobs.first; base < jobs.last; base += p.tile, buf ^= 1) {
+        const int n = jobs.last - base < p.tile ? (int)(jobs.last - base) : p.tile;
+        const char *tg = static_cast<const char *>(p.dy) + base * p.dy_stride + head0;
+        const char *tx = static_cast<const char *>(p.x) + base * p.x_stride + head0;
+        char *ty = static_cast<char *>(p.y) + base * p.y_stride + head0;
+        Tile at{0, warp};
+        at.settle(n, iters);
         Raw da[K], db[K], xa[KN], xb[KN];
-        if (j < n) load(base + j, i, da, db, xa, xb);
+        auto load = [&]() {
+            int h = at.i * hpw + group;
+            h = h < heads ? h : heads - 1;
+            const uint32_t go = (uint32_t)at.j * (uint32_t)p.dy_stride + (uint32_t)h * head_bytes;
+            const uint32_t xo = (uint32_t)at.j * (uint32_t)p.x_stride + (uint32_t)h * head_bytes;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                da[k] = P::load(tg + (go + my.oa[k]));
+                db[k] = P::load(tg + (go + my.ob[k]));
+                if constexpr (NORM) {
+                    xa[k] = P::load(tx + (xo + my.oa[k]));
+                    xb[k] = P::load(tx + (xo + my.ob[k]));
+                }
+            }
+        };
+        if (at.j < n) load();
+        if (!prepared) {
+            make_fractions<VE>(p, frac);
+            if constexpr (NORM) make_weights<T, VE, IL>(p, wsm);
+            __syncthreads();
+            prepared = true;
+        }
         if (warp < n)
-            make_angles<VE>(p, tiles + (buf * kRopeMaxWarps + warp) * 2 * p.R, lane,
+            make_angles<VE>(p, frac, tiles + (buf * kRopeMaxWarps + warp) * 2 * kRopeTable, lane,
                             lane_position(p, lane, base + warp));
-        if (first_tile && NORM) make_weights<T, VE, IL>(p, wsm);
-        first_tile = false;
         __syncthreads();   // two buffers: the tile before this one may still be read
-        while (j < n) {
+        while (at.j < n) {
             Raw ea[K], eb[K], ya[KN], yb[KN];
 #pragma unroll
             for (int k = 0; k < K; ++k) ea[k] = da[k], eb[k] = db[k];
 #pragma unroll
             for (int k = 0; k < KN; ++k) ya[k] = xa[k], yb[k] = xb[k];
-            const int64_t token = base + j;
-            const int h = i * hpw + group;
-            const float *cs = tiles + (buf * kRopeMaxWarps + j) * 2 * p.R;
-            i += kRopeMaxWarps;
-            while (j < n && i >= iters) i -= iters, ++j;
-            if (j < n) load(base + j, i, da, db, xa, xb);
+            const int job = at.j, h = at.i * hpw + group;
+            at.i += kRopeMaxWarps;
+            at.settle(n, iters);
+            if (at.j < n) load();   // the next heads are on their way
+            const float *cs = tiles + (buf * kRopeMaxWarps + job) * 2 * kRopeTable;
 
             float g[K][2 * VE];
-            float s1 = 0.f, s2 = 0.f;
+            float sums[2] = {0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 widen_unit<T, VE>(ea[k], eb[k], g[k]);
+                const float *wu = w + table_at<VE>(my.unit[k], 0), *cu = cs + table_at<VE>(my.unit[k], 0);
                 if (my.unit[k] < p.rot_units) {
 #pragma unroll
                     for (int q = 0; q < VE; q += N) {
                         float c[N], s[N];
-                        const int turn = table_at<VE>(p.rot_units, my.unit[k], q);
-                        read_table<N>(cs + turn, c);
-                        read_table<N>(cs + p.R + turn, s);
+                        read_table<N>(cu + table_at<VE>(0, q), c);
+                        read_table<N>(cu + kRopeTable + table_at<VE>(0, q), s);
 #pragma unroll
                         for (int v = 0; v < N; ++v) s[v] = -s[v];
                         turn_pairs<VE, IL, N>(g[k], q, c, s);
@@ -754,9 +778,8 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(VE, K)) 
 #pragma unroll
                     for (int q = 0; q < VE; q += N) {
                         float w0[N], w1[N];
-                        const int at = table_at<VE>(p.units, my.unit[k], q);
-                        read_table<N>(w + at, w0);
-                        read_table<N>(w + p.head_dim / 2 + at, w1);
+                        read_table<N>(wu + table_at<VE>(0, q), w0);
+                        read_table<N>(wu + kRopeTable + table_at<VE>(0, q), w1);
 #pragma unroll
                         for (int v = 0; v < N; ++v) {
                             const int a = first_of<VE, IL>(q + v), b = second_of<VE, IL>(q + v);
@@ -764,31 +787,28 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(VE, K)) 
                                              make_float2(x[a], x[b]), dot);
                         }
                     }
-                    s1 += my.act[k] ? sq.x + sq.y : 0.f;
-                    s2 += my.act[k] ? dot.x + dot.y : 0.f;
+                    sums[0] += my.act[k] ? sq.x + sq.y : 0.f;
+                    sums[1] += my.act[k] ? dot.x + dot.y : 0.f;
                 }
             }
             float r = 1.f, mean = 0.f;
             if constexpr (NORM) {
-                s1 = lanes_sum(s1, G);
-                s2 = lanes_sum(s2, G);
-                r = rsqrtf(fmaf(s1, p.inv_dim, p.eps));
-                mean = -(s2 * p.inv_dim) * r;   // dx = r (w g - (x r) mean)
-#pragma unroll
-                for (int k = 0; k < K; ++k) forget(ya[k]), forget(yb[k]);
+                lanes_sum<2>(sums, G, t, lane);
+                r = rsqrtf(fmaf(sums[0], p.inv_dim, p.eps));
+                mean = -(sums[1] * p.inv_dim) * r;   // dx = r (w g - (x r) mean)
             }
-            char *dst = static_cast<char *>(p.y) + token * p.y_stride + head0 + (int64_t)h * head_bytes;
+            char *dst = ty + ((uint32_t)job * (uint32_t)p.y_stride + (uint32_t)h * head_bytes);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 if constexpr (NORM) {
                     float x[2 * VE];
                     widen_unit<T, VE>(ya[k], yb[k], x);
+                    const float *wu = w + table_at<VE>(my.unit[k], 0);
 #pragma unroll
                     for (int q = 0; q < VE; q += N) {
                         float w0[N], w1[N];
-                        const int at = table_at<VE>(p.units, my.unit[k], q);
-                        read_table<N>(w + at, w0);
-                        read_table<N>(w + p.head_dim / 2 + at, w1);
+                        read_table<N>(wu + table_at<VE>(0, q), w0);
+                        read_table<N>(wu + kRopeTable + table_at<VE>(0, q), w1);
 #pragma unroll
                         for (int v = 0; v < N; ++v) {
                             const int a = first_of<VE, IL>(q + v), b = second_of<VE, IL>(q + v);
@@ -821,8 +841,10 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(VE, K)) 
 #pragma unroll
             for (int k = 0; k < K; ++k)
 #pragma unroll
-                for (int v = 0; v < 2 * VE; ++v)
-                    for (int off = G; off < 32; off <<= 1) gw[k][v] += __shfl_xor_sync(0xffffffffu, gw[k][v], off);
+                for (int v = 0; v < 2 * VE; ++v) {
+                    const float own = gw[k][v];
+                    for (int g = 1; g < hpw; ++g) gw[k][v] += __shfl_sync(0xffffffffu, own, (lane + g * G) & 31);
+                }
             __syncthreads();   // the tables are read; their place takes the warps' sums [kRopeMaxWarps][D]
             if (group == 0) {
 #pragma unroll

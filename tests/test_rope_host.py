@@ -48,7 +48,7 @@ def test_rope_refusals_without_cuda(over):
 
 def test_rope_limits_and_empty_batches_without_cuda():
     assert fwd(d=514, xs=12 * 514, ys=12 * 514) == N.RMSNORM_EUNSUPPORTED
-    assert fwd(q=1 << 20, xs=1 << 40, ys=1 << 40) == N.RMSNORM_EUNSUPPORTED
+    assert fwd(q=1 << 23, xs=1 << 40, ys=1 << 40) == N.RMSNORM_EUNSUPPORTED
     assert fwd(x=None, y=None, tokens=0) == N.RMSNORM_OK
     assert fwd(x=None, y=None, tokens=0, r=rope(positions=None, inv_freq=None)) == N.RMSNORM_OK
     assert ctypes.sizeof(N.Rope) == 56 and ctypes.sizeof(N.PagedKV) == 112
