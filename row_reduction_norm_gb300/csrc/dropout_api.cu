@@ -126,15 +126,15 @@ int backward(const void *dy, const void *h, const void *w, const void *dh, void 
                                        : rrn::drop_bwd_f32(gt, ch, dw != nullptr);
             threads = rrn::drop_block_threads(gt);
             groups = div_up(rows, threads / gt);
-            if (dw != nullptr && threads > gt) smem = (size_t)hidden * sizeof(float);
+            smem = (size_t)rrn::drop_ring_bytes(gt, ch);
         } else {
             threads = loop_block(vec, hidden);
             fn = rrn::drop_bwd_loop(dtype, vec, threads, dw != nullptr);
             p.acc_in_smem = dw != nullptr && hidden <= kSmemSums;
             smem = (p.acc_in_smem ? (size_t)hidden * sizeof(float) : 0) + (size_t)(thr ? p.blocks_per_row : 0);
-            if (smem > 48 * 1024 && (st = rrn::allow_smem(dev, fn)) != RMSNORM_OK) return st;
         }
         if (fn == nullptr) return RMSNORM_EINVAL;
+        if (smem > 48 * 1024 && (st = rrn::allow_smem(dev, fn)) != RMSNORM_OK) return st;
         int resident = 0;
         if ((st = rrn::resident_blocks(dev, fn, threads, smem, &resident)) != RMSNORM_OK) return st;
         blocks = (int64_t)sms * resident;

@@ -43,41 +43,72 @@ struct DropParams {
 
 // --------------------------------------------------------------- generator
 
-__device__ __forceinline__ uint4 philox(uint64_t seed, uint64_t offset, uint64_t index) {
-    uint32_t c0 = (uint32_t)index, c1 = (uint32_t)(index >> 32);
-    uint32_t c2 = (uint32_t)offset, c3 = (uint32_t)(offset >> 32);
+// M calls at once: a round's key is made once for all of them.
+template <int M>
+__device__ __forceinline__ void philox(uint64_t seed, uint64_t offset, const uint64_t (&index)[M], uint32_t (&out)[M][4]) {
     uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
 #pragma unroll
+    for (int m = 0; m < M; ++m) {
+        out[m][0] = (uint32_t)index[m];
+        out[m][1] = (uint32_t)(index[m] >> 32);
+        out[m][2] = (uint32_t)offset;
+        out[m][3] = (uint32_t)(offset >> 32);
+    }
+#pragma unroll
     for (int r = 0; r < 10; ++r) {
-        const uint64_t p = (uint64_t)c0 * 0xD2511F53u, q = (uint64_t)c2 * 0xCD9E8D57u;
-        c0 = (uint32_t)(q >> 32) ^ c1 ^ k0;
-        c1 = (uint32_t)q;
-        c2 = (uint32_t)(p >> 32) ^ c3 ^ k1;
-        c3 = (uint32_t)p;
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            uint32_t(&c)[4] = out[m];
+            const uint64_t p = (uint64_t)c[0] * 0xD2511F53u, q = (uint64_t)c[2] * 0xCD9E8D57u;
+            c[0] = (uint32_t)(q >> 32) ^ c[1] ^ k0;
+            c[1] = (uint32_t)q;
+            c[2] = (uint32_t)(p >> 32) ^ c[3] ^ k1;
+            c[3] = (uint32_t)p;
+        }
         k0 += 0x9E3779B9u;
         k1 += 0xBB67AE85u;
     }
-    return make_uint4(c0, c1, c2, c3);
 }
 
-__device__ __forceinline__ uint32_t keep2(uint32_t word, uint32_t thr) {
-    return (uint32_t)((word & 0xffffu) >= thr) | ((uint32_t)((word >> 16) >= thr) << 1);
+// Whether element e of a block is kept; thr_hi = thr << 16 (the low half of a
+// word is compared where the high half stands).
+__device__ __forceinline__ bool kept(const uint32_t (&w)[4], int e, uint32_t thr_hi) {
+    return ((e & 1) ? w[e / 2] : w[e / 2] << 16) >= thr_hi;
+}
+
+// The words of M chunks of a row (chunk u of V elements: a block of 8, or half
+// a one, then in words 0 and 1).
+template <int V, int M>
+__device__ __forceinline__ void chunk_words(uint64_t seed, uint64_t offset, uint64_t row_block, const int (&u)[M],
+                                            uint32_t (&w)[M][4]) {
+    uint64_t index[M];
+#pragma unroll
+    for (int m = 0; m < M; ++m) index[m] = row_block + (uint32_t)(V == 8 ? u[m] : u[m] / 2);
+    philox<M>(seed, offset, index, w);
+    if constexpr (V == 4) {
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            w[m][0] = (u[m] & 1) ? w[m][2] : w[m][0];
+            w[m][1] = (u[m] & 1) ? w[m][3] : w[m][1];
+        }
+    }
+}
+
+// a[e] = kept ? a[e] * scale : 0
+template <int V>
+__device__ __forceinline__ void drop(float (&a)[V], const uint32_t (&w)[4], uint32_t thr_hi, float scale) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) a[e] = kept(w, e, thr_hi) ? a[e] * scale : 0.f;
 }
 
 // Bit e of the result: whether element e of the 8-element block is kept.
 __device__ __forceinline__ uint32_t keep_block(uint64_t seed, uint64_t offset, uint64_t index, uint32_t thr) {
-    const uint4 u = philox(seed, offset, index);
-    return keep2(u.x, thr) | (keep2(u.y, thr) << 2) | (keep2(u.z, thr) << 4) | (keep2(u.w, thr) << 6);
-}
-
-// The V bits of 16-byte chunk u of a row (a block, or half a one).
-template <int V>
-__device__ __forceinline__ uint32_t keep_chunk(uint64_t seed, uint64_t offset, int64_t row_block, int u, uint32_t thr) {
-    if constexpr (V == 8) {
-        return keep_block(seed, offset, (uint64_t)(row_block + u), thr);
-    } else {
-        return keep_block(seed, offset, (uint64_t)(row_block + u / 2), thr) >> (4 * (u & 1));
-    }
+    const uint64_t at[1] = {index};
+    uint32_t w[1][4], bits = 0;
+    philox<1>(seed, offset, at, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) bits |= (uint32_t)kept(w[0], e, thr << 16) << e;
+    return bits;
 }
 
 __host__ __device__ constexpr int drop_block_threads(int gt) { return gt >= 256 ? gt : 256; }
@@ -137,18 +168,27 @@ __global__ void __launch_bounds__(drop_block_threads(GT)) drop_fwd_kernel(const 
         float acc[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) acc[e] = 0.f;
+        constexpr int M = CH % 2 == 0 ? 2 : 1;   // chunks whose generator calls go together
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const int u = c * GT + t;
-            const uint32_t keep = p.thr ? keep_chunk<V>(seed, offset, row * p.blocks_per_row, u, p.thr) : 0xffu;
-            float a[V], b[V];
-            unpack(xc[c], a, T{});
-            unpack(hc[c], b, T{});
+        for (int c0 = 0; c0 < CH; c0 += M) {
+            int u[M];
+            uint32_t word[M][4];
 #pragma unroll
-            for (int e = 0; e < V; ++e) a[e] = add_round(b[e], (keep >> e) & 1u ? a[e] * p.scale : 0.f, T{});
-            hc[c] = pack(a, T{});
-            if (ok && u < p.units) st16(static_cast<char *>(p.h_out) + off + (int64_t)u * 16, hc[c]);
-            sq_accumulate(a, acc);
+            for (int m = 0; m < M; ++m) u[m] = (c0 + m) * GT + t;
+            if (p.thr) chunk_words<V, M>(seed, offset, (uint64_t)(row * p.blocks_per_row), u, word);
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                const int c = c0 + m;
+                float a[V], b[V];
+                unpack(xc[c], a, T{});
+                unpack(hc[c], b, T{});
+                if (p.thr) drop<V>(a, word[m], p.thr << 16, p.scale);
+#pragma unroll
+                for (int e = 0; e < V; ++e) a[e] = add_round(b[e], a[e], T{});
+                hc[c] = pack(a, T{});
+                if (ok && u[m] < p.units) st16(static_cast<char *>(p.h_out) + off + (int64_t)u[m] * 16, hc[c]);
+                sq_accumulate(a, acc);
+            }
         }
         const float sum = row_sums<GT>(tree_sum(acc), 0.f, red[parity], slot, t).x;
         parity ^= 1;
@@ -269,22 +309,96 @@ __global__ void __launch_bounds__(BLOCK) drop_fwd_loop_kernel(const DropParams p
 }
 
 // ---------------------------------------------------------------- gradient
-// Persistent blocks of RPB row slots; a thread keeps its columns' share of dw
-// in registers over all its rows, the slots are added up in order at the end
-// and the block's sums go to partial[block].
+
+__device__ __forceinline__ void copy_async16(void *smem, const void *global) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                 : : "r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(global) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copy_async_wait() {
+    asm volatile("cp.async.wait_group %0;" : : "n"(PENDING) : "memory");
+}
+
+// Row groups a block has on their way or in hand.
+constexpr int kDropStages = 2;
+__host__ __device__ constexpr int drop_ring_bytes(int gt, int ch) {
+    return kDropStages * 3 * ch * drop_block_threads(gt) * 16;
+}
+// Blocks a SM the registers are budgeted for.
+__host__ __device__ constexpr int drop_bwd_resident(int gt) { return drop_block_threads(gt) == 256 ? 2 : 1; }
+
+template <int N>
+__device__ __forceinline__ void mul_pairs(float (&a)[N], const float (&b)[N]) {
+#pragma unroll
+    for (int k = 0; k < N; k += 2) {
+        const float2 v = __fmul2_rn(make_float2(a[k], a[k + 1]), make_float2(b[k], b[k + 1]));
+        a[k] = v.x, a[k + 1] = v.y;
+    }
+}
+// acc += a * b
+template <int N>
+__device__ __forceinline__ void fma_pairs(float (&acc)[N], const float (&a)[N], const float (&b)[N]) {
+#pragma unroll
+    for (int k = 0; k < N; k += 2) {
+        const float2 v = __ffma2_rn(make_float2(a[k], a[k + 1]), make_float2(b[k], b[k + 1]),
+                                    make_float2(acc[k], acc[k + 1]));
+        acc[k] = v.x, acc[k + 1] = v.y;
+    }
+}
+template <int N>
+__device__ __forceinline__ void scale_pairs(float (&a)[N], float r) {
+#pragma unroll
+    for (int k = 0; k < N; k += 2) {
+        const float2 v = __fmul2_rn(make_float2(a[k], a[k + 1]), make_float2(r, r));
+        a[k] = v.x, a[k + 1] = v.y;
+    }
+}
+
+// Persistent blocks of RPB row slots.  A thread copies its own chunks of dy, h
+// and dh into its own places of a shared-memory ring, a row group ahead, and
+// reads them back where they are used: what is on its way needs no registers
+// and no barrier (a thread waits for its own copies only), and what stays in
+// registers is the thread's columns' share of dw over all its rows.  The
+// slots are added up in order at the end and the block's sums go to
+// partial[block].
 template <typename T, int GT, int CH, bool DW>
-__global__ void __launch_bounds__(drop_block_threads(GT)) drop_bwd_kernel(const DropParams p) {
+__global__ void __launch_bounds__(drop_block_threads(GT), drop_bwd_resident(GT)) drop_bwd_kernel(const DropParams p) {
     constexpr int V = T::kVec, BLOCK = drop_block_threads(GT), RPB = BLOCK / GT;
     __shared__ float2 red[2][RPB][GT > 32 ? GT / 32 : 1];
-    extern __shared__ float slots[];   // [row_elems], with DW and RPB > 1
+    extern __shared__ __align__(16) Chunk ring[];   // [stage][dy, h, dh][CH][BLOCK]
     const int tid = threadIdx.x, slot = tid / GT, t = tid % GT;
     pdl_wait_for_inputs();
     pdl_allow_dependents();
+
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    auto place = [&](int stage, int tensor, int c) -> Chunk & { return ring[((stage * 3 + tensor) * CH + c) * BLOCK + tid]; };
+    auto issue = [&](int64_t first, int stage) {
+        const int64_t row = first + slot;
+        if (row < p.rows) {
+            const int64_t off = row * p.row_bytes + t * 16;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                if (c * GT + t < p.units) {
+                    copy_async16(&place(stage, 0, c), static_cast<const char *>(p.dy) + off + c * GT * 16);
+                    copy_async16(&place(stage, 1, c), static_cast<const char *>(p.h) + off + c * GT * 16);
+                    if (p.dh != nullptr)
+                        copy_async16(&place(stage, 2, c), static_cast<const char *>(p.dh) + off + c * GT * 16);
+                }
+            }
+        }
+        copy_async_commit();   // an empty group past the end
+    };
+    int64_t first = (int64_t)blockIdx.x * RPB;
+    issue(first, 0);
+
     uint64_t seed = 0, offset = 0;
     if (p.thr) {
         seed = p.rng[0];
         offset = p.rng[1];
     }
+    const uint32_t thr_hi = p.thr << 16;
+    const bool weighted = p.w != nullptr;
     float dw[DW ? CH : 1][V];
 #pragma unroll
     for (int c = 0; c < (DW ? CH : 1); ++c)
@@ -294,79 +408,100 @@ __global__ void __launch_bounds__(drop_block_threads(GT)) drop_bwd_kernel(const 
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
         const int u = c * GT + t;
-        wc[c] = p.w != nullptr && u < p.units ? ld_readonly16(static_cast<const char *>(p.w) + (int64_t)u * 16)
-                                              : Chunk{{0u, 0u, 0u, 0u}};
+        wc[c] = weighted && u < p.units ? ld_readonly16(static_cast<const char *>(p.w) + (int64_t)u * 16)
+                                        : Chunk{{0u, 0u, 0u, 0u}};
     }
+    auto weight = [&](int c, float (&w)[V]) {
+        unpack(wc[c], w, T{});
+        const float2 b2 = make_float2(p.w_bias, p.w_bias);
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+            const float2 v = __fadd2_rn(make_float2(w[e], w[e + 1]), b2);
+            w[e] = v.x, w[e + 1] = v.y;
+        }
+    };
+
     int parity = 0;
-    for (int64_t first = (int64_t)blockIdx.x * RPB; first < p.rows; first += (int64_t)gridDim.x * RPB) {
+    for (; first < p.rows; first += step) {
         const int64_t row = first + slot;
         const bool ok = row < p.rows;
-        const int64_t off = row * p.row_bytes;
-        Chunk gc[CH], hc[CH], dc[CH];
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const int u = c * GT + t;
-            const bool in = ok && u < p.units;
-            gc[c] = in ? ld_stream16(static_cast<const char *>(p.dy) + off + (int64_t)u * 16) : Chunk{{0u, 0u, 0u, 0u}};
-            hc[c] = in ? ld_stream16(static_cast<const char *>(p.h) + off + (int64_t)u * 16) : Chunk{{0u, 0u, 0u, 0u}};
-        }
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const int u = c * GT + t;
-            dc[c] = ok && u < p.units && p.dh != nullptr
-                        ? ld_stream16(static_cast<const char *>(p.dh) + off + (int64_t)u * 16)
-                        : Chunk{{0u, 0u, 0u, 0u}};
-        }
+        const int64_t off = row * p.row_bytes + t * 16;
+        issue(first + step, parity ^ 1);
+        copy_async_wait<1>();   // this group's copies of this thread are there
         float sq[V], dot[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) sq[e] = dot[e] = 0.f;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            float h[V], g[V], w[V];
-            unpack(hc[c], h, T{});
-            unpack(gc[c], g, T{});
-            unpack(wc[c], w, T{});
-            sq_accumulate(h, sq);
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                if (p.w != nullptr) g[e] *= w[e] + p.w_bias;
-                dot[e] = fmaf(g[e], h[e], dot[e]);
+            if (ok && c * GT + t < p.units) {
+                float h[V], g[V], w[V];
+                unpack(place(parity, 1, c), h, T{});
+                unpack(place(parity, 0, c), g, T{});
+                sq_accumulate(h, sq);
+                if (weighted) {
+                    weight(c, w);
+                    mul_pairs(g, w);
+                }
+                fma_pairs(dot, g, h);
             }
         }
         const float2 s = row_sums<GT>(tree_sum(sq), tree_sum(dot), red[parity], slot, t);
-        parity ^= 1;
-        // an idle slot's zeros must add nothing, whatever eps is
-        const float r = ok ? rsqrtf(s.x / p.hidden_f + p.eps) : 0.f;
-        const float m = (r * r) * (s.y / p.hidden_f);
+        const float r = rsqrtf(s.x / p.hidden_f + p.eps);
+        const float m = -(r * (s.y / p.hidden_f));   // d = r (g - (h r) mean(g h) r) + dh
+        constexpr int M = CH % 2 == 0 ? 2 : 1;
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const int u = c * GT + t;
-            float h[V], g[V], w[V], d[V];
-            unpack(hc[c], h, T{});
-            unpack(gc[c], g, T{});
-            unpack(wc[c], w, T{});
-            unpack(dc[c], d, T{});
+        for (int c0 = 0; c0 < CH; c0 += M) {
+            uint32_t word[M][4];
+            if (p.thr) {
+                int u[M];
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                if constexpr (DW) dw[c][e] = fmaf(g[e], h[e] * r, dw[c][e]);
-                if (p.w != nullptr) g[e] *= w[e] + p.w_bias;
-                const float v = r * (g[e] - h[e] * m);
-                d[e] = p.dh != nullptr ? v + d[e] : v;
+                for (int k = 0; k < M; ++k) u[k] = (c0 + k) * GT + t;
+                chunk_words<V, M>(seed, offset, (uint64_t)(row * p.blocks_per_row), u, word);
             }
-            if (ok && u < p.units) {
-                st16(static_cast<char *>(p.dres) + off + (int64_t)u * 16, pack(d, T{}));
-                if (p.dx != nullptr) {
-                    const uint32_t keep = p.thr ? keep_chunk<V>(seed, offset, row * p.blocks_per_row, u, p.thr) : 0xffu;
 #pragma unroll
-                    for (int e = 0; e < V; ++e) d[e] = (keep >> e) & 1u ? d[e] * p.scale : 0.f;
-                    st16(static_cast<char *>(p.dx) + off + (int64_t)u * 16, pack(d, T{}));
+            for (int k = 0; k < M; ++k) {
+                const int c = c0 + k;
+                if (ok && c * GT + t < p.units) {
+                    float h[V], g[V], w[V], d[V];
+                    unpack(place(parity, 1, c), h, T{});
+                    unpack(place(parity, 0, c), g, T{});
+                    scale_pairs(h, r);
+                    if constexpr (DW) fma_pairs(dw[c], g, h);
+                    if (weighted) {
+                        weight(c, w);
+                        mul_pairs(g, w);
+                    }
+                    float mm[V];
+#pragma unroll
+                    for (int e = 0; e < V; ++e) mm[e] = m;
+                    fma_pairs(g, h, mm);
+                    if (p.dh != nullptr) {
+                        unpack(place(parity, 2, c), d, T{});
+                        float rr[V];
+#pragma unroll
+                        for (int e = 0; e < V; ++e) rr[e] = r;
+                        fma_pairs(d, g, rr);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < V; ++e) d[e] = g[e];
+                        scale_pairs(d, r);
+                    }
+                    st16(static_cast<char *>(p.dres) + off + c * GT * 16, pack(d, T{}));
+                    if (p.dx != nullptr) {
+                        if (p.thr) drop<V>(d, word[k], thr_hi, p.scale);
+                        st16(static_cast<char *>(p.dx) + off + c * GT * 16, pack(d, T{}));
+                    }
                 }
             }
         }
+        parity ^= 1;
     }
+    copy_async_wait<0>();
     if constexpr (DW) {
         float *out = p.partial + (int64_t)blockIdx.x * p.row_elems;
         if constexpr (RPB > 1) {
+            float *slots = reinterpret_cast<float *>(ring);   // [row_elems], at most a third of the ring
+            __syncthreads();   // every thread is done with its places
             for (int s = 0; s < RPB; ++s) {
                 if (slot == s) {
 #pragma unroll
