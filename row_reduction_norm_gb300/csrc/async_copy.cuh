@@ -1,0 +1,26 @@
+// async_copy.cuh -- per-thread asynchronous copies from global to shared
+// memory: a thread waits for its own copies only and reads back its own
+// places, so a ring of them needs no barrier.
+#pragma once
+
+#include <stdint.h>
+
+namespace rrn {
+
+// BYTES: 4, 8 or 16, both addresses aligned to it.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *smem, const void *global) {
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(smem);
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" : : "r"(to), "l"(global) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" : : "r"(to), "l"(global), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most PENDING of the thread's groups are on their way.
+template <int PENDING>
+__device__ __forceinline__ void copy_async_wait() {
+    asm volatile("cp.async.wait_group %0;" : : "n"(PENDING) : "memory");
+}
+
+}  // namespace rrn

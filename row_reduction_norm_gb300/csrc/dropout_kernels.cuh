@@ -20,6 +20,7 @@
 // probability with which they are really kept, so the mean is exact.
 #pragma once
 
+#include "async_copy.cuh"
 #include "rmsnorm_kernels.cuh"
 
 namespace rrn {
@@ -310,16 +311,6 @@ __global__ void __launch_bounds__(BLOCK) drop_fwd_loop_kernel(const DropParams p
 
 // ---------------------------------------------------------------- gradient
 
-__device__ __forceinline__ void copy_async16(void *smem, const void *global) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
-                 : : "r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(global) : "memory");
-}
-__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int PENDING>
-__device__ __forceinline__ void copy_async_wait() {
-    asm volatile("cp.async.wait_group %0;" : : "n"(PENDING) : "memory");
-}
-
 // Row groups a block has on their way or in hand.
 constexpr int kDropStages = 2;
 __host__ __device__ constexpr int drop_ring_bytes(int gt, int ch) {
@@ -380,10 +371,10 @@ __global__ void __launch_bounds__(drop_block_threads(GT), drop_bwd_resident(GT))
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
                 if (c * GT + t < p.units) {
-                    copy_async16(&place(stage, 0, c), static_cast<const char *>(p.dy) + off + c * GT * 16);
-                    copy_async16(&place(stage, 1, c), static_cast<const char *>(p.h) + off + c * GT * 16);
+                    copy_async<16>(&place(stage, 0, c), static_cast<const char *>(p.dy) + off + c * GT * 16);
+                    copy_async<16>(&place(stage, 1, c), static_cast<const char *>(p.h) + off + c * GT * 16);
                     if (p.dh != nullptr)
-                        copy_async16(&place(stage, 2, c), static_cast<const char *>(p.dh) + off + c * GT * 16);
+                        copy_async<16>(&place(stage, 2, c), static_cast<const char *>(p.dh) + off + c * GT * 16);
                 }
             }
         }

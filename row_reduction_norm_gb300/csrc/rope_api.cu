@@ -188,7 +188,7 @@ int rmsnorm_qk_rope_fwd(const void *x, void *y, int64_t tokens, int64_t x_token_
 int64_t rmsnorm_qk_rope_bwd_workspace_bytes(int64_t head_dim) {
     if (head_dim <= 0 || head_dim % 2 != 0) return RMSNORM_EINVAL;
     if (head_dim > rrn::kRopeMaxDim) return RMSNORM_EUNSUPPORTED;
-    return (int64_t)kBwdMaxBlocks * head_dim * (int64_t)sizeof(float);
+    return (int64_t)kBwdMaxBlocks * 2 * head_dim * (int64_t)sizeof(float);
 }
 
 int rmsnorm_qk_rope_bwd(const void *dy, const void *x, void *dx, int64_t tokens, int64_t dy_token_stride,
@@ -223,7 +223,7 @@ int rmsnorm_qk_rope_bwd(const void *dy, const void *x, void *dx, int64_t tokens,
     p.dy_stride = dy_token_stride * s;
     p.y_stride = dx_token_stride * s;
     p.partial = static_cast<float *>(dq_w != nullptr ? workspace : nullptr);
-    int64_t blocks_q = 0, blocks_k = 0;
+    int64_t blocks = 0;
     if (tokens > 0) {
         Unit u;
         u.at(dy, s), u.at(dx, s), u.at(q_w, s), u.at(k_w, s);
@@ -239,33 +239,34 @@ int rmsnorm_qk_rope_bwd(const void *dy, const void *x, void *dx, int64_t tokens,
         p.iters = (int32_t)div_up(q_heads, p.heads_a_warp);
         p.iters_k = (int32_t)div_up(k_heads, p.heads_a_warp);
         p.tile = tile_reaches(p.dy_stride, p.y_stride, norm == 1 ? p.x_stride : 0) ? rrn::kRopeMaxWarps : 1;
-        const size_t smem = rrn::kRopeSmemBytes;
+        const rrn::RopeShape held = (dtype == RMSNORM_BF16 ? rrn::kRopeShapesBf16 : rrn::kRopeShapesF32)[shape];
+        const size_t smem = rrn::kRopeSmemBytes + rrn::rope_ring_bytes(held.ve * (int)s, held.k, norm == 1);
         int resident = 0;
+        if (smem > 48 * 1024 && (st = rrn::allow_smem(dev, fn)) != RMSNORM_OK) return st;
         if ((st = rrn::resident_blocks(dev, fn, 32 * rrn::kRopeMaxWarps, smem, &resident)) != RMSNORM_OK) return st;
         int64_t most = (int64_t)sms * resident;
         if (most > kBwdMaxBlocks) most = kBwdMaxBlocks;
-        // blocks shared out by the head iterations of the two kinds, at most
-        // one a token for each
-        const int64_t all = (int64_t)p.iters + p.iters_k;
-        int64_t bq = q_heads == 0 ? 0 : k_heads == 0 ? most : most * p.iters / all;
-        if (q_heads > 0 && bq < 1) bq = 1;
-        int64_t bk = k_heads == 0 ? 0 : most - bq;
-        if (k_heads > 0 && bk < 1) bk = 1;
-        if (bq > tokens) bq = tokens;
-        if (bk > tokens) bk = tokens;
-        p.q_blocks = (int32_t)bq;
-        p.each = bq > 0 ? tokens / bq : 0;
-        p.extra = bq > 0 ? tokens % bq : 0;
-        p.each_k = bk > 0 ? tokens / bk : 0;
-        p.extra_k = bk > 0 ? tokens % bk : 0;
-        blocks_q = bq;
-        blocks_k = bk;
+        blocks = tokens < most ? tokens : most;
+        p.each = tokens / blocks;
+        p.extra = tokens % blocks;
+        // the split of a block's warps that leaves the longer of the two kinds
+        // the fewest head iterations a warp and tile
+        int64_t best = INT64_MAX;
+        for (int qw = q_heads > 0 ? 1 : 0; qw <= rrn::kRopeMaxWarps - (k_heads > 0 ? 1 : 0); ++qw) {
+            const int64_t q_turns = q_heads > 0 ? div_up((int64_t)p.tile * p.iters, qw) : 0;
+            const int64_t k_turns = k_heads > 0 ? div_up((int64_t)p.tile * p.iters_k, rrn::kRopeMaxWarps - qw) : 0;
+            const int64_t turns = q_turns > k_turns ? q_turns : k_turns;
+            if (turns < best) {
+                best = turns;
+                p.q_warps = qw;
+            }
+        }
         void *argv[] = {&p};
-        st = rrn::launch_kernel(fn, dim3((unsigned)(bq + bk)), 32 * rrn::kRopeMaxWarps, smem, stream, argv);
+        st = rrn::launch_kernel(fn, dim3((unsigned)blocks), 32 * rrn::kRopeMaxWarps, smem, stream, argv);
         if (st != RMSNORM_OK) return st;
     }
     if (dq_w == nullptr) return RMSNORM_OK;
-    return rrn::launch_colsum(static_cast<const float *>(workspace), (int)blocks_q, (int)blocks_k, head_dim, dq_w, dk_w,
+    return rrn::launch_colsum(static_cast<const float *>(workspace), (int)blocks, (int)blocks, head_dim, dq_w, dk_w,
                               dtype, stream);
 }
 

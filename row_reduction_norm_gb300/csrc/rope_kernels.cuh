@@ -29,6 +29,7 @@
 // be kept or read.
 #pragma once
 
+#include "async_copy.cuh"
 #include "rmsnorm_kernels.cuh"
 
 namespace rrn {
@@ -36,19 +37,23 @@ namespace rrn {
 constexpr int kRopeMaxDim = 512;      // head_dim
 constexpr int kRopeMaxAxes = 4;
 constexpr int kRopeMaxWarps = 8;      // warps a block
+#ifndef ROPE_BR
+#define ROPE_BR 2
+#endif
 // Blocks a SM that a shape's registers are budgeted for.  Measured on GB300,
 // bf16 8192 tokens x 40 heads of 128: the forward 31.0 us with four blocks
 // (64 registers a thread), 32.5 with three, 38.7 with five (which spill); the
 // gradient 63.5 us with two, 75.5 with three.
-__host__ __device__ constexpr int rope_resident(int ve, int k) { return ve * k <= 8 && ve > 1 ? 4 : 2; }
-__host__ __device__ constexpr int rope_bwd_resident(int ve, int k) { return ve * k <= 8 && ve > 1 ? 2 : 1; }
+// bytes: of a piece.
+__host__ __device__ constexpr int rope_resident(int bytes, int k) { return bytes * k <= 16 && bytes >= 4 ? 4 : 2; }
+__host__ __device__ constexpr int rope_bwd_resident(int bytes, int k) { return bytes * k <= 16 && bytes >= 4 ? ROPE_BR : 1; }
 
 struct RopeParams {
     const void *x;            // packed token rows (query, key, [value] heads)
     const void *dy;           // gradient: of the rotated rows
     void *y;                  // rotated rows (append: of the query heads); gradient: dx
     const void *q_w, *k_w;    // nullable
-    float *partial;           // gradient: [blocks][D] sums of the weights' gradients, or NULL
+    float *partial;           // gradient: [kind][blocks][D] sums of the weights' gradients, or NULL
     int64_t tokens;
     int64_t x_stride, y_stride, dy_stride;   // bytes between token rows
     int32_t q_heads, k_heads, v_heads;       // v_heads: append only
@@ -67,8 +72,8 @@ struct RopeParams {
     int32_t heads_a_warp;     // 32 / G, of one head iteration
     int32_t iters, iters_k;   // head iterations a job (gradient: a token's query heads, its key heads)
     int32_t slices, tile;     // forward: jobs a token; jobs a tile (1 or kRopeMaxWarps)
-    int32_t q_blocks;         // gradient: blocks of the query heads
-    int64_t each, extra, each_k, extra_k;   // a block's run of jobs: each, one more for the first `extra`
+    int32_t q_warps;          // gradient: warps of a block that take the query heads
+    int64_t each, extra;      // a block's run of jobs: each, one more for the first `extra`
     // paged cache (append)
     const int32_t *cu_tokens, *cache_lens, *page_table;
     int64_t table_stride;
@@ -152,6 +157,21 @@ struct Piece {
             asm volatile("st.global.u16 [%0], %1;" : : "l"(p), "h"((unsigned short)u[0]) : "memory");
         }
     }
+    // The same piece on its way to shared memory, and read back from there.
+    __device__ static __forceinline__ void copy(char *smem, const char *p) { copy_async<kBytes>(smem, p); }
+    __device__ static __forceinline__ Raw take(const char *smem) {
+        Raw r = zero();
+        if constexpr (kBytes == 16) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(smem);
+            r.u[0] = v.x, r.u[1] = v.y, r.u[2] = v.z, r.u[3] = v.w;
+        } else if constexpr (kBytes == 8) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(smem);
+            r.u[0] = v.x, r.u[1] = v.y;
+        } else if constexpr (kBytes == 4) {
+            r.u[0] = *reinterpret_cast<const uint32_t *>(smem);
+        }
+        return r;
+    }
     // E4M3 codes of f * inv, nearest-even, saturated at 448 (NaN stays NaN).
     __device__ static __forceinline__ void store_e4m3(char *p, const float (&f)[VE], float inv) {
         if constexpr (VE == 1) {
@@ -191,24 +211,34 @@ __device__ __forceinline__ void unit_offsets(const RopeParams &p, int u, int &a,
     }
 }
 
-// Places of a unit's pair j in the unit's 2 VE elements (a's, then b's).
-template <int VE, bool IL>
-__device__ __forceinline__ constexpr int first_of(int j) { return IL ? 2 * j : j; }
-template <int VE, bool IL>
-__device__ __forceinline__ constexpr int second_of(int j) { return IL ? 2 * j + 1 : VE + j; }
-
-// Pairs read from a table of factors at a time.
+// Factors are read for N pairs of a unit at a time, as two runs of N values;
+// the elements they go with are two runs of N as well.  Half split: the
+// pairs' first elements (q .. q + N - 1 of piece a) and their second ones (of
+// piece b).  Interleaved: the 2 N neighbours in order.
 __host__ __device__ constexpr int pairs_at_once(int ve) { return ve < 4 ? ve : 4; }
+template <int VE, bool IL>
+__device__ __forceinline__ constexpr int run_a(int q) { return IL ? 2 * q : q; }
+template <int VE, bool IL>
+__device__ __forceinline__ constexpr int run_b(int q) { return IL ? 2 * q + pairs_at_once(VE) : VE + q; }
 
-// Where pair j of unit u stands in a table of factors: the lanes of a head
-// read consecutive 16 (8, 4) bytes, and every table has kRopeTable places
-// whatever the head's size (VE * K * 32 lanes at most), so that one address
-// serves all of a unit's reads.
+// Where the first run of the N pairs from q on of unit u stands in a table of
+// factors; the second run is kRopeTable further.  The lanes of a head read
+// consecutive 16 (8, 4) bytes, and every table has as many places whatever the
+// head's size (VE * K * 32 lanes at most), so one address serves all of a
+// unit's reads.
 constexpr int kRopeTable = 256;
 template <int VE>
-__device__ __forceinline__ constexpr int table_at(int u, int j) {
+__device__ __forceinline__ constexpr int table_at(int u, int q) {
     constexpr int N = pairs_at_once(VE);
-    return (j / N) * 32 * N + u * N + j % N;
+    return (q / N) * 32 * N + u * N;
+}
+// Where a factor of pair i's first (second) element stands.
+template <int VE, bool IL>
+__device__ __forceinline__ int factor_at(int i, int second) {
+    constexpr int N = pairs_at_once(VE);
+    const int j = i % N, at = table_at<VE>(i / VE, i % VE);
+    const int place = IL ? 2 * j + second : second * N + j;
+    return at + place % N + (place / N) * kRopeTable;
 }
 
 template <int N>
@@ -224,67 +254,82 @@ __device__ __forceinline__ void read_table(const float *p, float (&v)[N]) {
     }
 }
 
-// Pairs j0 .. j0 + N - 1 of a unit turned by (c, s), two fp32 operations an
-// instruction.
-template <int VE, bool IL, int N>
-__device__ __forceinline__ void turn_pairs(float (&e)[2 * VE], int j0, const float (&c)[N], const float (&s)[N]) {
+// Two runs of N elements turned by their factors f, g (half split: cosines and
+// sines; interleaved: cosine, sine of each pair in turn); BACK: by the
+// opposite angle.  Two fp32 operations an instruction.
+template <bool IL, bool BACK, int N>
+__device__ __forceinline__ void turn_runs(float *a, float *b, const float (&f)[N], const float (&g)[N]) {
     if constexpr (N == 1) {
-        float &a = e[first_of<VE, IL>(j0)], &b = e[second_of<VE, IL>(j0)];
-        const float x = a, y = b;
-        a = fmaf(x, c[0], -(y * s[0]));
-        b = fmaf(x, s[0], y * c[0]);
+        const float x = a[0], y = b[0], s = BACK ? -g[0] : g[0];
+        a[0] = fmaf(x, f[0], -(y * s));
+        b[0] = fmaf(x, s, y * f[0]);
     } else if constexpr (IL) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            float &a = e[2 * (j0 + j)], &b = e[2 * (j0 + j) + 1];
-            const float2 v = __ffma2_rn(make_float2(a, a), make_float2(c[j], s[j]),
-                                        __fmul2_rn(make_float2(b, b), make_float2(-s[j], c[j])));
-            a = v.x, b = v.y;
+        for (int j = 0; j < 2 * N; j += 2) {
+            float *e = j < N ? a + j : b + (j - N);
+            const float c = j < N ? f[j % N] : g[j % N];
+            const float s = j < N ? f[j % N + 1] : g[j % N + 1];
+            const float2 v = BACK ? __ffma2_rn(make_float2(e[0], e[0]), make_float2(c, -s),
+                                               __fmul2_rn(make_float2(e[1], e[1]), make_float2(s, c)))
+                                  : __ffma2_rn(make_float2(e[0], e[0]), make_float2(c, s),
+                                               __fmul2_rn(make_float2(e[1], e[1]), make_float2(-s, c)));
+            e[0] = v.x, e[1] = v.y;
         }
     } else {
 #pragma unroll
         for (int j = 0; j < N; j += 2) {
-            const float2 a = make_float2(e[j0 + j], e[j0 + j + 1]);
-            const float2 b = make_float2(e[VE + j0 + j], e[VE + j0 + j + 1]);
-            const float2 cc = make_float2(c[j], c[j + 1]), ss = make_float2(s[j], s[j + 1]);
-            const float2 u = __ffma2_rn(a, cc, __fmul2_rn(b, make_float2(-s[j], -s[j + 1])));
-            const float2 v = __ffma2_rn(a, ss, __fmul2_rn(b, cc));
-            e[j0 + j] = u.x, e[j0 + j + 1] = u.y;
-            e[VE + j0 + j] = v.x, e[VE + j0 + j + 1] = v.y;
+            const float2 x = make_float2(a[j], a[j + 1]), y = make_float2(b[j], b[j + 1]);
+            const float2 c = make_float2(f[j], f[j + 1]), s = make_float2(g[j], g[j + 1]);
+            const float2 n = make_float2(-s.x, -s.y);
+            const float2 u = __ffma2_rn(x, c, __fmul2_rn(y, BACK ? s : n));
+            const float2 v = __ffma2_rn(x, BACK ? n : s, __fmul2_rn(y, c));
+            a[j] = u.x, a[j + 1] = u.y;
+            b[j] = v.x, b[j + 1] = v.y;
         }
     }
 }
 
-// The N pairs from j0 on, first and second elements, times (w0, w1) and r.
-template <int VE, bool IL, int N>
-__device__ __forceinline__ void weigh_pairs(float (&e)[2 * VE], int j0, const float (&w0)[N], const float (&w1)[N],
-                                            float r) {
-    const float2 r2 = make_float2(r, r);
-    if constexpr (N == 1 || IL) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            float &a = e[first_of<VE, IL>(j0 + j)], &b = e[second_of<VE, IL>(j0 + j)];
-            const float2 v = __fmul2_rn(__fmul2_rn(make_float2(a, b), r2), make_float2(w0[j], w1[j]));
-            a = v.x, b = v.y;
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < N; j += 2) {
-            float &a0 = e[j0 + j], &a1 = e[j0 + j + 1], &b0 = e[VE + j0 + j], &b1 = e[VE + j0 + j + 1];
-            const float2 u = __fmul2_rn(__fmul2_rn(make_float2(a0, a1), r2), make_float2(w0[j], w0[j + 1]));
-            const float2 v = __fmul2_rn(__fmul2_rn(make_float2(b0, b1), r2), make_float2(w1[j], w1[j + 1]));
-            a0 = u.x, a1 = u.y, b0 = v.x, b1 = v.y;
-        }
-    }
-}
-
-// acc += sum of squares of a unit's elements.
+// Elementwise on a run of N: x *= y;  x *= r;  acc += x y;  x = fma(y, r, x).
 template <int N>
-__device__ __forceinline__ void squares_into(float2 &acc, const float (&e)[N]) {
+__device__ __forceinline__ void run_times(float *x, const float (&y)[N]) {
+    if constexpr (N == 1) {
+        x[0] *= y[0];
+    } else {
 #pragma unroll
-    for (int j = 0; j < N; j += 2) {
-        const float2 v = make_float2(e[j], e[j + 1]);
-        acc = __ffma2_rn(v, v, acc);
+        for (int j = 0; j < N; j += 2) {
+            const float2 v = __fmul2_rn(make_float2(x[j], x[j + 1]), make_float2(y[j], y[j + 1]));
+            x[j] = v.x, x[j + 1] = v.y;
+        }
+    }
+}
+template <int N>
+__device__ __forceinline__ void run_scale(float *x, float r) {
+    float y[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) y[j] = r;
+    run_times<N>(x, y);
+}
+template <int N>
+__device__ __forceinline__ void run_fma(float *acc, const float *x, const float *y) {
+    if constexpr (N == 1) {
+        acc[0] = fmaf(x[0], y[0], acc[0]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; j += 2) {
+            const float2 v = __ffma2_rn(make_float2(x[j], x[j + 1]), make_float2(y[j], y[j + 1]),
+                                        make_float2(acc[j], acc[j + 1]));
+            acc[j] = v.x, acc[j + 1] = v.y;
+        }
+    }
+}
+template <int N>
+__device__ __forceinline__ void run_dot(float2 &acc, const float *x, const float *y) {
+    if constexpr (N == 1) {
+        acc.x = fmaf(x[0], y[0], acc.x);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; j += 2)
+            acc = __ffma2_rn(make_float2(x[j], x[j + 1]), make_float2(y[j], y[j + 1]), acc);
     }
 }
 
@@ -338,6 +383,10 @@ __device__ __forceinline__ int axis_of(const RopeParams &p, int i) {
 // Shared memory of a block: the pairs' turn fractions (64 bits each), the
 // weights of the pairs' first and second elements (a table each for query and
 // key), then two tiles of a table of cosines and one of sines a token.
+// The gradient adds its ring of pieces on their way.
+__host__ __device__ constexpr int rope_ring_bytes(int bytes, int k, bool norm) {
+    return bytes < 4 ? 0 : 2 * (norm ? 4 : 2) * k * 32 * kRopeMaxWarps * bytes;
+}
 constexpr int kRopeSmemBytes = 8 * kRopeTable + 4 * (4 * kRopeTable + 2 * kRopeMaxWarps * 2 * kRopeTable);
 
 // A token's position on axis `lane` (lanes past the axes: the last one).
@@ -348,7 +397,7 @@ __device__ __forceinline__ int64_t lane_position(const RopeParams &p, int lane, 
 
 // A token's tables of cosines and sines by one warp, pair i
 // by lane i % 32, from the position that lane a holds for axis a.
-template <int VE>
+template <int VE, bool IL>
 __device__ __forceinline__ void make_angles(const RopeParams &p, const uint64_t *frac, float *cs, int lane, int64_t pos) {
     for (int i = lane; i - lane < p.R; i += 32) {
         int64_t at = pos;
@@ -356,9 +405,8 @@ __device__ __forceinline__ void make_angles(const RopeParams &p, const uint64_t 
         if (i < p.R) {
             float s, c;
             sincos_turns((uint64_t)at * frac[i], s, c);
-            const int k = table_at<VE>(i / VE, i % VE);   // pair i % VE of unit i / VE
-            cs[k] = c;
-            cs[kRopeTable + k] = s;
+            cs[factor_at<VE, IL>(i, 0)] = c;
+            cs[factor_at<VE, IL>(i, 1)] = s;
         }
     }
 }
@@ -391,7 +439,7 @@ __device__ __forceinline__ void make_weights(const RopeParams &p, float *wsm) {
         }
         float v = 1.f;
         if (w != nullptr) v = widen_bits(ld_bits(w, e, T{}, 2), T{}) + p.w_bias;
-        wsm[(kind * 2 + second) * kRopeTable + table_at<VE>(pair / VE, pair % VE)] = v;
+        wsm[kind * 2 * kRopeTable + factor_at<VE, IL>(pair, second)] = v;
     }
 }
 
@@ -520,7 +568,7 @@ struct Tile {
 
 // ----------------------------------------------------------------- forward
 template <typename T, int VE, int K, bool IL, int MODE>
-__global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(VE, K)) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(Piece<T, VE>::kBytes, K)) rope_kernel(const RopeParams p) {
     using P = Piece<T, VE>;
     using Raw = typename P::Raw;
     constexpr int S = (int)sizeof(typename T::storage);
@@ -549,6 +597,21 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(VE, K)) rope
         if (jobs.last > most) jobs.last = most;
     }
 
+    // the warp's token of a tile: axis a's position in lane a, its cache row
+    int64_t pos = 0, row_of_mine = -1;
+    auto look_up = [&](int64_t base) {
+        const int64_t job = base + (p.tile > 1 ? warp : 0);
+        if (job < jobs.last && (warp == 0 || p.tile > 1)) {
+            const int64_t mine = p.slices > 1 ? job / p.slices : job;
+            if constexpr (APPEND) {
+                const int seq = sequence_of(p, mine, lane);
+                pos = (int64_t)p.cache_lens[seq] + (mine - p.cu_tokens[seq]);
+                row_of_mine = cache_row(p, seq, pos);
+            }
+            if (!APPEND || p.pos != nullptr) pos = lane_position(p, lane, mine);
+        }
+    };
+
     bool prepared = false;
     int buf = 0;
     for (int64_t base = jobs.first; base < jobs.last; base += p.tile, buf ^= 1) {
@@ -572,6 +635,7 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(VE, K)) rope
         };
         if (at.j < n) load();
         if (!prepared) {
+            look_up(base);
             make_fractions<VE>(p, frac);
             make_weights<T, VE, IL>(p, wsm);
             __syncthreads();
@@ -579,17 +643,10 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(VE, K)) rope
         }
         // the warp's own token of the tile: where it goes, its angles
         if (warp < n) {
-            const int64_t mine = token0 + warp;
-            int64_t pos = 0;
-            if constexpr (APPEND) {
-                const int seq = sequence_of(p, mine, lane);
-                pos = (int64_t)p.cache_lens[seq] + (mine - p.cu_tokens[seq]);
-                const int64_t row = cache_row(p, seq, pos);
-                if (lane == 0) rows[buf][warp] = row;
-            }
-            if (!APPEND || p.pos != nullptr) pos = lane_position(p, lane, mine);
-            make_angles<VE>(p, frac, tiles + (buf * kRopeMaxWarps + warp) * 2 * kRopeTable, lane, pos);
+            if (APPEND && lane == 0) rows[buf][warp] = row_of_mine;
+            make_angles<VE, IL>(p, frac, tiles + (buf * kRopeMaxWarps + warp) * 2 * kRopeTable, lane, pos);
         }
+        look_up(base + p.tile);   // the next tile's, while this one is worked on
         __syncthreads();   // two buffers: the tile before this one may still be read
         while (at.j < n) {
             Raw ca[K], cb[K];
@@ -607,7 +664,7 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(VE, K)) rope
                     float e[2 * VE];
                     widen_unit<T, VE>(ca[k], cb[k], e);
                     float2 acc = make_float2(0.f, 0.f);
-                    squares_into<2 * VE>(acc, e);
+                    run_dot<2 * VE>(acc, e, e);
                     sum[0] += my.act[k] ? acc.x + acc.y : 0.f;
                 }
                 lanes_sum<1>(sum, G, t, lane);
@@ -631,20 +688,23 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(VE, K)) rope
                 widen_unit<T, VE>(ca[k], cb[k], e);
                 if (!value) {
                     const float *wu = w + table_at<VE>(my.unit[k], 0), *cu = cs + table_at<VE>(my.unit[k], 0);
+                    const bool rot = my.unit[k] < p.rot_units;
+                    if (p.norm) run_scale<2 * VE>(e, r);
 #pragma unroll
                     for (int q = 0; q < VE; q += N) {
-                        float w0[N], w1[N];
-                        read_table<N>(wu + table_at<VE>(0, q), w0);
-                        read_table<N>(wu + kRopeTable + table_at<VE>(0, q), w1);
-                        weigh_pairs<VE, IL, N>(e, q, w0, w1, r);
+                        float *a = e + run_a<VE, IL>(q), *b = e + run_b<VE, IL>(q), f[N], g[N];
+                        read_table<N>(wu + table_at<VE>(0, q), f);
+                        read_table<N>(wu + kRopeTable + table_at<VE>(0, q), g);
+                        run_times<N>(a, f);
+                        run_times<N>(b, g);
                     }
-                    if (my.unit[k] < p.rot_units) {
+                    if (rot) {
 #pragma unroll
                         for (int q = 0; q < VE; q += N) {
-                            float c[N], s[N];
-                            read_table<N>(cu + table_at<VE>(0, q), c);
-                            read_table<N>(cu + kRopeTable + table_at<VE>(0, q), s);
-                            turn_pairs<VE, IL, N>(e, q, c, s);
+                            float *a = e + run_a<VE, IL>(q), *b = e + run_b<VE, IL>(q), f[N], g[N];
+                            read_table<N>(cu + table_at<VE>(0, q), f);
+                            read_table<N>(cu + kRopeTable + table_at<VE>(0, q), g);
+                            turn_runs<IL, false, N>(a, b, f, g);
                         }
                     }
                 }
@@ -667,19 +727,22 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(VE, K)) rope
 }
 
 // ---------------------------------------------------------------- gradient
-// Blocks 0 .. q_blocks - 1 take the query heads, the rest the key heads, an
-// equal run of tokens each.  A thread keeps its units' share of the weight's
-// gradient in registers; the block's sum goes to partial[block][D], and the
-// blocks' are added up by another kernel.  The order of every sum follows
-// from the sizes and the grid: no atomics.
+// A block's first q_warps warps take its tokens' query heads, the rest the
+// key heads (so a thread keeps one kind's share of the weight's gradient in
+// registers and both kinds share the tokens' angles: with blocks of one kind
+// each token's were made twice, 62.5 against XXX us for bf16 8192 tokens x 40
+// heads of 128).  The block's sums go to partial[kind][block][D], and the
+// blocks' are added up by another kernel.  The order of every sum follows from
+// the sizes and the grid: no atomics.
 // x is read only with the norm; without it dx = dy turned back.
 template <typename T, int VE, int K, bool IL, bool NORM>
-__global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(VE, K)) rope_bwd_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(Piece<T, VE>::kBytes, K)) rope_bwd_kernel(const RopeParams p) {
     using P = Piece<T, VE>;
     using Raw = typename P::Raw;
     constexpr int S = (int)sizeof(typename T::storage);
     constexpr int N = pairs_at_once(VE);
     constexpr int KN = NORM ? K : 1;
+    constexpr bool ASYNC = P::kBytes >= 4;
     extern __shared__ __align__(16) unsigned char smem[];
     uint64_t *frac = reinterpret_cast<uint64_t *>(smem);
     float *wsm = reinterpret_cast<float *>(smem + 8 * kRopeTable);
@@ -689,10 +752,11 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(VE, K)) 
     const uint32_t head_bytes = (uint32_t)(p.head_dim * S);
     Lane<VE, K, IL, S> my;
     my.set(p, t, group);
-    const bool key = (int)blockIdx.x >= p.q_blocks;
+    const bool key = warp >= p.q_warps;
     const int heads = key ? p.k_heads : p.q_heads, iters = key ? p.iters_k : p.iters;
+    const int mates = key ? kRopeMaxWarps - p.q_warps : p.q_warps;   // warps of the kind
     Jobs jobs;
-    jobs.set(key ? blockIdx.x - p.q_blocks : blockIdx.x, key ? p.each_k : p.each, key ? p.extra_k : p.extra);
+    jobs.set(blockIdx.x, p.each, p.extra);
     const uint32_t head0 = key ? (uint32_t)p.q_heads * head_bytes : 0u;
     const float *w = wsm + (key ? 2 * kRopeTable : 0);
 
@@ -705,6 +769,16 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(VE, K)) 
 #pragma unroll
         for (int v = 0; v < 2 * VE; ++v) gw[k][v] = 0.f;
 
+    int64_t pos = 0;   // of the warp's token of a tile: axis a's in lane a
+    // A thread's own places of the ring [stage][dy a, dy b, x a, x b][K], where
+    // pieces are wide enough to be copied asynchronously.
+    Raw da[K], db[K], xa[KN], xb[KN];
+    int stage = 0;
+    auto place = [&](int piece, int k) {
+        return reinterpret_cast<char *>(tiles + 2 * kRopeMaxWarps * 2 * kRopeTable) +
+               ((((stage * (NORM ? 4 : 2) + piece) * K + k) * 32 * kRopeMaxWarps) + (int)threadIdx.x) * P::kBytes;
+    };
+
     bool prepared = false;
     int buf = 0;
     for (int64_t base = jobs.first; base < jobs.last; base += p.tile, buf ^= 1) {
@@ -712,9 +786,8 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(VE, K)) 
         const char *tg = static_cast<const char *>(p.dy) + base * p.dy_stride + head0;
         const char *tx = static_cast<const char *>(p.x) + base * p.x_stride + head0;
         char *ty = static_cast<char *>(p.y) + base * p.y_stride + head0;
-        Tile at{0, warp};
+        Tile at{0, key ? warp - p.q_warps : warp};
         at.settle(n, iters);
-        Raw da[K], db[K], xa[KN], xb[KN];
         auto load = [&]() {
             int h = at.i * hpw + group;
             h = h < heads ? h : heads - 1;
@@ -722,38 +795,67 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(VE, K)) 
             const uint32_t xo = (uint32_t)at.j * (uint32_t)p.x_stride + (uint32_t)h * head_bytes;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                da[k] = P::load(tg + (go + my.oa[k]));
-                db[k] = P::load(tg + (go + my.ob[k]));
-                if constexpr (NORM) {
-                    xa[k] = P::load(tx + (xo + my.oa[k]));
-                    xb[k] = P::load(tx + (xo + my.ob[k]));
+                if constexpr (ASYNC) {
+                    P::copy(place(0, k), tg + (go + my.oa[k]));
+                    P::copy(place(1, k), tg + (go + my.ob[k]));
+                    if constexpr (NORM) {
+                        P::copy(place(2, k), tx + (xo + my.oa[k]));
+                        P::copy(place(3, k), tx + (xo + my.ob[k]));
+                    }
+                } else {
+                    da[k] = P::load(tg + (go + my.oa[k]));
+                    db[k] = P::load(tg + (go + my.ob[k]));
+                    if constexpr (NORM) {
+                        xa[k] = P::load(tx + (xo + my.oa[k]));
+                        xb[k] = P::load(tx + (xo + my.ob[k]));
+                    }
                 }
             }
         };
         if (at.j < n) load();
+        if constexpr (ASYNC) copy_async_commit();
         if (!prepared) {
+            if (base + warp < jobs.last) pos = lane_position(p, lane, base + warp);
             make_fractions<VE>(p, frac);
             if constexpr (NORM) make_weights<T, VE, IL>(p, wsm);
             __syncthreads();
             prepared = true;
         }
         if (warp < n)
-            make_angles<VE>(p, frac, tiles + (buf * kRopeMaxWarps + warp) * 2 * kRopeTable, lane,
-                            lane_position(p, lane, base + warp));
+            make_angles<VE, IL>(p, frac, tiles + (buf * kRopeMaxWarps + warp) * 2 * kRopeTable, lane, pos);
+        if (base + p.tile + warp < jobs.last) pos = lane_position(p, lane, base + p.tile + warp);   // the next tile's
         __syncthreads();   // two buffers: the tile before this one may still be read
         while (at.j < n) {
             Raw ea[K], eb[K], ya[KN], yb[KN];
+            if constexpr (!ASYNC) {
 #pragma unroll
-            for (int k = 0; k < K; ++k) ea[k] = da[k], eb[k] = db[k];
+                for (int k = 0; k < K; ++k) ea[k] = da[k], eb[k] = db[k];
 #pragma unroll
-            for (int k = 0; k < KN; ++k) ya[k] = xa[k], yb[k] = xb[k];
+                for (int k = 0; k < KN; ++k) ya[k] = xa[k], yb[k] = xb[k];
+            }
             const int job = at.j, h = at.i * hpw + group;
-            at.i += kRopeMaxWarps;
+            at.i += mates;
             at.settle(n, iters);
+            stage ^= 1;
             if (at.j < n) load();   // the next heads are on their way
+            if constexpr (ASYNC) {
+                copy_async_commit();
+                copy_async_wait<1>();   // these heads are there
+                stage ^= 1;
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    ea[k] = P::take(place(0, k));
+                    eb[k] = P::take(place(1, k));
+                    if constexpr (NORM) {
+                        ya[k] = P::take(place(2, k));
+                        yb[k] = P::take(place(3, k));
+                    }
+                }
+                stage ^= 1;
+            }
             const float *cs = tiles + (buf * kRopeMaxWarps + job) * 2 * kRopeTable;
 
-            float g[K][2 * VE];
+            float g[K][2 * VE], x[KN][2 * VE];
             float sums[2] = {0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < K; ++k) {
@@ -762,69 +864,62 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(VE, K)) 
                 if (my.unit[k] < p.rot_units) {
 #pragma unroll
                     for (int q = 0; q < VE; q += N) {
-                        float c[N], s[N];
-                        read_table<N>(cu + table_at<VE>(0, q), c);
-                        read_table<N>(cu + kRopeTable + table_at<VE>(0, q), s);
-#pragma unroll
-                        for (int v = 0; v < N; ++v) s[v] = -s[v];
-                        turn_pairs<VE, IL, N>(g[k], q, c, s);
+                        float f[N], h2[N];
+                        read_table<N>(cu + table_at<VE>(0, q), f);
+                        read_table<N>(cu + kRopeTable + table_at<VE>(0, q), h2);
+                        turn_runs<IL, true, N>(g[k] + run_a<VE, IL>(q), g[k] + run_b<VE, IL>(q), f, h2);
                     }
                 }
                 if constexpr (NORM) {
-                    float x[2 * VE];
-                    widen_unit<T, VE>(ya[k], yb[k], x);
+                    widen_unit<T, VE>(ya[k], yb[k], x[k]);
                     float2 sq = make_float2(0.f, 0.f), dot = sq;
-                    squares_into<2 * VE>(sq, x);
+                    run_dot<2 * VE>(sq, x[k], x[k]);
 #pragma unroll
                     for (int q = 0; q < VE; q += N) {
-                        float w0[N], w1[N];
-                        read_table<N>(wu + table_at<VE>(0, q), w0);
-                        read_table<N>(wu + kRopeTable + table_at<VE>(0, q), w1);
-#pragma unroll
-                        for (int v = 0; v < N; ++v) {
-                            const int a = first_of<VE, IL>(q + v), b = second_of<VE, IL>(q + v);
-                            dot = __ffma2_rn(__fmul2_rn(make_float2(g[k][a], g[k][b]), make_float2(w0[v], w1[v])),
-                                             make_float2(x[a], x[b]), dot);
-                        }
+                        const int a = run_a<VE, IL>(q), b = run_b<VE, IL>(q);
+                        float f[N], h2[N];
+                        read_table<N>(wu + table_at<VE>(0, q), f);
+                        read_table<N>(wu + kRopeTable + table_at<VE>(0, q), h2);
+                        run_times<N>(f, reinterpret_cast<const float(&)[N]>(g[k][a]));
+                        run_times<N>(h2, reinterpret_cast<const float(&)[N]>(g[k][b]));
+                        run_dot<N>(dot, f, x[k] + a);
+                        run_dot<N>(dot, h2, x[k] + b);
                     }
                     sums[0] += my.act[k] ? sq.x + sq.y : 0.f;
                     sums[1] += my.act[k] ? dot.x + dot.y : 0.f;
                 }
             }
-            float r = 1.f, mean = 0.f;
             if constexpr (NORM) {
                 lanes_sum<2>(sums, G, t, lane);
-                r = rsqrtf(fmaf(sums[0], p.inv_dim, p.eps));
-                mean = -(sums[1] * p.inv_dim) * r;   // dx = r (w g - (x r) mean)
+                const float r = rsqrtf(fmaf(sums[0], p.inv_dim, p.eps));
+                const float mean = -(sums[1] * p.inv_dim) * r;   // dx = r (w g - (x r) mean)
+                float mm[2 * VE];
+#pragma unroll
+                for (int v = 0; v < 2 * VE; ++v) mm[v] = mean;
+#pragma unroll
+                for (int k = 0; k < K; ++k) run_scale<2 * VE>(x[k], r);
+                if (h < heads) {   // an idle head's copy adds nothing
+#pragma unroll
+                    for (int k = 0; k < K; ++k) run_fma<2 * VE>(gw[k], g[k], x[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const float *wu = w + table_at<VE>(my.unit[k], 0);
+#pragma unroll
+                    for (int q = 0; q < VE; q += N) {
+                        float f[N], h2[N];
+                        read_table<N>(wu + table_at<VE>(0, q), f);
+                        read_table<N>(wu + kRopeTable + table_at<VE>(0, q), h2);
+                        run_times<N>(g[k] + run_a<VE, IL>(q), f);
+                        run_times<N>(g[k] + run_b<VE, IL>(q), h2);
+                    }
+                    run_fma<2 * VE>(g[k], x[k], mm);
+                    run_scale<2 * VE>(g[k], r);
+                }
             }
             char *dst = ty + ((uint32_t)job * (uint32_t)p.y_stride + (uint32_t)h * head_bytes);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                if constexpr (NORM) {
-                    float x[2 * VE];
-                    widen_unit<T, VE>(ya[k], yb[k], x);
-                    const float *wu = w + table_at<VE>(my.unit[k], 0);
-#pragma unroll
-                    for (int q = 0; q < VE; q += N) {
-                        float w0[N], w1[N];
-                        read_table<N>(wu + table_at<VE>(0, q), w0);
-                        read_table<N>(wu + kRopeTable + table_at<VE>(0, q), w1);
-#pragma unroll
-                        for (int v = 0; v < N; ++v) {
-                            const int a = first_of<VE, IL>(q + v), b = second_of<VE, IL>(q + v);
-                            const float2 xr = __fmul2_rn(make_float2(x[a], x[b]), make_float2(r, r));
-                            const float2 gv = make_float2(g[k][a], g[k][b]);
-                            if (h < heads) {   // an idle head's copy adds nothing
-                                const float2 acc = __ffma2_rn(gv, xr, make_float2(gw[k][a], gw[k][b]));
-                                gw[k][a] = acc.x, gw[k][b] = acc.y;
-                            }
-                            const float2 d = __fmul2_rn(
-                                __ffma2_rn(xr, make_float2(mean, mean), __fmul2_rn(gv, make_float2(w0[v], w1[v]))),
-                                make_float2(r, r));
-                            g[k][a] = d.x, g[k][b] = d.y;
-                        }
-                    }
-                }
                 if (h < heads && my.act[k]) {
                     float u[VE], v[VE];
 #pragma unroll
@@ -849,7 +944,7 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(VE, K)) 
             if (group == 0) {
 #pragma unroll
                 for (int k = 0; k < K; ++k)
-                    if (my.act[k])
+                    if (my.act[k] && heads > 0)
 #pragma unroll
                         for (int v = 0; v < VE; ++v) {
                             wsm[warp * p.head_dim + my.oa[k] / S + v] = gw[k][v];
@@ -857,11 +952,12 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(VE, K)) 
                         }
             }
             __syncthreads();
-            float *out = p.partial + (int64_t)blockIdx.x * p.head_dim;
-            for (int d = threadIdx.x; d < p.head_dim; d += blockDim.x) {
+            for (int i = threadIdx.x; i < 2 * p.head_dim; i += blockDim.x) {
+                const int kind = i >= p.head_dim, d = i - kind * p.head_dim;
                 float v = 0.f;
-                for (int k = 0; k < kRopeMaxWarps; ++k) v += wsm[k * p.head_dim + d];
-                out[d] = v;
+                for (int k = kind ? p.q_warps : 0; k < (kind ? kRopeMaxWarps : p.q_warps); ++k)
+                    v += wsm[k * p.head_dim + d];
+                p.partial[((int64_t)kind * gridDim.x + blockIdx.x) * p.head_dim + d] = v;
             }
         }
     }

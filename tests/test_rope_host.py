@@ -56,14 +56,14 @@ def test_rope_limits_and_empty_batches_without_cuda():
 
 def bwd(dy=P, x=P, dx=P, tokens=4, gs=768, xs=768, ds=768, q=8, k=4, d=64, qw=P, kw=P, dqw=P, dkw=P, bias=0.0,
         eps=1e-6, norm=1, r="default", dtype=1, ws=P, wb=None):
-    wb = 1024 * 64 * 4 if wb is None else wb
+    wb = 1024 * 2 * 64 * 4 if wb is None else wb
     return N.rmsnorm_qk_rope_bwd_status(dy, x, dx, tokens, gs, xs, ds, q, k, d, qw, kw, dqw, dkw, bias, eps, norm,
                                         rope() if r == "default" else r, dtype, ws, wb)
 
 
 @pytest.mark.parametrize("over", [
     dict(dy=None), dict(x=None), dict(dx=None), dict(gs=767), dict(xs=767), dict(ds=767), dict(dqw=None),
-    dict(dkw=None), dict(qw=None, kw=None), dict(ws=None), dict(ws=P + 8), dict(wb=1024 * 64 * 4 - 1),
+    dict(dkw=None), dict(qw=None, kw=None), dict(ws=None), dict(ws=P + 8), dict(wb=1024 * 2 * 64 * 4 - 1),
     dict(norm=0), dict(dqw=P + 1), dict(gs=800), dict(xs=800), dict(dy=P + 1), dict(r=rope(positions=None)),
     dict(tokens=-1), dict(d=62, r=rope(rot_dim=64)),
 ])
@@ -72,7 +72,7 @@ def test_rope_gradient_refusals_without_cuda(over):
 
 
 def test_rope_gradient_workspace_bytes():
-    assert R.rmsnorm_qk_rope_bwd_workspace_bytes(64) == 1024 * 64 * 4
+    assert R.rmsnorm_qk_rope_bwd_workspace_bytes(64) == 1024 * 2 * 64 * 4
     for bad in (0, -2, 63):
         with pytest.raises(N.RmsNormError):
             R.rmsnorm_qk_rope_bwd_workspace_bytes(bad)
