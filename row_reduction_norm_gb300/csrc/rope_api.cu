@@ -124,8 +124,11 @@ bool tile_reaches(int64_t a, int64_t b, int64_t c) {
     return a <= most && b <= most && c <= most;
 }
 
-const void *forward_kernel(int dtype, int shape, bool il, int mode) {
-    return dtype == RMSNORM_BF16 ? rrn::rope_fwd_bf16(shape, il, mode) : rrn::rope_fwd_f32(shape, il, mode);
+int whole_head(const rrn::RopeParams *p) { return 2 * p->R == p->head_dim ? p->head_dim : 0; }
+
+const void *forward_kernel(int dtype, int shape, bool il, int mode, int whole) {
+    return dtype == RMSNORM_BF16 ? rrn::rope_fwd_bf16(shape, il, mode, whole)
+                                 : rrn::rope_fwd_f32(shape, il, mode, whole);
 }
 
 int launch_forward(rrn::RopeParams *p, int dtype, int64_t unit, bool il, int mode, rmsnorm_stream_t stream) {
@@ -133,7 +136,7 @@ int launch_forward(rrn::RopeParams *p, int dtype, int64_t unit, bool il, int mod
     int st = rrn::current_device_sms(&dev, &sms);
     if (st != RMSNORM_OK) return st;
     const int shape = pick_shape(dtype, unit, p);
-    const void *fn = forward_kernel(dtype, shape, il, mode);
+    const void *fn = forward_kernel(dtype, shape, il, mode, whole_head(p));
     if (fn == nullptr) return RMSNORM_EINVAL;
     // A run of jobs for every resident block.  A job is a token's heads; with
     // fewer tokens than blocks it is a slice of them, one head iteration a
@@ -233,8 +236,8 @@ int rmsnorm_qk_rope_bwd(const void *dy, const void *x, void *dx, int64_t tokens,
         if ((st = rrn::current_device_sms(&dev, &sms)) != RMSNORM_OK) return st;
         const int shape = pick_shape(dtype, u.get(), &p);
         const bool il = rope->interleaved == 1;
-        const void *fn = dtype == RMSNORM_BF16 ? rrn::rope_bwd_bf16(shape, il, norm == 1)
-                                               : rrn::rope_bwd_f32(shape, il, norm == 1);
+        const void *fn = dtype == RMSNORM_BF16 ? rrn::rope_bwd_bf16(shape, il, norm == 1, whole_head(&p))
+                                               : rrn::rope_bwd_f32(shape, il, norm == 1, whole_head(&p));
         if (fn == nullptr) return RMSNORM_EINVAL;
         p.iters = (int32_t)div_up(q_heads, p.heads_a_warp);
         p.iters_k = (int32_t)div_up(k_heads, p.heads_a_warp);

@@ -5,15 +5,23 @@
 namespace rrn {
 namespace {
 
-template <typename T, int VE, int K, bool IL>
+template <typename T, int VE, int K, bool IL, int HD = 0>
 const void *one(bool norm) {
-    return norm ? reinterpret_cast<const void *>(&rope_bwd_kernel<T, VE, K, IL, true>)
-                : reinterpret_cast<const void *>(&rope_bwd_kernel<T, VE, K, IL, false>);
+    return norm ? reinterpret_cast<const void *>(&rope_bwd_kernel<T, VE, K, IL, true, HD>)
+                : reinterpret_cast<const void *>(&rope_bwd_kernel<T, VE, K, IL, false, HD>);
 }
 
 }  // namespace
 
-const void *rope_bwd_bf16(int shape, bool il, bool norm) {
+const void *rope_bwd_bf16(int shape, bool il, bool norm, int whole) {
+    if (shape == 0) {
+        switch (whole) {
+            case 64: return il ? one<BF16, 8, 1, true, 64>(norm) : one<BF16, 8, 1, false, 64>(norm);
+            case 128: return il ? one<BF16, 8, 1, true, 128>(norm) : one<BF16, 8, 1, false, 128>(norm);
+            case 256: return il ? one<BF16, 8, 1, true, 256>(norm) : one<BF16, 8, 1, false, 256>(norm);
+            default: break;
+        }
+    }
     switch (shape) {
         case 0: return il ? one<BF16, 8, 1, true>(norm) : one<BF16, 8, 1, false>(norm);
         case 1: return il ? one<BF16, 4, 1, true>(norm) : one<BF16, 4, 1, false>(norm);

@@ -5,12 +5,12 @@
 namespace rrn {
 namespace {
 
-template <typename T, int VE, int K, bool IL>
+template <typename T, int VE, int K, bool IL, int HD = 0>
 const void *one(int mode) {
     switch (mode) {
-        case kRopePlain: return reinterpret_cast<const void *>(&rope_kernel<T, VE, K, IL, kRopePlain>);
-        case kRopeAppend: return reinterpret_cast<const void *>(&rope_kernel<T, VE, K, IL, kRopeAppend>);
-        case kRopeAppendE4m3: return reinterpret_cast<const void *>(&rope_kernel<T, VE, K, IL, kRopeAppendE4m3>);
+        case kRopePlain: return reinterpret_cast<const void *>(&rope_kernel<T, VE, K, IL, kRopePlain, HD>);
+        case kRopeAppend: return reinterpret_cast<const void *>(&rope_kernel<T, VE, K, IL, kRopeAppend, HD>);
+        case kRopeAppendE4m3: return reinterpret_cast<const void *>(&rope_kernel<T, VE, K, IL, kRopeAppendE4m3, HD>);
         default: return nullptr;
     }
 }
@@ -22,7 +22,15 @@ const void *mode_of(bool il, int mode) {
 
 }  // namespace
 
-const void *rope_fwd_bf16(int shape, bool il, int mode) {
+const void *rope_fwd_bf16(int shape, bool il, int mode, int whole) {
+    if (shape == 0) {
+        switch (whole) {
+            case 64: return il ? one<BF16, 8, 1, true, 64>(mode) : one<BF16, 8, 1, false, 64>(mode);
+            case 128: return il ? one<BF16, 8, 1, true, 128>(mode) : one<BF16, 8, 1, false, 128>(mode);
+            case 256: return il ? one<BF16, 8, 1, true, 256>(mode) : one<BF16, 8, 1, false, 256>(mode);
+            default: break;
+        }
+    }
     switch (shape) {
         case 0: return mode_of<BF16, 8, 1>(il, mode);
         case 1: return mode_of<BF16, 4, 1>(il, mode);

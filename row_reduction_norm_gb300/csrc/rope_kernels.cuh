@@ -480,18 +480,28 @@ enum RopeMode { kRopePlain = 0, kRopeAppend = 1, kRopeAppendE4m3 = 2 };
 // A lane's units of a head: where their pieces start (bytes), and which exist.
 // Lanes without a unit take unit 0's place (they load it like a neighbour: no
 // branch, no zeroing) and have no part in sums and stores.
-template <int VE, int K, bool IL, int S>
+// HD: a head size known at compile time (whole heads turned, a power of two
+// of lanes a head, K = 1): every lane has a unit, the pieces a fixed distance.
+template <int VE, int K, bool IL, int S, int HD>
 struct Lane {
     int oa[K], ob[K], unit[K];
-    bool act[K];
+    bool act[K], rot[K];
     __device__ __forceinline__ void set(const RopeParams &p, int t, int group) {
+        if constexpr (HD > 0) {
+            unit[0] = t;
+            act[0] = rot[0] = true;
+            oa[0] = (IL ? 2 * t * VE : t * VE) * S;
+            ob[0] = oa[0] + (IL ? VE : HD / 2) * S;
+        } else {
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            act[k] = t + k * p.lanes < p.units && group < p.heads_a_warp;
-            unit[k] = act[k] ? t + k * p.lanes : 0;
-            unit_offsets<VE, IL>(p, unit[k], oa[k], ob[k]);
-            oa[k] *= S;
-            ob[k] *= S;
+            for (int k = 0; k < K; ++k) {
+                act[k] = t + k * p.lanes < p.units && group < p.heads_a_warp;
+                unit[k] = act[k] ? t + k * p.lanes : 0;
+                rot[k] = unit[k] < p.rot_units;
+                unit_offsets<VE, IL>(p, unit[k], oa[k], ob[k]);
+                oa[k] *= S;
+                ob[k] *= S;
+            }
         }
     }
 };
@@ -567,7 +577,7 @@ struct Tile {
 };
 
 // ----------------------------------------------------------------- forward
-template <typename T, int VE, int K, bool IL, int MODE>
+template <typename T, int VE, int K, bool IL, int MODE, int HD>
 __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(Piece<T, VE>::kBytes, K)) rope_kernel(const RopeParams p) {
     using P = Piece<T, VE>;
     using Raw = typename P::Raw;
@@ -581,10 +591,11 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(Piece<T, VE>
     float *tiles = wsm + 4 * kRopeTable;
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int G = p.lanes, group = lane / G, t = lane - group * G, hpw = p.heads_a_warp;
+    const int G = HD ? HD / 2 / VE : p.lanes, group = lane / G, t = lane - group * G;
+    const int hpw = HD ? 32 / G : p.heads_a_warp;
     const int heads = p.q_heads + p.k_heads + p.v_heads, turned = p.q_heads + p.k_heads;
-    const uint32_t head_bytes = (uint32_t)(p.head_dim * S);
-    Lane<VE, K, IL, S> my;
+    const uint32_t head_bytes = (uint32_t)((HD ? HD : p.head_dim) * S);
+    Lane<VE, K, IL, S, HD> my;
     my.set(p, t, group);
     Jobs jobs;
     jobs.set(blockIdx.x, p.each, p.extra);
@@ -629,8 +640,9 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(Piece<T, VE>
             const uint32_t off = (uint32_t)at.j * (uint32_t)p.x_stride + (uint32_t)h * head_bytes;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                ra[k] = P::load(tx + (off + my.oa[k]));
-                rb[k] = P::load(tx + (off + my.ob[k]));
+                const char *src = tx + (off + my.oa[k]);
+                ra[k] = P::load(src);
+                rb[k] = P::load(src + (HD ? (IL ? VE : HD / 2) * S : my.ob[k] - my.oa[k]));
             }
         };
         if (at.j < n) load();
@@ -688,7 +700,7 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(Piece<T, VE>
                 widen_unit<T, VE>(ca[k], cb[k], e);
                 if (!value) {
                     const float *wu = w + table_at<VE>(my.unit[k], 0), *cu = cs + table_at<VE>(my.unit[k], 0);
-                    const bool rot = my.unit[k] < p.rot_units;
+                    const bool rot = my.rot[k];
                     if (p.norm) run_scale<2 * VE>(e, r);
 #pragma unroll
                     for (int q = 0; q < VE; q += N) {
@@ -712,13 +724,16 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(Piece<T, VE>
                     float x[VE], y[VE];
 #pragma unroll
                     for (int v = 0; v < VE; ++v) x[v] = e[v], y[v] = e[VE + v];
+                    const int d = HD ? (IL ? VE : HD / 2) * S : my.ob[k] - my.oa[k];
                     if (MODE == kRopeAppendE4m3 && key) {
                         const float inv = value ? p.v_inv : p.k_inv;
-                        P::store_e4m3(dst + my.oa[k] / S, x, inv);
-                        P::store_e4m3(dst + my.ob[k] / S, y, inv);
+                        char *to = dst + my.oa[k] / S;
+                        P::store_e4m3(to, x, inv);
+                        P::store_e4m3(to + d / S, y, inv);
                     } else {
-                        P::store(dst + my.oa[k], x);
-                        P::store(dst + my.ob[k], y);
+                        char *to = dst + my.oa[k];
+                        P::store(to, x);
+                        P::store(to + d, y);
                     }
                 }
             }
@@ -735,7 +750,7 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(Piece<T, VE>
 // blocks' are added up by another kernel.  The order of every sum follows from
 // the sizes and the grid: no atomics.
 // x is read only with the norm; without it dx = dy turned back.
-template <typename T, int VE, int K, bool IL, bool NORM>
+template <typename T, int VE, int K, bool IL, bool NORM, int HD>
 __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(Piece<T, VE>::kBytes, K)) rope_bwd_kernel(const RopeParams p) {
     using P = Piece<T, VE>;
     using Raw = typename P::Raw;
@@ -748,9 +763,10 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(Piece<T,
     float *wsm = reinterpret_cast<float *>(smem + 8 * kRopeTable);
     float *tiles = wsm + 4 * kRopeTable;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int G = p.lanes, group = lane / G, t = lane - group * G, hpw = p.heads_a_warp;
-    const uint32_t head_bytes = (uint32_t)(p.head_dim * S);
-    Lane<VE, K, IL, S> my;
+    const int G = HD ? HD / 2 / VE : p.lanes, group = lane / G, t = lane - group * G;
+    const int hpw = HD ? 32 / G : p.heads_a_warp;
+    const uint32_t head_bytes = (uint32_t)((HD ? HD : p.head_dim) * S);
+    Lane<VE, K, IL, S, HD> my;
     my.set(p, t, group);
     const bool key = warp >= p.q_warps;
     const int heads = key ? p.k_heads : p.q_heads, iters = key ? p.iters_k : p.iters;
@@ -796,11 +812,13 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(Piece<T,
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 if constexpr (ASYNC) {
-                    P::copy(place(0, k), tg + (go + my.oa[k]));
-                    P::copy(place(1, k), tg + (go + my.ob[k]));
+                    const int d = HD ? (IL ? VE : HD / 2) * S : my.ob[k] - my.oa[k];
+                    const char *ga = tg + (go + my.oa[k]), *at_x = tx + (xo + my.oa[k]);
+                    P::copy(place(0, k), ga);
+                    P::copy(place(1, k), ga + d);
                     if constexpr (NORM) {
-                        P::copy(place(2, k), tx + (xo + my.oa[k]));
-                        P::copy(place(3, k), tx + (xo + my.ob[k]));
+                        P::copy(place(2, k), at_x);
+                        P::copy(place(3, k), at_x + d);
                     }
                 } else {
                     da[k] = P::load(tg + (go + my.oa[k]));
@@ -861,7 +879,7 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(Piece<T,
             for (int k = 0; k < K; ++k) {
                 widen_unit<T, VE>(ea[k], eb[k], g[k]);
                 const float *wu = w + table_at<VE>(my.unit[k], 0), *cu = cs + table_at<VE>(my.unit[k], 0);
-                if (my.unit[k] < p.rot_units) {
+                if (my.rot[k]) {
 #pragma unroll
                     for (int q = 0; q < VE; q += N) {
                         float f[N], h2[N];
@@ -924,8 +942,9 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(Piece<T,
                     float u[VE], v[VE];
 #pragma unroll
                     for (int e = 0; e < VE; ++e) u[e] = g[k][e], v[e] = g[k][VE + e];
-                    P::store(dst + my.oa[k], u);
-                    P::store(dst + my.ob[k], v);
+                    char *to = dst + my.oa[k];
+                    P::store(to, u);
+                    P::store(to + (HD ? (IL ? VE : HD / 2) * S : my.ob[k] - my.oa[k]), v);
                 }
             }
         }
