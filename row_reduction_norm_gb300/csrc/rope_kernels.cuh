@@ -445,21 +445,16 @@ __device__ __forceinline__ void make_weights(const RopeParams &p, float *wsm) {
 
 // ------------------------------------------------------------ paged cache
 
-// The sequence of a token: the last s with cu_tokens[s] <= token, found by
-// the whole warp 32 ways at a time (a batch of single tokens, where token t
-// is sequence t's, is seen at once).  Whatever cu_tokens holds, the answer is
-// in [0, seqs).
-__device__ __forceinline__ int sequence_of(const RopeParams &p, int64_t token, int lane) {
+// The sequence of a token: the last s with cu_tokens[s] <= token, by halving
+// (a batch of single tokens, where token t is sequence t's, is seen at once).
+// Whatever cu_tokens holds, the answer is in [0, seqs).
+__device__ __forceinline__ int sequence_of(const RopeParams &p, int64_t token) {
     if (token < p.seqs && p.cu_tokens[token] <= token && token < p.cu_tokens[token + 1]) return (int)token;
     int lo = 0, hi = p.seqs;
     while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32;
-        const int64_t i = lo + (int64_t)lane * step;
-        const bool in = i < hi && p.cu_tokens[i] <= token;
-        const int n = __popc(__ballot_sync(0xffffffffu, in));
-        const int next = lo + (n > 0 ? n - 1 : 0) * step;
-        hi = hi - next < step ? hi : next + step;
-        lo = next;
+        const int mid = lo + (hi - lo) / 2;
+        if (p.cu_tokens[mid] <= token) lo = mid;
+        else hi = mid;
     }
     return lo;
 }
@@ -585,7 +580,10 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(Piece<T, VE>
     constexpr int N = pairs_at_once(VE);
     constexpr bool APPEND = MODE != kRopePlain;
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ int64_t rows[2][kRopeMaxWarps];   // append: where the tile's tokens go, -1: nowhere
+    // append: where the tokens of kLookUps jobs go (-1: nowhere), and their
+    // indices in their sequences, looked up a thread each
+    constexpr int kLookUps = 8 * kRopeMaxWarps;
+    __shared__ int64_t rows[APPEND ? kLookUps : 1], indices[APPEND ? kLookUps : 1];
     uint64_t *frac = reinterpret_cast<uint64_t *>(smem);
     float *wsm = reinterpret_cast<float *>(smem + 8 * kRopeTable);
     float *tiles = wsm + 4 * kRopeTable;
@@ -608,18 +606,15 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(Piece<T, VE>
         if (jobs.last > most) jobs.last = most;
     }
 
-    // the warp's token of a tile: axis a's position in lane a, its cache row
-    int64_t pos = 0, row_of_mine = -1;
-    auto look_up = [&](int64_t base) {
-        const int64_t job = base + (p.tile > 1 ? warp : 0);
-        if (job < jobs.last && (warp == 0 || p.tile > 1)) {
-            const int64_t mine = p.slices > 1 ? job / p.slices : job;
-            if constexpr (APPEND) {
-                const int seq = sequence_of(p, mine, lane);
-                pos = (int64_t)p.cache_lens[seq] + (mine - p.cu_tokens[seq]);
-                row_of_mine = cache_row(p, seq, pos);
-            }
-            if (!APPEND || p.pos != nullptr) pos = lane_position(p, lane, mine);
+    int64_t known = jobs.first;   // first of the jobs looked up
+    auto look_up = [&]() {
+        const int64_t job = known + threadIdx.x;
+        if (threadIdx.x < kLookUps && job < jobs.last) {
+            const int64_t token = p.slices > 1 ? job / p.slices : job;
+            const int seq = sequence_of(p, token);
+            const int64_t index = (int64_t)p.cache_lens[seq] + (token - p.cu_tokens[seq]);
+            indices[threadIdx.x] = index;
+            rows[threadIdx.x] = cache_row(p, seq, index);
         }
     };
 
@@ -646,19 +641,25 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(Piece<T, VE>
             }
         };
         if (at.j < n) load();
+        if (APPEND && base - known >= kLookUps) {
+            __syncthreads();   // what was looked up before is read
+            known = base;
+            look_up();
+            __syncthreads();
+        }
         if (!prepared) {
-            look_up(base);
+            if constexpr (APPEND) look_up();
             make_fractions<VE>(p, frac);
             make_weights<T, VE, IL>(p, wsm);
             __syncthreads();
             prepared = true;
         }
-        // the warp's own token of the tile: where it goes, its angles
-        if (warp < n) {
-            if (APPEND && lane == 0) rows[buf][warp] = row_of_mine;
+        if (warp < n) {   // the warp's own token of the tile
+            int64_t pos = 0;
+            if (!APPEND || p.pos != nullptr) pos = lane_position(p, lane, token0 + warp);
+            else pos = indices[base - known + warp];
             make_angles<VE, IL>(p, frac, tiles + (buf * kRopeMaxWarps + warp) * 2 * kRopeTable, lane, pos);
         }
-        look_up(base + p.tile);   // the next tile's, while this one is worked on
         __syncthreads();   // two buffers: the tile before this one may still be read
         while (at.j < n) {
             Raw ca[K], cb[K];
@@ -688,7 +689,7 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(Piece<T, VE>
             char *dst = ty + ((uint32_t)job * (uint32_t)p.y_stride + (uint32_t)h * head_bytes);
             bool store = h < heads;
             if (APPEND && key) {
-                const int64_t row = rows[buf][job];
+                const int64_t row = rows[base - known + job];
                 const int o = value ? h - turned : h - p.q_heads;
                 dst = static_cast<char *>(value ? p.v_cache : p.k_cache) + row + (int64_t)o * p.head_stride;
                 store = store && row >= 0;

@@ -142,17 +142,17 @@ class Bounded:
 
 
 def sequence_of(cu, seqs, token):
-    """The kernel's search, its 32 lanes one after another."""
+    """The kernel's search."""
     if token < seqs and cu[token] <= token and token < cu[token + 1]:
         return token
     lo, hi = 0, seqs
     while hi - lo > 1:
-        step = (hi - lo + 31) // 32
-        n = sum(1 for lane in range(32) if lo + lane * step < hi and cu[lo + lane * step] <= token)
-        nxt = lo + (n - 1 if n > 0 else 0) * step
-        hi = hi if hi - nxt < step else nxt + step
-        lo = nxt
-        assert 0 <= lo < hi <= seqs
+        mid = lo + (hi - lo) // 2
+        if cu[mid] <= token:
+            lo = mid
+        else:
+            hi = mid
+    assert 0 <= lo < seqs
     return lo
 
 
