@@ -37,16 +37,13 @@ namespace rrn {
 constexpr int kRopeMaxDim = 512;      // head_dim
 constexpr int kRopeMaxAxes = 4;
 constexpr int kRopeMaxWarps = 8;      // warps a block
-#ifndef ROPE_BR
-#define ROPE_BR 2
-#endif
 // Blocks a SM that a shape's registers are budgeted for.  Measured on GB300,
 // bf16 8192 tokens x 40 heads of 128: the forward 31.0 us with four blocks
 // (64 registers a thread), 32.5 with three, 38.7 with five (which spill); the
 // gradient 63.5 us with two, 75.5 with three.
 // bytes: of a piece.
 __host__ __device__ constexpr int rope_resident(int bytes, int k) { return bytes * k <= 16 && bytes >= 4 ? 4 : 2; }
-__host__ __device__ constexpr int rope_bwd_resident(int bytes, int k) { return bytes * k <= 16 && bytes >= 4 ? ROPE_BR : 1; }
+__host__ __device__ constexpr int rope_bwd_resident(int bytes, int k) { return bytes * k <= 16 && bytes >= 4 ? 2 : 1; }
 
 struct RopeParams {
     const void *x;            // packed token rows (query, key, [value] heads)
@@ -746,7 +743,7 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(Piece<T, VE>
 // A block's first q_warps warps take its tokens' query heads, the rest the
 // key heads (so a thread keeps one kind's share of the weight's gradient in
 // registers and both kinds share the tokens' angles: with blocks of one kind
-// each token's were made twice, 62.5 against XXX us for bf16 8192 tokens x 40
+// each token's were made twice, 62.5 against 49.5 us for bf16 8192 tokens x 40
 // heads of 128).  The block's sums go to partial[kind][block][D], and the
 // blocks' are added up by another kernel.  The order of every sum follows from
 // the sizes and the grid: no atomics.
@@ -776,6 +773,14 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(Piece<T,
     jobs.set(blockIdx.x, p.each, p.extra);
     const uint32_t head0 = key ? (uint32_t)p.q_heads * head_bytes : 0u;
     const float *w = wsm + (key ? 2 * kRopeTable : 0);
+    // The block's first token row into L2 before the wait (bf16 8192 tokens x
+    // 40 heads of 128 44.6 -> 44.0 us; more rows, or rows in the forward, did
+    // not pay).
+    if (P::kBytes == 16 && threadIdx.x == 0 && jobs.first < jobs.last) {
+        const uint32_t bytes = (uint32_t)(p.q_heads + p.k_heads) * head_bytes;
+        prefetch_l2(static_cast<const char *>(p.dy) + jobs.first * p.dy_stride, bytes);
+        if constexpr (NORM) prefetch_l2(static_cast<const char *>(p.x) + jobs.first * p.x_stride, bytes);
+    }
 
     pdl_wait_for_inputs();
     pdl_allow_dependents();
