@@ -7,6 +7,7 @@
 
 #include "launch_util.h"
 #include "rope_kernels.cuh"
+#include "rope_ragged.cuh"
 #include "rope_pick.h"
 
 namespace {
@@ -98,6 +99,21 @@ int pick_shape(int dtype, int64_t unit, rrn::RopeParams *p) {
     const rrn::RopeShape *table = dtype == RMSNORM_BF16 ? rrn::kRopeShapesBf16 : rrn::kRopeShapesF32;
     const int tail = p->head_dim / 2 - p->R;
     for (int i = 0; i < rrn::kRopeShapes; ++i) {
+        // Pairs that 16-byte pieces do not hold, nor (bf16) 8-byte ones: whole
+        // heads through shared memory, where they come in 16-byte chunks.
+        // Measured on GB300, 8192 tokens x 40 heads: bf16 heads of 80, 20 of
+        // them rotated, 41.7 us that way, 78.8 in 4-byte pieces; bf16 heads of
+        // 72 in 8-byte pieces 28.0 us, 36.7 that way; fp32 heads of 80 (4096
+        // tokens) 33.8 us that way, 38.9 in 8-byte pieces.
+        if (i == 2 && p->head_dim % table[0].ve == 0 && unit % table[0].ve == 0) {
+            const int ve = table[0].ve, turned = (p->R + ve - 1) / ve, units = turned + (tail + ve - 1) / ve;
+            if (units <= 32) {
+                p->units = p->lanes = units;
+                p->rot_units = turned;
+                p->heads_a_warp = 32 / units;
+                return rrn::kRopeRagged;
+            }
+        }
         const int ve = table[i].ve, units = p->head_dim / 2 / ve;
         if (p->R % ve != 0 || tail % ve != 0 || unit % ve != 0 || units > 32 * table[i].k) continue;
         p->units = units;
@@ -127,8 +143,24 @@ bool tile_reaches(int64_t a, int64_t b, int64_t c) {
 int whole_head(const rrn::RopeParams *p) { return 2 * p->R == p->head_dim ? p->head_dim : 0; }
 
 const void *forward_kernel(int dtype, int shape, bool il, int mode, int whole) {
+    if (shape == rrn::kRopeRagged)
+        return dtype == RMSNORM_BF16 ? rrn::rope_ragged_bf16(il, mode) : rrn::rope_ragged_f32(il, mode);
     return dtype == RMSNORM_BF16 ? rrn::rope_fwd_bf16(shape, il, mode, whole)
                                  : rrn::rope_fwd_f32(shape, il, mode, whole);
+}
+
+const void *backward_kernel(int dtype, int shape, bool il, bool norm, int whole) {
+    if (shape == rrn::kRopeRagged)
+        return dtype == RMSNORM_BF16 ? rrn::rope_ragged_bwd_bf16(il, norm) : rrn::rope_ragged_bwd_f32(il, norm);
+    return dtype == RMSNORM_BF16 ? rrn::rope_bwd_bf16(shape, il, norm, whole)
+                                 : rrn::rope_bwd_f32(shape, il, norm, whole);
+}
+
+// Shared memory of a gradient block.
+size_t backward_smem(int dtype, int shape, bool norm) {
+    if (shape == rrn::kRopeRagged) return rrn::kRagSmemBytes;
+    const rrn::RopeShape held = (dtype == RMSNORM_BF16 ? rrn::kRopeShapesBf16 : rrn::kRopeShapesF32)[shape];
+    return (size_t)rrn::kRopeSmemBytes + rrn::rope_ring_bytes(held.ve * rrn::size_of(dtype), held.k, norm);
 }
 
 int launch_forward(rrn::RopeParams *p, int dtype, int64_t unit, bool il, int mode, rmsnorm_stream_t stream) {
@@ -142,8 +174,9 @@ int launch_forward(rrn::RopeParams *p, int dtype, int64_t unit, bool il, int mod
     // fewer tokens than blocks it is a slice of them, one head iteration a
     // warp where that many blocks fit.
     const int64_t iters = div_up((int64_t)p->q_heads + p->k_heads + p->v_heads, p->heads_a_warp);
-    const size_t smem = rrn::kRopeSmemBytes;
+    const size_t smem = shape == rrn::kRopeRagged ? rrn::kRagSmemBytes : rrn::kRopeSmemBytes;
     int resident = 0;
+    if (smem > 48 * 1024 && (st = rrn::allow_smem(dev, fn)) != RMSNORM_OK) return st;
     if ((st = rrn::resident_blocks(dev, fn, 32 * rrn::kRopeMaxWarps, smem, &resident)) != RMSNORM_OK) return st;
     const int64_t most = (int64_t)sms * resident;
     int64_t slices = 1;
@@ -236,14 +269,12 @@ int rmsnorm_qk_rope_bwd(const void *dy, const void *x, void *dx, int64_t tokens,
         if ((st = rrn::current_device_sms(&dev, &sms)) != RMSNORM_OK) return st;
         const int shape = pick_shape(dtype, u.get(), &p);
         const bool il = rope->interleaved == 1;
-        const void *fn = dtype == RMSNORM_BF16 ? rrn::rope_bwd_bf16(shape, il, norm == 1, whole_head(&p))
-                                               : rrn::rope_bwd_f32(shape, il, norm == 1, whole_head(&p));
+        const void *fn = backward_kernel(dtype, shape, il, norm == 1, whole_head(&p));
         if (fn == nullptr) return RMSNORM_EINVAL;
         p.iters = (int32_t)div_up(q_heads, p.heads_a_warp);
         p.iters_k = (int32_t)div_up(k_heads, p.heads_a_warp);
         p.tile = tile_reaches(p.dy_stride, p.y_stride, norm == 1 ? p.x_stride : 0) ? rrn::kRopeMaxWarps : 1;
-        const rrn::RopeShape held = (dtype == RMSNORM_BF16 ? rrn::kRopeShapesBf16 : rrn::kRopeShapesF32)[shape];
-        const size_t smem = rrn::kRopeSmemBytes + rrn::rope_ring_bytes(held.ve * (int)s, held.k, norm == 1);
+        const size_t smem = backward_smem(dtype, shape, norm == 1);
         int resident = 0;
         if (smem > 48 * 1024 && (st = rrn::allow_smem(dev, fn)) != RMSNORM_OK) return st;
         if ((st = rrn::resident_blocks(dev, fn, 32 * rrn::kRopeMaxWarps, smem, &resident)) != RMSNORM_OK) return st;

@@ -154,8 +154,15 @@ struct Piece {
             asm volatile("st.global.u16 [%0], %1;" : : "l"(p), "h"((unsigned short)u[0]) : "memory");
         }
     }
+    // A 16-byte piece into shared memory.
+    __device__ static __forceinline__ void give(unsigned char *smem, const Raw &r) {
+        static_assert(kBytes == 16, "16-byte pieces");
+        *reinterpret_cast<uint4 *>(smem) = make_uint4(r.u[0], r.u[1], r.u[2], r.u[3]);
+    }
     // The same piece on its way to shared memory, and read back from there.
-    __device__ static __forceinline__ void copy(char *smem, const char *p) { copy_async<kBytes>(smem, p); }
+    // L1: a lane's other piece is in the same 32 bytes (interleaved pairs).
+    template <bool L1>
+    __device__ static __forceinline__ void copy(char *smem, const char *p) { copy_async<kBytes, L1>(smem, p); }
     __device__ static __forceinline__ Raw take(const char *smem) {
         Raw r = zero();
         if constexpr (kBytes == 16) {
@@ -260,17 +267,14 @@ __device__ __forceinline__ void turn_runs(float *a, float *b, const float (&f)[N
         const float x = a[0], y = b[0], s = BACK ? -g[0] : g[0];
         a[0] = fmaf(x, f[0], -(y * s));
         b[0] = fmaf(x, s, y * f[0]);
-    } else if constexpr (IL) {
+    } else if constexpr (IL) {   // one at a time: packing neighbours both ways costs more than it saves
 #pragma unroll
         for (int j = 0; j < 2 * N; j += 2) {
             float *e = j < N ? a + j : b + (j - N);
-            const float c = j < N ? f[j % N] : g[j % N];
-            const float s = j < N ? f[j % N + 1] : g[j % N + 1];
-            const float2 v = BACK ? __ffma2_rn(make_float2(e[0], e[0]), make_float2(c, -s),
-                                               __fmul2_rn(make_float2(e[1], e[1]), make_float2(s, c)))
-                                  : __ffma2_rn(make_float2(e[0], e[0]), make_float2(c, s),
-                                               __fmul2_rn(make_float2(e[1], e[1]), make_float2(-s, c)));
-            e[0] = v.x, e[1] = v.y;
+            const float c = j < N ? f[j % N] : g[j % N], x = e[0], y = e[1];
+            const float s = BACK ? -(j < N ? f[j % N + 1] : g[j % N + 1]) : (j < N ? f[j % N + 1] : g[j % N + 1]);
+            e[0] = fmaf(x, c, -(y * s));
+            e[1] = fmaf(x, s, y * c);
         }
     } else {
 #pragma unroll
@@ -423,8 +427,11 @@ __device__ __forceinline__ void make_weights(const RopeParams &p, float *wsm) {
         const void *w = kind ? p.k_w : p.q_w;
         // element e: which pair, and whether it is its second element
         int pair, second;
+        // (the pairs past the rotated part start with a unit of their own)
+        const int tail = p.rot_units * VE;
         if (IL) {
             pair = e >> 1;
+            pair = pair < p.R ? pair : tail + pair - p.R;
             second = e & 1;
         } else if (e < 2 * p.R) {
             second = e >= p.R;
@@ -432,7 +439,7 @@ __device__ __forceinline__ void make_weights(const RopeParams &p, float *wsm) {
         } else {
             const int half = D / 2 - p.R;
             second = e - 2 * p.R >= half;
-            pair = p.R + (e - 2 * p.R - second * half);
+            pair = tail + (e - 2 * p.R - second * half);
         }
         float v = 1.f;
         if (w != nullptr) v = widen_bits(ld_bits(w, e, T{}, 2), T{}) + p.w_bias;
@@ -820,11 +827,11 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(Piece<T,
                 if constexpr (ASYNC) {
                     const int d = HD ? (IL ? VE : HD / 2) * S : my.ob[k] - my.oa[k];
                     const char *ga = tg + (go + my.oa[k]), *at_x = tx + (xo + my.oa[k]);
-                    P::copy(place(0, k), ga);
-                    P::copy(place(1, k), ga + d);
+                    P::template copy<IL>(place(0, k), ga);
+                    P::template copy<IL>(place(1, k), ga + d);
                     if constexpr (NORM) {
-                        P::copy(place(2, k), at_x);
-                        P::copy(place(3, k), at_x + d);
+                        P::template copy<IL>(place(2, k), at_x);
+                        P::template copy<IL>(place(3, k), at_x + d);
                     }
                 } else {
                     da[k] = P::load(tg + (go + my.oa[k]));

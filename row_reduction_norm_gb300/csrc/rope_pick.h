@@ -19,4 +19,11 @@ const void *rope_fwd_f32(int shape, bool interleaved, int mode, int whole);
 const void *rope_bwd_bf16(int shape, bool interleaved, bool norm, int whole);
 const void *rope_bwd_f32(int shape, bool interleaved, bool norm, int whole);
 
+// Heads in 16-byte chunks whose pairs do not fall on them (rope_ragged.cuh).
+constexpr int kRopeRagged = kRopeShapes;
+const void *rope_ragged_bf16(bool interleaved, int mode);
+const void *rope_ragged_f32(bool interleaved, int mode);
+const void *rope_ragged_bwd_bf16(bool interleaved, bool norm);
+const void *rope_ragged_bwd_f32(bool interleaved, bool norm);
+
 }  // namespace rrn
