@@ -7,6 +7,7 @@ fallback path.
 """
 from __future__ import annotations
 
+import ctypes
 import functools
 import struct
 from typing import Optional
@@ -187,8 +188,33 @@ def _empty(shape, dtype, device, stream):
 
 
 # The calls below are made once a layer and token batch, and their kernels may
-# take two microseconds: the checks compare device numbers, types and shapes
-# without making device objects or contexts.
+# take two microseconds.  The extension module ``_fastcall`` makes their checks
+# and calls in native code; what it finds out of the ordinary it leaves to the
+# Python bodies here (``None``), which say what is wrong or do it themselves.
+_fast = None
+_FAST_NAMES = ("rmsnorm_qk_rope_fwd", "rmsnorm_qk_rope_bwd", "rmsnorm_qk_rope_bwd_workspace_bytes",
+               "rmsnorm_qkv_append", "rmsnorm_dropout_fwd", "rmsnorm_bwd", "rmsnorm_bwd_workspace_bytes",
+               "rmsnorm_dropout_bwd")
+
+
+def _bind_fast():
+    global _fast
+    lib = N.load()
+    from . import _fastcall   # built beside the library
+    _fastcall.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in _FAST_NAMES))
+    _fast = _fastcall
+    return _fast
+
+
+def _took(result, where: str) -> bool:
+    """Whether the native call was made; a status it came back with is raised."""
+    if result is None:
+        return False
+    if type(result) is int:
+        raise N.RmsNormError(result, where)
+    return True
+
+
 _raw_stream = torch._C._cuda_getCurrentRawStream      # the current stream's handle, by device number
 _current_device = torch._C._cuda_getDevice
 
@@ -288,6 +314,11 @@ def qk_norm_rope(qkv: torch.Tensor, q_heads: int, k_heads: int, head_dim: int, p
     q_heads + k_heads heads are written (``out=qkv`` works in place), or to a
     new [tokens, (q_heads + k_heads) * head_dim] tensor.
     """
+    if stream is None and qkv.is_cuda:
+        y = (_fast or _bind_fast()).qk_norm_rope(qkv, q_heads, k_heads, head_dim, positions, inv_freq, q_w, k_w, eps,
+                                                 weight_bias, norm, sections, interleaved, out)
+        if _took(y, "rmsnorm_qk_rope_fwd"):
+            return y
     t = qkv.dtype
     code = dtype_code(t)
     dev = _device_of(qkv, "qkv")
@@ -319,6 +350,12 @@ def qk_norm_rope_backward(dout: torch.Tensor, qkv: Optional[torch.Tensor], q_hea
     tensor of ``rmsnorm_qk_rope_bwd_workspace_bytes(head_dim)`` bytes
     (allocated when not given).
     """
+    if stream is None and dout.is_cuda:
+        r = (_fast or _bind_fast()).qk_norm_rope_backward(dout, qkv, q_heads, k_heads, head_dim, positions, inv_freq,
+                                                          q_w, k_w, eps, weight_bias, norm, sections, interleaved, out,
+                                                          workspace)
+        if _took(r, "rmsnorm_qk_rope_bwd"):
+            return r
     t = dout.dtype
     code = dtype_code(t)
     dev = _device_of(dout, "dout")
@@ -336,7 +373,7 @@ def qk_norm_rope_backward(dout: torch.Tensor, qkv: Optional[torch.Tensor], q_hea
     dq_w = dk_w = dq = dk = None
     ws = need = 0
     if qw is not None and kw is not None:
-        dq_w, dk_w = _empty((2, head_dim), t, dout.device, stream).unbind(0)
+        dq_w, dk_w = (_empty((head_dim,), t, dout.device, stream) for _ in range(2))
         dq, dk = dq_w.data_ptr(), dk_w.data_ptr()
         need = _rope_workspace_bytes(head_dim)
         workspace = _workspace(workspace, need, dout.device, stream)
@@ -393,6 +430,12 @@ def qkv_append(qkv: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     sequence are left alone; rows without a page are not written and counted
     in ``dropped`` (int32, [1], added to) where given.
     """
+    if stream is None and qkv.is_cuda:
+        r = (_fast or _bind_fast()).qkv_append(qkv, k_cache, v_cache, page_table, cu_tokens, cache_lens, q_heads,
+                                               kv_heads, head_dim, inv_freq, positions, q_w, k_w, eps, weight_bias,
+                                               norm, sections, interleaved, k_scale, v_scale, q_out, dropped)
+        if _took(r, "rmsnorm_qkv_append"):
+            return r
     t = qkv.dtype
     code = dtype_code(t)
     dev = _device_of(qkv, "qkv")
@@ -479,6 +522,10 @@ def rms_norm_dropout(x: torch.Tensor, residual: torch.Tensor, p: float, rng: Opt
     2^-16, and kept elements are scaled by the inverse of the probability that
     makes.
     """
+    if stream is None and x.is_cuda:
+        r = (_fast or _bind_fast()).rms_norm_dropout(x, residual, p, rng, w, eps, weight_bias, out, residual_out)
+        if _took(r, "rmsnorm_dropout_fwd"):
+            return r
     code = dtype_code(x.dtype)
     dev, rows, hidden = _rows_of(x, "x")
     res = _like(residual, "residual", x, dev)
@@ -520,6 +567,10 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, w: Optional[torch.Tenso
     ``rmsnorm_bwd_workspace_bytes(rows, hidden, dtype)`` bytes (allocated when
     not given).
     """
+    if stream is None and dy.is_cuda:
+        r = (_fast or _bind_fast()).rms_norm_backward(dy, h, w, dresidual_out, eps, weight_bias, out, workspace)
+        if _took(r, "rmsnorm_bwd"):
+            return r
     dev, code, rows, hidden, at, dw, ws, need, keep = _backward_args(dy, h, w, dresidual_out, workspace, stream)
     if out is None:
         out = _empty(dy.shape, dy.dtype, dy.device, stream)
@@ -536,6 +587,11 @@ def rms_norm_dropout_backward(dy: torch.Tensor, h: torch.Tensor, p: float, rng: 
     """Gradient of ``rms_norm_dropout`` (``h``: its residual_out, with the same
     ``p`` and ``rng``): returns (dresidual, dx, dw), dw None without a weight.
     Other arguments as ``rms_norm_backward``."""
+    if stream is None and dy.is_cuda:
+        r = (_fast or _bind_fast()).rms_norm_dropout_backward(dy, h, p, rng, w, dresidual_out, eps, weight_bias,
+                                                              dresidual, dx, workspace)
+        if _took(r, "rmsnorm_dropout_bwd"):
+            return r
     dev, code, rows, hidden, at, dw, ws, need, keep = _backward_args(dy, h, w, dresidual_out, workspace, stream)
     r = _rng_arg(rng, p, dev)
     if dresidual is None:

@@ -1,0 +1,449 @@
+// fastcall.cpp -- the Python calls of the rotary, append and dropout operators
+// without Python's own cost: a CPython module that takes torch tensors, makes
+// the checks of api.py on them, and calls the C ABI on the current stream.
+//
+// These kernels take two microseconds for a decode step while the checks, the
+// argument conversion and the allocations of a call through Python objects and
+// ctypes take seven to thirty.  Each function here takes what the api.py
+// function of its name takes, by position; it returns that function's result,
+// or None when anything about the arguments is out of the ordinary (a stream
+// given, another device current, a wrong shape or type, a tensor subclass):
+// api.py then goes its own way, which is also where every refusal is worded.
+// A status of the C ABI other than RMSNORM_OK comes back as an int.
+//
+// Nothing is computed and nothing is kept here; the C ABI's addresses are
+// handed over once by bind().
+#include <Python.h>
+
+#include <ATen/ATen.h>
+#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <cstring>
+
+#include "rmsnorm.h"
+
+namespace {
+
+decltype(&rmsnorm_qk_rope_fwd) qk_rope_fwd;
+decltype(&rmsnorm_qk_rope_bwd) qk_rope_bwd;
+decltype(&rmsnorm_qk_rope_bwd_workspace_bytes) qk_rope_bwd_workspace_bytes;
+decltype(&rmsnorm_qkv_append) qkv_append_fn;
+decltype(&rmsnorm_dropout_fwd) dropout_fwd;
+decltype(&rmsnorm_bwd) norm_bwd;
+decltype(&rmsnorm_bwd_workspace_bytes) bwd_workspace_bytes;
+decltype(&rmsnorm_dropout_bwd) dropout_bwd;
+
+// Thrown (and caught in this file) to leave a call to api.py.
+struct Elsewhere {};
+
+void need(bool ok) {
+    if (!ok) throw Elsewhere();
+}
+
+const at::Tensor &tensor(PyObject *o) {
+    need(THPVariable_CheckExact(o));
+    const at::Tensor &t = THPVariable_Unpack(o);
+    need(t.defined() && t.is_cuda() && t.layout() == at::kStrided);
+    return t;
+}
+
+int64_t whole(PyObject *o) {
+    need(PyLong_CheckExact(o));
+    int over = 0;
+    const long long v = PyLong_AsLongLongAndOverflow(o, &over);
+    need(over == 0);
+    return (int64_t)v;
+}
+
+int32_t count(PyObject *o) {
+    const int64_t v = whole(o);
+    need(v >= 0 && v <= INT32_MAX);
+    return (int32_t)v;
+}
+
+float real(PyObject *o) {
+    if (PyFloat_CheckExact(o)) return (float)PyFloat_AS_DOUBLE(o);
+    return (float)whole(o);
+}
+
+bool truth(PyObject *o) {
+    need(o == Py_True || o == Py_False);
+    return o == Py_True;
+}
+
+int code_of(const at::Tensor &t) {
+    if (t.scalar_type() == at::kBFloat16) return RMSNORM_BF16;
+    need(t.scalar_type() == at::kFloat);
+    return RMSNORM_F32;
+}
+
+// The device of the call, which has to be the current one.
+struct Where {
+    int dev;
+    explicit Where(const at::Tensor &t) : dev(t.get_device()) { need(dev >= 0 && c10::cuda::current_device() == dev); }
+    rmsnorm_stream_t stream() const {
+        return reinterpret_cast<rmsnorm_stream_t>(c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream());
+    }
+    void same(const at::Tensor &t, at::ScalarType type) const {
+        need(t.get_device() == dev && t.scalar_type() == type);
+    }
+};
+
+// Address of a contiguous [size] tensor, or NULL for None.
+void *vector(PyObject *o, int64_t size, at::ScalarType type, const Where &w) {
+    if (o == Py_None) return nullptr;
+    const at::Tensor &t = tensor(o);
+    w.same(t, type);
+    need(t.dim() == 1 && t.size(0) == size && (size <= 1 || t.stride(0) == 1));
+    return t.data_ptr();
+}
+
+// Token stride of a [tokens, >= width] tensor of packed heads.
+int64_t head_rows(const at::Tensor &t, int64_t width, int64_t tokens, at::ScalarType type, const Where &w) {
+    w.same(t, type);
+    need(t.dim() == 2 && t.size(0) == tokens && t.size(1) >= width && (t.stride(1) == 1 || t.size(1) <= 1));
+    const int64_t s = t.stride(0), n = t.size(1);
+    return tokens > 1 || s > n ? s : n;
+}
+
+void *like(const at::Tensor &t, const at::Tensor &x, const Where &w) {
+    w.same(t, x.scalar_type());
+    need(t.sizes() == x.sizes() && t.is_contiguous());
+    return t.data_ptr();
+}
+
+void rope_arg(rmsnorm_rope_t *r, PyObject *positions, PyObject *inv_freq, PyObject *sections, PyObject *interleaved,
+              int64_t tokens, int64_t head_dim, const Where &w) {
+    std::memset(r, 0, sizeof(*r));
+    const at::Tensor &f = tensor(inv_freq);
+    const int64_t pairs = f.numel();
+    need(pairs >= 1 && pairs <= head_dim / 2);
+    r->inv_freq = static_cast<const float *>(vector(inv_freq, pairs, at::kFloat, w));
+    if (sections == Py_None) {
+        r->axes = 1;
+        r->section[0] = (int32_t)pairs;
+    } else {
+        need(PyList_CheckExact(sections) || PyTuple_CheckExact(sections));
+        const Py_ssize_t axes = PySequence_Fast_GET_SIZE(sections);
+        need(axes >= 1 && axes <= 4);
+        int64_t sum = 0;
+        for (Py_ssize_t a = 0; a < axes; ++a) {
+            r->section[a] = count(PySequence_Fast_GET_ITEM(sections, a));
+            sum += r->section[a];
+        }
+        need(sum == pairs);
+        r->axes = (int32_t)axes;
+    }
+    r->rot_dim = (int32_t)(2 * pairs);
+    r->interleaved = truth(interleaved);
+    r->position_bytes = 4;
+    if (positions != Py_None) {
+        const at::Tensor &p = tensor(positions);
+        need(p.get_device() == w.dev && (p.scalar_type() == at::kLong || p.scalar_type() == at::kInt));
+        if (p.dim() == 1) need(r->axes == 1 && p.size(0) == tokens);
+        else need(p.dim() == 2 && p.size(0) == r->axes && p.size(1) == tokens);
+        need(tokens <= 1 || p.stride(p.dim() - 1) == 1);
+        r->positions = p.data_ptr();
+        r->position_bytes = p.scalar_type() == at::kLong ? 8 : 4;
+        if (r->axes > 1) r->position_stride = tokens > 1 || p.stride(0) > tokens ? p.stride(0) : tokens;
+    }
+}
+
+at::Tensor bytes_on(const at::Tensor &t, int64_t n) { return at::empty({n}, t.options().dtype(at::kByte)); }
+
+// A workspace given, or made.
+void *workspace_of(PyObject *given, int64_t n, const at::Tensor &x, const Where &w, at::Tensor *made) {
+    if (given == Py_None) {
+        *made = bytes_on(x, n);
+        return made->data_ptr();
+    }
+    const at::Tensor &t = tensor(given);
+    need(t.get_device() == w.dev && t.is_contiguous() && t.numel() * (int64_t)t.element_size() >= n);
+    return t.data_ptr();
+}
+
+PyObject *status_of(int st) { return PyLong_FromLong(st); }
+
+PyObject *wrap_or_none(const at::Tensor &t) {
+    if (t.defined()) return THPVariable_Wrap(t);
+    Py_RETURN_NONE;
+}
+
+PyObject *same_object(PyObject *o) {
+    Py_INCREF(o);
+    return o;
+}
+
+// Runs a call; what it leaves to api.py comes back as None.
+template <typename F>
+PyObject *guarded(F f) {
+    try {
+        return f();
+    } catch (const Elsewhere &) {
+        Py_RETURN_NONE;
+    } catch (const std::exception &e) {   // an allocation that failed
+        PyErr_Clear();
+        Py_RETURN_NONE;
+    }
+}
+
+// (qkv, q_heads, k_heads, head_dim, positions, inv_freq, q_w, k_w, eps, weight_bias, norm, sections, interleaved, out)
+PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        need(n == 14 && qk_rope_fwd != nullptr);
+        const at::Tensor &x = tensor(a[0]);
+        const int code = code_of(x);
+        const Where w(x);
+        const int32_t q = count(a[1]), k = count(a[2]);
+        const int64_t d = whole(a[3]), tokens = x.dim() == 2 ? x.size(0) : -1, width = ((int64_t)q + k) * d;
+        const int64_t xs = head_rows(x, width, tokens, x.scalar_type(), w);
+        void *qw = vector(a[6], d, x.scalar_type(), w), *kw = vector(a[7], d, x.scalar_type(), w);
+        rmsnorm_rope_t rope;
+        need(a[4] != Py_None);
+        rope_arg(&rope, a[4], a[5], a[11], a[12], tokens, d, w);
+        at::Tensor made;
+        if (a[13] == Py_None) made = at::empty({tokens, width}, x.options());
+        const at::Tensor &y = made.defined() ? made : tensor(a[13]);
+        const int64_t ys = head_rows(y, width, tokens, x.scalar_type(), w);
+        const int st = qk_rope_fwd(x.data_ptr(), y.data_ptr(), tokens, xs, ys, q, k, d, qw, kw, real(a[9]), real(a[8]),
+                                   truth(a[10]), &rope, code, w.stream());
+        if (st != RMSNORM_OK) return status_of(st);
+        return made.defined() ? THPVariable_Wrap(made) : same_object(a[13]);
+    });
+}
+
+// (dout, qkv, q_heads, k_heads, head_dim, positions, inv_freq, q_w, k_w, eps, weight_bias, norm, sections, interleaved,
+//  out, workspace)
+PyObject *qk_norm_rope_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        need(n == 16 && qk_rope_bwd != nullptr);
+        const at::Tensor &g = tensor(a[0]);
+        const int code = code_of(g);
+        const Where w(g);
+        const int32_t q = count(a[2]), k = count(a[3]);
+        const int64_t d = whole(a[4]), tokens = g.dim() == 2 ? g.size(0) : -1, width = ((int64_t)q + k) * d;
+        const int64_t gs = head_rows(g, width, tokens, g.scalar_type(), w);
+        const bool norm = truth(a[11]);
+        need(!norm || a[1] != Py_None);
+        void *x = nullptr;
+        int64_t xs = width;
+        if (a[1] != Py_None) {
+            const at::Tensor &t = tensor(a[1]);
+            xs = head_rows(t, width, tokens, g.scalar_type(), w);
+            x = t.data_ptr();
+        }
+        void *qw = vector(a[7], d, g.scalar_type(), w), *kw = vector(a[8], d, g.scalar_type(), w);
+        rmsnorm_rope_t rope;
+        need(a[5] != Py_None);
+        rope_arg(&rope, a[5], a[6], a[12], a[13], tokens, d, w);
+        at::Tensor made, dq, dk, ws;
+        if (a[14] == Py_None) made = at::empty({tokens, width}, g.options());
+        const at::Tensor &y = made.defined() ? made : tensor(a[14]);
+        const int64_t ys = head_rows(y, width, tokens, g.scalar_type(), w);
+        void *at_ws = nullptr;
+        int64_t bytes = 0;
+        if (qw != nullptr && kw != nullptr) {
+            bytes = qk_rope_bwd_workspace_bytes(d);
+            need(bytes > 0);
+            dq = at::empty({d}, g.options());
+            dk = at::empty({d}, g.options());
+            at_ws = workspace_of(a[15], bytes, g, w, &ws);
+        }
+        const int st = qk_rope_bwd(g.data_ptr(), x, y.data_ptr(), tokens, gs, xs, ys, q, k, d, qw, kw,
+                                   dq.defined() ? dq.data_ptr() : nullptr, dk.defined() ? dk.data_ptr() : nullptr,
+                                   real(a[10]), real(a[9]), norm, &rope, code, at_ws, (uint64_t)bytes, w.stream());
+        if (st != RMSNORM_OK) return status_of(st);
+        return Py_BuildValue("(NNN)", made.defined() ? THPVariable_Wrap(made) : same_object(a[14]), wrap_or_none(dq),
+                             wrap_or_none(dk));
+    });
+}
+
+// (qkv, k_cache, v_cache, page_table, cu_tokens, cache_lens, q_heads, kv_heads, head_dim, inv_freq, positions, q_w, k_w,
+//  eps, weight_bias, norm, sections, interleaved, k_scale, v_scale, q_out, dropped)
+PyObject *qkv_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        need(n == 22 && qkv_append_fn != nullptr);
+        const at::Tensor &x = tensor(a[0]);
+        const int code = code_of(x);
+        const Where w(x);
+        const int32_t q = count(a[6]), kv_heads = count(a[7]);
+        need(q > 0);
+        const int64_t d = whole(a[8]), tokens = x.dim() == 2 ? x.size(0) : -1;
+        const int64_t xs = head_rows(x, ((int64_t)q + 2 * (int64_t)kv_heads) * d, tokens, x.scalar_type(), w);
+        void *qw = vector(a[11], d, x.scalar_type(), w), *kw = vector(a[12], d, x.scalar_type(), w);
+        rmsnorm_rope_t rope;
+        rope_arg(&rope, a[10], a[9], a[16], a[17], tokens, d, w);
+        const at::Tensor &kc = tensor(a[1]), &vc = tensor(a[2]), &table = tensor(a[3]);
+        const at::ScalarType held = kc.scalar_type();
+        need(held == x.scalar_type() || held == at::kFloat8_e4m3fn);
+        w.same(kc, held);
+        w.same(vc, held);
+        need(kc.dim() == 4 && kc.size(2) == kv_heads && kc.size(3) == d && kc.stride(3) == 1 &&
+             vc.sizes() == kc.sizes() && vc.strides() == kc.strides());
+        w.same(table, at::kInt);
+        need(table.dim() == 2 && (table.stride(1) == 1 || table.size(1) <= 1));
+        const int64_t seqs = table.size(0), max_pages = table.size(1);
+        need(seqs <= INT32_MAX && max_pages <= INT32_MAX && kc.size(0) <= INT32_MAX && kc.size(1) <= INT32_MAX);
+        rmsnorm_paged_kv_t kv;
+        std::memset(&kv, 0, sizeof(kv));
+        kv.k_cache = kc.data_ptr();
+        kv.v_cache = vc.data_ptr();
+        kv.page_table = static_cast<const int32_t *>(table.data_ptr());
+        need(a[4] != Py_None && a[5] != Py_None);
+        kv.cu_tokens = static_cast<const int32_t *>(vector(a[4], seqs + 1, at::kInt, w));
+        kv.cache_lens = static_cast<const int32_t *>(vector(a[5], seqs, at::kInt, w));
+        kv.dropped = static_cast<int32_t *>(vector(a[21], 1, at::kInt, w));
+        kv.page_table_stride = seqs > 1 || table.stride(0) > max_pages ? table.stride(0) : max_pages;
+        kv.page_stride = kc.size(0) > 1 ? kc.stride(0) : 0;
+        kv.row_stride = kc.size(1) > 1 ? kc.stride(1) : 0;
+        kv.head_stride = kc.size(2) > 1 ? kc.stride(2) : 0;
+        kv.seqs = (int32_t)seqs;
+        kv.max_pages = (int32_t)max_pages;
+        kv.num_pages = (int32_t)kc.size(0);
+        kv.page_size = (int32_t)kc.size(1);
+        kv.cache_dtype = held == at::kFloat8_e4m3fn ? (int)RMSNORM_E4M3 : code;
+        kv.k_scale = real(a[18]);
+        kv.v_scale = real(a[19]);
+        at::Tensor made;
+        if (a[20] == Py_None) made = at::empty({tokens, (int64_t)q * d}, x.options());
+        const at::Tensor &y = made.defined() ? made : tensor(a[20]);
+        const int64_t ys = head_rows(y, (int64_t)q * d, tokens, x.scalar_type(), w);
+        const int st = qkv_append_fn(x.data_ptr(), y.data_ptr(), tokens, xs, ys, q, kv_heads, d, qw, kw, real(a[14]),
+                                     real(a[13]), truth(a[15]), &rope, &kv, code, w.stream());
+        if (st != RMSNORM_OK) return status_of(st);
+        return made.defined() ? THPVariable_Wrap(made) : same_object(a[20]);
+    });
+}
+
+struct Rows {
+    int64_t rows, hidden;
+    explicit Rows(const at::Tensor &t) {
+        need(t.dim() >= 1 && t.size(-1) >= 1 && t.is_contiguous());
+        hidden = t.size(-1);
+        rows = t.numel() / hidden;
+    }
+};
+
+const uint64_t *rng_of(PyObject *o, float p, const Where &w) {
+    if (o == Py_None) {
+        need(p == 0.f);
+        return nullptr;
+    }
+    return static_cast<const uint64_t *>(vector(o, 2, at::kLong, w));
+}
+
+// (x, residual, p, rng, w, eps, weight_bias, out, residual_out)
+PyObject *rms_norm_dropout(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        need(n == 9 && dropout_fwd != nullptr);
+        const at::Tensor &x = tensor(a[0]);
+        const int code = code_of(x);
+        const Where w(x);
+        const Rows r(x);
+        const void *res = like(tensor(a[1]), x, w);
+        const float p = real(a[2]);
+        const uint64_t *rng = rng_of(a[3], p, w);
+        void *weight = vector(a[4], r.hidden, x.scalar_type(), w);
+        at::Tensor y, h;
+        if (a[7] == Py_None) y = at::empty(x.sizes(), x.options());
+        if (a[8] == Py_None) h = at::empty(x.sizes(), x.options());
+        void *yp = y.defined() ? y.data_ptr() : like(tensor(a[7]), x, w);
+        void *hp = h.defined() ? h.data_ptr() : like(tensor(a[8]), x, w);
+        const int st = dropout_fwd(x.data_ptr(), res, weight, yp, hp, r.rows, r.hidden, real(a[5]), real(a[6]), p, rng,
+                                   code, w.stream());
+        if (st != RMSNORM_OK) return status_of(st);
+        return Py_BuildValue("(NN)", y.defined() ? THPVariable_Wrap(y) : same_object(a[7]),
+                             h.defined() ? THPVariable_Wrap(h) : same_object(a[8]));
+    });
+}
+
+// What the two gradients of the norm share: dw and the workspace, with a weight.
+struct Backward {
+    const at::Tensor &dy;
+    int code;
+    Where w;
+    Rows r;
+    void *h, *weight, *dh;
+    at::Tensor dw, ws;
+    void *at_ws = nullptr;
+    int64_t bytes = 0;
+    Backward(PyObject *dy_, PyObject *h_, PyObject *w_, PyObject *dh_, PyObject *workspace)
+        : dy(tensor(dy_)), code(code_of(dy)), w(dy), r(dy), h(like(tensor(h_), dy, w)),
+          weight(vector(w_, r.hidden, dy.scalar_type(), w)), dh(dh_ == Py_None ? nullptr : like(tensor(dh_), dy, w)) {
+        if (weight == nullptr) return;
+        bytes = bwd_workspace_bytes(r.rows, r.hidden, code);
+        need(bytes > 0);
+        dw = at::empty({r.hidden}, dy.options());
+        at_ws = workspace_of(workspace, bytes, dy, w, &ws);
+    }
+    void *dw_at() const { return dw.defined() ? dw.data_ptr() : nullptr; }
+};
+
+// (dy, h, w, dresidual_out, eps, weight_bias, out, workspace)
+PyObject *rms_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        need(n == 8 && norm_bwd != nullptr);
+        Backward b(a[0], a[1], a[2], a[3], a[7]);
+        at::Tensor made;
+        if (a[6] == Py_None) made = at::empty(b.dy.sizes(), b.dy.options());
+        void *dx = made.defined() ? made.data_ptr() : like(tensor(a[6]), b.dy, b.w);
+        const int st = norm_bwd(b.dy.data_ptr(), b.h, b.weight, b.dh, dx, b.dw_at(), b.r.rows, b.r.hidden, real(a[4]),
+                                real(a[5]), b.code, b.at_ws, (uint64_t)b.bytes, b.w.stream());
+        if (st != RMSNORM_OK) return status_of(st);
+        return Py_BuildValue("(NN)", made.defined() ? THPVariable_Wrap(made) : same_object(a[6]), wrap_or_none(b.dw));
+    });
+}
+
+// (dy, h, p, rng, w, dresidual_out, eps, weight_bias, dresidual, dx, workspace)
+PyObject *rms_norm_dropout_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        need(n == 11 && dropout_bwd != nullptr);
+        Backward b(a[0], a[1], a[4], a[5], a[10]);
+        const float p = real(a[2]);
+        const uint64_t *rng = rng_of(a[3], p, b.w);
+        at::Tensor dres, dx;
+        if (a[8] == Py_None) dres = at::empty(b.dy.sizes(), b.dy.options());
+        if (a[9] == Py_None) dx = at::empty(b.dy.sizes(), b.dy.options());
+        void *rp = dres.defined() ? dres.data_ptr() : like(tensor(a[8]), b.dy, b.w);
+        void *xp = dx.defined() ? dx.data_ptr() : like(tensor(a[9]), b.dy, b.w);
+        const int st = dropout_bwd(b.dy.data_ptr(), b.h, b.weight, b.dh, rp, xp, b.dw_at(), b.r.rows, b.r.hidden,
+                                   real(a[6]), real(a[7]), p, rng, b.code, b.at_ws, (uint64_t)b.bytes, b.w.stream());
+        if (st != RMSNORM_OK) return status_of(st);
+        return Py_BuildValue("(NNN)", dres.defined() ? THPVariable_Wrap(dres) : same_object(a[8]),
+                             dx.defined() ? THPVariable_Wrap(dx) : same_object(a[9]), wrap_or_none(b.dw));
+    });
+}
+
+// Addresses of the C ABI's functions, in the order below.
+PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    void *at[8];
+    if (n != 8) {
+        PyErr_SetString(PyExc_TypeError, "bind takes 8 addresses");
+        return nullptr;
+    }
+    for (int i = 0; i < 8; ++i) {
+        at[i] = PyLong_AsVoidPtr(a[i]);
+        if (PyErr_Occurred()) return nullptr;
+    }
+    std::memcpy(&qk_rope_fwd, &at[0], sizeof(void *));
+    std::memcpy(&qk_rope_bwd, &at[1], sizeof(void *));
+    std::memcpy(&qk_rope_bwd_workspace_bytes, &at[2], sizeof(void *));
+    std::memcpy(&qkv_append_fn, &at[3], sizeof(void *));
+    std::memcpy(&dropout_fwd, &at[4], sizeof(void *));
+    std::memcpy(&norm_bwd, &at[5], sizeof(void *));
+    std::memcpy(&bwd_workspace_bytes, &at[6], sizeof(void *));
+    std::memcpy(&dropout_bwd, &at[7], sizeof(void *));
+    Py_RETURN_NONE;
+}
+
+#define ENTRY(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(&f)), METH_FASTCALL, nullptr}
+PyMethodDef methods[] = {ENTRY(bind), ENTRY(qk_norm_rope), ENTRY(qk_norm_rope_backward), ENTRY(qkv_append),
+                         ENTRY(rms_norm_dropout), ENTRY(rms_norm_backward), ENTRY(rms_norm_dropout_backward),
+                         {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__fastcall() { return PyModule_Create(&module); }
