@@ -20,7 +20,10 @@ constexpr int64_t kSmemSums = 49152;
 
 // Blocks a SM of the gradient at most: each keeps a row of fp32 sums, which
 // are written and read once more.
-int64_t blocks_a_sm(int64_t hidden) { return hidden <= 2048 ? 4 : hidden <= 16384 ? 2 : 1; }
+int64_t blocks_a_sm(int64_t hidden) { return hidden <= 1024 ? 8 : hidden <= 4096 ? 4 : hidden <= 16384 ? 2 : 1; }
+
+// Columns of the partial sums' rows.
+int64_t partial_ld(int64_t hidden) { return (hidden + 3) / 4 * 4; }
 
 int check_rows(const void *const *ptrs, int n, int64_t rows, int64_t hidden, float eps, float w_bias, const void *w,
                int dtype) {
@@ -71,6 +74,13 @@ bool reg_shape(int64_t nch, int max_ch, int *gt, int *ch) {
     return false;
 }
 
+// The rows-of-single-elements kernel that holds a row, or -1.
+int scalar_shape(bool vec, int64_t hidden) {
+    for (int i = 0; !vec && i < rrn::kDropScalars; ++i)
+        if (hidden <= (int64_t)rrn::kDropScalar[i].gt * rrn::kDropScalar[i].ch) return i;
+    return -1;
+}
+
 int loop_block(bool vec, int64_t hidden) { return vec || hidden > 4096 ? 1024 : 256; }
 
 void fill(rrn::DropParams *p, const void *w, int64_t rows, int64_t hidden, float eps, float w_bias, uint32_t thr,
@@ -114,6 +124,7 @@ int backward(const void *dy, const void *h, const void *w, const void *dh, void 
         p.dres = dres;
         p.dx = dx;
         p.partial = static_cast<float *>(workspace);
+        p.partial_ld = partial_ld(hidden);
         const bool vec = vec_ok(ptrs, 6, hidden, dtype);
         const int V = 16 / rrn::size_of(dtype);
         p.units = (int32_t)(vec ? hidden / V : hidden);
@@ -127,6 +138,10 @@ int backward(const void *dy, const void *h, const void *w, const void *dh, void 
             threads = rrn::drop_block_threads(gt);
             groups = div_up(rows, threads / gt);
             smem = (size_t)rrn::drop_ring_bytes(gt, ch);
+        } else if (const int shape = scalar_shape(vec, hidden); shape >= 0) {
+            threads = rrn::kDropScalar[shape].gt;
+            fn = rrn::drop_bwd_scalar(dtype, shape, dw != nullptr);
+            smem = (size_t)(thr ? 2 * p.blocks_per_row : 0);
         } else {
             threads = loop_block(vec, hidden);
             fn = rrn::drop_bwd_loop(dtype, vec, threads, dw != nullptr);
@@ -145,7 +160,8 @@ int backward(const void *dy, const void *h, const void *w, const void *dh, void 
         if (st != RMSNORM_OK) return st;
     }
     if (dw == nullptr) return RMSNORM_OK;
-    return rrn::launch_colsum(static_cast<const float *>(workspace), (int)blocks, 0, hidden, dw, nullptr, dtype, stream);
+    return rrn::launch_colsum(static_cast<const float *>(workspace), (int)blocks, 0, hidden, partial_ld(hidden), dw, nullptr,
+                              dtype, stream);
 }
 
 }  // namespace
@@ -181,6 +197,10 @@ int rmsnorm_dropout_fwd(const void *x, const void *residual, const void *w, void
         fn = dtype == RMSNORM_BF16 ? rrn::drop_fwd_bf16(gt, ch) : rrn::drop_fwd_f32(gt, ch);
         threads = rrn::drop_block_threads(gt);
         blocks = div_up(rows, threads / gt);
+    } else if (const int shape = scalar_shape(vec, hidden); shape >= 0) {
+        threads = rrn::kDropScalar[shape].gt;
+        fn = rrn::drop_fwd_scalar(dtype, shape);
+        smem = (size_t)(thr ? p.blocks_per_row : 0);
     } else {
         threads = loop_block(vec, hidden);
         fn = rrn::drop_fwd_loop(dtype, vec, threads);
@@ -200,7 +220,7 @@ int64_t rmsnorm_bwd_workspace_bytes(int64_t rows, int64_t hidden, int dtype) {
     if (st != RMSNORM_OK) return st;
     int64_t blocks = blocks_a_sm(hidden) * sms;
     if (blocks > rows) blocks = rows > 0 ? rows : 1;
-    return blocks * hidden * (int64_t)sizeof(float);
+    return blocks * partial_ld(hidden) * (int64_t)sizeof(float);
 }
 
 int rmsnorm_bwd(const void *dy, const void *h, const void *w, const void *dresidual_out, void *dx, void *dw,

@@ -30,7 +30,8 @@ struct DropParams {
     const void *dy, *h, *dh;     // gradient: dh (of residual_out) nullable
     void *y, *h_out;             // forward
     void *dres, *dx;             // gradient: dx only with dropout
-    float *partial;              // gradient: [blocks][row_elems] sums of dw, or NULL
+    float *partial;              // gradient: [blocks][partial_ld] sums of dw, or NULL
+    int64_t partial_ld;          // row_elems rounded up to a multiple of 4
     const uint64_t *rng;         // seed, offset
     int64_t rows;
     int64_t row_elems, row_bytes;
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(drop_block_threads(GT), drop_bwd_resident(GT))
     }
     copy_async_wait<0>();
     if constexpr (DW) {
-        float *out = p.partial + (int64_t)blockIdx.x * p.row_elems;
+        float *out = p.partial + (int64_t)blockIdx.x * p.partial_ld;
         if constexpr (RPB > 1) {
             float *slots = reinterpret_cast<float *>(ring);   // [row_elems], at most a third of the ring
             __syncthreads();   // every thread is done with its places
@@ -543,7 +544,7 @@ __global__ void __launch_bounds__(BLOCK) drop_bwd_loop_kernel(const DropParams p
     extern __shared__ float sums[];   // [row_elems] with acc_in_smem, then the mask's bytes
     const int tid = threadIdx.x;
     const int64_t n = p.units;
-    float *out = DW ? p.partial + (int64_t)blockIdx.x * p.row_elems : nullptr;
+    float *out = DW ? p.partial + (int64_t)blockIdx.x * p.partial_ld : nullptr;
     float *acc = DW && p.acc_in_smem ? sums : out;
     uint8_t *mask = reinterpret_cast<uint8_t *>(sums + (DW && p.acc_in_smem ? p.row_elems : 0));
     pdl_wait_for_inputs();
@@ -643,6 +644,175 @@ __global__ void __launch_bounds__(BLOCK) drop_bwd_loop_kernel(const DropParams p
 #pragma unroll
                 for (int e = 0; e < VE; ++e) out[u * VE + e] = sums[u * VE + e];
         }
+    }
+}
+
+// -------------------------------------------------- rows of single elements
+// Rows without 16-byte alignment (an odd width, a view off a boundary) that fit
+// a block's registers: thread t owns columns t, t + GT, ... (CH of them), so a
+// warp's accesses are consecutive, every element is read once, and what a
+// 2-byte access wastes is issue slots, not bandwidth.  The mask is made a byte
+// for 8 elements by whichever threads, in shared memory.  bf16 16384 x 2047
+// takes 78 us (52 % of the measured copy bandwidth), its gradient 135 (37 %);
+// two passes over the row (below) took 102 and 255.  Blocks of 1024 threads
+// for the longer rows measured slower than 512 with twice the columns (8192 x
+// 8191 226 against 183 us).
+
+template <typename T, int GT, int CH>
+__global__ void __launch_bounds__(GT) drop_fwd_scalar_kernel(const DropParams p) {
+    __shared__ float2 red[2][1][GT / 32];
+    extern __shared__ uint8_t mask[];   // [blocks_per_row], with dropout
+    const int t = threadIdx.x, n = p.units;
+    pdl_wait_for_inputs();
+    pdl_allow_dependents();
+    uint64_t seed = 0, offset = 0;
+    if (p.thr) {
+        seed = p.rng[0];
+        offset = p.rng[1];
+    }
+    int parity = 0;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        const int64_t off = row * p.row_bytes;
+        const void *xr = static_cast<const char *>(p.x) + off, *rr = static_cast<const char *>(p.res) + off;
+        void *hr = static_cast<char *>(p.h_out) + off, *yr = static_cast<char *>(p.y) + off;
+        uint32_t xb[CH], rb[CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int e = c * GT + t;
+            xb[c] = e < n ? ld_bits(xr, e, T{}, 1) : 0u;
+            rb[c] = e < n ? ld_bits(rr, e, T{}, 1) : 0u;
+        }
+        if (p.thr) {   // the last row's readers are behind its sum's barrier
+            stage_mask(p, mask, seed, offset, row);
+            __syncthreads();
+        }
+        float h[CH], acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int e = c * GT + t;
+            const bool keep = !p.thr || (e < n && ((mask[e >> 3] >> (e & 7)) & 1));
+            const float x = widen_bits(xb[c], T{});
+            h[c] = add_round(widen_bits(rb[c], T{}), p.thr ? (keep ? x * p.scale : 0.f) : x, T{});
+            if (e < n) st_scalar(hr, e, h[c], T{});
+            acc[c & 3] = fmaf(h[c], h[c], acc[c & 3]);
+        }
+        const float sum = row_sums<GT>(tree_sum(acc), 0.f, red[parity], 0, t).x;
+        parity ^= 1;
+        const float r = rsqrtf(sum / p.hidden_f + p.eps);
+        if (p.w != nullptr) {
+            uint32_t wb[CH];
+#pragma unroll
+            for (int c = 0; c < CH; ++c) wb[c] = c * GT + t < n ? ld_bits(p.w, c * GT + t, T{}, 2) : 0u;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) h[c] = (h[c] * r) * (widen_bits(wb[c], T{}) + p.w_bias);
+        } else {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) h[c] *= r;
+        }
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+            if (c * GT + t < n) st_scalar(yr, c * GT + t, h[c], T{});
+    }
+}
+
+// An element of dy and one of h: one register for bf16.
+struct BothBF16 {
+    uint32_t u;
+    __device__ __forceinline__ void set(uint32_t g, uint32_t h) { u = (g & 0xffffu) | (h << 16); }
+    __device__ __forceinline__ float g() const { return bf16_lo(u); }
+    __device__ __forceinline__ float h() const { return bf16_hi(u); }
+};
+struct BothF32 {
+    float a, b;
+    __device__ __forceinline__ void set(uint32_t g, uint32_t h) { a = __uint_as_float(g), b = __uint_as_float(h); }
+    __device__ __forceinline__ float g() const { return a; }
+    __device__ __forceinline__ float h() const { return b; }
+};
+__device__ __forceinline__ BothBF16 both_of(BF16) { return {}; }
+__device__ __forceinline__ BothF32 both_of(F32) { return {}; }
+
+template <typename T, int GT, int CH, bool DW>
+__global__ void __launch_bounds__(GT) drop_bwd_scalar_kernel(const DropParams p) {
+    using Both = decltype(both_of(T{}));
+    __shared__ float2 red[2][1][GT / 32];
+    extern __shared__ uint8_t masks[];   // [2][blocks_per_row], with dropout
+    const int t = threadIdx.x, n = p.units;
+    pdl_wait_for_inputs();
+    pdl_allow_dependents();
+    uint64_t seed = 0, offset = 0;
+    if (p.thr) {
+        seed = p.rng[0];
+        offset = p.rng[1];
+    }
+    float dw[DW ? CH : 1];
+#pragma unroll
+    for (int c = 0; c < (DW ? CH : 1); ++c) dw[c] = 0.f;
+    float w[CH];   // the columns' weight, for every row
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int e = c * GT + t;
+        w[c] = p.w != nullptr && e < n ? widen_bits(ld_bits(p.w, e, T{}, 2), T{}) + p.w_bias : 1.f;
+    }
+    int parity = 0;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        const int64_t off = row * p.row_bytes;
+        const void *dr = p.dh != nullptr ? static_cast<const char *>(p.dh) + off : nullptr;
+        void *outr = static_cast<char *>(p.dres) + off;
+        void *xr = p.dx != nullptr ? static_cast<char *>(p.dx) + off : nullptr;
+        const void *gr = static_cast<const char *>(p.dy) + off, *hr = static_cast<const char *>(p.h) + off;
+        Both v[CH];
+        uint32_t db[CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int e = c * GT + t;
+            const uint32_t g = e < n ? ld_bits(gr, e, T{}, 1) : 0u, h = e < n ? ld_bits(hr, e, T{}, 1) : 0u;
+            v[c].set(g, h);
+        }
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int e = c * GT + t;
+            db[c] = dr != nullptr && e < n ? ld_bits(dr, e, T{}, 1) : 0u;
+        }
+        uint8_t *mask = masks + parity * p.blocks_per_row;   // the other one may still be read
+        if (p.thr) stage_mask(p, mask, seed, offset, row);   // read after the sums' barrier
+        float sq[4] = {0.f, 0.f, 0.f, 0.f}, dot[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const float h = v[c].h();
+            const float g = v[c].g() * w[c];
+            sq[c & 3] = fmaf(h, h, sq[c & 3]);
+            dot[c & 3] = fmaf(g, h, dot[c & 3]);
+        }
+        const float2 s = row_sums<GT>(tree_sum(sq), tree_sum(dot), red[parity], 0, t);
+        parity ^= 1;
+        const float r = rsqrtf(s.x / p.hidden_f + p.eps);
+        const float m = -(r * (s.y / p.hidden_f));
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int e = c * GT + t;
+            if (e < n) {
+                const float h = v[c].h() * r;
+                const float g = v[c].g();
+                if constexpr (DW) dw[c] = fmaf(g, h, dw[c]);
+                float d = fmaf(h, m, g * w[c]);
+                if (dr != nullptr) {
+                    d = fmaf(d, r, widen_bits(db[c], T{}));
+                } else {
+                    d *= r;
+                }
+                st_scalar(outr, e, d, T{});
+                if (xr != nullptr) {
+                    if (p.thr) d = (mask[e >> 3] >> (e & 7)) & 1 ? d * p.scale : 0.f;
+                    st_scalar(xr, e, d, T{});
+                }
+            }
+        }
+    }
+    if constexpr (DW) {
+        float *out = p.partial + (int64_t)blockIdx.x * p.partial_ld;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+            if (c * GT + t < n) out[c * GT + t] = dw[c];
     }
 }
 

@@ -48,9 +48,11 @@ inline int launch_kernel(const void *fn, dim3 grid, int block, size_t smem, rmsn
 // Opt a kernel in to 226 KB of dynamic shared memory (cached per device and kernel).
 int allow_smem(int dev, const void *fn);
 
-// Sums of the columns of partial[rows0 + rows1][cols] into the I/O type: of
-// the first rows0 rows to out0, of the rest to out1 (nullable; colsum.cu).
-int launch_colsum(const float *partial, int rows0, int rows1, int64_t cols, void *out0, void *out1, int dtype,
-                  rmsnorm_stream_t stream);
+// Sums of the columns of partial[rows0 + rows1][ld] into the I/O type: of the
+// first rows0 rows to out0, of the rest to out1 (nullable).  partial is 16-byte
+// aligned, ld a multiple of 4 (what stands past the cols columns of a row must
+// be readable; it is not used).  colsum.cu.
+int launch_colsum(const float *partial, int rows0, int rows1, int64_t cols, int64_t ld, void *out0, void *out1,
+                  int dtype, rmsnorm_stream_t stream);
 
 }  // namespace rrn

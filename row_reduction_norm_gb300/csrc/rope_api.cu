@@ -134,6 +134,9 @@ struct Unit {
     int64_t get() const { return (int64_t)(bits & (~bits + 1)); }
 };
 
+// Columns of the partial sums' rows.
+int64_t partial_ld(int64_t head_dim) { return (head_dim + 3) / 4 * 4; }
+
 // Whether every byte of a tile's token rows is within 31 bits of its first.
 bool tile_reaches(int64_t a, int64_t b, int64_t c) {
     const int64_t most = INT32_MAX / rrn::kRopeMaxWarps;
@@ -224,7 +227,7 @@ int rmsnorm_qk_rope_fwd(const void *x, void *y, int64_t tokens, int64_t x_token_
 int64_t rmsnorm_qk_rope_bwd_workspace_bytes(int64_t head_dim) {
     if (head_dim <= 0 || head_dim % 2 != 0) return RMSNORM_EINVAL;
     if (head_dim > rrn::kRopeMaxDim) return RMSNORM_EUNSUPPORTED;
-    return (int64_t)kBwdMaxBlocks * 2 * head_dim * (int64_t)sizeof(float);
+    return (int64_t)kBwdMaxBlocks * 2 * partial_ld(head_dim) * (int64_t)sizeof(float);
 }
 
 int rmsnorm_qk_rope_bwd(const void *dy, const void *x, void *dx, int64_t tokens, int64_t dy_token_stride,
@@ -259,6 +262,7 @@ int rmsnorm_qk_rope_bwd(const void *dy, const void *x, void *dx, int64_t tokens,
     p.dy_stride = dy_token_stride * s;
     p.y_stride = dx_token_stride * s;
     p.partial = static_cast<float *>(dq_w != nullptr ? workspace : nullptr);
+    p.partial_ld = (int32_t)partial_ld(head_dim);
     int64_t blocks = 0;
     if (tokens > 0) {
         Unit u;
@@ -300,7 +304,8 @@ int rmsnorm_qk_rope_bwd(const void *dy, const void *x, void *dx, int64_t tokens,
         if (st != RMSNORM_OK) return st;
     }
     if (dq_w == nullptr) return RMSNORM_OK;
-    return rrn::launch_colsum(static_cast<const float *>(workspace), (int)blocks, (int)blocks, head_dim, dq_w, dk_w,
+    return rrn::launch_colsum(static_cast<const float *>(workspace), (int)blocks, (int)blocks, head_dim,
+                              partial_ld(head_dim), dq_w, dk_w,
                               dtype, stream);
 }
 

@@ -50,7 +50,8 @@ struct RopeParams {
     const void *dy;           // gradient: of the rotated rows
     void *y;                  // rotated rows (append: of the query heads); gradient: dx
     const void *q_w, *k_w;    // nullable
-    float *partial;           // gradient: [kind][blocks][D] sums of the weights' gradients, or NULL
+    float *partial;           // gradient: [kind][blocks][partial_ld] sums of the weights' gradients, or NULL
+    int32_t partial_ld;
     int64_t tokens;
     int64_t x_stride, y_stride, dy_stride;   // bytes between token rows
     int32_t q_heads, k_heads, v_heads;       // v_heads: append only
@@ -989,7 +990,7 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(Piece<T,
                 float v = 0.f;
                 for (int k = kind ? p.q_warps : 0; k < (kind ? kRopeMaxWarps : p.q_warps); ++k)
                     v += wsm[k * p.head_dim + d];
-                p.partial[((int64_t)kind * gridDim.x + blockIdx.x) * p.head_dim + d] = v;
+                p.partial[((int64_t)kind * gridDim.x + blockIdx.x) * p.partial_ld + d] = v;
             }
         }
     }

@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, 2) rope_ragged_bwd_kernel(
                 float v = 0.f;
                 for (int k = kind ? p.q_warps : 0; k < (kind ? kRopeMaxWarps : p.q_warps); ++k)
                     v += wsm[k * p.head_dim + d];
-                p.partial[((int64_t)kind * gridDim.x + blockIdx.x) * p.head_dim + d] = v;
+                p.partial[((int64_t)kind * gridDim.x + blockIdx.x) * p.partial_ld + d] = v;
             }
         }
     }
