@@ -345,10 +345,10 @@ typedef struct {
  * Fused query + key head norm and rotation in one launch: the heads, layout,
  * weights, weight_bias and eps of rmsnorm_qk_fwd, the normalised heads then
  * turned as above and rounded once.  norm = 0 turns the heads as they are (no
- * weights, no bias).  head_dim is even, at most 512 (RMSNORM_EUNSUPPORTED
- * above).  y == x (same stride) works in place; other overlaps are undefined.
+ * weights, no bias).  head_dim is even; head_dim above 512, or a token row
+ * above 2^28 elements, is RMSNORM_EUNSUPPORTED.  y == x (same stride) works in place; other overlaps are undefined.
  * Accuracy: fp32 arithmetic; the sine and cosine of the exact angle to 2e-7.
- * Pointers and strides that are multiples of 16 bytes, with rot_dim / 2 and
+ * x, y and strides that are multiples of 16 bytes, with rot_dim / 2 and
  * (head_dim - rot_dim) / 2 multiples of 16 bytes of elements, move 128 bits
  * at a time; anything else narrower, with the same results up to rounding.
  * Returns RMSNORM_OK or a negative status (RMSNORM_EINVAL also for a

@@ -319,6 +319,7 @@ def qk_norm_rope(qkv: torch.Tensor, q_heads: int, k_heads: int, head_dim: int, p
                                                  weight_bias, norm, sections, interleaved, out)
         if _took(y, "rmsnorm_qk_rope_fwd"):
             return y
+    q_heads, k_heads, head_dim = int(q_heads), int(k_heads), int(head_dim)
     t = qkv.dtype
     code = dtype_code(t)
     dev = _device_of(qkv, "qkv")
@@ -331,7 +332,7 @@ def qk_norm_rope(qkv: torch.Tensor, q_heads: int, k_heads: int, head_dim: int, p
         out = _empty((tokens, width), t, qkv.device, stream)
     ys = _head_rows(out, "out", width, tokens, t, dev)
     _launch(dev, stream, N.rmsnorm_qk_rope_fwd, qkv.data_ptr(), out.data_ptr(), tokens, xs, ys, q_heads, k_heads,
-            head_dim, qw, kw, weight_bias, eps, 1 if norm else 0, rope, code)
+            head_dim, qw, kw, float(weight_bias), float(eps), 1 if norm else 0, rope, code)
     return out
 
 
@@ -356,6 +357,7 @@ def qk_norm_rope_backward(dout: torch.Tensor, qkv: Optional[torch.Tensor], q_hea
                                                           workspace)
         if _took(r, "rmsnorm_qk_rope_bwd"):
             return r
+    q_heads, k_heads, head_dim = int(q_heads), int(k_heads), int(head_dim)
     t = dout.dtype
     code = dtype_code(t)
     dev = _device_of(dout, "dout")
@@ -379,7 +381,7 @@ def qk_norm_rope_backward(dout: torch.Tensor, qkv: Optional[torch.Tensor], q_hea
         workspace = _workspace(workspace, need, dout.device, stream)
         ws = workspace.data_ptr()
     _launch(dev, stream, N.rmsnorm_qk_rope_bwd, dout.data_ptr(), _ptr(qkv), out.data_ptr(), tokens, gs, xs, ds, q_heads,
-            k_heads, head_dim, qw, kw, dq, dk, weight_bias, eps, 1 if norm else 0, rope, code, ws, need)
+            k_heads, head_dim, qw, kw, dq, dk, float(weight_bias), float(eps), 1 if norm else 0, rope, code, ws, need)
     return out, dq_w, dk_w
 
 
@@ -436,6 +438,7 @@ def qkv_append(qkv: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
                                                norm, sections, interleaved, k_scale, v_scale, q_out, dropped)
         if _took(r, "rmsnorm_qkv_append"):
             return r
+    q_heads, kv_heads, head_dim = int(q_heads), int(kv_heads), int(head_dim)
     t = qkv.dtype
     code = dtype_code(t)
     dev = _device_of(qkv, "qkv")
@@ -474,9 +477,10 @@ def qkv_append(qkv: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     kv = N.PagedKV.from_buffer_copy(_pack_kv(
         k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), cu, lens, drop,
         p0 if seqs > 1 else max(p0, max_pages), strides[0] if shape[0] > 1 else 0, strides[1] if shape[1] > 1 else 0,
-        strides[2] if shape[2] > 1 else 0, seqs, max_pages, shape[0], shape[1], _CACHE_CODES[kind], k_scale, v_scale))
+        strides[2] if shape[2] > 1 else 0, seqs, max_pages, shape[0], shape[1], _CACHE_CODES[kind], float(k_scale),
+        float(v_scale)))
     _launch(dev, stream, N.rmsnorm_qkv_append, qkv.data_ptr(), q_at, tokens, xs, qs, q_heads, kv_heads, head_dim, qw,
-            kw, weight_bias, eps, 1 if norm else 0, rope, kv, code)
+            kw, float(weight_bias), float(eps), 1 if norm else 0, rope, kv, code)
     return q_out
 
 
@@ -536,7 +540,8 @@ def rms_norm_dropout(x: torch.Tensor, residual: torch.Tensor, p: float, rng: Opt
     if residual_out is None:
         residual_out = _empty(x.shape, x.dtype, x.device, stream)
     _launch(dev, stream, N.rmsnorm_dropout_fwd, x.data_ptr(), res, wp, _like(out, "out", x, dev),
-            _like(residual_out, "residual_out", x, dev), rows, hidden, eps, weight_bias, p, r, code)
+            _like(residual_out, "residual_out", x, dev), rows, hidden, float(eps), float(weight_bias), float(p), r,
+            code)
     return out, residual_out
 
 
@@ -575,7 +580,7 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, w: Optional[torch.Tenso
     if out is None:
         out = _empty(dy.shape, dy.dtype, dy.device, stream)
     _launch(dev, stream, N.rmsnorm_bwd, *at, _like(out, "out", dy, dev), None if dw is None else dw.data_ptr(), rows,
-            hidden, eps, weight_bias, code, ws, need)
+            hidden, float(eps), float(weight_bias), code, ws, need)
     return out, dw
 
 
@@ -599,7 +604,8 @@ def rms_norm_dropout_backward(dy: torch.Tensor, h: torch.Tensor, p: float, rng: 
     if dx is None:
         dx = _empty(dy.shape, dy.dtype, dy.device, stream)
     _launch(dev, stream, N.rmsnorm_dropout_bwd, *at, _like(dresidual, "dresidual", dy, dev), _like(dx, "dx", dy, dev),
-            None if dw is None else dw.data_ptr(), rows, hidden, eps, weight_bias, p, r, code, ws, need)
+            None if dw is None else dw.data_ptr(), rows, hidden, float(eps), float(weight_bias), float(p), r,
+            code, ws, need)
     return dresidual, dx, dw
 
 

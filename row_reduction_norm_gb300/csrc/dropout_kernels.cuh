@@ -593,10 +593,7 @@ __global__ void __launch_bounds__(BLOCK) drop_bwd_loop_kernel(const DropParams p
                 }
             }
         }
-        if (p.thr) {
-            if (BLOCK == 32) __syncwarp();
-            stage_mask(p, mask, seed, offset, row);   // read after the sums' barrier
-        }
+        if (p.thr) stage_mask(p, mask, seed, offset, row);   // read after the sums' barrier
         const float2 s = row_sums<BLOCK>(tree_sum(sq), tree_sum(dot), red[parity], 0, tid);
         parity ^= 1;
         const float r = rsqrtf(s.x / p.hidden_f + p.eps);

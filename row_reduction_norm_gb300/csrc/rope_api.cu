@@ -126,7 +126,8 @@ int pick_shape(int dtype, int64_t unit, rrn::RopeParams *p) {
 }
 
 // Largest power of two (at most 16) that divides every address and stride
-// given, in elements of `s` bytes.
+// given, in elements of `s` bytes.  (The weights are read an element at a
+// time, into tables, and have no part in it.)
 struct Unit {
     uint64_t bits = 16;
     void at(const void *ptr, int64_t s) { bits |= (uint64_t)(reinterpret_cast<uintptr_t>(ptr) / (uintptr_t)s); }
@@ -219,7 +220,7 @@ int rmsnorm_qk_rope_fwd(const void *x, void *y, int64_t tokens, int64_t x_token_
     p.y = y;
     p.y_stride = y_token_stride * s;
     Unit u;
-    u.at(x, s), u.at(y, s), u.at(q_w, s), u.at(k_w, s);
+    u.at(x, s), u.at(y, s);
     u.step(x_token_stride), u.step(y_token_stride);
     return launch_forward(&p, dtype, u.get(), rope->interleaved == 1, rrn::kRopePlain, stream);
 }
@@ -266,7 +267,7 @@ int rmsnorm_qk_rope_bwd(const void *dy, const void *x, void *dx, int64_t tokens,
     int64_t blocks = 0;
     if (tokens > 0) {
         Unit u;
-        u.at(dy, s), u.at(dx, s), u.at(q_w, s), u.at(k_w, s);
+        u.at(dy, s), u.at(dx, s);
         u.step(dy_token_stride), u.step(dx_token_stride);
         if (norm == 1) u.at(x, s), u.step(x_token_stride);
         int dev = 0, sms = 0;
@@ -368,7 +369,7 @@ int rmsnorm_qkv_append(const void *x, void *q_out, int64_t tokens, int64_t x_tok
     p.v_inv = e4m3 ? (float)(1.0 / (double)kv->v_scale) : 1.f;
     p.dropped = kv->dropped;
     Unit u;
-    u.at(x, s), u.at(q_w, s), u.at(k_w, s), u.at(kv->k_cache, c), u.at(kv->v_cache, c);
+    u.at(x, s), u.at(kv->k_cache, c), u.at(kv->v_cache, c);
     u.step(x_token_stride), u.step(kv->page_stride), u.step(kv->row_stride), u.step(kv->head_stride);
     if (q_heads > 0) u.at(q_out, s), u.step(q_token_stride);
     return launch_forward(&p, dtype, u.get(), rope->interleaved == 1, e4m3 ? rrn::kRopeAppendE4m3 : rrn::kRopeAppend,

@@ -30,10 +30,10 @@ def threshold(p):
     return int(np.floor(float(np.float32(p)) * 65536.0 + 0.5))
 
 
-def kept(rows, hidden, p, seed, offset):
-    """Boolean [rows, hidden]."""
+def kept(rows, hidden, p, seed, offset, first=0):
+    """Boolean [rows, hidden], of the rows from `first` on."""
     blocks = (hidden + 7) // 8
-    b = np.arange(rows * blocks, dtype=np.uint64)
+    b = np.arange(rows * blocks, dtype=np.uint64) + np.uint64(first * blocks)
     c = np.stack([b & np.uint64(0xFFFFFFFF), b >> np.uint64(32), np.full_like(b, offset & 0xFFFFFFFF),
                   np.full_like(b, (offset >> 32) & 0xFFFFFFFF)], -1)
     w = philox(c, (seed & 0xFFFFFFFF, (seed >> 32) & 0xFFFFFFFF))
