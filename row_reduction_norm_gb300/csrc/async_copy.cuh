@@ -19,6 +19,11 @@ __device__ __forceinline__ void copy_async(void *smem, const void *global) {
     else
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" : : "r"(to), "l"(global), "n"(BYTES) : "memory");
 }
+// The first `bytes` of 16, zeros after them.
+__device__ __forceinline__ void copy_async_part(void *smem, const void *global, uint32_t bytes) {
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(smem);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" : : "r"(to), "l"(global), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Waits until at most PENDING of the thread's groups are on their way.
 template <int PENDING>

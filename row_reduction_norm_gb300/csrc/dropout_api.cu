@@ -7,6 +7,7 @@
 
 #include "dropout_kernels.cuh"
 #include "dropout_pick.h"
+#include "dropout_shift.cuh"
 #include "launch_util.h"
 
 namespace {
@@ -80,6 +81,42 @@ bool reg_shape(int64_t nch, int max_ch, int *gt, int *ch) {
     return false;
 }
 
+// The kernel for rows of a length that is no multiple of 16 bytes, in tensors
+// that start on a 16-byte boundary, that holds a row's chunks; or -1 where the
+// rows of single elements are faster.  Starting costs the former more (weights
+// an element at a time, blocks of several rows) and a row less.  Measured on
+// GB300, us, shifted / single elements, dropout 0.1:
+//   gradient  bf16 501 x 608 rows 5.2 / 5.5, 1001 x 608 7.4 / 6.5, x 2000 11.5 /
+//             12.3, 2047 x 608 8.8 / 10.7, 8191 x 6000 125 / 313; fp32 501 x 608
+//             5.9 / 5.0, x 2000 8.4 / 9.0, 1001 x 2000 17.5 / 13.3, x 6000 29.5 /
+//             31.7, 3001 x 152 6.4 / 9.5, x 6000 65 / 95; and with a third of
+//             the chunks unused, 2047 x 6000 55.9 / 51.3
+//   forward   bf16 101 x 2000 4.3 / 3.5, x 6000 5.3 / 6.9, 2047 x 2000 12.5 /
+//             11.0, x 6000 28.9 / 30.5, 3001 x 608 6.8 / 8.1, 12001 x 6000 127 /
+//             389; fp32 101 x 6000 4.7 / 6.6, 501 x 6000 10.4 / 11.4, and wider
+//             rows no faster (1001 x 6000 19.8 / 17.5, 4095 x 6000 88 / 65)
+int shift_shape(const void *const *ptrs, int n, int64_t rows, int64_t hidden, int dtype, bool gradient) {
+    for (int i = 0; i < n; ++i)
+        if (!rrn::on_boundary(ptrs[i], 16)) return -1;
+    const bool bf16 = dtype == RMSNORM_BF16;
+    const int64_t V = 16 / rrn::size_of(dtype), chunks = (hidden + 2 * V - 2) / V;
+    if (gradient) {
+        if (!(hidden > 2048 || (hidden <= 512 && rows >= 1024) || rows >= (bf16 ? 1 << 20 : 1 << 22) / hidden)) return -1;
+    } else if (!(rows >= 4096 || (bf16 && hidden > 2048))) {
+        return -1;
+    }
+    for (int i = 0; i < (bf16 || gradient ? rrn::kDropShifts : rrn::kDropShiftsF32); ++i) {
+        const int64_t held = (int64_t)rrn::kDropShift[i].gt * rrn::kDropShift[i].ch;
+        if (chunks <= held) return bf16 || hidden <= 512 || 10 * chunks >= 7 * held ? i : -1;
+    }
+    return -1;
+}
+
+// Blocks of `groups` row groups in all, at most `most`, that keep a thread's
+// rows equally far past a boundary: a multiple of 8 (any row count is) when
+// they take more than one group each.
+int64_t shift_blocks(int64_t groups, int64_t most) { return groups <= most ? groups : most < 8 ? 8 : most / 8 * 8; }
+
 // The rows-of-single-elements kernel that holds a row, or -1.
 int scalar_shape(bool vec, int64_t hidden) {
     for (int i = 0; !vec && i < rrn::kDropScalars; ++i)
@@ -138,12 +175,22 @@ int backward(const void *dy, const void *h, const void *w, const void *dh, void 
         int threads, gt = 0, ch = 0;
         int64_t groups = rows;
         size_t smem = 0;
+        // the weight may stand anywhere: it is read an element at a time
+        const void *rows_of[] = {dy, h, dh, dres, dx};
+        const int shift = vec ? -1 : shift_shape(rows_of, 5, rows, hidden, dtype, true);
         if (vec && reg_shape(hidden / V, 4, &gt, &ch)) {
             fn = dtype == RMSNORM_BF16 ? rrn::drop_bwd_bf16(gt, ch, dw != nullptr)
                                        : rrn::drop_bwd_f32(gt, ch, dw != nullptr);
             threads = rrn::drop_block_threads(gt);
             groups = div_up(rows, threads / gt);
             smem = (size_t)rrn::drop_ring_bytes(gt, ch);
+        } else if (shift >= 0) {
+            gt = rrn::kDropShift[shift].gt;
+            fn = dtype == RMSNORM_BF16 ? rrn::drop_bwd_shift_bf16(shift, dw != nullptr)
+                                       : rrn::drop_bwd_shift_f32(shift, dw != nullptr);
+            threads = rrn::drop_block_threads(gt);
+            groups = div_up(rows, threads / gt);
+            smem = (size_t)rrn::shift_ring_bytes(gt, rrn::kDropShift[shift].ch);
         } else if (const int shape = scalar_shape(vec, hidden); shape >= 0) {
             threads = rrn::kDropScalar[shape].gt;
             fn = rrn::drop_bwd_scalar(dtype, shape, dw != nullptr);
@@ -160,7 +207,7 @@ int backward(const void *dy, const void *h, const void *w, const void *dh, void 
         if ((st = rrn::resident_blocks(dev, fn, threads, smem, &resident)) != RMSNORM_OK) return st;
         blocks = (int64_t)sms * resident;
         if (dw != nullptr && blocks > most) blocks = most;
-        if (blocks > groups) blocks = groups;
+        blocks = shift >= 0 ? shift_blocks(groups, blocks) : blocks > groups ? groups : blocks;
         void *argv[] = {&p};
         st = rrn::launch_kernel(fn, dim3((unsigned)blocks), threads, smem, stream, argv);
         if (st != RMSNORM_OK) return st;
@@ -199,10 +246,21 @@ int rmsnorm_dropout_fwd(const void *x, const void *residual, const void *w, void
     int threads, gt = 0, ch = 0;
     int64_t blocks = rows;
     size_t smem = 0;
+    const void *rows_of[] = {x, residual, y, residual_out};
+    const int shift = vec ? -1 : shift_shape(rows_of, 4, rows, hidden, dtype, false);
     if (vec && reg_shape(hidden / V, 8, &gt, &ch)) {
         fn = dtype == RMSNORM_BF16 ? rrn::drop_fwd_bf16(gt, ch) : rrn::drop_fwd_f32(gt, ch);
         threads = rrn::drop_block_threads(gt);
         blocks = div_up(rows, threads / gt);
+    } else if (shift >= 0) {
+        gt = rrn::kDropShift[shift].gt;
+        fn = rrn::drop_fwd_shift(dtype, shift);
+        threads = rrn::drop_block_threads(gt);
+        if (fn == nullptr) return RMSNORM_EINVAL;
+        int dev = 0, sms = 0, resident = 0;
+        if ((st = rrn::current_device_sms(&dev, &sms)) != RMSNORM_OK) return st;
+        if ((st = rrn::resident_blocks(dev, fn, threads, 0, &resident)) != RMSNORM_OK) return st;
+        blocks = shift_blocks(div_up(rows, threads / gt), (int64_t)sms * resident);
     } else if (const int shape = scalar_shape(vec, hidden); shape >= 0) {
         threads = rrn::kDropScalar[shape].gt;
         fn = rrn::drop_fwd_scalar(dtype, shape);

@@ -11,12 +11,19 @@ const void *drop_fwd_bf16(int gt, int ch);
 const void *drop_fwd_f32(int gt, int ch);
 const void *drop_bwd_bf16(int gt, int ch, bool dw);
 const void *drop_bwd_f32(int gt, int ch, bool dw);
-// Rows of single elements in registers: threads a row, elements a thread.
-struct DropScalar {
+// Rows on 16-byte chunks that do not start with one: threads a row, chunks a thread.
+struct DropShape {
     int gt, ch;
 };
+constexpr int kDropShifts = 11, kDropShiftsF32 = 3;   // of these for the fp32 forward
+constexpr DropShape kDropShift[kDropShifts] = {{8, 4},   {32, 2},  {32, 4},  {64, 3},  {64, 4}, {128, 3},
+                                               {128, 4}, {256, 3}, {256, 4}, {512, 3}, {512, 4}};
+const void *drop_fwd_shift(int dtype, int shape);
+const void *drop_bwd_shift_bf16(int shape, bool dw);
+const void *drop_bwd_shift_f32(int shape, bool dw);
+// Rows of single elements in registers: threads a row, elements a thread.
 constexpr int kDropScalars = 5;
-constexpr DropScalar kDropScalar[kDropScalars] = {{64, 4}, {128, 8}, {256, 8}, {256, 16}, {512, 16}};
+constexpr DropShape kDropScalar[kDropScalars] = {{64, 4}, {128, 8}, {256, 8}, {256, 16}, {512, 16}};
 const void *drop_fwd_scalar(int dtype, int shape);
 const void *drop_bwd_scalar(int dtype, int shape, bool dw);
 // Two-pass kernels: blocks of 256 (scalar only) or 1024 threads.

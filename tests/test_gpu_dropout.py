@@ -80,7 +80,7 @@ def test_many_rows_a_block(dtype, rows, hidden):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("hidden", [576, 2048, 20480])
+@pytest.mark.parametrize("hidden", [576, 1001, 2048, 8191, 20480])
 def test_unaligned_tensors_and_in_place(dtype, hidden):
     """Tensors one element off a 16-byte boundary (same values up to rounding,
     the same mask), and every allowed use of an input's buffer as an output."""
@@ -256,3 +256,65 @@ def test_python_refusals():
                  lambda: R.rms_norm_dropout_backward(x, x, 0.1, rng, dresidual=x, dx=x)):
         with pytest.raises((ValueError, N.RmsNormError)):
             call()
+
+
+# widths that are no multiple of 16 bytes: each number of chunks a thread takes, and rows a block
+@pytest.mark.parametrize("dtype,hidden", [
+    ("bf16", 7), ("bf16", 13), ("bf16", 241), ("bf16", 505), ("bf16", 1001), ("bf16", 2047), ("bf16", 2999),
+    ("bf16", 4090), ("bf16", 6001), ("bf16", 8191), ("bf16", 12001), ("bf16", 16377), ("bf16", 16379),
+    ("f32", 5), ("f32", 121), ("f32", 253), ("f32", 1001), ("f32", 1531), ("f32", 2045), ("f32", 3001), ("f32", 4093),
+    ("f32", 6002), ("f32", 8189), ("f32", 8191),
+])
+@pytest.mark.parametrize("few", [True, False])
+def test_widths_off_the_boundary(dtype, hidden, few):
+    """Rows that start anywhere between two boundaries; infinities in the rows
+    beside a finite one stay out of it, and what is behind the tensors is left alone."""
+    rows = 11 if few else 20000 if hidden < 300 else 4501 if hidden < 2100 else 701
+    t, p, g = T[dtype], 0.25, gen(hidden + rows)
+
+    def within(fill=None):   # a tensor of rows, on a boundary, with something else behind it
+        room = torch.full((rows * hidden + 64,), 7.5, dtype=t, device=DEV)
+        v = room[:rows * hidden].view(rows, hidden)
+        if fill is not None:
+            v.copy_(fill)
+        return room, v
+
+    src = [normal(g, rows, hidden, dtype=t) for _ in range(4)]
+    src[1][4] = float("inf")
+    (_, x), (_, res), (_, dy), (_, dh) = (within(v) for v in src)
+    w = normal(g, hidden + 1, dtype=t, std=0.2, mean=1.0)[1:]
+    rng = rng_of()
+    rooms = [within() for _ in range(4)]
+    y, h, dres, dx = (v for _, v in rooms)
+    R.rms_norm_dropout(x, res, p, rng, w, out=y, residual_out=h)
+    keep = ref.kept(rows, hidden, p, SEED, OFFSET)
+    want = ref.forward_h(x, res, keep, p).to(DEV)
+    fine = torch.arange(rows, device=DEV) != 4
+    assert torch.equal(h, want)
+    assert_within(y[fine], *ref.norm(want[fine], w, 1e-6, 0.0), "y")
+
+    h[4] = src[1][3]   # the gradient's rows are finite, but one of dy, which is left out of dw's
+    dy[4] = float("nan")
+    _, _, dw = R.rms_norm_dropout_backward(dy, h, p, rng, w, dh, dresidual=dres, dx=dx)
+    keep = keep.to(DEV)
+    want = ref.backward(dy[fine], h[fine], w, dh[fine], keep[fine], p, 1e-6, 0.0)
+    assert_within(dres[fine], want[0], want[1], "dresidual")
+    assert_within(dx[fine], want[2], want[3], "dx")
+    assert bool(dw.isnan().all())
+    dy[4] = 0.0
+    only, dw = R.rms_norm_backward(dy, h, w)
+    want = ref.backward(dy, h, w, None, None, 0.0, 1e-6, 0.0)
+    assert_within(only, want[0], want[1], "dx alone")
+    assert_within(dw, want[4], want[5], "dw")
+    for room, _ in rooms:
+        assert bool((room[rows * hidden:] == 7.5).all())
+    # from a place off the boundary, element by element
+    off = torch.empty(rows * hidden + 1, dtype=t, device=DEV)[1:].view(rows, hidden)
+    y2, h2 = R.rms_norm_dropout(off.copy_(x), res, p, rng, w)
+    same = R.rms_norm_dropout(x, res, p, rng, w)[1]
+    assert torch.equal(h2[fine], same[fine])
+    assert_within(y2[fine], *ref.norm(h2[fine], w, 1e-6, 0.0), "y, element by element")
+    off.copy_(dy)
+    two, dw2 = R.rms_norm_backward(off, h, w)
+    assert_within(two, want[0], want[1], "dx alone, element by element")
+    assert_within(dw2, want[4], want[5], "dw, element by element")
