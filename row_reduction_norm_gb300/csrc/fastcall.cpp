@@ -16,6 +16,8 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/Allocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -151,13 +153,20 @@ void rope_arg(rmsnorm_rope_t *r, PyObject *positions, PyObject *inv_freq, PyObje
     }
 }
 
-at::Tensor bytes_on(const at::Tensor &t, int64_t n) { return at::empty({n}, t.options().dtype(at::kByte)); }
+// A tensor of x's type and device, uninitialised.  Straight from the allocator
+// of the current stream: through the dispatcher an allocation takes 1.5 us on
+// the host, nearly a launch (the norm's gradient with a weight 7.7 -> 6.0 us of
+// host time a call, with the workspace's memory alone in place of a tensor).
+at::Tensor fresh(at::IntArrayRef size, const at::Tensor &x) {
+    return at::Tensor(at::detail::empty_cuda(size, x.scalar_type(), x.device(), std::nullopt));
+}
 
-// A workspace given, or made.
-void *workspace_of(PyObject *given, int64_t n, const at::Tensor &x, const Where &w, at::Tensor *made) {
+// A workspace given, or made (memory of the current stream, handed back when
+// the call is over and used again only behind it).
+void *workspace_of(PyObject *given, int64_t n, const Where &w, c10::DataPtr *made) {
     if (given == Py_None) {
-        *made = bytes_on(x, n);
-        return made->data_ptr();
+        *made = c10::GetAllocator(c10::kCUDA)->allocate((size_t)n);
+        return made->get();
     }
     const at::Tensor &t = tensor(given);
     need(t.get_device() == w.dev && t.is_contiguous() && t.numel() * (int64_t)t.element_size() >= n);
@@ -204,7 +213,7 @@ PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
         need(a[4] != Py_None);
         rope_arg(&rope, a[4], a[5], a[11], a[12], tokens, d, w);
         at::Tensor made;
-        if (a[13] == Py_None) made = at::empty({tokens, width}, x.options());
+        if (a[13] == Py_None) made = fresh({tokens, width}, x);
         const at::Tensor &y = made.defined() ? made : tensor(a[13]);
         const int64_t ys = head_rows(y, width, tokens, x.scalar_type(), w);
         const int st = qk_rope_fwd(x.data_ptr(), y.data_ptr(), tokens, xs, ys, q, k, d, qw, kw, real(a[9]), real(a[8]),
@@ -238,8 +247,9 @@ PyObject *qk_norm_rope_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         rmsnorm_rope_t rope;
         need(a[5] != Py_None);
         rope_arg(&rope, a[5], a[6], a[12], a[13], tokens, d, w);
-        at::Tensor made, dq, dk, ws;
-        if (a[14] == Py_None) made = at::empty({tokens, width}, g.options());
+        at::Tensor made, dq, dk;
+        c10::DataPtr ws;
+        if (a[14] == Py_None) made = fresh({tokens, width}, g);
         const at::Tensor &y = made.defined() ? made : tensor(a[14]);
         const int64_t ys = head_rows(y, width, tokens, g.scalar_type(), w);
         void *at_ws = nullptr;
@@ -247,9 +257,9 @@ PyObject *qk_norm_rope_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (qw != nullptr && kw != nullptr) {
             bytes = qk_rope_bwd_workspace_bytes(d);
             need(bytes > 0);
-            dq = at::empty({d}, g.options());
-            dk = at::empty({d}, g.options());
-            at_ws = workspace_of(a[15], bytes, g, w, &ws);
+            dq = fresh({d}, g);
+            dk = fresh({d}, g);
+            at_ws = workspace_of(a[15], bytes, w, &ws);
         }
         const int st = qk_rope_bwd(g.data_ptr(), x, y.data_ptr(), tokens, gs, xs, ys, q, k, d, qw, kw,
                                    dq.defined() ? dq.data_ptr() : nullptr, dk.defined() ? dk.data_ptr() : nullptr,
@@ -307,7 +317,7 @@ PyObject *qkv_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
         kv.k_scale = real(a[18]);
         kv.v_scale = real(a[19]);
         at::Tensor made;
-        if (a[20] == Py_None) made = at::empty({tokens, (int64_t)q * d}, x.options());
+        if (a[20] == Py_None) made = fresh({tokens, (int64_t)q * d}, x);
         const at::Tensor &y = made.defined() ? made : tensor(a[20]);
         const int64_t ys = head_rows(y, (int64_t)q * d, tokens, x.scalar_type(), w);
         const int st = qkv_append_fn(x.data_ptr(), y.data_ptr(), tokens, xs, ys, q, kv_heads, d, qw, kw, real(a[14]),
@@ -347,8 +357,8 @@ PyObject *rms_norm_dropout(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const uint64_t *rng = rng_of(a[3], p, w);
         void *weight = vector(a[4], r.hidden, x.scalar_type(), w);
         at::Tensor y, h;
-        if (a[7] == Py_None) y = at::empty(x.sizes(), x.options());
-        if (a[8] == Py_None) h = at::empty(x.sizes(), x.options());
+        if (a[7] == Py_None) y = fresh(x.sizes(), x);
+        if (a[8] == Py_None) h = fresh(x.sizes(), x);
         void *yp = y.defined() ? y.data_ptr() : like(tensor(a[7]), x, w);
         void *hp = h.defined() ? h.data_ptr() : like(tensor(a[8]), x, w);
         const int st = dropout_fwd(x.data_ptr(), res, weight, yp, hp, r.rows, r.hidden, real(a[5]), real(a[6]), p, rng,
@@ -366,7 +376,8 @@ struct Backward {
     Where w;
     Rows r;
     void *h, *weight, *dh;
-    at::Tensor dw, ws;
+    at::Tensor dw;
+    c10::DataPtr ws;
     void *at_ws = nullptr;
     int64_t bytes = 0;
     Backward(PyObject *dy_, PyObject *h_, PyObject *w_, PyObject *dh_, PyObject *workspace)
@@ -375,8 +386,8 @@ struct Backward {
         if (weight == nullptr) return;
         bytes = bwd_workspace_bytes(r.rows, r.hidden, code);
         need(bytes > 0);
-        dw = at::empty({r.hidden}, dy.options());
-        at_ws = workspace_of(workspace, bytes, dy, w, &ws);
+        dw = fresh({r.hidden}, dy);
+        at_ws = workspace_of(workspace, bytes, w, &ws);
     }
     void *dw_at() const { return dw.defined() ? dw.data_ptr() : nullptr; }
 };
@@ -387,7 +398,7 @@ PyObject *rms_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         need(n == 8 && norm_bwd != nullptr);
         Backward b(a[0], a[1], a[2], a[3], a[7]);
         at::Tensor made;
-        if (a[6] == Py_None) made = at::empty(b.dy.sizes(), b.dy.options());
+        if (a[6] == Py_None) made = fresh(b.dy.sizes(), b.dy);
         void *dx = made.defined() ? made.data_ptr() : like(tensor(a[6]), b.dy, b.w);
         const int st = norm_bwd(b.dy.data_ptr(), b.h, b.weight, b.dh, dx, b.dw_at(), b.r.rows, b.r.hidden, real(a[4]),
                                 real(a[5]), b.code, b.at_ws, (uint64_t)b.bytes, b.w.stream());
@@ -404,8 +415,8 @@ PyObject *rms_norm_dropout_backward(PyObject *, PyObject *const *a, Py_ssize_t n
         const float p = real(a[2]);
         const uint64_t *rng = rng_of(a[3], p, b.w);
         at::Tensor dres, dx;
-        if (a[8] == Py_None) dres = at::empty(b.dy.sizes(), b.dy.options());
-        if (a[9] == Py_None) dx = at::empty(b.dy.sizes(), b.dy.options());
+        if (a[8] == Py_None) dres = fresh(b.dy.sizes(), b.dy);
+        if (a[9] == Py_None) dx = fresh(b.dy.sizes(), b.dy);
         void *rp = dres.defined() ? dres.data_ptr() : like(tensor(a[8]), b.dy, b.w);
         void *xp = dx.defined() ? dx.data_ptr() : like(tensor(a[9]), b.dy, b.w);
         const int st = dropout_bwd(b.dy.data_ptr(), b.h, b.weight, b.dh, rp, xp, b.dw_at(), b.r.rows, b.r.hidden,

@@ -38,9 +38,11 @@ constexpr int kRopeMaxDim = 512;      // head_dim
 constexpr int kRopeMaxAxes = 4;
 constexpr int kRopeMaxWarps = 8;      // warps a block
 // Blocks a SM that a shape's registers are budgeted for.  Measured on GB300,
-// bf16 8192 tokens x 40 heads of 128: the forward 31.0 us with four blocks
-// (64 registers a thread), 32.5 with three, 38.7 with five (which spill); the
-// gradient 63.5 us with two, 75.5 with three.
+// bf16 8192 tokens x 40 heads of 128, when the factors had moved to shared
+// memory: the forward 31.0 us with four blocks (64 registers a thread), 32.5
+// with three, 38.7 with five (which spill); the gradient 63.5 us with two, 75.5
+// with three.  Kernels of their own for whole heads and the gradient's ring
+// took them to 30.4 and 43.4 us.
 // bytes: of a piece.
 __host__ __device__ constexpr int rope_resident(int bytes, int k) { return bytes * k <= 16 && bytes >= 4 ? 4 : 2; }
 __host__ __device__ constexpr int rope_bwd_resident(int bytes, int k) { return bytes * k <= 16 && bytes >= 4 ? 2 : 1; }
