@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(drop_block_threads(GT), GT < 512 ? 3 : 1) drop
 // 8191 167 (213 and 419 by single elements; aligned 8192 x 8192 rows 107):
 // what bounds it is issue slots, about 350 instructions for 32 chunks.
 template <typename T, int GT, int CH, bool DW>
-__global__ void __launch_bounds__(drop_block_threads(GT), GT < 512 ? 2 : 1) drop_bwd_shift_kernel(const DropParams p) {
+__global__ void __launch_bounds__(drop_block_threads(GT), drop_bwd_resident(GT)) drop_bwd_shift_kernel(const DropParams p) {
     constexpr int V = T::kVec, S = 16 / V, BLOCK = drop_block_threads(GT), RPB = BLOCK / GT;
     __shared__ float2 red[2][RPB][GT > 32 ? GT / 32 : 1];
     extern __shared__ __align__(16) Chunk ring[];   // [stage][dy, h, dh][CH][BLOCK], then the masks' bytes [2][RPB][GT CH + 1]

@@ -276,18 +276,29 @@ int rmsnorm_qk_rope_bwd(const void *dy, const void *x, void *dx, int64_t tokens,
         const bool il = rope->interleaved == 1;
         const void *fn = backward_kernel(dtype, shape, il, norm == 1, whole_head(&p));
         if (fn == nullptr) return RMSNORM_EINVAL;
-        p.iters = (int32_t)div_up(q_heads, p.heads_a_warp);
-        p.iters_k = (int32_t)div_up(k_heads, p.heads_a_warp);
-        p.tile = tile_reaches(p.dy_stride, p.y_stride, norm == 1 ? p.x_stride : 0) ? rrn::kRopeMaxWarps : 1;
+        const int64_t iters_q = div_up(q_heads, p.heads_a_warp), iters_k = div_up(k_heads, p.heads_a_warp);
         const size_t smem = backward_smem(dtype, shape, norm == 1);
         int resident = 0;
         if (smem > 48 * 1024 && (st = rrn::allow_smem(dev, fn)) != RMSNORM_OK) return st;
         if ((st = rrn::resident_blocks(dev, fn, 32 * rrn::kRopeMaxWarps, smem, &resident)) != RMSNORM_OK) return st;
         int64_t most = (int64_t)sms * resident;
         if (most > kBwdMaxBlocks) most = kBwdMaxBlocks;
-        blocks = tokens < most ? tokens : most;
-        p.each = tokens / blocks;
-        p.extra = tokens % blocks;
+        // fewer tokens than blocks: a token's heads in slices, one head
+        // iteration a warp where that many blocks fit (2 tokens of 56 bf16
+        // heads of 128, 10 elements turned: 10.3 -> 7.5 us)
+        int64_t slices = 1;
+        if (tokens < most) {
+            slices = most / tokens;
+            const int64_t enough = div_up(iters_q + iters_k, rrn::kRopeMaxWarps);
+            if (slices > enough) slices = enough;
+        }
+        p.iters = (int32_t)div_up(iters_q, slices);
+        p.iters_k = (int32_t)div_up(iters_k, slices);
+        p.slices = (int32_t)slices;
+        p.tile = slices == 1 && tile_reaches(p.dy_stride, p.y_stride, norm == 1 ? p.x_stride : 0) ? rrn::kRopeMaxWarps : 1;
+        blocks = tokens * slices < most ? tokens * slices : most;
+        p.each = tokens * slices / blocks;
+        p.extra = tokens * slices % blocks;
         // the split of a block's warps that leaves the longer of the two kinds
         // the fewest head iterations a warp and tile
         int64_t best = INT64_MAX;

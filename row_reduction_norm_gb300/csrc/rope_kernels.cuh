@@ -42,10 +42,14 @@ constexpr int kRopeMaxWarps = 8;      // warps a block
 // memory: the forward 31.0 us with four blocks (64 registers a thread), 32.5
 // with three, 38.7 with five (which spill); the gradient 63.5 us with two, 75.5
 // with three.  Kernels of their own for whole heads and the gradient's ring
-// took them to 30.4 and 43.4 us.
+// took them to 30.4 and 43.5 us.
 // bytes: of a piece.
 __host__ __device__ constexpr int rope_resident(int bytes, int k) { return bytes * k <= 16 && bytes >= 4 ? 4 : 2; }
-__host__ __device__ constexpr int rope_bwd_resident(int bytes, int k) { return bytes * k <= 16 && bytes >= 4 ? 2 : 1; }
+// The gradient has 112 registers a thread where two blocks fit: what they leave
+// is a block of the column sums' (256 threads of 32), which then stands ready
+// when they end.  One register more cost 0.6 us (43.6 -> 44.2 us; 2326 tokens x
+// 4 heads 6.7 -> 7.4 us).
+__host__ __device__ constexpr int rope_bwd_registers(int bytes, int k) { return bytes * k <= 16 && bytes >= 4 ? 112 : 255; }
 
 struct RopeParams {
     const void *x;            // packed token rows (query, key, [value] heads)
@@ -70,8 +74,8 @@ struct RopeParams {
     int32_t units, rot_units; // pair units of a head, and the rotated ones among them
     int32_t lanes;            // G: lanes a head
     int32_t heads_a_warp;     // 32 / G, of one head iteration
-    int32_t iters, iters_k;   // head iterations a job (gradient: a token's query heads, its key heads)
-    int32_t slices, tile;     // forward: jobs a token; jobs a tile (1 or kRopeMaxWarps)
+    int32_t iters, iters_k;   // head iterations a job (gradient: of query heads, of key heads)
+    int32_t slices, tile;     // jobs a token; jobs a tile (1 or kRopeMaxWarps)
     int32_t q_warps;          // gradient: warps of a block that take the query heads
     int64_t each, extra;      // a block's run of jobs: each, one more for the first `extra`
     // paged cache (append)
@@ -759,7 +763,7 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(Piece<T, VE>
 // the sizes and the grid: no atomics.
 // x is read only with the norm; without it dx = dy turned back.
 template <typename T, int VE, int K, bool IL, bool NORM, int HD>
-__global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(Piece<T, VE>::kBytes, K)) rope_bwd_kernel(const RopeParams p) {
+__global__ void __maxnreg__(rope_bwd_registers(Piece<T, VE>::kBytes, K)) rope_bwd_kernel(const RopeParams p) {
     using P = Piece<T, VE>;
     using Raw = typename P::Raw;
     constexpr int S = (int)sizeof(typename T::storage);
@@ -783,13 +787,22 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(Piece<T,
     jobs.set(blockIdx.x, p.each, p.extra);
     const uint32_t head0 = key ? (uint32_t)p.q_heads * head_bytes : 0u;
     const float *w = wsm + (key ? 2 * kRopeTable : 0);
+    // With few tokens a block has one slice of one token's heads: the token is
+    // job - skip, the slice's first iteration i0.
+    int64_t skip = 0;
+    int i0 = 0;
+    if (p.slices > 1) {
+        const uint32_t token = (uint32_t)jobs.first / (uint32_t)p.slices;
+        i0 = (int)((uint32_t)jobs.first - token * (uint32_t)p.slices) * iters;
+        skip = jobs.first - token;
+    }
     // The block's first token row into L2 before the wait (bf16 8192 tokens x
     // 40 heads of 128 44.6 -> 44.0 us; more rows, or rows in the forward, did
     // not pay).
     if (P::kBytes == 16 && threadIdx.x == 0 && jobs.first < jobs.last) {
         const uint32_t bytes = (uint32_t)(p.q_heads + p.k_heads) * head_bytes;
-        prefetch_l2(static_cast<const char *>(p.dy) + jobs.first * p.dy_stride, bytes);
-        if constexpr (NORM) prefetch_l2(static_cast<const char *>(p.x) + jobs.first * p.x_stride, bytes);
+        prefetch_l2(static_cast<const char *>(p.dy) + (jobs.first - skip) * p.dy_stride, bytes);
+        if constexpr (NORM) prefetch_l2(static_cast<const char *>(p.x) + (jobs.first - skip) * p.x_stride, bytes);
     }
 
     pdl_wait_for_inputs();
@@ -815,13 +828,14 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(Piece<T,
     int buf = 0;
     for (int64_t base = jobs.first; base < jobs.last; base += p.tile, buf ^= 1) {
         const int n = jobs.last - base < p.tile ? (int)(jobs.last - base) : p.tile;
-        const char *tg = static_cast<const char *>(p.dy) + base * p.dy_stride + head0;
-        const char *tx = static_cast<const char *>(p.x) + base * p.x_stride + head0;
-        char *ty = static_cast<char *>(p.y) + base * p.y_stride + head0;
+        const int64_t token0 = base - skip;
+        const char *tg = static_cast<const char *>(p.dy) + token0 * p.dy_stride + head0;
+        const char *tx = static_cast<const char *>(p.x) + token0 * p.x_stride + head0;
+        char *ty = static_cast<char *>(p.y) + token0 * p.y_stride + head0;
         Tile at{0, key ? warp - p.q_warps : warp};
         at.settle(n, iters);
         auto load = [&]() {
-            int h = at.i * hpw + group;
+            int h = (i0 + at.i) * hpw + group;
             h = h < heads ? h : heads - 1;
             const uint32_t go = (uint32_t)at.j * (uint32_t)p.dy_stride + (uint32_t)h * head_bytes;
             const uint32_t xo = (uint32_t)at.j * (uint32_t)p.x_stride + (uint32_t)h * head_bytes;
@@ -849,7 +863,7 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(Piece<T,
         if (at.j < n) load();
         if constexpr (ASYNC) copy_async_commit();
         if (!prepared) {
-            if (base + warp < jobs.last) pos = lane_position(p, lane, base + warp);
+            if (base + warp < jobs.last) pos = lane_position(p, lane, token0 + warp);
             make_fractions<VE>(p, frac);
             if constexpr (NORM) make_weights<T, VE, IL>(p, wsm);
             __syncthreads();
@@ -857,7 +871,7 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(Piece<T,
         }
         if (warp < n)
             make_angles<VE, IL>(p, frac, tiles + (buf * kRopeMaxWarps + warp) * 2 * kRopeTable, lane, pos);
-        if (base + p.tile + warp < jobs.last) pos = lane_position(p, lane, base + p.tile + warp);   // the next tile's
+        if (base + p.tile + warp < jobs.last) pos = lane_position(p, lane, token0 + p.tile + warp);   // the next tile's
         __syncthreads();   // two buffers: the tile before this one may still be read
         while (at.j < n) {
             Raw ea[K], eb[K], ya[KN], yb[KN];
@@ -867,7 +881,7 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_bwd_resident(Piece<T,
 #pragma unroll
                 for (int k = 0; k < KN; ++k) ya[k] = xa[k], yb[k] = xb[k];
             }
-            const int job = at.j, h = at.i * hpw + group;
+            const int job = at.j, h = (i0 + at.i) * hpw + group;
             at.i += mates;
             at.settle(n, iters);
             stage ^= 1;

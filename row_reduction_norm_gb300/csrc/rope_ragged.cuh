@@ -327,6 +327,13 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, 2) rope_ragged_bwd_kernel(
     jobs.set(blockIdx.x, p.each, p.extra);
     const uint32_t head0 = key ? (uint32_t)p.q_heads * head_bytes : 0u;
     const float *w = wsm + (key ? 2 * kRopeTable : 0) + table_at<VE>(my.unit, 0);
+    int64_t skip = 0;   // see rope_bwd_kernel
+    int i0 = 0;
+    if (p.slices > 1) {
+        const uint32_t token = (uint32_t)jobs.first / (uint32_t)p.slices;
+        i0 = (int)((uint32_t)jobs.first - token * (uint32_t)p.slices) * iters;
+        skip = jobs.first - token;
+    }
 
     pdl_wait_for_inputs();
     pdl_allow_dependents();
@@ -341,18 +348,19 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, 2) rope_ragged_bwd_kernel(
     int buf = 0;
     for (int64_t base = jobs.first; base < jobs.last; base += p.tile, buf ^= 1) {
         const int n = jobs.last - base < p.tile ? (int)(jobs.last - base) : p.tile;
-        const char *tg = static_cast<const char *>(p.dy) + base * p.dy_stride + head0;
-        const char *tx = static_cast<const char *>(p.x) + base * p.x_stride + head0;
-        char *ty = static_cast<char *>(p.y) + base * p.y_stride + head0;
+        const int64_t token0 = base - skip;
+        const char *tg = static_cast<const char *>(p.dy) + token0 * p.dy_stride + head0;
+        const char *tx = static_cast<const char *>(p.x) + token0 * p.x_stride + head0;
+        char *ty = static_cast<char *>(p.y) + token0 * p.y_stride + head0;
         Tile at{0, key ? warp - p.q_warps : warp};
         at.settle(n, iters);
         Raw next_g[2], next_x[2];
         auto chunks_at = [&]() {
-            const int left = heads - at.i * hpw;
+            const int left = heads - (i0 + at.i) * hpw;
             return (left < hpw ? left : hpw) * head_chunks;
         };
         auto load = [&]() {
-            const uint32_t off = (uint32_t)(at.i * hpw) * head_bytes;
+            const uint32_t off = (uint32_t)((i0 + at.i) * hpw) * head_bytes;
             const char *gs = tg + ((uint32_t)at.j * (uint32_t)p.dy_stride + off);
             const char *xs = tx + ((uint32_t)at.j * (uint32_t)p.x_stride + off);
             const int n16 = chunks_at();
@@ -365,7 +373,7 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, 2) rope_ragged_bwd_kernel(
         };
         if (at.j < n) load();
         if (!prepared) {
-            if (base + warp < jobs.last) pos = lane_position(p, lane, base + warp);
+            if (base + warp < jobs.last) pos = lane_position(p, lane, token0 + warp);
             make_fractions<VE>(p, frac);
             if constexpr (NORM) make_weights<T, VE, IL>(p, wsm);
             __syncthreads();
@@ -373,10 +381,10 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, 2) rope_ragged_bwd_kernel(
         }
         if (warp < n)
             make_angles<VE, IL>(p, frac, tiles + (buf * kRopeMaxWarps + warp) * 2 * kRopeTable, lane, pos);
-        if (base + p.tile + warp < jobs.last) pos = lane_position(p, lane, base + p.tile + warp);
+        if (base + p.tile + warp < jobs.last) pos = lane_position(p, lane, token0 + p.tile + warp);
         __syncthreads();   // two buffers: the tile before this one may still be read
         while (at.j < n) {
-            const int job = at.j, first = at.i * hpw, h = first + group, n16 = chunks_at();
+            const int job = at.j, first = (i0 + at.i) * hpw, h = first + group, n16 = chunks_at();
 #pragma unroll
             for (int l = 0; l < 2; ++l)
                 if (lane + 32 * l < n16) {

@@ -191,3 +191,25 @@ def test_threads_on_their_own_streams():
     for t in threads:
         t.join()
     assert not errors
+
+
+# a token's heads in slices over the blocks: whole pieces, narrow ones, heads through shared memory
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("tokens,q,k", [(1, 48, 12), (2, 5, 64), (7, 64, 0), (29, 33, 31), (151, 40, 9)])
+@pytest.mark.parametrize("d,rot", [(128, 128), (72, 48), (80, 20), (34, 34)])
+def test_few_tokens_of_many_heads(dtype, tokens, q, k, d, rot):
+    g, qkv, pos, f, qw, kw = inputs(dtype, tokens, q, k, d, rot, (rot // 2,), tokens + d)
+    dy = normal(g, tokens, (q + k) * d, dtype=T[dtype])
+    theta = ref.phases(pos, f, (rot // 2,))
+    y = R.qk_norm_rope(qkv, q, k, d, pos, f, qw, kw)
+    ref.assert_within(y, *ref.forward(qkv, q, k, d, theta, rot, False, qw, kw, 1e-6, 0.0, True), "y")
+    got = R.qk_norm_rope_backward(dy, qkv, q, k, d, pos, f, qw, kw)
+    want = ref.backward(dy, qkv, q, k, d, theta, rot, False, qw, kw, 1e-6, 0.0, True)
+    for i, name in enumerate(("dx", "dq_w", "dk_w")):
+        ref.assert_within(got[i], want[2 * i], want[2 * i + 1], name)
+    dx = R.qk_norm_rope_backward(dy, None, q, k, d, pos, f, norm=False, out=dy)[0]   # in place
+    assert dx is dy
+    back = ref.rotate(want[0].new_tensor(0.0) + y.double().reshape(tokens, q + k, d), theta, d, rot, False, back=True)
+    again = R.qk_norm_rope_backward(y, None, q, k, d, pos, f, norm=False)[0]
+    ref.assert_within(again, back[0], 32 * ref.U * back[1] + ref.half_step(T[dtype]) * (1 + 32 * ref.U) * back[0].abs(),
+                      "turned back")
