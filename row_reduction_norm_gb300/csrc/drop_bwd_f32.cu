@@ -17,13 +17,16 @@ const void *of_ch(int ch) {
 }
 
 template <typename T, int GT>
-const void *of_dw(int ch, bool dw) {
+const void *of_dw(int ch, int dw) {
+    if (dw == 2)
+        return ch == 2 ? reinterpret_cast<const void *>(&drop_bwd_kernel<T, GT, 2, true, true>)
+                       : reinterpret_cast<const void *>(&drop_bwd_kernel<T, GT, 4, true, true>);
     return dw ? of_ch<T, GT, true>(ch) : of_ch<T, GT, false>(ch);
 }
 
 }  // namespace
 
-const void *drop_bwd_f32(int gt, int ch, bool dw) {
+const void *drop_bwd_f32(int gt, int ch, int dw) {
     switch (gt) {
         case 8: return of_dw<F32, 8>(ch, dw);
         case 32: return of_dw<F32, 32>(ch, dw);

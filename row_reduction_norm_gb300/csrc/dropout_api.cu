@@ -179,10 +179,11 @@ int backward(const void *dy, const void *h, const void *w, const void *dh, void 
         const void *rows_of[] = {dy, h, dh, dres, dx};
         const int shift = vec ? -1 : shift_shape(rows_of, 5, rows, hidden, dtype, true);
         if (vec && reg_shape(hidden / V, 4, &gt, &ch)) {
-            fn = dtype == RMSNORM_BF16 ? rrn::drop_bwd_bf16(gt, ch, dw != nullptr)
-                                       : rrn::drop_bwd_f32(gt, ch, dw != nullptr);
             threads = rrn::drop_block_threads(gt);
             groups = div_up(rows, threads / gt);
+            const int part = dw == nullptr ? 0 : groups <= rrn::kFinishBlocks ? 2 : 1;
+            if (part == 2) ch = ch <= 2 ? 2 : 4;
+            fn = dtype == RMSNORM_BF16 ? rrn::drop_bwd_bf16(gt, ch, part) : rrn::drop_bwd_f32(gt, ch, part);
             smem = (size_t)rrn::drop_ring_bytes(gt, ch);
         } else if (shift >= 0) {
             gt = rrn::kDropShift[shift].gt;
@@ -207,10 +208,13 @@ int backward(const void *dy, const void *h, const void *w, const void *dh, void 
         if ((st = rrn::resident_blocks(dev, fn, threads, smem, &resident)) != RMSNORM_OK) return st;
         blocks = (int64_t)sms * resident;
         if (dw != nullptr && blocks > most) blocks = most;
+        // few row groups, a block each: a single cluster, which adds dw up itself
+        const bool alone = dw != nullptr && groups <= rrn::kFinishBlocks;
         blocks = shift >= 0 ? shift_blocks(groups, blocks) : blocks > groups ? groups : blocks;
+        if (alone) p.dw = dw;
         void *argv[] = {&p};
-        st = rrn::launch_kernel(fn, dim3((unsigned)blocks), threads, smem, stream, argv);
-        if (st != RMSNORM_OK) return st;
+        st = rrn::launch_kernel(fn, dim3((unsigned)blocks), threads, smem, stream, argv, alone ? (int)blocks : 1);
+        if (st != RMSNORM_OK || alone) return st;
     }
     if (dw == nullptr) return RMSNORM_OK;
     return rrn::launch_colsum(static_cast<const float *>(workspace), (int)blocks, 0, hidden, partial_ld(hidden), dw, nullptr,

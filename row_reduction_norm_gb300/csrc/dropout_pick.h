@@ -9,8 +9,10 @@ constexpr int kDropGT[6] = {8, 32, 64, 128, 256, 512};
 
 const void *drop_fwd_bf16(int gt, int ch);
 const void *drop_fwd_f32(int gt, int ch);
-const void *drop_bwd_bf16(int gt, int ch, bool dw);
-const void *drop_bwd_f32(int gt, int ch, bool dw);
+// dw: 0 no gradient of the weight, 1 its partial sums, 2 all of it by a single
+// cluster (2 or 4 chunks a thread).
+const void *drop_bwd_bf16(int gt, int ch, int dw);
+const void *drop_bwd_f32(int gt, int ch, int dw);
 // Rows on 16-byte chunks that do not start with one: threads a row, chunks a thread.
 struct DropShape {
     int gt, ch;

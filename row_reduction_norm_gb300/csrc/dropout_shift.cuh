@@ -382,6 +382,7 @@ __global__ void __launch_bounds__(drop_block_threads(GT), drop_bwd_resident(GT))
             }
             out[i] = v;
         }
+        finish_dw<T>(p);
     }
 }
 

@@ -27,17 +27,22 @@ inline bool on_boundary(const void *p, int64_t bytes) {
 
 // Launch with programmatic stream serialisation (every kernel of the library
 // waits for the work before it through griddepcontrol before it touches memory).
-inline int launch_kernel(const void *fn, dim3 grid, int block, size_t smem, rmsnorm_stream_t stream, void **argv) {
-    cudaLaunchAttribute attr[1];
+// cluster: blocks of a thread-block cluster.
+inline int launch_kernel(const void *fn, dim3 grid, int block, size_t smem, rmsnorm_stream_t stream, void **argv,
+                         int cluster = 1) {
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     if (cudaLaunchKernelExC(&cfg, fn, argv) != cudaSuccess) {
         (void)cudaGetLastError();   // clear the non-sticky launch error
         return RMSNORM_ECUDA;

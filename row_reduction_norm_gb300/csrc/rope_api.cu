@@ -286,6 +286,11 @@ int rmsnorm_qk_rope_bwd(const void *dy, const void *x, void *dx, int64_t tokens,
         // fewer tokens than blocks: a token's heads in slices, one head
         // iteration a warp where that many blocks fit (2 tokens of 56 bf16
         // heads of 128, 10 elements turned: 10.3 -> 7.5 us)
+        // With weights, up to two iterations a warp of a single cluster: it
+        // adds the weights' gradients up itself.
+        const bool alone = dq_w != nullptr && tokens * (iters_q + iters_k) <=
+                                                  2 * rrn::kFinishBlocks * rrn::kRopeMaxWarps;
+        if (alone && most > rrn::kFinishBlocks) most = rrn::kFinishBlocks;
         int64_t slices = 1;
         if (tokens < most) {
             slices = most / tokens;
@@ -311,9 +316,11 @@ int rmsnorm_qk_rope_bwd(const void *dy, const void *x, void *dx, int64_t tokens,
                 p.q_warps = qw;
             }
         }
+        if (alone) p.dq_w = dq_w, p.dk_w = dk_w;
         void *argv[] = {&p};
-        st = rrn::launch_kernel(fn, dim3((unsigned)blocks), 32 * rrn::kRopeMaxWarps, smem, stream, argv);
-        if (st != RMSNORM_OK) return st;
+        st = rrn::launch_kernel(fn, dim3((unsigned)blocks), 32 * rrn::kRopeMaxWarps, smem, stream, argv,
+                                alone ? (int)blocks : 1);
+        if (st != RMSNORM_OK || alone) return st;
     }
     if (dq_w == nullptr) return RMSNORM_OK;
     return rrn::launch_colsum(static_cast<const float *>(workspace), (int)blocks, (int)blocks, head_dim,

@@ -30,6 +30,7 @@
 #pragma once
 
 #include "async_copy.cuh"
+#include "finish.cuh"
 #include "rmsnorm_kernels.cuh"
 
 namespace rrn {
@@ -57,6 +58,7 @@ struct RopeParams {
     void *y;                  // rotated rows (append: of the query heads); gradient: dx
     const void *q_w, *k_w;    // nullable
     float *partial;           // gradient: [kind][blocks][partial_ld] sums of the weights' gradients, or NULL
+    void *dq_w, *dk_w;        // gradient of a single cluster: the weights' gradients, or NULL
     int32_t partial_ld;
     int64_t tokens;
     int64_t x_stride, y_stride, dy_stride;   // bytes between token rows
@@ -1007,6 +1009,13 @@ __global__ void __maxnreg__(rope_bwd_registers(Piece<T, VE>::kBytes, K)) rope_bw
                 for (int k = kind ? p.q_warps : 0; k < (kind ? kRopeMaxWarps : p.q_warps); ++k)
                     v += wsm[k * p.head_dim + d];
                 p.partial[((int64_t)kind * gridDim.x + blockIdx.x) * p.partial_ld + d] = v;
+            }
+            if (p.dq_w != nullptr) {   // few blocks: one cluster
+                behind_the_cluster();
+                const int mine = (int)(blockIdx.x * blockDim.x + threadIdx.x), all = (int)(gridDim.x * blockDim.x);
+                finish_columns<T>(p.partial, (int)gridDim.x, p.partial_ld, p.head_dim, p.dq_w, mine, all);
+                finish_columns<T>(p.partial + (int64_t)gridDim.x * p.partial_ld, (int)gridDim.x, p.partial_ld, p.head_dim,
+                                  p.dk_w, mine, all);
             }
         }
     }

@@ -466,6 +466,13 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, 2) rope_ragged_bwd_kernel(
                     v += wsm[k * p.head_dim + d];
                 p.partial[((int64_t)kind * gridDim.x + blockIdx.x) * p.partial_ld + d] = v;
             }
+            if (p.dq_w != nullptr) {   // few blocks: one cluster
+                behind_the_cluster();
+                const int mine = (int)(blockIdx.x * blockDim.x + threadIdx.x), all = (int)(gridDim.x * blockDim.x);
+                finish_columns<T>(p.partial, (int)gridDim.x, p.partial_ld, p.head_dim, p.dq_w, mine, all);
+                finish_columns<T>(p.partial + (int64_t)gridDim.x * p.partial_ld, (int)gridDim.x, p.partial_ld, p.head_dim,
+                                  p.dk_w, mine, all);
+            }
         }
     }
 }
