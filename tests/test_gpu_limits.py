@@ -213,3 +213,81 @@ def test_few_tokens_of_many_heads(dtype, tokens, q, k, d, rot):
     again = R.qk_norm_rope_backward(y, None, q, k, d, pos, f, norm=False)[0]
     ref.assert_within(again, back[0], 32 * ref.U * back[1] + ref.half_step(T[dtype]) * (1 + 32 * ref.U) * back[0].abs(),
                       "turned back")
+
+
+# around the row and token counts from which a weight's gradient takes a second launch
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hidden", [40, 192, 832, 2048, 8192, 201, 2051, 20480])
+def test_weight_gradients_of_few_rows(dtype, hidden):
+    t, g, p = T[dtype], gen(hidden), 0.25
+    rng = torch.tensor([SEED, OFFSET], dtype=torch.int64, device=DEV)
+    w = normal(g, hidden, dtype=t, std=0.2, mean=1.0)
+    ws = torch.full((R.rmsnorm_bwd_workspace_bytes(600, hidden, {"f32": 0, "bf16": 1}[dtype]),), 255, dtype=torch.uint8,
+                    device=DEV)   # NaN where nothing is written
+    for rows in (1, 2, 7, 8, 9, 16, 17, 33, 64, 65, 256, 257):
+        dy, h, dh = (normal(g, rows, hidden, dtype=t) for _ in range(3))
+        keep = drop_ref.kept(rows, hidden, p, SEED, OFFSET).to(DEV)
+        want = drop_ref.backward(dy, h, w, dh, keep, p, 1e-6, 0.0)
+        got = R.rms_norm_dropout_backward(dy, h, p, rng, w, dh, workspace=ws)
+        for i, name in enumerate(("dresidual", "dx", "dw")):
+            ref.assert_within(got[i], want[2 * i], want[2 * i + 1], f"{name}, {rows} rows")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("q,k,d,rot", [(4, 2, 64, 64), (24, 8, 96, 96), (0, 3, 80, 20), (5, 0, 34, 34)])
+def test_weight_gradients_of_few_tokens(dtype, q, k, d, rot):
+    for tokens in (1, 2, 7, 8, 9, 16, 40, 64, 65, 129, 304):
+        g, qkv, pos, f, qw, kw = inputs(dtype, tokens, q, k, d, rot, (rot // 2,), tokens)
+        dy = normal(g, tokens, (q + k) * d, dtype=T[dtype])
+        theta = ref.phases(pos, f, (rot // 2,))
+        want = ref.backward(dy, qkv, q, k, d, theta, rot, False, qw, kw, 1e-6, 0.0, True)
+        ws = torch.full((R.rmsnorm_qk_rope_bwd_workspace_bytes(d),), 255, dtype=torch.uint8, device=DEV)
+        got = R.qk_norm_rope_backward(dy, qkv, q, k, d, pos, f, qw, kw, workspace=ws)
+        for i, name in enumerate(("dx", "dq_w", "dk_w")):
+            ref.assert_within(got[i], want[2 * i], want[2 * i + 1], f"{name}, {tokens} tokens")
+
+
+def test_small_gradients_in_a_graph():
+    """Calls of one cluster and of two launches, one after another on one
+    workspace, replayed on new inputs; two graphs on two streams."""
+    g = gen(12)
+    q, k, d = 4, 2, 64
+    f, qw, kw = freqs(d), normal(g, d, dtype=torch.bfloat16, mean=1.0), normal(g, d, dtype=torch.bfloat16, mean=1.0)
+    sizes = [(3, 9), (200, 700), (1, 30), (64, 2)]
+    sets = []
+    for _ in range(2):
+        ws = torch.empty(8 << 20, dtype=torch.uint8, device=DEV)
+        one = [dict(x=normal(g, a, (q + k) * d, dtype=torch.bfloat16), dy=normal(g, a, (q + k) * d, dtype=torch.bfloat16),
+                    pos=torch.arange(a, device=DEV), h=normal(g, b, 832, dtype=torch.bfloat16),
+                    dh=normal(g, b, 832, dtype=torch.bfloat16)) for a, b in sizes]
+        sets.append((ws, one))
+    w = normal(g, 832, dtype=torch.bfloat16, mean=1.0)
+
+    def run(ws, one):
+        out = []
+        for s in one:
+            out += R.qk_norm_rope_backward(s["dy"], s["x"], q, k, d, s["pos"], f, qw, kw, workspace=ws)
+            out += R.rms_norm_backward(s["dh"], s["h"], w, workspace=ws)
+        return out
+
+    for s in sets:
+        run(*s)
+    graphs = []
+    for s in sets:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            graphs.append((gr, run(*s)))
+    streams = [torch.cuda.Stream() for _ in sets]
+    for turn in range(3):
+        for _, one in sets:
+            for s in one:
+                for name in ("x", "dy", "h", "dh"):
+                    s[name].copy_(normal(g, *s[name].shape, dtype=torch.bfloat16))
+        torch.cuda.synchronize()
+        for s, (gr, _) in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                gr.replay()
+        torch.cuda.synchronize()
+        for s, (_, got) in zip(sets, graphs):
+            for a, b in zip(run(*s), got):
+                assert torch.equal(a, b)
