@@ -43,12 +43,12 @@ constexpr int kRopeMaxWarps = 8;      // warps a block
 // memory: the forward 31.0 us with four blocks (64 registers a thread), 32.5
 // with three, 38.7 with five (which spill); the gradient 63.5 us with two, 75.5
 // with three.  Kernels of their own for whole heads and the gradient's ring
-// took them to 30.4 and 43.5 us.
+// took them to 30.4 and 43.9 us.
 // bytes: of a piece.
 __host__ __device__ constexpr int rope_resident(int bytes, int k) { return bytes * k <= 16 && bytes >= 4 ? 4 : 2; }
 // The gradient has 112 registers a thread where two blocks fit: what they leave
 // is a block of the column sums' (256 threads of 32), which then stands ready
-// when they end.  One register more cost 0.6 us (43.6 -> 44.2 us; 2326 tokens x
+// when they end.  One register more cost 0.5 us (43.6 -> 44.1 us; 2326 tokens x
 // 4 heads 6.7 -> 7.4 us).
 __host__ __device__ constexpr int rope_bwd_registers(int bytes, int k) { return bytes * k <= 16 && bytes >= 4 ? 112 : 255; }
 
