@@ -7,9 +7,11 @@ namespace {
 
 template <typename T, int GT, bool DW>
 const void *of_ch(int ch) {
+    if constexpr (drop_least_ch(GT) <= 1)
+        if (ch == 1) return reinterpret_cast<const void *>(&drop_bwd_kernel<T, GT, 1, DW>);
+    if constexpr (drop_least_ch(GT) <= 2)
+        if (ch == 2) return reinterpret_cast<const void *>(&drop_bwd_kernel<T, GT, 2, DW>);
     switch (ch) {
-        case 1: return reinterpret_cast<const void *>(&drop_bwd_kernel<T, GT, 1, DW>);
-        case 2: return reinterpret_cast<const void *>(&drop_bwd_kernel<T, GT, 2, DW>);
         case 3: return reinterpret_cast<const void *>(&drop_bwd_kernel<T, GT, 3, DW>);
         case 4: return reinterpret_cast<const void *>(&drop_bwd_kernel<T, GT, 4, DW>);
         default: return nullptr;
@@ -18,9 +20,9 @@ const void *of_ch(int ch) {
 
 template <typename T, int GT>
 const void *of_dw(int ch, int dw) {
-    if (dw == 2)
-        return ch == 2 ? reinterpret_cast<const void *>(&drop_bwd_kernel<T, GT, 2, true, true>)
-                       : reinterpret_cast<const void *>(&drop_bwd_kernel<T, GT, 4, true, true>);
+    if constexpr (drop_least_ch(GT) <= 2)
+        if (dw == 2 && ch == 2) return reinterpret_cast<const void *>(&drop_bwd_kernel<T, GT, 2, true, true>);
+    if (dw == 2) return ch == 4 ? reinterpret_cast<const void *>(&drop_bwd_kernel<T, GT, 4, true, true>) : nullptr;
     return dw ? of_ch<T, GT, true>(ch) : of_ch<T, GT, false>(ch);
 }
 

@@ -7,9 +7,11 @@ namespace {
 
 template <typename T, int GT>
 const void *of_ch(int ch) {
+    if constexpr (drop_least_ch(GT) <= 1)
+        if (ch == 1) return reinterpret_cast<const void *>(&drop_fwd_kernel<T, GT, 1>);
+    if constexpr (drop_least_ch(GT) <= 2)
+        if (ch == 2) return reinterpret_cast<const void *>(&drop_fwd_kernel<T, GT, 2>);
     switch (ch) {
-        case 1: return reinterpret_cast<const void *>(&drop_fwd_kernel<T, GT, 1>);
-        case 2: return reinterpret_cast<const void *>(&drop_fwd_kernel<T, GT, 2>);
         case 3: return reinterpret_cast<const void *>(&drop_fwd_kernel<T, GT, 3>);
         case 4: return reinterpret_cast<const void *>(&drop_fwd_kernel<T, GT, 4>);
         default: return nullptr;

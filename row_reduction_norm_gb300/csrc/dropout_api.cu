@@ -124,8 +124,6 @@ int scalar_shape(bool vec, int64_t hidden) {
     return -1;
 }
 
-int loop_block(bool vec, int64_t hidden) { return vec || hidden > 4096 ? 1024 : 256; }
-
 void fill(rrn::DropParams *p, const void *w, int64_t rows, int64_t hidden, float eps, float w_bias, uint32_t thr,
           const uint64_t *rng, int dtype) {
     std::memset(p, 0, sizeof(*p));
@@ -197,8 +195,8 @@ int backward(const void *dy, const void *h, const void *w, const void *dh, void 
             fn = rrn::drop_bwd_scalar(dtype, shape, dw != nullptr);
             smem = (size_t)(thr ? 2 * p.blocks_per_row : 0);
         } else {
-            threads = loop_block(vec, hidden);
-            fn = rrn::drop_bwd_loop(dtype, vec, threads, dw != nullptr);
+            threads = rrn::kDropLoopThreads;
+            fn = rrn::drop_bwd_loop(dtype, vec, dw != nullptr);
             p.acc_in_smem = dw != nullptr && hidden <= kSmemSums;
             smem = (p.acc_in_smem ? (size_t)hidden * sizeof(float) : 0) + (size_t)(thr ? p.blocks_per_row : 0);
         }
@@ -270,8 +268,8 @@ int rmsnorm_dropout_fwd(const void *x, const void *residual, const void *w, void
         fn = rrn::drop_fwd_scalar(dtype, shape);
         smem = (size_t)(thr ? p.blocks_per_row : 0);
     } else {
-        threads = loop_block(vec, hidden);
-        fn = rrn::drop_fwd_loop(dtype, vec, threads);
+        threads = rrn::kDropLoopThreads;
+        fn = rrn::drop_fwd_loop(dtype, vec);
         smem = (size_t)(thr ? p.blocks_per_row : 0);
     }
     if (fn == nullptr) return RMSNORM_EINVAL;

@@ -3,9 +3,11 @@
 
 namespace rrn {
 
-// Threads a row compiled for the register kernels, and chunks a thread: 1..4
-// for each, and 6, 8 for the forward's 512 threads.
+// Threads a row compiled for the register kernels, and chunks a thread: from
+// drop_least_ch (with fewer, fewer threads hold the row) to 4, and 6, 8 for the
+// forward's 512 threads.
 constexpr int kDropGT[6] = {8, 32, 64, 128, 256, 512};
+constexpr int drop_least_ch(int gt) { return gt == 8 ? 1 : gt == 32 ? 2 : 3; }
 
 const void *drop_fwd_bf16(int gt, int ch);
 const void *drop_fwd_f32(int gt, int ch);
@@ -28,8 +30,9 @@ constexpr int kDropScalars = 5;
 constexpr DropShape kDropScalar[kDropScalars] = {{64, 4}, {128, 8}, {256, 8}, {256, 16}, {512, 16}};
 const void *drop_fwd_scalar(int dtype, int shape);
 const void *drop_bwd_scalar(int dtype, int shape, bool dw);
-// Two-pass kernels: blocks of 256 (scalar only) or 1024 threads.
-const void *drop_fwd_loop(int dtype, bool vec, int block);
-const void *drop_bwd_loop(int dtype, bool vec, int block, bool dw);
+// Two-pass kernels: blocks of kDropLoopThreads.
+constexpr int kDropLoopThreads = 1024;
+const void *drop_fwd_loop(int dtype, bool vec);
+const void *drop_bwd_loop(int dtype, bool vec, bool dw);
 
 }  // namespace rrn
