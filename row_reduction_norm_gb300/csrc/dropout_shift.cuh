@@ -14,6 +14,7 @@
 #pragma once
 
 #include "dropout_kernels.cuh"
+#include "shift_layout.h"
 
 namespace rrn {
 
@@ -60,21 +61,6 @@ template <int V>
 __device__ __forceinline__ uint32_t shifted_mask(const uint8_t *mask, int u, int s) {
     return (((uint32_t)mask[u] & ((1u << V) - 1u)) | ((uint32_t)mask[u + 1] << V)) >> (V - s);
 }
-
-// How a row lies on the 16-byte chunks: elements of the row before in its
-// first one, chunks, elements of its own in the last one.
-template <int V>
-struct ShiftedRow {
-    int s, chunks, tail;
-    __device__ __forceinline__ void set(int64_t row, int64_t hidden) {
-        s = (int)(((row & (V - 1)) * (hidden & (V - 1))) & (V - 1));
-        chunks = (int)((s + hidden + V - 1) / V);
-        tail = (int)(s + hidden - (int64_t)(chunks - 1) * V);
-    }
-    // Elements lo .. hi - 1 of chunk u are the row's.
-    __device__ __forceinline__ int lo(int u) const { return u == 0 ? s : 0; }
-    __device__ __forceinline__ int hi(int u) const { return u == chunks - 1 ? tail : V; }
-};
 
 // Chunk of the weight for the columns u V - s and on (0 off its ends).
 template <typename T>
@@ -155,7 +141,7 @@ __global__ void __launch_bounds__(drop_block_threads(GT), GT < 512 ? 3 : 1) drop
             const int u = c * GT + t;
             xc[c] = hc[c] = Chunk{{0u, 0u, 0u, 0u}};
             if (ok && u < at.chunks) {
-                if (u + 1 < at.chunks || at.tail == V || row + 1 < p.rows) {
+                if (at.whole(u, row, p.rows, hidden)) {
                     xc[c] = ld_stream16(xr + c * GT * 16);
                     hc[c] = ld_stream16(rr + c * GT * 16);
                 } else {   // the tensors' last elements
