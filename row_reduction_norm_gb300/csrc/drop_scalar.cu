@@ -6,28 +6,22 @@
 namespace rrn {
 namespace {
 
-template <typename T>
+template <typename T, int I = 0>
 const void *fwd(int shape) {
-    switch (shape) {
-        case 0: return reinterpret_cast<const void *>(&drop_fwd_scalar_kernel<T, 64, 4>);
-        case 1: return reinterpret_cast<const void *>(&drop_fwd_scalar_kernel<T, 128, 8>);
-        case 2: return reinterpret_cast<const void *>(&drop_fwd_scalar_kernel<T, 256, 8>);
-        case 3: return reinterpret_cast<const void *>(&drop_fwd_scalar_kernel<T, 256, 16>);
-        case 4: return reinterpret_cast<const void *>(&drop_fwd_scalar_kernel<T, 512, 16>);
-        default: return nullptr;
-    }
+    constexpr bool narrow = I == 1;   // fp32 alone
+    if constexpr (I == kDropScalars) return nullptr;
+    else if constexpr (narrow && T::kVec == 8) return fwd<T, I + 1>(shape);
+    else if (shape == I) return reinterpret_cast<const void *>(&drop_fwd_scalar_kernel<T, kDropScalar[I].gt, kDropScalar[I].ch>);
+    else return fwd<T, I + 1>(shape);
 }
 
-template <typename T, bool DW>
+template <typename T, bool DW, int I = 0>
 const void *bwd(int shape) {
-    switch (shape) {
-        case 0: return reinterpret_cast<const void *>(&drop_bwd_scalar_kernel<T, 64, 4, DW>);
-        case 1: return reinterpret_cast<const void *>(&drop_bwd_scalar_kernel<T, 128, 8, DW>);
-        case 2: return reinterpret_cast<const void *>(&drop_bwd_scalar_kernel<T, 256, 8, DW>);
-        case 3: return reinterpret_cast<const void *>(&drop_bwd_scalar_kernel<T, 256, 16, DW>);
-        case 4: return reinterpret_cast<const void *>(&drop_bwd_scalar_kernel<T, 512, 16, DW>);
-        default: return nullptr;
-    }
+    constexpr bool narrow = I == 1;
+    if constexpr (I == kDropScalars) return nullptr;
+    else if constexpr (narrow && T::kVec == 8) return bwd<T, DW, I + 1>(shape);
+    else if (shape == I) return reinterpret_cast<const void *>(&drop_bwd_scalar_kernel<T, kDropScalar[I].gt, kDropScalar[I].ch, DW>);
+    else return bwd<T, DW, I + 1>(shape);
 }
 
 }  // namespace

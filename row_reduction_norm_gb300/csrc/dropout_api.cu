@@ -81,6 +81,15 @@ bool reg_shape(int64_t nch, int max_ch, int *gt, int *ch) {
     return false;
 }
 
+// Of the shifted kernels' shapes, the first that holds a row of this width
+// wherever it starts, or kDropShifts.
+int shift_holding(int64_t hidden, int dtype) {
+    const int64_t V = 16 / rrn::size_of(dtype), chunks = (hidden + 2 * V - 2) / V;
+    int i = 0;
+    while (i < rrn::kDropShifts && chunks > (int64_t)rrn::kDropShift[i].gt * rrn::kDropShift[i].ch) ++i;
+    return i;
+}
+
 // The kernel for rows of a length that is no multiple of 16 bytes, in tensors
 // that start on a 16-byte boundary, that holds a row's chunks; or -1 where the
 // rows of single elements are faster.  Starting costs the former more (weights
@@ -99,17 +108,15 @@ int shift_shape(const void *const *ptrs, int n, int64_t rows, int64_t hidden, in
     for (int i = 0; i < n; ++i)
         if (!rrn::on_boundary(ptrs[i], 16)) return -1;
     const bool bf16 = dtype == RMSNORM_BF16;
-    const int64_t V = 16 / rrn::size_of(dtype), chunks = (hidden + 2 * V - 2) / V;
     if (gradient) {
         if (!(hidden > 2048 || (hidden <= 512 && rows >= 1024) || rows >= (bf16 ? 1 << 20 : 1 << 22) / hidden)) return -1;
     } else if (!(rows >= 4096 || (bf16 && hidden > 2048))) {
         return -1;
     }
-    for (int i = 0; i < (bf16 || gradient ? rrn::kDropShifts : rrn::kDropShiftsF32); ++i) {
-        const int64_t held = (int64_t)rrn::kDropShift[i].gt * rrn::kDropShift[i].ch;
-        if (chunks <= held) return bf16 || hidden <= 512 || 10 * chunks >= 7 * held ? i : -1;
-    }
-    return -1;
+    const int i = shift_holding(hidden, dtype);
+    if (i >= (bf16 || gradient ? rrn::kDropShifts : rrn::kDropShiftsF32)) return -1;
+    const int64_t V = 16 / rrn::size_of(dtype), chunks = (hidden + 2 * V - 2) / V;
+    return bf16 || hidden <= 512 || 10 * chunks >= 7 * (int64_t)rrn::kDropShift[i].gt * rrn::kDropShift[i].ch ? i : -1;
 }
 
 // Blocks of `groups` row groups in all, at most `most`, that keep a thread's
@@ -117,10 +124,21 @@ int shift_shape(const void *const *ptrs, int n, int64_t rows, int64_t hidden, in
 // they take more than one group each.
 int64_t shift_blocks(int64_t groups, int64_t most) { return groups <= most ? groups : most < 8 ? 8 : most / 8 * 8; }
 
-// The rows-of-single-elements kernel that holds a row, or -1.
-int scalar_shape(bool vec, int64_t hidden) {
-    for (int i = 0; !vec && i < rrn::kDropScalars; ++i)
-        if (hidden <= (int64_t)rrn::kDropScalar[i].gt * rrn::kDropScalar[i].ch) return i;
+// The rows-of-single-elements kernel that holds a row, or -1, and its classes
+// of columns a thread: those of the shifted kernel for the width, so that the
+// rows have the same bits from either (up to 2048 columns, where the number of
+// rows decides between the two).
+int scalar_shape(bool vec, int64_t hidden, int dtype, int32_t *classes) {
+    if (vec) return -1;
+    const int held = shift_holding(hidden, dtype);
+    const int64_t all = held < rrn::kDropShifts ? rrn::kDropShift[held].gt * 16 / rrn::size_of(dtype) : INT64_MAX;
+    for (int i = 0; i < rrn::kDropScalars; ++i) {
+        const int64_t gt = rrn::kDropScalar[i].gt;
+        if (hidden > gt * rrn::kDropScalar[i].ch || gt > all) continue;
+        const int64_t most = hidden <= 2048 ? 4 : gt < 512 ? 2 : 1;
+        *classes = (int32_t)(all / gt < most ? all / gt : most);
+        return i;
+    }
     return -1;
 }
 
@@ -190,7 +208,7 @@ int backward(const void *dy, const void *h, const void *w, const void *dh, void 
             threads = rrn::drop_block_threads(gt);
             groups = div_up(rows, threads / gt);
             smem = (size_t)rrn::shift_ring_bytes(gt, rrn::kDropShift[shift].ch);
-        } else if (const int shape = scalar_shape(vec, hidden); shape >= 0) {
+        } else if (const int shape = scalar_shape(vec, hidden, dtype, &p.classes); shape >= 0) {
             threads = rrn::kDropScalar[shape].gt;
             fn = rrn::drop_bwd_scalar(dtype, shape, dw != nullptr);
             smem = (size_t)(thr ? 2 * p.blocks_per_row : 0);
@@ -263,7 +281,7 @@ int rmsnorm_dropout_fwd(const void *x, const void *residual, const void *w, void
         if ((st = rrn::current_device_sms(&dev, &sms)) != RMSNORM_OK) return st;
         if ((st = rrn::resident_blocks(dev, fn, threads, 0, &resident)) != RMSNORM_OK) return st;
         blocks = shift_blocks(div_up(rows, threads / gt), (int64_t)sms * resident);
-    } else if (const int shape = scalar_shape(vec, hidden); shape >= 0) {
+    } else if (const int shape = scalar_shape(vec, hidden, dtype, &p.classes); shape >= 0) {
         threads = rrn::kDropScalar[shape].gt;
         fn = rrn::drop_fwd_scalar(dtype, shape);
         smem = (size_t)(thr ? p.blocks_per_row : 0);

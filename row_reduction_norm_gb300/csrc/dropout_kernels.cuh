@@ -23,6 +23,7 @@
 #include "async_copy.cuh"
 #include "finish.cuh"
 #include "rmsnorm_kernels.cuh"
+#include "row_classes.cuh"
 
 namespace rrn {
 
@@ -42,6 +43,7 @@ struct DropParams {
     uint32_t thr;                // 0: no dropout
     float scale;
     float hidden_f, eps, w_bias;
+    int32_t classes;             // rows of single elements: accumulators a thread (row_classes.cuh)
     int32_t acc_in_smem;         // two-pass gradient: dw sums in shared memory, else in partial
 };
 
@@ -678,7 +680,7 @@ __global__ void __launch_bounds__(BLOCK) drop_bwd_loop_kernel(const DropParams p
 
 template <typename T, int GT, int CH>
 __global__ void __launch_bounds__(GT) drop_fwd_scalar_kernel(const DropParams p) {
-    __shared__ float2 red[2][1][GT / 32];
+    __shared__ float red[2][1][32];
     extern __shared__ uint8_t mask[];   // [blocks_per_row], with dropout
     const int t = threadIdx.x, n = p.units;
     pdl_wait_for_inputs();
@@ -704,7 +706,7 @@ __global__ void __launch_bounds__(GT) drop_fwd_scalar_kernel(const DropParams p)
             stage_mask(p, mask, seed, offset, row);
             __syncthreads();
         }
-        float h[CH], acc[4] = {0.f, 0.f, 0.f, 0.f};
+        float h[CH];
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int e = c * GT + t;
@@ -712,11 +714,11 @@ __global__ void __launch_bounds__(GT) drop_fwd_scalar_kernel(const DropParams p)
             const float x = widen_bits(xb[c], T{});
             h[c] = add_round(widen_bits(rb[c], T{}), p.thr ? (keep ? x * p.scale : 0.f) : x, T{});
             if (e < n) st_scalar(hr, e, h[c], T{});
-            acc[c & 3] = fmaf(h[c], h[c], acc[c & 3]);
         }
-        const float sum = row_sums<GT>(tree_sum(acc), 0.f, red[parity], 0, t).x;
+        float sum[1];
+        class_sums<GT, CH, 1>(p.classes, [&](int, int c) { return h[c]; }, [&](int c) { return h[c]; }, red[parity], t, sum);
         parity ^= 1;
-        const float r = rsqrtf(sum / p.hidden_f + p.eps);
+        const float r = rsqrtf(sum[0] / p.hidden_f + p.eps);
         if (p.w != nullptr) {
             uint32_t wb[CH];
 #pragma unroll
@@ -752,7 +754,7 @@ __device__ __forceinline__ BothF32 both_of(F32) { return {}; }
 template <typename T, int GT, int CH, bool DW>
 __global__ void __launch_bounds__(GT) drop_bwd_scalar_kernel(const DropParams p) {
     using Both = decltype(both_of(T{}));
-    __shared__ float2 red[2][1][GT / 32];
+    __shared__ float red[2][2][32];
     extern __shared__ uint8_t masks[];   // [2][blocks_per_row], with dropout
     const int t = threadIdx.x, n = p.units;
     pdl_wait_for_inputs();
@@ -793,18 +795,12 @@ __global__ void __launch_bounds__(GT) drop_bwd_scalar_kernel(const DropParams p)
         }
         uint8_t *mask = masks + parity * p.blocks_per_row;   // the other one may still be read
         if (p.thr) stage_mask(p, mask, seed, offset, row);   // read after the sums' barrier
-        float sq[4] = {0.f, 0.f, 0.f, 0.f}, dot[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const float h = v[c].h();
-            const float g = v[c].g() * w[c];
-            sq[c & 3] = fmaf(h, h, sq[c & 3]);
-            dot[c & 3] = fmaf(g, h, dot[c & 3]);
-        }
-        const float2 s = row_sums<GT>(tree_sum(sq), tree_sum(dot), red[parity], 0, t);
+        float s[2];   // of h h, of g h
+        class_sums<GT, CH, 2>(p.classes, [&](int m, int c) { return m ? v[c].g() * w[c] : v[c].h(); },
+                              [&](int c) { return v[c].h(); }, red[parity], t, s);
         parity ^= 1;
-        const float r = rsqrtf(s.x / p.hidden_f + p.eps);
-        const float m = -(r * (s.y / p.hidden_f));
+        const float r = rsqrtf(s[0] / p.hidden_f + p.eps);
+        const float m = -(r * (s[1] / p.hidden_f));
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int e = c * GT + t;

@@ -25,9 +25,10 @@ constexpr DropShape kDropShift[kDropShifts] = {{8, 4},   {32, 2},  {32, 4},  {64
 const void *drop_fwd_shift(int dtype, int shape);
 const void *drop_bwd_shift_bf16(int shape, bool dw);
 const void *drop_bwd_shift_f32(int shape, bool dw);
-// Rows of single elements in registers: threads a row, elements a thread.
-constexpr int kDropScalars = 5;
-constexpr DropShape kDropScalar[kDropScalars] = {{64, 4}, {128, 8}, {256, 8}, {256, 16}, {512, 16}};
+// Rows of single elements in registers: threads a row, elements a thread (the
+// second for fp32 alone, whose narrowest rows have 32 classes of columns).
+constexpr int kDropScalars = 6;
+constexpr DropShape kDropScalar[kDropScalars] = {{64, 4}, {32, 4}, {128, 8}, {256, 8}, {256, 16}, {512, 16}};
 const void *drop_fwd_scalar(int dtype, int shape);
 const void *drop_bwd_scalar(int dtype, int shape, bool dw);
 // Two-pass kernels: blocks of kDropLoopThreads.

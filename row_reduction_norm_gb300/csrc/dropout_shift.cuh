@@ -14,6 +14,7 @@
 #pragma once
 
 #include "dropout_kernels.cuh"
+#include "row_classes.cuh"
 #include "shift_layout.h"
 
 namespace rrn {
@@ -110,7 +111,7 @@ __device__ __forceinline__ void put_chunk(char *at, const float (&v)[T::kVec], i
 template <typename T, int GT, int CH>
 __global__ void __launch_bounds__(drop_block_threads(GT), GT < 512 ? 3 : 1) drop_fwd_shift_kernel(const DropParams p) {
     constexpr int V = T::kVec, S = 16 / V, BLOCK = drop_block_threads(GT), RPB = BLOCK / GT;
-    __shared__ float2 red[2][RPB][GT > 32 ? GT / 32 : 1];
+    __shared__ ShiftedSums<GT, 1> red[RPB];
     __shared__ uint8_t masks[2][RPB][GT * CH + 1];
     const int tid = threadIdx.x, slot = tid / GT, t = tid % GT;
     const int hidden = (int)p.row_elems;
@@ -161,9 +162,9 @@ __global__ void __launch_bounds__(drop_block_threads(GT), GT < 512 ? 3 : 1) drop
             if constexpr (GT > 32) __syncthreads();
             else __syncwarp();
         }
-        float acc[V];
+        float acc[1][V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = 0.f;
+        for (int e = 0; e < V; ++e) acc[0][e] = 0.f;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int u = c * GT + t;
@@ -184,12 +185,13 @@ __global__ void __launch_bounds__(drop_block_threads(GT), GT < 512 ? 3 : 1) drop
                 }
                 hc[c] = pack(a, T{});
                 put_chunk<T>(static_cast<char *>(p.h_out) + off + c * GT * 16, a, lo, hi);
-                sq_accumulate(a, acc);
+                sq_accumulate(a, acc[0]);
             }
         }
-        const float sum = row_sums<GT>(tree_sum(acc), 0.f, red[parity], slot, t).x;
+        float sum[1];
+        shifted_sums<GT, V, 1>(acc, at.s, red[slot], t, sum);
         parity ^= 1;
-        const float r = rsqrtf(sum / p.hidden_f + p.eps);
+        const float r = rsqrtf(sum[0] / p.hidden_f + p.eps);
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int u = c * GT + t;
@@ -214,7 +216,7 @@ __global__ void __launch_bounds__(drop_block_threads(GT), GT < 512 ? 3 : 1) drop
 template <typename T, int GT, int CH, bool DW>
 __global__ void __launch_bounds__(drop_block_threads(GT), drop_bwd_resident(GT)) drop_bwd_shift_kernel(const DropParams p) {
     constexpr int V = T::kVec, S = 16 / V, BLOCK = drop_block_threads(GT), RPB = BLOCK / GT;
-    __shared__ float2 red[2][RPB][GT > 32 ? GT / 32 : 1];
+    __shared__ ShiftedSums<GT, 2> red[RPB];
     extern __shared__ __align__(16) Chunk ring[];   // [stage][dy, h, dh][CH][BLOCK], then the masks' bytes [2][RPB][GT CH + 1]
     const int tid = threadIdx.x, slot = tid / GT, t = tid % GT;
     uint8_t *masks = reinterpret_cast<uint8_t *>(ring + kDropStages * 3 * CH * BLOCK);
@@ -285,27 +287,28 @@ __global__ void __launch_bounds__(drop_block_threads(GT), drop_bwd_resident(GT))
             clear_ends<T>(place(parity, 0, 0), at.s, V);
             clear_ends<T>(place(parity, 1, 0), at.s, V);
         }
-        float sq[V], dot[V];
+        float acc[2][V];   // of h h, of g h
 #pragma unroll
-        for (int e = 0; e < V; ++e) sq[e] = dot[e] = 0.f;
+        for (int e = 0; e < V; ++e) acc[0][e] = acc[1][e] = 0.f;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             if (ok && c * GT + t < at.chunks) {
                 float h[V], g[V], w[V];
                 unpack(place(parity, 1, c), h, T{});
                 unpack(place(parity, 0, c), g, T{});
-                sq_accumulate(h, sq);
+                sq_accumulate(h, acc[0]);
                 if (weighted) {
                     weight(c, w);
                     mul_pairs(g, w);
                 }
-                fma_pairs(dot, g, h);
+                fma_pairs(acc[1], g, h);
             }
         }
         if constexpr (GT <= 32) __syncwarp();
-        const float2 sums = row_sums<GT>(tree_sum(sq), tree_sum(dot), red[parity], slot, t);
-        const float r = rsqrtf(sums.x / p.hidden_f + p.eps);
-        const float m = -(r * (sums.y / p.hidden_f));   // d = r (g - (h r) mean(g h) r) + dh
+        float sums[2];
+        shifted_sums<GT, V, 2>(acc, at.s, red[slot], t, sums);
+        const float r = rsqrtf(sums[0] / p.hidden_f + p.eps);
+        const float m = -(r * (sums[1] / p.hidden_f));   // d = r (g - (h r) mean(g h) r) + dh
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int u = c * GT + t;
