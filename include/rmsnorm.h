@@ -410,7 +410,7 @@ typedef struct {
     int32_t num_pages;          /* pages of the cache                                    */
     int32_t page_size;          /* rows of a page, >= 1                                  */
     int32_t cache_dtype;        /* the I/O type, or RMSNORM_E4M3                         */
-    float k_scale, v_scale;     /* E4M3: a code stands for code * scale (> 0, finite)    */
+    float k_scale, v_scale;     /* E4M3: a code stands for code * scale (2^-100 .. 2^100) */
 } rmsnorm_paged_kv_t;
 
 /*
@@ -422,8 +422,8 @@ typedef struct {
  * stride works in place), keys and values to the cache.  Token t of sequence
  * s is row cache_lens[s] + t - cu_tokens[s] of it, which is also its position
  * when rope->positions is NULL (one axis then).  E4M3 caches hold
- * E4M3(value / scale) of the unrounded value, nearest-even, saturated at 448
- * (infinities too; NaN stays NaN).
+ * E4M3(value / scale) of the unrounded value, the exact quotient rounded once,
+ * nearest-even, saturated at 448 (infinities too; NaN stays NaN).
  *   tokens       rows of x and q_out; rows from cu_tokens[seqs] on are padding:
  *                not read, and q_out left as it was there
  *   cache_lens   is not changed: the caller adds the new tokens to it

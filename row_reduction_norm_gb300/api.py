@@ -424,7 +424,7 @@ def qkv_append(qkv: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     [num_pages, page_size, kv_heads, head_dim] tensors of any strides with a
     contiguous last dimension (so a permuted view of a cache kept head by head
     too), in qkv's type or float8_e4m3fn, where a code stands for
-    code * ``k_scale`` (``v_scale``).  Sequence s brings the tokens
+    code * ``k_scale`` (``v_scale``; 2^-100 .. 2^100).  Sequence s brings the tokens
     cu_tokens[s] .. cu_tokens[s + 1] - 1 (int32, [seqs + 1]) and has
     cache_lens[s] rows (int32) in the pages page_table[s] (int32, [seqs,
     max_pages], -1: no page); cache_lens is left as it is.  ``positions``

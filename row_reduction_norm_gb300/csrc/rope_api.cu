@@ -144,11 +144,19 @@ bool tile_reaches(int64_t a, int64_t b, int64_t c) {
     return a <= most && b <= most && c <= most;
 }
 
+// Scales of an 8-bit cache: within 2^-100 .. 2^100 (see settle_quotient).
+bool scale_ok(float s) { return s >= 0x1p-100f && s <= 0x1p100f; }
+bool power_of_two(float s) {
+    int e;
+    return std::frexp(s, &e) == 0.5f;
+}
+
 int whole_head(const rrn::RopeParams *p) { return 2 * p->R == p->head_dim ? p->head_dim : 0; }
 
 const void *forward_kernel(int dtype, int shape, bool il, int mode, int whole) {
+    const int ragged = mode == rrn::kRopeAppendSettled ? (int)rrn::kRopeAppendE4m3 : mode;
     if (shape == rrn::kRopeRagged)
-        return dtype == RMSNORM_BF16 ? rrn::rope_ragged_bf16(il, mode) : rrn::rope_ragged_f32(il, mode);
+        return dtype == RMSNORM_BF16 ? rrn::rope_ragged_bf16(il, ragged) : rrn::rope_ragged_f32(il, ragged);
     return dtype == RMSNORM_BF16 ? rrn::rope_fwd_bf16(shape, il, mode, whole)
                                  : rrn::rope_fwd_f32(shape, il, mode, whole);
 }
@@ -343,9 +351,7 @@ int rmsnorm_qkv_append(const void *x, void *q_out, int64_t tokens, int64_t x_tok
     if (rope->positions == nullptr && rope->axes != 1) return RMSNORM_EINVAL;
     const bool e4m3 = kv->cache_dtype == RMSNORM_E4M3;
     if (!e4m3 && kv->cache_dtype != dtype) return RMSNORM_EINVAL;
-    if (e4m3 && (!(kv->k_scale > 0.f) || !std::isfinite(kv->k_scale) || !(kv->v_scale > 0.f) ||
-                 !std::isfinite(kv->v_scale)))
-        return RMSNORM_EINVAL;
+    if (e4m3 && (!scale_ok(kv->k_scale) || !scale_ok(kv->v_scale))) return RMSNORM_EINVAL;
     if (kv->seqs < 0 || kv->max_pages < 0 || kv->num_pages < 0 || kv->page_size < 1) return RMSNORM_EINVAL;
     if (kv->page_table_stride < kv->max_pages || kv->page_stride < 0 || kv->row_stride < 0 || kv->head_stride < 0)
         return RMSNORM_EINVAL;
@@ -383,15 +389,20 @@ int rmsnorm_qkv_append(const void *x, void *q_out, int64_t tokens, int64_t x_tok
     p.page_stride = kv->page_stride * c;
     p.row_stride = kv->row_stride * c;
     p.head_stride = kv->head_stride * c;
-    p.k_inv = e4m3 ? (float)(1.0 / (double)kv->k_scale) : 1.f;
-    p.v_inv = e4m3 ? (float)(1.0 / (double)kv->v_scale) : 1.f;
+    if (e4m3) {
+        p.k_inv = (float)(1.0 / (double)kv->k_scale);
+        p.v_inv = (float)(1.0 / (double)kv->v_scale);
+        p.k_scale = kv->k_scale;
+        p.v_scale = kv->v_scale;
+        p.settle = !power_of_two(kv->k_scale) || !power_of_two(kv->v_scale);
+    }
     p.dropped = kv->dropped;
     Unit u;
     u.at(x, s), u.at(kv->k_cache, c), u.at(kv->v_cache, c);
     u.step(x_token_stride), u.step(kv->page_stride), u.step(kv->row_stride), u.step(kv->head_stride);
     if (q_heads > 0) u.at(q_out, s), u.step(q_token_stride);
-    return launch_forward(&p, dtype, u.get(), rope->interleaved == 1, e4m3 ? rrn::kRopeAppendE4m3 : rrn::kRopeAppend,
-                          stream);
+    const int mode = !e4m3 ? rrn::kRopeAppend : p.settle ? rrn::kRopeAppendSettled : rrn::kRopeAppendE4m3;
+    return launch_forward(&p, dtype, u.get(), rope->interleaved == 1, mode, stream);
 }
 
 }  // extern "C"

@@ -11,6 +11,7 @@ const void *one(int mode) {
         case kRopePlain: return reinterpret_cast<const void *>(&rope_kernel<T, VE, K, IL, kRopePlain, HD>);
         case kRopeAppend: return reinterpret_cast<const void *>(&rope_kernel<T, VE, K, IL, kRopeAppend, HD>);
         case kRopeAppendE4m3: return reinterpret_cast<const void *>(&rope_kernel<T, VE, K, IL, kRopeAppendE4m3, HD>);
+        case kRopeAppendSettled: return reinterpret_cast<const void *>(&rope_kernel<T, VE, K, IL, kRopeAppendSettled, HD>);
         default: return nullptr;
     }
 }

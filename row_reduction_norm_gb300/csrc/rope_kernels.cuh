@@ -86,9 +86,29 @@ struct RopeParams {
     int32_t seqs, max_pages, num_pages, page_size;
     void *k_cache, *v_cache;
     int64_t page_stride, row_stride, head_stride;   // bytes
-    float k_inv, v_inv;       // 8-bit cache: 1 / scale
+    float k_inv, v_inv;       // 8-bit cache: 1 / scale, rounded
+    float k_scale, v_scale;
+    int32_t settle;           // an inverse is not exact
     int32_t *dropped;
 };
+
+// ------------------------------------------------------------- 8-bit codes
+// What E4M3 code v / scale has, without a division.  v * (1 / scale), both
+// rounded, is within 2 steps (2^-23) of the quotient, so its code can be
+// another one only next to a point halfway between two codes.  Those points
+// have at most four leading bits (the low 19 bits of their mantissa are 0), and
+// there one fused multiply-add tells on which side of the point the quotient
+// lies: v - point * scale is rounded once, so its sign is exact (scales are
+// within 2^-100 .. 2^100: nothing that matters underflows).
+__device__ __forceinline__ float settle_quotient(float q, float v, float scale) {
+    const uint32_t near = __float_as_uint(q) + 3u;
+    if ((near & 0x7FFFFu) > 6u || !(fabsf(q) < 512.f)) return q;
+    const uint32_t point = near & ~0x7FFFFu;
+    const float over = fmaf(-__uint_as_float(point), scale, v);
+    if (over == 0.f) return __uint_as_float(point);
+    // one step to the quotient's side of the point
+    return __uint_as_float((__float_as_uint(over) ^ point) >> 31 ? point - 1u : point + 1u);
+}
 
 // ------------------------------------------------------------------ pieces
 // VE consecutive elements as one access of VE * sizeof(T) bytes.
@@ -185,14 +205,23 @@ struct Piece {
         }
         return r;
     }
-    // E4M3 codes of f * inv, nearest-even, saturated at 448 (NaN stays NaN).
-    __device__ static __forceinline__ void store_e4m3(char *p, const float (&f)[VE], float inv) {
+    // E4M3 codes of the quotients f / scale, nearest-even, saturated at 448 (NaN
+    // stays NaN).  SETTLE: inv is not exact.
+    template <bool SETTLE>
+    __device__ static __forceinline__ void store_e4m3(char *p, const float (&f)[VE], float inv, float scale) {
+        float q[VE];
+#pragma unroll
+        for (int i = 0; i < VE; ++i) q[i] = f[i] * inv;
+        if constexpr (SETTLE) {
+#pragma unroll
+            for (int i = 0; i < VE; ++i) q[i] = settle_quotient(q[i], f[i], scale);
+        }
         if constexpr (VE == 1) {
-            *reinterpret_cast<uint8_t *>(p) = e4m3_of(f[0] * inv);
+            *reinterpret_cast<uint8_t *>(p) = e4m3_of(q[0]);
         } else {
             uint16_t h[VE / 2];
 #pragma unroll
-            for (int i = 0; i < VE / 2; ++i) h[i] = e4m3x2(f[2 * i] * inv, f[2 * i + 1] * inv);
+            for (int i = 0; i < VE / 2; ++i) h[i] = e4m3x2(q[2 * i], q[2 * i + 1]);
             if constexpr (VE == 8) {
                 asm volatile("st.global.v2.u32 [%0], {%1, %2};"
                              : : "l"(p), "r"((uint32_t)h[0] | ((uint32_t)h[1] << 16)),
@@ -483,7 +512,12 @@ __device__ __forceinline__ int64_t cache_row(const RopeParams &p, int seq, int64
     return (int64_t)page * p.page_stride + (int64_t)((uint32_t)index - n * (uint32_t)p.page_size) * p.row_stride;
 }
 
-enum RopeMode { kRopePlain = 0, kRopeAppend = 1, kRopeAppendE4m3 = 2 };
+// E4m3: scales whose inverses are exact (powers of two); Settled: any.  A kernel
+// of its own costs the others nothing: 8192 tokens of 32 + 2 * 8 bf16 heads of
+// 128 35.5 us with exact inverses, 37.5 settled, 36.3 and 37.5 from one kernel.
+// (The kernels of rope_ragged.cuh look at `settle`.)
+enum RopeMode { kRopePlain = 0, kRopeAppend = 1, kRopeAppendE4m3 = 2, kRopeAppendSettled = 3 };
+__host__ __device__ constexpr bool rope_codes(int mode) { return mode >= kRopeAppendE4m3; }
 
 // A lane's units of a head: where their pieces start (bytes), and which exist.
 // Lanes without a unit take unit 0's place (they load it like a neighbour: no
@@ -739,11 +773,11 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, rope_resident(Piece<T, VE>
 #pragma unroll
                     for (int v = 0; v < VE; ++v) x[v] = e[v], y[v] = e[VE + v];
                     const int d = HD ? (IL ? VE : HD / 2) * S : my.ob[k] - my.oa[k];
-                    if (MODE == kRopeAppendE4m3 && key) {
-                        const float inv = value ? p.v_inv : p.k_inv;
+                    if (rope_codes(MODE) && key) {
+                        const float inv = value ? p.v_inv : p.k_inv, scale = value ? p.v_scale : p.k_scale;
                         char *to = dst + my.oa[k] / S;
-                        P::store_e4m3(to, x, inv);
-                        P::store_e4m3(to + d / S, y, inv);
+                        P::template store_e4m3<MODE == kRopeAppendSettled>(to, x, inv, scale);
+                        P::template store_e4m3<MODE == kRopeAppendSettled>(to + d / S, y, inv, scale);
                     } else {
                         char *to = dst + my.oa[k];
                         P::store(to, x);

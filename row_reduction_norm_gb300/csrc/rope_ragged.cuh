@@ -103,10 +103,16 @@ __device__ __forceinline__ void put_run(unsigned char *img, int first, int n, co
     }
 }
 template <int VE>
-__device__ __forceinline__ void put_codes(unsigned char *img, int first, int n, float inv, const float *e) {
+__device__ __forceinline__ void put_codes(unsigned char *img, int first, int n, float inv, float scale, bool settle, const float *e) {
+    if (settle) {
 #pragma unroll
-    for (int j = 0; j < VE; ++j)
-        if (j < n) img[first + j] = e4m3_of(e[j] * inv);
+        for (int j = 0; j < VE; ++j)
+            if (j < n) img[first + j] = e4m3_of(settle_quotient(e[j] * inv, e[j], scale));
+    } else {
+#pragma unroll
+        for (int j = 0; j < VE; ++j)
+            if (j < n) img[first + j] = e4m3_of(e[j] * inv);
+    }
 }
 
 // The factors of a unit applied to its runs: times the weights, turned.
@@ -260,9 +266,9 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, 4) rope_ragged_kernel(cons
             __syncwarp();   // the image is read: it takes the results
             if (mine) {
                 if (MODE == kRopeAppendE4m3 && key) {
-                    const float inv = value ? p.v_inv : p.k_inv;
-                    put_codes<VE>(img, my.a, my.in_a(), inv, e);
-                    put_codes<VE>(img, my.b, my.in_b(), inv, e + VE);
+                    const float inv = value ? p.v_inv : p.k_inv, scale = value ? p.v_scale : p.k_scale;
+                    put_codes<VE>(img, my.a, my.in_a(), inv, scale, p.settle, e);
+                    put_codes<VE>(img, my.b, my.in_b(), inv, scale, p.settle, e + VE);
                 } else {
                     put_run<T, VE>(img, my.a, my.in_a(), e);
                     put_run<T, VE>(img, my.b, my.in_b(), e + VE);
