@@ -13,6 +13,11 @@
 //
 // Nothing is computed and nothing is kept here; the C ABI's addresses are
 // handed over once by bind().
+//
+// Arguments are read with the interpreter's lock held; allocations and the C
+// ABI's calls are made without it, as torch's and ctypes' are: either may block
+// (a full launch queue, an allocator's own lock), and what they wait for may
+// need another Python thread.
 #include <Python.h>
 
 #include <ATen/ATen.h>
@@ -161,28 +166,62 @@ at::Tensor fresh(at::IntArrayRef size, const at::Tensor &x) {
     return at::Tensor(at::detail::empty_cuda(size, x.scalar_type(), x.device(), std::nullopt));
 }
 
-// A workspace given, or made (memory of the current stream, handed back when
-// the call is over and used again only behind it).
-void *workspace_of(PyObject *given, int64_t n, const Where &w, c10::DataPtr *made) {
-    if (given == Py_None) {
-        *made = c10::GetAllocator(c10::kCUDA)->allocate((size_t)n);
-        return made->get();
+// A workspace given, or made without the lock (memory of the current stream,
+// handed back when the call is over and used again only behind it).
+struct Workspace {
+    c10::DataPtr made;
+    void *at = nullptr;
+    int64_t bytes = 0;
+    void given(PyObject *o, int64_t n, const Where &w) {
+        bytes = n;
+        if (o == Py_None) return;
+        const at::Tensor &t = tensor(o);
+        need(t.get_device() == w.dev && t.is_contiguous() && t.numel() * (int64_t)t.element_size() >= n);
+        at = t.data_ptr();
     }
-    const at::Tensor &t = tensor(given);
-    need(t.get_device() == w.dev && t.is_contiguous() && t.numel() * (int64_t)t.element_size() >= n);
-    return t.data_ptr();
-}
+    void make() {
+        if (bytes == 0 || at != nullptr) return;
+        made = c10::GetAllocator(c10::kCUDA)->allocate((size_t)bytes);
+        at = made.get();
+    }
+};
+
+// A span without the interpreter's lock.  No Python object is touched in it;
+// an exception takes the lock back on its way out.
+class Unlocked {
+    PyThreadState *state;
+
+public:
+    Unlocked() : state(PyEval_SaveThread()) {}
+    ~Unlocked() { PyEval_RestoreThread(state); }
+    Unlocked(const Unlocked &) = delete;
+    Unlocked &operator=(const Unlocked &) = delete;
+};
+
+// An output given, or made without the lock.
+struct Output {
+    PyObject *object;
+    at::Tensor made;
+    void *at = nullptr;
+    explicit Output(PyObject *o) : object(o) {}
+    bool given() const { return object != Py_None; }
+    void make(at::IntArrayRef size, const at::Tensor &x) {
+        if (given()) return;
+        made = fresh(size, x);
+        at = made.data_ptr();
+    }
+    PyObject *result() const {
+        if (!given()) return THPVariable_Wrap(made);
+        Py_INCREF(object);
+        return object;
+    }
+};
 
 PyObject *status_of(int st) { return PyLong_FromLong(st); }
 
 PyObject *wrap_or_none(const at::Tensor &t) {
     if (t.defined()) return THPVariable_Wrap(t);
     Py_RETURN_NONE;
-}
-
-PyObject *same_object(PyObject *o) {
-    Py_INCREF(o);
-    return o;
 }
 
 // Runs a call; what it leaves to api.py comes back as None.
@@ -202,7 +241,8 @@ PyObject *guarded(F f) {
 PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&]() -> PyObject * {
         need(n == 14 && qk_rope_fwd != nullptr);
-        const at::Tensor &x = tensor(a[0]);
+        const at::Tensor x = tensor(a[0]);
+        void *from = x.data_ptr();
         const int code = code_of(x);
         const Where w(x);
         const int32_t q = count(a[1]), k = count(a[2]);
@@ -212,14 +252,22 @@ PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
         rmsnorm_rope_t rope;
         need(a[4] != Py_None);
         rope_arg(&rope, a[4], a[5], a[11], a[12], tokens, d, w);
-        at::Tensor made;
-        if (a[13] == Py_None) made = fresh({tokens, width}, x);
-        const at::Tensor &y = made.defined() ? made : tensor(a[13]);
-        const int64_t ys = head_rows(y, width, tokens, x.scalar_type(), w);
-        const int st = qk_rope_fwd(x.data_ptr(), y.data_ptr(), tokens, xs, ys, q, k, d, qw, kw, real(a[9]), real(a[8]),
-                                   truth(a[10]), &rope, code, w.stream());
-        if (st != RMSNORM_OK) return status_of(st);
-        return made.defined() ? THPVariable_Wrap(made) : same_object(a[13]);
+        const float bias = real(a[9]), eps = real(a[8]);
+        const int norm = truth(a[10]);
+        Output y(a[13]);
+        int64_t ys = width;
+        if (y.given()) {
+            const at::Tensor &o = tensor(a[13]);
+            ys = head_rows(o, width, tokens, x.scalar_type(), w);
+            y.at = o.data_ptr();
+        }
+        int st;
+        {
+            const Unlocked span;
+            y.make({tokens, width}, x);
+            st = qk_rope_fwd(from, y.at, tokens, xs, ys, q, k, d, qw, kw, bias, eps, norm, &rope, code, w.stream());
+        }
+        return st == RMSNORM_OK ? y.result() : status_of(st);
     });
 }
 
@@ -228,7 +276,8 @@ PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
 PyObject *qk_norm_rope_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&]() -> PyObject * {
         need(n == 16 && qk_rope_bwd != nullptr);
-        const at::Tensor &g = tensor(a[0]);
+        const at::Tensor g = tensor(a[0]);
+        void *from = g.data_ptr();
         const int code = code_of(g);
         const Where w(g);
         const int32_t q = count(a[2]), k = count(a[3]);
@@ -247,26 +296,37 @@ PyObject *qk_norm_rope_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         rmsnorm_rope_t rope;
         need(a[5] != Py_None);
         rope_arg(&rope, a[5], a[6], a[12], a[13], tokens, d, w);
-        at::Tensor made, dq, dk;
-        c10::DataPtr ws;
-        if (a[14] == Py_None) made = fresh({tokens, width}, g);
-        const at::Tensor &y = made.defined() ? made : tensor(a[14]);
-        const int64_t ys = head_rows(y, width, tokens, g.scalar_type(), w);
-        void *at_ws = nullptr;
-        int64_t bytes = 0;
-        if (qw != nullptr && kw != nullptr) {
-            bytes = qk_rope_bwd_workspace_bytes(d);
-            need(bytes > 0);
-            dq = fresh({d}, g);
-            dk = fresh({d}, g);
-            at_ws = workspace_of(a[15], bytes, w, &ws);
+        const float bias = real(a[10]), eps = real(a[9]);
+        Output y(a[14]);
+        int64_t ys = width;
+        if (y.given()) {
+            const at::Tensor &o = tensor(a[14]);
+            ys = head_rows(o, width, tokens, g.scalar_type(), w);
+            y.at = o.data_ptr();
         }
-        const int st = qk_rope_bwd(g.data_ptr(), x, y.data_ptr(), tokens, gs, xs, ys, q, k, d, qw, kw,
-                                   dq.defined() ? dq.data_ptr() : nullptr, dk.defined() ? dk.data_ptr() : nullptr,
-                                   real(a[10]), real(a[9]), norm, &rope, code, at_ws, (uint64_t)bytes, w.stream());
+        at::Tensor dq, dk;
+        Workspace ws;
+        const bool weights = qw != nullptr && kw != nullptr;
+        if (weights) {
+            const int64_t bytes = qk_rope_bwd_workspace_bytes(d);
+            need(bytes > 0);
+            ws.given(a[15], bytes, w);
+        }
+        int st;
+        {
+            const Unlocked span;
+            y.make({tokens, width}, g);
+            if (weights) {
+                dq = fresh({d}, g);
+                dk = fresh({d}, g);
+                ws.make();
+            }
+            st = qk_rope_bwd(from, x, y.at, tokens, gs, xs, ys, q, k, d, qw, kw, weights ? dq.data_ptr() : nullptr,
+                             weights ? dk.data_ptr() : nullptr, bias, eps, norm, &rope, code, ws.at,
+                             (uint64_t)ws.bytes, w.stream());
+        }
         if (st != RMSNORM_OK) return status_of(st);
-        return Py_BuildValue("(NNN)", made.defined() ? THPVariable_Wrap(made) : same_object(a[14]), wrap_or_none(dq),
-                             wrap_or_none(dk));
+        return Py_BuildValue("(NNN)", y.result(), wrap_or_none(dq), wrap_or_none(dk));
     });
 }
 
@@ -275,7 +335,8 @@ PyObject *qk_norm_rope_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
 PyObject *qkv_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&]() -> PyObject * {
         need(n == 22 && qkv_append_fn != nullptr);
-        const at::Tensor &x = tensor(a[0]);
+        const at::Tensor x = tensor(a[0]);
+        void *from = x.data_ptr();
         const int code = code_of(x);
         const Where w(x);
         const int32_t q = count(a[6]), kv_heads = count(a[7]);
@@ -316,14 +377,23 @@ PyObject *qkv_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
         kv.cache_dtype = held == at::kFloat8_e4m3fn ? (int)RMSNORM_E4M3 : code;
         kv.k_scale = real(a[18]);
         kv.v_scale = real(a[19]);
-        at::Tensor made;
-        if (a[20] == Py_None) made = fresh({tokens, (int64_t)q * d}, x);
-        const at::Tensor &y = made.defined() ? made : tensor(a[20]);
-        const int64_t ys = head_rows(y, (int64_t)q * d, tokens, x.scalar_type(), w);
-        const int st = qkv_append_fn(x.data_ptr(), y.data_ptr(), tokens, xs, ys, q, kv_heads, d, qw, kw, real(a[14]),
-                                     real(a[13]), truth(a[15]), &rope, &kv, code, w.stream());
-        if (st != RMSNORM_OK) return status_of(st);
-        return made.defined() ? THPVariable_Wrap(made) : same_object(a[20]);
+        const float bias = real(a[14]), eps = real(a[13]);
+        const int norm = truth(a[15]);
+        Output y(a[20]);
+        int64_t ys = (int64_t)q * d;
+        if (y.given()) {
+            const at::Tensor &o = tensor(a[20]);
+            ys = head_rows(o, ys, tokens, x.scalar_type(), w);
+            y.at = o.data_ptr();
+        }
+        int st;
+        {
+            const Unlocked span;
+            y.make({tokens, (int64_t)q * d}, x);
+            st = qkv_append_fn(from, y.at, tokens, xs, ys, q, kv_heads, d, qw, kw, bias, eps, norm, &rope, &kv, code,
+                               w.stream());
+        }
+        return st == RMSNORM_OK ? y.result() : status_of(st);
     });
 }
 
@@ -348,7 +418,8 @@ const uint64_t *rng_of(PyObject *o, float p, const Where &w) {
 PyObject *rms_norm_dropout(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&]() -> PyObject * {
         need(n == 9 && dropout_fwd != nullptr);
-        const at::Tensor &x = tensor(a[0]);
+        const at::Tensor x = tensor(a[0]);
+        void *from = x.data_ptr();
         const int code = code_of(x);
         const Where w(x);
         const Rows r(x);
@@ -356,40 +427,46 @@ PyObject *rms_norm_dropout(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const float p = real(a[2]);
         const uint64_t *rng = rng_of(a[3], p, w);
         void *weight = vector(a[4], r.hidden, x.scalar_type(), w);
-        at::Tensor y, h;
-        if (a[7] == Py_None) y = fresh(x.sizes(), x);
-        if (a[8] == Py_None) h = fresh(x.sizes(), x);
-        void *yp = y.defined() ? y.data_ptr() : like(tensor(a[7]), x, w);
-        void *hp = h.defined() ? h.data_ptr() : like(tensor(a[8]), x, w);
-        const int st = dropout_fwd(x.data_ptr(), res, weight, yp, hp, r.rows, r.hidden, real(a[5]), real(a[6]), p, rng,
-                                   code, w.stream());
+        const float eps = real(a[5]), bias = real(a[6]);
+        Output y(a[7]), h(a[8]);
+        if (y.given()) y.at = like(tensor(a[7]), x, w);
+        if (h.given()) h.at = like(tensor(a[8]), x, w);
+        int st;
+        {
+            const Unlocked span;
+            y.make(x.sizes(), x);
+            h.make(x.sizes(), x);
+            st = dropout_fwd(from, res, weight, y.at, h.at, r.rows, r.hidden, eps, bias, p, rng, code, w.stream());
+        }
         if (st != RMSNORM_OK) return status_of(st);
-        return Py_BuildValue("(NN)", y.defined() ? THPVariable_Wrap(y) : same_object(a[7]),
-                             h.defined() ? THPVariable_Wrap(h) : same_object(a[8]));
+        return Py_BuildValue("(NN)", y.result(), h.result());
     });
 }
 
 // What the two gradients of the norm share: dw and the workspace, with a weight.
 struct Backward {
-    const at::Tensor &dy;
+    const at::Tensor dy;
     int code;
     Where w;
     Rows r;
-    void *h, *weight, *dh;
+    void *from, *h, *weight, *dh;
     at::Tensor dw;
-    c10::DataPtr ws;
-    void *at_ws = nullptr;
-    int64_t bytes = 0;
+    void *dw_at = nullptr;
+    Workspace ws;
     Backward(PyObject *dy_, PyObject *h_, PyObject *w_, PyObject *dh_, PyObject *workspace)
-        : dy(tensor(dy_)), code(code_of(dy)), w(dy), r(dy), h(like(tensor(h_), dy, w)),
+        : dy(tensor(dy_)), code(code_of(dy)), w(dy), r(dy), from(dy.data_ptr()), h(like(tensor(h_), dy, w)),
           weight(vector(w_, r.hidden, dy.scalar_type(), w)), dh(dh_ == Py_None ? nullptr : like(tensor(dh_), dy, w)) {
         if (weight == nullptr) return;
-        bytes = bwd_workspace_bytes(r.rows, r.hidden, code);
+        const int64_t bytes = bwd_workspace_bytes(r.rows, r.hidden, code);
         need(bytes > 0);
-        dw = fresh({r.hidden}, dy);
-        at_ws = workspace_of(workspace, bytes, w, &ws);
+        ws.given(workspace, bytes, w);
     }
-    void *dw_at() const { return dw.defined() ? dw.data_ptr() : nullptr; }
+    void make() {   // without the lock
+        if (weight == nullptr) return;
+        dw = fresh({r.hidden}, dy);
+        dw_at = dw.data_ptr();
+        ws.make();
+    }
 };
 
 // (dy, h, w, dresidual_out, eps, weight_bias, out, workspace)
@@ -397,13 +474,19 @@ PyObject *rms_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&]() -> PyObject * {
         need(n == 8 && norm_bwd != nullptr);
         Backward b(a[0], a[1], a[2], a[3], a[7]);
-        at::Tensor made;
-        if (a[6] == Py_None) made = fresh(b.dy.sizes(), b.dy);
-        void *dx = made.defined() ? made.data_ptr() : like(tensor(a[6]), b.dy, b.w);
-        const int st = norm_bwd(b.dy.data_ptr(), b.h, b.weight, b.dh, dx, b.dw_at(), b.r.rows, b.r.hidden, real(a[4]),
-                                real(a[5]), b.code, b.at_ws, (uint64_t)b.bytes, b.w.stream());
+        const float eps = real(a[4]), bias = real(a[5]);
+        Output dx(a[6]);
+        if (dx.given()) dx.at = like(tensor(a[6]), b.dy, b.w);
+        int st;
+        {
+            const Unlocked span;
+            b.make();
+            dx.make(b.dy.sizes(), b.dy);
+            st = norm_bwd(b.from, b.h, b.weight, b.dh, dx.at, b.dw_at, b.r.rows, b.r.hidden, eps, bias, b.code, b.ws.at,
+                          (uint64_t)b.ws.bytes, b.w.stream());
+        }
         if (st != RMSNORM_OK) return status_of(st);
-        return Py_BuildValue("(NN)", made.defined() ? THPVariable_Wrap(made) : same_object(a[6]), wrap_or_none(b.dw));
+        return Py_BuildValue("(NN)", dx.result(), wrap_or_none(b.dw));
     });
 }
 
@@ -412,18 +495,22 @@ PyObject *rms_norm_dropout_backward(PyObject *, PyObject *const *a, Py_ssize_t n
     return guarded([&]() -> PyObject * {
         need(n == 11 && dropout_bwd != nullptr);
         Backward b(a[0], a[1], a[4], a[5], a[10]);
-        const float p = real(a[2]);
+        const float p = real(a[2]), eps = real(a[6]), bias = real(a[7]);
         const uint64_t *rng = rng_of(a[3], p, b.w);
-        at::Tensor dres, dx;
-        if (a[8] == Py_None) dres = fresh(b.dy.sizes(), b.dy);
-        if (a[9] == Py_None) dx = fresh(b.dy.sizes(), b.dy);
-        void *rp = dres.defined() ? dres.data_ptr() : like(tensor(a[8]), b.dy, b.w);
-        void *xp = dx.defined() ? dx.data_ptr() : like(tensor(a[9]), b.dy, b.w);
-        const int st = dropout_bwd(b.dy.data_ptr(), b.h, b.weight, b.dh, rp, xp, b.dw_at(), b.r.rows, b.r.hidden,
-                                   real(a[6]), real(a[7]), p, rng, b.code, b.at_ws, (uint64_t)b.bytes, b.w.stream());
+        Output dres(a[8]), dx(a[9]);
+        if (dres.given()) dres.at = like(tensor(a[8]), b.dy, b.w);
+        if (dx.given()) dx.at = like(tensor(a[9]), b.dy, b.w);
+        int st;
+        {
+            const Unlocked span;
+            b.make();
+            dres.make(b.dy.sizes(), b.dy);
+            dx.make(b.dy.sizes(), b.dy);
+            st = dropout_bwd(b.from, b.h, b.weight, b.dh, dres.at, dx.at, b.dw_at, b.r.rows, b.r.hidden, eps, bias, p,
+                             rng, b.code, b.ws.at, (uint64_t)b.ws.bytes, b.w.stream());
+        }
         if (st != RMSNORM_OK) return status_of(st);
-        return Py_BuildValue("(NNN)", dres.defined() ? THPVariable_Wrap(dres) : same_object(a[8]),
-                             dx.defined() ? THPVariable_Wrap(dx) : same_object(a[9]), wrap_or_none(b.dw));
+        return Py_BuildValue("(NNN)", dres.result(), dx.result(), wrap_or_none(b.dw));
     });
 }
 
