@@ -9,7 +9,10 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
+import os
 import struct
+import warnings
 from typing import Optional
 
 import torch
@@ -197,13 +200,38 @@ _FAST_NAMES = ("rmsnorm_qk_rope_fwd", "rmsnorm_qk_rope_bwd", "rmsnorm_qk_rope_bw
                "rmsnorm_dropout_bwd")
 
 
+class _PythonCalls:
+    """In place of the extension module where there is none that the running
+    torch and Python can load: every call is left to the Python bodies."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
+def _load_fast():
+    from . import build
+    path = build.fastcall_path()
+    try:
+        if not os.path.exists(path):
+            raise ImportError(f"{path} does not exist")
+        spec = importlib.util.spec_from_file_location(f"{__package__}._fastcall", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        return module
+    except ImportError as e:
+        warnings.warn(f"no native Python calls for this torch and Python ({e}): the same kernels are called several "
+                      "microseconds slower; python -m row_reduction_norm_gb300.build makes them", RuntimeWarning,
+                      stacklevel=4)
+        return _PythonCalls()
+
+
 def _bind_fast():
     global _fast
     lib = N.load()
-    from . import _fastcall   # built beside the library
-    _fastcall.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in _FAST_NAMES))
-    _fast = _fastcall
-    return _fast
+    fast = _load_fast()
+    fast.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in _FAST_NAMES))
+    _fast = fast
+    return fast
 
 
 def _took(result, where: str) -> bool:

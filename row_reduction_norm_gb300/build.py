@@ -3,8 +3,9 @@
 Every ``csrc/*.cu`` file is compiled for sm_103a only (one ``-gencode``) in
 parallel, then linked into one shared library with the CUDA runtime linked
 statically.  No cmake, no torch extension machinery: plain nvcc.  Beside it,
-``csrc/fastcall.cpp`` becomes the Python module ``_fastcall.so`` (plain g++
-against the headers and libraries of the installed torch).
+``csrc/fastcall.cpp`` becomes the Python module ``_fastcall`` (plain g++ against
+the headers and libraries of the installed torch, whose version and Python's are
+part of its file name: a module for another torch or Python is never loaded).
 
     python -m row_reduction_norm_gb300.build [--force]
 """
@@ -27,7 +28,6 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "librmsnorm_gb300.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 FAST_SRC = os.path.join(CSRC, "fastcall.cpp")
-FAST_PATH = os.path.join(PKG, "_fastcall.so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-I", INCLUDE, "-I", CSRC]
@@ -56,26 +56,33 @@ def is_stale() -> bool:
     return any(os.path.getmtime(d) > t for d in _deps())
 
 
+def fastcall_path() -> str:
+    """Where the native Python calls for the running torch and Python are."""
+    import torch
+    return os.path.join(PKG, f"_fastcall-torch{torch.__version__}" + sysconfig.get_config_var("EXT_SUFFIX"))
+
+
 def build_fastcall(force: bool = False) -> str:
-    """Compile the native Python calls if they are missing or older than their sources."""
-    header = os.path.join(INCLUDE, "rmsnorm.h")
-    if not force and os.path.exists(FAST_PATH) and os.path.getmtime(FAST_PATH) > max(
+    """Compile the native Python calls if there are none for the running torch
+    and Python, or older ones than their sources."""
+    header, path = os.path.join(INCLUDE, "rmsnorm.h"), fastcall_path()
+    if not force and os.path.exists(path) and os.path.getmtime(path) > max(
             os.path.getmtime(FAST_SRC), os.path.getmtime(header)):
-        return FAST_PATH
+        return path
     import torch
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     includes = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(cuda, "include"), os.path.join(root, "include"),
                 os.path.join(root, "include", "torch", "csrc", "api", "include")]
-    tmp = FAST_PATH + f".tmp{os.getpid()}"
+    tmp = path + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
            *(f for i in includes for f in ("-I", i)), FAST_SRC, "-o", tmp, "-L", os.path.join(root, "lib"),
            "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on fastcall.cpp:\n{r.stderr}")
-    os.replace(tmp, FAST_PATH)
-    return FAST_PATH
+    os.replace(tmp, path)
+    return path
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:

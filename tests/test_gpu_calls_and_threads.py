@@ -58,3 +58,11 @@ def test_other_threads_run_during_a_native_call(tmp_path):
     seen = [s for s in stamps if first <= s <= last]
     gap = max(b - a for a, b in zip([first, *seen], [*seen, last]))
     assert gap < 0.1, f"another thread stood still for {gap * 1e3:.0f} ms"
+
+
+def test_without_the_native_calls(monkeypatch):
+    """The Python bodies on the current stream make the same calls."""
+    want = calls(7)
+    monkeypatch.setattr(api, "_fast", api._PythonCalls())
+    got = calls(7)
+    assert len(got) == len(want) and all(torch.equal(a, b) for a, b in zip(got, want))
