@@ -219,7 +219,7 @@ int backward(const void *dy, const void *h, const void *w, const void *dh, void 
             smem = (p.acc_in_smem ? (size_t)hidden * sizeof(float) : 0) + (size_t)(thr ? p.blocks_per_row : 0);
         }
         if (fn == nullptr) return RMSNORM_EINVAL;
-        if (smem > 48 * 1024 && (st = rrn::allow_smem(dev, fn)) != RMSNORM_OK) return st;
+        if (smem > rrn::kSmemUnasked && (st = rrn::allow_smem(dev, fn)) != RMSNORM_OK) return st;
         int resident = 0;
         if ((st = rrn::resident_blocks(dev, fn, threads, smem, &resident)) != RMSNORM_OK) return st;
         blocks = (int64_t)sms * resident;

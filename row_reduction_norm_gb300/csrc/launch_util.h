@@ -52,6 +52,9 @@ inline int launch_kernel(const void *fn, dim3 grid, int block, size_t smem, rmsn
 
 // Opt a kernel in to 226 KB of dynamic shared memory (cached per device and kernel).
 int allow_smem(int dev, const void *fn);
+// Dynamic shared memory for which that is needed: the limit without it is 48 KB
+// together with a kernel's static arrays, 1 KB of them at most.
+constexpr size_t kSmemUnasked = 47 * 1024;
 
 // Sums of the columns of partial[rows0 + rows1][ld] into the I/O type: of the
 // first rows0 rows to out0, of the rest to out1 (nullable).  partial is 16-byte

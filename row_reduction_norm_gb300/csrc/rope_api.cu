@@ -188,7 +188,7 @@ int launch_forward(rrn::RopeParams *p, int dtype, int64_t unit, bool il, int mod
     const int64_t iters = div_up((int64_t)p->q_heads + p->k_heads + p->v_heads, p->heads_a_warp);
     const size_t smem = shape == rrn::kRopeRagged ? rrn::kRagSmemBytes : rrn::kRopeSmemBytes;
     int resident = 0;
-    if (smem > 48 * 1024 && (st = rrn::allow_smem(dev, fn)) != RMSNORM_OK) return st;
+    if (smem > rrn::kSmemUnasked && (st = rrn::allow_smem(dev, fn)) != RMSNORM_OK) return st;
     if ((st = rrn::resident_blocks(dev, fn, 32 * rrn::kRopeMaxWarps, smem, &resident)) != RMSNORM_OK) return st;
     const int64_t most = (int64_t)sms * resident;
     int64_t slices = 1;
@@ -287,7 +287,7 @@ int rmsnorm_qk_rope_bwd(const void *dy, const void *x, void *dx, int64_t tokens,
         const int64_t iters_q = div_up(q_heads, p.heads_a_warp), iters_k = div_up(k_heads, p.heads_a_warp);
         const size_t smem = backward_smem(dtype, shape, norm == 1);
         int resident = 0;
-        if (smem > 48 * 1024 && (st = rrn::allow_smem(dev, fn)) != RMSNORM_OK) return st;
+        if (smem > rrn::kSmemUnasked && (st = rrn::allow_smem(dev, fn)) != RMSNORM_OK) return st;
         if ((st = rrn::resident_blocks(dev, fn, 32 * rrn::kRopeMaxWarps, smem, &resident)) != RMSNORM_OK) return st;
         int64_t most = (int64_t)sms * resident;
         if (most > kBwdMaxBlocks) most = kBwdMaxBlocks;
