@@ -17,7 +17,7 @@ using rrn::div_up;
 constexpr int64_t kMaxHidden = 65536;
 // Rows the two-pass gradient keeps its sums of dw for in shared memory: 192
 // KB of sums and 6 KB of mask bits within the 227 KB of a block.
-constexpr int64_t kSmemSums = 49152;
+constexpr int64_t kSmemSums = 49152;   // (208 KB in drop_loop_smem's steps)
 
 // Blocks of the gradient at most: each keeps a row of fp32 sums, which are
 // written and read once more.  Four a SM, twice that for narrow rows once a
@@ -211,12 +211,12 @@ int backward(const void *dy, const void *h, const void *w, const void *dh, void 
         } else if (const int shape = scalar_shape(vec, hidden, dtype, &p.classes); shape >= 0) {
             threads = rrn::kDropScalar[shape].gt;
             fn = rrn::drop_bwd_scalar(dtype, shape, dw != nullptr);
-            smem = (size_t)(thr ? 2 * p.blocks_per_row : 0);
+            smem = rrn::drop_scalar_smem(hidden, thr != 0);
         } else {
             threads = rrn::kDropLoopThreads;
             fn = rrn::drop_bwd_loop(dtype, vec, dw != nullptr);
             p.acc_in_smem = dw != nullptr && hidden <= kSmemSums;
-            smem = (p.acc_in_smem ? (size_t)hidden * sizeof(float) : 0) + (size_t)(thr ? p.blocks_per_row : 0);
+            smem = rrn::drop_loop_smem(hidden, p.acc_in_smem, thr != 0);
         }
         if (fn == nullptr) return RMSNORM_EINVAL;
         if (smem > rrn::kSmemUnasked && (st = rrn::allow_smem(dev, fn)) != RMSNORM_OK) return st;

@@ -1,6 +1,9 @@
 // dropout_pick.h -- the compiled residual-dropout and gradient kernels (internal).
 #pragma once
 
+#include <stddef.h>
+#include <stdint.h>
+
 namespace rrn {
 
 // Threads a row compiled for the register kernels, and chunks a thread: from
@@ -33,6 +36,23 @@ const void *drop_fwd_scalar(int dtype, int shape);
 const void *drop_bwd_scalar(int dtype, int shape, bool dw);
 // Two-pass kernels: blocks of kDropLoopThreads.
 constexpr int kDropLoopThreads = 1024;
+// Dynamic shared memory of the gradient's kernels whose need follows from the
+// width, in steps: it is part of the key under which a kernel's occupancy is
+// kept, for every operator of the library, so a process that meets many widths
+// must not make a key of each.  The steps cost no resident block: masks are at
+// most 8 KB, and of the two-pass kernel's 1024 threads two blocks stand on a SM
+// with up to 112 KB each.
+constexpr size_t kDropMaskStep = 1024, kDropSumsStep = 16384;
+inline size_t drop_smem_in_steps(size_t bytes, size_t step) { return (bytes + step - 1) / step * step; }
+// Single elements: two masks, a byte for eight elements, with dropout.
+inline size_t drop_scalar_smem(int64_t hidden, bool dropout) {
+    return dropout ? drop_smem_in_steps(2 * (size_t)((hidden + 7) / 8), kDropMaskStep) : 0;
+}
+// Two passes: fp32 sums of the columns, where they are kept there, and a mask.
+inline size_t drop_loop_smem(int64_t hidden, bool sums, bool dropout) {
+    const size_t mask = dropout ? (size_t)((hidden + 7) / 8) : 0;
+    return sums ? drop_smem_in_steps((size_t)hidden * 4 + mask, kDropSumsStep) : drop_smem_in_steps(mask, kDropMaskStep);
+}
 const void *drop_fwd_loop(int dtype, bool vec);
 const void *drop_bwd_loop(int dtype, bool vec, bool dw);
 
