@@ -20,10 +20,13 @@ constexpr int64_t kMaxHidden = 65536;
 constexpr int64_t kSmemSums = 49152;   // (208 KB in drop_loop_smem's steps)
 
 // Blocks of the gradient at most: each keeps a row of fp32 sums, which are
-// written and read once more.  Four a SM, twice that for narrow rows once a
-// block has 16 of them to read: bf16 32768 x 575 takes 92 us with eight a SM
-// and 139 with four, fp32 1023 x 1001 takes 6.5 us with four (6.6 with three,
-// 7.2 with two).
+// written and read once more.  Four a SM for narrow rows (fp32 1023 x 1001 takes
+// 6.5 us with four, 6.6 with three, 7.2 with two), and eight once a block has 16
+// of them to read: that is for rows of single elements, in tensors that start off
+// the 16-byte boundary (with dropout, eight / four a SM: bf16 32768 x 575 86 /
+// 141 us, 65536 x 201 100 / 177, fp32 32768 x 1001 115 / 141).  Aligned rows
+// take the same time with either, most of their kernels having fewer blocks
+// resident; but the workspace's size is asked for without the addresses.
 int64_t most_blocks(int64_t rows, int64_t hidden, int sms) {
     const int64_t few = hidden <= 4096 ? 4 : hidden <= 16384 ? 2 : 1;
     return sms * (hidden <= 1024 && rows >= 16 * 8 * (int64_t)sms ? 8 : few);
