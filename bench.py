@@ -105,11 +105,6 @@ def load_peaks():
         return FALLBACK_HBM_GBS, "fallback"
 
 
-# Host-side planning and argument checks: not device code, so not part of
-# the hash that says whether a profile still describes the kernels.
-HOST_ONLY_SOURCES = ("rmsnorm_api.cu", "rmsnorm_host.cu", "rmsnorm_host_static.cu")   # no kernel in them
-
-
 def code_tokens(text):
     """C/C++ source with comments removed and whitespace collapsed (a comment
     edit does not change the code a profile describes)."""
@@ -134,16 +129,42 @@ def code_tokens(text):
     return " ".join("".join(out).split())
 
 
-def kernel_source_hash():
-    """Hash of the device code (kernels and their instantiations), comments
-    and layout aside."""
+# The .cu files that a family of kernels is instantiated in, by how their names
+# begin; what they include belongs to the family too.  A profile is of one
+# family, and other families' files say nothing about it.
+KERNEL_FAMILIES = {
+    "norm": ("cast_", "cluster.cu", "ln_", "loop_", "mx_", "nv_", "reg_", "tma.cu"),
+    "rope": ("rope_fwd_", "rope_bwd_", "rope_rag_", "colsum.cu"),
+    "dropout": ("drop_", "colsum.cu"),
+}
+
+
+def family_sources(family, names, read):
+    """The files of a family among ``names``, sorted; read(name) gives a file's text."""
+    left = [n for n in names if n.endswith(".cu") and n.startswith(KERNEL_FAMILIES[family])]
+    found = set()
+    while left:
+        name = left.pop()
+        if name in names and name not in found:
+            found.add(name)
+            left += re.findall(r'^\s*#include\s+"([^"]+)"', read(name), re.M)
+    return sorted(found)
+
+
+def kernel_source_hash(family="norm"):
+    """Hash of a family's device code (kernels and their instantiations),
+    comments and layout aside."""
     import hashlib
-    h = hashlib.sha256()
     csrc = os.path.join(ROOT, "row_reduction_norm_gb300", "csrc")
-    for name in sorted(os.listdir(csrc)):
-        if name.endswith((".cu", ".cuh", ".h")) and name not in HOST_ONLY_SOURCES:
-            with open(os.path.join(csrc, name), encoding="utf-8") as f:
-                h.update(name.encode() + b"\0" + code_tokens(f.read()).encode())
+    names = [n for n in os.listdir(csrc) if n.endswith((".cu", ".cuh", ".h"))]
+
+    def read(name):
+        with open(os.path.join(csrc, name), encoding="utf-8") as f:
+            return f.read()
+
+    h = hashlib.sha256()
+    for name in family_sources(family, names, read):
+        h.update(name.encode() + b"\0" + code_tokens(read(name)).encode())
     return h.hexdigest()[:16]
 
 
