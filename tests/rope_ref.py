@@ -6,8 +6,8 @@ Tolerances, u = 2^-24 (half a step of fp32 relative to the value):
   normalised value  18 u relative (the derivation in parity.py: a sum tree of
                     at most 21 levels, mean, eps, rsqrtf, two products; a lane
                     adds at most 8 units, 3 levels in one, 5 shuffles)
-  sine and cosine   2e-7 absolute, 3.4 u (sincospif's 2 ulp and the rounding
-                    of the argument, at most an eighth of a turn, to fp32)
+  sine and cosine   2e-7 absolute, 3.4 u (the kernels' own series on at most an
+                    eighth of a turn: test_rope_angles_host.py)
   rotation          a product and a fused multiply-add: 2 u of |n_a| + |n_b|
 so a rotated value is within 24 u (|n_a| + |n_b|), taken as 32 u = 1.9e-6,
 and one rounding to the output type, eps / 2 relative.  A value's partner
