@@ -680,7 +680,7 @@ __global__ void __launch_bounds__(BLOCK) drop_bwd_loop_kernel(const DropParams p
 
 template <typename T, int GT, int CH>
 __global__ void __launch_bounds__(GT) drop_fwd_scalar_kernel(const DropParams p) {
-    __shared__ float red[2][1][32];
+    __shared__ __align__(16) float red[2][1][32];
     extern __shared__ uint8_t mask[];   // [blocks_per_row], with dropout
     const int t = threadIdx.x, n = p.units;
     pdl_wait_for_inputs();
@@ -754,7 +754,7 @@ __device__ __forceinline__ BothF32 both_of(F32) { return {}; }
 template <typename T, int GT, int CH, bool DW>
 __global__ void __launch_bounds__(GT) drop_bwd_scalar_kernel(const DropParams p) {
     using Both = decltype(both_of(T{}));
-    __shared__ float red[2][2][32];
+    __shared__ __align__(16) float red[2][2][32];
     extern __shared__ uint8_t masks[];   // [2][blocks_per_row], with dropout
     const int t = threadIdx.x, n = p.units;
     pdl_wait_for_inputs();

@@ -60,10 +60,25 @@ __device__ __forceinline__ int value_of(int lane) {
     else return lane & (K - 1);
 }
 
-// Sums of M values' N parts each (parts[m][i], in shared memory), neighbours
-// added in pairs, for every lane.  stride: between the values' parts.
+// Sums of M values' N parts each (parts[m * stride + i], in shared memory),
+// neighbours added in pairs, for every lane: read by every lane, or, many of
+// them, a part a lane.
 template <int N, int M>
-__device__ __forceinline__ void parts_add(const float *parts, int stride, int lane, float (&sum)[M]) {
+__device__ __forceinline__ void parts_read(const float *parts, int stride, float (&sum)[M]) {
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        float v[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = parts[m * stride + i];
+#pragma unroll
+        for (int n = N; n > 1; n /= 2)
+#pragma unroll
+            for (int i = 0; i < n / 2; ++i) v[i] = v[2 * i] + v[2 * i + 1];
+        sum[m] = v[0];
+    }
+}
+template <int N, int M>
+__device__ __forceinline__ void parts_share(const float *parts, int stride, int lane, float (&sum)[M]) {
     if constexpr (M == 2 && N <= 16) {   // both at once, in the halves of the warp
         float v = parts[(lane >> 4) * stride + (lane & (N - 1))];
 #pragma unroll
@@ -105,7 +120,8 @@ __device__ __forceinline__ void class_sums(X x, Y y, float (*red)[32], int t, fl
         red[i / A][i % A * WPR + t / 32] = v;
     }
     __syncthreads();
-    parts_add<A * WPR, M>(red[0], 32, t & 31, sum);
+    if constexpr (A * WPR <= 8) parts_read<A * WPR, M>(red[0], 32, sum);
+    else parts_share<A * WPR, M>(red[0], 32, t & 31, sum);
 }
 // With the classes as a number: 1, 2 or, up to 2048 columns, 4.
 template <int GT, int CH, int M, typename X, typename Y>
@@ -188,17 +204,7 @@ __device__ __forceinline__ void shifted_sums(const float (&acc)[M][V], int s, Sh
     if constexpr (WPR > 1) {
         if (lane < M) sh.warp[lane][t / 32] = all;
         __syncthreads();
-#pragma unroll
-        for (int m = 0; m < M; ++m) {
-            float w[WPR];
-#pragma unroll
-            for (int i = 0; i < WPR; ++i) w[i] = sh.warp[m][i];
-#pragma unroll
-            for (int n = WPR; n > 1; n /= 2)
-#pragma unroll
-                for (int i = 0; i < n / 2; ++i) w[i] = w[2 * i] + w[2 * i + 1];
-            sum[m] = w[0];
-        }
+        parts_read<WPR, M>(sh.warp[0], WPR, sum);
     } else if constexpr (M == 2) {
         const float other = __shfl_xor_sync(0xffffffffu, all, 1);
         sum[0] = lane & 1 ? other : all;
