@@ -98,15 +98,16 @@ int shift_holding(int64_t hidden, int dtype) {
 // rows of single elements are faster.  Starting costs the former more (weights
 // an element at a time, blocks of several rows) and a row less.  Measured on
 // GB300, us, shifted / single elements, dropout 0.1:
-//   gradient  bf16 501 x 608 rows 5.2 / 5.5, 1001 x 608 7.4 / 6.5, x 2000 11.5 /
-//             12.3, 2047 x 608 8.8 / 10.7, 8191 x 6000 125 / 313; fp32 501 x 608
-//             5.9 / 5.0, x 2000 8.4 / 9.0, 1001 x 2000 17.5 / 13.3, x 6000 29.5 /
-//             31.7, 3001 x 152 6.4 / 9.5, x 6000 65 / 95; and with a third of
-//             the chunks unused, 2047 x 6000 55.9 / 51.3
-//   forward   bf16 101 x 2000 4.3 / 3.5, x 6000 5.3 / 6.9, 2047 x 2000 12.5 /
-//             11.0, x 6000 28.9 / 30.5, 3001 x 608 6.8 / 8.1, 12001 x 6000 127 /
-//             389; fp32 101 x 6000 4.7 / 6.6, 501 x 6000 10.4 / 11.4, and wider
-//             rows no faster (1001 x 6000 19.8 / 17.5, 4095 x 6000 88 / 65)
+//   gradient  bf16 501 x 608 rows 5.2 / 5.5, 1001 x 608 7.4 / 6.7, x 2000 11.7 /
+//             12.5, 2047 x 608 9.0 / 8.6, 8191 x 6000 130 / 261; fp32 501 x 608
+//             5.8 / 5.0, x 2000 8.4 / 8.7, 1001 x 2000 17.8 / 12.9, x 6000 30.7 /
+//             30.9, 3001 x 152 6.6 / 7.4, x 6000 70 / 89; and with a third of
+//             the chunks unused, 2047 x 6000 60.0 / 49.8
+//   forward   bf16 101 x 2000 4.3 / 3.1, x 6000 5.4 / 6.6, 2047 x 2000 12.8 /
+//             11.7, x 6000 30.0 / 32.2, 3001 x 608 6.7 / 7.9, 12001 x 6000 132 /
+//             391; fp32 101 x 6000 4.8 / 6.6, 501 x 6000 10.8 / 12.0, and wider
+//             rows no faster (1001 x 6000 20.0 / 17.5, 4095 x 6000 93 / 66)
+// Rows have the same bits from either (row_classes.cuh).
 int shift_shape(const void *const *ptrs, int n, int64_t rows, int64_t hidden, int dtype, bool gradient) {
     for (int i = 0; i < n; ++i)
         if (!rrn::on_boundary(ptrs[i], 16)) return -1;

@@ -672,11 +672,10 @@ __global__ void __launch_bounds__(BLOCK) drop_bwd_loop_kernel(const DropParams p
 // thread t owns columns t, t + GT, ... (CH of them), so a warp's accesses are
 // consecutive, every element is read once, and what a 2-byte access wastes is
 // issue slots, not bandwidth.  The mask is made a byte for 8 elements by
-// whichever threads, in shared memory.  bf16 16384 x 2047 takes 78 us (52 % of
-// the measured copy bandwidth), its gradient 135 (37 %); two passes over the
-// row (below) took 102 and 255.  Blocks of 1024 threads for the longer rows
-// measured slower than 512 with twice the columns (8192 x 8191 226 against 183
-// us).
+// whichever threads, in shared memory.  bf16 16384 x 2047 takes 83 us (49 % of
+// the measured copy bandwidth), its gradient 113 (45 %); two passes over the row
+// (above) took 102 and 255.  Blocks of 1024 threads for the longer rows measured
+// a quarter slower than 512 with twice the columns.
 
 template <typename T, int GT, int CH>
 __global__ void __launch_bounds__(GT) drop_fwd_scalar_kernel(const DropParams p) {

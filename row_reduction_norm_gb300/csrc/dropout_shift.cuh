@@ -106,8 +106,8 @@ __device__ __forceinline__ void put_chunk(char *at, const float (&v)[T::kVec], i
     }
 }
 
-// Three blocks a SM rather than two: bf16 16384 x 2047 68.8 us, 81.8 with two
-// (78 us element by element).
+// bf16 16384 x 2047 takes 71.8 us (82.7 element by element).  Three blocks a SM
+// rather than two, with which it took a fifth more.
 template <typename T, int GT, int CH>
 __global__ void __launch_bounds__(drop_block_threads(GT), GT < 512 ? 3 : 1) drop_fwd_shift_kernel(const DropParams p) {
     constexpr int V = T::kVec, S = 16 / V, BLOCK = drop_block_threads(GT), RPB = BLOCK / GT;
@@ -210,9 +210,9 @@ __global__ void __launch_bounds__(drop_block_threads(GT), GT < 512 ? 3 : 1) drop
     }
 }
 
-// The gradient (see drop_bwd_kernel).  bf16 8192 x 4095 takes 86 us, 8192 x
-// 8191 167 (213 and 419 by single elements; aligned 8192 x 8192 rows 107):
-// what bounds it is issue slots, about 350 instructions for 32 chunks.
+// The gradient (see drop_bwd_kernel).  bf16 8192 x 4095 takes 91 us, 8192 x
+// 8191 173 (172 and 349 by single elements; aligned 8192 x 8192 rows 107):
+// what bounds it is issue slots, 435 instructions for 32 chunks.
 template <typename T, int GT, int CH, bool DW>
 __global__ void __launch_bounds__(drop_block_threads(GT), drop_bwd_resident(GT)) drop_bwd_shift_kernel(const DropParams p) {
     constexpr int V = T::kVec, S = 16 / V, BLOCK = drop_block_threads(GT), RPB = BLOCK / GT;
