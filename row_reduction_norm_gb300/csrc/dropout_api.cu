@@ -98,11 +98,11 @@ int shift_holding(int64_t hidden, int dtype) {
 // rows of single elements are faster.  Starting costs the former more (weights
 // an element at a time, blocks of several rows) and a row less.  Measured on
 // GB300, us, shifted / single elements, dropout 0.1:
-//   gradient  bf16 501 x 608 rows 5.2 / 5.5, 1001 x 608 7.4 / 6.7, x 2000 11.7 /
-//             12.5, 2047 x 608 9.0 / 8.6, 8191 x 6000 130 / 261; fp32 501 x 608
-//             5.8 / 5.0, x 2000 8.4 / 8.7, 1001 x 2000 17.8 / 12.9, x 6000 30.7 /
-//             30.9, 3001 x 152 6.6 / 7.4, x 6000 70 / 89; and with a third of
-//             the chunks unused, 2047 x 6000 60.0 / 49.8
+//   gradient  bf16 501 x 608 rows 5.2 / 5.5, 1001 x 608 7.4 / 6.6, x 2000 11.7 /
+//             12.2, 2047 x 608 9.0 / 8.6, 8191 x 6000 130 / 257; fp32 501 x 608
+//             5.8 / 5.1, x 2000 8.4 / 8.8, 1001 x 2000 17.8 / 13.0, x 6000 30.6 /
+//             30.7, 3001 x 152 6.6 / 7.6, x 6000 70 / 89; and with a third of
+//             the chunks unused, 2047 x 6000 60.0 / 49.3
 //   forward   bf16 101 x 2000 4.3 / 3.1, x 6000 5.4 / 6.6, 2047 x 2000 12.8 /
 //             11.7, x 6000 30.0 / 32.2, 3001 x 608 6.7 / 7.9, 12001 x 6000 132 /
 //             391; fp32 101 x 6000 4.8 / 6.6, 501 x 6000 10.8 / 12.0, and wider

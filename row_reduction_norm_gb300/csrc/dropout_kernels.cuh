@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(BLOCK) drop_bwd_loop_kernel(const DropParams p
 // consecutive, every element is read once, and what a 2-byte access wastes is
 // issue slots, not bandwidth.  The mask is made a byte for 8 elements by
 // whichever threads, in shared memory.  bf16 16384 x 2047 takes 83 us (49 % of
-// the measured copy bandwidth), its gradient 113 (45 %); two passes over the row
+// the measured copy bandwidth), its gradient 111 (45 %); two passes over the row
 // (above) took 102 and 255.  Blocks of 1024 threads for the longer rows measured
 // a quarter slower than 512 with twice the columns.
 

@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(drop_block_threads(GT), GT < 512 ? 3 : 1) drop
 }
 
 // The gradient (see drop_bwd_kernel).  bf16 8192 x 4095 takes 91 us, 8192 x
-// 8191 173 (172 and 349 by single elements; aligned 8192 x 8192 rows 107):
+// 8191 173 (169 and 343 by single elements; aligned 8192 x 8192 rows 107):
 // what bounds it is issue slots, 435 instructions for 32 chunks.
 template <typename T, int GT, int CH, bool DW>
 __global__ void __launch_bounds__(drop_block_threads(GT), drop_bwd_resident(GT)) drop_bwd_shift_kernel(const DropParams p) {
