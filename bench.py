@@ -136,6 +136,9 @@ KERNEL_FAMILIES = {
     "norm": ("cast_", "cluster.cu", "ln_", "loop_", "mx_", "nv_", "reg_", "tma.cu"),
     "rope": ("rope_fwd_", "rope_bwd_", "rope_rag_", "colsum.cu"),
     "dropout": ("drop_", "colsum.cu"),
+    "embedding": ("embed_",),
+    "logprobs": ("logprobs_",),
+    "grads": ("grads_",),
 }
 
 

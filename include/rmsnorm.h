@@ -502,6 +502,135 @@ int rmsnorm_dropout_bwd(const void *dy, const void *h, const void *w, const void
                         void *workspace, uint64_t workspace_bytes, rmsnorm_stream_t stream);
 
 /*
+ * Lookup of token embeddings with scaling:
+ *   y[t] = RN_T( scale * table[tokens[t]] ),   t = 0 .. count - 1
+ *   tokens      DEVICE int32 or int64 [count] (token_bytes 4 or 8).  A token
+ *               outside 0 .. vocab - 1 (-1 marks padding) gives a row of zeros
+ *   table       [vocab, width], rows table_stride elements apart
+ *   y           [count, width] contiguous, not overlapping the table
+ * table, y and rows that are multiples of 16 bytes move 128 bits at a time,
+ * others in pieces of the largest power of two bytes that divides them, with
+ * the same results.  width above 65536 is RMSNORM_EUNSUPPORTED.  count == 0
+ * does nothing.  Like the calls below it returns RMSNORM_OK or a negative
+ * status.
+ */
+int rmsnorm_embedding_fwd(const void *tokens, int token_bytes, const void *table, void *y, int64_t count,
+                          int64_t vocab, int64_t width, int64_t table_stride, float scale, int dtype,
+                          rmsnorm_stream_t stream);
+
+/*
+ * Gradient of rmsnorm_embedding_fwd in the table:
+ *   dtable[v] = RN( scale * sum over t with tokens[t] = v of dy[t] )
+ * with accumulate = 0 (every row is written, zeros where no token is v), and
+ * with accumulate = 1
+ *   dtable[v] = RN( dtable[v] + scale * sum ... )     for the v among the tokens
+ * (other rows are neither read nor written).  Tokens outside 0 .. vocab - 1
+ * take no part.
+ *   dy          [count, width] contiguous, of type dtype
+ *   dtable      [vocab, width], rows table_stride elements apart, of type
+ *               grad_dtype: dtype, or RMSNORM_F32 with bf16 dy
+ *   workspace   DEVICE memory, 16-byte aligned, of at least
+ *               rmsnorm_embedding_bwd_workspace_bytes(count, vocab, width)
+ *               bytes, used by no one else until the call's work is done
+ * The tokens are sorted (stably) and a row's terms added up in fp32 in an
+ * order that follows from the tokens alone: no atomics on values, equal bits
+ * from run to run.  count and vocab up to 2^30, width up to 65536 (else
+ * RMSNORM_EUNSUPPORTED).
+ */
+int rmsnorm_embedding_bwd(const void *dy, const void *tokens, int token_bytes, void *dtable, int64_t count,
+                          int64_t vocab, int64_t width, int64_t table_stride, float scale, int accumulate,
+                          int dtype, int grad_dtype, void *workspace, uint64_t workspace_bytes,
+                          rmsnorm_stream_t stream);
+
+/* Bytes of workspace rmsnorm_embedding_bwd needs (no CUDA call), or a negative status. */
+int64_t rmsnorm_embedding_bwd_workspace_bytes(int64_t count, int64_t vocab, int64_t width);
+
+/*
+ * Log probabilities of given tokens, with the entropy and the likeliest
+ * alternatives, of rows of logits x, all in one pass over them.  With
+ * m = max_v x_v, z_v = (x_v - m) / temperature and L = log(sum_v exp(z_v)):
+ *   logprobs[r]      z_{tokens[r]} - L;  0 where the token lies outside
+ *                    0 .. vocab - 1 (a place that is left out)
+ *   stats[r]         (m, L), what rmsnorm_logprobs_bwd starts from
+ *   entropy[r]       -sum_v p_v log p_v = L - sum_v p_v z_v,  p_v = exp(z_v - L)
+ *   top_ids[r]       the `top` tokens of the largest logits, largest first,
+ *                    equal ones (+0 and -0 are) by the lower id; a NaN counts
+ *                    as -infinity here
+ *   top_logprobs[r]  their log probabilities
+ *   logits           [rows, vocab], rows row_stride elements apart
+ *   tokens           DEVICE int32 or int64 [rows] (token_bytes 4 or 8); may be
+ *                    NULL with logprobs NULL
+ *   logprobs, stats, entropy   fp32, [rows], [rows, 2] and [rows], each optional
+ *   top_logprobs, top_ids      [rows, top] fp32 and int32, NULL with top = 0;
+ *                              top up to 32 and at most vocab
+ * Logits of -infinity are masked: probability 0, no part in the entropy.  A
+ * row of nothing else has log probabilities of -infinity, an entropy of 0,
+ * and stats (-infinity, -infinity).  A row that holds a NaN or +infinity has
+ * NaN for all of them.  Sums are fp32 in an order that follows from vocab and
+ * dtype alone: a row has the same bits in every batch and at every address.
+ * vocab up to 2^20 (else RMSNORM_EUNSUPPORTED); 0 < temperature, with
+ * temperature and its inverse finite and normal.  rows == 0 does nothing.
+ */
+int rmsnorm_logprobs_fwd(const void *logits, const void *tokens, int token_bytes, float *logprobs, float *stats,
+                         float *entropy, float *top_logprobs, int32_t *top_ids, int64_t rows, int64_t vocab,
+                         int64_t row_stride, int32_t top, float temperature, int dtype, rmsnorm_stream_t stream);
+
+/*
+ * Gradient of rmsnorm_logprobs_fwd's log probabilities and entropies in the
+ * logits, one pass.  With g = dlogprobs[r] (0 where the token lies outside
+ * 0 .. vocab - 1) and h = dentropy[r]:
+ *   dlogits_v = RN_T( ( g ([v = tokens[r]] - p_v) - h p_v (log p_v + entropy[r]) ) / temperature )
+ *   stats, entropy   the forward's (entropy only with dentropy)
+ *   dlogprobs, dentropy   fp32 [rows], each optional
+ *   dlogits          [rows, vocab], rows dlogits_stride elements apart; may be
+ *                    the logits (same stride)
+ * Masked logits get 0 (but for a masked token's own g).  Rows with g = h = 0,
+ * and rows of masked logits only, are zeros, and their logits are not read.
+ * Other arguments and limits as the forward.
+ */
+int rmsnorm_logprobs_bwd(const void *logits, const void *tokens, int token_bytes, const float *stats,
+                         const float *dlogprobs, const float *entropy, const float *dentropy, void *dlogits,
+                         int64_t rows, int64_t vocab, int64_t row_stride, int64_t dlogits_stride,
+                         float temperature, int dtype, rmsnorm_stream_t stream);
+
+/* A tensor among those whose norm is taken together (a HOST array of them). */
+typedef struct {
+    const void *grad;   /* device, [count] contiguous                              */
+    void *out;          /* device, [count]: where the clipped one goes (may be grad) */
+    int64_t count;      /* elements, >= 0                                          */
+    int32_t dtype;      /* RMSNORM_F32 or RMSNORM_BF16                             */
+    int32_t reserved;   /* 0                                                       */
+} rmsnorm_grad_t;
+
+/*
+ * The norm of many tensors together, and their clipping:
+ *   norm   = sqrt( sum over all elements of g^2 )
+ *   factor = min(1, max_norm / norm)            (1 for a norm of 0)
+ *   out    = RN( g factor )
+ *   grads       HOST array of n, read during the call
+ *   norm        DEVICE fp32 [1]
+ *   max_norm    >= 0
+ *   workspace   DEVICE memory, 16-byte aligned, of at least
+ *               rmsnorm_grad_norm_workspace_bytes() bytes, used by no one else
+ *               until the call's work is done
+ * rmsnorm_grad_norm writes the norm alone (`out` is not looked at);
+ * rmsnorm_clip_grads the tensors too, of which those with out == grad are not
+ * touched when the factor is 1.  Squares beyond fp32's range do not over- or
+ * underflow the norm (blocks of elements that hold such are added up again,
+ * scaled).  An infinite norm has the factor 0 (finite elements become 0,
+ * infinite ones NaN), a NaN makes the norm and every element NaN.  Sums are
+ * formed in an order that follows from the sizes, the alignment and the
+ * device alone (no atomics).  n == 0 writes a norm of 0.
+ */
+int rmsnorm_grad_norm(const rmsnorm_grad_t *grads, int64_t n, float *norm, void *workspace,
+                      uint64_t workspace_bytes, rmsnorm_stream_t stream);
+int rmsnorm_clip_grads(const rmsnorm_grad_t *grads, int64_t n, float max_norm, float *norm, void *workspace,
+                       uint64_t workspace_bytes, rmsnorm_stream_t stream);
+
+/* Bytes of workspace rmsnorm_grad_norm and rmsnorm_clip_grads need (no CUDA call). */
+int64_t rmsnorm_grad_norm_workspace_bytes(void);
+
+/*
  * RMSNorm with a block-scaled MXFP8 output (OCP Microscaling Formats v1.0:
  * E4M3 elements, one E8M0 scale per 32 elements; block-scaled low-precision
  * formats are named in "CuTeDSL at Perplexity", section "Blackwell

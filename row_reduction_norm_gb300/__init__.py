@@ -12,6 +12,8 @@ from ._native import (  # noqa: F401  (the C ABI, same names)
     rmsnorm_max_hidden, rmsnorm_plan, rmsnorm_plan_ex, rmsnorm_plan_for, rmsnorm_regime, rmsnorm_qk_fwd, rmsnorm_qk_plan_for,
     Rope, PagedKV, rmsnorm_qk_rope_fwd, rmsnorm_qk_rope_bwd, rmsnorm_qk_rope_bwd_workspace_bytes, rmsnorm_qkv_append,
     rmsnorm_dropout_fwd, rmsnorm_bwd, rmsnorm_bwd_workspace_bytes, rmsnorm_dropout_bwd,
+    rmsnorm_embedding_fwd, rmsnorm_embedding_bwd, rmsnorm_embedding_bwd_workspace_bytes, rmsnorm_logprobs_fwd,
+    rmsnorm_logprobs_bwd, Grad, rmsnorm_grad_norm, rmsnorm_clip_grads, rmsnorm_grad_norm_workspace_bytes,
     layernorm_fwd, layernorm_plan_for, rmsnorm_fwd_mxfp8, rmsnorm_mxfp8_plan_for, rmsnorm_fwd_nvfp4,
     rmsnorm_nvfp4_plan_for, rmsnorm_fwd_host, rmsnorm_host_workspace_bytes, rmsnorm_fwd_host_static,
     rmsnorm_reg_max_chunks, rmsnorm_wait_timeouts, rmsnorm_strerror,
@@ -20,6 +22,7 @@ from ._native import (  # noqa: F401  (the C ABI, same names)
 from .api import (  # noqa: F401
     rms_norm, plan_for, qk_norm, qk_plan_for, qk_norm_rope, qk_norm_rope_backward, qkv_append,
     rms_norm_dropout, rms_norm_dropout_backward, rms_norm_backward, layer_norm, layer_norm_plan_for, rms_norm_mxfp8,
-    rms_norm_mxfp8_plan_for, rms_norm_nvfp4, rms_norm_nvfp4_plan_for, rms_norm_host, dtype_code)
+    rms_norm_mxfp8_plan_for, rms_norm_nvfp4, rms_norm_nvfp4_plan_for, rms_norm_host, dtype_code,
+    embedding, embedding_backward, TokenLogprobs, token_logprobs, token_logprobs_backward, grad_norm, clip_grad_norm)
 
 __version__ = "0.1.0"

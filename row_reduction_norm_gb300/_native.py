@@ -69,6 +69,9 @@ EXPORTED = ["rmsnorm_fwd", "rmsnorm_regime", "rmsnorm_plan", "rmsnorm_plan_ex", 
             "rmsnorm_qk_fwd", "rmsnorm_qk_plan_for",
             "rmsnorm_qk_rope_fwd", "rmsnorm_qk_rope_bwd", "rmsnorm_qk_rope_bwd_workspace_bytes", "rmsnorm_qkv_append",
             "rmsnorm_dropout_fwd", "rmsnorm_bwd", "rmsnorm_bwd_workspace_bytes", "rmsnorm_dropout_bwd",
+            "rmsnorm_embedding_fwd", "rmsnorm_embedding_bwd", "rmsnorm_embedding_bwd_workspace_bytes",
+            "rmsnorm_logprobs_fwd", "rmsnorm_logprobs_bwd",
+            "rmsnorm_grad_norm", "rmsnorm_clip_grads", "rmsnorm_grad_norm_workspace_bytes",
             "rmsnorm_fwd_mxfp8", "rmsnorm_mxfp8_plan_for",
             "rmsnorm_fwd_nvfp4", "rmsnorm_nvfp4_plan_for",
             "layernorm_fwd", "layernorm_plan_for",
@@ -152,6 +155,17 @@ class PagedKV(ctypes.Structure):
     ]
 
 
+class Grad(ctypes.Structure):
+    """Mirror of ``rmsnorm_grad_t``."""
+    _fields_ = [
+        ("grad", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("count", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -210,6 +224,22 @@ def load():
         lib.rmsnorm_bwd_workspace_bytes.restype = i64
         lib.rmsnorm_dropout_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, f32, f32, f32, vp, i32, vp, u64, vp]
         lib.rmsnorm_dropout_bwd.restype = i32
+        lib.rmsnorm_embedding_fwd.argtypes = [vp, i32, vp, vp, i64, i64, i64, i64, f32, i32, vp]
+        lib.rmsnorm_embedding_fwd.restype = i32
+        lib.rmsnorm_embedding_bwd.argtypes = [vp, vp, i32, vp, i64, i64, i64, i64, f32, i32, i32, i32, vp, u64, vp]
+        lib.rmsnorm_embedding_bwd.restype = i32
+        lib.rmsnorm_embedding_bwd_workspace_bytes.argtypes = [i64, i64, i64]
+        lib.rmsnorm_embedding_bwd_workspace_bytes.restype = i64
+        lib.rmsnorm_logprobs_fwd.argtypes = [vp, vp, i32, vp, vp, vp, vp, vp, i64, i64, i64, ctypes.c_int32, f32, i32, vp]
+        lib.rmsnorm_logprobs_fwd.restype = i32
+        lib.rmsnorm_logprobs_bwd.argtypes = [vp, vp, i32, vp, vp, vp, vp, vp, i64, i64, i64, i64, f32, i32, vp]
+        lib.rmsnorm_logprobs_bwd.restype = i32
+        lib.rmsnorm_grad_norm.argtypes = [ctypes.POINTER(Grad), i64, vp, vp, u64, vp]
+        lib.rmsnorm_grad_norm.restype = i32
+        lib.rmsnorm_clip_grads.argtypes = [ctypes.POINTER(Grad), i64, f32, vp, vp, u64, vp]
+        lib.rmsnorm_clip_grads.restype = i32
+        lib.rmsnorm_grad_norm_workspace_bytes.argtypes = []
+        lib.rmsnorm_grad_norm_workspace_bytes.restype = i64
         lib.rmsnorm_fwd_mxfp8.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, ctypes.c_float, ctypes.c_float, i32,
                                           ctypes.POINTER(Plan), vp]
         lib.rmsnorm_fwd_mxfp8.restype = i32
@@ -413,6 +443,84 @@ def rmsnorm_dropout_bwd_status(dy, h, w, dresidual_out, dresidual, dx, dw, rows,
                                dtype, workspace, workspace_bytes, stream=0) -> int:
     return load().rmsnorm_dropout_bwd(dy, h, w, dresidual_out, dresidual, dx, dw, rows, hidden, eps, weight_bias,
                                       p_drop, rng, dtype, workspace, workspace_bytes, stream)
+
+
+def rmsnorm_embedding_fwd(tokens, token_bytes, table, y, count, vocab, width, table_stride, scale, dtype, stream=0):
+    _check(rmsnorm_embedding_fwd_status(tokens, token_bytes, table, y, count, vocab, width, table_stride, scale,
+                                        dtype, stream),
+           "rmsnorm_embedding_fwd")
+
+
+def rmsnorm_embedding_fwd_status(tokens, token_bytes, table, y, count, vocab, width, table_stride, scale, dtype,
+                                 stream=0) -> int:
+    return load().rmsnorm_embedding_fwd(tokens, token_bytes, table, y, count, vocab, width, table_stride, scale,
+                                        dtype, stream)
+
+
+def rmsnorm_embedding_bwd(dy, tokens, token_bytes, dtable, count, vocab, width, table_stride, scale, accumulate,
+                          dtype, grad_dtype, workspace, workspace_bytes, stream=0):
+    _check(rmsnorm_embedding_bwd_status(dy, tokens, token_bytes, dtable, count, vocab, width, table_stride, scale,
+                                        accumulate, dtype, grad_dtype, workspace, workspace_bytes, stream),
+           "rmsnorm_embedding_bwd")
+
+
+def rmsnorm_embedding_bwd_status(dy, tokens, token_bytes, dtable, count, vocab, width, table_stride, scale,
+                                 accumulate, dtype, grad_dtype, workspace, workspace_bytes, stream=0) -> int:
+    return load().rmsnorm_embedding_bwd(dy, tokens, token_bytes, dtable, count, vocab, width, table_stride, scale,
+                                        accumulate, dtype, grad_dtype, workspace, workspace_bytes, stream)
+
+
+def rmsnorm_embedding_bwd_workspace_bytes(count, vocab, width) -> int:
+    return _bytes_or_raise(load().rmsnorm_embedding_bwd_workspace_bytes(count, vocab, width),
+                           "rmsnorm_embedding_bwd_workspace_bytes")
+
+
+def rmsnorm_logprobs_fwd(logits, tokens, token_bytes, logprobs, stats, entropy, top_logprobs, top_ids, rows, vocab,
+                         row_stride, top, temperature, dtype, stream=0):
+    _check(rmsnorm_logprobs_fwd_status(logits, tokens, token_bytes, logprobs, stats, entropy, top_logprobs, top_ids,
+                                       rows, vocab, row_stride, top, temperature, dtype, stream),
+           "rmsnorm_logprobs_fwd")
+
+
+def rmsnorm_logprobs_fwd_status(logits, tokens, token_bytes, logprobs, stats, entropy, top_logprobs, top_ids, rows,
+                                vocab, row_stride, top, temperature, dtype, stream=0) -> int:
+    return load().rmsnorm_logprobs_fwd(logits, tokens, token_bytes, logprobs, stats, entropy, top_logprobs, top_ids,
+                                       rows, vocab, row_stride, top, temperature, dtype, stream)
+
+
+def rmsnorm_logprobs_bwd(logits, tokens, token_bytes, stats, dlogprobs, entropy, dentropy, dlogits, rows, vocab,
+                         row_stride, dlogits_stride, temperature, dtype, stream=0):
+    _check(rmsnorm_logprobs_bwd_status(logits, tokens, token_bytes, stats, dlogprobs, entropy, dentropy, dlogits,
+                                       rows, vocab, row_stride, dlogits_stride, temperature, dtype, stream),
+           "rmsnorm_logprobs_bwd")
+
+
+def rmsnorm_logprobs_bwd_status(logits, tokens, token_bytes, stats, dlogprobs, entropy, dentropy, dlogits, rows,
+                                vocab, row_stride, dlogits_stride, temperature, dtype, stream=0) -> int:
+    return load().rmsnorm_logprobs_bwd(logits, tokens, token_bytes, stats, dlogprobs, entropy, dentropy, dlogits,
+                                       rows, vocab, row_stride, dlogits_stride, temperature, dtype, stream)
+
+
+def rmsnorm_grad_norm(grads, n, norm, workspace, workspace_bytes, stream=0):
+    _check(rmsnorm_grad_norm_status(grads, n, norm, workspace, workspace_bytes, stream),
+           "rmsnorm_grad_norm")
+
+
+def rmsnorm_grad_norm_status(grads, n, norm, workspace, workspace_bytes, stream=0) -> int:
+    return load().rmsnorm_grad_norm(grads, n, norm, workspace, workspace_bytes, stream)
+
+
+def rmsnorm_clip_grads(grads, n, max_norm, norm, workspace, workspace_bytes, stream=0):
+    _check(rmsnorm_clip_grads_status(grads, n, max_norm, norm, workspace, workspace_bytes, stream),
+           "rmsnorm_clip_grads")
+
+
+def rmsnorm_clip_grads_status(grads, n, max_norm, norm, workspace, workspace_bytes, stream=0) -> int:
+    return load().rmsnorm_clip_grads(grads, n, max_norm, norm, workspace, workspace_bytes, stream)
+
+
+def rmsnorm_grad_norm_workspace_bytes() -> int:
+    return int(load().rmsnorm_grad_norm_workspace_bytes())
 
 
 def rmsnorm_fwd_mxfp8(x, residual, w, codes, scales, residual_out, rows, hidden, eps, weight_bias, dtype,

@@ -13,7 +13,7 @@ import importlib.util
 import os
 import struct
 import warnings
-from typing import Optional
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
@@ -197,7 +197,9 @@ def _empty(shape, dtype, device, stream):
 _fast = None
 _FAST_NAMES = ("rmsnorm_qk_rope_fwd", "rmsnorm_qk_rope_bwd", "rmsnorm_qk_rope_bwd_workspace_bytes",
                "rmsnorm_qkv_append", "rmsnorm_dropout_fwd", "rmsnorm_bwd", "rmsnorm_bwd_workspace_bytes",
-               "rmsnorm_dropout_bwd")
+               "rmsnorm_dropout_bwd", "rmsnorm_embedding_fwd", "rmsnorm_embedding_bwd",
+               "rmsnorm_embedding_bwd_workspace_bytes", "rmsnorm_logprobs_fwd", "rmsnorm_logprobs_bwd",
+               "rmsnorm_grad_norm", "rmsnorm_clip_grads", "rmsnorm_grad_norm_workspace_bytes")
 
 
 class _PythonCalls:
@@ -635,6 +637,237 @@ def rms_norm_dropout_backward(dy: torch.Tensor, h: torch.Tensor, p: float, rng: 
             None if dw is None else dw.data_ptr(), rows, hidden, float(eps), float(weight_bias), float(p), r,
             code, ws, need)
     return dresidual, dx, dw
+
+
+def _ids(t: torch.Tensor, name: str, shape, dev: int):
+    """(address, bytes of an id) of a contiguous tensor of token ids."""
+    kind = t.dtype
+    if t.get_device() != dev or (kind is not torch.int64 and kind is not torch.int32) or not t.is_contiguous() or (
+            shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be a contiguous int32 or int64 tensor on cuda:{dev}"
+                         + ("" if shape is None else f" of shape {tuple(shape)}"))
+    return t.data_ptr(), 8 if kind is torch.int64 else 4
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Elements between the rows of a 2-D tensor (the last dimension contiguous)."""
+    shape = t.shape
+    if len(shape) != 2 or shape[1] < 1:
+        raise ValueError(f"{name} must be a 2-D tensor with rows of at least one element, got {tuple(shape)}")
+    s0, s1 = t.stride()
+    if s1 != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return s0 if shape[0] > 1 else max(s0, shape[1])
+
+
+def embedding(tokens: torch.Tensor, table: torch.Tensor, scale: float = 1.0, out: Optional[torch.Tensor] = None,
+              stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Rows of ``table`` times ``scale`` for each token, rounded once.
+
+    ``tokens`` is an int32 or int64 tensor of any shape, ``table`` [vocab,
+    width] (last dimension contiguous, rows evenly strided); the result is
+    [*tokens.shape, width].  A token outside 0 .. vocab - 1 (-1 marks padding)
+    gives a row of zeros.
+    """
+    if stream is None and table.is_cuda:
+        y = (_fast or _bind_fast()).embedding(tokens, table, scale, out)
+        if _took(y, "rmsnorm_embedding_fwd"):
+            return y
+    t = table.dtype
+    code = dtype_code(t)
+    dev = _device_of(table, "table")
+    stride = _row_stride(table, "table")
+    at, size = _ids(tokens, "tokens", None, dev)
+    vocab, width = table.shape
+    shape = (*tokens.shape, width)
+    if out is None:
+        out = _empty(shape, t, table.device, stream)
+    elif out.get_device() != dev or out.dtype is not t or out.shape != shape or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous {shape} tensor of {t} on cuda:{dev}")
+    _launch(dev, stream, N.rmsnorm_embedding_fwd, at, size, table.data_ptr(), out.data_ptr(), tokens.numel(), vocab,
+            width, stride, float(scale), code)
+    return out
+
+
+def embedding_backward(dout: torch.Tensor, tokens: torch.Tensor, vocab: int, scale: float = 1.0,
+                       out: Optional[torch.Tensor] = None, accumulate: bool = False,
+                       workspace: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Gradient of ``embedding`` in its table: [vocab, width], a token's row the
+    sum of its places' ``dout`` times ``scale``, other rows zeros.
+
+    ``out`` (dout's type, or float32; the last dimension contiguous, rows
+    evenly strided) takes the gradient; with ``accumulate`` it is added to what
+    ``out`` holds, and only rows of tokens that occur are touched.  Sums are
+    fp32 in an order that follows from the tokens alone.  ``workspace`` is a
+    CUDA uint8 tensor of ``rmsnorm_embedding_bwd_workspace_bytes(tokens, vocab,
+    width)`` bytes (allocated when not given).
+    """
+    if stream is None and dout.is_cuda:
+        r = (_fast or _bind_fast()).embedding_backward(dout, tokens, vocab, scale, out, accumulate, workspace)
+        if _took(r, "rmsnorm_embedding_bwd"):
+            return r
+    vocab = int(vocab)
+    t = dout.dtype
+    code = dtype_code(t)
+    dev, count, width = _rows_of(dout, "dout")
+    at, size = _ids(tokens, "tokens", dout.shape[:-1], dev)
+    if vocab < 1:
+        raise ValueError("vocab must be at least 1")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate adds to out, which is not given")
+        out = _empty((vocab, width), t, dout.device, stream)
+    if out.get_device() != dev or out.shape != (vocab, width) or (out.dtype is not t and out.dtype is not torch.float32):
+        raise ValueError(f"out must be a {(vocab, width)} tensor of {t} or float32 on cuda:{dev}")
+    need = N.rmsnorm_embedding_bwd_workspace_bytes(count, vocab, width)
+    workspace = _workspace(workspace, need, dout.device, stream)
+    _launch(dev, stream, N.rmsnorm_embedding_bwd, dout.data_ptr(), at, size, out.data_ptr(), count, vocab, width,
+            _row_stride(out, "out"), float(scale), 1 if accumulate else 0, code, dtype_code(out.dtype),
+            workspace.data_ptr(), need)
+    return out
+
+
+class TokenLogprobs(NamedTuple):
+    """What ``token_logprobs`` returns; None for what was not asked for."""
+    logprobs: Optional[torch.Tensor]       # [rows] float32
+    stats: torch.Tensor                    # [rows, 2] float32: the largest logit, and the log of the sum relative to it
+    entropy: Optional[torch.Tensor]        # [rows] float32
+    top_logprobs: Optional[torch.Tensor]   # [rows, top] float32
+    top_ids: Optional[torch.Tensor]        # [rows, top] int32
+
+
+def _logits_args(logits, tokens, name):
+    code = dtype_code(logits.dtype)
+    dev = _device_of(logits, name)
+    stride = _row_stride(logits, name)
+    rows, vocab = logits.shape
+    at, size = (None, 4) if tokens is None else _ids(tokens, "tokens", (rows,), dev)
+    return code, dev, stride, rows, vocab, at, size
+
+
+def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor], temperature: float = 1.0, top: int = 0,
+                   entropy: bool = False, stream: Optional[torch.cuda.Stream] = None) -> TokenLogprobs:
+    """Log probabilities of the given tokens under softmax(logits / temperature),
+    and on request the entropy of each row and the ``top`` (up to 32) likeliest
+    tokens with theirs, in one pass over the logits.
+
+    ``logits`` is [rows, vocab] (last dimension contiguous, rows evenly
+    strided, so a view of padded rows too), ``tokens`` int32 or int64 [rows], or
+    None for no log probabilities; places whose token lies outside 0 .. vocab -
+    1 get 0.  -infinity masks a token; a row of nothing else has log
+    probabilities of -infinity and an entropy of 0.  Equal logits are ordered by
+    the lower id.  ``stats`` is what ``token_logprobs_backward`` starts from.
+    """
+    if stream is None and logits.is_cuda:
+        r = (_fast or _bind_fast()).token_logprobs(logits, tokens, temperature, top, entropy)
+        if _took(r, "rmsnorm_logprobs_fwd"):
+            return TokenLogprobs._make(r)
+    top = int(top)
+    code, dev, stride, rows, vocab, at, size = _logits_args(logits, tokens, "logits")
+    if not 0 <= top <= min(32, vocab):
+        raise ValueError(f"top must be 0 .. {min(32, vocab)}")
+    f32, there = torch.float32, logits.device
+    made = TokenLogprobs(None if tokens is None else _empty((rows,), f32, there, stream),
+                         _empty((rows, 2), f32, there, stream),
+                         _empty((rows,), f32, there, stream) if entropy else None,
+                         _empty((rows, top), f32, there, stream) if top else None,
+                         _empty((rows, top), torch.int32, there, stream) if top else None)
+    _launch(dev, stream, N.rmsnorm_logprobs_fwd, logits.data_ptr(), at, size, *(_ptr(t) for t in made), rows, vocab,
+            stride, top, float(temperature), code)
+    return made
+
+
+def token_logprobs_backward(logits: torch.Tensor, tokens: Optional[torch.Tensor], stats: torch.Tensor,
+                            dlogprobs: Optional[torch.Tensor], entropy: Optional[torch.Tensor] = None,
+                            dentropy: Optional[torch.Tensor] = None, temperature: float = 1.0,
+                            out: Optional[torch.Tensor] = None,
+                            stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Gradient of ``token_logprobs`` in the logits, of the log probabilities
+    (``dlogprobs``, float32 [rows], or None) and of the entropies (``dentropy``
+    with the forward's ``entropy``).  ``stats`` is the forward's.  Goes to
+    ``out`` (``out=logits`` works in place) or a new [rows, vocab] tensor."""
+    if stream is None and logits.is_cuda:
+        r = (_fast or _bind_fast()).token_logprobs_backward(logits, tokens, stats, dlogprobs, entropy, dentropy,
+                                                            temperature, out)
+        if _took(r, "rmsnorm_logprobs_bwd"):
+            return r
+    code, dev, stride, rows, vocab, at, size = _logits_args(logits, tokens, "logits")
+    f32 = torch.float32
+    if stats.get_device() != dev or stats.dtype is not f32 or stats.shape != (rows, 2) or not stats.is_contiguous():
+        raise ValueError(f"stats must be a contiguous [{rows}, 2] float32 tensor on cuda:{dev}")
+    if dlogprobs is not None and tokens is None:
+        raise ValueError("dlogprobs needs the tokens")
+    if dentropy is not None and entropy is None:
+        raise ValueError("dentropy needs the forward's entropy")
+    if out is None:
+        out = _empty((rows, vocab), logits.dtype, logits.device, stream)
+    if out.get_device() != dev or out.dtype is not logits.dtype or out.shape != logits.shape:
+        raise ValueError(f"out must be a {(rows, vocab)} tensor of {logits.dtype} on cuda:{dev}")
+    _launch(dev, stream, N.rmsnorm_logprobs_bwd, logits.data_ptr(), at, size, stats.data_ptr(),
+            _vector(dlogprobs, "dlogprobs", rows, f32, dev), _vector(entropy, "entropy", rows, f32, dev),
+            _vector(dentropy, "dentropy", rows, f32, dev), out.data_ptr(), rows, vocab, stride,
+            _row_stride(out, "out"), float(temperature), code)
+    return out
+
+
+def _grads_arg(grads, out):
+    """(device number, device, array of the tensors that are there)."""
+    pairs = [(g, g if out is None else out[i]) for i, g in enumerate(grads) if g is not None]
+    if not pairs:
+        raise ValueError("no gradients: every entry is None, or there are none")
+    dev = _device_of(pairs[0][0], "grads[0]")
+    array = (N.Grad * len(pairs))()
+    for a, (g, o) in zip(array, pairs):
+        if g.get_device() != dev or not g.is_contiguous():
+            raise ValueError(f"gradients must be contiguous tensors on cuda:{dev}")
+        if o is not g and (o is None or o.get_device() != dev or o.dtype is not g.dtype or o.shape != g.shape
+                           or not o.is_contiguous()):
+            raise ValueError("out must hold a contiguous tensor like each gradient")
+        a.grad, a.out, a.count, a.dtype = g.data_ptr(), o.data_ptr(), g.numel(), dtype_code(g.dtype)
+    return dev, pairs[0][0].device, array
+
+
+def grad_norm(grads: Sequence[Optional[torch.Tensor]], workspace: Optional[torch.Tensor] = None,
+              stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """The 2-norm of all the tensors together, float32 [1] on their device (see ``clip_grad_norm``)."""
+    return _norm_or_clip(grads, None, None, workspace, stream)
+
+
+def clip_grad_norm(grads: Sequence[Optional[torch.Tensor]], max_norm: float,
+                   out: Optional[Sequence[Optional[torch.Tensor]]] = None, workspace: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Scales the gradients by min(1, max_norm / norm), norm the 2-norm of all of
+    them together, and returns the norm: float32 [1] on their device, not
+    waited for.
+
+    ``grads`` is a list of contiguous bf16 and float32 tensors of one device
+    (None entries are passed over), changed in place, or written to ``out``, a
+    tensor like each.  An infinite norm makes the factor 0, NaN everything NaN:
+    a caller that skips such steps looks at the norm.  ``workspace`` is a CUDA
+    uint8 tensor of ``rmsnorm_grad_norm_workspace_bytes()`` bytes (allocated
+    when not given).
+    """
+    return _norm_or_clip(grads, max_norm, out, workspace, stream)
+
+
+def _norm_or_clip(grads, max_norm, out, workspace, stream):
+    if out is not None and len(out) != len(grads):
+        raise ValueError(f"out holds {len(out)} tensors, grads {len(grads)}")
+    if stream is None:
+        r = (_fast or _bind_fast()).clip_grad_norm(grads, max_norm, out, workspace)
+        if _took(r, "rmsnorm_grad_norm" if max_norm is None else "rmsnorm_clip_grads"):
+            return r
+    dev, device, array = _grads_arg(grads, out)
+    norm = _empty((1,), torch.float32, device, stream)
+    need = N.rmsnorm_grad_norm_workspace_bytes()
+    workspace = _workspace(workspace, need, device, stream)
+    if max_norm is None:
+        _launch(dev, stream, N.rmsnorm_grad_norm, array, len(array), norm.data_ptr(), workspace.data_ptr(), need)
+    else:
+        _launch(dev, stream, N.rmsnorm_clip_grads, array, len(array), float(max_norm), norm.data_ptr(),
+                workspace.data_ptr(), need)
+    return norm
 
 
 def qk_plan_for(qkv: torch.Tensor, q_heads: int, k_heads: int, head_dim: int, q_w=None, k_w=None,

@@ -1,5 +1,5 @@
-// fastcall.cpp -- the Python calls of the rotary, append and dropout operators
-// without Python's own cost: a CPython module that takes torch tensors, makes
+// fastcall.cpp -- the Python calls of the rotary, append, dropout, embedding,
+// log probability and clipping operators without Python's own cost: a CPython module that takes torch tensors, makes
 // the checks of api.py on them, and calls the C ABI on the current stream.
 //
 // These kernels take two microseconds for a decode step while the checks, the
@@ -28,6 +28,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstring>
+#include <vector>
 
 #include "rmsnorm.h"
 
@@ -41,6 +42,14 @@ decltype(&rmsnorm_dropout_fwd) dropout_fwd;
 decltype(&rmsnorm_bwd) norm_bwd;
 decltype(&rmsnorm_bwd_workspace_bytes) bwd_workspace_bytes;
 decltype(&rmsnorm_dropout_bwd) dropout_bwd;
+decltype(&rmsnorm_embedding_fwd) embedding_fwd;
+decltype(&rmsnorm_embedding_bwd) embedding_bwd;
+decltype(&rmsnorm_embedding_bwd_workspace_bytes) embedding_bwd_workspace_bytes;
+decltype(&rmsnorm_logprobs_fwd) logprobs_fwd;
+decltype(&rmsnorm_logprobs_bwd) logprobs_bwd;
+decltype(&rmsnorm_grad_norm) norm_of_grads;
+decltype(&rmsnorm_clip_grads) clip_grads;
+decltype(&rmsnorm_grad_norm_workspace_bytes) grad_norm_workspace_bytes;
 
 // Thrown (and caught in this file) to leave a call to api.py.
 struct Elsewhere {};
@@ -162,9 +171,10 @@ void rope_arg(rmsnorm_rope_t *r, PyObject *positions, PyObject *inv_freq, PyObje
 // of the current stream: through the dispatcher an allocation takes 1.5 us on
 // the host, nearly a launch (the norm's gradient with a weight 7.7 -> 6.0 us of
 // host time a call, with the workspace's memory alone in place of a tensor).
-at::Tensor fresh(at::IntArrayRef size, const at::Tensor &x) {
-    return at::Tensor(at::detail::empty_cuda(size, x.scalar_type(), x.device(), std::nullopt));
+at::Tensor fresh_of(at::IntArrayRef size, at::ScalarType type, const at::Tensor &x) {
+    return at::Tensor(at::detail::empty_cuda(size, type, x.device(), std::nullopt));
 }
+at::Tensor fresh(at::IntArrayRef size, const at::Tensor &x) { return fresh_of(size, x.scalar_type(), x); }
 
 // A workspace given, or made without the lock (memory of the current stream,
 // handed back when the call is over and used again only behind it).
@@ -514,32 +524,253 @@ PyObject *rms_norm_dropout_backward(PyObject *, PyObject *const *a, Py_ssize_t n
     });
 }
 
+// Contiguous token ids, of the shape given or of any.
+struct Ids {
+    void *at = nullptr;
+    int bytes = 4;
+    Ids(PyObject *o, const int64_t *rows, const Where &w) {
+        const at::Tensor &t = tensor(o);
+        need(t.get_device() == w.dev && (t.scalar_type() == at::kLong || t.scalar_type() == at::kInt) && t.is_contiguous());
+        if (rows != nullptr) need(t.dim() == 1 && t.size(0) == *rows);
+        at = t.data_ptr();
+        bytes = t.scalar_type() == at::kLong ? 8 : 4;
+    }
+    Ids() = default;
+};
+
+// Row stride of a 2-D tensor.
+int64_t row_stride(const at::Tensor &t) {
+    need(t.dim() == 2 && t.size(1) >= 1 && (t.stride(1) == 1 || t.size(1) == 1));
+    return t.size(0) > 1 || t.stride(0) > t.size(1) ? t.stride(0) : t.size(1);
+}
+
+// (tokens, table, scale, out)
+PyObject *embedding(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        need(n == 4 && embedding_fwd != nullptr);
+        const at::Tensor table = tensor(a[1]), tokens = tensor(a[0]);
+        const int code = code_of(table);
+        const Where w(table);
+        const int64_t stride = row_stride(table), vocab = table.size(0), width = table.size(1), count = tokens.numel();
+        const Ids ids(a[0], nullptr, w);
+        const float scale = real(a[2]);
+        c10::SmallVector<int64_t, 6> shape(tokens.sizes().begin(), tokens.sizes().end());
+        shape.push_back(width);
+        Output y(a[3]);
+        if (y.given()) {
+            const at::Tensor &o = tensor(a[3]);
+            w.same(o, table.scalar_type());
+            need(o.sizes() == at::IntArrayRef(shape) && o.is_contiguous());
+            y.at = o.data_ptr();
+        }
+        int st;
+        {
+            const Unlocked span;
+            y.make(shape, table);
+            st = embedding_fwd(ids.at, ids.bytes, table.data_ptr(), y.at, count, vocab, width, stride, scale, code,
+                               w.stream());
+        }
+        return st == RMSNORM_OK ? y.result() : status_of(st);
+    });
+}
+
+// (dout, tokens, vocab, scale, out, accumulate, workspace)
+PyObject *embedding_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        need(n == 7 && embedding_bwd != nullptr);
+        const at::Tensor dy = tensor(a[0]), tokens = tensor(a[1]);
+        const int code = code_of(dy);
+        const Where w(dy);
+        const Rows r(dy);
+        const Ids ids(a[1], nullptr, w);
+        need(tokens.sizes() == dy.sizes().slice(0, dy.dim() - 1));
+        const int64_t vocab = whole(a[2]);
+        need(vocab >= 1);
+        const float scale = real(a[3]);
+        const bool add = truth(a[5]);
+        Output d(a[4]);
+        int64_t stride = r.hidden;
+        int held = code;
+        if (d.given()) {
+            const at::Tensor &o = tensor(a[4]);
+            held = code_of(o);
+            need(o.get_device() == w.dev && (held == code || held == RMSNORM_F32) && o.dim() == 2 && o.size(0) == vocab &&
+                 o.size(1) == r.hidden);
+            stride = row_stride(o);
+            d.at = o.data_ptr();
+        } else {
+            need(!add);
+        }
+        Workspace ws;
+        const int64_t bytes = embedding_bwd_workspace_bytes(r.rows, vocab, r.hidden);
+        need(bytes > 0);
+        ws.given(a[6], bytes, w);
+        int st;
+        {
+            const Unlocked span;
+            d.make({vocab, r.hidden}, dy);
+            ws.make();
+            st = embedding_bwd(dy.data_ptr(), ids.at, ids.bytes, d.at, r.rows, vocab, r.hidden, stride, scale, add, code,
+                               held, ws.at, (uint64_t)ws.bytes, w.stream());
+        }
+        return st == RMSNORM_OK ? d.result() : status_of(st);
+    });
+}
+
+float *floats(const at::Tensor &t) { return t.defined() ? static_cast<float *>(t.data_ptr()) : nullptr; }
+
+// (logits, tokens, temperature, top, entropy)
+PyObject *token_logprobs(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        need(n == 5 && logprobs_fwd != nullptr);
+        const at::Tensor x = tensor(a[0]);
+        const int code = code_of(x);
+        const Where w(x);
+        const int64_t stride = row_stride(x), rows = x.size(0), vocab = x.size(1);
+        const bool given = a[1] != Py_None;
+        const Ids ids = given ? Ids(a[1], &rows, w) : Ids();
+        const float temperature = real(a[2]);
+        const int32_t top = count(a[3]);
+        need(top <= 32 && top <= vocab);
+        const bool entropy = truth(a[4]);
+        at::Tensor lp, stats, ent, top_lp, top_ids;
+        int st;
+        {
+            const Unlocked span;
+            if (given) lp = fresh_of({rows}, at::kFloat, x);
+            stats = fresh_of({rows, 2}, at::kFloat, x);
+            if (entropy) ent = fresh_of({rows}, at::kFloat, x);
+            if (top > 0) {
+                top_lp = fresh_of({rows, top}, at::kFloat, x);
+                top_ids = fresh_of({rows, top}, at::kInt, x);
+            }
+            st = logprobs_fwd(x.data_ptr(), ids.at, ids.bytes, floats(lp), floats(stats), floats(ent), floats(top_lp),
+                              top > 0 ? static_cast<int32_t *>(top_ids.data_ptr()) : nullptr, rows, vocab, stride, top,
+                              temperature, code, w.stream());
+        }
+        if (st != RMSNORM_OK) return status_of(st);
+        return Py_BuildValue("(NNNNN)", wrap_or_none(lp), wrap_or_none(stats), wrap_or_none(ent), wrap_or_none(top_lp),
+                             wrap_or_none(top_ids));
+    });
+}
+
+// (logits, tokens, stats, dlogprobs, entropy, dentropy, temperature, out)
+PyObject *token_logprobs_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        need(n == 8 && logprobs_bwd != nullptr);
+        const at::Tensor x = tensor(a[0]);
+        const int code = code_of(x);
+        const Where w(x);
+        const int64_t stride = row_stride(x), rows = x.size(0), vocab = x.size(1);
+        const Ids ids = a[1] != Py_None ? Ids(a[1], &rows, w) : Ids();
+        const at::Tensor &stats = tensor(a[2]);
+        w.same(stats, at::kFloat);
+        need(stats.dim() == 2 && stats.size(0) == rows && stats.size(1) == 2 && stats.is_contiguous());
+        const float *of = static_cast<const float *>(stats.data_ptr());
+        const float *dlp = static_cast<const float *>(vector(a[3], rows, at::kFloat, w));
+        const float *ent = static_cast<const float *>(vector(a[4], rows, at::kFloat, w));
+        const float *dent = static_cast<const float *>(vector(a[5], rows, at::kFloat, w));
+        need((dlp == nullptr || ids.at != nullptr) && (dent == nullptr || ent != nullptr));
+        const float temperature = real(a[6]);
+        Output d(a[7]);
+        int64_t dstride = vocab;
+        if (d.given()) {
+            const at::Tensor &o = tensor(a[7]);
+            w.same(o, x.scalar_type());
+            need(o.sizes() == x.sizes());
+            dstride = row_stride(o);
+            d.at = o.data_ptr();
+        }
+        int st;
+        {
+            const Unlocked span;
+            d.make({rows, vocab}, x);
+            st = logprobs_bwd(x.data_ptr(), ids.at, ids.bytes, of, dlp, ent, dent, d.at, rows, vocab, stride, dstride,
+                              temperature, code, w.stream());
+        }
+        return st == RMSNORM_OK ? d.result() : status_of(st);
+    });
+}
+
+// (grads, max_norm or None for the norm alone, out, workspace)
+PyObject *clip_grad_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        need(n == 4 && clip_grads != nullptr);
+        need(PyList_CheckExact(a[0]) || PyTuple_CheckExact(a[0]));
+        need(a[2] == Py_None || PyList_CheckExact(a[2]) || PyTuple_CheckExact(a[2]));
+        const Py_ssize_t many = PySequence_Fast_GET_SIZE(a[0]);
+        need(a[2] == Py_None || PySequence_Fast_GET_SIZE(a[2]) == many);
+        std::vector<rmsnorm_grad_t> grads;
+        std::vector<at::Tensor> held;   // the lists may change while the lock is not held
+        grads.reserve(many);
+        held.reserve(2 * many);
+        for (Py_ssize_t i = 0; i < many; ++i) {
+            PyObject *of = PySequence_Fast_GET_ITEM(a[0], i);
+            if (of == Py_None) continue;
+            const at::Tensor &g = tensor(of);
+            need(g.is_contiguous() && (held.empty() || g.get_device() == held[0].get_device()));
+            rmsnorm_grad_t e;
+            std::memset(&e, 0, sizeof(e));
+            e.grad = g.data_ptr();
+            e.out = g.data_ptr();
+            e.count = g.numel();
+            e.dtype = code_of(g);
+            held.push_back(g);
+            if (a[2] != Py_None) {
+                const at::Tensor &o = tensor(PySequence_Fast_GET_ITEM(a[2], i));
+                need(o.get_device() == g.get_device() && o.scalar_type() == g.scalar_type() && o.sizes() == g.sizes() &&
+                     o.is_contiguous());
+                e.out = o.data_ptr();
+                held.push_back(o);
+            }
+            grads.push_back(e);
+        }
+        need(!held.empty());
+        const Where w(held[0]);
+        const bool clip = a[1] != Py_None;
+        const float most = clip ? real(a[1]) : 0.f;
+        Workspace ws;
+        ws.given(a[3], grad_norm_workspace_bytes(), w);
+        at::Tensor norm;
+        int st;
+        {
+            const Unlocked span;
+            norm = fresh_of({1}, at::kFloat, held[0]);
+            ws.make();
+            st = clip ? clip_grads(grads.data(), (int64_t)grads.size(), most, floats(norm), ws.at, (uint64_t)ws.bytes,
+                                   w.stream())
+                      : norm_of_grads(grads.data(), (int64_t)grads.size(), floats(norm), ws.at, (uint64_t)ws.bytes,
+                                      w.stream());
+        }
+        return st == RMSNORM_OK ? THPVariable_Wrap(norm) : status_of(st);
+    });
+}
+
 // Addresses of the C ABI's functions, in the order below.
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    void *at[8];
-    if (n != 8) {
-        PyErr_SetString(PyExc_TypeError, "bind takes 8 addresses");
+    void *const to[] = {&qk_rope_fwd, &qk_rope_bwd, &qk_rope_bwd_workspace_bytes, &qkv_append_fn, &dropout_fwd, &norm_bwd,
+                        &bwd_workspace_bytes, &dropout_bwd, &embedding_fwd, &embedding_bwd,
+                        &embedding_bwd_workspace_bytes, &logprobs_fwd, &logprobs_bwd, &norm_of_grads, &clip_grads,
+                        &grad_norm_workspace_bytes};
+    constexpr int kMany = sizeof(to) / sizeof(to[0]);
+    void *at[kMany];
+    if (n != kMany) {
+        PyErr_Format(PyExc_TypeError, "bind takes %d addresses", kMany);
         return nullptr;
     }
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kMany; ++i) {
         at[i] = PyLong_AsVoidPtr(a[i]);
         if (PyErr_Occurred()) return nullptr;
     }
-    std::memcpy(&qk_rope_fwd, &at[0], sizeof(void *));
-    std::memcpy(&qk_rope_bwd, &at[1], sizeof(void *));
-    std::memcpy(&qk_rope_bwd_workspace_bytes, &at[2], sizeof(void *));
-    std::memcpy(&qkv_append_fn, &at[3], sizeof(void *));
-    std::memcpy(&dropout_fwd, &at[4], sizeof(void *));
-    std::memcpy(&norm_bwd, &at[5], sizeof(void *));
-    std::memcpy(&bwd_workspace_bytes, &at[6], sizeof(void *));
-    std::memcpy(&dropout_bwd, &at[7], sizeof(void *));
+    for (int i = 0; i < kMany; ++i) std::memcpy(to[i], &at[i], sizeof(void *));
     Py_RETURN_NONE;
 }
 
 #define ENTRY(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(&f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(bind), ENTRY(qk_norm_rope), ENTRY(qk_norm_rope_backward), ENTRY(qkv_append),
                          ENTRY(rms_norm_dropout), ENTRY(rms_norm_backward), ENTRY(rms_norm_dropout_backward),
-                         {nullptr, nullptr, 0, nullptr}};
+                         ENTRY(embedding), ENTRY(embedding_backward), ENTRY(token_logprobs),
+                         ENTRY(token_logprobs_backward), ENTRY(clip_grad_norm), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

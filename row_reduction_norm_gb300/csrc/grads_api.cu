@@ -1,0 +1,125 @@
+// grads_api.cu -- entry points of the norm of many tensors together and their
+// clipping (declared in include/rmsnorm.h): argument checks, the launches.
+#include <climits>
+#include <cmath>
+#include <cstring>
+
+#include "grads_kernels.cuh"
+#include "launch_util.h"
+
+namespace {
+
+using rrn::GradEntry;
+using rrn::GradTable;
+
+uint32_t blocks_of(const rmsnorm_grad_t &g) {
+    const int64_t s = rrn::size_of(g.dtype);
+    return (uint32_t)rrn::div_up((int64_t)(reinterpret_cast<uintptr_t>(g.grad) & 15) + g.count * s, rrn::kGradBlock);
+}
+
+int check_grads(const rmsnorm_grad_t *grads, int64_t n, bool clip, const float *norm, const void *workspace,
+                uint64_t workspace_bytes) {
+    if (n < 0 || (n > 0 && grads == nullptr) || norm == nullptr || !rrn::on_boundary(norm, 4)) return RMSNORM_EINVAL;
+    if (workspace == nullptr || !rrn::on_boundary(workspace, 16) ||
+        workspace_bytes < (uint64_t)rmsnorm_grad_norm_workspace_bytes())
+        return RMSNORM_EINVAL;
+    for (int64_t i = 0; i < n; ++i) {
+        const rmsnorm_grad_t &g = grads[i];
+        if ((g.dtype != RMSNORM_F32 && g.dtype != RMSNORM_BF16) || g.reserved != 0) return RMSNORM_EINVAL;
+        if (g.count < 0 || g.count > INT64_MAX / 8) return RMSNORM_EINVAL;
+        if (g.count == 0) continue;
+        const int64_t s = rrn::size_of(g.dtype);
+        if (g.grad == nullptr || !rrn::on_boundary(g.grad, s)) return RMSNORM_EINVAL;
+        if (clip && (g.out == nullptr || !rrn::on_boundary(g.out, s))) return RMSNORM_EINVAL;
+        if (g.count > (int64_t)1 << 44) return RMSNORM_EUNSUPPORTED;
+    }
+    return RMSNORM_OK;
+}
+
+// One launch's entries, from tensor i on; returns the next one's.
+template <int CAP>
+int64_t fill(GradTable<CAP> *t, const rmsnorm_grad_t *grads, int64_t i, int64_t n) {
+    t->n = 0;
+    t->blocks = 0;
+    for (; i < n && t->n < CAP; ++i) {
+        const rmsnorm_grad_t &g = grads[i];
+        if (g.count == 0) continue;
+        const uint32_t blocks = blocks_of(g);
+        if (t->n > 0 && blocks > (uint32_t)INT_MAX - t->blocks) break;
+        t->e[t->n++] = GradEntry{static_cast<const char *>(g.grad), static_cast<char *>(g.out), g.count, t->blocks,
+                                 g.dtype};
+        t->blocks += blocks;
+    }
+    return i;
+}
+
+template <int CAP>
+int run(const rmsnorm_grad_t *grads, int64_t n, bool clip, float max_norm, float *norm, void *workspace,
+        rmsnorm_stream_t stream) {
+    int dev = 0, sms = 0, resident = 0;
+    int st = rrn::current_device_sms(&dev, &sms);
+    if (st != RMSNORM_OK) return st;
+    const void *squares = reinterpret_cast<const void *>(&rrn::grad_squares_kernel<CAP>);
+    const void *scale = reinterpret_cast<const void *>(&rrn::grad_scale_kernel<CAP>);
+    const void *only = reinterpret_cast<const void *>(&rrn::grad_norm_kernel<CAP>);
+    GradTable<CAP> t;
+    std::memset(&t, 0, offsetof(GradTable<CAP>, e));
+    t.partial = static_cast<double *>(workspace);
+    t.norm = norm;
+    t.max_norm = max_norm;
+    void *argv[] = {&t};
+    if ((st = rrn::resident_blocks(dev, squares, rrn::kGradThreads, 0, &resident)) != RMSNORM_OK) return st;
+    // launches of the norm share the partial sums out
+    int64_t launches = 0;
+    for (int64_t i = 0; i < n || launches == 0; ++launches) i = fill(&t, grads, i, n);
+    if (launches > rrn::kGradPartials) return RMSNORM_EUNSUPPORTED;
+    int64_t most = rrn::kGradPartials / launches;
+    if (most > (int64_t)sms * resident) most = (int64_t)sms * resident;
+    t.slot = 0;
+    for (int64_t i = 0, l = 0; l < launches; ++l) {
+        i = fill(&t, grads, i, n);
+        if (t.blocks == 0) continue;
+        const unsigned grid = (unsigned)(t.blocks < most ? t.blocks : most);
+        if ((st = rrn::launch_kernel(squares, dim3(grid), rrn::kGradThreads, 0, stream, argv)) != RMSNORM_OK) return st;
+        t.slot += (int32_t)grid;
+    }
+    t.sums = t.slot;
+    if (!clip || t.sums == 0) return rrn::launch_kernel(only, dim3(1), rrn::kGradThreads, 0, stream, argv);
+    if ((st = rrn::resident_blocks(dev, scale, rrn::kGradThreads, 0, &resident)) != RMSNORM_OK) return st;
+    most = (int64_t)sms * resident;
+    t.write_norm = 1;
+    for (int64_t i = 0, l = 0; l < launches; ++l) {
+        i = fill(&t, grads, i, n);
+        if (t.blocks == 0) continue;
+        const unsigned grid = (unsigned)(t.blocks < most ? t.blocks : most);
+        if ((st = rrn::launch_kernel(scale, dim3(grid), rrn::kGradThreads, 0, stream, argv)) != RMSNORM_OK) return st;
+    }
+    return RMSNORM_OK;
+}
+
+int norm_and_clip(const rmsnorm_grad_t *grads, int64_t n, bool clip, float max_norm, float *norm, void *workspace,
+                  uint64_t workspace_bytes, rmsnorm_stream_t stream) {
+    const int st = check_grads(grads, n, clip, norm, workspace, workspace_bytes);
+    if (st != RMSNORM_OK) return st;
+    return n <= rrn::kGradSmall ? run<rrn::kGradSmall>(grads, n, clip, max_norm, norm, workspace, stream)
+                                : run<rrn::kGradMost>(grads, n, clip, max_norm, norm, workspace, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t rmsnorm_grad_norm_workspace_bytes(void) { return rrn::kGradPartials * (int64_t)sizeof(double); }
+
+int rmsnorm_grad_norm(const rmsnorm_grad_t *grads, int64_t n, float *norm, void *workspace, uint64_t workspace_bytes,
+                      rmsnorm_stream_t stream) {
+    return norm_and_clip(grads, n, false, 0.f, norm, workspace, workspace_bytes, stream);
+}
+
+int rmsnorm_clip_grads(const rmsnorm_grad_t *grads, int64_t n, float max_norm, float *norm, void *workspace,
+                       uint64_t workspace_bytes, rmsnorm_stream_t stream) {
+    if (!(max_norm >= 0.f)) return RMSNORM_EINVAL;   // infinity: nothing is clipped
+    return norm_and_clip(grads, n, true, max_norm, norm, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

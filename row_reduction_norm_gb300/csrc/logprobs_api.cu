@@ -1,0 +1,131 @@
+// logprobs_api.cu -- entry points of the tokens' log probabilities and their
+// gradient (declared in include/rmsnorm.h): argument checks, the choice of a
+// kernel and its grid, the launch.
+#include <climits>
+#include <cmath>
+#include <cstring>
+
+#include "launch_util.h"
+#include "logprobs_kernels.cuh"
+
+namespace {
+
+constexpr int64_t kMaxVocab = 1 << 20;
+
+int check_logits(const void *logits, const void *tokens, int token_bytes, int64_t rows, int64_t vocab, int64_t stride,
+                 float temperature, int dtype) {
+    if (dtype != RMSNORM_F32 && dtype != RMSNORM_BF16) return RMSNORM_EINVAL;
+    if ((token_bytes != 4 && token_bytes != 8) || rows < 0 || vocab <= 0 || (rows > 1 && stride < vocab))
+        return RMSNORM_EINVAL;
+    if (!(temperature > 0.f) || !std::isnormal(temperature) || !std::isnormal((float)(1.0 / (double)temperature)))
+        return RMSNORM_EINVAL;
+    if (vocab > kMaxVocab) return RMSNORM_EUNSUPPORTED;
+    if (rows > 1 && stride > INT64_MAX / 8 / rows) return RMSNORM_EINVAL;
+    if (rows > 0 && logits == nullptr) return RMSNORM_EINVAL;
+    if (!rrn::on_boundary(logits, rrn::size_of(dtype)) || !rrn::on_boundary(tokens, token_bytes)) return RMSNORM_EINVAL;
+    return RMSNORM_OK;
+}
+
+const void *forward_kernel(int dtype, bool entropy, bool top) {
+#define FWD(T) \
+    (entropy ? top ? reinterpret_cast<const void *>(&rrn::logprobs_fwd_kernel<rrn::T, true, true>) \
+                   : reinterpret_cast<const void *>(&rrn::logprobs_fwd_kernel<rrn::T, true, false>) \
+             : top ? reinterpret_cast<const void *>(&rrn::logprobs_fwd_kernel<rrn::T, false, true>) \
+                   : reinterpret_cast<const void *>(&rrn::logprobs_fwd_kernel<rrn::T, false, false>))
+    return dtype == RMSNORM_BF16 ? FWD(BF16) : FWD(F32);
+#undef FWD
+}
+
+const void *backward_kernel(int dtype, bool entropy) {
+    if (dtype == RMSNORM_BF16)
+        return entropy ? reinterpret_cast<const void *>(&rrn::logprobs_bwd_kernel<rrn::BF16, true>)
+                       : reinterpret_cast<const void *>(&rrn::logprobs_bwd_kernel<rrn::BF16, false>);
+    return entropy ? reinterpret_cast<const void *>(&rrn::logprobs_bwd_kernel<rrn::F32, true>)
+                   : reinterpret_cast<const void *>(&rrn::logprobs_bwd_kernel<rrn::F32, false>);
+}
+
+}  // namespace
+
+extern "C" {
+
+int rmsnorm_logprobs_fwd(const void *logits, const void *tokens, int token_bytes, float *logprobs, float *stats,
+                         float *entropy, float *top_logprobs, int32_t *top_ids, int64_t rows, int64_t vocab,
+                         int64_t row_stride, int32_t top, float temperature, int dtype, rmsnorm_stream_t stream) {
+    int st = check_logits(logits, tokens, token_bytes, rows, vocab, row_stride, temperature, dtype);
+    if (st != RMSNORM_OK) return st;
+    if (top < 0 || top > rrn::kLpTop || top > vocab) return RMSNORM_EINVAL;
+    if (rows == 0) return RMSNORM_OK;
+    if ((logprobs != nullptr && tokens == nullptr) || (top > 0 && (top_logprobs == nullptr || top_ids == nullptr)))
+        return RMSNORM_EINVAL;
+    const void *fp[] = {logprobs, entropy, top_logprobs, top_ids};
+    for (const void *q : fp)
+        if (!rrn::on_boundary(q, 4)) return RMSNORM_EINVAL;
+    if (!rrn::on_boundary(stats, 8)) return RMSNORM_EINVAL;
+    const int64_t s = rrn::size_of(dtype);
+    rrn::LogprobParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.logits = static_cast<const char *>(logits);
+    p.tokens = tokens;
+    p.logprobs = logprobs;
+    p.stats = stats;
+    p.entropy = entropy;
+    p.top_logprobs = top_logprobs;
+    p.top_ids = top_ids;
+    p.stride = row_stride * s;
+    p.vocab = (int32_t)vocab;
+    p.units = (int32_t)rrn::div_up(vocab, dtype == RMSNORM_BF16 ? rrn::lp_unit<rrn::BF16>() : rrn::lp_unit<rrn::F32>());
+    p.top = top;
+    p.wide = token_bytes == 8;
+    p.aligned = rrn::on_boundary(logits, 16) && (rows == 1 || p.stride % 16 == 0);
+    p.inv_t = (float)(1.0 / (double)temperature);
+    p.c = (float)(1.4426950408889634 / (double)temperature);
+    int dev = 0, sms = 0;
+    if ((st = rrn::current_device_sms(&dev, &sms)) != RMSNORM_OK) return st;
+    // a row over as many blocks as give every SM one, while each of their warps has a unit
+    int cluster = 1;
+    while (cluster < 8 && rows * cluster < sms && 2 * cluster * rrn::kLpWarps <= p.units + rrn::kLpWarps - 1) cluster *= 2;
+    if (rows > INT_MAX / cluster) return RMSNORM_EUNSUPPORTED;
+    void *argv[] = {&p};
+    return rrn::launch_kernel(forward_kernel(dtype, entropy != nullptr, top > 0), dim3((unsigned)(rows * cluster)),
+                              rrn::kLpThreads, (size_t)p.units * 12, stream, argv, cluster);
+}
+
+int rmsnorm_logprobs_bwd(const void *logits, const void *tokens, int token_bytes, const float *stats,
+                         const float *dlogprobs, const float *entropy, const float *dentropy, void *dlogits,
+                         int64_t rows, int64_t vocab, int64_t row_stride, int64_t dlogits_stride, float temperature,
+                         int dtype, rmsnorm_stream_t stream) {
+    const int st = check_logits(logits, tokens, token_bytes, rows, vocab, row_stride, temperature, dtype);
+    if (st != RMSNORM_OK) return st;
+    if (rows > 1 && (dlogits_stride < vocab || dlogits_stride > INT64_MAX / 8 / rows)) return RMSNORM_EINVAL;
+    if (rows == 0) return RMSNORM_OK;
+    const int64_t s = rrn::size_of(dtype);
+    if (dlogits == nullptr || !rrn::on_boundary(dlogits, s) || stats == nullptr || !rrn::on_boundary(stats, 8))
+        return RMSNORM_EINVAL;
+    if ((dlogprobs != nullptr && tokens == nullptr) || (dentropy != nullptr && entropy == nullptr)) return RMSNORM_EINVAL;
+    const void *fp[] = {dlogprobs, entropy, dentropy};
+    for (const void *q : fp)
+        if (!rrn::on_boundary(q, 4)) return RMSNORM_EINVAL;
+    rrn::LogprobBwdParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.logits = static_cast<const char *>(logits);
+    p.tokens = tokens;
+    p.stats = stats;
+    p.dlogprobs = dlogprobs;
+    p.entropy = entropy;
+    p.dentropy = dentropy;
+    p.dlogits = static_cast<char *>(dlogits);
+    p.stride = row_stride * s;
+    p.dstride = dlogits_stride * s;
+    p.vocab = (int32_t)vocab;
+    p.slices = (int32_t)rrn::div_up(vocab * s, 16 * rrn::kLpThreads * rrn::kLpBwdChunks);
+    p.wide = token_bytes == 8;
+    p.aligned = rrn::on_boundary(logits, 16) && rrn::on_boundary(dlogits, 16) &&
+                (rows == 1 || (p.stride % 16 == 0 && p.dstride % 16 == 0));
+    p.inv_t = (float)(1.0 / (double)temperature);
+    if (rows > INT_MAX / p.slices) return RMSNORM_EUNSUPPORTED;
+    void *argv[] = {&p};
+    return rrn::launch_kernel(backward_kernel(dtype, dentropy != nullptr), dim3((unsigned)(rows * p.slices)),
+                              rrn::kLpThreads, 0, stream, argv);
+}
+
+}  // extern "C"
