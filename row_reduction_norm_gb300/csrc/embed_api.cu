@@ -1,6 +1,7 @@
 // embed_api.cu -- entry points of the embedding lookup and its gradient
 // (declared in include/rmsnorm.h): argument checks, the choice of a kernel and
 // its grid, the launches.
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstring>
@@ -40,8 +41,11 @@ const void *forward_kernel(int dtype, int64_t bytes, bool one) {
 #undef FWD
 }
 
-const void *sum_kernel(int dtype, int grad_dtype, int64_t p) {
-#define SUM(T, TG, P) reinterpret_cast<const void *>(&rrn::embed_sum_kernel<rrn::T, rrn::TG, P>)
+// The kernel of the sums over sorted tokens, or over few tokens without a sort.
+const void *sum_kernel(int dtype, int grad_dtype, int64_t p, bool direct) {
+#define SUM(T, TG, P) \
+    (direct ? reinterpret_cast<const void *>(&rrn::embed_direct_kernel<rrn::T, rrn::TG, P>) \
+            : reinterpret_cast<const void *>(&rrn::embed_sum_kernel<rrn::T, rrn::TG, P>))
     if (dtype == RMSNORM_F32) return p == 4 ? SUM(F32, F32, 4) : p == 2 ? SUM(F32, F32, 2) : SUM(F32, F32, 1);
     if (grad_dtype == RMSNORM_F32)
         return p == 8 ? SUM(BF16, F32, 8) : p == 4 ? SUM(BF16, F32, 4) : p == 2 ? SUM(BF16, F32, 2) : SUM(BF16, F32, 1);
@@ -56,26 +60,64 @@ const void *join_kernel(int grad_dtype, int64_t p) {
 #undef JOIN
 }
 
+// Sorted tokens of a warp: 32, or fewer where that leaves less than 8192 warps
+// (a wave of 54 an SM).
+int run_of(int64_t count, int64_t tiles) {
+    int run = 32;
+    while (run > 4 && rrn::div_up(count, run) * tiles < 8192) run /= 2;
+    return run;
+}
+
 // What the gradient's workspace holds, in bytes from its start.
 struct Layout {
-    int64_t a, b, present, partial, bytes, words, segments, tiles;
+    int64_t a, b, present, partial, bytes, words, chunks, tiles;
+    int run;
     Layout(int64_t count, int64_t vocab, int64_t width) {
         words = rrn::div_up(vocab, 32);
-        segments = rrn::div_up(count, rrn::kSegment);
         tiles = rrn::div_up(width, rrn::kTile);
+        run = run_of(count, tiles);
+        chunks = rrn::div_up(count, (int64_t)rrn::kSumWarps * run);
         a = 0;
         b = a + rrn::div_up(count * 8, 16) * 16;
         present = b + rrn::div_up(count * 8, 16) * 16;
         partial = present + rrn::div_up(words * 4, 16) * 16;
-        bytes = partial + 2 * segments * tiles * rrn::kTile * 4;
+        bytes = partial + 2 * chunks * tiles * rrn::kTile * 4;
     }
 };
 
-// Blocks of the sorting cluster: one while its threads have at most two tokens each.
+// Whether the device takes the sort as a cluster of more than the portable 8
+// blocks, which has to be allowed and needs as many SMs side by side (asked once
+// a device).
+bool large_cluster(int dev, const void *fn, size_t smem) {
+    static std::atomic<uint64_t> asked{0}, fits{0};
+    const uint64_t bit = (uint64_t)1 << (dev & 63);
+    if (!(asked.load() & bit)) {
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = rrn::kSortBlocks;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(rrn::kSortBlocks);
+        cfg.blockDim = dim3(rrn::kSortThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+            cudaOccupancyMaxActiveClusters(&clusters, fn, &cfg) == cudaSuccess && clusters > 0)
+            fits.fetch_or(bit);
+        (void)cudaGetLastError();
+        asked.fetch_or(bit);
+    }
+    return fits.load() & bit;
+}
+
+// Blocks of the sorting cluster: one while its threads have at most two tokens
+// each, and 16 (whose barriers take 2000 cycles, not 800) from eight a thread on.
 int sort_blocks(int64_t count) {
     int n = 1;
-    while (n < 8 && count > 2048 * n) n *= 2;
-    return n;
+    while (n < rrn::kClusterMaxCtas && count > 2 * rrn::kSortThreads * n) n *= 2;
+    return count > 8 * rrn::kSortThreads * n ? rrn::kSortBlocks : n;
 }
 
 }  // namespace
@@ -137,6 +179,48 @@ int rmsnorm_embedding_bwd(const void *dy, const void *tokens, int token_bytes, v
     if (count == 0 && accumulate) return RMSNORM_OK;
     char *ws = static_cast<char *>(workspace);
 
+    rrn::SumParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.tokens = tokens;
+    p.wide = token_bytes == 8;
+    p.dy = static_cast<const char *>(dy);
+    p.dtable = static_cast<char *>(dtable);
+    p.dy_stride = width * s;
+    p.table_stride = table_stride * sg;
+    p.vocab = vocab;
+    p.count = (int32_t)count;
+    p.width = (int32_t)width;
+    p.tiles = (int32_t)at.tiles;
+    p.run = at.run;
+    p.scale = scale;
+    p.accumulate = accumulate;
+    // elements of a piece: what dy's rows and the gradient's both allow
+    int64_t bytes = common_bytes(width * s, 16, 16);
+    while (!rrn::on_boundary(dy, bytes)) bytes /= 2;
+    int64_t held = common_bytes(table_stride * sg, width * sg, 16);
+    while (!rrn::on_boundary(dtable, held)) held /= 2;
+    p.zero_bytes = (int32_t)held;
+    int64_t piece = bytes / s;
+    while (piece * sg > held && held < 16) piece /= 2;
+    const bool direct = count <= rrn::kDirect;
+    p.words = (int32_t)at.words;
+    p.zero_parts = (int32_t)rrn::div_up(width * sg, rrn::kZeroBytes);
+    p.chunks = direct ? rrn::div_up(count, rrn::kSumWarps) : at.chunks;
+    p.work_blocks = p.chunks * at.tiles;
+    // Zeros that are written while the tokens are sorted, as many bytes as that
+    // takes time for (12 us, and 4 for 65536 tokens more); the sums' blocks
+    // write the rest where no token is.
+    const int64_t row_bytes = width * sg;
+    int64_t early = direct || accumulate ? 0 : (((int64_t)48 << 20) + count * 512) / row_bytes / 32 * 32;
+    if (early > vocab) early = vocab;
+    p.first_word = (int32_t)rrn::div_up(early, 32);
+    const int64_t blocks = p.work_blocks +
+                           (accumulate ? 0 : rrn::div_up((at.words - p.first_word) * p.zero_parts, rrn::kSumWarps));
+    if (blocks > INT_MAX) return RMSNORM_EUNSUPPORTED;
+    void *argv[] = {&p};
+    const void *sums = sum_kernel(dtype, grad_dtype, piece, direct);
+    if (direct) return rrn::launch_kernel(sums, dim3((unsigned)blocks), rrn::kSumThreads, 0, stream, argv);
+
     rrn::SortParams q;
     q.tokens = tokens;
     q.a = reinterpret_cast<uint2 *>(ws + at.a);
@@ -147,53 +231,34 @@ int rmsnorm_embedding_bwd(const void *dy, const void *tokens, int token_bytes, v
     q.vocab = (uint32_t)vocab;
     int bits = 1;
     while (vocab >> bits) ++bits;   // of 0 .. vocab
-    q.passes = (int32_t)rrn::div_up(bits, 10);
+    q.passes = (int32_t)rrn::div_up(bits, rrn::kSortMaxBits);
     q.bits = (int32_t)rrn::div_up(bits, q.passes);
-    q.wide = token_bytes == 8;
+    q.wide = p.wide;
+    q.dtable = p.dtable;
+    q.table_stride = p.table_stride;
+    q.zero_rows = early;
+    q.row_bytes = (int32_t)row_bytes;
+    q.zero_bytes = p.zero_bytes;
     int dev = 0, sms = 0;
     if ((st = rrn::current_device_sms(&dev, &sms)) != RMSNORM_OK) return st;
     const void *sort = reinterpret_cast<const void *>(&rrn::embed_sort_kernel);
     if ((st = rrn::allow_smem(dev, sort)) != RMSNORM_OK) return st;
+    int cluster = sort_blocks(count);
+    if (cluster > rrn::kClusterMaxCtas && !large_cluster(dev, sort, rrn::sort_smem(rrn::kSortMaxBits, rrn::kSortWords)))
+        cluster = rrn::kClusterMaxCtas;
     void *sort_argv[] = {&q};
-    const int cluster = sort_blocks(count);
-    st = rrn::launch_kernel(sort, dim3((unsigned)cluster), rrn::kSortThreads,
-                            (size_t)rrn::sort_smem(q.bits), stream, sort_argv, cluster);
+    const int more = early > 0 ? (sms - cluster) / cluster : 0;   // clusters that write zeros
+    st = rrn::launch_kernel(sort, dim3((unsigned)(cluster * (1 + more))), rrn::kSortThreads, (size_t)rrn::sort_smem(q.bits, q.words),
+                            stream, sort_argv, cluster);
     if (st != RMSNORM_OK) return st;
 
-    rrn::SumParams p;
-    std::memset(&p, 0, sizeof(p));
     p.sorted = q.passes % 2 ? q.a : q.b;
-    p.dy = static_cast<const char *>(dy);
-    p.dtable = static_cast<char *>(dtable);
     p.present = q.present;
     p.partial = reinterpret_cast<float *>(ws + at.partial);
-    p.dy_stride = width * s;
-    p.table_stride = table_stride * sg;
-    p.vocab = vocab;
-    p.count = (int32_t)count;
-    p.width = (int32_t)width;
-    p.segments = (int32_t)at.segments;
-    p.tiles = (int32_t)at.tiles;
-    p.scale = scale;
-    p.accumulate = accumulate;
-    p.work_blocks = rrn::div_up(at.segments * at.tiles, rrn::kSumWarps);
-    // elements of a piece: what dy's rows and the gradient's both allow
-    int64_t bytes = common_bytes(width * s, 16, 16);
-    while (!rrn::on_boundary(dy, bytes)) bytes /= 2;
-    int64_t held = common_bytes(table_stride * sg, width * sg, 16);
-    while (!rrn::on_boundary(dtable, held)) held /= 2;
-    p.zero_bytes = (int32_t)held;
-    int64_t piece = bytes / s;
-    while (piece * sg > held && held < 16) piece /= 2;
-    const int64_t blocks = p.work_blocks + (accumulate ? 0 : rrn::div_up(vocab, rrn::kSumWarps));
-    if (blocks > INT_MAX) return RMSNORM_EUNSUPPORTED;
-    void *argv[] = {&p};
-    st = rrn::launch_kernel(sum_kernel(dtype, grad_dtype, piece), dim3((unsigned)blocks), rrn::kSumThreads, 0, stream,
-                            argv);
-    if (st != RMSNORM_OK || at.segments < 2) return st;
-    return rrn::launch_kernel(join_kernel(grad_dtype, piece),
-                              dim3((unsigned)rrn::div_up((at.segments - 1) * at.tiles, rrn::kSumWarps)),
-                              rrn::kSumThreads, 0, stream, argv);
+    st = rrn::launch_kernel(sums, dim3((unsigned)blocks), rrn::kSumThreads, 0, stream, argv);
+    if (st != RMSNORM_OK || at.chunks < 2) return st;
+    return rrn::launch_kernel(join_kernel(grad_dtype, piece), dim3((unsigned)(at.chunks - 1)), rrn::kSumThreads, 0,
+                              stream, argv);
 }
 
 }  // extern "C"
