@@ -26,22 +26,29 @@ int check_logits(const void *logits, const void *tokens, int token_bytes, int64_
     return RMSNORM_OK;
 }
 
-const void *forward_kernel(int dtype, bool entropy, bool top) {
-#define FWD(T) \
-    (entropy ? top ? reinterpret_cast<const void *>(&rrn::logprobs_fwd_kernel<rrn::T, true, true>) \
-                   : reinterpret_cast<const void *>(&rrn::logprobs_fwd_kernel<rrn::T, true, false>) \
-             : top ? reinterpret_cast<const void *>(&rrn::logprobs_fwd_kernel<rrn::T, false, true>) \
-                   : reinterpret_cast<const void *>(&rrn::logprobs_fwd_kernel<rrn::T, false, false>))
-    return dtype == RMSNORM_BF16 ? FWD(BF16) : FWD(F32);
-#undef FWD
+template <typename T, bool ALIGNED>
+const void *forward_of(bool entropy, bool top) {
+    if (entropy)
+        return top ? reinterpret_cast<const void *>(&rrn::logprobs_fwd_kernel<T, ALIGNED, true, true>)
+                   : reinterpret_cast<const void *>(&rrn::logprobs_fwd_kernel<T, ALIGNED, true, false>);
+    return top ? reinterpret_cast<const void *>(&rrn::logprobs_fwd_kernel<T, ALIGNED, false, true>)
+               : reinterpret_cast<const void *>(&rrn::logprobs_fwd_kernel<T, ALIGNED, false, false>);
+}
+const void *forward_kernel(int dtype, bool aligned, bool entropy, bool top) {
+    if (dtype == RMSNORM_BF16)
+        return aligned ? forward_of<rrn::BF16, true>(entropy, top) : forward_of<rrn::BF16, false>(entropy, top);
+    return aligned ? forward_of<rrn::F32, true>(entropy, top) : forward_of<rrn::F32, false>(entropy, top);
 }
 
-const void *backward_kernel(int dtype, bool entropy) {
+template <typename T, bool ALIGNED>
+const void *backward_of(bool entropy) {
+    return entropy ? reinterpret_cast<const void *>(&rrn::logprobs_bwd_kernel<T, ALIGNED, true>)
+                   : reinterpret_cast<const void *>(&rrn::logprobs_bwd_kernel<T, ALIGNED, false>);
+}
+const void *backward_kernel(int dtype, bool aligned, bool entropy) {
     if (dtype == RMSNORM_BF16)
-        return entropy ? reinterpret_cast<const void *>(&rrn::logprobs_bwd_kernel<rrn::BF16, true>)
-                       : reinterpret_cast<const void *>(&rrn::logprobs_bwd_kernel<rrn::BF16, false>);
-    return entropy ? reinterpret_cast<const void *>(&rrn::logprobs_bwd_kernel<rrn::F32, true>)
-                   : reinterpret_cast<const void *>(&rrn::logprobs_bwd_kernel<rrn::F32, false>);
+        return aligned ? backward_of<rrn::BF16, true>(entropy) : backward_of<rrn::BF16, false>(entropy);
+    return aligned ? backward_of<rrn::F32, true>(entropy) : backward_of<rrn::F32, false>(entropy);
 }
 
 }  // namespace
@@ -75,19 +82,26 @@ int rmsnorm_logprobs_fwd(const void *logits, const void *tokens, int token_bytes
     p.vocab = (int32_t)vocab;
     p.units = (int32_t)rrn::div_up(vocab, dtype == RMSNORM_BF16 ? rrn::lp_unit<rrn::BF16>() : rrn::lp_unit<rrn::F32>());
     p.top = top;
+    p.rows = rows;
     p.wide = token_bytes == 8;
-    p.aligned = rrn::on_boundary(logits, 16) && (rows == 1 || p.stride % 16 == 0);
+    const bool aligned = rrn::on_boundary(logits, 16) && (rows == 1 || p.stride % 16 == 0);
     p.inv_t = (float)(1.0 / (double)temperature);
     p.c = (float)(1.4426950408889634 / (double)temperature);
     int dev = 0, sms = 0;
     if ((st = rrn::current_device_sms(&dev, &sms)) != RMSNORM_OK) return st;
+    // a warp a unit, up to the block's eight; short rows several a block, unless
+    // there are few and alternatives to be found, which all warps take part in
+    p.warps = top > 0 && rows <= 2 * sms ? rrn::kLpWarps : 1;
+    while (p.warps < rrn::kLpWarps && p.warps < p.units) p.warps *= 2;
+    const int64_t groups = rrn::div_up(rows, rrn::kLpWarps / p.warps);
     // a row over as many blocks as give every SM one, while each of their warps has a unit
     int cluster = 1;
-    while (cluster < 8 && rows * cluster < sms && 2 * cluster * rrn::kLpWarps <= p.units + rrn::kLpWarps - 1) cluster *= 2;
-    if (rows > INT_MAX / cluster) return RMSNORM_EUNSUPPORTED;
+    while (cluster < 8 && groups * cluster < sms && 2 * cluster * rrn::kLpWarps <= p.units + rrn::kLpWarps - 1) cluster *= 2;
+    if (groups > INT_MAX / cluster) return RMSNORM_EUNSUPPORTED;
     void *argv[] = {&p};
-    return rrn::launch_kernel(forward_kernel(dtype, entropy != nullptr, top > 0), dim3((unsigned)(rows * cluster)),
-                              rrn::kLpThreads, (size_t)p.units * 12, stream, argv, cluster);
+    return rrn::launch_kernel(forward_kernel(dtype, aligned, entropy != nullptr, top > 0),
+                              dim3((unsigned)(groups * cluster)), rrn::kLpThreads,
+                              (size_t)p.units * 12 * (rrn::kLpWarps / p.warps), stream, argv, cluster);
 }
 
 int rmsnorm_logprobs_bwd(const void *logits, const void *tokens, int token_bytes, const float *stats,
@@ -117,14 +131,21 @@ int rmsnorm_logprobs_bwd(const void *logits, const void *tokens, int token_bytes
     p.stride = row_stride * s;
     p.dstride = dlogits_stride * s;
     p.vocab = (int32_t)vocab;
-    p.slices = (int32_t)rrn::div_up(vocab * s, 16 * rrn::kLpThreads * rrn::kLpBwdChunks);
+    p.rows = rows;
     p.wide = token_bytes == 8;
-    p.aligned = rrn::on_boundary(logits, 16) && rrn::on_boundary(dlogits, 16) &&
-                (rows == 1 || (p.stride % 16 == 0 && p.dstride % 16 == 0));
+    const bool aligned = rrn::on_boundary(logits, 16) && rrn::on_boundary(dlogits, 16) &&
+                         (rows == 1 || (p.stride % 16 == 0 && p.dstride % 16 == 0));
     p.inv_t = (float)(1.0 / (double)temperature);
-    if (rows > INT_MAX / p.slices) return RMSNORM_EUNSUPPORTED;
+    p.c = (float)(1.4426950408889634 / (double)temperature);
+    // chunks of a row, one more where they may start before it
+    const int64_t chunks = rrn::div_up(vocab * s, 16) + (aligned ? 0 : 1);
+    p.shift = 5;
+    while (p.shift < 8 && chunks > rrn::kLpBwdChunks << p.shift) ++p.shift;
+    p.slices = (int32_t)rrn::div_up(chunks, (int64_t)rrn::kLpBwdChunks << p.shift);
+    const int64_t groups = rrn::div_up(rows, rrn::kLpThreads >> p.shift);
+    if (groups > INT_MAX / p.slices) return RMSNORM_EUNSUPPORTED;
     void *argv[] = {&p};
-    return rrn::launch_kernel(backward_kernel(dtype, dentropy != nullptr), dim3((unsigned)(rows * p.slices)),
+    return rrn::launch_kernel(backward_kernel(dtype, aligned, dentropy != nullptr), dim3((unsigned)(groups * p.slices)),
                               rrn::kLpThreads, 0, stream, argv);
 }
 

@@ -13,8 +13,11 @@
 // Alternatives: each thread knows the largest logit it saw.  The k-th largest
 // of the maxima of 32 groups of threads is a bound that at least k logits
 // reach, so only threads whose maximum reaches it can hold one of the k
-// largest; their few chunks are read again (from L2) by whole warps, which
-// keep the 32 best in order, a key of value and place a lane.
+// largest; their few chunks are read again (from L2), one a thread, and what
+// reaches the bound, a key of value and place, is gathered in shared memory.
+// Where that is too much (equal logits, masks, a heap of large ones in one
+// place), what was gathered gives a higher bound in the same way.  The few that
+// are left find their places by counting the larger ones.
 //
 // Gradient: elementwise, given the forward's statistics.  One read and one
 // write of every element; HBM bandwidth bounds both.
@@ -38,10 +41,10 @@ struct LogprobParams {
     const void *tokens;
     float *logprobs, *stats, *entropy, *top_logprobs;
     int32_t *top_ids;
-    int64_t stride;      // bytes
+    int64_t rows, stride;   // bytes
     int32_t vocab, units, top;
     int32_t wide;        // 64-bit tokens
-    int32_t aligned;     // every row on a 16-byte boundary
+    int32_t warps;       // of a row: 1, 2, 4, 8 (of every block of a cluster)
     float inv_t, c;      // 1 / temperature, and times log2(e)
 };
 
@@ -60,27 +63,78 @@ __device__ __forceinline__ float warp_max(float v) {
     return r;
 }
 
-// Elements i .. i + V - 1 of a row as a chunk; -infinity behind its end.
+// Elements i .. i + V - 1 of a row as a chunk, one at a time; -infinity outside
+// the row (i may be negative).
 template <typename T>
-__device__ __forceinline__ Chunk logits_chunk(const char *row, int i, int vocab, bool aligned) {
-    constexpr int V = T::kVec;
-    constexpr int E = 16 / V;
-    if (aligned && i + V <= vocab) return ld_keep_l2_16(row + (int64_t)i * E);
+__device__ __forceinline__ Chunk edge_chunk(const char *row, int i, int vocab) {
     Chunk c;
-    if constexpr (V == 8) {
-        const uint16_t *at = reinterpret_cast<const uint16_t *>(row) + i;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t lo = i + 2 * k < vocab ? at[2 * k] : 0xff80u;
-            const uint32_t hi = i + 2 * k + 1 < vocab ? at[2 * k + 1] : 0xff80u;
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (T::kVec == 8) {
+            const uint16_t *at = reinterpret_cast<const uint16_t *>(row);
+            const int a = i + 2 * k, b = a + 1;
+            const uint32_t lo = (uint32_t)a < (uint32_t)vocab ? at[a] : 0xff80u;
+            const uint32_t hi = (uint32_t)b < (uint32_t)vocab ? at[b] : 0xff80u;
             c.u[k] = lo | hi << 16;
+        } else {
+            const int a = i + k;
+            c.u[k] = (uint32_t)a < (uint32_t)vocab ? reinterpret_cast<const uint32_t *>(row)[a] : 0xff800000u;
         }
-    } else {
-        const uint32_t *at = reinterpret_cast<const uint32_t *>(row) + i;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) c.u[k] = i + k < vocab ? at[k] : 0xff800000u;
     }
     return c;
+}
+
+// A 16-byte load that other lanes read from L1 too.
+__device__ __forceinline__ uint4 ld_shared16(const char *p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+// 16 bytes that start `off` bytes into a and go on into b.
+template <typename T>
+__device__ __forceinline__ Chunk across(const uint4 &a, const uint4 &b, int off) {
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int k = 0; k < 6; ++k) w[k] = off & 8 ? w[k + 2] : w[k];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) w[k] = off & 4 ? w[k + 1] : w[k];
+    Chunk c;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c.u[k] = T::kVec == 8 && (off & 2) ? __funnelshift_r(w[k], w[k + 1], 16) : w[k];
+    return c;
+}
+
+// N chunks of a row `step` elements apart, from element i on; -infinity outside
+// the row, and no byte outside it is read.  ALIGNED: they start on 16-byte
+// boundaries, else `off` bytes past them: then each lies in two of memory's own
+// chunks, the second of which is a neighbouring lane's first and comes from L1.
+// Chunks from the first on that lies behind the row are not looked at.
+template <typename T, bool ALIGNED, int N>
+__device__ __forceinline__ void load_chunks(Chunk (&c)[N], const char *row, int i, int step, int vocab, int off) {
+    constexpr int V = T::kVec, E = 16 / V;
+    if (ALIGNED || off == 0) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int at = i + j * step;
+            if (at >= 0 && at + V <= vocab) c[j] = ld_keep_l2_16(row + (int64_t)at * E);
+            else c[j] = edge_chunk<T>(row, at, vocab);
+        }
+        return;
+    }
+    const int least = off / E, most = vocab - 2 * V + off / E;   // places with both chunks within the row
+    uint4 a[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int at = i + j * step;
+        if (at >= least && at <= most) a[j] = ld_shared16(row + (int64_t)at * E - off);
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int at = i + j * step;
+        if (at >= least && at <= most) c[j] = across<T>(a[j], ld_shared16(row + (int64_t)at * E - off + 16), off);
+        else c[j] = edge_chunk<T>(row, at, vocab);
+    }
 }
 
 // The largest element of the chunks (a NaN is passed over).
@@ -115,15 +169,25 @@ __device__ __forceinline__ float value_of(uint32_t o) {
     return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
 }
 
-// One key more into the warp's 32 best, lane 0 the best (a lower one changes nothing).
-__device__ __forceinline__ void insert_key(uint64_t &best, uint64_t key, int lane) {
-    const int at = __popc(__ballot_sync(0xffffffffu, best > key));
-    const uint64_t above = __shfl_up_sync(0xffffffffu, best, 1);
-    if (lane == at) best = key;
-    else if (lane > at) best = above;
+__device__ __forceinline__ uint64_t key_of(float x, int place) { return (uint64_t)order_of(x) << 32 | (uint32_t)~place; }
+
+// Element k of the chunks.
+template <typename T, int N>
+__device__ __forceinline__ float element_of(const Chunk (&c)[N], int k) {
+    constexpr int V = T::kVec;
+    const int word = V == 8 ? k / 2 : k;
+    uint32_t w[4 * N];
+#pragma unroll
+    for (int i = 0; i < 4 * N; ++i) w[i] = c[i / 4].u[i % 4];
+#pragma unroll
+    for (int half = 2 * N; half > 0; half /= 2)
+#pragma unroll
+        for (int i = 0; i < half; ++i) w[i] = word & half ? w[i + half] : w[i];
+    if constexpr (V == 8) return k & 1 ? bf16_hi(w[0]) : bf16_lo(w[0]);
+    return __uint_as_float(w[0]);
 }
 
-// The 32 best of two such lists.
+// The 32 best of two lists of 32 keys, the best in lane 0.
 __device__ __forceinline__ void merge_keys(uint64_t &best, uint64_t other, int lane) {
     const uint64_t turned = __shfl_sync(0xffffffffu, other, 31 - lane);
     uint64_t v = best > turned ? best : turned;   // a bitonic run: one half-cleaner after another orders it
@@ -160,126 +224,271 @@ __device__ __forceinline__ void add_part(Part &a, const Part &b, float c) {
     if (f > 0.f) a.t = fmaf(f, fmaf(d, b.s, b.t), a.t);
 }
 
-template <typename T, bool ENT, bool TOP>
-__global__ void __launch_bounds__(kLpThreads) logprobs_fwd_kernel(const LogprobParams p) {
-    constexpr int V = T::kVec;
-    extern __shared__ float parts[];   // the row's units: maxima, sums, sums of z exp(z)
-    __shared__ float group_max[32];
-    __shared__ uint64_t lists[kLpWarps][32], others[kClusterMaxCtas][32];
-    __shared__ int flagged_count, flagged[kLpThreads];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// Lists of 32 keys in order, `many` of them (up to 8) `step` apart: the best 32
+// of all, by half of the warps at a time.  Every thread of the block calls it.
+__device__ __forceinline__ void merge_lists(uint64_t (*lists)[32], int many, int warp, int lane) {
+#pragma unroll
+    for (int half = 4; half > 0; half /= 2) {
+        __syncthreads();
+        if (warp < half && warp + half < many) {
+            uint64_t best = lists[warp][lane];
+            merge_keys(best, lists[warp + half][lane], lane);
+            lists[warp][lane] = best;
+        }
+        if (many > half) many = half;
+    }
+}
+
+// The `top`-th largest of 32 values (equal ones in their order), lane i's being
+// the i-th.
+template <typename V>
+__device__ __forceinline__ V nth_largest(const V *values, V mine, int top, int lane) {
+    int before = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const V v = values[i];
+        before += v > mine || (v == mine && i < lane);
+    }
+    return __shfl_sync(0xffffffffu, mine, __ffs(__ballot_sync(0xffffffffu, before == top - 1)) - 1);
+}
+
+// Keys gathered for a row at most; from kLpFew on they give a higher bound.
+__host__ __device__ constexpr int lp_room(int warps) { return warps < 2 ? 256 : 128 * warps; }
+constexpr int kLpFew = 96;
+
+// Barrier of a row's warps alone.
+__device__ __forceinline__ void row_barrier(int slot, int warps) {
+    if (warps == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" : : "r"(slot + 1), "r"(warps * 32) : "memory");
+}
+
+template <typename T, bool ALIGNED, bool ENT, bool TOP>
+__global__ void __launch_bounds__(kLpThreads, ALIGNED ? 4 : 3) logprobs_fwd_kernel(const LogprobParams p) {
+    constexpr int V = T::kVec, U = 16 / V;
+    extern __shared__ float parts[];   // each row's units: maxima, sums, sums of z exp(z)
+    __shared__ __align__(16) float maxima[kLpWarps][32];
+    __shared__ __align__(16) uint64_t lists[kLpWarps][32], others[kClusterMaxCtas][32];
+    __shared__ int flagged_count[kLpWarps], gathered_count[kLpWarps], flagged[kLpThreads];
+    __shared__ uint64_t gathered[TOP ? 2048 : 1];   // lp_room(warps) for each row
+    const int tid = threadIdx.x, lane = tid & 31;
     const uint32_t rank = cluster_rank();
     const int blocks = (int)cluster_ctas();
-    const int64_t r = cluster_index();
+    // a block has 8 / warps rows, and a cluster of several blocks one
+    const int warps = p.warps, warp = (tid >> 5) % warps, slot = (tid >> 5) / warps;
+    const int64_t r = (int64_t)cluster_index() * (kLpWarps / warps) + slot;
+    const bool there = r < p.rows;
     const char *row = p.logits + r * p.stride;
+    const int off = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(row) & 15);
+    float *mine = parts + (int64_t)slot * 3 * p.units;
     // before a block writes to the first one's shared memory, that has started
-    asm volatile("barrier.cluster.arrive.release.aligned;" : : : "memory");
+    if (blocks > 1) asm volatile("barrier.cluster.arrive.release.aligned;" : : : "memory");
     pdl_wait_for_inputs();
     pdl_allow_dependents();
-    if (TOP && tid == 0) flagged_count = 0;
-    // the given token's logit, on its way while the sums are formed
+    if (TOP && tid < kLpWarps) flagged_count[tid] = gathered_count[tid] = 0;
+    // the given token; its logit is on its way with the first unit's
     int64_t token = -1;
     float given = 0.f;
-    if (rank == 0 && tid == 0 && p.logprobs != nullptr) {
+    if (there && rank == 0 && warp == 0 && p.logprobs != nullptr)
         token = p.wide ? static_cast<const int64_t *>(p.tokens)[r] : (int64_t) static_cast<const int32_t *>(p.tokens)[r];
-        if ((uint64_t)token < (uint64_t)p.vocab)
-            given = widen_bits(ld_bits(row, token, T{}, 0), T{});
-    }
-    __syncwarp();
-    asm volatile("barrier.cluster.wait.acquire.aligned;" : : : "memory");
+    const int step = blocks * warps, begin = there ? (int)rank * warps + warp : p.units;
     float seen = neg_inf();   // the largest logit of this thread
-    const int step = blocks * kLpWarps;
-    for (int unit = (int)rank * kLpWarps + warp; unit < p.units; unit += step) {
+    for (int unit = begin; unit < p.units; unit += step) {
         Chunk c[kLpChunks];
-        const int first = unit * lp_unit<T>() + lane * V;
-#pragma unroll
-        for (int j = 0; j < kLpChunks; ++j) c[j] = logits_chunk<T>(row, first + j * 32 * V, p.vocab, p.aligned);
+        load_chunks<T, ALIGNED>(c, row, unit * lp_unit<T>() + lane * V, 32 * V, p.vocab, off);
+        if (unit == 0 && (uint64_t)token < (uint64_t)p.vocab) given = widen_bits(ld_bits(row, token, T{}, 0), T{});
         const float local = chunks_max(c, T{});
         if (TOP) seen = fmaxf(seen, local);
         const float m = warp_max(local);
         const float from = m == neg_inf() ? 0.f : m;
         float2 s = make_float2(0.f, 0.f), t = make_float2(0.f, 0.f);
-        const float2 off = make_float2(-from, -from), cc = make_float2(p.c, p.c);
-#pragma unroll
-        for (int j = 0; j < kLpChunks; ++j) {
+        const float2 less = make_float2(-from, -from), cc = make_float2(p.c, p.c);
+        auto add = [&](const Chunk &chunk) {
             float x[V];
-            unpack(c[j], x, T{});
+            unpack(chunk, x, T{});
 #pragma unroll
             for (int k = 0; k < V; k += 2) {
-                const float2 z = __fmul2_rn(__fadd2_rn(make_float2(x[k], x[k + 1]), off), cc);
+                const float2 z = __fmul2_rn(__fadd2_rn(make_float2(x[k], x[k + 1]), less), cc);
                 const float2 e = make_float2(ex2(z.x), ex2(z.y));
                 s = __fadd2_rn(s, e);
                 // a masked logit's z is -infinity: no part in the sum
                 if (ENT) t = __ffma2_rn(e, make_float2(fmaxf(z.x, -1e4f), fmaxf(z.y, -1e4f)), t);
             }
+        };
+        // chunks that some lane has in the row
+        const int used = (p.vocab - unit * lp_unit<T>() + 32 * V - 1) / (32 * V);
+        if (used >= kLpChunks) {
+#pragma unroll
+            for (int j = 0; j < kLpChunks; ++j) add(c[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kLpChunks; ++j) {
+                if (j >= used) break;
+                add(c[j]);
+            }
         }
         const float sum = butterfly_sum<32>(s.x + s.y);
         const float zsum = ENT ? butterfly_sum<32>(t.x + t.y) : 0.f;
+        if (blocks > 1 && unit == begin) {   // (every warp has one, or had none to begin with)
+            __syncwarp();
+            asm volatile("barrier.cluster.wait.acquire.aligned;" : : : "memory");
+        }
         if (lane == 0) {
-            st_cluster_f32(parts + unit, 0, m);
-            st_cluster_f32(parts + p.units + unit, 0, sum);
-            if (ENT) st_cluster_f32(parts + 2 * p.units + unit, 0, zsum);
-        }
-    }
-    uint64_t best = 0;
-    if (TOP) {
-        const float of_group = fmaxf(fmaxf(seen, __shfl_xor_sync(0xffffffffu, seen, 1)), neg_inf());
-        const float two = fmaxf(of_group, __shfl_xor_sync(0xffffffffu, of_group, 2));
-        const float four = fmaxf(two, __shfl_xor_sync(0xffffffffu, two, 4));
-        if (lane % 8 == 0) group_max[warp * 4 + lane / 8] = four;
-        __syncthreads();
-        // the bound: the group maximum that p.top - 1 others come before
-        const float held = group_max[lane];
-        int before = 0;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const float v = __shfl_sync(0xffffffffu, held, i);
-            before += v > held || (v == held && i < lane);
-        }
-        const float bound = __shfl_sync(0xffffffffu, held, __ffs(__ballot_sync(0xffffffffu, before == p.top - 1)) - 1);
-        if (seen >= bound) flagged[atomicAdd(&flagged_count, 1)] = tid;   // in any order: the keys decide
-        __syncthreads();
-        const uint32_t least = order_of(bound);
-        const int many = flagged_count;
-        const int mine = p.units / step * kLpChunks + kLpChunks;   // chunks of a thread at most
-        for (int f = warp; f < many; f += kLpWarps) {
-            const int owner = flagged[f];
-            for (int i0 = 0; i0 < mine; i0 += 32) {
-                const int i = i0 + lane;
-                const int unit = (int)rank * kLpWarps + (owner >> 5) + i / kLpChunks * step;
-                const bool there = i < mine && unit < p.units;
-                const int at = unit * lp_unit<T>() + (i % kLpChunks * 32 + (owner & 31)) * V;
-                float x[V];
-                if (there) unpack(logits_chunk<T>(row, at, p.vocab, p.aligned), x, T{});
-                const uint64_t worst = __shfl_sync(0xffffffffu, best, p.top - 1);
-#pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    const uint32_t o = there && at + k < p.vocab ? order_of(x[k]) : 0;
-                    const uint64_t key = o >= least ? (uint64_t)o << 32 | (uint32_t)~(at + k) : 0;
-                    uint32_t todo = __ballot_sync(0xffffffffu, key > worst);
-                    while (todo) {
-                        const int from = __ffs(todo) - 1;
-                        todo &= todo - 1;
-                        insert_key(best, __shfl_sync(0xffffffffu, key, from), lane);
-                    }
-                }
+            if (blocks > 1) {
+                st_cluster_f32(mine + unit, 0, m);
+                st_cluster_f32(mine + p.units + unit, 0, sum);
+                if (ENT) st_cluster_f32(mine + 2 * p.units + unit, 0, zsum);
+            } else {
+                mine[unit] = m;
+                mine[p.units + unit] = sum;
+                if (ENT) mine[2 * p.units + unit] = zsum;
             }
         }
-        lists[warp][lane] = best;
-        __syncthreads();
-        if (warp == 0) {
-            for (int w = 1; w < kLpWarps; ++w) merge_keys(best, lists[w][lane], lane);
-            if (rank != 0) st_cluster_u64(&others[rank][lane], 0, best);
-        }
     }
-    __syncwarp();
-    cluster_barrier();
-    if (rank != 0 || warp != 0) return;
+    if (blocks > 1 && begin >= p.units) asm volatile("barrier.cluster.wait.acquire.aligned;" : : : "memory");
+    if (TOP) {
+        // 32 groups of a row's threads: a lane's of every warp
+        maxima[slot * warps + warp][lane] = seen;
+        lists[slot * warps + warp][lane] = 0;
+        __syncthreads();
+        float of_group = neg_inf();
+        for (int w = 0; w < warps; ++w) of_group = fmaxf(of_group, maxima[slot * warps + w][lane]);
+        row_barrier(slot, warps);
+        if (warp == 0) maxima[slot * warps][lane] = of_group;
+        row_barrier(slot, warps);
+        const float bound = nth_largest(maxima[slot * warps], of_group, p.top, lane);
+        uint64_t least = (uint64_t)order_of(bound) << 32;
+        if (seen >= bound && begin < p.units)
+            flagged[slot * warps * 32 + atomicAdd(flagged_count + slot, 1)] = warp * 32 + lane;   // in any order
+        row_barrier(slot, warps);
+        const int room = lp_room(warps), threads = warps * 32;
+        uint64_t *keys = gathered + slot * room;
+        int *count = gathered_count + slot;
+        // every chunk of the flagged threads, one a thread
+        const int each = begin < p.units + warp ? (p.units - (int)rank * warps + step - 1) / step * kLpChunks : 0;
+        const int many = flagged_count[slot] * each;
+        int found;
+        for (;;) {
+            for (int i0 = warp * 32; i0 < many && *reinterpret_cast<volatile int *>(count) <= room; i0 += threads * U) {
+                Chunk c[U];
+                int at[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int i = i0 + u * threads + lane;
+                    at[u] = p.vocab;
+                    if (i < many) {
+                        const int f = i / each, j = i - f * each, owner = flagged[slot * threads + f];
+                        const int unit = (int)rank * warps + (owner >> 5) + j / kLpChunks * step;
+                        if (unit < p.units) at[u] = unit * lp_unit<T>() + (j % kLpChunks * 32 + (owner & 31)) * V;
+                    }
+                    if (at[u] < p.vocab) {
+                        Chunk one[1];
+                        load_chunks<T, ALIGNED>(one, row, at[u], 0, p.vocab, off);
+                        c[u] = one[0];
+                    }
+                }
+                // which of them, then places for the warp's all at once
+                uint32_t these = 0;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float x[V];
+                    unpack(c[u], x, T{});
+#pragma unroll
+                    for (int k = 0; k < V; ++k)
+                        if (!(x[k] < bound) && at[u] + k < p.vocab) these |= 1u << (u * V + k);
+                }
+                if (least != (uint64_t)order_of(bound) << 32) {   // a bound that goes by places too
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        float x[V];
+                        unpack(c[u], x, T{});
+#pragma unroll
+                        for (int k = 0; k < V; ++k)
+                            if (key_of(x[k], at[u] + k) < least) these &= ~(1u << (u * V + k));
+                    }
+                }
+                int place = __popc(these), all = place;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int n = __shfl_up_sync(0xffffffffu, all, o);
+                    if (lane >= o) all += n;
+                }
+                int first = 0;
+                if (lane == 31 && all > 0) first = atomicAdd(count, all);   // in any order: the keys decide
+                place = __shfl_sync(0xffffffffu, first, 31) + all - place;
+                for (; these != 0; these &= these - 1, ++place) {
+                    if (place >= room) break;
+                    const int k = __ffs(these) - 1;
+                    const float x = element_of<T>(c, k);
+                    int where = at[0];
+#pragma unroll
+                    for (int u = 1; u < U; ++u) where = k / V == u ? at[u] : where;
+                    keys[place] = key_of(x, where + k % V);
+                }
+            }
+            row_barrier(slot, warps);
+            found = *count;
+            const int held = found < room ? found : room;
+            if (found <= kLpFew) break;
+            // the bound that 32 groups of these give
+            uint64_t best = 0;
+            for (int i = lane; i < held; i += 32) best = best > keys[i] ? best : keys[i];
+            uint64_t kept[8];   // room / threads at most
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int i = warp * 32 + lane + k * threads;
+                kept[k] = i < held ? keys[i] : 0;
+            }
+            row_barrier(slot, warps);
+            if (warp == 0) {
+                lists[slot * warps][lane] = best;
+                if (lane == 0) *count = 0;
+            }
+            row_barrier(slot, warps);
+            const uint64_t higher = nth_largest(lists[slot * warps], best, p.top, lane);
+            const bool again = found > room;
+            if (!again)
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (kept[k] >= higher && kept[k] != 0) keys[atomicAdd(count, 1)] = kept[k];
+            row_barrier(slot, warps);
+            if (warp == 0) lists[slot * warps][lane] = 0;
+            if (!again) {
+                found = *count;
+                row_barrier(slot, warps);
+                break;
+            }
+            least = higher > least ? higher : least;
+            row_barrier(slot, warps);
+        }
+        // their order, by counting the larger ones
+        for (int i = (warp * 32 + lane) / 8; i < (found + 3) / 4 * 4; i += threads / 8) {   // eight lanes a key
+            const uint64_t key = i < found ? keys[i] : 0;
+            int before = 0;
+            for (int j = lane % 8; j < found; j += 8) before += keys[j] > key;
+#pragma unroll
+            for (int o = 1; o < 8; o *= 2) before += __shfl_xor_sync(0xffffffffu, before, o);
+            if (i < found && before < 32 && lane % 8 == 0) {
+                if (blocks > 1) st_cluster_u64(&others[rank][before], 0, key);
+                else lists[slot * warps][before] = key;
+            }
+        }
+        // where there are fewer than 32
+        if (blocks > 1 && warp == 0 && lane >= found) st_cluster_u64(&others[rank][lane], 0, 0);
+    }
+    if (blocks > 1) {
+        __syncwarp();
+        cluster_barrier();
+    } else {
+        __syncthreads();
+    }
+    if (rank != 0) return;
+    if (TOP && blocks > 1) merge_lists(others, blocks, warp, lane);   // the same in the block
+    if (warp != 0 || !there) return;
     float most = neg_inf();
-    for (int u = lane; u < p.units; u += 32) most = fmaxf(most, parts[u]);
+    for (int u = lane; u < p.units; u += 32) most = fmaxf(most, mine[u]);
     Part a = {warp_max(most), 0.f, 0.f};
     for (int u = lane; u < p.units; u += 32)
-        add_part(a, Part{parts[u], parts[p.units + u], ENT ? parts[2 * p.units + u] : 0.f}, p.c);
+        add_part(a, Part{mine[u], mine[p.units + u], ENT ? mine[2 * p.units + u] : 0.f}, p.c);
     a.s = butterfly_sum<32>(a.s);
     if (ENT) a.t = butterfly_sum<32>(a.t);
     const bool none = a.m == neg_inf() && a.s == 0.f;   // every logit masked
@@ -290,12 +499,10 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_fwd_kernel(const LogprobP
         if (p.stats != nullptr) *reinterpret_cast<float2 *>(p.stats + 2 * r) = make_float2(a.m, log);
         if (ENT) p.entropy[r] = none ? 0.f : log - kLn2 * a.t / a.s;
     }
-    if (TOP) {
-        for (int q = 1; q < blocks; ++q) merge_keys(best, others[q][lane], lane);
-        if (lane < p.top) {
-            p.top_ids[r * p.top + lane] = (int32_t) ~(uint32_t)best;
-            p.top_logprobs[r * p.top + lane] = none ? neg_inf() : (value_of((uint32_t)(best >> 32)) - a.m) * p.inv_t - log;
-        }
+    if (TOP && lane < p.top) {
+        const uint64_t best = blocks > 1 ? others[0][lane] : lists[slot * warps][lane];
+        p.top_ids[r * p.top + lane] = (int32_t) ~(uint32_t)best;
+        p.top_logprobs[r * p.top + lane] = none ? neg_inf() : (value_of((uint32_t)(best >> 32)) - a.m) * p.inv_t - log;
     }
 }
 
@@ -306,83 +513,92 @@ struct LogprobBwdParams {
     const void *tokens;
     const float *stats, *dlogprobs, *entropy, *dentropy;
     char *dlogits;
-    int64_t stride, dstride;   // bytes
-    int32_t vocab, slices;     // blocks of a row
+    int64_t rows, stride, dstride;   // bytes
+    int32_t vocab, slices;           // blocks of a row
+    int32_t shift;                   // 2^shift threads of a row in a block: 32 .. 256
     int32_t wide;
-    int32_t aligned;
-    float inv_t;
+    float inv_t, c;
 };
 
 constexpr int kLpBwdChunks = 4;
 
-// d_v = (g [v is the token] - p_v (g + h (log p_v + H))) / temperature
-template <typename T, bool ENT>
-__global__ void __launch_bounds__(kLpThreads) logprobs_bwd_kernel(const LogprobBwdParams p) {
+// d_v = (g [v is the token] - p_v (g + h (log p_v + H))) / temperature, with
+// q = log2 p_v:  p (a + b q).  Chunks lie on dlogits' 16-byte boundaries
+// (ALIGNED: on both tensors').
+template <typename T, bool ALIGNED, bool ENT>
+__global__ void __launch_bounds__(kLpThreads, ALIGNED ? 6 : 4) logprobs_bwd_kernel(const LogprobBwdParams p) {
     constexpr int V = T::kVec, E = 16 / V;
-    const int64_t r = blockIdx.x / p.slices;
-    const int slice = (int)(blockIdx.x - r * p.slices);
-    const char *row = p.logits + r * p.stride;
-    char *to = p.dlogits + r * p.dstride;
+    const uint32_t group = blockIdx.x / (uint32_t)p.slices;
+    const int slice = (int)(blockIdx.x - group * p.slices);
+    const int64_t r = ((int64_t)group << (8 - p.shift)) + (threadIdx.x >> p.shift);
     pdl_wait_for_inputs();
     pdl_allow_dependents();
-    int64_t token = -1;
+    if (r >= p.rows) return;
+    const char *row = p.logits + r * p.stride;
+    char *to = p.dlogits + r * p.dstride;
+    const int head = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(to) & 15) / E;
+    const int off = ALIGNED ? 0 : (int)((reinterpret_cast<uintptr_t>(row) - head * E) & 15);
+    int token = -1;
     float g = 0.f, h = 0.f, own = 0.f;
     if (p.dlogprobs != nullptr) {
-        token = p.wide ? static_cast<const int64_t *>(p.tokens)[r] : (int64_t) static_cast<const int32_t *>(p.tokens)[r];
-        if ((uint64_t)token < (uint64_t)p.vocab) g = p.dlogprobs[r];
-        else token = -1;
+        const int64_t id = p.wide ? static_cast<const int64_t *>(p.tokens)[r]
+                                  : (int64_t) static_cast<const int32_t *>(p.tokens)[r];
+        if ((uint64_t)id < (uint64_t)p.vocab) {
+            token = (int)id;
+            g = p.dlogprobs[r];
+        }
     }
     if (ENT) h = p.dentropy[r];
     const float2 stats = *reinterpret_cast<const float2 *>(p.stats + 2 * r);
     if (ENT) own = h == 0.f ? 0.f : h * p.entropy[r];
     const bool zero = (g == 0.f && h == 0.f) || (stats.x == neg_inf() && stats.y == neg_inf());
-    const float gt = g * p.inv_t;
-    const float a = -(g + own) * p.inv_t, b = -h * p.inv_t;   // d = p (a + b log p)
-    const float2 off = make_float2(-stats.x, -stats.x), it = make_float2(p.inv_t, p.inv_t);
-    const float2 nl = make_float2(-stats.y, -stats.y), l2 = make_float2(kLog2e, kLog2e);
-    const float2 a2 = make_float2(a, a), b2 = make_float2(b, b);
-    const int first = (slice * kLpBwdChunks * kLpThreads + threadIdx.x) * V;
-    Chunk c[kLpBwdChunks];
+    const int step = V << p.shift;
+    const int first = slice * kLpBwdChunks * step + ((int)threadIdx.x & ((1 << p.shift) - 1)) * V - head;
+    if (zero) {   // nothing is read
 #pragma unroll
-    for (int j = 0; j < kLpBwdChunks; ++j) {
-        const int i = first + j * kLpThreads * V;
-        if (!zero && i < p.vocab) c[j] = logits_chunk<T>(row, i, p.vocab, p.aligned);
-        else c[j] = Chunk{};
+        for (int j = 0; j < kLpBwdChunks; ++j) {
+            const int i = first + j * step;
+            if (i >= 0 && i + V <= p.vocab) {
+                st16(to + (int64_t)i * E, Chunk{});
+            } else {
+                for (int k = 0; k < V; ++k)
+                    if (i + k >= 0 && i + k < p.vocab) st_scalar(to, i + k, 0.f, T{});
+            }
+        }
+        return;
     }
+    Chunk c[kLpBwdChunks];
+    load_chunks<T, ALIGNED>(c, row, first, step, p.vocab, off);
+    const float2 less = make_float2(-stats.x, -stats.x), cc = make_float2(p.c, p.c);
+    const float l = -stats.y * kLog2e, a = -(g + own) * p.inv_t, b = -h * p.inv_t * kLn2;
 #pragma unroll
     for (int j = 0; j < kLpBwdChunks; ++j) {
-        const int i = first + j * kLpThreads * V;
+        const int i = first + j * step;
         if (i >= p.vocab) return;
         float x[V];
         unpack(c[j], x, T{});
-        if (zero) {
 #pragma unroll
-            for (int k = 0; k < V; ++k) x[k] = 0.f;
-        } else {
-#pragma unroll
-            for (int k = 0; k < V; k += 2) {
-                float2 lp = __ffma2_rn(__fadd2_rn(make_float2(x[k], x[k + 1]), off), it, nl);
-                const float2 q = __fmul2_rn(lp, l2);
-                const float2 e = make_float2(ex2(q.x), ex2(q.y));
-                float2 d = a2;
-                if (ENT) d = __ffma2_rn(b2, make_float2(fmaxf(lp.x, -1e4f), fmaxf(lp.y, -1e4f)), a2);
-                d = __fmul2_rn(e, d);
-                x[k] = d.x;
-                x[k + 1] = d.y;
-            }
-            const uint32_t at = (uint32_t)((int)token - i);
-            if (at < (uint32_t)V) {
-#pragma unroll
-                for (int k = 0; k < V; ++k)
-                    if (at == (uint32_t)k) x[k] += gt;
-            }
+        for (int k = 0; k < V; k += 2) {
+            const float2 q = __ffma2_rn(__fadd2_rn(make_float2(x[k], x[k + 1]), less), cc, make_float2(l, l));
+            const float2 e = make_float2(ex2(q.x), ex2(q.y));
+            float2 d = make_float2(a, a);
+            if (ENT) d = __ffma2_rn(make_float2(b, b), make_float2(fmaxf(q.x, -1e4f), fmaxf(q.y, -1e4f)), d);
+            d = __fmul2_rn(e, d);
+            x[k] = d.x;
+            x[k + 1] = d.y;
         }
-        if (p.aligned && i + V <= p.vocab) {
+        const uint32_t at = (uint32_t)(token - i);
+        if (at < (uint32_t)V && token >= 0) {
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+                if (at == (uint32_t)k) x[k] += g * p.inv_t;
+        }
+        if ((ALIGNED || i >= 0) && i + V <= p.vocab) {
             st16(to + (int64_t)i * E, pack(x, T{}));
         } else {
 #pragma unroll
             for (int k = 0; k < V; ++k)
-                if (i + k < p.vocab) st_scalar(to, i + k, x[k], T{});
+                if (i + k >= 0 && i + k < p.vocab) st_scalar(to, i + k, x[k], T{});
         }
     }
 }
