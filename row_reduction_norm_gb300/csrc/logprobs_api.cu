@@ -98,10 +98,13 @@ int rmsnorm_logprobs_fwd(const void *logits, const void *tokens, int token_bytes
     int cluster = 1;
     while (cluster < 8 && groups * cluster < sms && 2 * cluster * rrn::kLpWarps <= p.units + rrn::kLpWarps - 1) cluster *= 2;
     if (groups > INT_MAX / cluster) return RMSNORM_EUNSUPPORTED;
+    const void *fn = forward_kernel(dtype, aligned, entropy != nullptr, top > 0);
+    const size_t smem = (size_t)p.units * 12 * (rrn::kLpWarps / p.warps);
+    int resident = 0;
+    if ((st = rrn::resident_blocks(dev, fn, rrn::kLpThreads, smem, &resident)) != RMSNORM_OK) return st;
+    p.ahead = (int64_t)resident * sms * (rrn::kLpWarps / p.warps);
     void *argv[] = {&p};
-    return rrn::launch_kernel(forward_kernel(dtype, aligned, entropy != nullptr, top > 0),
-                              dim3((unsigned)(groups * cluster)), rrn::kLpThreads,
-                              (size_t)p.units * 12 * (rrn::kLpWarps / p.warps), stream, argv, cluster);
+    return rrn::launch_kernel(fn, dim3((unsigned)(groups * cluster)), rrn::kLpThreads, smem, stream, argv, cluster);
 }
 
 int rmsnorm_logprobs_bwd(const void *logits, const void *tokens, int token_bytes, const float *stats,
@@ -141,8 +144,16 @@ int rmsnorm_logprobs_bwd(const void *logits, const void *tokens, int token_bytes
     const int64_t chunks = rrn::div_up(vocab * s, 16) + (aligned ? 0 : 1);
     p.shift = 5;
     while (p.shift < 8 && chunks > rrn::kLpBwdChunks << p.shift) ++p.shift;
-    p.slices = (int32_t)rrn::div_up(chunks, (int64_t)rrn::kLpBwdChunks << p.shift);
     const int64_t groups = rrn::div_up(rows, rrn::kLpThreads >> p.shift);
+    const int64_t parts = rrn::div_up(chunks, (int64_t)rrn::kLpBwdChunks << p.shift);
+    int dev = 0, sms = 0;
+    const int got = rrn::current_device_sms(&dev, &sms);
+    if (got != RMSNORM_OK) return got;
+    // Parts of a row that a block takes: four where that leaves four waves of
+    // blocks (bf16 8192 x 131072: one 700 us, two 635, four 622, sixteen 635).
+    const int64_t most = groups * parts / (16 * (int64_t)sms);
+    p.turns = most >= 4 ? 4 : most >= 2 ? 2 : 1;
+    p.slices = (int32_t)rrn::div_up(parts, p.turns);
     if (groups > INT_MAX / p.slices) return RMSNORM_EUNSUPPORTED;
     void *argv[] = {&p};
     return rrn::launch_kernel(backward_kernel(dtype, aligned, dentropy != nullptr), dim3((unsigned)(groups * p.slices)),

@@ -29,6 +29,7 @@ namespace rrn {
 
 constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32, kLpChunks = 8;
 constexpr int kLpTop = 32;   // alternatives at most
+constexpr int kLpAhead = 32 * 1024;   // bytes of a row that are asked for ahead
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <typename T>
@@ -45,6 +46,7 @@ struct LogprobParams {
     int32_t vocab, units, top;
     int32_t wide;        // 64-bit tokens
     int32_t warps;       // of a row: 1, 2, 4, 8 (of every block of a cluster)
+    int64_t ahead;       // rows that the device holds at once
     float inv_t, c;      // 1 / temperature, and times log2(e)
 };
 
@@ -63,25 +65,58 @@ __device__ __forceinline__ float warp_max(float v) {
     return r;
 }
 
-// Elements i .. i + V - 1 of a row as a chunk, one at a time; -infinity outside
-// the row (i may be negative).
+// Elements i .. i + V - 1 of a row as a chunk, each by itself; -infinity outside
+// the row (i may be negative).  Shifted in, for few registers: it is for the
+// first and the last chunk of a tensor.
 template <typename T>
 __device__ __forceinline__ Chunk edge_chunk(const char *row, int i, int vocab) {
-    Chunk c;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    Chunk c = {};
+#pragma unroll 4
+    for (int k = T::kVec - 1; k >= 0; --k) {
+        const bool in = (uint32_t)(i + k) < (uint32_t)vocab;
         if constexpr (T::kVec == 8) {
-            const uint16_t *at = reinterpret_cast<const uint16_t *>(row);
-            const int a = i + 2 * k, b = a + 1;
-            const uint32_t lo = (uint32_t)a < (uint32_t)vocab ? at[a] : 0xff80u;
-            const uint32_t hi = (uint32_t)b < (uint32_t)vocab ? at[b] : 0xff80u;
-            c.u[k] = lo | hi << 16;
+            const uint32_t v = in ? reinterpret_cast<const uint16_t *>(row)[i + k] : 0xff80u;
+            c.u[3] = __funnelshift_l(c.u[2], c.u[3], 16);
+            c.u[2] = __funnelshift_l(c.u[1], c.u[2], 16);
+            c.u[1] = __funnelshift_l(c.u[0], c.u[1], 16);
+            c.u[0] = c.u[0] << 16 | v;
         } else {
-            const int a = i + k;
-            c.u[k] = (uint32_t)a < (uint32_t)vocab ? reinterpret_cast<const uint32_t *>(row)[a] : 0xff800000u;
+            c.u[3] = c.u[2];
+            c.u[2] = c.u[1];
+            c.u[1] = c.u[0];
+            c.u[0] = in ? reinterpret_cast<const uint32_t *>(row)[i + k] : 0xff800000u;
         }
     }
     return c;
+}
+
+template <typename T>
+__device__ __forceinline__ Chunk minus_infinity() {
+    const uint32_t v = T::kVec == 8 ? 0xff80ff80u : 0xff800000u;
+    return Chunk{{v, v, v, v}};
+}
+
+// -infinity in the places of a chunk, which starts at element i, outside the row.
+template <typename T>
+__device__ __forceinline__ void mask_chunk(Chunk &c, int i, int vocab) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (T::kVec == 8) {
+            if ((uint32_t)(i + 2 * k) >= (uint32_t)vocab) c.u[k] = (c.u[k] & 0xffff0000u) | 0xff80u;
+            if ((uint32_t)(i + 2 * k + 1) >= (uint32_t)vocab) c.u[k] = (c.u[k] & 0xffffu) | 0xff800000u;
+        } else {
+            if ((uint32_t)(i + k) >= (uint32_t)vocab) c.u[k] = 0xff800000u;
+        }
+    }
+}
+
+// Whether 32 bytes before a row's first byte, and behind its last, are the
+// tensor's too: chunks that begin or end outside the row may be read whole then.
+struct Around {
+    bool before, behind;
+};
+__device__ __forceinline__ Around around(const char *tensor, const char *row, int64_t rows, int64_t stride) {
+    return Around{row - tensor >= 32, tensor + (rows - 1) * stride - row >= 32};
 }
 
 // A 16-byte load that other lanes read from L1 too.
@@ -106,35 +141,106 @@ __device__ __forceinline__ Chunk across(const uint4 &a, const uint4 &b, int off)
 }
 
 // N chunks of a row `step` elements apart, from element i on; -infinity outside
-// the row, and no byte outside it is read.  ALIGNED: they start on 16-byte
-// boundaries, else `off` bytes past them: then each lies in two of memory's own
-// chunks, the second of which is a neighbouring lane's first and comes from L1.
-// Chunks from the first on that lies behind the row are not looked at.
+// the row, and no byte outside the tensor is read.  ALIGNED: they start on
+// 16-byte boundaries, else `off` bytes past them: then each lies in two of
+// memory's own chunks, the second of which is a neighbouring lane's first and
+// comes from L1.
 template <typename T, bool ALIGNED, int N>
-__device__ __forceinline__ void load_chunks(Chunk (&c)[N], const char *row, int i, int step, int vocab, int off) {
+__device__ __forceinline__ void load_chunks(Chunk (&c)[N], const char *row, int i, int step, int vocab, int off,
+                                            Around there) {
     constexpr int V = T::kVec, E = 16 / V;
-    if (ALIGNED || off == 0) {
+    // places of chunks that may be read whole, both of memory's where there are two
+    const bool two = !ALIGNED && off != 0;
+    const int least = there.before ? 1 - V : two ? off / E : 0;
+    const int most = there.behind ? vocab - 1 : two ? vocab - 2 * V + off / E : vocab - V;
+    if (two) {
+        uint4 a[N];
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const int at = i + j * step;
-            if (at >= 0 && at + V <= vocab) c[j] = ld_keep_l2_16(row + (int64_t)at * E);
-            else c[j] = edge_chunk<T>(row, at, vocab);
+            if (at >= least && at <= most) a[j] = ld_shared16(row + (int64_t)at * E - off);
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int at = i + j * step;
+            if (at >= least && at <= most) c[j] = across<T>(a[j], ld_shared16(row + (int64_t)at * E - off + 16), off);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int at = i + j * step;
+            if (at >= least && at <= most) c[j] = ld_keep_l2_16(row + (int64_t)at * E);
+        }
+    }
+    const int last = i + (N - 1) * step;
+    if (i >= 0 && i >= least && last <= most && last + V <= vocab) return;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int at = i + j * step;
+        if (at < least || at > most) c[j] = edge_chunk<T>(row, at, vocab);
+        else if (at < 0 || at + V > vocab) mask_chunk<T>(c[j], at, vocab);
+    }
+}
+
+// A warp's unit of a row, lane l's chunk j being the unit's chunk 32 j + l;
+// -infinity behind the row's end.  Units well within the row are plain loads.  In
+// the others addresses are held within the tensor, what lies behind the row is
+// masked, and the chunks at the tensor's two ends are put together by themselves.
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ void load_unit(Chunk (&c)[kLpChunks], const char *row, int unit, int lane, int vocab, int off,
+                                          Around there) {
+    constexpr int V = T::kVec, E = 16 / V, N = kLpChunks, STEP = 32 * 16;   // bytes between a lane's chunks
+    const bool two = !ALIGNED && off != 0;
+    const int first = unit * lp_unit<T>(), end = first + lp_unit<T>();
+    const char *from = row + (int64_t)first * E + lane * 16;
+    const bool inside = end <= vocab && (!two || ((first > 0 || there.before) &&
+                                                  (there.behind || end * E + 16 - off <= vocab * E)));
+    if (inside) {
+        if (two) {
+            uint4 a[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) a[j] = ld_shared16(from - off + j * STEP);
+#pragma unroll
+            for (int j = 0; j < N; ++j) c[j] = across<T>(a[j], ld_shared16(from - off + 16 + j * STEP), off);
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j) c[j] = ld_keep_l2_16(from + j * STEP);
         }
         return;
     }
-    const int least = off / E, most = vocab - 2 * V + off / E;   // places with both chunks within the row
-    uint4 a[N];
+    // bytes from the row's start at which memory's chunks lie whole in the tensor
+    const int low = two ? there.before ? -off : 16 - off : 0;
+    const int bytes = vocab * E;
+    const int high = ((bytes + off) / 16 - (there.behind ? 0 : 1)) * 16 - off;
+    const bool any = high >= low;
+    const int at = first * E + lane * 16;
+    const int used = (vocab - first + 32 * V - 1) / (32 * V);   // chunks that some lane has in the row
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-        const int at = i + j * step;
-        if (at >= least && at <= most) a[j] = ld_shared16(row + (int64_t)at * E - off);
+        c[j] = minus_infinity<T>();
+        if (j >= used) continue;
+        const int a = max(low, min(at + j * STEP - off, high)), b = max(low, min(at + j * STEP - off + 16, high));
+        if (!any) continue;
+        if (two) c[j] = across<T>(ld_shared16(row + a), ld_shared16(row + b), off);
+        else c[j] = ld_keep_l2_16(row + a);
     }
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-        const int at = i + j * step;
-        if (at >= least && at <= most) c[j] = across<T>(a[j], ld_shared16(row + (int64_t)at * E - off + 16), off);
-        else c[j] = edge_chunk<T>(row, at, vocab);
+        const int i = first + j * 32 * V + lane * V;
+        if (j < used && i + V > vocab) mask_chunk<T>(c[j], i, vocab);
     }
+    if ((there.before || !two) && (there.behind || (!two && vocab % V == 0))) return;
+#pragma unroll 1
+    for (int k = there.before || !two ? 2 - two : 0; k < (there.behind ? 1 : 3); ++k) {   // the first, the last but one, the last
+        const int i = k == 0 ? 0 : ((vocab - 1) / V - (2 - k)) * V;
+        const int mine = i - first - lane * V;
+        if (i < 0 || mine < 0 || mine % (32 * V) != 0) continue;
+        const Chunk e = edge_chunk<T>(row, i, vocab);
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (mine == j * 32 * V) c[j] = e;
+    }
+    __syncwarp();
 }
 
 // The largest element of the chunks (a NaN is passed over).
@@ -239,6 +345,25 @@ __device__ __forceinline__ void merge_lists(uint64_t (*lists)[32], int many, int
     }
 }
 
+// What a row's units come to.
+struct RowSums {
+    float m, log, entropy;
+    bool none;   // every logit masked
+};
+template <bool ENT>
+__device__ __forceinline__ RowSums sum_units(const float *units, const LogprobParams &p, int lane) {
+    float most = neg_inf();
+    for (int u = lane; u < p.units; u += 32) most = fmaxf(most, units[u]);
+    Part a = {warp_max(most), 0.f, 0.f};
+    for (int u = lane; u < p.units; u += 32)
+        add_part(a, Part{units[u], units[p.units + u], ENT ? units[2 * p.units + u] : 0.f}, p.c);
+    a.s = butterfly_sum<32>(a.s);
+    if (ENT) a.t = butterfly_sum<32>(a.t);
+    const bool none = a.m == neg_inf() && a.s == 0.f;
+    const float log = none ? neg_inf() : logf(a.s);
+    return RowSums{a.m, log, !ENT || none ? 0.f : log - kLn2 * a.t / a.s, none};
+}
+
 // The `top`-th largest of 32 values (equal ones in their order), lane i's being
 // the i-th.
 template <typename V>
@@ -263,13 +388,14 @@ __device__ __forceinline__ void row_barrier(int slot, int warps) {
 }
 
 template <typename T, bool ALIGNED, bool ENT, bool TOP>
-__global__ void __launch_bounds__(kLpThreads, ALIGNED ? 4 : 3) logprobs_fwd_kernel(const LogprobParams p) {
+__global__ void __launch_bounds__(kLpThreads, 4) logprobs_fwd_kernel(const LogprobParams p) {
     constexpr int V = T::kVec, U = 16 / V;
     extern __shared__ float parts[];   // each row's units: maxima, sums, sums of z exp(z)
     __shared__ __align__(16) float maxima[kLpWarps][32];
     __shared__ __align__(16) uint64_t lists[kLpWarps][32], others[kClusterMaxCtas][32];
     __shared__ int flagged_count[kLpWarps], gathered_count[kLpWarps], flagged[kLpThreads];
     __shared__ uint64_t gathered[TOP ? 2048 : 1];   // lp_room(warps) for each row
+    __shared__ RowSums row_sums[kLpWarps];
     const int tid = threadIdx.x, lane = tid & 31;
     const uint32_t rank = cluster_rank();
     const int blocks = (int)cluster_ctas();
@@ -279,6 +405,7 @@ __global__ void __launch_bounds__(kLpThreads, ALIGNED ? 4 : 3) logprobs_fwd_kern
     const bool there = r < p.rows;
     const char *row = p.logits + r * p.stride;
     const int off = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(row) & 15);
+    const Around space = around(p.logits, row, p.rows, p.stride);
     float *mine = parts + (int64_t)slot * 3 * p.units;
     // before a block writes to the first one's shared memory, that has started
     if (blocks > 1) asm volatile("barrier.cluster.arrive.release.aligned;" : : : "memory");
@@ -294,7 +421,7 @@ __global__ void __launch_bounds__(kLpThreads, ALIGNED ? 4 : 3) logprobs_fwd_kern
     float seen = neg_inf();   // the largest logit of this thread
     for (int unit = begin; unit < p.units; unit += step) {
         Chunk c[kLpChunks];
-        load_chunks<T, ALIGNED>(c, row, unit * lp_unit<T>() + lane * V, 32 * V, p.vocab, off);
+        load_unit<T, ALIGNED>(c, row, unit, lane, p.vocab, off, space);
         if (unit == 0 && (uint64_t)token < (uint64_t)p.vocab) given = widen_bits(ld_bits(row, token, T{}, 0), T{});
         const float local = chunks_max(c, T{});
         if (TOP) seen = fmaxf(seen, local);
@@ -345,11 +472,25 @@ __global__ void __launch_bounds__(kLpThreads, ALIGNED ? 4 : 3) logprobs_fwd_kern
         }
     }
     if (blocks > 1 && begin >= p.units) asm volatile("barrier.cluster.wait.acquire.aligned;" : : : "memory");
+    // The row that the next block on this SM is likely to take, its first units
+    // into L2: blocks end about together, and memory would idle while they do.
+    if (tid == 0 && r + p.ahead < p.rows && blocks == 1) {
+        const char *next = p.logits + (r + p.ahead) * p.stride;
+        const int64_t bytes = (int64_t)p.vocab * (16 / V), skip = 16 - ((reinterpret_cast<uintptr_t>(next) - 1) & 15) - 1;
+        const int64_t most = (bytes - skip) / 16 * 16;
+        if (most > 0) prefetch_l2(next + skip, (unsigned)(most < kLpAhead ? most : kLpAhead));
+    }
+    // the units' sums are added up by the row's last warp while others look for alternatives
+    const bool early = TOP && blocks == 1 && warps > 1;
     if (TOP) {
         // 32 groups of a row's threads: a lane's of every warp
         maxima[slot * warps + warp][lane] = seen;
         lists[slot * warps + warp][lane] = 0;
         __syncthreads();
+        if (early && warp == warps - 1 && there) {
+            const RowSums sums = sum_units<ENT>(mine, p, lane);
+            if (lane == 0) row_sums[slot] = sums;
+        }
         float of_group = neg_inf();
         for (int w = 0; w < warps; ++w) of_group = fmaxf(of_group, maxima[slot * warps + w][lane]);
         row_barrier(slot, warps);
@@ -382,7 +523,7 @@ __global__ void __launch_bounds__(kLpThreads, ALIGNED ? 4 : 3) logprobs_fwd_kern
                     }
                     if (at[u] < p.vocab) {
                         Chunk one[1];
-                        load_chunks<T, ALIGNED>(one, row, at[u], 0, p.vocab, off);
+                        load_chunks<T, ALIGNED>(one, row, at[u], 0, p.vocab, off, space);
                         c[u] = one[0];
                     }
                 }
@@ -484,25 +625,20 @@ __global__ void __launch_bounds__(kLpThreads, ALIGNED ? 4 : 3) logprobs_fwd_kern
     if (rank != 0) return;
     if (TOP && blocks > 1) merge_lists(others, blocks, warp, lane);   // the same in the block
     if (warp != 0 || !there) return;
-    float most = neg_inf();
-    for (int u = lane; u < p.units; u += 32) most = fmaxf(most, mine[u]);
-    Part a = {warp_max(most), 0.f, 0.f};
-    for (int u = lane; u < p.units; u += 32)
-        add_part(a, Part{mine[u], mine[p.units + u], ENT ? mine[2 * p.units + u] : 0.f}, p.c);
-    a.s = butterfly_sum<32>(a.s);
-    if (ENT) a.t = butterfly_sum<32>(a.t);
-    const bool none = a.m == neg_inf() && a.s == 0.f;   // every logit masked
-    const float log = none ? neg_inf() : logf(a.s);
+    const RowSums sums = early ? row_sums[slot] : sum_units<ENT>(mine, p, lane);
     if (lane == 0) {
         if (p.logprobs != nullptr)
-            p.logprobs[r] = (uint64_t)token >= (uint64_t)p.vocab ? 0.f : none ? neg_inf() : (given - a.m) * p.inv_t - log;
-        if (p.stats != nullptr) *reinterpret_cast<float2 *>(p.stats + 2 * r) = make_float2(a.m, log);
-        if (ENT) p.entropy[r] = none ? 0.f : log - kLn2 * a.t / a.s;
+            p.logprobs[r] = (uint64_t)token >= (uint64_t)p.vocab ? 0.f
+                            : sums.none                          ? neg_inf()
+                                                                 : (given - sums.m) * p.inv_t - sums.log;
+        if (p.stats != nullptr) *reinterpret_cast<float2 *>(p.stats + 2 * r) = make_float2(sums.m, sums.log);
+        if (ENT) p.entropy[r] = sums.entropy;
     }
     if (TOP && lane < p.top) {
         const uint64_t best = blocks > 1 ? others[0][lane] : lists[slot * warps][lane];
         p.top_ids[r * p.top + lane] = (int32_t) ~(uint32_t)best;
-        p.top_logprobs[r * p.top + lane] = none ? neg_inf() : (value_of((uint32_t)(best >> 32)) - a.m) * p.inv_t - log;
+        p.top_logprobs[r * p.top + lane] =
+            sums.none ? neg_inf() : (value_of((uint32_t)(best >> 32)) - sums.m) * p.inv_t - sums.log;
     }
 }
 
@@ -514,7 +650,7 @@ struct LogprobBwdParams {
     const float *stats, *dlogprobs, *entropy, *dentropy;
     char *dlogits;
     int64_t rows, stride, dstride;   // bytes
-    int32_t vocab, slices;           // blocks of a row
+    int32_t vocab, slices, turns;    // blocks of a row, and parts of it that each takes
     int32_t shift;                   // 2^shift threads of a row in a block: 32 .. 256
     int32_t wide;
     float inv_t, c;
@@ -526,7 +662,7 @@ constexpr int kLpBwdChunks = 4;
 // q = log2 p_v:  p (a + b q).  Chunks lie on dlogits' 16-byte boundaries
 // (ALIGNED: on both tensors').
 template <typename T, bool ALIGNED, bool ENT>
-__global__ void __launch_bounds__(kLpThreads, ALIGNED ? 6 : 4) logprobs_bwd_kernel(const LogprobBwdParams p) {
+__global__ void __launch_bounds__(kLpThreads, 4) logprobs_bwd_kernel(const LogprobBwdParams p) {
     constexpr int V = T::kVec, E = 16 / V;
     const uint32_t group = blockIdx.x / (uint32_t)p.slices;
     const int slice = (int)(blockIdx.x - group * p.slices);
@@ -538,68 +674,90 @@ __global__ void __launch_bounds__(kLpThreads, ALIGNED ? 6 : 4) logprobs_bwd_kern
     char *to = p.dlogits + r * p.dstride;
     const int head = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(to) & 15) / E;
     const int off = ALIGNED ? 0 : (int)((reinterpret_cast<uintptr_t>(row) - head * E) & 15);
+    const int step = V << p.shift, turn = kLpBwdChunks * step;
+    const int begin = slice * p.turns * turn - head;
+    const int place = ((int)threadIdx.x & ((1 << p.shift) - 1)) * V;
+    const Around space = around(p.logits, row, p.rows, p.stride);
+    // Chunks of a turn: all within the row, with what else is read (32 bytes), or some at its ends.
+    Chunk c[kLpBwdChunks];
+    auto whole = [&](int first) { return (ALIGNED || first > 0) && first + turn + (ALIGNED ? 0 : 2 * V) <= p.vocab; };
+    auto load = [&](int first) {
+        if (!whole(first)) {
+            load_chunks<T, ALIGNED>(c, row, first + place, step, p.vocab, off, space);
+            return;
+        }
+        const char *from = row + (int64_t)(first + place) * E - off;
+        if (ALIGNED || off == 0) {
+#pragma unroll
+            for (int j = 0; j < kLpBwdChunks; ++j) c[j] = ld_keep_l2_16(from + j * step * E);
+        } else {
+            uint4 a[kLpBwdChunks];
+#pragma unroll
+            for (int j = 0; j < kLpBwdChunks; ++j) a[j] = ld_shared16(from + j * step * E);
+#pragma unroll
+            for (int j = 0; j < kLpBwdChunks; ++j) c[j] = across<T>(a[j], ld_shared16(from + j * step * E + 16), off);
+        }
+    };
+    // The first turn's chunks come with the row's numbers, not behind them (bf16
+    // 8192 x 131072: 659 us, and 720 behind them).
+    load(begin);
     int token = -1;
     float g = 0.f, h = 0.f, own = 0.f;
     if (p.dlogprobs != nullptr) {
+        const float given = p.dlogprobs[r];
         const int64_t id = p.wide ? static_cast<const int64_t *>(p.tokens)[r]
                                   : (int64_t) static_cast<const int32_t *>(p.tokens)[r];
         if ((uint64_t)id < (uint64_t)p.vocab) {
             token = (int)id;
-            g = p.dlogprobs[r];
+            g = given;
         }
     }
-    if (ENT) h = p.dentropy[r];
+    if (ENT) {
+        h = p.dentropy[r];
+        own = p.entropy[r];
+    }
     const float2 stats = *reinterpret_cast<const float2 *>(p.stats + 2 * r);
-    if (ENT) own = h == 0.f ? 0.f : h * p.entropy[r];
+    own = h == 0.f ? 0.f : h * own;
     const bool zero = (g == 0.f && h == 0.f) || (stats.x == neg_inf() && stats.y == neg_inf());
-    const int step = V << p.shift;
-    const int first = slice * kLpBwdChunks * step + ((int)threadIdx.x & ((1 << p.shift) - 1)) * V - head;
-    if (zero) {   // nothing is read
-#pragma unroll
-        for (int j = 0; j < kLpBwdChunks; ++j) {
-            const int i = first + j * step;
-            if (i >= 0 && i + V <= p.vocab) {
-                st16(to + (int64_t)i * E, Chunk{});
-            } else {
-                for (int k = 0; k < V; ++k)
-                    if (i + k >= 0 && i + k < p.vocab) st_scalar(to, i + k, 0.f, T{});
-            }
-        }
-        return;
-    }
-    Chunk c[kLpBwdChunks];
-    load_chunks<T, ALIGNED>(c, row, first, step, p.vocab, off);
     const float2 less = make_float2(-stats.x, -stats.x), cc = make_float2(p.c, p.c);
     const float l = -stats.y * kLog2e, a = -(g + own) * p.inv_t, b = -h * p.inv_t * kLn2;
+    for (int first = begin, t = 0;;) {
+        const bool inside = whole(first);
 #pragma unroll
-    for (int j = 0; j < kLpBwdChunks; ++j) {
-        const int i = first + j * step;
-        if (i >= p.vocab) return;
-        float x[V];
-        unpack(c[j], x, T{});
+        for (int j = 0; j < kLpBwdChunks; ++j) {
+            const int i = first + place + j * step;
+            if (!inside && i >= p.vocab) break;
+            float x[V];
+            unpack(c[j], x, T{});
 #pragma unroll
-        for (int k = 0; k < V; k += 2) {
-            const float2 q = __ffma2_rn(__fadd2_rn(make_float2(x[k], x[k + 1]), less), cc, make_float2(l, l));
-            const float2 e = make_float2(ex2(q.x), ex2(q.y));
-            float2 d = make_float2(a, a);
-            if (ENT) d = __ffma2_rn(make_float2(b, b), make_float2(fmaxf(q.x, -1e4f), fmaxf(q.y, -1e4f)), d);
-            d = __fmul2_rn(e, d);
-            x[k] = d.x;
-            x[k + 1] = d.y;
+            for (int k = 0; k < V; k += 2) {
+                const float2 q = __ffma2_rn(__fadd2_rn(make_float2(x[k], x[k + 1]), less), cc, make_float2(l, l));
+                const float2 e = make_float2(ex2(q.x), ex2(q.y));
+                float2 d = make_float2(a, a);
+                if (ENT) d = __ffma2_rn(make_float2(b, b), make_float2(fmaxf(q.x, -1e4f), fmaxf(q.y, -1e4f)), d);
+                d = __fmul2_rn(e, d);
+                x[k] = d.x;
+                x[k + 1] = d.y;
+            }
+            const uint32_t at = (uint32_t)(token - i);
+            if (at < (uint32_t)V && token >= 0) {
+#pragma unroll
+                for (int k = 0; k < V; ++k)
+                    if (at == (uint32_t)k) x[k] += g * p.inv_t;
+            }
+            const Chunk out = zero ? Chunk{} : pack(x, T{});
+            if (inside || (i >= 0 && i + V <= p.vocab)) {
+                st16(to + (int64_t)i * E, out);
+            } else {
+                unpack(out, x, T{});
+#pragma unroll
+                for (int k = 0; k < V; ++k)
+                    if (i + k >= 0 && i + k < p.vocab) st_scalar(to, i + k, x[k], T{});
+            }
         }
-        const uint32_t at = (uint32_t)(token - i);
-        if (at < (uint32_t)V && token >= 0) {
-#pragma unroll
-            for (int k = 0; k < V; ++k)
-                if (at == (uint32_t)k) x[k] += g * p.inv_t;
-        }
-        if ((ALIGNED || i >= 0) && i + V <= p.vocab) {
-            st16(to + (int64_t)i * E, pack(x, T{}));
-        } else {
-#pragma unroll
-            for (int k = 0; k < V; ++k)
-                if (i + k >= 0 && i + k < p.vocab) st_scalar(to, i + k, x[k], T{});
-        }
+        first += turn;
+        if (++t == p.turns || first >= p.vocab) return;
+        if (!zero) load(first);   // rows that nothing reaches are not read on
     }
 }
 
