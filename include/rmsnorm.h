@@ -585,7 +585,7 @@ int rmsnorm_logprobs_fwd(const void *logits, const void *tokens, int token_bytes
  *   dlogits          [rows, vocab], rows dlogits_stride elements apart; may be
  *                    the logits (same stride)
  * Masked logits get 0 (but for a masked token's own g).  Rows with g = h = 0,
- * and rows of masked logits only, are zeros, and their logits are not read.
+ * and rows of masked logits only, are zeros, whatever else they hold.
  * Other arguments and limits as the forward.
  */
 int rmsnorm_logprobs_bwd(const void *logits, const void *tokens, int token_bytes, const float *stats,

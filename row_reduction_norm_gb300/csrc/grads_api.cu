@@ -12,9 +12,11 @@ namespace {
 using rrn::GradEntry;
 using rrn::GradTable;
 
-uint32_t blocks_of(const rmsnorm_grad_t &g) {
+// Parts of a tensor that `threads` threads take one of.
+uint32_t parts_of(const rmsnorm_grad_t &g, int threads) {
     const int64_t s = rrn::size_of(g.dtype);
-    return (uint32_t)rrn::div_up((int64_t)(reinterpret_cast<uintptr_t>(g.grad) & 15) + g.count * s, rrn::kGradBlock);
+    return (uint32_t)rrn::div_up((int64_t)(reinterpret_cast<uintptr_t>(g.grad) & 15) + g.count * s,
+                                 rrn::grad_part(threads));
 }
 
 int check_grads(const rmsnorm_grad_t *grads, int64_t n, bool clip, const float *norm, const void *workspace,
@@ -38,24 +40,27 @@ int check_grads(const rmsnorm_grad_t *grads, int64_t n, bool clip, const float *
 
 // One launch's entries, from tensor i on; returns the next one's.
 template <int CAP>
-int64_t fill(GradTable<CAP> *t, const rmsnorm_grad_t *grads, int64_t i, int64_t n) {
+int64_t fill(GradTable<CAP> *t, const rmsnorm_grad_t *grads, int64_t i, int64_t n, int threads) {
     t->n = 0;
-    t->blocks = 0;
+    t->parts = 0;
     for (; i < n && t->n < CAP; ++i) {
         const rmsnorm_grad_t &g = grads[i];
         if (g.count == 0) continue;
-        const uint32_t blocks = blocks_of(g);
-        if (t->n > 0 && blocks > (uint32_t)INT_MAX - t->blocks) break;
-        t->e[t->n++] = GradEntry{static_cast<const char *>(g.grad), static_cast<char *>(g.out), g.count, t->blocks,
+        const uint32_t parts = parts_of(g, threads);
+        if (t->n > 0 && parts > (uint32_t)INT_MAX - t->parts) break;
+        t->e[t->n++] = GradEntry{static_cast<const char *>(g.grad), static_cast<char *>(g.out), g.count, t->parts,
                                  g.dtype};
-        t->blocks += blocks;
+        t->parts += parts;
     }
     return i;
 }
 
+// Parts of 4 KB that one block takes, a warp each.
+constexpr int64_t kAloneParts = rrn::kGradAlone / 32;
+
 template <int CAP>
-int run(const rmsnorm_grad_t *grads, int64_t n, bool clip, float max_norm, float *norm, void *workspace,
-        rmsnorm_stream_t stream) {
+int run(const rmsnorm_grad_t *grads, int64_t n, int64_t small_parts, bool clip, float max_norm, float *norm,
+        void *workspace, rmsnorm_stream_t stream) {
     int dev = 0, sms = 0, resident = 0;
     int st = rrn::current_device_sms(&dev, &sms);
     if (st != RMSNORM_OK) return st;
@@ -67,31 +72,36 @@ int run(const rmsnorm_grad_t *grads, int64_t n, bool clip, float max_norm, float
     t.partial = static_cast<double *>(workspace);
     t.norm = norm;
     t.max_norm = max_norm;
+    t.clip = clip;
     void *argv[] = {&t};
+    if (n <= CAP && small_parts <= kAloneParts) {
+        fill(&t, grads, 0, n, 32);
+        return rrn::launch_kernel(reinterpret_cast<const void *>(&rrn::grad_alone_kernel<CAP>), dim3(1),
+                                  32 * (t.parts > 0 ? (int)t.parts : 1), 0, stream, argv);
+    }
     if ((st = rrn::resident_blocks(dev, squares, rrn::kGradThreads, 0, &resident)) != RMSNORM_OK) return st;
     // launches of the norm share the partial sums out
     int64_t launches = 0;
-    for (int64_t i = 0; i < n || launches == 0; ++launches) i = fill(&t, grads, i, n);
+    for (int64_t i = 0; i < n; ++launches) i = fill(&t, grads, i, n, rrn::kGradThreads);
     if (launches > rrn::kGradPartials) return RMSNORM_EUNSUPPORTED;
     int64_t most = rrn::kGradPartials / launches;
     if (most > (int64_t)sms * resident) most = (int64_t)sms * resident;
     t.slot = 0;
     for (int64_t i = 0, l = 0; l < launches; ++l) {
-        i = fill(&t, grads, i, n);
-        if (t.blocks == 0) continue;
-        const unsigned grid = (unsigned)(t.blocks < most ? t.blocks : most);
+        i = fill(&t, grads, i, n, rrn::kGradThreads);
+        if (t.parts == 0) continue;
+        const unsigned grid = (unsigned)(t.parts < most ? t.parts : most);
         if ((st = rrn::launch_kernel(squares, dim3(grid), rrn::kGradThreads, 0, stream, argv)) != RMSNORM_OK) return st;
         t.slot += (int32_t)grid;
     }
     t.sums = t.slot;
-    if (!clip || t.sums == 0) return rrn::launch_kernel(only, dim3(1), rrn::kGradThreads, 0, stream, argv);
+    if (!clip) return rrn::launch_kernel(only, dim3(1), 32, 0, stream, argv);
     if ((st = rrn::resident_blocks(dev, scale, rrn::kGradThreads, 0, &resident)) != RMSNORM_OK) return st;
     most = (int64_t)sms * resident;
-    t.write_norm = 1;
     for (int64_t i = 0, l = 0; l < launches; ++l) {
-        i = fill(&t, grads, i, n);
-        if (t.blocks == 0) continue;
-        const unsigned grid = (unsigned)(t.blocks < most ? t.blocks : most);
+        i = fill(&t, grads, i, n, rrn::kGradThreads);
+        if (t.parts == 0) continue;
+        const unsigned grid = (unsigned)(t.parts < most ? t.parts : most);
         if ((st = rrn::launch_kernel(scale, dim3(grid), rrn::kGradThreads, 0, stream, argv)) != RMSNORM_OK) return st;
     }
     return RMSNORM_OK;
@@ -101,8 +111,11 @@ int norm_and_clip(const rmsnorm_grad_t *grads, int64_t n, bool clip, float max_n
                   uint64_t workspace_bytes, rmsnorm_stream_t stream) {
     const int st = check_grads(grads, n, clip, norm, workspace, workspace_bytes);
     if (st != RMSNORM_OK) return st;
-    return n <= rrn::kGradSmall ? run<rrn::kGradSmall>(grads, n, clip, max_norm, norm, workspace, stream)
-                                : run<rrn::kGradMost>(grads, n, clip, max_norm, norm, workspace, stream);
+    int64_t parts = 0;
+    for (int64_t i = 0; i < n && parts <= kAloneParts; ++i)
+        if (grads[i].count > 0) parts += parts_of(grads[i], 32);
+    return n <= rrn::kGradSmall ? run<rrn::kGradSmall>(grads, n, parts, clip, max_norm, norm, workspace, stream)
+                                : run<rrn::kGradMost>(grads, n, parts, clip, max_norm, norm, workspace, stream);
 }
 
 }  // namespace

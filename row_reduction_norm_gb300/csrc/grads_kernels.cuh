@@ -1,28 +1,35 @@
 // grads_kernels.cuh -- the norm of many tensors together, and their clipping:
 // norm = sqrt(sum g^2), out = RN(g min(1, max_norm / norm)).
 //
-// Two launches over the same blocks of 32 KB: sums of squares, then the
-// scaling, whose blocks each add up the first launch's partial sums for
+// Two launches over the same parts of 32 KB, a block each: sums of squares, then
+// the scaling, whose blocks each add up the first launch's partial sums for
 // themselves (a few thousand bytes from L2) rather than wait for a launch in
 // between.  HBM bandwidth bounds both: every byte is read twice and written
-// once.  The scaling goes through the blocks from the last to the first: what
+// once.  The scaling goes through the parts from the last to the first: what
 // the norm read last is still in L2.
+//
+// Up to 128 KB are one launch of one block, in parts of 4 KB, a warp each, which
+// stay in registers between the two steps (20 x 1000 fp32: 4.3 us, and 6.0 in two
+// launches).
 //
 // The tensors' addresses travel as the launch's parameters (up to 32 KB of
 // them), so nothing is copied to the device beforehand and a captured call
 // replays by itself.
 #pragma once
 
-#include "rmsnorm_kernels.cuh"
+#include "rmsnorm_cluster.cuh"
 
 namespace rrn {
 
-constexpr int kGradThreads = 256, kGradWarps = kGradThreads / 32, kGradChunks = 8;
-constexpr int kGradBlock = kGradThreads * kGradChunks * 16;   // bytes of a block of elements
-constexpr int kGradPartials = 2048;                           // blocks of the norm's launches at most
+constexpr int kGradThreads = 256, kGradChunks = 8;
+constexpr int kGradPartials = 2048;                             // blocks of the norm's launches at most
+constexpr int kGradAlone = 1024;   // threads of the single block at most
 
-// A tensor of a launch: its blocks are first .. the next one's first - 1, cut at
-// multiples of 32 KB behind the 16-byte boundary at or before its start.
+// Bytes of a part that `threads` threads take.
+__host__ __device__ constexpr int grad_part(int threads) { return threads * kGradChunks * 16; }
+
+// A tensor of a launch: its parts are first .. the next one's first - 1, cut at
+// multiples of their size behind the 16-byte boundary at or before its start.
 struct GradEntry {
     const char *grad;
     char *out;
@@ -39,11 +46,11 @@ struct GradTable {
     double *partial;    // of this call, [kGradPartials]
     float *norm;
     int32_t n;          // entries here
-    uint32_t blocks;    // of elements, here
+    uint32_t parts;     // here
     int32_t slot;       // first partial sum of this launch
     int32_t sums;       // partial sums of the whole call
     float max_norm;
-    int32_t write_norm;
+    int32_t clip;       // the single block's launch: the tensors too, not the norm alone
     GradEntry e[CAP];
 };
 
@@ -87,15 +94,21 @@ __device__ __forceinline__ int64_t grad_head(const char *grad) {
     return (int64_t)((reinterpret_cast<uintptr_t>(grad) & 15) / (16 / T::kVec));
 }
 
-// Sum of the squares of the thread's chunks of a block, each element times
-// `scale` (a power of two) first.
-template <typename T>
-__device__ __forceinline__ float block_squares(const char *grad, int64_t count, uint32_t block, float scale) {
+// Thread t's chunks of a part that THREADS threads take, and the first one's place.
+template <typename T, int THREADS>
+__device__ __forceinline__ int64_t load_part(Chunk (&c)[kGradChunks], const GradEntry &e, uint32_t part, int t) {
     constexpr int V = T::kVec;
-    const int64_t first = ((int64_t)block * kGradThreads * kGradChunks + threadIdx.x) * V - grad_head<T>(grad);
-    Chunk c[kGradChunks];
+    const int64_t first = ((int64_t)part * THREADS * kGradChunks + t) * V - grad_head<T>(e.grad);
 #pragma unroll
-    for (int j = 0; j < kGradChunks; ++j) c[j] = grad_chunk<T>(grad, first + (int64_t)j * kGradThreads * V, count);
+    for (int j = 0; j < kGradChunks; ++j) c[j] = grad_chunk<T>(e.grad, first + (int64_t)j * THREADS * V, e.count);
+    return first;
+}
+
+// Sum of the squares of a thread's chunks, each element times `scale` (a power
+// of two) first.
+template <typename T>
+__device__ __forceinline__ float squares_of(const Chunk (&c)[kGradChunks], float scale) {
+    constexpr int V = T::kVec;
     float acc[V] = {};
 #pragma unroll
     for (int j = 0; j < kGradChunks; ++j) {
@@ -108,85 +121,123 @@ __device__ __forceinline__ float block_squares(const char *grad, int64_t count, 
     return tree_sum(acc);
 }
 
-__device__ __forceinline__ double warp_sum(double v) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+// A sum and what its roundings lost: fp32 pairs, since the device has two fp64
+// lanes an SM (a block's sum, root and quotient in fp64 by every thread took two
+// small launches from 5.3 to 7.1 us).
+struct Pair {
+    float sum, lost;
+};
+__device__ __forceinline__ void add(Pair &a, float v) {
+    const float s = a.sum + v, w = s - a.sum;
+    a.lost += (a.sum - (s - w)) + (v - w);
+    a.sum = s;
+}
+__device__ __forceinline__ double whole(const Pair &a) {
+    // an infinite sum has lost nothing that can be said
+    return isfinite(a.sum) ? (double)a.sum + (double)a.lost : (double)a.sum;
+}
+
+// The block's threads' pairs added up, for every thread.
+template <int WARPS>
+__device__ __forceinline__ Pair block_sum(Pair v, Pair (&sums)[WARPS]) {
+    auto lanes = [&](int width) {
+        for (int off = width / 2; off > 0; off >>= 1) {
+            const Pair w = {__shfl_xor_sync(0xffffffffu, v.sum, off), __shfl_xor_sync(0xffffffffu, v.lost, off)};
+            const float s = v.sum + w.sum, d = s - v.sum;
+            v.lost = (v.lost + w.lost) + ((v.sum - (s - d)) + (w.sum - d));
+            v.sum = s;
+        }
+    };
+    lanes(32);
+    __syncthreads();
+    if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = sums[threadIdx.x % WARPS];
+    lanes(WARPS);
+    v.sum = __shfl_sync(0xffffffffu, v.sum, 0);
+    v.lost = __shfl_sync(0xffffffffu, v.lost, 0);
     return v;
 }
 
-// The block's threads' values added up, for every thread.
-__device__ __forceinline__ double block_sum(double v, double (&part)[kGradWarps]) {
-    v = warp_sum(v);
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
-    __syncthreads();
-    double s = 0.;
-#pragma unroll
-    for (int w = 0; w < kGradWarps; ++w) s += part[w];
-    return s;
-}
-
-// Squares of all the blocks this one takes, as fp32 sums of 64 or fewer
-// squares, those added up in two parts (a sum and what its roundings lost).
-template <int CAP>
-__device__ __forceinline__ double grid_squares(const GradTable<CAP> &t, float scale, double back, double (&part)[kGradWarps]) {
-    float sum = 0.f, lost = 0.f;
-    for (uint32_t b = blockIdx.x; b < t.blocks; b += gridDim.x) {
-        const GradEntry &e = t.e[entry_of(t, b)];
-        const float v = e.dtype == 1 ? block_squares<BF16>(e.grad, e.count, b - e.first, scale)
-                                     : block_squares<F32>(e.grad, e.count, b - e.first, scale);
-        const float s = sum + v, w = s - sum;
-        lost += (sum - (s - w)) + (v - w);
-        sum = s;
+// All of a block's squares, for its first thread; `squares(scale)` gives a
+// thread's.  Those past fp32's range, above or below (2^-80: sums so small that
+// squares of 2^-126 count), once more, scaled by a power of two.  All threads of
+// a block see the same sum.
+template <int WARPS, typename F>
+__device__ __forceinline__ double block_squares(Pair (&sums)[WARPS], F squares) {
+    double back = 1.;
+    Pair s = block_sum(squares(1.f), sums);
+    if (!isfinite(s.sum) || s.sum < 0x1p-80f) {
+        const bool large = !isfinite(s.sum);
+        s = block_sum(squares(large ? 0x1p-80f : 0x1p80f), sums);
+        back = large ? 0x1p160 : 0x1p-160;
     }
-    // an infinite sum has lost nothing that can be said
-    const double both = isfinite(sum) ? (double)sum + (double)lost : (double)sum;
-    return block_sum(both, part) * back;
+    return threadIdx.x == 0 ? whole(s) * back : 0.;
 }
 
 template <int CAP>
 __global__ void __launch_bounds__(kGradThreads) grad_squares_kernel(const __grid_constant__ GradTable<CAP> t) {
-    __shared__ double part[kGradWarps];
+    __shared__ Pair sums[kGradThreads / 32];
+    const int hint = entry_of(t, blockIdx.x);   // (the parameters are there before the wait)
     pdl_wait_for_inputs();
     pdl_allow_dependents();
-    double s = grid_squares(t, 1.f, 1., part);
-    // Squares past fp32's range, above or below (2^-80: sums so small that
-    // squares of 2^-126 count): once more, scaled by a power of two.  All
-    // threads of a block see the same sum.
-    if (!(s <= 1.7e308) || isinf(s)) s = grid_squares(t, 0x1p-80f, 0x1p160, part);
-    else if (s < 0x1p-80) s = grid_squares(t, 0x1p80f, 0x1p-160, part);
+    const double s = block_squares(sums, [&](float scale) {
+        Pair sum = {0.f, 0.f};
+        for (uint32_t b = blockIdx.x; b < t.parts; b += gridDim.x) {   // fp32 sums of 64 or fewer squares
+            const GradEntry &e = t.e[b == blockIdx.x ? hint : entry_of(t, b)];
+            Chunk c[kGradChunks];
+            if (e.dtype == 1) {
+                load_part<BF16, kGradThreads>(c, e, b - e.first, threadIdx.x);
+                add(sum, squares_of<BF16>(c, scale));
+            } else {
+                load_part<F32, kGradThreads>(c, e, b - e.first, threadIdx.x);
+                add(sum, squares_of<F32>(c, scale));
+            }
+        }
+        return sum;
+    });
     if (threadIdx.x == 0) t.partial[t.slot + blockIdx.x] = s;
 }
 
-// The norm from the partial sums, the same in every block that asks.
+// The factor from a norm, for the block's other threads; its first thread calls.
 template <int CAP>
-__device__ __forceinline__ double norm_of(const GradTable<CAP> &t, double (&part)[kGradWarps]) {
+__device__ __forceinline__ float factor_of(const GradTable<CAP> &t, double norm) {
+    return norm <= (double)t.max_norm ? 1.f : (float)((double)t.max_norm / norm);
+}
+
+// The norm from the partial sums, by the block's first warp, in its lane 0.
+template <int CAP>
+__device__ __forceinline__ double norm_of(const GradTable<CAP> &t) {
+    constexpr int U = 8;
     double s = 0.;
-    for (int i = threadIdx.x; i < t.sums; i += kGradThreads) s += __ldcg(t.partial + i);
-    return sqrt(block_sum(s, part));
+    for (int i = threadIdx.x; i < t.sums; i += 32 * U) {
+        double v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = i + 32 * u < t.sums ? __ldcg(t.partial + i + 32 * u) : 0.;
+#pragma unroll
+        for (int u = 0; u < U; ++u) s += v[u];
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_down_sync(0xffffffffu, s, off);
+    return threadIdx.x == 0 ? sqrt(s) : 0.;
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kGradThreads) grad_norm_kernel(const __grid_constant__ GradTable<CAP> t) {
-    __shared__ double part[kGradWarps];
+__global__ void __launch_bounds__(32) grad_norm_kernel(const __grid_constant__ GradTable<CAP> t) {
     pdl_wait_for_inputs();
     pdl_allow_dependents();
-    const double norm = norm_of(t, part);
+    const double norm = norm_of(t);
     if (threadIdx.x == 0) *t.norm = (float)norm;
 }
 
-template <typename T>
-__device__ __forceinline__ void scale_block(const GradEntry &e, uint32_t block, float f) {
+// A thread's chunks of a part times the factor, to the tensor's out.
+template <typename T, int THREADS>
+__device__ __forceinline__ void store_part(const Chunk (&c)[kGradChunks], const GradEntry &e, int64_t first, float f) {
     constexpr int V = T::kVec, E = 16 / V;
-    const int64_t head = grad_head<T>(e.grad);
-    const int64_t first = ((int64_t)block * kGradThreads * kGradChunks + threadIdx.x) * V - head;
     const bool alike = ((reinterpret_cast<uintptr_t>(e.grad) ^ reinterpret_cast<uintptr_t>(e.out)) & 15) == 0;
-    Chunk c[kGradChunks];
-#pragma unroll
-    for (int j = 0; j < kGradChunks; ++j) c[j] = grad_chunk<T>(e.grad, first + (int64_t)j * kGradThreads * V, e.count);
 #pragma unroll
     for (int j = 0; j < kGradChunks; ++j) {
-        const int64_t i = first + (int64_t)j * kGradThreads * V;
+        const int64_t i = first + (int64_t)j * THREADS * V;
         float x[V];
         unpack(c[j], x, T{});
 #pragma unroll
@@ -201,21 +252,66 @@ __device__ __forceinline__ void scale_block(const GradEntry &e, uint32_t block, 
     }
 }
 
+// The parts from the last to the first.
 template <int CAP>
 __global__ void __launch_bounds__(kGradThreads) grad_scale_kernel(const __grid_constant__ GradTable<CAP> t) {
-    __shared__ double part[kGradWarps];
+    __shared__ float factor;
+    const int hint = entry_of(t, t.parts - 1 - blockIdx.x);
     pdl_wait_for_inputs();
     pdl_allow_dependents();
-    const double norm = norm_of(t, part);
-    if (t.write_norm && blockIdx.x == 0 && threadIdx.x == 0) *t.norm = (float)norm;
-    const float f = norm <= (double)t.max_norm ? 1.f : (float)((double)t.max_norm / norm);
-    for (uint32_t b = blockIdx.x; b < t.blocks; b += gridDim.x) {
-        const uint32_t block = t.blocks - 1 - b;
-        const GradEntry &e = t.e[entry_of(t, block)];
-        if (f == 1.f && e.out == e.grad) continue;
-        if (e.dtype == 1) scale_block<BF16>(e, block - e.first, f);
-        else scale_block<F32>(e, block - e.first, f);
+    if (threadIdx.x < 32) {
+        const double norm = norm_of(t);
+        if (threadIdx.x == 0) {
+            factor = factor_of(t, norm);
+            if (blockIdx.x == 0) *t.norm = (float)norm;
+        }
     }
+    __syncthreads();
+    const float f = factor;
+    for (uint32_t b = blockIdx.x; b < t.parts; b += gridDim.x) {
+        const uint32_t part = t.parts - 1 - b;
+        const GradEntry &e = t.e[b == blockIdx.x ? hint : entry_of(t, part)];
+        if (f == 1.f && e.out == e.grad) continue;
+        Chunk c[kGradChunks];
+        if (e.dtype == 1) {
+            const int64_t first = load_part<BF16, kGradThreads>(c, e, part - e.first, threadIdx.x);
+            store_part<BF16, kGradThreads>(c, e, first, f);
+        } else {
+            const int64_t first = load_part<F32, kGradThreads>(c, e, part - e.first, threadIdx.x);
+            store_part<F32, kGradThreads>(c, e, first, f);
+        }
+    }
+}
+
+// Both steps by one block, a part a warp.
+template <int CAP>
+__global__ void __launch_bounds__(kGradAlone, 1) grad_alone_kernel(const __grid_constant__ GradTable<CAP> t) {
+    __shared__ Pair sums[kGradAlone / 32];
+    __shared__ float factor;
+    const uint32_t part = threadIdx.x / 32;
+    const bool there = part < t.parts;
+    const GradEntry &e = t.e[there ? entry_of(t, part) : 0];
+    const bool bf16 = e.dtype == 1;
+    if (threadIdx.x < kGradAlone / 32) sums[threadIdx.x] = Pair{0.f, 0.f};   // the block may have fewer warps
+    pdl_wait_for_inputs();
+    pdl_allow_dependents();
+    Chunk c[kGradChunks] = {};
+    int64_t first = 0;
+    if (there) first = bf16 ? load_part<BF16, 32>(c, e, part - e.first, threadIdx.x % 32)
+                            : load_part<F32, 32>(c, e, part - e.first, threadIdx.x % 32);
+    const double s = block_squares(sums, [&](float scale) {
+        return Pair{bf16 ? squares_of<BF16>(c, scale) : squares_of<F32>(c, scale), 0.f};
+    });
+    if (threadIdx.x == 0) {
+        const double norm = sqrt(s);
+        *t.norm = (float)norm;
+        factor = factor_of(t, norm);
+    }
+    __syncthreads();
+    const float f = factor;
+    if (!t.clip || !there || (f == 1.f && e.out == e.grad)) return;
+    if (bf16) store_part<BF16, 32>(c, e, first, f);
+    else store_part<F32, 32>(c, e, first, f);
 }
 
 }  // namespace rrn
