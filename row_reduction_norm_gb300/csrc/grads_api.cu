@@ -114,8 +114,9 @@ int norm_and_clip(const rmsnorm_grad_t *grads, int64_t n, bool clip, float max_n
     int64_t parts = 0;
     for (int64_t i = 0; i < n && parts <= kAloneParts; ++i)
         if (grads[i].count > 0) parts += parts_of(grads[i], 32);
-    return n <= rrn::kGradSmall ? run<rrn::kGradSmall>(grads, n, parts, clip, max_norm, norm, workspace, stream)
-                                : run<rrn::kGradMost>(grads, n, parts, clip, max_norm, norm, workspace, stream);
+    if (n <= rrn::kGradSmall) return run<rrn::kGradSmall>(grads, n, parts, clip, max_norm, norm, workspace, stream);
+    if (n <= rrn::kGradSome) return run<rrn::kGradSome>(grads, n, parts, clip, max_norm, norm, workspace, stream);
+    return run<rrn::kGradMost>(grads, n, parts, clip, max_norm, norm, workspace, stream);
 }
 
 }  // namespace

@@ -38,8 +38,10 @@ struct GradEntry {
     int32_t dtype;
 };
 
-// Most tensors of a launch: 32,764 bytes of parameters.
-constexpr int kGradSmall = 40, kGradMost = 1020;
+// Tensors of a launch at most, 32,764 bytes of parameters.  Parameters cost host
+// time (two launches for 60 tensors: 8.8 us with room for 1020), so fewer tensors
+// are launched with room for fewer.
+constexpr int kGradSmall = 40, kGradSome = 160, kGradMost = 1020;
 
 template <int CAP>
 struct GradTable {

@@ -487,10 +487,6 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_fwd_kernel(const Logpr
         maxima[slot * warps + warp][lane] = seen;
         lists[slot * warps + warp][lane] = 0;
         __syncthreads();
-        if (early && warp == warps - 1 && there) {
-            const RowSums sums = sum_units<ENT>(mine, p, lane);
-            if (lane == 0) row_sums[slot] = sums;
-        }
         float of_group = neg_inf();
         for (int w = 0; w < warps; ++w) of_group = fmaxf(of_group, maxima[slot * warps + w][lane]);
         row_barrier(slot, warps);
@@ -507,6 +503,10 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_fwd_kernel(const Logpr
         // every chunk of the flagged threads, one a thread
         const int each = begin < p.units + warp ? (p.units - (int)rank * warps + step - 1) / step * kLpChunks : 0;
         const int many = flagged_count[slot] * each;
+        if (early && warp == warps - 1 && there) {
+            const RowSums sums = sum_units<ENT>(mine, p, lane);
+            if (lane == 0) row_sums[slot] = sums;
+        }
         int found;
         for (;;) {
             for (int i0 = warp * 32; i0 < many && *reinterpret_cast<volatile int *>(count) <= room; i0 += threads * U) {
@@ -623,9 +623,15 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_fwd_kernel(const Logpr
         __syncthreads();
     }
     if (rank != 0) return;
-    if (TOP && blocks > 1) merge_lists(others, blocks, warp, lane);   // the same in the block
+    if (TOP && blocks > 1) {
+        if (warp == kLpWarps - 1) {
+            const RowSums sums = sum_units<ENT>(mine, p, lane);
+            if (lane == 0) row_sums[slot] = sums;
+        }
+        merge_lists(others, blocks, warp, lane);   // (barriers of the block)
+    }
     if (warp != 0 || !there) return;
-    const RowSums sums = early ? row_sums[slot] : sum_units<ENT>(mine, p, lane);
+    const RowSums sums = TOP && warps > 1 ? row_sums[slot] : sum_units<ENT>(mine, p, lane);
     if (lane == 0) {
         if (p.logprobs != nullptr)
             p.logprobs[r] = (uint64_t)token >= (uint64_t)p.vocab ? 0.f
