@@ -758,6 +758,7 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor], tempera
     1 get 0.  -infinity masks a token; a row of nothing else has log
     probabilities of -infinity and an entropy of 0.  Equal logits are ordered by
     the lower id.  ``stats`` is what ``token_logprobs_backward`` starts from.
+    What is returned may share one allocation.
     """
     if stream is None and logits.is_cuda:
         r = (_fast or _bind_fast()).token_logprobs(logits, tokens, temperature, top, entropy)
@@ -843,7 +844,7 @@ def clip_grad_norm(grads: Sequence[Optional[torch.Tensor]], max_norm: float,
 
     ``grads`` is a list of contiguous bf16 and float32 tensors of one device
     (None entries are passed over), changed in place, or written to ``out``, a
-    tensor like each.  An infinite norm makes the factor 0, NaN everything NaN:
+    tensor like each; none may be written twice.  An infinite norm makes the factor 0, NaN everything NaN:
     a caller that skips such steps looks at the norm.  ``workspace`` is a CUDA
     uint8 tensor of ``rmsnorm_grad_norm_workspace_bytes()`` bytes (allocated
     when not given).

@@ -207,11 +207,20 @@ int rmsnorm_embedding_bwd(const void *dy, const void *tokens, int token_bytes, v
     p.zero_parts = (int32_t)rrn::div_up(width * sg, rrn::kZeroBytes);
     p.chunks = direct ? rrn::div_up(count, rrn::kSumWarps) : at.chunks;
     p.work_blocks = p.chunks * at.tiles;
-    // Zeros that are written while the tokens are sorted, as many bytes as that
-    // takes time for (12 us, and 4 for 65536 tokens more); the sums' blocks
-    // write the rest where no token is.
+    int dev = 0, sms = 0;
+    if ((st = rrn::current_device_sms(&dev, &sms)) != RMSNORM_OK) return st;
+    const void *sort = reinterpret_cast<const void *>(&rrn::embed_sort_kernel);
+    int cluster = sort_blocks(count);
+    if (!direct && cluster > rrn::kClusterMaxCtas &&
+        !large_cluster(dev, sort, rrn::sort_smem(rrn::kSortMaxBits, rrn::kSortWords)))
+        cluster = rrn::kClusterMaxCtas;
+    // Zeros that are written while the tokens are sorted, by as many clusters more
+    // as the device has SMs for, and as many bytes as the sort takes time for (12
+    // us, and 4 for 65536 tokens more); the sums' blocks write the rest where no
+    // token is.
+    const int more = direct || accumulate ? 0 : (sms - cluster) / cluster;
     const int64_t row_bytes = width * sg;
-    int64_t early = direct || accumulate ? 0 : (((int64_t)48 << 20) + count * 512) / row_bytes / 32 * 32;
+    int64_t early = more < 1 ? 0 : (((int64_t)48 << 20) + count * 512) / row_bytes / 32 * 32;
     if (early > vocab) early = vocab;
     p.first_word = (int32_t)rrn::div_up(early, 32);
     const int64_t blocks = p.work_blocks +
@@ -239,16 +248,9 @@ int rmsnorm_embedding_bwd(const void *dy, const void *tokens, int token_bytes, v
     q.zero_rows = early;
     q.row_bytes = (int32_t)row_bytes;
     q.zero_bytes = p.zero_bytes;
-    int dev = 0, sms = 0;
-    if ((st = rrn::current_device_sms(&dev, &sms)) != RMSNORM_OK) return st;
-    const void *sort = reinterpret_cast<const void *>(&rrn::embed_sort_kernel);
     if ((st = rrn::allow_smem(dev, sort)) != RMSNORM_OK) return st;
-    int cluster = sort_blocks(count);
-    if (cluster > rrn::kClusterMaxCtas && !large_cluster(dev, sort, rrn::sort_smem(rrn::kSortMaxBits, rrn::kSortWords)))
-        cluster = rrn::kClusterMaxCtas;
     void *sort_argv[] = {&q};
-    const int more = early > 0 ? (sms - cluster) / cluster : 0;   // clusters that write zeros
-    st = rrn::launch_kernel(sort, dim3((unsigned)(cluster * (1 + more))), rrn::kSortThreads, (size_t)rrn::sort_smem(q.bits, q.words),
+    st = rrn::launch_kernel(sort, dim3((unsigned)(cluster * (early > 0 ? 1 + more : 1))), rrn::kSortThreads, (size_t)rrn::sort_smem(q.bits, q.words),
                             stream, sort_argv, cluster);
     if (st != RMSNORM_OK) return st;
 

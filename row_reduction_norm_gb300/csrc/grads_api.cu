@@ -2,7 +2,10 @@
 // clipping (declared in include/rmsnorm.h): argument checks, the launches.
 #include <climits>
 #include <cmath>
+#include <cstddef>
 #include <cstring>
+#include <memory>
+#include <new>
 
 #include "grads_kernels.cuh"
 #include "launch_util.h"
@@ -34,6 +37,29 @@ int check_grads(const rmsnorm_grad_t *grads, int64_t n, bool clip, const float *
         if (g.grad == nullptr || !rrn::on_boundary(g.grad, s)) return RMSNORM_EINVAL;
         if (clip && (g.out == nullptr || !rrn::on_boundary(g.out, s))) return RMSNORM_EINVAL;
         if (g.count > (int64_t)1 << 44) return RMSNORM_EUNSUPPORTED;
+    }
+    return RMSNORM_OK;
+}
+
+// Whether two of the tensors have the same out: they would be scaled twice, or
+// once, as it comes.  A status.
+int distinct_outs(const rmsnorm_grad_t *grads, int64_t n) {
+    if (n <= 24) {
+        for (int64_t i = 1; i < n; ++i)
+            for (int64_t j = 0; j < i; ++j)
+                if (grads[i].out == grads[j].out && grads[i].count > 0 && grads[j].count > 0) return RMSNORM_EINVAL;
+        return RMSNORM_OK;
+    }
+    uint64_t room = 64;
+    while (room < 2 * (uint64_t)n) room *= 2;
+    const std::unique_ptr<const void *[]> seen(new (std::nothrow) const void *[room]());
+    if (seen == nullptr) return RMSNORM_EUNSUPPORTED;
+    for (int64_t i = 0; i < n; ++i) {
+        if (grads[i].count == 0) continue;
+        uint64_t at = (reinterpret_cast<uintptr_t>(grads[i].out) >> 4) * 0x9E3779B97F4A7C15u >> 20 & (room - 1);
+        for (; seen[at] != nullptr; at = (at + 1) & (room - 1))
+            if (seen[at] == grads[i].out) return RMSNORM_EINVAL;
+        seen[at] = grads[i].out;
     }
     return RMSNORM_OK;
 }
@@ -109,7 +135,8 @@ int run(const rmsnorm_grad_t *grads, int64_t n, int64_t small_parts, bool clip, 
 
 int norm_and_clip(const rmsnorm_grad_t *grads, int64_t n, bool clip, float max_norm, float *norm, void *workspace,
                   uint64_t workspace_bytes, rmsnorm_stream_t stream) {
-    const int st = check_grads(grads, n, clip, norm, workspace, workspace_bytes);
+    int st = check_grads(grads, n, clip, norm, workspace, workspace_bytes);
+    if (st == RMSNORM_OK && clip) st = distinct_outs(grads, n);
     if (st != RMSNORM_OK) return st;
     int64_t parts = 0;
     for (int64_t i = 0; i < n && parts <= kAloneParts; ++i)
