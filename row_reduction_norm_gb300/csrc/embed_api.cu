@@ -1,7 +1,6 @@
 // embed_api.cu -- entry points of the embedding lookup and its gradient
 // (declared in include/rmsnorm.h): argument checks, the choice of a kernel and
 // its grid, the launches.
-#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstring>
@@ -84,33 +83,6 @@ struct Layout {
         bytes = partial + 2 * chunks * tiles * rrn::kTile * 4;
     }
 };
-
-// Whether the device takes the sort as a cluster of more than the portable 8
-// blocks, which has to be allowed and needs as many SMs side by side (asked once
-// a device).
-bool large_cluster(int dev, const void *fn, size_t smem) {
-    static std::atomic<uint64_t> asked{0}, fits{0};
-    const uint64_t bit = (uint64_t)1 << (dev & 63);
-    if (!(asked.load() & bit)) {
-        cudaLaunchAttribute attr;
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = rrn::kSortBlocks;
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(rrn::kSortBlocks);
-        cfg.blockDim = dim3(rrn::kSortThreads);
-        cfg.dynamicSmemBytes = smem;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        int clusters = 0;
-        if (cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
-            cudaOccupancyMaxActiveClusters(&clusters, fn, &cfg) == cudaSuccess && clusters > 0)
-            fits.fetch_or(bit);
-        (void)cudaGetLastError();
-        asked.fetch_or(bit);
-    }
-    return fits.load() & bit;
-}
 
 // Blocks of the sorting cluster: one while its threads have at most two tokens
 // each, and 16 (whose barriers take 2000 cycles, not 800) from eight a thread on.
@@ -210,9 +182,11 @@ int rmsnorm_embedding_bwd(const void *dy, const void *tokens, int token_bytes, v
     int dev = 0, sms = 0;
     if ((st = rrn::current_device_sms(&dev, &sms)) != RMSNORM_OK) return st;
     const void *sort = reinterpret_cast<const void *>(&rrn::embed_sort_kernel);
+    if (!direct && (st = rrn::allow_smem(dev, sort)) != RMSNORM_OK) return st;
     int cluster = sort_blocks(count);
     if (!direct && cluster > rrn::kClusterMaxCtas &&
-        !large_cluster(dev, sort, rrn::sort_smem(rrn::kSortMaxBits, rrn::kSortWords)))
+        !rrn::large_cluster(dev, sort, rrn::kSortBlocks, rrn::kSortThreads,
+                            (size_t)rrn::sort_smem(rrn::kSortMaxBits, rrn::kSortWords)))
         cluster = rrn::kClusterMaxCtas;
     // Zeros that are written while the tokens are sorted, by as many clusters more
     // as the device has SMs for, and as many bytes as the sort takes time for (12
@@ -248,7 +222,6 @@ int rmsnorm_embedding_bwd(const void *dy, const void *tokens, int token_bytes, v
     q.zero_rows = early;
     q.row_bytes = (int32_t)row_bytes;
     q.zero_bytes = p.zero_bytes;
-    if ((st = rrn::allow_smem(dev, sort)) != RMSNORM_OK) return st;
     void *sort_argv[] = {&q};
     st = rrn::launch_kernel(sort, dim3((unsigned)(cluster * (early > 0 ? 1 + more : 1))), rrn::kSortThreads, (size_t)rrn::sort_smem(q.bits, q.words),
                             stream, sort_argv, cluster);

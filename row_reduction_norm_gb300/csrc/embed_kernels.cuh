@@ -347,6 +347,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const SortP
         }
         // the next pass reads what all blocks wrote, and writes where this
         // one's totals are
+        if (pass == p.passes - 1) return;
         if (blocks > 1) cluster_barrier();
         else __syncthreads();
     }

@@ -81,8 +81,9 @@ int64_t fill(GradTable<CAP> *t, const rmsnorm_grad_t *grads, int64_t i, int64_t 
     return i;
 }
 
-// Parts of 4 KB that one block takes, a warp each.
-constexpr int64_t kAloneParts = rrn::kGradAlone / 32;
+// Parts of 4 KB that one cluster takes, a warp each, of 8 blocks and of 16.
+constexpr int64_t kAloneParts = rrn::kClusterMaxCtas * rrn::kGradAlone / 32;
+constexpr int64_t kAloneMost = rrn::kGradAloneBlocks * rrn::kGradAlone / 32;
 
 template <int CAP>
 int run(const rmsnorm_grad_t *grads, int64_t n, int64_t small_parts, bool clip, float max_norm, float *norm,
@@ -100,10 +101,16 @@ int run(const rmsnorm_grad_t *grads, int64_t n, int64_t small_parts, bool clip, 
     t.max_norm = max_norm;
     t.clip = clip;
     void *argv[] = {&t};
-    if (n <= CAP && small_parts <= kAloneParts) {
+    const void *alone = reinterpret_cast<const void *>(&rrn::grad_alone_kernel<CAP>);
+    if (n <= CAP && small_parts <= kAloneMost &&
+        (small_parts <= kAloneParts ||
+         rrn::large_cluster(dev, alone, rrn::kGradAloneBlocks, rrn::kGradAlone, 0))) {
         fill(&t, grads, 0, n, 32);
-        return rrn::launch_kernel(reinterpret_cast<const void *>(&rrn::grad_alone_kernel<CAP>), dim3(1),
-                                  32 * (t.parts > 0 ? (int)t.parts : 1), 0, stream, argv);
+        int blocks = 1;
+        while (blocks < rrn::kGradAloneBlocks && t.parts > (uint32_t)(blocks * rrn::kGradAlone / 32)) blocks *= 2;
+        return rrn::launch_kernel(alone, dim3((unsigned)blocks),
+                                  blocks > 1 ? rrn::kGradAlone : 32 * (t.parts > 0 ? (int)t.parts : 1), 0, stream, argv,
+                                  blocks);
     }
     if ((st = rrn::resident_blocks(dev, squares, rrn::kGradThreads, 0, &resident)) != RMSNORM_OK) return st;
     // launches of the norm share the partial sums out
@@ -139,7 +146,7 @@ int norm_and_clip(const rmsnorm_grad_t *grads, int64_t n, bool clip, float max_n
     if (st == RMSNORM_OK && clip) st = distinct_outs(grads, n);
     if (st != RMSNORM_OK) return st;
     int64_t parts = 0;
-    for (int64_t i = 0; i < n && parts <= kAloneParts; ++i)
+    for (int64_t i = 0; i < n && parts <= kAloneMost; ++i)
         if (grads[i].count > 0) parts += parts_of(grads[i], 32);
     if (n <= rrn::kGradSmall) return run<rrn::kGradSmall>(grads, n, parts, clip, max_norm, norm, workspace, stream);
     if (n <= rrn::kGradSome) return run<rrn::kGradSome>(grads, n, parts, clip, max_norm, norm, workspace, stream);

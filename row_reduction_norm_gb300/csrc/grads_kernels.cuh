@@ -8,9 +8,9 @@
 // once.  The scaling goes through the parts from the last to the first: what
 // the norm read last is still in L2.
 //
-// Up to 128 KB are one launch of one block, in parts of 4 KB, a warp each, which
-// stay in registers between the two steps (20 x 1000 fp32: 4.3 us, and 6.0 in two
-// launches).
+// Up to 2 MB are one launch of one block, or one cluster, in parts of 4 KB, a warp
+// each, which stay in registers between the two steps; the blocks' sums meet in
+// distributed shared memory.
 //
 // The tensors' addresses travel as the launch's parameters (up to 32 KB of
 // them), so nothing is copied to the device beforehand and a captured call
@@ -23,7 +23,7 @@ namespace rrn {
 
 constexpr int kGradThreads = 256, kGradChunks = 8;
 constexpr int kGradPartials = 2048;                             // blocks of the norm's launches at most
-constexpr int kGradAlone = 1024;   // threads of the single block at most
+constexpr int kGradAlone = 1024, kGradAloneBlocks = 16;   // threads of a block of the single cluster, and blocks
 
 // Bytes of a part that `threads` threads take.
 __host__ __device__ constexpr int grad_part(int threads) { return threads * kGradChunks * 16; }
@@ -52,7 +52,7 @@ struct GradTable {
     int32_t slot;       // first partial sum of this launch
     int32_t sums;       // partial sums of the whole call
     float max_norm;
-    int32_t clip;       // the single block's launch: the tensors too, not the norm alone
+    int32_t clip;       // the single cluster's launch: the tensors too, not the norm alone
     GradEntry e[CAP];
 };
 
@@ -285,16 +285,27 @@ __global__ void __launch_bounds__(kGradThreads) grad_scale_kernel(const __grid_c
     }
 }
 
-// Both steps by one block, a part a warp.
+__device__ __forceinline__ void st_cluster_f64(const double *local, uint32_t rank, double v) {
+    const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(local));
+    uint32_t ra;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(a), "r"(rank));
+    asm volatile("st.shared::cluster.f64 [%0], %1;" : : "r"(ra), "d"(v) : "memory");
+}
+
+// Both steps by one cluster, a part a warp.
 template <int CAP>
 __global__ void __launch_bounds__(kGradAlone, 1) grad_alone_kernel(const __grid_constant__ GradTable<CAP> t) {
     __shared__ Pair sums[kGradAlone / 32];
+    __shared__ double of_block[kGradAloneBlocks];
     __shared__ float factor;
-    const uint32_t part = threadIdx.x / 32;
+    const uint32_t rank = cluster_rank(), blocks = cluster_ctas();
+    const uint32_t part = threadIdx.x / 32 * blocks + rank;
     const bool there = part < t.parts;
     const GradEntry &e = t.e[there ? entry_of(t, part) : 0];
     const bool bf16 = e.dtype == 1;
-    if (threadIdx.x < kGradAlone / 32) sums[threadIdx.x] = Pair{0.f, 0.f};   // the block may have fewer warps
+    if (threadIdx.x < kGradAlone / 32) sums[threadIdx.x] = Pair{0.f, 0.f};   // a block may have fewer warps
+    // before a block writes to another's shared memory, that has started
+    if (blocks > 1) asm volatile("barrier.cluster.arrive.release.aligned;" : : : "memory");
     pdl_wait_for_inputs();
     pdl_allow_dependents();
     Chunk c[kGradChunks] = {};
@@ -304,9 +315,20 @@ __global__ void __launch_bounds__(kGradAlone, 1) grad_alone_kernel(const __grid_
     const double s = block_squares(sums, [&](float scale) {
         return Pair{bf16 ? squares_of<BF16>(c, scale) : squares_of<F32>(c, scale), 0.f};
     });
+    if (blocks > 1) {
+        asm volatile("barrier.cluster.wait.acquire.aligned;" : : : "memory");
+        const double mine = __shfl_sync(0xffffffffu, s, 0);
+        if (threadIdx.x < blocks) st_cluster_f64(of_block + rank, threadIdx.x, mine);
+        __syncwarp();
+        cluster_barrier();
+    } else if (threadIdx.x == 0) {
+        of_block[0] = s;
+    }
     if (threadIdx.x == 0) {
-        const double norm = sqrt(s);
-        *t.norm = (float)norm;
+        double all = 0.;
+        for (uint32_t q = 0; q < blocks; ++q) all += of_block[q];
+        const double norm = sqrt(all);
+        if (rank == 0) *t.norm = (float)norm;
         factor = factor_of(t, norm);
     }
     __syncthreads();

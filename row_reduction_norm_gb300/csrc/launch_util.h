@@ -56,6 +56,11 @@ int allow_smem(int dev, const void *fn);
 // together with a kernel's static arrays, 1 KB of them at most.
 constexpr size_t kSmemUnasked = 47 * 1024;
 
+// Whether the device takes a kernel as a cluster of more than the portable 8
+// blocks, which has to be allowed and needs as many SMs side by side (asked once
+// a device and kernel; its dynamic shared memory allowed before).
+bool large_cluster(int dev, const void *fn, int blocks, int threads, size_t smem);
+
 // Sums of the columns of partial[rows0 + rows1][ld] into the I/O type: of the
 // first rows0 rows to out0, of the rest to out1 (nullable).  partial is 16-byte
 // aligned, ld a multiple of 4 (what stands past the cols columns of a row must

@@ -818,6 +818,35 @@ int allow_smem(int dev, const void *fn) {
     return RMSNORM_OK;
 }
 
+bool large_cluster(int dev, const void *fn, int blocks, int threads, size_t smem) {
+    struct Entry {
+        int dev;
+        const void *fn;
+        bool fits;
+    };
+    static Entry asked[kMaxDevices * 4];
+    static int used = 0;
+    std::lock_guard<std::mutex> lk(g_mu);
+    for (int i = 0; i < used; ++i)
+        if (asked[i].dev == dev && asked[i].fn == fn) return asked[i].fits;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)blocks;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    const bool fits = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                      cudaOccupancyMaxActiveClusters(&clusters, fn, &cfg) == cudaSuccess && clusters > 0;
+    (void)cudaGetLastError();
+    if (used < kMaxDevices * 4) asked[used++] = Entry{dev, fn, fits};
+    return fits;
+}
+
 }  // namespace rrn
 
 extern "C" {
