@@ -620,10 +620,10 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const SumParams
 // Without a sort: every block has all the ids in shared memory, a warp takes a
 // place and 256 columns.  The first place of an id adds its row up: the warp
 // finds the others by comparing 32 ids at a time, and adds their rows in their
-// order; of more than 16, eight warps take an eighth of the places each.  A
+// order; of more than 8, eight warps take an eighth of the places each.  A
 // block's places are far apart: common ids come early, and eight long rows in
 // one block would follow one another.
-constexpr int kDirectAlone = 16;
+constexpr int kDirectAlone = 8;
 
 template <typename T, typename TG, int P>
 __global__ void __launch_bounds__(kSumThreads) embed_direct_kernel(const SumParams p) {

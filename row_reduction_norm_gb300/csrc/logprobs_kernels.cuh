@@ -197,11 +197,24 @@ __device__ __forceinline__ void load_unit(Chunk (&c)[kLpChunks], const char *row
                                                   (there.behind || end * E + 16 - off <= vocab * E)));
     if (inside) {
         if (two) {
-            uint4 a[N];
+            // the second of memory's chunks is the next lane's first, or the first
+            // lane's next
+            Chunk a[N], last = {};
 #pragma unroll
-            for (int j = 0; j < N; ++j) a[j] = ld_shared16(from - off + j * STEP);
+            for (int j = 0; j < N; ++j) a[j] = ld_keep_l2_16(from - off + j * STEP);
+            if (lane == 31) last = ld_keep_l2_16(from - off + 16 + (N - 1) * STEP);
 #pragma unroll
-            for (int j = 0; j < N; ++j) c[j] = across<T>(a[j], ld_shared16(from - off + 16 + j * STEP), off);
+            for (int j = 0; j < N; ++j) {
+                Chunk b;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t give = j + 1 < N && lane == 0 ? a[j + 1 < N ? j + 1 : j].u[k] : a[j].u[k];
+                    b.u[k] = __shfl_sync(0xffffffffu, give, (lane + 1) & 31);
+                    if (j == N - 1 && lane == 31) b.u[k] = last.u[k];
+                }
+                c[j] = across<T>(make_uint4(a[j].u[0], a[j].u[1], a[j].u[2], a[j].u[3]),
+                                 make_uint4(b.u[0], b.u[1], b.u[2], b.u[3]), off);
+            }
         } else {
 #pragma unroll
             for (int j = 0; j < N; ++j) c[j] = ld_keep_l2_16(from + j * STEP);
