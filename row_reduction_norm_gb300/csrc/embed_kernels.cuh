@@ -400,10 +400,10 @@ __device__ __forceinline__ void write_row(const SumParams &p, uint32_t id, int t
     }
 }
 
-// Rows of dy on their way at once: 32 registers a lane.
-template <typename T>
+// Rows of dy on their way at once: 32 registers a lane, one at least a piece.
+template <typename T, int P>
 __host__ __device__ constexpr int rows_ahead() {
-    return 16 / elem_bytes<T>();
+    return elem_bytes<T>() == 2 && P > 1 ? 8 : 4;
 }
 
 // The lane's eight columns of U rows of dy, those of them below `n`.
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumParams 
     bool began = first_id != before;   // this run, here
     const bool goes_on = n > 0 && !(ends >> (n - 1) & 1);
     float sum[8] = {};
-    constexpr int U = rows_ahead<T>();
+    constexpr int U = rows_ahead<T, P>();
     RowsOf<T, P, U> rows;
     for (int j = 0; j < n; j += U) {
         rows.load(p, tile, lane, e.y, j, n);
@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const SumParams
 constexpr int kDirectAlone = 8;
 
 template <typename T, typename TG, int P>
-__global__ void __launch_bounds__(kSumThreads) embed_direct_kernel(const SumParams p) {
+__global__ void __launch_bounds__(kSumThreads, elem_bytes<T>() == 4 ? 4 : 1) embed_direct_kernel(const SumParams p) {
     __shared__ uint32_t ids[kDirect];
     __shared__ uint32_t list[kSumWarps][32];
     __shared__ float4 part[kSumWarps][64];
@@ -667,7 +667,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_direct_kernel(const SumPara
             n += __popc(same);
         }
     if (lane == 0) many[warp] = n;
-    constexpr int U = rows_ahead<T>();
+    constexpr int U = rows_ahead<T, P>();
     RowsOf<T, P, U> rows;
     auto add_list = [&](int of, float (&sum)[8]) {
         __syncwarp();

@@ -402,7 +402,7 @@ __device__ __forceinline__ void row_barrier(int slot, int warps) {
 
 template <typename T, bool ALIGNED, bool ENT, bool TOP>
 __global__ void __launch_bounds__(kLpThreads, 4) logprobs_fwd_kernel(const LogprobParams p) {
-    constexpr int V = T::kVec, U = 16 / V;
+    constexpr int V = T::kVec, U = 8 / V;
     extern __shared__ float parts[];   // each row's units: maxima, sums, sums of z exp(z)
     __shared__ __align__(16) float maxima[kLpWarps][32];
     __shared__ __align__(16) uint64_t lists[kLpWarps][32], others[kClusterMaxCtas][32];
@@ -516,6 +516,8 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_fwd_kernel(const Logpr
         // every chunk of the flagged threads, one a thread
         const int each = begin < p.units + warp ? (p.units - (int)rank * warps + step - 1) / step * kLpChunks : 0;
         const int many = flagged_count[slot] * each;
+        // i / each is the product's high word: exact while i < 2^18 and each <= 1024
+        const uint32_t inverse = each > 1 ? 0xffffffffu / (uint32_t)each + 1 : 0;
         if (early && warp == warps - 1 && there) {
             const RowSums sums = sum_units<ENT>(mine, p, lane);
             if (lane == 0) row_sums[slot] = sums;
@@ -530,7 +532,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_fwd_kernel(const Logpr
                     const int i = i0 + u * threads + lane;
                     at[u] = p.vocab;
                     if (i < many) {
-                        const int f = i / each, j = i - f * each, owner = flagged[slot * threads + f];
+                        const int f = (int)__umulhi((uint32_t)i, inverse), j = i - f * each, owner = flagged[slot * threads + f];
                         const int unit = (int)rank * warps + (owner >> 5) + j / kLpChunks * step;
                         if (unit < p.units) at[u] = unit * lp_unit<T>() + (j % kLpChunks * 32 + (owner & 31)) * V;
                     }
