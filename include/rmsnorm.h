@@ -1,6 +1,7 @@
 /*
  * rmsnorm.h -- C ABI of the GB300 (sm_103a) fused row-wise RMSNorm library
- * (with its LayerNorm and fused Q+K head-norm variants).
+ * (with its LayerNorm and fused Q+K head-norm variants, and the operators of a
+ * transformer that stand beside the norm and at the model's two ends).
  *
  * The operation (one row at a time, rows of a row-major [rows, hidden] tensor):
  *
@@ -532,9 +533,9 @@ int rmsnorm_embedding_fwd(const void *tokens, int token_bytes, const void *table
  *   workspace   DEVICE memory, 16-byte aligned, of at least
  *               rmsnorm_embedding_bwd_workspace_bytes(count, vocab, width)
  *               bytes, used by no one else until the call's work is done
- * The tokens are sorted (stably) and a row's terms added up in fp32 in an
- * order that follows from the tokens alone: no atomics on values, equal bits
- * from run to run.  count and vocab up to 2^30, width up to 65536 (else
+ * A row's terms are added up in fp32 in an order that follows from the tokens
+ * and the sizes alone: no atomics on values, equal bits from run to run.
+ * count and vocab up to 2^30, width up to 65536 (else
  * RMSNORM_EUNSUPPORTED).
  */
 int rmsnorm_embedding_bwd(const void *dy, const void *tokens, int token_bytes, void *dtable, int64_t count,

@@ -699,7 +699,7 @@ def embedding_backward(dout: torch.Tensor, tokens: torch.Tensor, vocab: int, sca
     ``out`` (dout's type, or float32; the last dimension contiguous, rows
     evenly strided) takes the gradient; with ``accumulate`` it is added to what
     ``out`` holds, and only rows of tokens that occur are touched.  Sums are
-    fp32 in an order that follows from the tokens alone.  ``workspace`` is a
+    fp32 in an order that follows from the tokens and the sizes alone.  ``workspace`` is a
     CUDA uint8 tensor of ``rmsnorm_embedding_bwd_workspace_bytes(tokens, vocab,
     width)`` bytes (allocated when not given).
     """

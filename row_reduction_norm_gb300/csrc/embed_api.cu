@@ -54,17 +54,27 @@ const void *sum_kernel(int dtype, int grad_dtype, int64_t p, bool direct) {
 
 const void *join_kernel(int grad_dtype, int64_t p) {
 #define JOIN(TG, P) reinterpret_cast<const void *>(&rrn::embed_join_kernel<rrn::TG, P>)
-    if (grad_dtype == RMSNORM_F32) return p == 8 ? JOIN(F32, 8) : p == 4 ? JOIN(F32, 4) : p == 2 ? JOIN(F32, 2) : JOIN(F32, 1);
+    if (grad_dtype == RMSNORM_F32)
+        return p == 8 ? JOIN(F32, 8) : p == 4 ? JOIN(F32, 4) : p == 2 ? JOIN(F32, 2) : JOIN(F32, 1);
     return p == 8 ? JOIN(BF16, 8) : p == 4 ? JOIN(BF16, 4) : p == 2 ? JOIN(BF16, 2) : JOIN(BF16, 1);
 #undef JOIN
 }
 
-// Sorted tokens of a warp: 32, or fewer where that leaves less than 8192 warps
-// (a wave of 54 an SM).
+// Sorted tokens of a warp: 32, or fewer where that leaves less than 2048 warps
+// (32 / this, us: bf16 65536 x 768 49.5 / 49.5, 16 tokens 52.8; 2000 x 1024 14.4 /
+// 11.6; 12000 x 256 15.4 / 14.3; 16384 x 4096 69.7 / 69.7, 8 tokens 80.4).
 int run_of(int64_t count, int64_t tiles) {
     int run = 32;
-    while (run > 4 && rrn::div_up(count, run) * tiles < 8192) run /= 2;
+    while (run > 4 && rrn::div_up(count, run) * tiles < 2048) run /= 2;
     return run;
+}
+
+// Whether tokens are added up without a sort: the work of that, every warp
+// comparing all ids, grows with the square of their number (without / with a
+// sort, us, table of 8192 rows: bf16 256 x 1024 6.1 / 9.3, 512 x 1024 9.5 / 9.4,
+// 1000 x 1024 14.2 / 9.8, 1000 x 4096 45.8 / 21.8; fp32 1000 x 256 8.4 / 9.4).
+bool direct_sums(int64_t count, int64_t tiles) {
+    return count <= rrn::kDirect && count * count * tiles <= 1 << 20;
 }
 
 // What the gradient's workspace holds, in bytes from its start.
@@ -85,7 +95,9 @@ struct Layout {
 };
 
 // Blocks of the sorting cluster: one while its threads have at most two tokens
-// each, and 16 (whose barriers take 2000 cycles, not 800) from eight a thread on.
+// each, and 16 (whose barriers take 2000 cycles, not 800) from eight a thread on
+// (8 / 16 blocks, us: bf16 12000 x 256 14.3 / 13.9, 16384 x 4096 69.8 / 72.3, 65536
+// x 768 65.5 / 52.8).
 int sort_blocks(int64_t count) {
     int n = 1;
     while (n < rrn::kClusterMaxCtas && count > 2 * rrn::kSortThreads * n) n *= 2;
@@ -102,7 +114,8 @@ int rmsnorm_embedding_fwd(const void *tokens, int token_bytes, const void *table
     if (st != RMSNORM_OK) return st;
     if (count == 0) return RMSNORM_OK;
     const int64_t s = rrn::size_of(dtype);
-    if (table == nullptr || y == nullptr || !rrn::on_boundary(table, s) || !rrn::on_boundary(y, s)) return RMSNORM_EINVAL;
+    if (table == nullptr || y == nullptr || !rrn::on_boundary(table, s) || !rrn::on_boundary(y, s))
+        return RMSNORM_EINVAL;
     int64_t bytes = common_bytes(width * s, table_stride * s, 16);
     while (!rrn::on_boundary(table, bytes) || !rrn::on_boundary(y, bytes)) bytes /= 2;
     rrn::EmbedParams p;
@@ -120,7 +133,9 @@ int rmsnorm_embedding_fwd(const void *tokens, int token_bytes, const void *table
     const int got = rrn::current_device_sms(&dev, &sms);
     if (got != RMSNORM_OK) return got;
     const int64_t all = count * p.pieces;
-    const bool one = all <= (int64_t)sms * rrn::kEmbedThreads * 4;
+    // a piece a thread, or four: one / four, us, bf16 rows of 4096: 8 rows 1.26 /
+    // 1.65, 64 1.32 / 1.64, 200 1.78 / 1.68, 2000 5.1 / 4.1, 16384 41 / 29
+    const bool one = all <= (int64_t)sms * rrn::kEmbedThreads * 2;
     const int64_t blocks = rrn::div_up(all, rrn::kEmbedThreads * (one ? 1 : 4));
     if (blocks > INT_MAX) return RMSNORM_EUNSUPPORTED;
     void *argv[] = {&p};
@@ -174,7 +189,7 @@ int rmsnorm_embedding_bwd(const void *dy, const void *tokens, int token_bytes, v
     p.zero_bytes = (int32_t)held;
     int64_t piece = bytes / s;
     while (piece * sg > held && held < 16) piece /= 2;
-    const bool direct = count <= rrn::kDirect;
+    const bool direct = direct_sums(count, at.tiles);
     p.words = (int32_t)at.words;
     p.zero_parts = (int32_t)rrn::div_up(width * sg, rrn::kZeroBytes);
     p.chunks = direct ? rrn::div_up(count, rrn::kSumWarps) : at.chunks;
@@ -191,7 +206,7 @@ int rmsnorm_embedding_bwd(const void *dy, const void *tokens, int token_bytes, v
     // Zeros that are written while the tokens are sorted, by as many clusters more
     // as the device has SMs for, and as many bytes as the sort takes time for (12
     // us, and 4 for 65536 tokens more); the sums' blocks write the rest where no
-    // token is.
+    // token is (bf16 16384 x 4096 75.1 -> 69.8 us, 2000 x 1024 14.3 -> 11.6).
     const int more = direct || accumulate ? 0 : (sms - cluster) / cluster;
     const int64_t row_bytes = width * sg;
     int64_t early = more < 1 ? 0 : (((int64_t)48 << 20) + count * 512) / row_bytes / 32 * 32;
@@ -223,8 +238,9 @@ int rmsnorm_embedding_bwd(const void *dy, const void *tokens, int token_bytes, v
     q.row_bytes = (int32_t)row_bytes;
     q.zero_bytes = p.zero_bytes;
     void *sort_argv[] = {&q};
-    st = rrn::launch_kernel(sort, dim3((unsigned)(cluster * (early > 0 ? 1 + more : 1))), rrn::kSortThreads, (size_t)rrn::sort_smem(q.bits, q.words),
-                            stream, sort_argv, cluster);
+    const int sort_blocks_all = cluster * (early > 0 ? 1 + more : 1);
+    st = rrn::launch_kernel(sort, dim3((unsigned)sort_blocks_all), rrn::kSortThreads,
+                            (size_t)rrn::sort_smem(q.bits, q.words), stream, sort_argv, cluster);
     if (st != RMSNORM_OK) return st;
 
     p.sorted = q.passes % 2 ? q.a : q.b;

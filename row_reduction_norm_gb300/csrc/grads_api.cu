@@ -81,7 +81,9 @@ int64_t fill(GradTable<CAP> *t, const rmsnorm_grad_t *grads, int64_t i, int64_t 
     return i;
 }
 
-// Parts of 4 KB that one cluster takes, a warp each, of 8 blocks and of 16.
+// Parts of 4 KB that one cluster takes, a warp each, of 8 blocks and of 16 (one
+// cluster / two launches, us, device and whole call: one tensor of 1000 2.7 / 5.9;
+// 1.6 MB in 20 6.3 and 6.4 / 5.4 and 9.7).
 constexpr int64_t kAloneParts = rrn::kClusterMaxCtas * rrn::kGradAlone / 32;
 constexpr int64_t kAloneMost = rrn::kGradAloneBlocks * rrn::kGradAlone / 32;
 

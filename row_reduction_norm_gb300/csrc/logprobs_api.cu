@@ -91,12 +91,17 @@ int rmsnorm_logprobs_fwd(const void *logits, const void *tokens, int token_bytes
     if ((st = rrn::current_device_sms(&dev, &sms)) != RMSNORM_OK) return st;
     // a warp a unit, up to the block's eight; short rows several a block, unless
     // there are few and alternatives to be found, which all warps take part in
-    p.warps = top > 0 && rows <= 2 * sms ? rrn::kLpWarps : 1;
+    // (one warp / eight, us, bf16 rows of 1000 with 5: 8 rows 6.1 / 4.6, 300 6.2 /
+    // 5.3, 600 6.4 / 6.2, 2000 7.5 / 19.7)
+    p.warps = top > 0 && rows <= 4 * sms ? rrn::kLpWarps : 1;
     while (p.warps < rrn::kLpWarps && p.warps < p.units) p.warps *= 2;
     const int64_t groups = rrn::div_up(rows, rrn::kLpWarps / p.warps);
-    // a row over as many blocks as give every SM one, while each of their warps has a unit
+    // a row over as many blocks as give every SM one, while each of their warps has
+    // a unit (alone / together, us, bf16: 8 x 131072 9.7 / 3.1, with 20 alternatives
+    // 17.1 / 6.7, 100 x 50264 5.9 / 5.0)
     int cluster = 1;
-    while (cluster < 8 && groups * cluster < sms && 2 * cluster * rrn::kLpWarps <= p.units + rrn::kLpWarps - 1) cluster *= 2;
+    while (cluster < 8 && groups * cluster < sms && 2 * cluster * rrn::kLpWarps <= p.units + rrn::kLpWarps - 1)
+        cluster *= 2;
     if (groups > INT_MAX / cluster) return RMSNORM_EUNSUPPORTED;
     const void *fn = forward_kernel(dtype, aligned, entropy != nullptr, top > 0);
     const size_t smem = (size_t)p.units * 12 * (rrn::kLpWarps / p.warps);
@@ -118,7 +123,8 @@ int rmsnorm_logprobs_bwd(const void *logits, const void *tokens, int token_bytes
     const int64_t s = rrn::size_of(dtype);
     if (dlogits == nullptr || !rrn::on_boundary(dlogits, s) || stats == nullptr || !rrn::on_boundary(stats, 8))
         return RMSNORM_EINVAL;
-    if ((dlogprobs != nullptr && tokens == nullptr) || (dentropy != nullptr && entropy == nullptr)) return RMSNORM_EINVAL;
+    if ((dlogprobs != nullptr && tokens == nullptr) || (dentropy != nullptr && entropy == nullptr))
+        return RMSNORM_EINVAL;
     const void *fp[] = {dlogprobs, entropy, dentropy};
     for (const void *q : fp)
         if (!rrn::on_boundary(q, 4)) return RMSNORM_EINVAL;

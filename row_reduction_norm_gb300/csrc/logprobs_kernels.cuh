@@ -21,6 +21,11 @@
 //
 // Gradient: elementwise, given the forward's statistics.  One read and one
 // write of every element; HBM bandwidth bounds both.
+//
+// bf16 8192 x 131072, 2.1 GB a tensor: forward 294 us (7.3 TB/s), gradient 618
+// (6.9); fp32 1001 x 50257, whose rows begin between the 16-byte boundaries,
+// with 5 alternatives: 39.9 (5.0), the alternatives' instructions and the waves'
+// end bound it; 8 rows of 131072 with 20 alternatives: 6.7, latency.
 #pragma once
 
 #include "rmsnorm_cluster.cuh"
@@ -187,8 +192,8 @@ __device__ __forceinline__ void load_chunks(Chunk (&c)[N], const char *row, int 
 // the others addresses are held within the tensor, what lies behind the row is
 // masked, and the chunks at the tensor's two ends are put together by themselves.
 template <typename T, bool ALIGNED>
-__device__ __forceinline__ void load_unit(Chunk (&c)[kLpChunks], const char *row, int unit, int lane, int vocab, int off,
-                                          Around there) {
+__device__ __forceinline__ void load_unit(Chunk (&c)[kLpChunks], const char *row, int unit, int lane, int vocab,
+                                          int off, Around there) {
     constexpr int V = T::kVec, E = 16 / V, N = kLpChunks, STEP = 32 * 16;   // bytes between a lane's chunks
     const bool two = !ALIGNED && off != 0;
     const int first = unit * lp_unit<T>(), end = first + lp_unit<T>();
@@ -243,8 +248,9 @@ __device__ __forceinline__ void load_unit(Chunk (&c)[kLpChunks], const char *row
         if (j < used && i + V > vocab) mask_chunk<T>(c[j], i, vocab);
     }
     if ((there.before || !two) && (there.behind || (!two && vocab % V == 0))) return;
+    // the first, the last but one, the last
 #pragma unroll 1
-    for (int k = there.before || !two ? 2 - two : 0; k < (there.behind ? 1 : 3); ++k) {   // the first, the last but one, the last
+    for (int k = there.before || !two ? 2 - two : 0; k < (there.behind ? 1 : 3); ++k) {
         const int i = k == 0 ? 0 : ((vocab - 1) / V - (2 - k)) * V;
         const int mine = i - first - lane * V;
         if (i < 0 || mine < 0 || mine % (32 * V) != 0) continue;
@@ -288,7 +294,9 @@ __device__ __forceinline__ float value_of(uint32_t o) {
     return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
 }
 
-__device__ __forceinline__ uint64_t key_of(float x, int place) { return (uint64_t)order_of(x) << 32 | (uint32_t)~place; }
+__device__ __forceinline__ uint64_t key_of(float x, int place) {
+    return (uint64_t)order_of(x) << 32 | (uint32_t)~place;
+}
 
 // Element k of the chunks.
 template <typename T, int N>
@@ -429,7 +437,8 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_fwd_kernel(const Logpr
     int64_t token = -1;
     float given = 0.f;
     if (there && rank == 0 && warp == 0 && p.logprobs != nullptr)
-        token = p.wide ? static_cast<const int64_t *>(p.tokens)[r] : (int64_t) static_cast<const int32_t *>(p.tokens)[r];
+        token = p.wide ? static_cast<const int64_t *>(p.tokens)[r]
+                       : (int64_t) static_cast<const int32_t *>(p.tokens)[r];
     const int step = blocks * warps, begin = there ? (int)rank * warps + warp : p.units;
     float seen = neg_inf();   // the largest logit of this thread
     for (int unit = begin; unit < p.units; unit += step) {
@@ -486,10 +495,11 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_fwd_kernel(const Logpr
     }
     if (blocks > 1 && begin >= p.units) asm volatile("barrier.cluster.wait.acquire.aligned;" : : : "memory");
     // The row that the next block on this SM is likely to take, its first units
-    // into L2: blocks end about together, and memory would idle while they do.
+    // into L2: blocks end about together, and memory would idle while they do
+    // (bf16 1191 x 105656 42.6 -> 41.2 us).
     if (tid == 0 && r + p.ahead < p.rows && blocks == 1) {
         const char *next = p.logits + (r + p.ahead) * p.stride;
-        const int64_t bytes = (int64_t)p.vocab * (16 / V), skip = 16 - ((reinterpret_cast<uintptr_t>(next) - 1) & 15) - 1;
+        const int64_t bytes = (int64_t)p.vocab * (16 / V), skip = -reinterpret_cast<uintptr_t>(next) & 15;
         const int64_t most = (bytes - skip) / 16 * 16;
         if (most > 0) prefetch_l2(next + skip, (unsigned)(most < kLpAhead ? most : kLpAhead));
     }
@@ -532,7 +542,8 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_fwd_kernel(const Logpr
                     const int i = i0 + u * threads + lane;
                     at[u] = p.vocab;
                     if (i < many) {
-                        const int f = (int)__umulhi((uint32_t)i, inverse), j = i - f * each, owner = flagged[slot * threads + f];
+                        const int f = (int)__umulhi((uint32_t)i, inverse), j = i - f * each;
+                        const int owner = flagged[slot * threads + f];
                         const int unit = (int)rank * warps + (owner >> 5) + j / kLpChunks * step;
                         if (unit < p.units) at[u] = unit * lp_unit<T>() + (j % kLpChunks * 32 + (owner & 31)) * V;
                     }

@@ -73,3 +73,14 @@ def test_the_same_ids_in_both_ways_of_adding_up():
     ids[-1] = -1
     dout = torch.randint(-8, 9, (1025, width), device=DEV, generator=g).float()
     assert torch.equal(R.embedding_backward(dout, ids, vocab), R.embedding_backward(dout[:-1], ids[:-1], vocab))
+
+
+@pytest.mark.parametrize("n,width", [(1024, 256), (1025, 256), (724, 512), (725, 512), (512, 1024), (513, 1000), (129, 16384),
+                                     (64, 65536), (65, 65530)])
+def test_few_tokens_of_wide_rows(n, width):
+    """Both sides of where the sort begins, which is earlier the wider the rows: whole numbers, the exact sums."""
+    g, vocab = gen(n), 40
+    ids = some_ids(g, n, vocab)
+    dout = torch.randint(-4, 5, (n, width), device=DEV, generator=g).to(BF)
+    d = R.embedding_backward(dout, ids, vocab, out=torch.empty(vocab, width, device=DEV))
+    assert torch.equal(d.double(), ref.embedding_backward(dout, ids, vocab, 1.0)[0])
