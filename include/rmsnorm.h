@@ -617,9 +617,9 @@ typedef struct {
  * rmsnorm_grad_norm writes the norm alone (`out` is not looked at);
  * rmsnorm_clip_grads the tensors too, of which those with out == grad are not
  * touched when the factor is 1; two tensors with the same out are
- * RMSNORM_EINVAL (other overlaps are undefined).  Squares beyond fp32's range do not over- or
- * underflow the norm (blocks of elements that hold such are added up again,
- * scaled).  An infinite norm has the factor 0 (finite elements become 0,
+ * RMSNORM_EINVAL (other overlaps are undefined).  Squares beyond fp32's range
+ * do not over- or underflow the norm (blocks of elements that hold such are
+ * added up again, scaled).  An infinite norm has the factor 0 (finite elements become 0,
  * infinite ones NaN), a NaN makes the norm and every element NaN.  Sums are
  * formed in an order that follows from the sizes, the alignment and the
  * device alone (no atomics).  n == 0 writes a norm of 0.

@@ -699,9 +699,10 @@ def embedding_backward(dout: torch.Tensor, tokens: torch.Tensor, vocab: int, sca
     ``out`` (dout's type, or float32; the last dimension contiguous, rows
     evenly strided) takes the gradient; with ``accumulate`` it is added to what
     ``out`` holds, and only rows of tokens that occur are touched.  Sums are
-    fp32 in an order that follows from the tokens and the sizes alone.  ``workspace`` is a
-    CUDA uint8 tensor of ``rmsnorm_embedding_bwd_workspace_bytes(tokens, vocab,
-    width)`` bytes (allocated when not given).
+    fp32 in an order that follows from the tokens and the sizes alone.
+    ``workspace`` is a CUDA uint8 tensor of
+    ``rmsnorm_embedding_bwd_workspace_bytes(tokens, vocab, width)`` bytes
+    (allocated when not given).
     """
     if stream is None and dout.is_cuda:
         r = (_fast or _bind_fast()).embedding_backward(dout, tokens, vocab, scale, out, accumulate, workspace)
@@ -844,10 +845,10 @@ def clip_grad_norm(grads: Sequence[Optional[torch.Tensor]], max_norm: float,
 
     ``grads`` is a list of contiguous bf16 and float32 tensors of one device
     (None entries are passed over), changed in place, or written to ``out``, a
-    tensor like each; none may be written twice.  An infinite norm makes the factor 0, NaN everything NaN:
-    a caller that skips such steps looks at the norm.  ``workspace`` is a CUDA
-    uint8 tensor of ``rmsnorm_grad_norm_workspace_bytes()`` bytes (allocated
-    when not given).
+    tensor like each; none may be written twice.  An infinite norm makes the
+    factor 0, NaN everything NaN: a caller that skips such steps looks at the
+    norm.  ``workspace`` is a CUDA uint8 tensor of
+    ``rmsnorm_grad_norm_workspace_bytes()`` bytes (allocated when not given).
     """
     return _norm_or_clip(grads, max_norm, out, workspace, stream)
 
