@@ -283,3 +283,15 @@ def test_refusals_of_python_calls():
     for t in (0.0, -1.0, float("nan")):
         with pytest.raises(R.RmsNormError):
             R.token_logprobs(x, ids, t)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("vocab,top", [(50000, 20), (131072, 32), (1 << 20, 13)])
+def test_more_candidates_than_there_is_room_for(vocab, top, dtype):
+    """Groups of threads that see no large logit leave a bound that most of the others' reach: rising, falling, in any order."""
+    g = gen(vocab + top)
+    i = torch.arange(vocab, device=DEV)
+    few = (i // (8 if dtype is BF else 4)) % 32 >= top - 1          # the lanes without
+    logits = torch.stack([torch.where(few, -1.0, x) for x in (i * 1e-4, (vocab - i) * 1e-4, normal(g, vocab).abs(),
+                                                              (i * 7919 % vocab) * 1e-4)]).to(dtype)
+    check(logits, torch.randint(0, vocab, (4,), device=DEV, generator=g), 1.0, top)
