@@ -60,19 +60,21 @@ const void *join_kernel(int grad_dtype, int64_t p) {
 #undef JOIN
 }
 
-// Sorted tokens of a warp: 32, or fewer where that leaves less than 2048 warps
-// (32 / this, us: bf16 65536 x 768 49.5 / 49.5, 16 tokens 52.8; 2000 x 1024 14.4 /
-// 11.6; 12000 x 256 15.4 / 14.3; 16384 x 4096 69.7 / 69.7, 8 tokens 80.4).
+// Sorted tokens of a warp: as many, from 4 to 64, as make one wave of blocks,
+// three on each of the device's 152 SMs; with more than that to do, 32 (us, bf16
+// 65536 x 768: 54, one wave, 46.0, 32 49.5, 16 52.8; 16384 x 4096: 36, two waves,
+// 70.7, 32 69.7, 8 80.4; 2000 x 1024: 4 11.3, 32 14.4).  (A constant for the SMs:
+// the workspace's size and the order of the sums follow from the sizes alone.)
 int run_of(int64_t count, int64_t tiles) {
-    int run = 32;
-    while (run > 4 && rrn::div_up(count, run) * tiles < 2048) run /= 2;
-    return run;
+    constexpr int64_t wave = 3 * 152, least = 4, most = 64, many = 32;
+    const int64_t run = rrn::div_up(count, rrn::kSumWarps * (wave / tiles));
+    return (int)(run < least ? least : run > most ? many : run);
 }
 
 // Whether tokens are added up without a sort: the work of that, every warp
 // comparing all ids, grows with the square of their number (without / with a
 // sort, us, table of 8192 rows: bf16 256 x 1024 6.1 / 9.3, 512 x 1024 9.5 / 9.4,
-// 1000 x 1024 14.2 / 9.8, 1000 x 4096 45.8 / 21.8; fp32 1000 x 256 8.4 / 9.4).
+// 1000 x 1024 14.2 / 9.8, 1000 x 4096 45.8 / 20.8; fp32 1000 x 256 8.4 / 9.4).
 bool direct_sums(int64_t count, int64_t tiles) {
     return count <= rrn::kDirect && count * count * tiles <= 1 << 20;
 }
@@ -206,7 +208,7 @@ int rmsnorm_embedding_bwd(const void *dy, const void *tokens, int token_bytes, v
     // Zeros that are written while the tokens are sorted, by as many clusters more
     // as the device has SMs for, and as many bytes as the sort takes time for (12
     // us, and 4 for 65536 tokens more); the sums' blocks write the rest where no
-    // token is (bf16 16384 x 4096 75.1 -> 69.8 us, 2000 x 1024 14.3 -> 11.6).
+    // token is (bf16 16384 x 4096 75.1 -> 69.8 us, 5000 x 1024 17.7 -> 14.6).
     const int more = direct || accumulate ? 0 : (sms - cluster) / cluster;
     const int64_t row_bytes = width * sg;
     int64_t early = more < 1 ? 0 : (((int64_t)48 << 20) + count * 512) / row_bytes / 32 * 32;

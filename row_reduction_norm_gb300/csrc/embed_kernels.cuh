@@ -372,7 +372,7 @@ struct SumParams {
     int64_t vocab;
     int64_t chunks, work_blocks;       // of the sums; the blocks behind them write zeros
     int32_t count, width, tiles;
-    int32_t run;                       // sorted tokens of a warp; 8 times that are a chunk
+    int32_t run;                       // sorted tokens of a warp, up to 64; 8 times that are a chunk
     int32_t words, zero_parts;         // 32 rows x 512 bytes each a warp
     int32_t first_word;                // those before are written already
     float scale;
@@ -450,10 +450,10 @@ __device__ __forceinline__ void zero_item(const SumParams &p, int64_t word, int 
 // dy, the next U of them on their way.  A run of equal ids within a warp's part
 // is written out; parts of runs that cross warps meet in shared memory, and
 // those that cross chunks in the workspace, where embed_join_kernel adds them
-// up.  HBM bounds it (with the sort, bf16: 16384 x 4096 onto 50264 rows 104 us, 668
-// MB at 6.4 TB/s) until rows are short and many: 65536 x 768 fp32 onto 50257 rows
-// 50 us, of which the sort 17.  Slots 2 c and 2 c + 1 of the workspace: the part of a run that chunk c
-// did not begin, and of one that it did.
+// up.  HBM bounds it (with the sort, bf16 16384 x 4096 onto fp32 32768 rows 104
+// us, 668 MB at 6.4 TB/s) until rows are short and many: 65536 x 768 onto bf16
+// 50257 rows 47 us, of which the sort 17.  Slots 2 c and 2 c + 1 of the workspace:
+// the part of a run that chunk c did not begin, and of one that it did.
 
 __device__ __forceinline__ float4 *partial_slot(const SumParams &p, int64_t slot, int tile, int lane) {
     return reinterpret_cast<float4 *>(p.partial + (slot * p.tiles + tile) * kTile) + lane;
@@ -484,39 +484,53 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumParams 
     const int tile = (int)(blockIdx.x - chunk * p.tiles);
     const int64_t first = (chunk * kSumWarps + warp) * p.run;
     const uint32_t none = (uint32_t)p.vocab;
-    const bool mine = lane < p.run && first + lane < p.count;
-    const uint2 e = mine ? p.sorted[first + lane] : make_uint2(none, 0);
+    auto token = [&](int i) {
+        return i < p.run && first + i < p.count ? p.sorted[first + i] : make_uint2(none, 0);
+    };
+    uint2 e = token(lane);
+    const uint2 second = token(32 + lane);   // a warp has up to 64
     const uint32_t before = first > 0 && first <= p.count ? p.sorted[first - 1].x : ~0u;
     const uint32_t behind = first + p.run < p.count ? p.sorted[first + p.run].x : none;
-    uint32_t next = __shfl_down_sync(0xffffffffu, e.x, 1);
-    if (lane == p.run - 1) next = behind;
-    const uint32_t ends = __ballot_sync(0xffffffffu, e.x < none && e.x != next);
-    const int n = __popc(__ballot_sync(0xffffffffu, e.x < none));   // valid ones come first
     const uint32_t first_id = __shfl_sync(0xffffffffu, e.x, 0);
     bool began = first_id != before;   // this run, here
-    const bool goes_on = n > 0 && !(ends >> (n - 1) & 1);
+    bool goes_on = false, ended = false;
+    uint32_t last_id = none;
     float sum[8] = {};
     constexpr int U = rows_ahead<T, P>();
     RowsOf<T, P, U> rows;
-    for (int j = 0; j < n; j += U) {
-        rows.load(p, tile, lane, e.y, j, n);
+    for (int left = p.run;;) {
+        const uint32_t after = left > 32 ? __shfl_sync(0xffffffffu, second.x, 0) : behind;
+        uint32_t next = __shfl_down_sync(0xffffffffu, e.x, 1);
+        if (lane == (left < 32 ? left : 32) - 1) next = after;
+        const uint32_t ends = __ballot_sync(0xffffffffu, e.x < none && e.x != next);
+        const int n = __popc(__ballot_sync(0xffffffffu, e.x < none));   // valid ones come first
+        if (n == 0) break;
+        for (int j = 0; j < n; j += U) {
+            rows.load(p, tile, lane, e.y, j, n);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (j + u >= n) break;
-            rows.add(u, sum);
-            if (ends >> (j + u) & 1) {
-                const uint32_t id = __shfl_sync(0xffffffffu, e.x, j + u);
-                if (began) write_row<TG, P>(p, id, tile, lane, sum);
-                else put8(&head[warp][lane], sum);
-                began = true;
+            for (int u = 0; u < U; ++u) {
+                if (j + u >= n) break;
+                rows.add(u, sum);
+                if (ends >> (j + u) & 1) {
+                    const uint32_t id = __shfl_sync(0xffffffffu, e.x, j + u);
+                    if (began) write_row<TG, P>(p, id, tile, lane, sum);
+                    else put8(&head[warp][lane], sum);
+                    began = true;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) sum[k] = 0.f;
+                    for (int k = 0; k < 8; ++k) sum[k] = 0.f;
+                }
             }
         }
+        goes_on = !(ends >> (n - 1) & 1);
+        ended |= ends != 0;
+        last_id = __shfl_sync(0xffffffffu, e.x, n - 1);
+        left -= 32;
+        if (left <= 0) break;
+        e = second;
     }
     if (goes_on) put8(began ? &tail[warp][lane] : &head[warp][lane], sum);
     if (lane == 0) {
-        head_ends[warp] = ends != 0;
+        head_ends[warp] = ended;
         has_tail[warp] = goes_on && began;
     }
     __syncthreads();
@@ -530,7 +544,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumParams 
         if (ended && id != none) write_row<TG, P>(p, id, tile, lane, sum);
         else put8(partial_slot(p, slot, tile, lane), sum);
     };
-    if (warp == 0 && n > 0 && first_id == before) {
+    if (warp == 0 && first_id < none && first_id == before) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) sum[k] = 0.f;
         add8(head[0][lane], head[0][lane + 32], sum);
@@ -540,7 +554,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumParams 
 #pragma unroll
         for (int k = 0; k < 8; ++k) sum[k] = 0.f;
         add8(tail[warp][lane], tail[warp][lane + 32], sum);
-        follow(warp, __shfl_sync(0xffffffffu, e.x, n - 1), 2 * chunk + 1, false);
+        follow(warp, last_id, 2 * chunk + 1, false);
     }
 }
 

@@ -84,3 +84,14 @@ def test_few_tokens_of_wide_rows(n, width):
     dout = torch.randint(-4, 5, (n, width), device=DEV, generator=g).to(BF)
     d = R.embedding_backward(dout, ids, vocab, out=torch.empty(vocab, width, device=DEV))
     assert torch.equal(d.double(), ref.embedding_backward(dout, ids, vocab, 1.0)[0])
+
+
+@pytest.mark.parametrize("n", [15000, 29184, 29185, 60000, 116736, 233472, 240000])
+@pytest.mark.parametrize("vocab", [60, 20000])
+def test_shares_of_a_warp_from_a_few_tokens_to_64(n, vocab):
+    """Runs of an id that end in a warp's first 32 tokens, in its last ones, and go on: whole numbers, the exact sums."""
+    g, width = gen(n + vocab), 11
+    ids = torch.randint(-1, vocab, (n,), device=DEV, generator=g)
+    dout = torch.randint(-4, 5, (n, width), device=DEV, generator=g).to(BF)
+    d = R.embedding_backward(dout, ids, vocab, out=torch.empty(vocab, width, device=DEV))
+    assert torch.equal(d.double(), ref.embedding_backward(dout, ids, vocab, 1.0)[0])
