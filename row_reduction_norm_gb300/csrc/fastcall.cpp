@@ -1,6 +1,7 @@
 // fastcall.cpp -- the Python calls of the rotary, append, dropout, embedding,
-// log probability and clipping operators without Python's own cost: a CPython module that takes torch tensors, makes
-// the checks of api.py on them, and calls the C ABI on the current stream.
+// log probability and clipping operators without Python's own cost: a CPython
+// module that takes torch tensors, makes the checks of api.py on them, and calls
+// the C ABI on the current stream.
 //
 // These kernels take two microseconds for a decode step while the checks, the
 // argument conversion and the allocations of a call through Python objects and
