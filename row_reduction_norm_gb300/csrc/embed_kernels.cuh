@@ -141,11 +141,12 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_fwd_kernel(const EmbedPar
 // takes a run of consecutive places, so that counts per warp, summed over the
 // warps and blocks before it, say where its next token of a digit belongs.
 // Ids outside the table become `vocab`, which sorts behind all others.  Latency
-// bounds it, and 32 sectors a warp's scattered store: 16384 tokens of 32768 ids
-// take 12 us, 65536 of them 17 (28,000 cycles: 5,800 and 4,600 the two passes'
-// placing, 1,000 to 2,200 each of their four cluster barriers).  Blocks of 1024 or
-// 256 threads are slower (with the sums, us: bf16 1000 x 1024 13.7 and 11.3, 512
-// threads 9.8; 65536 x 768 47.2 and 51.8, 46.3).
+// bounds it: 16384 tokens of 32768 ids take 12 us, 65536 of them 17 (28,000
+// cycles: 5,800 and 4,600 the two passes' placing, 1,000 to 2,200 each of their
+// four cluster barriers).  Blocks of 1024 or 256 threads are slower (with the
+// sums, us: bf16 1000 x 1024 13.7 and 11.3, 512 threads 9.8; 65536 x 768 47.2 and
+// 51.8, 46.3), and so are tokens put in order in shared memory before they are
+// stored side by side (5000 x 1024 13.3, 13.0; 65536 x 768 50.0, 49.6).
 
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32, kSortMaxBits = 9;
 constexpr int kSortBlocks = 16, kSortSteps = 8;   // steps of 32 tokens that a warp holds in registers
