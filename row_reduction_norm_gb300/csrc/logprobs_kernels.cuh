@@ -28,6 +28,7 @@
 // end bound it; 8 rows of 131072 with 20 alternatives: 6.7, latency.
 #pragma once
 
+#include "key_search.h"
 #include "rmsnorm_cluster.cuh"
 
 namespace rrn {
@@ -516,7 +517,9 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_fwd_kernel(const Logpr
         if (warp == 0) maxima[slot * warps][lane] = of_group;
         row_barrier(slot, warps);
         const float bound = nth_largest(maxima[slot * warps], of_group, p.top, lane);
-        uint64_t least = (uint64_t)order_of(bound) << 32;
+        const bool lowest = bound == neg_inf();
+        KeySearch search;
+        search.start((uint64_t)order_of(bound) << 32);
         if (seen >= bound && begin < p.units)
             flagged[slot * warps * 32 + atomicAdd(flagged_count + slot, 1)] = warp * 32 + lane;   // in any order
         row_barrier(slot, warps);
@@ -561,16 +564,16 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_fwd_kernel(const Logpr
                     unpack(c[u], x, T{});
 #pragma unroll
                     for (int k = 0; k < V; ++k)
-                        if (!(x[k] < bound) && at[u] + k < p.vocab) these |= 1u << (u * V + k);
+                        if (reaches(x[k], bound, lowest) && at[u] + k < p.vocab) these |= 1u << (u * V + k);
                 }
-                if (least != (uint64_t)order_of(bound) << 32) {   // a bound that goes by places too
+                if (search.round > 0) {   // a bound that goes by places too
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
                         float x[V];
                         unpack(c[u], x, T{});
 #pragma unroll
                         for (int k = 0; k < V; ++k)
-                            if (key_of(x[k], at[u] + k) < least) these &= ~(1u << (u * V + k));
+                            if (key_of(x[k], at[u] + k) < search.least) these &= ~(1u << (u * V + k));
                     }
                 }
                 int place = __popc(these), all = place;
@@ -595,7 +598,8 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_fwd_kernel(const Logpr
             row_barrier(slot, warps);
             found = *count;
             const int held = found < room ? found : room;
-            if (found <= kLpFew) break;
+            const bool enough = search.enough(found, room, p.top);
+            if (enough && found <= kLpFew) break;
             // the bound that 32 groups of these give
             uint64_t best = 0;
             for (int i = lane; i < held; i += 32) best = best > keys[i] ? best : keys[i];
@@ -612,19 +616,18 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_fwd_kernel(const Logpr
             }
             row_barrier(slot, warps);
             const uint64_t higher = nth_largest(lists[slot * warps], best, p.top, lane);
-            const bool again = found > room;
-            if (!again)
+            if (enough)
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     if (kept[k] >= higher && kept[k] != 0) keys[atomicAdd(count, 1)] = kept[k];
             row_barrier(slot, warps);
             if (warp == 0) lists[slot * warps][lane] = 0;
-            if (!again) {
+            if (enough) {
                 found = *count;
                 row_barrier(slot, warps);
                 break;
             }
-            least = higher > least ? higher : least;
+            search.next(found, room, higher);
             row_barrier(slot, warps);
         }
         // their order, by counting the larger ones
