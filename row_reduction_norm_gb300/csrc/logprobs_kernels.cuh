@@ -537,7 +537,10 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_fwd_kernel(const Logpr
         }
         int found;
         for (;;) {
-            for (int i0 = warp * 32; i0 < many && *reinterpret_cast<volatile int *>(count) <= room; i0 += threads * U) {
+            for (int i0 = warp * 32; i0 < many; i0 += threads * U) {
+                // Other warps add to the count meanwhile: one lane's read of it
+                // decides for all, so that they stay together.
+                if (__shfl_sync(0xffffffffu, *reinterpret_cast<volatile int *>(count), 0) > room) break;
                 Chunk c[U];
                 int at[U];
 #pragma unroll
