@@ -130,7 +130,8 @@ int run(const rmsnorm_grad_t *grads, int64_t n, int64_t small_parts, bool clip, 
         t.slot += (int32_t)grid;
     }
     t.sums = t.slot;
-    if (!clip) return rrn::launch_kernel(only, dim3(1), 32, 0, stream, argv);
+    // the scaling's blocks write the norm; of tensors without elements there are none
+    if (!clip || t.sums == 0) return rrn::launch_kernel(only, dim3(1), 32, 0, stream, argv);
     if ((st = rrn::resident_blocks(dev, scale, rrn::kGradThreads, 0, &resident)) != RMSNORM_OK) return st;
     most = (int64_t)sms * resident;
     for (int64_t i = 0, l = 0; l < launches; ++l) {
