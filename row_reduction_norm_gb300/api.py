@@ -850,10 +850,13 @@ def clip_grad_norm(grads: Sequence[Optional[torch.Tensor]], max_norm: float,
     norm.  ``workspace`` is a CUDA uint8 tensor of
     ``rmsnorm_grad_norm_workspace_bytes()`` bytes (allocated when not given).
     """
+    if max_norm is None:
+        raise ValueError("max_norm must be a number (grad_norm takes the norm alone)")
     return _norm_or_clip(grads, max_norm, out, workspace, stream)
 
 
 def _norm_or_clip(grads, max_norm, out, workspace, stream):
+    """``max_norm`` None for the norm alone."""
     if out is not None and len(out) != len(grads):
         raise ValueError(f"out holds {len(out)} tensors, grads {len(grads)}")
     if stream is None:
