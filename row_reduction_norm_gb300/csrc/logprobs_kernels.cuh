@@ -669,7 +669,10 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_fwd_kernel(const Logpr
             p.logprobs[r] = (uint64_t)token >= (uint64_t)p.vocab ? 0.f
                             : sums.none                          ? neg_inf()
                                                                  : (given - sums.m) * p.inv_t - sums.log;
-        if (p.stats != nullptr) *reinterpret_cast<float2 *>(p.stats + 2 * r) = make_float2(sums.m, sums.log);
+        // a NaN takes no part in the maximum, but the row's is NaN where its log is
+        if (p.stats != nullptr)
+            *reinterpret_cast<float2 *>(p.stats + 2 * r) =
+                make_float2(sums.log != sums.log ? sums.log : sums.m, sums.log);
         if (ENT) p.entropy[r] = sums.entropy;
     }
     if (TOP && lane < p.top) {

@@ -45,3 +45,22 @@ def test_nan_beside_groups_that_hold_the_largest(rows, vocab, dtype):
         logits = torch.stack(kinds).repeat(rows // 3 + 1, 1)[:rows].to(dtype)
         r = R.token_logprobs(logits, None, top=top)
         assert torch.equal(r.top_ids.long(), ref.likeliest(logits, top)), top
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("vocab", [1, 9, 3000, 50257])
+def test_everything_of_a_row_with_nan_or_infinity_is_nan(vocab, dtype):
+    """And its gradient; the rows beside it are as without it."""
+    g = gen(vocab)
+    x = normal(g, 7, vocab)
+    x[1, vocab // 2] = NAN
+    x[2, vocab - 1] = float("inf")
+    x[3] = NAN
+    x[4] = LOW
+    x[5] = torch.where(torch.arange(vocab, device=DEV) == 0, NAN, LOW)
+    logits, ids, one = x.to(dtype), torch.zeros(7, dtype=torch.int64, device=DEV), torch.ones(7, device=DEV)
+    r = R.token_logprobs(logits, ids, 1.0, min(3, vocab), True)
+    d = R.token_logprobs_backward(logits, ids, r.stats, one, r.entropy, one)
+    for part in (r.logprobs, r.stats, r.entropy, r.top_logprobs, d):
+        assert bool(part[[1, 2, 3, 5]].isnan().all()) and not bool(part[[0, 4, 6]].isnan().any())
+    assert bool((r.stats[4] == LOW).all()) and not d[4].any()
