@@ -584,7 +584,7 @@ int rmsnorm_logprobs_fwd(const void *logits, const void *tokens, int token_bytes
  *   stats, entropy   the forward's (entropy only with dentropy)
  *   dlogprobs, dentropy   fp32 [rows], each optional
  *   dlogits          [rows, vocab], rows dlogits_stride elements apart; may be
- *                    the logits (same stride)
+ *                    the logits (another stride is RMSNORM_EINVAL then)
  * Masked logits get 0 (but for a masked token's own g).  Rows with g = h = 0,
  * and rows of masked logits only, are zeros, whatever else they hold.
  * Other arguments and limits as the forward.

@@ -121,6 +121,8 @@ int rmsnorm_logprobs_bwd(const void *logits, const void *tokens, int token_bytes
     if (rows > 1 && (dlogits_stride < vocab || dlogits_stride > INT64_MAX / 8 / rows)) return RMSNORM_EINVAL;
     if (rows == 0) return RMSNORM_OK;
     const int64_t s = rrn::size_of(dtype);
+    // in place only onto itself: other strides would write rows that are still read
+    if (dlogits == logits && rows > 1 && dlogits_stride != row_stride) return RMSNORM_EINVAL;
     if (dlogits == nullptr || !rrn::on_boundary(dlogits, s) || stats == nullptr || !rrn::on_boundary(stats, 8))
         return RMSNORM_EINVAL;
     if ((dlogprobs != nullptr && tokens == nullptr) || (dentropy != nullptr && entropy == nullptr))
