@@ -7,6 +7,7 @@
 
 #include "launch_util.h"
 #include "logprobs_kernels.cuh"
+#include "logprobs_pick.h"
 
 namespace {
 
@@ -104,7 +105,7 @@ int rmsnorm_logprobs_fwd(const void *logits, const void *tokens, int token_bytes
         cluster *= 2;
     if (groups > INT_MAX / cluster) return RMSNORM_EUNSUPPORTED;
     const void *fn = forward_kernel(dtype, aligned, entropy != nullptr, top > 0);
-    const size_t smem = (size_t)p.units * 12 * (rrn::kLpWarps / p.warps);
+    const size_t smem = rrn::lp_smem(p.units, rrn::kLpWarps / p.warps);
     int resident = 0;
     if ((st = rrn::resident_blocks(dev, fn, rrn::kLpThreads, smem, &resident)) != RMSNORM_OK) return st;
     p.ahead = (int64_t)resident * sms * (rrn::kLpWarps / p.warps);
