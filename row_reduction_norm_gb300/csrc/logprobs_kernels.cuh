@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_fwd_kernel(const Logpr
         const float bound = nth_largest(maxima[slot * warps], of_group, p.top, lane);
         const bool lowest = bound == neg_inf();
         KeySearch search;
-        search.start((uint64_t)order_of(bound) << 32);
+        search.start(order_of(bound), order_of(warp_max(of_group)));
         if (seen >= bound && begin < p.units)
             flagged[slot * warps * 32 + atomicAdd(flagged_count + slot, 1)] = warp * 32 + lane;   // in any order
         row_barrier(slot, warps);

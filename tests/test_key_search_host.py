@@ -54,7 +54,7 @@ static int search(const vector<float> &x, int warps, int vec, int top, Order ord
     const float bound = sorted[top - 1];
     const bool lowest = bound == kLow;
     rrn::KeySearch s;
-    s.start(key_of(bound, 0) >> 32 << 32);
+    s.start(key_of(bound, 0) >> 32, key_of(sorted[0], 0) >> 32);
     vector<uint64_t> want;
     for (int i = 0; i < n; ++i) want.push_back(key_of(x[i], i));
     std::partial_sort(want.begin(), want.begin() + top, want.end(), std::greater<>());
