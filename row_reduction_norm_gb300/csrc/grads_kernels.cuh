@@ -204,17 +204,15 @@ __global__ void __launch_bounds__(kGradThreads) grad_squares_kernel(const __grid
 }
 
 // The factor from a norm, for the block's other threads; its first thread calls.
-// Below fp32's smallest normal number, where it would lose bits, as one 2^126
-// times as large and that power (elements are multiplied by one after the other).
-struct Factor {
-    float f, power;
-    __device__ __forceinline__ bool one() const { return f == 1.f && power == 1.f; }
-};
+// Below fp32's smallest normal number it would lose bits: there it is 2^126 times
+// as large and negative, and store_part multiplies by the power too.
 template <int CAP>
-__device__ __forceinline__ Factor factor_of(const GradTable<CAP> &t, double norm) {
-    if (norm <= (double)t.max_norm) return Factor{1.f, 1.f};
-    const double f = (double)t.max_norm / norm;
-    return f < 0x1p-126 ? Factor{(float)(f * 0x1p126), 0x1p-126f} : Factor{(float)f, 1.f};
+__device__ __forceinline__ float factor_of(const GradTable<CAP> &t, double norm) {
+    if (norm <= (double)t.max_norm) return 1.f;
+    const double q = (double)t.max_norm / norm;
+    const float f = (float)q;
+    if (__builtin_expect(f < 0x1p-126f, 0)) return (float)(q * -0x1p126);
+    return f;
 }
 
 // The norm from the partial sums, by the block's first warp, in its lane 0.
@@ -242,9 +240,9 @@ __global__ void __launch_bounds__(32) grad_norm_kernel(const __grid_constant__ G
     if (threadIdx.x == 0) *t.norm = (float)norm;
 }
 
-// A thread's chunks of a part times the factor, to the tensor's out.
+// A thread's chunks of a part times the factor (factor_of's), to the tensor's out.
 template <typename T, int THREADS>
-__device__ __forceinline__ void store_part(const Chunk (&c)[kGradChunks], const GradEntry &e, int64_t first, Factor f) {
+__device__ __forceinline__ void store_part(const Chunk (&c)[kGradChunks], const GradEntry &e, int64_t first, float f) {
     constexpr int V = T::kVec, E = 16 / V;
     const bool alike = ((reinterpret_cast<uintptr_t>(e.grad) ^ reinterpret_cast<uintptr_t>(e.out)) & 15) == 0;
 #pragma unroll
@@ -253,7 +251,11 @@ __device__ __forceinline__ void store_part(const Chunk (&c)[kGradChunks], const 
         float x[V];
         unpack(c[j], x, T{});
 #pragma unroll
-        for (int k = 0; k < V; ++k) x[k] = x[k] * f.f * f.power;
+        for (int k = 0; k < V; ++k) x[k] *= fabsf(f);
+        if (f < 0.f) {
+#pragma unroll
+            for (int k = 0; k < V; ++k) x[k] *= 0x1p-126f;
+        }
         if (alike && i >= 0 && i + V <= e.count) {
             st16(e.out + i * E, pack(x, T{}));
         } else {
@@ -267,7 +269,7 @@ __device__ __forceinline__ void store_part(const Chunk (&c)[kGradChunks], const 
 // The parts from the last to the first.
 template <int CAP>
 __global__ void __launch_bounds__(kGradThreads) grad_scale_kernel(const __grid_constant__ GradTable<CAP> t) {
-    __shared__ Factor factor;
+    __shared__ float factor;
     const int hint = entry_of(t, t.parts - 1 - blockIdx.x);
     pdl_wait_for_inputs();
     pdl_allow_dependents();
@@ -279,11 +281,11 @@ __global__ void __launch_bounds__(kGradThreads) grad_scale_kernel(const __grid_c
         }
     }
     __syncthreads();
-    const Factor f = factor;
+    const float f = factor;
     for (uint32_t b = blockIdx.x; b < t.parts; b += gridDim.x) {
         const uint32_t part = t.parts - 1 - b;
         const GradEntry &e = t.e[b == blockIdx.x ? hint : entry_of(t, part)];
-        if (f.one() && e.out == e.grad) continue;
+        if (f == 1.f && e.out == e.grad) continue;
         Chunk c[kGradChunks];
         if (e.dtype == 1) {
             const int64_t first = load_part<BF16, kGradThreads>(c, e, part - e.first, threadIdx.x);
@@ -307,7 +309,7 @@ template <int CAP>
 __global__ void __launch_bounds__(kGradAlone, 1) grad_alone_kernel(const __grid_constant__ GradTable<CAP> t) {
     __shared__ Pair sums[kGradAlone / 32];
     __shared__ double of_block[kGradAloneBlocks];
-    __shared__ Factor factor;
+    __shared__ float factor;
     const uint32_t rank = cluster_rank(), blocks = cluster_ctas();
     const uint32_t part = threadIdx.x / 32 * blocks + rank;
     const bool there = part < t.parts;
@@ -342,8 +344,8 @@ __global__ void __launch_bounds__(kGradAlone, 1) grad_alone_kernel(const __grid_
         factor = factor_of(t, norm);
     }
     __syncthreads();
-    const Factor f = factor;
-    if (!t.clip || !there || (f.one() && e.out == e.grad)) return;
+    const float f = factor;
+    if (!t.clip || !there || (f == 1.f && e.out == e.grad)) return;
     if (bf16) store_part<BF16, 32>(c, e, first, f);
     else store_part<F32, 32>(c, e, first, f);
 }
