@@ -504,7 +504,7 @@ int rmsnorm_dropout_bwd(const void *dy, const void *h, const void *w, const void
 
 /*
  * Lookup of token embeddings with scaling:
- *   y[t] = RN_T( scale * table[tokens[t]] ),   t = 0 .. count - 1
+ *   y[t] = RN_T( scale * table[tokens[t]] ),   t = 0 .. count - 1   (an fp32 product)
  *   tokens      DEVICE int32 or int64 [count] (token_bytes 4 or 8).  A token
  *               outside 0 .. vocab - 1 (-1 marks padding) gives a row of zeros
  *   table       [vocab, width], rows table_stride elements apart
@@ -619,8 +619,10 @@ typedef struct {
  * touched when the factor is 1; two tensors with the same out are
  * RMSNORM_EINVAL (other overlaps are undefined).  Squares beyond fp32's range
  * do not over- or underflow the norm (blocks of elements that hold such are
- * added up again, scaled).  An infinite norm has the factor 0 (finite elements become 0,
- * infinite ones NaN), a NaN makes the norm and every element NaN.  Sums are
+ * added up again, scaled).  With an infinite element the factor is 0 (finite
+ * elements become 0, infinite ones NaN); a NaN makes the norm and every element
+ * NaN.  A norm past fp32's range is infinite in `norm`, and the factor is that of
+ * the norm itself.  Sums are
  * formed in an order that follows from the sizes, the alignment and the
  * device alone (no atomics).  n == 0 writes a norm of 0.
  */

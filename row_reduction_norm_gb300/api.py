@@ -662,12 +662,13 @@ def _row_stride(t: torch.Tensor, name: str) -> int:
 
 def embedding(tokens: torch.Tensor, table: torch.Tensor, scale: float = 1.0, out: Optional[torch.Tensor] = None,
               stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
-    """Rows of ``table`` times ``scale`` for each token, rounded once.
+    """Rows of ``table`` times ``scale`` for each token: an fp32 product, rounded to
+    the table's type.
 
     ``tokens`` is an int32 or int64 tensor of any shape, ``table`` [vocab,
     width] (last dimension contiguous, rows evenly strided); the result is
     [*tokens.shape, width].  A token outside 0 .. vocab - 1 (-1 marks padding)
-    gives a row of zeros.
+    gives a row of zeros.  ``out`` must not overlap the table.
     """
     if stream is None and table.is_cuda:
         y = (_fast or _bind_fast()).embedding(tokens, table, scale, out)
@@ -759,7 +760,10 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor], tempera
     1 get 0.  -infinity masks a token; a row of nothing else has log
     probabilities of -infinity and an entropy of 0.  Equal logits are ordered by
     the lower id.  ``stats`` is what ``token_logprobs_backward`` starts from.
-    What is returned may share one allocation.
+    A row that holds a NaN or +infinity has NaN for all of these; among the
+    alternatives a NaN counts as -infinity.  What is returned may share one
+    allocation: any of it keeps all of it, and ``torch.save`` writes all of it
+    (``clone`` what is to be kept by itself).
     """
     if stream is None and logits.is_cuda:
         r = (_fast or _bind_fast()).token_logprobs(logits, tokens, temperature, top, entropy)
@@ -845,9 +849,9 @@ def clip_grad_norm(grads: Sequence[Optional[torch.Tensor]], max_norm: float,
 
     ``grads`` is a list of contiguous bf16 and float32 tensors of one device
     (None entries are passed over), changed in place, or written to ``out``, a
-    tensor like each; none may be written twice.  An infinite norm makes the
+    tensor like each; none may be written twice.  An infinite element makes the
     factor 0, NaN everything NaN: a caller that skips such steps looks at the
-    norm.  ``workspace`` is a CUDA uint8 tensor of
+    norm (infinite too where it is past float32's range).  ``workspace`` is a CUDA uint8 tensor of
     ``rmsnorm_grad_norm_workspace_bytes()`` bytes (allocated when not given).
     """
     if max_norm is None:

@@ -12,7 +12,7 @@
 // Up to 2 MB are one launch of one block, or one cluster, in parts of 4 KB, a warp
 // each, which stay in registers between the two steps; the blocks' sums meet in
 // distributed shared memory (20 tensors of 20,000 elements together 4.3 us, 6.0 in
-// two launches; of 1.4 MB 5.6).
+// two launches; of 1.4 MB 5.8).
 //
 // The tensors' addresses travel as the launch's parameters (up to 32 KB of
 // them), so nothing is copied to the device beforehand and a captured call

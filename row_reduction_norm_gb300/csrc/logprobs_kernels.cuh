@@ -16,16 +16,19 @@
 // largest; their few chunks are read again (from L2), one a thread, and what
 // reaches the bound, a key of value and place, is gathered in shared memory.
 // Where that is too much (equal logits, masks, a heap of large ones in one
-// place), what was gathered gives a higher bound in the same way.  The few that
+// place), what was gathered gives a higher bound in the same way, in as many
+// rounds as key_search.h allows.  The few that
 // are left find their places by counting the larger ones.
 //
 // Gradient: elementwise, given the forward's statistics.  One read and one
 // write of every element; HBM bandwidth bounds both.
 //
 // bf16 8192 x 131072, 2.1 GB a tensor: forward 294 us (7.3 TB/s), gradient 618
-// (6.9); fp32 1001 x 50257, whose rows begin between the 16-byte boundaries,
-// with 5 alternatives: 39.9 (5.0), the alternatives' instructions and the waves'
-// end bound it; 8 rows of 131072 with 20 alternatives: 6.7, latency.
+// (6.9); fp32 1001 x 50257 with 5 alternatives: 39.7 (5.1) in rows of 50304, the
+// alternatives' look-up and the waves' end bound it, and 45.0 (4.5) in rows that
+// begin between the 16-byte boundaries; 8 rows of 131072 with 20 alternatives: 6.9,
+// latency.  bf16 8192 x 50257 between the boundaries 166, in rows of 50264 122:
+// 1.6 times the instructions an element.
 #pragma once
 
 #include "key_search.h"
